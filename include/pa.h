@@ -70,6 +70,10 @@ typedef enum {
 /* Row formats, numbered as ggml numbers them. */
 typedef enum { PA_F16 = 1, PA_Q4_0 = 2, PA_Q8_0 = 8 } pa_type;
 
+/* Number types of rows outside the pools (queries, outputs, projections),
+ * numbered as ggml numbers them. */
+typedef enum { PA_DT_F32 = 0, PA_DT_F16 = 1, PA_DT_BF16 = 30 } pa_dtype;
+
 typedef struct {
   uint32_t n_blocks;   /* blocks in the pool, 1 .. 2^31-1 */
   uint32_t page_size;  /* positions (rows) per block, a multiple of 16 */
@@ -208,6 +212,87 @@ pa_status pa_append_rows_f16(const pa_pool* pool, void* k_pool, void* v_pool, co
                              uint32_t n_rows, const int32_t* block_table, uint32_t table_stride,
                              uint32_t n_seq, int32_t* err, pa_stream_t stream);
 
+/* ------------------------------------------------------------------ norm and rotation
+ * The pages describe no counterpart of the calls from here to "decode"; they
+ * exist for users of this library.
+ *
+ * What a model does to the query and key heads of a projection before the
+ * cache sees them.  For a head x of head_dim = 256 values at position p:
+ *   norm      (only with a weight w) x_i <- x_i (w_i + weight_offset) /
+ *             sqrt(mean(x^2) + eps);
+ *   rotation  for pair i of rot_dim / 2: (a, b) <- (a c - b s, b c + a s) with
+ *             c = attn_factor cos(p inv_freq[i]), s = attn_factor
+ *             sin(p inv_freq[i]); the pair is values (i, i + rot_dim / 2), or
+ *             (2i, 2i + 1) when interleaved.  Values from rot_dim on stay.
+ * Arithmetic is fp32; the angle is reduced in 64-bit fixed point, so far
+ * positions lose nothing.  Positions are any int32. */
+typedef struct {
+  uint32_t rot_dim;     /* rotated leading values of a head: a multiple of 16, 0 .. 256 */
+  int32_t interleaved;  /* 0 or 1 */
+  float eps;            /* >= 0 */
+  float weight_offset;  /* added to every weight (1 where weights are stored as w - 1) */
+  float attn_factor;    /* on cosines and sines; 1 for a plain rotation */
+  double inv_freq[128]; /* radians per position of pair i; the first rot_dim / 2 are read, finite */
+} pa_rope_desc;
+
+/* Norm and rotation of query and key heads in one launch.
+ *
+ * rope:     host; copied by the call.
+ * q, k:     device rows of n_q_heads / n_kv_heads heads of 256 values of
+ *           in_type (a pa_dtype); q_stride and k_stride are elements between
+ *           rows (at least heads * 256, a multiple of 16 bytes), so q and k may
+ *           be parts of one projection.  A pointer is NULL exactly when its head
+ *           count is 0; at most 4096 heads each.
+ * q_weight, k_weight: device [256] of w_type, shared by the heads, or NULL: not
+ *           normalised, only rotated.
+ * row_pos:  device int32 [n_rows].
+ * q_out, k_out: device rows of out_type with their own strides.  An output may
+ *           be its input (same type and stride); other overlaps race.
+ * Every pointer 16-byte aligned (row_pos 4).  PA_ERR_INVALID or
+ * PA_ERR_UNSUPPORTED (a type, a rot_dim) before anything is launched. */
+pa_status pa_norm_rope(const pa_rope_desc* rope, const void* q, int64_t q_stride, uint32_t n_q_heads, const void* k,
+                       int64_t k_stride, uint32_t n_kv_heads, int32_t in_type, const void* q_weight,
+                       const void* k_weight, int32_t w_type, const int32_t* row_pos, uint32_t n_rows, void* q_out,
+                       int64_t q_out_stride, void* k_out, int64_t k_out_stride, int32_t out_type,
+                       pa_stream_t stream);
+
+/* Append with the norm and rotation on the way: rows straight from the
+ * projection.  Keys are normalised (k_weight), rotated and stored in the
+ * pool's K format, values stored in its V format as they are, both quantised
+ * from fp32 by the rule of pa_append_rows_f16 (an F16 pool rounds once, to
+ * nearest even), and, if q is given, queries normalised, rotated and written
+ * to q_out -- one launch for all that stands between a projection and the
+ * decode.
+ *
+ * k_rows, v_rows: device rows of n_kv_heads heads of in_type, strides as
+ *           above; q, q_stride, n_q_heads, q_weight, q_out, q_out_stride,
+ *           q_out_type as in pa_norm_rope (q and q_out NULL and n_q_heads 0 for
+ *           none).
+ * row_seq, row_pos, block_table, pools, err: as pa_append_rows; a row's
+ *           position is also its rotation's.  A row whose sequence, page or
+ *           table entry is out of range (the padding of a batch: row_seq -1) is
+ *           not stored and sets *err = PA_ERR_BOUNDS; its query is still
+ *           written.  Rows with the same (seq, pos) in one call race.  Values
+ *           are finite. */
+pa_status pa_append_rows_rope(const pa_pool* pool, void* k_pool, void* v_pool, const pa_rope_desc* rope,
+                              const void* k_rows, int64_t k_stride, const void* v_rows, int64_t v_stride,
+                              int32_t in_type, const void* k_weight, int32_t w_type, const void* q, int64_t q_stride,
+                              uint32_t n_q_heads, const void* q_weight, void* q_out, int64_t q_out_stride,
+                              int32_t q_out_type, const int32_t* row_seq, const int32_t* row_pos, uint32_t n_rows,
+                              const int32_t* block_table, uint32_t table_stride, uint32_t n_seq, int32_t* err,
+                              pa_stream_t stream);
+
+/* Rows of the cache as floating values: the inverse of an append, for a
+ * prompt whose attention runs elsewhere, and for looking at a cache.
+ * k_out, v_out: device [n_rows][n_kv_heads][256] of out_type, 16-byte aligned;
+ * either may be NULL (not both).  A stored value is scale * quant in fp32,
+ * rounded once to out_type.  row_seq, row_pos, block_table, pools, err: as
+ * pa_append_rows; a row out of range reads as zeros and sets *err =
+ * PA_ERR_BOUNDS.  Rows may repeat. */
+pa_status pa_read_rows(const pa_pool* pool, const void* k_pool, const void* v_pool, const int32_t* row_seq,
+                       const int32_t* row_pos, uint32_t n_rows, const int32_t* block_table, uint32_t table_stride,
+                       uint32_t n_seq, void* k_out, void* v_out, int32_t out_type, int32_t* err, pa_stream_t stream);
+
 /* ------------------------------------------------------------------ decode
  * Single-step GQA decode attention over a paged cache: split-K flash decoding
  * through a block table, with a log-sum-exp merge of the splits (llama.cpp
@@ -336,6 +421,44 @@ pa_status pa_decode_noalloc(const pa_pool* pool, const float* q, const void* k_p
                             const int32_t* block_table, uint32_t table_stride, const int32_t* seq_lens_dev,
                             const int32_t* seq_lens_host, uint32_t n_seq, uint32_t n_qtok, uint32_t n_q_heads,
                             float scale, float* out, float* lse, int32_t* err, pa_stream_t stream);
+
+/* ------------------------------------------------------------------ decode with shared prefixes
+ * The pages describe no counterpart of this call beyond the shared blocks
+ * themselves; it exists for users of this library.
+ *
+ * pa_decode for a batch whose sequences share prefixes: the batch is cut into
+ * n_groups runs of consecutive sequences (group_sizes: host, each >= 1, summing
+ * to n_seq), and the first prefix_lens[g] positions (host, >= 0) of all the
+ * sequences of group g hold the same rows.  Those rows are read and multiplied
+ * once for the whole group, through the table row of its first sequence; the
+ * rest of each sequence as in pa_decode; the parts are merged by log-sum-exp.
+ * The caller vouches for the shared rows (with pa_share_blocks the tables hold
+ * the same blocks; a page that the prefix ends in may be each sequence's own
+ * copy).  The result is that of pa_decode on the same batch, up to rounding;
+ * a prefix length of 0 shares nothing.
+ *
+ * q, out:   device [n_seq][n_qtok][n_q_heads][head_dim] of q_type / out_type (a
+ *           pa_dtype), 16-byte aligned.  Queries of fp32 are rounded to
+ *           binary16, as in pa_decode; quantised K (scale * quant) is too, so a
+ *           logit is off by about 2^-12 |q| |k| scale at most.
+ * prefix_lens: at most seq_lens_host - n_qtok of every sequence of the group
+ *           (PA_ERR_INVALID otherwise): the new tokens are each sequence's own.
+ * workspace: ws_bytes >= pa_decode_prefix_workspace_size(), 256-byte aligned.
+ * Everything else (lengths, tables, masks, lse, errors, supported shapes) as
+ * pa_decode.  Launches as pa_decode; sub-batches of at most 256 sequences,
+ * a group cut by a sub-batch's end being read once in each. */
+pa_status pa_decode_prefix(const pa_pool* pool, const void* q, int32_t q_type, const void* k_pool,
+                           const void* v_pool, const int32_t* block_table, uint32_t table_stride,
+                           const int32_t* seq_lens_dev, const int32_t* seq_lens_host, uint32_t n_seq,
+                           const uint32_t* group_sizes, const int32_t* prefix_lens, uint32_t n_groups,
+                           uint32_t n_qtok, uint32_t n_q_heads, float scale, void* out, int32_t out_type, float* lse,
+                           void* workspace, size_t ws_bytes, int32_t* err, pa_stream_t stream);
+
+/* Scratch bytes pa_decode_prefix needs for up to n_seq sequences in up to
+ * n_groups groups of n_qtok query tokens on CUDA device `device`, whatever their
+ * lengths and the groups' sizes.  0 for an unsupported shape. */
+size_t pa_decode_prefix_workspace_size(const pa_pool* pool, uint32_t n_seq, uint32_t n_groups, uint32_t n_qtok,
+                                       int device);
 
 /* ------------------------------------------------------------------ errors */
 

@@ -20,10 +20,12 @@ from . import _build
 __all__ = [
     "PA_F16", "PA_Q4_0", "PA_Q8_0", "PaError", "Pool", "load", "row_bytes", "pa_append_rows", "pa_append_rows_f16", "pa_copy_blocks", "pa_decode",
     "pa_decode_workspace_size", "pa_decode_plan", "pa_get_error", "pa_selftest_wait_timeout", "status_name",
-    "library_path", "pa_decode_noalloc",
+    "library_path", "pa_decode_noalloc", "PA_DT_F32", "PA_DT_F16", "PA_DT_BF16", "RopeDesc", "dtype_number",
+    "pa_norm_rope", "pa_append_rows_rope", "pa_read_rows", "pa_decode_prefix", "pa_decode_prefix_workspace_size",
 ]
 
 PA_F16, PA_Q4_0, PA_Q8_0 = 1, 2, 8
+PA_DT_F32, PA_DT_F16, PA_DT_BF16 = 0, 1, 30
 STATUS = ["PA_OK", "PA_ERR_INVALID", "PA_ERR_UNSUPPORTED", "PA_ERR_OOM", "PA_ERR_STALE", "PA_ERR_BOUNDS",
           "PA_ERR_TIMEOUT", "PA_ERR_CUDA"]
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_OOM, PA_ERR_STALE, PA_ERR_BOUNDS, PA_ERR_TIMEOUT, PA_ERR_CUDA = range(8)
@@ -33,7 +35,8 @@ EXPORTS = ["pa_pool_create", "pa_pool_destroy", "pa_pool_get_desc", "pa_row_byte
            "pa_alloc_blocks", "pa_release", "pa_block_index", "pa_pool_free_count", "pa_share_blocks", "pa_block_refcount",
            "pa_cow_blocks", "pa_copy_blocks", "pa_append_rows", "pa_append_rows_f16",
            "pa_decode", "pa_decode_split", "pa_decode_merge", "pa_decode_workspace_size", "pa_decode_plan", "pa_get_error", "pa_status_string",
-           "pa_selftest_wait_timeout", "pa_decode_noalloc"]
+           "pa_selftest_wait_timeout", "pa_decode_noalloc", "pa_norm_rope", "pa_append_rows_rope", "pa_read_rows",
+           "pa_decode_prefix", "pa_decode_prefix_workspace_size"]
 
 
 class PaError(RuntimeError):
@@ -49,6 +52,11 @@ def status_name(s: int) -> str:
 class PoolDesc(C.Structure):
     _fields_ = [("n_blocks", C.c_uint32), ("page_size", C.c_uint32), ("n_kv_heads", C.c_uint32),
                 ("head_dim", C.c_uint32), ("k_type", C.c_int32), ("v_type", C.c_int32)]
+
+
+class RopeDesc(C.Structure):
+    _fields_ = [("rot_dim", C.c_uint32), ("interleaved", C.c_int32), ("eps", C.c_float),
+                ("weight_offset", C.c_float), ("attn_factor", C.c_float), ("inv_freq", C.c_double * 128)]
 
 
 _lock = threading.Lock()
@@ -69,7 +77,7 @@ def load():
         if not os.path.exists(path):
             raise RuntimeError(f"libpa is not built ({path} missing); run paged_kv_gqa_11_gb300._build.build()")
         L = C.CDLL(path)
-        vp, u32, i32, sz = C.c_void_p, C.c_uint32, C.c_int32, C.c_size_t
+        vp, u32, i32, sz, i64 = C.c_void_p, C.c_uint32, C.c_int32, C.c_size_t, C.c_int64
         sig = {
             "pa_pool_create": (C.c_int, [C.POINTER(PoolDesc), C.POINTER(vp)]),
             "pa_pool_destroy": (None, [vp]),
@@ -96,6 +104,14 @@ def load():
             "pa_selftest_wait_timeout": (C.c_int, [u32, vp, vp]),
             "pa_decode_noalloc": (C.c_int, [vp, vp, vp, vp, vp, u32, vp, vp, u32, u32, u32, C.c_float, vp, vp,
                                             vp, vp]),
+            "pa_norm_rope": (C.c_int, [vp, vp, i64, u32, vp, i64, u32, i32, vp, vp, i32, vp, u32, vp, i64, vp, i64, i32,
+                                       vp]),
+            "pa_append_rows_rope": (C.c_int, [vp, vp, vp, vp, vp, i64, vp, i64, i32, vp, i32, vp, i64, u32, vp, vp, i64,
+                                              i32, vp, vp, u32, vp, u32, u32, vp, vp]),
+            "pa_read_rows": (C.c_int, [vp, vp, vp, vp, vp, u32, vp, u32, u32, vp, vp, i32, vp, vp]),
+            "pa_decode_prefix": (C.c_int, [vp, vp, i32, vp, vp, vp, u32, vp, vp, u32, vp, vp, u32, u32, u32, C.c_float,
+                                           vp, i32, vp, vp, sz, vp, vp]),
+            "pa_decode_prefix_workspace_size": (sz, [vp, u32, u32, u32, C.c_int]),
         }
         sig["pa_decode_split"] = sig["pa_decode_merge"] = sig["pa_decode"]
         for name, (res, args) in sig.items():
@@ -282,3 +298,64 @@ def pa_decode_noalloc(pool: Pool, q, k_pool, v_pool, block_table, table_stride: 
                                         table_stride, _ptr(seq_lens_dev), _ptr(seq_lens_host), n_seq, n_qtok,
                                         n_q_heads, C.c_float(scale), _ptr(out), _ptr(lse), _ptr(err),
                                         _stream(stream)))
+
+
+_DTYPES = {}
+
+
+def dtype_number(t) -> int:
+    """The library's number of a torch dtype (float32, float16, bfloat16)."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: PA_DT_F32, torch.float16: PA_DT_F16, torch.bfloat16: PA_DT_BF16})
+    if t not in _DTYPES:
+        raise PaError(PA_ERR_UNSUPPORTED, str(t))
+    return _DTYPES[t]
+
+
+def pa_norm_rope(rope: int, q, q_stride: int, n_q_heads: int, k, k_stride: int, n_kv_heads: int, in_type: int,
+                 q_weight, k_weight, w_type: int, row_pos, n_rows: int, q_out, q_out_stride: int, k_out,
+                 k_out_stride: int, out_type: int, stream=None) -> None:
+    """rope: the address of a RopeDesc; strides in elements between rows."""
+    _check(load().pa_norm_rope(rope, _ptr(q), q_stride, n_q_heads, _ptr(k), k_stride, n_kv_heads, in_type,
+                               _ptr(q_weight), _ptr(k_weight), w_type, _ptr(row_pos), n_rows, _ptr(q_out),
+                               q_out_stride, _ptr(k_out), k_out_stride, out_type, _stream(stream)), "pa_norm_rope")
+
+
+def pa_append_rows_rope(pool: Pool, k_pool, v_pool, rope: int, k_rows, k_stride: int, v_rows, v_stride: int,
+                        in_type: int, k_weight, w_type: int, q, q_stride: int, n_q_heads: int, q_weight, q_out,
+                        q_out_stride: int, q_out_type: int, row_seq, row_pos, n_rows: int, block_table,
+                        table_stride: int, n_seq: int, err, stream=None) -> None:
+    """Keys normalised, rotated and stored, values stored, queries normalised and rotated (q may be None)."""
+    _check(load().pa_append_rows_rope(pool.handle, _ptr(k_pool), _ptr(v_pool), rope, _ptr(k_rows), k_stride,
+                                      _ptr(v_rows), v_stride, in_type, _ptr(k_weight), w_type, _ptr(q), q_stride,
+                                      n_q_heads, _ptr(q_weight), _ptr(q_out), q_out_stride, q_out_type, _ptr(row_seq),
+                                      _ptr(row_pos), n_rows, _ptr(block_table), table_stride, n_seq, _ptr(err),
+                                      _stream(stream)), "pa_append_rows_rope")
+
+
+def pa_read_rows(pool: Pool, k_pool, v_pool, row_seq, row_pos, n_rows: int, block_table, table_stride: int,
+                 n_seq: int, k_out, v_out, out_type: int, err, stream=None) -> None:
+    """Rows [n_rows][n_kv_heads][head_dim] of the pools as values of out_type (k_out or v_out may be None)."""
+    _check(load().pa_read_rows(pool.handle, _ptr(k_pool), _ptr(v_pool), _ptr(row_seq), _ptr(row_pos), n_rows,
+                               _ptr(block_table), table_stride, n_seq, _ptr(k_out), _ptr(v_out), out_type, _ptr(err),
+                               _stream(stream)), "pa_read_rows")
+
+
+def pa_decode_prefix_workspace_size(pool: Pool, n_seq: int, n_groups: int, n_qtok: int, device: int = 0) -> int:
+    return int(load().pa_decode_prefix_workspace_size(pool.handle, n_seq, n_groups, n_qtok, device))
+
+
+def pa_decode_prefix(pool: Pool, q, q_type: int, k_pool, v_pool, block_table, table_stride: int, seq_lens_dev,
+                     seq_lens_host, n_seq: int, group_sizes, prefix_lens, n_groups: int, n_qtok: int, n_q_heads: int,
+                     scale: float, out, out_type: int, lse, workspace, ws_bytes: int, err, stream=None,
+                     check: bool = True) -> int:
+    """seq_lens_host (int32), group_sizes (uint32) and prefix_lens (int32): host
+    buffers that stay alive for the call."""
+    rc = load().pa_decode_prefix(pool.handle, _ptr(q), q_type, _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
+                                 table_stride, _ptr(seq_lens_dev), _ptr(seq_lens_host), n_seq, _ptr(group_sizes),
+                                 _ptr(prefix_lens), n_groups, n_qtok, n_q_heads, scale, _ptr(out), out_type, _ptr(lse),
+                                 _ptr(workspace), ws_bytes, _ptr(err), _stream(stream))
+    if check:
+        _check(rc, "pa_decode_prefix")
+    return rc
