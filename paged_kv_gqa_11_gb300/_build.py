@@ -18,11 +18,13 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libpa.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 TYPES = {"f16": 1, "q4_0": 2, "q8_0": 8}  # pa_type numbers
-# (source, object name, extra defines): the split-decode kernels are one
-# source compiled once per (K, V) format pair.
+# (source, object name, extra defines): the split-decode and shared-prefix
+# kernels are one source each, compiled once per (K, V) format pair.
 UNITS = [("pa_pool.cpp", "pa_pool", []), ("pa_append.cu", "pa_append", []), ("pa_decode.cu", "pa_decode", []),
          ("pa_rope.cu", "pa_rope", []), ("pa_prefix.cu", "pa_prefix", [])]
 UNITS += [("pa_decode_kern.cu", f"pa_decode_kern_{k}_{v}", [f"-DPA_KT={TYPES[k]}", f"-DPA_VT={TYPES[v]}"])
+          for k in TYPES for v in TYPES]
+UNITS += [("pa_prefix_kern.cu", f"pa_prefix_kern_{k}_{v}", [f"-DPA_KT={TYPES[k]}", f"-DPA_VT={TYPES[v]}"])
           for k in TYPES for v in TYPES]
 
 

@@ -1,0 +1,1037 @@
+// Decode with shared prefixes on the fifth-generation tensor core (sm_103a).
+//
+// The mathematics.  A group of sequences shares its first P keys; query row r
+// (a token's query head) of any of its sequences attends to those P keys and
+// to its own sequence's later ones.  The softmax splits: with m, l, O the
+// maximum, the sum of weights and the weighted V of a part of the keys, the
+// parts merge by log-sum-exp.  So a prefix is one dense contraction of all the
+// group's query rows (6 per token and KV head) with its keys, read once, and
+// each suffix a small one of its own.
+//
+//   segment  = (group, KV head, tile of 64 query rows) over the prefix's keys,
+//              or (sequence, KV head, row tile) over the suffix's; cut into key
+//              tiles of 128; all tiles of the batch are laid end to end and cut
+//              into one contiguous range per CTA (one CTA per SM).  A range's
+//              share of a segment is a piece; every piece leaves (m, l) and O in
+//              the workspace for the merge.
+//   S^T      = K Q^T    tcgen05.mma M = 128 keys, N = query rows (16 to 64),
+//   O^T     += V^T P^T  tcgen05.mma M = 128 dims (twice), N = query rows,
+//              K = keys.
+//
+// Why transposed.  A decode has few query rows: as the MMA's M dimension (128)
+// most of them would be padding, as its N dimension (a multiple of 16) none
+// is.  K and V are then the A operands, and those may lie in tensor memory:
+// a dequantising warp goes from raw quants in shared memory through registers
+// into tensor memory, and the binary16 K and V never touch shared memory,
+// whose bandwidth a kernel with both operands there runs out of first.  An
+// MMA of up to 64 columns takes about 48 cycles whatever N is, so 128 keys
+// cost 32 x 48 cycles for up to 64 rows.
+//
+// Tensor memory (512 columns x 128 lanes): O^T dims 0-127 in columns 0-63 and
+// dims 128-255 in 64-127 (lane = dim, column = query row), S^T in 128-191
+// (lane = key), and five operand units of 64 columns.  A K unit is 128 keys x
+// 128 dims (lane = key, a column = two dims), a V unit 64 keys x 256 dims (lane
+// = dim, a column = two keys, dims 128-255 in its upper 32 columns); each is
+// worth eight MMAs, and they form a ring in the order in which the MMA warp
+// consumes them: K(0) | K(1) V(0) | K(2) V(1) | ... | V(n - 1), so that S of the
+// next tile is computed while the softmax of this one runs.
+//
+// Warps, hand-offs on mbarriers, every wait bounded:
+//   0-7    K dequantisation: (half of the dims, lane quarter), thread = key;
+//   8-15   V dequantisation: (half of the tile's keys, lane quarter), by
+//          transposing ldmatrix;
+//   16-23  softmax: 16 keys each, all query rows, in mma fragments; P^T goes to
+//          shared memory by transposing stmatrix; they also rescale O^T (rarely:
+//          the reference maximum is raised only past 2^8) and write the pieces;
+//   24     MMA issue; 25 and 26 raw K and V copies (cp.async.bulk); 27 stages the
+//          query rows of the pieces after the first (the softmax warps stage it).
+//
+// The key order inside a group of 16 is key16 below: it is the order in which
+// a transposing ldmatrix delivers key pairs to the columns of a V unit, chosen so
+// that both its rows and the K threads' row reads fall in different banks.
+//
+// Precision.  Q, K, V (scale * quant, rounded once) and P are binary16, products
+// are accumulated in fp32, m, l and O are fp32, and l sums the weights before
+// their rounding.  Rounding K costs a logit 2^-12 |q| |k| scale at most, the size
+// of the rounding of Q that fp32 queries meet anyway; keeping K exact would take
+// a second product and half again the dequantisation.
+#pragma once
+
+#include "pa_decode_impl.cuh"
+
+namespace pa_prefix {
+
+using namespace pa_dev;
+using pa_layout::Fmt;
+using pa_layout::kGroup;
+using pa_split::kD;
+using pa_split::kGqa;
+
+constexpr int kKeys = 128;        // keys per tile
+constexpr int kStageKeys = 64;    // keys per copy stage and per V unit
+constexpr int kRows = 64;         // query rows per row tile
+constexpr int kMaxSeqs = 256;     // sequences per launch
+constexpr int kMaxGroups = 128;   // shared prefixes per launch (two sequences each at least)
+constexpr int kUnits = 5;         // operand units in tensor memory
+constexpr int kKWarp0 = 0, kVWarp0 = 8, kSmWarp0 = 16, kMmaWarp = 24, kCopyKWarp = 25, kCopyVWarp = 26, kQWarp = 27;
+constexpr int kThreads = 28 * 32;
+constexpr int kSmThreads = 256;
+constexpr uint32_t kTmemCols = 512, kOCol = 0, kSCol = 128, kUnitCol = 192;
+constexpr float kLazyLog2 = 8.f;  // the reference maximum is raised past this
+
+struct Params {
+  const uint8_t* q;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const int32_t* table;
+  int32_t* err;
+  float2* part_ml;  // (reference maximum in log2 units, sum of weights) per slot row
+  float* part_o;    // [slot row][256]
+  int q_type, n_qtok, n_kv_heads, n_q_heads, page_size, table_stride, n_blocks;
+  int n_seq, n_groups, n_ctas;
+  int prefix_tiles, total_tiles;
+  int suffix_row_tiles, suffix_rows;  // row tiles of a suffix segment; rows of its slot
+  int suffix_base;                    // first slot row of the suffixes
+  float scale_log2;
+  int32_t len[kMaxSeqs], start[kMaxSeqs];  // a suffix's keys are start .. len - 1
+  int32_t seq_tile[kMaxSeqs + 1];          // suffix tiles before a sequence
+  int32_t group_first[kMaxGroups], group_seqs[kMaxGroups], group_keys[kMaxGroups];
+  int32_t group_tile[kMaxGroups + 1], group_seg[kMaxGroups];  // tiles and segments before a group
+};
+
+// ------------------------------------------------------------------ the walk
+
+__host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// The CTA whose range holds tile x: CTA i takes tiles i T / G .. (i + 1) T / G - 1.
+__host__ __device__ inline int cta_of(int x, int total, int ctas) {
+  return (int)((((long long)x + 1) * ctas - 1) / total);
+}
+
+struct Pos {
+  int unit;        // group or sequence
+  int head, rt, j;  // KV head, row tile, key tile
+  int nt, nrt;     // key tiles of the segment, row tiles of the (unit, head)
+  bool pre;
+};
+
+__device__ __forceinline__ void pos_sizes(const Params& p, Pos& t) {
+  if (t.pre) {
+    t.nt = ceil_div(p.group_keys[t.unit], kKeys);
+    t.nrt = ceil_div(kGqa * p.n_qtok * p.group_seqs[t.unit], kRows);
+  } else {
+    t.nt = ceil_div(p.len[t.unit] - p.start[t.unit], kKeys);
+    t.nrt = p.suffix_row_tiles;
+  }
+}
+
+__device__ __forceinline__ Pos locate(const Params& p, int x) {
+  Pos t;
+  t.pre = x < p.prefix_tiles;
+  const int32_t* cum = t.pre ? p.group_tile : p.seq_tile;
+  if (!t.pre) x -= p.prefix_tiles;
+  int lo = 0, hi = (t.pre ? p.n_groups : p.n_seq) - 1;  // the last unit whose first tile is <= x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cum[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  t.unit = lo;
+  x -= cum[lo];
+  pos_sizes(p, t);
+  const int seg = x / t.nt;
+  t.j = x - seg * t.nt;
+  t.head = seg / t.nrt;
+  t.rt = seg - t.head * t.nrt;
+  return t;
+}
+
+__device__ __forceinline__ void advance(const Params& p, Pos& t) {
+  if (++t.j < t.nt) return;
+  t.j = 0;
+  if (++t.rt < t.nrt) return;
+  t.rt = 0;
+  if (++t.head < p.n_kv_heads) return;
+  t.head = 0;
+  ++t.unit;
+  if (t.pre && t.unit == p.n_groups) {
+    t.pre = false;
+    t.unit = 0;
+  }
+  if (!t.pre && t.unit >= p.n_seq) return;  // past the last tile
+  pos_sizes(p, t);
+}
+
+__device__ __forceinline__ int pos_seq(const Params& p, const Pos& t) { return t.pre ? p.group_first[t.unit] : t.unit; }
+__device__ __forceinline__ int pos_key0(const Params& p, const Pos& t) {
+  return (t.pre ? 0 : p.start[t.unit]) + t.j * kKeys;
+}
+__device__ __forceinline__ int pos_end(const Params& p, const Pos& t) {
+  return t.pre ? p.group_keys[t.unit] : p.len[t.unit];
+}
+// Query rows of the segment (the unit's rows of this head and row tile).
+__device__ __forceinline__ int pos_rows(const Params& p, const Pos& t) {
+  const int all = kGqa * p.n_qtok * (t.pre ? p.group_seqs[t.unit] : 1);
+  return min(kRows, all - t.rt * kRows);
+}
+__device__ __forceinline__ int pos_slot_row(const Params& p, const Pos& t, int cta) {
+  if (t.pre) return (cta + p.group_seg[t.unit] + t.head * t.nrt + t.rt) * kRows;
+  return p.suffix_base + (cta + (t.unit * p.n_kv_heads + t.head) * t.nrt + t.rt) * p.suffix_rows;
+}
+
+// Operand units are numbered in the order of consumption: the two of K(j), and
+// the two of V(j), of a CTA's n tiles.
+__device__ __forceinline__ int k_num(int j) { return j == 0 ? 0 : 4 * j - 2; }
+__device__ __forceinline__ int v_num(int j, int n) { return j == n - 1 ? 4 * j + 2 : 4 * j + 4; }
+
+// The row of a 16-key group at position p of the tile's key order.
+__host__ __device__ constexpr int key16(int p) {
+  const int t = p >> 2, e = p & 3;
+  return e < 2 ? 2 * t + e : 8 + ((2 * t + (e & 1)) ^ 4);
+}
+
+// ------------------------------------------------------------------ shared memory
+
+template <int KT, int VT>
+struct Smem {
+  static constexpr int kKStage = 4 * pa_layout::group_bytes<KT>(), kVStage = 4 * pa_layout::group_bytes<VT>();
+  static constexpr int kQBytes = kRows * kD * 2, kPBytes = kRows * kKeys * 2;
+  static constexpr int kQ = 0, kP = 2 * kQBytes, kRing = kP + kPBytes;
+  static constexpr int kTail = 8 * kRows * 4 + 3 * kRows * 4 + 16 * 32 + 64 + 512;  // red, references, tiles, barriers
+  // K and V stages in rings of their own, both of an even number of stages: a
+  // warp reads every second stage of its ring, and so sees every use of those it
+  // reads (a parity wait must never be two phases ahead of its barrier).  Two
+  // each, then two more to the ring with fewer, as long as they fit.
+  static constexpr int kRoom = 232448 - 1024 - kRing - kTail;
+  static constexpr int fit(bool v) {
+    int nk = 2, nv = 2;
+    for (int i = 0; i < 8; ++i) {
+      const bool to_k = nk <= nv;
+      if ((nk + 2 * to_k) * kKStage + (nv + 2 * !to_k) * kVStage > kRoom) {
+        if ((nk + 2 * !to_k) * kKStage + (nv + 2 * to_k) * kVStage > kRoom) break;
+        (to_k ? nv : nk) += 2;
+      } else {
+        (to_k ? nk : nv) += 2;
+      }
+    }
+    return v ? nv : nk;
+  }
+  static constexpr int kKStages = fit(false), kVStages = fit(true);
+  static_assert(2 * (kKStage + kVStage) <= kRoom, "a tile of stages does not fit");
+  static constexpr int kVRing = kRing + kKStages * kKStage;
+  static constexpr int kRed = kVRing + kVStages * kVStage;
+  static constexpr int kRef = kRed + 8 * kRows * 4, kDelta = kRef + kRows * 4, kAlpha = kDelta + kRows * 4;
+  static constexpr int kTile = kAlpha + kRows * 4, kLeft = kTile + 16 * 32, kBar = kLeft + 64;
+  // K and V raw full / empty [stages], unit full / empty [5], s full / empty, p full, pv done, q full / empty [2], o free, drain
+  static constexpr int kNBar = 2 * (kKStages + kVStages) + 2 * kUnits + 4 + 4 + 2;
+  static constexpr int kMisc = kBar + 8 * kNBar;  // abort, tmem base, the first tile's place
+  static constexpr int kTotal = kMisc + 16 + 32;
+  static constexpr int kLaunch = kTotal + 1024;  // the base is aligned to 1024 inside
+  static_assert(kTotal - kBar <= 512 && kLaunch <= 232448, "shared memory");
+};
+
+// Canonical K-major byte offset (core matrices of 8 rows x 16 bytes) of row r,
+// 8-element slot s, of an operand with `slots` slots per row.
+__device__ __forceinline__ uint32_t canon(int r, int s, int slots) {
+  return (uint32_t)((((r >> 3) * slots + s) << 7) + ((r & 7) << 4));
+}
+
+// ------------------------------------------------------------------ tensor memory
+
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+}
+
+// 16 lanes x 16 columns in the mma fragment distribution: thread 4g + t gets
+// (lane g, columns 2t, 2t + 1), (lane g + 8, the same), then columns 8 on.
+__device__ __forceinline__ void tmem_ld_frag2(uint32_t a, uint32_t (&u)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+               : "r"(a));
+}
+
+// Registers of a tensor-memory load are read only after its wait: nothing that
+// uses them moves above this.
+template <int N>
+__device__ __forceinline__ void loaded(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                      "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+// 16 lanes x 8 columns, the same distribution, stored.
+__device__ __forceinline__ void tmem_st_frag1(uint32_t a, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
+}
+
+// ------------------------------------------------------------------ dequantisation
+//
+// The loops are rolled: the roles' code runs side by side on every scheduler,
+// and the instruction cache is the first thing that it runs out of.
+
+constexpr uint32_t kM1152 = pa_split::kHalf2_m1152, kM1032 = pa_split::kHalf2_m1032, kR16 = pa_split::kHalf2_1_16,
+                   kM72 = pa_split::kHalf2_m72, kMagic = pa_split::kMagic64;
+
+// This thread's key, dims 128 kd .. + 127, from raw shared memory into a K
+// unit's 64 columns at taddr, 32 dims (16 columns) at a time.  grp: the key's row
+// group, r its row there.
+template <int T>
+__device__ __forceinline__ void dequant_k(uint32_t grp, int r, int kd, uint32_t taddr) {
+  const uint32_t row = grp + Fmt<T>::kScales + r * Fmt<T>::kRowQ;
+  const int r7 = r & 7;
+  uint2 sc = make_uint2(0u, 0u);
+  if (T != PA_F16) sc = lds64(grp + 16 * r + 8 * kd);  // four block scales
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const int b = 4 * kd + i;
+    uint32_t out[16];
+    if constexpr (T == PA_F16) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint4 x = lds128(row + (((4 * b + c) ^ r7) << 4));
+        out[4 * c] = x.x;
+        out[4 * c + 1] = x.y;
+        out[4 * c + 2] = x.z;
+        out[4 * c + 3] = x.w;
+      }
+    } else {
+      const uint32_t d2 = prmt((i & 2) ? sc.y : sc.x, 0u, (i & 1) ? 0x3232 : 0x1010);
+      if constexpr (T == PA_Q8_0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint4 x = lds128(row + (((2 * b + c) ^ r7) << 4));
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t u = w[k] ^ 0x80808080u;  // int8 -> 128 + q as an unsigned byte
+            out[8 * c + 2 * k] = hmul2(hadd2(prmt(u, kMagic, 0x4140), kM1152), d2);
+            out[8 * c + 2 * k + 1] = hmul2(hadd2(prmt(u, kMagic, 0x4342), kM1152), d2);
+          }
+        }
+      } else {  // Q4_0: word k of the block holds dims 4k .. 4k+3 (low nibbles) and 16 + 4k .. (high)
+        const uint4 x = lds128(row + ((b ^ r7) << 4));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t u = w[k] >> 8;
+          out[4 * k] = hmul2(hadd2(and_or(w[k], 0x000f000fu, 0x64006400u), kM1032), d2);
+          out[4 * k + 1] = hmul2(hadd2(and_or(u, 0x000f000fu, 0x64006400u), kM1032), d2);
+          out[4 * k + 2] = hmul2(hfma2(and_or(w[k], 0x00f000f0u, 0x64006400u), kR16, kM72), d2);
+          out[4 * k + 3] = hmul2(hfma2(and_or(u, 0x00f000f0u, 0x64006400u), kR16, kM72), d2);
+        }
+      }
+    }
+    tmem_st16(taddr + 16 * i, out);
+  }
+}
+
+// The four dims at load 0 and at load 1 of an 8-position slot of K's dim order,
+// and their order: natural, or for Q4_0 the order of dequant_k's columns.
+template <int T>
+__device__ __forceinline__ int q_dim(int slot, int half) {
+  if (T == PA_Q4_0) return (slot >> 2) * 32 + (slot & 3) * 4 + 16 * half;
+  return 8 * slot + 4 * half;
+}
+
+// The dim of lane l (of 32) that dequant_v writes.
+template <int T>
+__host__ __device__ constexpr int v_dim(int l) {
+  return T == PA_F16 ? l : 16 * (l >> 4) + 2 * (l & 7) + ((l >> 3) & 1);
+}
+
+// 64 keys x 32 dims twice (blocks b and b + 4) of a V stage into a V unit's 32
+// lanes at taddr (lane field included): columns 0-31 and 32-63, eight for every
+// 16 keys.  n_keys: live keys of the stage; the others' values become zeros,
+// whatever bytes lie there.
+template <int T>
+__device__ __forceinline__ void dequant_v(uint32_t stage, int b, int n_keys, uint32_t taddr, int lane) {
+  constexpr int GB = pa_layout::group_bytes<T>(), RQ = Fmt<T>::kRowQ;
+  // ldmatrix: matrices 0 and 2 hold rows 0..7 of a group, 1 and 3 rows 8 + (i ^ 4)
+  const int mi = lane >> 3, i = lane & 7, r7 = (mi & 1) ? i ^ 4 : i, t = lane & 3;
+  uint32_t row = stage + Fmt<T>::kScales + ((mi & 1) * 8 + r7) * RQ;
+  // scales of the key pairs (2t, 2t + 1) and 8 + ((2t, 2t + 1) ^ 4): b + 4 is 128 bytes on
+  uint32_t sa = stage + 64 * (b >> 1) + 8 * (b & 1) + 16 * t, sb = (sa ^ 32) + 4;
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    uint32_t ma = 0xffffffffu, mb = 0xffffffffu;  // live keys of the pairs
+    if (n_keys < kStageKeys) {
+      const int left = n_keys - 16 * g, ka = 2 * t, kb = 8 + ((2 * t) ^ 4);
+      ma = (ka < left ? 0xffffu : 0u) | (ka + 1 < left ? 0xffff0000u : 0u);
+      mb = (kb < left ? 0xffffu : 0u) | (kb + 1 < left ? 0xffff0000u : 0u);
+    }
+    [[maybe_unused]] uint32_t xq[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // block b, block b + 4
+      [[maybe_unused]] uint32_t x[4];
+      uint32_t lo[4], hi[4];  // lanes 0-15 and 16-31 of the quarter
+      if constexpr (T == PA_F16) {
+        ldsm_x4_trans(row + (((4 * b + 16 * h + (mi >> 1)) ^ r7) << 4), lo);
+        ldsm_x4_trans(row + (((4 * b + 16 * h + 2 + (mi >> 1)) ^ r7) << 4), hi);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          lo[m] &= (m & 1) ? mb : ma;
+          hi[m] &= (m & 1) ? mb : ma;
+        }
+      } else {
+        uint32_t da, db;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(da) : "r"(sa + 128 * h));
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(db) : "r"(sb + 128 * h));
+        da &= ma;
+        db &= mb;
+        if constexpr (T == PA_Q8_0) {
+          ldsm_x4_trans(row + (((2 * b + 8 * h + (mi >> 1)) ^ r7) << 4), x);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t u = x[m] ^ 0x80808080u, d2 = (m & 1) ? db : da;
+            uint32_t* o = (m >> 1) ? hi : lo;
+            // bytes 0, 2: dim 2g of the key pair; bytes 1, 3: dim 2g + 1
+            o[m & 1] = hmul2(hadd2(prmt(u, kMagic, 0x4240), kM1152), d2);
+            o[2 + (m & 1)] = hmul2(hadd2(prmt(u, kMagic, 0x4341), kM1152), d2);
+          }
+        } else {
+          if (h == 0) ldsm_x4_trans(row + (((b + 4 * (mi >> 1)) ^ r7) << 4), xq);  // blocks b (0, 1) and b + 4 (2, 3)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const uint32_t u = xq[2 * h + m], v = u >> 8, d2 = m ? db : da;
+            lo[m] = hmul2(hadd2(and_or(u, 0x000f000fu, 0x64006400u), kM1032), d2);
+            lo[2 + m] = hmul2(hadd2(and_or(v, 0x000f000fu, 0x64006400u), kM1032), d2);
+            hi[m] = hmul2(hfma2(and_or(u, 0x00f000f0u, 0x64006400u), kR16, kM72), d2);
+            hi[2 + m] = hmul2(hfma2(and_or(v, 0x00f000f0u, 0x64006400u), kR16, kM72), d2);
+          }
+        }
+      }
+      tmem_st_frag1(taddr + 32 * h + 8 * g, lo);
+      tmem_st_frag1(taddr + 32 * h + 8 * g + (16u << 16), hi);
+    }
+    row += GB;
+    sa += GB;
+    sb += GB;
+  }
+}
+
+// ------------------------------------------------------------------ query rows
+
+__device__ __forceinline__ float4 load4(int type, const uint8_t* base, long long i) {
+  if (type == PA_DT_F32) return *reinterpret_cast<const float4*>(base + 4 * i);
+  const uint2 v = *reinterpret_cast<const uint2*>(base + 2 * i);
+  if (type == PA_DT_F16) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x)),
+                 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xffff0000u));
+}
+
+// Worker w of nw (warps) stages its share of the segment's query rows as
+// binary16 into the B operand at dst, in K's dim order; rows past the segment's
+// up to n (a multiple of 16) are zeros.
+template <int KT>
+__device__ __forceinline__ void stage_q(const Params& p, const Pos& t, uint32_t dst, int n, int w, int nw, int lane) {
+  const int all = kGqa * p.n_qtok * (t.pre ? p.group_seqs[t.unit] : 1);
+  const long long tok0 = (long long)pos_seq(p, t) * p.n_qtok;
+#pragma unroll 4
+  for (int it = w; it < n; it += nw) {  // (row group of 8, slot group of 4): n / 8 * 8 of them
+    const int row = (it >> 3) * 8 + (lane & 7), slot = (it & 7) * 4 + (lane >> 3), rg = t.rt * kRows + row;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (rg < all) {
+      const long long at = ((tok0 + rg / kGqa) * p.n_q_heads + t.head * kGqa + rg % kGqa) * kD;
+      a = load4(p.q_type, p.q, at + q_dim<KT>(slot, 0));
+      b = load4(p.q_type, p.q, at + q_dim<KT>(slot, 1));
+    }
+    uint4 v;
+    if (KT == PA_Q4_0) v = make_uint4(pack_half2(a.x, a.z), pack_half2(a.y, a.w), pack_half2(b.x, b.z), pack_half2(b.y, b.w));
+    else v = make_uint4(pack_half2(a.x, a.y), pack_half2(a.z, a.w), pack_half2(b.x, b.y), pack_half2(b.z, b.w));
+    sts128(dst + canon(row, slot, kD / 8), v);
+  }
+}
+
+// ------------------------------------------------------------------ pairs of floats
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+// The pair of floats in two registers.
+__device__ __forceinline__ uint64_t get2(const uint32_t* r) { return pack2(__uint_as_float(r[0]), __uint_as_float(r[1])); }
+__device__ __forceinline__ void put2(uint32_t* r, uint64_t v) {
+  const float2 f = unpack2(v);
+  r[0] = __float_as_uint(f.x);
+  r[1] = __float_as_uint(f.y);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// ------------------------------------------------------------------ the roles' common parts
+
+__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t count, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, "
+      "q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
+
+// A bounded wait of the whole warp; false once any of its lanes gave up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, abort));
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// What the softmax and the MMA warp need to know of a tile; the K copy warp
+// writes it, sixteen tiles deep (the roles are never that far apart: the copy
+// stages and operand units between them hold fewer tiles).
+struct alignas(16) Tile {
+  int rows;      // query rows of the segment
+  int first;     // the first tile of a piece
+  int last;      // the last
+  int open;      // keys of the tile that every row sees (<= 0: none; >= 128: no edge here)
+  int causal;    // row r sees (row0 + r) / 6 more than `open`
+  int row0;      // first query row of the row tile
+  int slot_row;  // first slot row of the piece
+  int pad;
+};
+constexpr int kTiles = 16;
+
+// The raw K (kIsV false) or V row groups of the CTA's tiles into a ring of NS
+// stages at ring, two stages per tile.  Lane g (0..7) looks after row group g of
+// the tile; its table entry is read a tile ahead.  Returns the number of
+// stages issued.
+template <int T, bool kIsV, int NS>
+__device__ __forceinline__ int copy_role(const Params& p, Pos pos, int n, uint32_t ring, uint32_t full, uint32_t empty,
+                                         Tile* tiles, int* lefts, volatile int* abort, int lane) {
+  constexpr int GB = pa_layout::group_bytes<T>(), RB = Fmt<T>::kRow;
+  const uint8_t* pool = kIsV ? p.v_pool : p.k_pool;
+  int slot = 0, issued = 0;
+  uint32_t parity = 1;  // of the wait for a stage's previous use; flips when the ring wraps
+  int entry = -1, off = 0, left = 0;
+  auto look = [&](const Pos& t) {
+    const int k0 = pos_key0(p, t), k = k0 + kGroup * lane;
+    left = min(kKeys, pos_end(p, t) - k0);
+    entry = -1;
+    if (lane < kKeys / kGroup && kGroup * lane < left) {
+      const int page = k / p.page_size;
+      off = k - page * p.page_size;
+      entry = __ldg(p.table + (long long)pos_seq(p, t) * p.table_stride + page);
+    }
+  };
+  look(pos);
+  for (int j = 0; j < n; ++j) {
+    if (lane == 0) {
+      if (kIsV) {
+        lefts[j & (kTiles - 1)] = left;
+      } else {
+        Tile& t = tiles[j & (kTiles - 1)];
+        t.rows = pos_rows(p, pos);
+        t.first = j == 0 || pos.j == 0;
+        t.last = j + 1 == n || pos.j + 1 == pos.nt;
+        // prefix: the tile's live keys; suffix: the new tokens' keys open one by one
+        t.open = pos.pre ? pos_end(p, pos) - pos_key0(p, pos) : pos_end(p, pos) - p.n_qtok + 1 - pos_key0(p, pos);
+        t.causal = !pos.pre;
+        t.row0 = pos.rt * kRows;
+        t.slot_row = pos_slot_row(p, pos, (int)blockIdx.x);
+      }
+    }
+    const int tb = entry, head = pos.head;
+    const bool mine = lane < kKeys / kGroup && kGroup * lane < left, ok = mine && tb >= 0 && tb < p.n_blocks;
+    const uint8_t* src = pool + (((long long)tb * p.n_kv_heads + head) * p.page_size + off) * RB;
+    if (j + 1 < n) {
+      advance(p, pos);
+      look(pos);
+    }
+    const uint32_t good = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, mine && !ok);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const uint32_t fb = full + 8 * slot, dst = ring + slot * (4 * GB);
+      if (issued >= NS && !warp_wait(empty + 8 * slot, parity, p.err, abort)) return issued;
+      if (bad) {  // rows of an entry outside the pool read as zeros
+        if (lane == 0) record_error(p.err, PA_ERR_BOUNDS);
+        for (int g = 0; g < 4; ++g) {
+          if (!((bad >> (4 * half + g)) & 1)) continue;
+          for (int i = lane; i < GB / 16; i += 32) sts128_zero(dst + g * GB + 16 * i);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive_expect_tx(fb, __popc(good & (0xfu << (4 * half))) * GB);
+      __syncwarp();
+      if (ok && (lane >> 2) == half)
+        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         dst + (lane & 3) * GB),
+                     "l"(src), "r"(GB), "r"(fb)
+                     : "memory");
+      ++issued;
+      if (++slot == NS) {
+        slot = 0;
+        parity ^= 1;
+      }
+    }
+  }
+  return issued;
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int KT, int VT>
+__global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_constant__ Params p) {
+  using SM = Smem<KT, VT>;
+  constexpr int NK = SM::kKStages, NV = SM::kVStages;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  // Hand-offs (unit numbers: k_num / v_num; tile j, piece i of the CTA):
+  //   kraw_*, vraw_* [(2 j + half) % stages]  copies <-> dequantisation (four warps read a stage)
+  //   unit_full / unit_empty [number % 5]     dequantisation (four warps) <-> MMA (commit)
+  //   s_full / s_empty                  S^T(j) in tensor memory / in the softmax registers
+  //   p_full / pv_done                  P^T(j) written / O^T holds tile j, P^T free
+  //   q_full / q_empty [i & 1]          query rows of piece i staged / no longer needed
+  //   o_free                            piece i's O^T has been read
+  // A role whose wait expires stops: it arrives nowhere any more.
+  const uint32_t kraw_full = base + SM::kBar, kraw_empty = kraw_full + 8 * NK, vraw_full = kraw_empty + 8 * NK,
+                 vraw_empty = vraw_full + 8 * NV, unit_full = vraw_empty + 8 * NV,
+                 unit_empty = unit_full + 8 * kUnits, s_full = unit_empty + 8 * kUnits, s_empty = s_full + 8,
+                 p_full = s_empty + 8, pv_done = p_full + 8, q_full = pv_done + 8, q_empty = q_full + 16,
+                 o_free = q_empty + 16, drain = o_free + 8;
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + SM::kMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc + 8);
+  Pos* start = reinterpret_cast<Pos*>(smem + SM::kMisc + 16);
+  Tile* tiles = reinterpret_cast<Tile*>(smem + SM::kTile);
+  int* lefts = reinterpret_cast<int*>(smem + SM::kLeft);
+  const int first = (int)((long long)blockIdx.x * p.total_tiles / p.n_ctas),
+            n = (int)((long long)(blockIdx.x + 1) * p.total_tiles / p.n_ctas) - first;  // at least 1
+  if (tid == 0) {
+    *abort = 0;
+    for (int i = 0; i < NK; ++i) {
+      mbar_init(kraw_full + 8 * i, 1);
+      mbar_init(kraw_empty + 8 * i, 4);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(vraw_full + 8 * i, 1);
+      mbar_init(vraw_empty + 8 * i, 4);
+    }
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(unit_full + 8 * i, 4);
+      mbar_init(unit_empty + 8 * i, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_empty, 8);
+    mbar_init(p_full, 8);
+    mbar_init(pv_done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 1);
+      mbar_init(q_empty + 8 * i, 1);
+    }
+    mbar_init(o_free, 8);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (tid == 32) *start = locate(p, first);
+  if (w == 0) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // nothing that another kernel wrote is read before this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tid == 0) asm volatile("griddepcontrol.launch_dependents;");
+  // All of tensor memory is this CTA's, so its columns start at 0; written as a
+  // constant, the MMAs' addresses need no register that the compiler would have
+  // to prove uniform.
+  const bool whole = *tmem_slot == 0;
+  if (!whole && tid == 0) record_error(p.err, PA_ERR_CUDA);
+  int issued_k = 0, issued_v = 0;  // copy stages (the copy warps')
+
+  if (!whole) {
+  } else if (w == kCopyKWarp) {
+    issued_k = copy_role<KT, false, NK>(p, *start, n, base + SM::kRing, kraw_full, kraw_empty, tiles, lefts, abort, lane);
+  } else if (w == kCopyVWarp) {
+    issued_v = copy_role<VT, true, NV>(p, *start, n, base + SM::kVRing, vraw_full, vraw_empty, tiles, lefts, abort, lane);
+  } else if (w < kVWarp0) {
+    // ---- K: thread = key (position 32 * quarter + lane), dims 128 kd .. + 127
+    const int kd = w >> 2, quarter = w & 3, at = 32 * quarter + lane;
+    const int r = key16(lane & 15);
+    const uint32_t grp = base + SM::kRing + ((at >> 4) & 3) * pa_layout::group_bytes<KT>();
+    const uint32_t t_lane = (uint32_t)(32 * quarter) << 16;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t stage = 2 * j + (quarter >> 1), slot = stage % NK, unit = k_num(j) + kd, us = unit % kUnits;
+      if (!warp_wait(kraw_full + 8 * slot, (stage / NK) & 1, p.err, abort)) break;
+      if (unit >= kUnits && !warp_wait(unit_empty + 8 * us, (unit / kUnits - 1) & 1, p.err, abort)) break;
+      tc_fence_after();
+      dequant_k<KT>(grp + slot * SM::kKStage, r, kd, kUnitCol + 64 * us + t_lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(kraw_empty + 8 * slot);
+      __syncwarp();
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(unit_full + 8 * us);
+    }
+  } else if (w < kSmWarp0) {
+    // ---- V: keys 64 vh .. + 63 of the tile, block `quarter` of each half of the dims
+    const int vh = (w - kVWarp0) >> 2, quarter = w & 3;
+    const uint32_t t_lane = (uint32_t)(32 * quarter) << 16;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t stage = 2 * j + vh, slot = stage % NV, num = v_num(j, n) + vh, us = num % kUnits;
+      if (!warp_wait(vraw_full + 8 * slot, (stage / NV) & 1, p.err, abort)) break;
+      if (num >= kUnits && !warp_wait(unit_empty + 8 * us, (num / kUnits - 1) & 1, p.err, abort)) break;
+      tc_fence_after();
+      dequant_v<VT>(base + SM::kVRing + slot * SM::kVStage, quarter, lefts[j & (kTiles - 1)] - kStageKeys * vh,
+                    kUnitCol + 64 * us + t_lane, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(vraw_empty + 8 * slot);
+      __syncwarp();
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(unit_full + 8 * us);
+    }
+  } else if (w == kMmaWarp) {
+    // ---- MMA issue by one elected lane
+    const uint64_t qdesc = smem_desc(base + SM::kQ, 128, 4096), pdesc = smem_desc(base + SM::kP, 128, 2048);
+    const bool leader = elect_one();
+    int piece = -1, prev_piece = 0;
+    uint32_t prev_idesc = 0;
+    bool prev_first = false, live = true;
+    auto pv = [&](int jj, bool first_tile, int pc, uint32_t idesc) -> bool {
+      if (!warp_wait(p_full, jj & 1, p.err, abort)) return false;
+      if (first_tile && pc > 0 && !warp_wait(o_free, (pc - 1) & 1, p.err, abort)) return false;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t num = v_num(jj, n) + h, us = num % kUnits;
+        if (!warp_wait(unit_full + 8 * us, (num / kUnits) & 1, p.err, abort)) return false;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t a = kUnitCol + 64 * us, acc = (first_tile && h == 0) ? 0u : 1u;
+          const uint64_t pd = pdesc + 64 * h;
+#pragma unroll
+          for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f16_tmem_a(kOCol + 64 * mb, a + 32 * mb + 8 * kk, pd + 16 * kk, idesc, kk ? 1u : acc);
+          tc_commit(unit_empty + 8 * us);
+          if (h) tc_commit(pv_done);
+        }
+        __syncwarp();
+      }
+      return true;
+    };
+    for (int j = 0; j < n; ++j) {
+      const uint32_t num0 = k_num(j);
+      live = warp_wait(unit_full + 8 * (num0 % kUnits), (num0 / kUnits) & 1, p.err, abort);
+      if (!live) break;
+      const Tile& t = tiles[j & (kTiles - 1)];
+      const bool first_tile = t.first, last_tile = t.last;
+      const uint32_t idesc = idesc_f16_f32(128, 0) | ((uint32_t)((t.rows + 15) >> 4) << 18);
+      if (first_tile) {
+        ++piece;
+        live = warp_wait(q_full + 8 * (piece & 1), (piece >> 1) & 1, p.err, abort);
+      }
+      if (live && j > 0) live = warp_wait(s_empty, (j - 1) & 1, p.err, abort);
+      if (!live) break;
+      const uint64_t qd0 = qdesc + (uint64_t)((piece & 1) * (SM::kQBytes >> 4));
+#pragma unroll 1
+      for (int d = 0; d < 2; ++d) {
+        const uint32_t num = num0 + d, us = num % kUnits;
+        live = warp_wait(unit_full + 8 * us, (num / kUnits) & 1, p.err, abort);
+        if (!live) break;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t a = kUnitCol + 64 * us;
+          const uint64_t qd = qd0 + 128 * d;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) tc_mma_f16_tmem_a(kSCol, a + 8 * ks, qd + 16 * ks, idesc, ks ? 1u : (uint32_t)d);
+          tc_commit(unit_empty + 8 * us);
+          if (d) {
+            tc_commit(s_full);
+            if (last_tile) tc_commit(q_empty + 8 * (piece & 1));
+          }
+        }
+        __syncwarp();
+      }
+      if (!live) break;
+      if (j > 0) live = pv(j - 1, prev_first, prev_piece, prev_idesc);
+      if (!live) break;
+      prev_first = first_tile;
+      prev_piece = piece;
+      prev_idesc = idesc;
+    }
+    live = live && pv(n - 1, prev_first, prev_piece, prev_idesc);
+    // the last commits have arrived before the CTA's barriers go away
+    for (int u = max(0, 4 * n - kUnits); live && u < 4 * n; ++u)
+      live = warp_wait(unit_empty + 8 * (u % kUnits), (u / kUnits) & 1, p.err, abort);
+    for (int i = max(0, piece - 1); live && i <= piece; ++i)
+      live = warp_wait(q_empty + 8 * (i & 1), (i >> 1) & 1, p.err, abort);
+    if (live) live = warp_wait(pv_done, (n - 1) & 1, p.err, abort);
+    if (!live) {  // what was issued ends before shared and tensor memory are released
+      if (leader) tc_commit(drain);
+      mbar_wait(drain, 0, p.err, abort, /*honour_abort=*/false);
+    }
+    __syncwarp();
+  } else if (w == kQWarp) {
+    // ---- query rows of the pieces after the first: a piece ends with its segment
+    Pos pos = *start;
+    int piece = 0;
+    for (int j = pos.nt - pos.j; j < n; j += pos.nt) {
+      pos.j = pos.nt - 1;
+      advance(p, pos);
+      ++piece;
+      if (piece >= 2 && !warp_wait(q_empty + 8 * (piece & 1), ((piece >> 1) - 1) & 1, p.err, abort)) break;
+      stage_q<KT>(p, pos, base + SM::kQ + (piece & 1) * SM::kQBytes, (pos_rows(p, pos) + 15) & ~15, 0, 1, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full + 8 * (piece & 1));
+    }
+  } else {
+    // ---- softmax: keys 16 hh + 32 quarter .. + 15 of the tile, all query rows;
+    // thread 4g + t holds keys g and g + 8 and columns 2t, 2t + 1 of every 8
+    const int sw = w - kSmWarp0, hh = sw >> 2, quarter = w & 3, g = lane >> 2, t2 = 2 * (lane & 3), st = tid - 32 * kSmWarp0;
+    {
+      const Pos pos = *start;
+      stage_q<KT>(p, pos, base + SM::kQ, (pos_rows(p, pos) + 15) & ~15, sw, 8, lane);
+    }
+    fence_proxy_async_smem();
+    named_bar_sync(1, kSmThreads);
+    if (st == 0) mbar_arrive(q_full);
+    float* red = reinterpret_cast<float*>(smem + SM::kRed);
+    float* nref = reinterpret_cast<float*>(smem + SM::kRef);      // minus the reference maximum
+    float* ndelta = reinterpret_cast<float*>(smem + SM::kDelta);  // minus what it was raised by
+    float* alpha = reinterpret_cast<float*>(smem + SM::kAlpha);
+    const uint32_t s_addr = kSCol + ((uint32_t)(32 * quarter + 16 * hh) << 16);
+    const uint32_t o_addr = kOCol + 64 * hh + ((uint32_t)(32 * quarter) << 16);
+    const int tile_key = 16 * (2 * quarter + hh);
+    const uint32_t p_addr = base + SM::kP + canon(8 * (lane >> 4) + (lane & 7), 4 * quarter + 2 * hh + ((lane >> 3) & 1), kKeys / 8);
+    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+    uint64_t l[4][2];  // sums of weights over this thread's keys: rows (16c + 8e + 2t, + 1)
+    bool live = true;  // a warp whose wait expired keeps to the group's barriers but arrives nowhere
+    for (int j = 0; j < n; ++j) {
+      live = live && warp_wait(s_full, j & 1, p.err, abort);
+      tc_fence_after();
+      const Tile& tl = tiles[j & (kTiles - 1)];
+      const int rows = tl.rows, nc = (rows + 15) >> 4, first_tile = tl.first, last_tile = tl.last, open = tl.open;
+      const long long slot = tl.slot_row;
+      uint32_t x[4][8];  // [16 columns][(8 columns e, key g or g + 8, column 2t or 2t + 1): 4e + 2k + i], floats
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < nc) tmem_ld_frag2(s_addr + 16 * c, x[c]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) loaded(x[c]);
+      tc_fence_before();
+      __syncwarp();
+      if (live && lane == 0) mbar_arrive(s_empty);
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c >= nc) continue;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint64_t m = first_tile ? 0ull : *reinterpret_cast<const uint64_t*>(nref + 16 * c + 8 * e + t2);
+          put2(x[c] + 4 * e, fma2(get2(x[c] + 4 * e), scale2, m));
+          put2(x[c] + 4 * e + 2, fma2(get2(x[c] + 4 * e + 2), scale2, m));
+        }
+      }
+      if (open < kKeys) {  // the edge: mask
+        const int ka = tile_key + key16(g), kb = tile_key + key16(g + 8), causal = tl.causal, row0 = tl.row0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c >= nc) continue;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = row0 + 16 * c + 8 * (i >> 2) + t2 + (i & 1);
+            if (((i & 2) ? kb : ka) >= open + (causal ? row / kGqa : 0)) x[c][i] = 0xff800000u;  // -inf
+          }
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c >= nc) continue;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])));
+      }
+      if (bar_or(1, kSmThreads, first_tile || top > kLazyLog2)) {
+        // ---- raise the reference maxima (always at a piece's first tile)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c >= nc) continue;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float u = fmaxf(__uint_as_float(x[c][4 * e]), __uint_as_float(x[c][4 * e + 2])),
+                  v = fmaxf(__uint_as_float(x[c][4 * e + 1]), __uint_as_float(x[c][4 * e + 3]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            }
+            if (g == 0) *reinterpret_cast<float2*>(red + sw * kRows + 16 * c + 8 * e + t2) = make_float2(u, v);
+          }
+        }
+        __syncwarp();
+        named_bar_sync(1, kSmThreads);
+        if (st < 16 * nc) {
+          float v = red[st];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) v = fmaxf(v, red[i * kRows + st]);
+          // a row that sees no key yet keeps a reference of 0; it will see none later in the piece either
+          const float d = first_tile ? (v == -INFINITY ? 0.f : v) : fmaxf(v, 0.f);
+          nref[st] = first_tile ? -d : nref[st] - d;
+          ndelta[st] = -d;
+          alpha[st] = ex2(-d);
+        }
+        __syncwarp();
+        named_bar_sync(1, kSmThreads);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c >= nc) continue;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t d = *reinterpret_cast<const uint64_t*>(ndelta + 16 * c + 8 * e + t2);
+            put2(x[c] + 4 * e, add2(get2(x[c] + 4 * e), d));
+            put2(x[c] + 4 * e + 2, add2(get2(x[c] + 4 * e + 2), d));
+            l[c][e] = first_tile ? 0ull : mul2(l[c][e], *reinterpret_cast<const uint64_t*>(alpha + 16 * c + 8 * e + t2));
+          }
+        }
+        if (!first_tile) {  // O^T holds the tiles before: dims of this warp, every row
+          live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < nc; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o_addr + 16 * c, o);
+            tmem_ld_wait();
+            loaded(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[16 * c + i]);
+            tmem_st16(o_addr + 16 * c, o);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+        }
+      }
+      if (j > 0) live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);  // P^T(j - 1) has been read
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c >= nc) continue;
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = ex2(__uint_as_float(x[c][2 * i])), b = ex2(__uint_as_float(x[c][2 * i + 1]));
+          l[c][i >> 1] = add2(l[c][i >> 1], pack2(a, b));
+          h[i] = pack_half2(a, b);
+        }
+        stsm_x4_trans(p_addr + c * (16 * kKeys * 2), h[0], h[1], h[2], h[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (live && lane == 0) mbar_arrive(p_full);
+      __syncwarp();
+      if (last_tile) {
+        // ---- the piece: sums of weights over the keys, then O^T
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c >= nc) continue;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float2 v = unpack2(l[c][e]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+              v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+            }
+            if (g == 0) *reinterpret_cast<float2*>(red + sw * kRows + 16 * c + 8 * e + t2) = v;
+          }
+        }
+        __syncwarp();
+        named_bar_sync(1, kSmThreads);
+        if (st < rows) {
+          float v = red[st];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) v += red[i * kRows + st];
+          p.part_ml[slot + st] = make_float2(-nref[st], v);
+        }
+        live = live && warp_wait(pv_done, j & 1, p.err, abort);
+        tc_fence_after();
+        float* dst = p.part_o + slot * kD + 128 * hh + 32 * quarter + v_dim<VT>(lane);
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+          uint32_t o[16];
+          tmem_ld16(o_addr + 16 * c, o);
+          tmem_ld_wait();
+          loaded(o);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (16 * c + i < rows) dst[(16 * c + i) * kD] = __uint_as_float(o[i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (live && lane == 0) mbar_arrive(o_free);
+        __syncwarp();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  // after an expired wait, copies that nobody waited for must still land
+  if (w == kCopyKWarp && *abort) {
+    for (int i = max(0, issued_k - NK); i < issued_k; ++i)
+      mbar_wait(kraw_full + 8 * (i % NK), (uint32_t)((i / NK) & 1), p.err, abort, false, kWaitTimeoutNs / 8);
+  }
+  if (w == kCopyVWarp && *abort) {
+    for (int i = max(0, issued_v - NV); i < issued_v; ++i)
+      mbar_wait(vraw_full + 8 * (i % NV), (uint32_t)((i / NV) & 1), p.err, abort, false, kWaitTimeoutNs / 8);
+  }
+  if (w == 0) {
+    tc_fence_after();
+    tmem_dealloc(*tmem_slot, kTmemCols);
+  }
+}
+
+struct KernelInfo {
+  void (*fn)(Params);
+  int smem;
+};
+
+#define PA_DECLARE_PREFIX(k, v) bool lookup_prefix_kernel_##k##_##v(KernelInfo* out);
+PA_DECLARE_PREFIX(1, 1) PA_DECLARE_PREFIX(1, 2) PA_DECLARE_PREFIX(1, 8)
+PA_DECLARE_PREFIX(2, 1) PA_DECLARE_PREFIX(2, 2) PA_DECLARE_PREFIX(2, 8)
+PA_DECLARE_PREFIX(8, 1) PA_DECLARE_PREFIX(8, 2) PA_DECLARE_PREFIX(8, 8)
+#undef PA_DECLARE_PREFIX
+
+}  // namespace pa_prefix
