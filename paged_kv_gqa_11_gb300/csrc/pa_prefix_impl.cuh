@@ -57,6 +57,8 @@
 // a second product and half again the dequantisation.
 #pragma once
 
+#include <type_traits>
+
 #include "pa_decode_impl.cuh"
 
 namespace pa_prefix {
@@ -180,8 +182,8 @@ __device__ __forceinline__ int pos_slot_row(const Params& p, const Pos& t, int c
 
 // Operand units are numbered in the order of consumption: the two of K(j), and
 // the two of V(j), of a CTA's n tiles.
-__device__ __forceinline__ int k_num(int j) { return j == 0 ? 0 : 4 * j - 2; }
-__device__ __forceinline__ int v_num(int j, int n) { return j == n - 1 ? 4 * j + 2 : 4 * j + 4; }
+__device__ __forceinline__ uint32_t k_num(uint32_t j) { return j == 0 ? 0 : 4 * j - 2; }
+__device__ __forceinline__ uint32_t v_num(uint32_t j, uint32_t n) { return j + 1 == n ? 4 * j + 2 : 4 * j + 4; }
 
 // The row of a 16-key group at position p of the tile's key order.
 __host__ __device__ constexpr int key16(int p) {
@@ -221,8 +223,8 @@ struct Smem {
   static constexpr int kRed = kVRing + kVStages * kVStage;
   static constexpr int kRef = kRed + 8 * kRows * 4, kDelta = kRef + kRows * 4, kAlpha = kDelta + kRows * 4;
   static constexpr int kTile = kAlpha + kRows * 4, kLeft = kTile + 16 * 32, kBar = kLeft + 64;
-  // K and V raw full / empty [stages], unit full / empty [5], s full / empty, p full, pv done, q full / empty [2], o free, drain
-  static constexpr int kNBar = 2 * (kKStages + kVStages) + 2 * kUnits + 4 + 4 + 2;
+  // K and V raw full / empty [stages], unit full / empty [5], s full / empty, p full, pv done, q full / empty [2], o free, drain, sink
+  static constexpr int kNBar = 2 * (kKStages + kVStages) + 2 * kUnits + 4 + 4 + 3;
   static constexpr int kMisc = kBar + 8 * kNBar;  // abort, tmem base, the first tile's place
   static constexpr int kTotal = kMisc + 16 + 32;
   static constexpr int kLaunch = kTotal + 1024;  // the base is aligned to 1024 inside
@@ -429,27 +431,55 @@ __device__ __forceinline__ float4 load4(int type, const uint8_t* base, long long
                      __uint_as_float(v.y & 0xffff0000u));
 }
 
-// Worker w of nw (warps) stages its share of the segment's query rows as
-// binary16 into the B operand at dst, in K's dim order; rows past the segment's
-// up to n (a multiple of 16) are zeros.
+// Worker w of nw (warps) stages row groups w, w + nw, ... of eight of the
+// segment's query rows as binary16 into the B operand at dst, in K's dim order;
+// rows past the segment's, up to n (a multiple of 16), are zeros.  Lane: row
+// lane % 8, slots lane / 8 + 4 i; half of a row group's loads are in flight at once.
+template <int KT, int QT>
+__device__ __forceinline__ void stage_q_as(const Params& p, const Pos& t, uint32_t dst, int n, int w, int nw, int lane) {
+  const int rows = pos_rows(p, t), s4 = lane >> 3;
+  const long long tok0 = (long long)pos_seq(p, t) * p.n_qtok;
+#pragma unroll 1
+  for (int r8 = 8 * w; r8 < n; r8 += 8 * nw) {
+    const int row = r8 + (lane & 7), rg = t.rt * kRows + row;
+    const uint32_t to = dst + canon(row, s4, kD / 8);
+    if (r8 >= rows) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sts128_zero(to + 512 * i);
+      continue;
+    }
+    const bool real = row < rows;
+    const long long at = ((tok0 + rg / kGqa) * p.n_q_heads + t.head * kGqa + rg % kGqa) * kD;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float4 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int slot = s4 + 4 * (4 * h + i);
+        a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (real) {
+          a[i] = load4(QT, p.q, at + q_dim<KT>(slot, 0));
+          b[i] = load4(QT, p.q, at + q_dim<KT>(slot, 1));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint4 v;
+        if (KT == PA_Q4_0)
+          v = make_uint4(pack_half2(a[i].x, a[i].z), pack_half2(a[i].y, a[i].w), pack_half2(b[i].x, b[i].z), pack_half2(b[i].y, b[i].w));
+        else
+          v = make_uint4(pack_half2(a[i].x, a[i].y), pack_half2(a[i].z, a[i].w), pack_half2(b[i].x, b[i].y), pack_half2(b[i].z, b[i].w));
+        sts128(to + 512 * (4 * h + i), v);
+      }
+    }
+  }
+}
+
 template <int KT>
 __device__ __forceinline__ void stage_q(const Params& p, const Pos& t, uint32_t dst, int n, int w, int nw, int lane) {
-  const int all = kGqa * p.n_qtok * (t.pre ? p.group_seqs[t.unit] : 1);
-  const long long tok0 = (long long)pos_seq(p, t) * p.n_qtok;
-#pragma unroll 4
-  for (int it = w; it < n; it += nw) {  // (row group of 8, slot group of 4): n / 8 * 8 of them
-    const int row = (it >> 3) * 8 + (lane & 7), slot = (it & 7) * 4 + (lane >> 3), rg = t.rt * kRows + row;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    if (rg < all) {
-      const long long at = ((tok0 + rg / kGqa) * p.n_q_heads + t.head * kGqa + rg % kGqa) * kD;
-      a = load4(p.q_type, p.q, at + q_dim<KT>(slot, 0));
-      b = load4(p.q_type, p.q, at + q_dim<KT>(slot, 1));
-    }
-    uint4 v;
-    if (KT == PA_Q4_0) v = make_uint4(pack_half2(a.x, a.z), pack_half2(a.y, a.w), pack_half2(b.x, b.z), pack_half2(b.y, b.w));
-    else v = make_uint4(pack_half2(a.x, a.y), pack_half2(a.z, a.w), pack_half2(b.x, b.y), pack_half2(b.z, b.w));
-    sts128(dst + canon(row, slot, kD / 8), v);
-  }
+  if (p.q_type == PA_DT_F32) stage_q_as<KT, PA_DT_F32>(p, t, dst, n, w, nw, lane);
+  else if (p.q_type == PA_DT_F16) stage_q_as<KT, PA_DT_F16>(p, t, dst, n, w, nw, lane);
+  else stage_q_as<KT, PA_DT_BF16>(p, t, dst, n, w, nw, lane);
 }
 
 // ------------------------------------------------------------------ pairs of floats
@@ -500,29 +530,45 @@ __device__ __forceinline__ bool bar_or(uint32_t id, uint32_t count, bool x) {
   return r != 0;
 }
 
-// A bounded wait of the whole warp; false once any of its lanes gave up.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, abort));
+// Out-of-line part of warp_wait: false once the wait gave up (after
+// kWaitTimeoutNs, which is recorded) or another role had to.
+template <bool kSleep>
+__device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort) {
+  const uint64_t t0 = globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (kSleep) __nanosleep(100);
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if ((i & 63u) == 0) {
+      const bool late = globaltimer() - t0 > kWaitTimeoutNs;
+      if (late) {
+        record_error(err, PA_ERR_TIMEOUT);
+        *abort = 1;
+      }
+      if (__any_sync(0xffffffffu, late || *abort != 0)) return false;
+    }
+  }
 }
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
+// A bounded wait of the whole warp, which branches as one (the vote keeps it
+// free of the convergence barriers of a wait per lane).  Polls cost issue slots
+// that the other warps need: the roles that run ahead of the MMAs sleep between
+// theirs, the ones in the MMA - softmax loop do not.
+template <bool kSleep = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait_slow<kSleep>(bar, parity, err, abort);
 }
 
 // What the softmax and the MMA warp need to know of a tile; the K copy warp
 // writes it, sixteen tiles deep (the roles are never that far apart: the copy
 // stages and operand units between them hold fewer tiles).
 struct alignas(16) Tile {
-  int rows;      // query rows of the segment
-  int first;     // the first tile of a piece
-  int last;      // the last
+  uint32_t info;  // query rows of the segment | first tile of a piece << 8 | last << 9
   int open;      // keys of the tile that every row sees (<= 0: none; >= 128: no edge here)
   int causal;    // row r sees (row0 + r) / 6 more than `open`
   int row0;      // first query row of the row tile
   int slot_row;  // first slot row of the piece
-  int pad;
+  int pad[3];
 };
 constexpr int kTiles = 16;
 
@@ -555,9 +601,8 @@ __device__ __forceinline__ int copy_role(const Params& p, Pos pos, int n, uint32
         lefts[j & (kTiles - 1)] = left;
       } else {
         Tile& t = tiles[j & (kTiles - 1)];
-        t.rows = pos_rows(p, pos);
-        t.first = j == 0 || pos.j == 0;
-        t.last = j + 1 == n || pos.j + 1 == pos.nt;
+        t.info = (uint32_t)pos_rows(p, pos) | ((j == 0 || pos.j == 0) ? 1u << 8 : 0u) |
+                 ((j + 1 == n || pos.j + 1 == pos.nt) ? 1u << 9 : 0u);
         // prefix: the tile's live keys; suffix: the new tokens' keys open one by one
         t.open = pos.pre ? pos_end(p, pos) - pos_key0(p, pos) : pos_end(p, pos) - p.n_qtok + 1 - pos_key0(p, pos);
         t.causal = !pos.pre;
@@ -576,7 +621,7 @@ __device__ __forceinline__ int copy_role(const Params& p, Pos pos, int n, uint32
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       const uint32_t fb = full + 8 * slot, dst = ring + slot * (4 * GB);
-      if (issued >= NS && !warp_wait(empty + 8 * slot, parity, p.err, abort)) return issued;
+      if (issued >= NS && !warp_wait<true>(empty + 8 * slot, parity, p.err, abort)) return issued;
       if (bad) {  // rows of an entry outside the pool read as zeros
         if (lane == 0) record_error(p.err, PA_ERR_BOUNDS);
         for (int g = 0; g < 4; ++g) {
@@ -603,6 +648,40 @@ __device__ __forceinline__ int copy_role(const Params& p, Pos pos, int n, uint32
   return issued;
 }
 
+// Eight MMAs of an operand unit (columns a, a + 8, ...), issued by the lane
+// whose leader is set: D[d] += A B for the descriptor steps b, b + 16, ... (kSplit
+// false), or four into d and four into d + 64, for b .. b + 48 both times (true).
+// acc 0: the first into each D overwrites it.  One statement, so that what
+// they share is moved to uniform registers once: the issuing warp has the
+// fewest issue slots to spare (12 instructions an MMA as separate statements, 6
+// so).
+template <bool kSplit>
+__device__ __forceinline__ void mma8(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t leader) {
+#define PA_MMA(D, AOFF, BOFF, P)                          \
+  "add.u32 a1, %1, " #AOFF ";\n\tadd.u64 b1, %2, " #BOFF \
+  ";\n\t@e tcgen05.mma.cta_group::1.kind::f16 [" D "], [a1], b1, %3, " P ";\n\t"
+  if (kSplit)
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b32 a1, d1;\n\t.reg .b64 b1;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, "
+                 "%5, 0;\n\tadd.u32 d1, %0, 64;\n\t" PA_MMA("%0", 0, 0, "p") PA_MMA("%0", 8, 16, "1") PA_MMA("%0", 16, 32, "1")
+                     PA_MMA("%0", 24, 48, "1") PA_MMA("d1", 32, 0, "p") PA_MMA("d1", 40, 16, "1") PA_MMA("d1", 48, 32, "1")
+                         PA_MMA("d1", 56, 48, "1") "}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
+                 : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, "
+                 "0;\n\t" PA_MMA("%0", 0, 0, "p") PA_MMA("%0", 8, 16, "1") PA_MMA("%0", 16, 32, "1") PA_MMA("%0", 24, 48, "1")
+                     PA_MMA("%0", 32, 64, "1") PA_MMA("%0", 40, 80, "1") PA_MMA("%0", 48, 96, "1") PA_MMA("%0", 56, 112, "1") "}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
+                 : "memory");
+#undef PA_MMA
+}
+
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+
 // ------------------------------------------------------------------ the kernel
 
 template <int KT, int VT>
@@ -626,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
                  vraw_empty = vraw_full + 8 * NV, unit_full = vraw_empty + 8 * NV,
                  unit_empty = unit_full + 8 * kUnits, s_full = unit_empty + 8 * kUnits, s_empty = s_full + 8,
                  p_full = s_empty + 8, pv_done = p_full + 8, q_full = pv_done + 8, q_empty = q_full + 16,
-                 o_free = q_empty + 16, drain = o_free + 8;
+                 o_free = q_empty + 16, drain = o_free + 8, sink = drain + 8;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + SM::kMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc + 8);
   Pos* start = reinterpret_cast<Pos*>(smem + SM::kMisc + 16);
@@ -658,6 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     }
     mbar_init(o_free, 8);
     mbar_init(drain, 1);
+    mbar_init(sink, 1);
     fence_mbar_init();
   }
   if (tid == 32) *start = locate(p, first);
@@ -691,8 +771,8 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     const uint32_t t_lane = (uint32_t)(32 * quarter) << 16;
     for (int j = 0; j < n; ++j) {
       const uint32_t stage = 2 * j + (quarter >> 1), slot = stage % NK, unit = k_num(j) + kd, us = unit % kUnits;
-      if (!warp_wait(kraw_full + 8 * slot, (stage / NK) & 1, p.err, abort)) break;
-      if (unit >= kUnits && !warp_wait(unit_empty + 8 * us, (unit / kUnits - 1) & 1, p.err, abort)) break;
+      if (!warp_wait<true>(kraw_full + 8 * slot, (stage / NK) & 1, p.err, abort)) break;
+      if (unit >= kUnits && !warp_wait<true>(unit_empty + 8 * us, (unit / kUnits - 1) & 1, p.err, abort)) break;
       tc_fence_after();
       dequant_k<KT>(grp + slot * SM::kKStage, r, kd, kUnitCol + 64 * us + t_lane);
       __syncwarp();
@@ -709,8 +789,8 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     const uint32_t t_lane = (uint32_t)(32 * quarter) << 16;
     for (int j = 0; j < n; ++j) {
       const uint32_t stage = 2 * j + vh, slot = stage % NV, num = v_num(j, n) + vh, us = num % kUnits;
-      if (!warp_wait(vraw_full + 8 * slot, (stage / NV) & 1, p.err, abort)) break;
-      if (num >= kUnits && !warp_wait(unit_empty + 8 * us, (num / kUnits - 1) & 1, p.err, abort)) break;
+      if (!warp_wait<true>(vraw_full + 8 * slot, (stage / NV) & 1, p.err, abort)) break;
+      if (num >= kUnits && !warp_wait<true>(unit_empty + 8 * us, (num / kUnits - 1) & 1, p.err, abort)) break;
       tc_fence_after();
       dequant_v<VT>(base + SM::kVRing + slot * SM::kVStage, quarter, lefts[j & (kTiles - 1)] - kStageKeys * vh,
                     kUnitCol + 64 * us + t_lane, lane);
@@ -723,84 +803,66 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       if (lane == 0) mbar_arrive(unit_full + 8 * us);
     }
   } else if (w == kMmaWarp) {
-    // ---- MMA issue by one elected lane
+    // ---- MMA issue: the whole warp runs the loop and an elected lane issues, so
+    // that the operands stay in uniform registers: what comes from shared memory
+    // goes through a warp reduction, and an expired wait leaves the control flow
+    // as it is -- from then on all commits go to a barrier that nobody waits on.
     const uint64_t qdesc = smem_desc(base + SM::kQ, 128, 4096), pdesc = smem_desc(base + SM::kP, 128, 2048);
-    const bool leader = elect_one();
-    int piece = -1, prev_piece = 0;
-    uint32_t prev_idesc = 0;
-    bool prev_first = false, live = true;
-    auto pv = [&](int jj, bool first_tile, int pc, uint32_t idesc) -> bool {
-      if (!warp_wait(p_full, jj & 1, p.err, abort)) return false;
-      if (first_tile && pc > 0 && !warp_wait(o_free, (pc - 1) & 1, p.err, abort)) return false;
-#pragma unroll 1
+    bool dead = false;
+    auto wait = [&](uint32_t bar, uint32_t parity) { dead |= !warp_wait(bar, parity, p.err, abort); };
+    auto commit = [&](uint32_t bar) { tc_commit_warp(dead ? sink : bar); };
+    const uint32_t leader = elect_one();
+    uint32_t piece = 0, prev_info = 0;
+    auto idesc_of = [](uint32_t info) { return idesc_f16_f32(128, 0) | (((info & 0xffu) + 15) >> 4 << 18); };
+    // O^T += V^T P^T of tile jj, of piece number pc (from 1)
+    auto pv = [&](uint32_t jj, uint32_t info, uint32_t pc) {
+      const bool first_tile = (info >> 8) & 1;
+      const uint32_t idesc = idesc_of(info);
+      wait(p_full, jj & 1);
+      if (first_tile && pc > 1) wait(o_free, pc & 1);
+#pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t num = v_num(jj, n) + h, us = num % kUnits;
-        if (!warp_wait(unit_full + 8 * us, (num / kUnits) & 1, p.err, abort)) return false;
+        wait(unit_full + 8 * us, (num / kUnits) & 1);
         tc_fence_after();
-        if (leader) {
-          const uint32_t a = kUnitCol + 64 * us, acc = (first_tile && h == 0) ? 0u : 1u;
-          const uint64_t pd = pdesc + 64 * h;
-#pragma unroll
-          for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_f16_tmem_a(kOCol + 64 * mb, a + 32 * mb + 8 * kk, pd + 16 * kk, idesc, kk ? 1u : acc);
-          tc_commit(unit_empty + 8 * us);
-          if (h) tc_commit(pv_done);
-        }
-        __syncwarp();
+        mma8<true>(kOCol, kUnitCol + 64 * us, pdesc + 64 * h, idesc, (h == 0 && first_tile) ? 0u : 1u, leader);
+        commit(unit_empty + 8 * us);
       }
-      return true;
+      commit(pv_done);
     };
-    for (int j = 0; j < n; ++j) {
+    for (uint32_t j = 0; j < (uint32_t)n; ++j) {
       const uint32_t num0 = k_num(j);
-      live = warp_wait(unit_full + 8 * (num0 % kUnits), (num0 / kUnits) & 1, p.err, abort);
-      if (!live) break;
-      const Tile& t = tiles[j & (kTiles - 1)];
-      const bool first_tile = t.first, last_tile = t.last;
-      const uint32_t idesc = idesc_f16_f32(128, 0) | ((uint32_t)((t.rows + 15) >> 4) << 18);
-      if (first_tile) {
+      wait(unit_full + 8 * (num0 % kUnits), (num0 / kUnits) & 1);
+      const uint32_t info = __reduce_or_sync(0xffffffffu, tiles[j & (kTiles - 1)].info);
+      const uint32_t prev_piece = piece;
+      if ((info >> 8) & 1) {
+        wait(q_full + 8 * (piece & 1), (piece >> 1) & 1);
         ++piece;
-        live = warp_wait(q_full + 8 * (piece & 1), (piece >> 1) & 1, p.err, abort);
       }
-      if (live && j > 0) live = warp_wait(s_empty, (j - 1) & 1, p.err, abort);
-      if (!live) break;
-      const uint64_t qd0 = qdesc + (uint64_t)((piece & 1) * (SM::kQBytes >> 4));
-#pragma unroll 1
+      if (j > 0) wait(s_empty, (j - 1) & 1);
+      const uint64_t qd = qdesc + (uint64_t)(((piece - 1) & 1) * (SM::kQBytes >> 4));
+      const uint32_t idesc = idesc_of(info);
+#pragma unroll
       for (int d = 0; d < 2; ++d) {
         const uint32_t num = num0 + d, us = num % kUnits;
-        live = warp_wait(unit_full + 8 * us, (num / kUnits) & 1, p.err, abort);
-        if (!live) break;
+        if (d) wait(unit_full + 8 * us, (num / kUnits) & 1);
         tc_fence_after();
-        if (leader) {
-          const uint32_t a = kUnitCol + 64 * us;
-          const uint64_t qd = qd0 + 128 * d;
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) tc_mma_f16_tmem_a(kSCol, a + 8 * ks, qd + 16 * ks, idesc, ks ? 1u : (uint32_t)d);
-          tc_commit(unit_empty + 8 * us);
-          if (d) {
-            tc_commit(s_full);
-            if (last_tile) tc_commit(q_empty + 8 * (piece & 1));
-          }
-        }
-        __syncwarp();
+        mma8<false>(kSCol, kUnitCol + 64 * us, qd + 128 * d, idesc, (uint32_t)d, leader);
+        commit(unit_empty + 8 * us);
       }
-      if (!live) break;
-      if (j > 0) live = pv(j - 1, prev_first, prev_piece, prev_idesc);
-      if (!live) break;
-      prev_first = first_tile;
-      prev_piece = piece;
-      prev_idesc = idesc;
+      commit(s_full);
+      if ((info >> 9) & 1) commit(q_empty + 8 * ((piece - 1) & 1));
+      if (j > 0) pv(j - 1, prev_info, prev_piece);
+      prev_info = info;
     }
-    live = live && pv(n - 1, prev_first, prev_piece, prev_idesc);
+    pv(n - 1, prev_info, piece);
     // the last commits have arrived before the CTA's barriers go away
-    for (int u = max(0, 4 * n - kUnits); live && u < 4 * n; ++u)
-      live = warp_wait(unit_empty + 8 * (u % kUnits), (u / kUnits) & 1, p.err, abort);
-    for (int i = max(0, piece - 1); live && i <= piece; ++i)
-      live = warp_wait(q_empty + 8 * (i & 1), (i >> 1) & 1, p.err, abort);
-    if (live) live = warp_wait(pv_done, (n - 1) & 1, p.err, abort);
-    if (!live) {  // what was issued ends before shared and tensor memory are released
-      if (leader) tc_commit(drain);
+    for (uint32_t u = 4 * n < kUnits ? 0 : 4 * n - kUnits; u < 4u * n; ++u)
+      wait(unit_empty + 8 * (u % kUnits), (u / kUnits) & 1);
+    for (uint32_t i = piece < 2 ? 0 : piece - 2; i < piece; ++i) wait(q_empty + 8 * (i & 1), (i >> 1) & 1);
+    wait(pv_done, (n - 1) & 1);
+    if (dead) {  // what was issued ends before shared and tensor memory are released
+      tc_commit_warp(drain);
       mbar_wait(drain, 0, p.err, abort, /*honour_abort=*/false);
     }
     __syncwarp();
@@ -812,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       pos.j = pos.nt - 1;
       advance(p, pos);
       ++piece;
-      if (piece >= 2 && !warp_wait(q_empty + 8 * (piece & 1), ((piece >> 1) - 1) & 1, p.err, abort)) break;
+      if (piece >= 2 && !warp_wait<true>(q_empty + 8 * (piece & 1), ((piece >> 1) - 1) & 1, p.err, abort)) break;
       stage_q<KT>(p, pos, base + SM::kQ + (piece & 1) * SM::kQBytes, (pos_rows(p, pos) + 15) & ~15, 0, 1, lane);
       fence_proxy_async_smem();
       __syncwarp();
@@ -840,122 +902,127 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     uint64_t l[4][2];  // sums of weights over this thread's keys: rows (16c + 8e + 2t, + 1)
     bool live = true;  // a warp whose wait expired keeps to the group's barriers but arrives nowhere
-    for (int j = 0; j < n; ++j) {
-      live = live && warp_wait(s_full, j & 1, p.err, abort);
-      tc_fence_after();
+    // One tile, its query rows NC times 16.
+    auto tile = [&](auto width, const int j, const uint32_t info) {
+      constexpr int NC = decltype(width)::value;
       const Tile& tl = tiles[j & (kTiles - 1)];
-      const int rows = tl.rows, nc = (rows + 15) >> 4, first_tile = tl.first, last_tile = tl.last, open = tl.open;
+      const int rows = info & 0xff, open = tl.open;
+      const bool first_tile = (info >> 8) & 1, last_tile = (info >> 9) & 1;
       const long long slot = tl.slot_row;
-      uint32_t x[4][8];  // [16 columns][(8 columns e, key g or g + 8, column 2t or 2t + 1): 4e + 2k + i], floats
+      uint32_t x[NC][8];  // [16 columns][(8 columns e, key g or g + 8, column 2t or 2t + 1): 4e + 2k + i], floats
+      uint64_t sum[NC][2];
+      // The weights against the present references.  If a sum of them passes 2^8
+      // (so no single one that is used does), once more with the references
+      // raised; the first tile of a piece raises them at once.  S^T stays in
+      // tensor memory until then.
+      bool raise = first_tile;
+      if (first_tile) named_bar_sync(1, kSmThreads);  // the piece before is done with the shared arrays
+#pragma unroll 1
+      for (;;) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (c < nc) tmem_ld_frag2(s_addr + 16 * c, x[c]);
-      tmem_ld_wait();
+        for (int c = 0; c < NC; ++c) tmem_ld_frag2(s_addr + 16 * c, x[c]);
+        tmem_ld_wait();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) loaded(x[c]);
+        for (int c = 0; c < NC; ++c) {
+          loaded(x[c]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t m = first_tile ? 0ull : *reinterpret_cast<const uint64_t*>(nref + 16 * c + 8 * e + t2);
+            put2(x[c] + 4 * e, fma2(get2(x[c] + 4 * e), scale2, m));
+            put2(x[c] + 4 * e + 2, fma2(get2(x[c] + 4 * e + 2), scale2, m));
+          }
+        }
+        if (open < kKeys) {  // the edge: mask
+          const int ka = tile_key + key16(g), kb = tile_key + key16(g + 8), causal = tl.causal, row0 = tl.row0;
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = row0 + 16 * c + 8 * (i >> 2) + t2 + (i & 1);
+              if (((i & 2) ? kb : ka) >= open + (causal ? row / kGqa : 0)) x[c][i] = 0xff800000u;  // -inf
+            }
+        }
+        if (raise) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float u = fmaxf(__uint_as_float(x[c][4 * e]), __uint_as_float(x[c][4 * e + 2])),
+                    v = fmaxf(__uint_as_float(x[c][4 * e + 1]), __uint_as_float(x[c][4 * e + 3]));
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) {
+                u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+              }
+              if (g == 0) *reinterpret_cast<float2*>(red + sw * kRows + 16 * c + 8 * e + t2) = make_float2(u, v);
+            }
+          __syncwarp();
+          named_bar_sync(1, kSmThreads);
+          if (st < 16 * NC) {
+            float v = red[st];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) v = fmaxf(v, red[i * kRows + st]);
+            // a row that sees no key yet keeps a reference of 0; it will see none later in the piece either
+            const float d = first_tile ? (v == -INFINITY ? 0.f : v) : fmaxf(v, 0.f);
+            nref[st] = first_tile ? -d : nref[st] - d;
+            ndelta[st] = -d;
+            alpha[st] = ex2(-d);
+          }
+          __syncwarp();
+          named_bar_sync(1, kSmThreads);
+#pragma unroll
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint64_t d = *reinterpret_cast<const uint64_t*>(ndelta + 16 * c + 8 * e + t2);
+              put2(x[c] + 4 * e, add2(get2(x[c] + 4 * e), d));
+              put2(x[c] + 4 * e + 2, add2(get2(x[c] + 4 * e + 2), d));
+              l[c][e] = first_tile ? 0ull : mul2(l[c][e], *reinterpret_cast<const uint64_t*>(alpha + 16 * c + 8 * e + t2));
+            }
+          if (!first_tile) {  // O^T holds the tiles before: dims of this warp, every row
+            live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < NC; ++c) {
+              uint32_t o[16];
+              tmem_ld16(o_addr + 16 * c, o);
+              tmem_ld_wait();
+              loaded(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[16 * c + i]);
+              tmem_st16(o_addr + 16 * c, o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[c][i] = __float_as_uint(ex2(__uint_as_float(x[c][i])));
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            sum[c][e] = add2(get2(x[c] + 4 * e), get2(x[c] + 4 * e + 2));
+            const float2 v = unpack2(sum[c][e]);
+            top = fmaxf(top, fmaxf(v.x, v.y));
+          }
+        }
+        if (raise || !bar_or(1, kSmThreads, top > 256.f)) break;
+        raise = true;
+      }
       tc_fence_before();
       __syncwarp();
       if (live && lane == 0) mbar_arrive(s_empty);
       __syncwarp();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c >= nc) continue;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint64_t m = first_tile ? 0ull : *reinterpret_cast<const uint64_t*>(nref + 16 * c + 8 * e + t2);
-          put2(x[c] + 4 * e, fma2(get2(x[c] + 4 * e), scale2, m));
-          put2(x[c] + 4 * e + 2, fma2(get2(x[c] + 4 * e + 2), scale2, m));
-        }
-      }
-      if (open < kKeys) {  // the edge: mask
-        const int ka = tile_key + key16(g), kb = tile_key + key16(g + 8), causal = tl.causal, row0 = tl.row0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c >= nc) continue;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = row0 + 16 * c + 8 * (i >> 2) + t2 + (i & 1);
-            if (((i & 2) ? kb : ka) >= open + (causal ? row / kGqa : 0)) x[c][i] = 0xff800000u;  // -inf
-          }
-        }
-      }
-      float top = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c >= nc) continue;
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])));
-      }
-      if (bar_or(1, kSmThreads, first_tile || top > kLazyLog2)) {
-        // ---- raise the reference maxima (always at a piece's first tile)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c >= nc) continue;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float u = fmaxf(__uint_as_float(x[c][4 * e]), __uint_as_float(x[c][4 * e + 2])),
-                  v = fmaxf(__uint_as_float(x[c][4 * e + 1]), __uint_as_float(x[c][4 * e + 3]));
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-              u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-            }
-            if (g == 0) *reinterpret_cast<float2*>(red + sw * kRows + 16 * c + 8 * e + t2) = make_float2(u, v);
-          }
-        }
-        __syncwarp();
-        named_bar_sync(1, kSmThreads);
-        if (st < 16 * nc) {
-          float v = red[st];
-#pragma unroll
-          for (int i = 1; i < 8; ++i) v = fmaxf(v, red[i * kRows + st]);
-          // a row that sees no key yet keeps a reference of 0; it will see none later in the piece either
-          const float d = first_tile ? (v == -INFINITY ? 0.f : v) : fmaxf(v, 0.f);
-          nref[st] = first_tile ? -d : nref[st] - d;
-          ndelta[st] = -d;
-          alpha[st] = ex2(-d);
-        }
-        __syncwarp();
-        named_bar_sync(1, kSmThreads);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c >= nc) continue;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint64_t d = *reinterpret_cast<const uint64_t*>(ndelta + 16 * c + 8 * e + t2);
-            put2(x[c] + 4 * e, add2(get2(x[c] + 4 * e), d));
-            put2(x[c] + 4 * e + 2, add2(get2(x[c] + 4 * e + 2), d));
-            l[c][e] = first_tile ? 0ull : mul2(l[c][e], *reinterpret_cast<const uint64_t*>(alpha + 16 * c + 8 * e + t2));
-          }
-        }
-        if (!first_tile) {  // O^T holds the tiles before: dims of this warp, every row
-          live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < nc; ++c) {
-            uint32_t o[16];
-            tmem_ld16(o_addr + 16 * c, o);
-            tmem_ld_wait();
-            loaded(o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[16 * c + i]);
-            tmem_st16(o_addr + 16 * c, o);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-        }
-      }
       if (j > 0) live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);  // P^T(j - 1) has been read
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c >= nc) continue;
+      for (int c = 0; c < NC; ++c) {
         uint32_t h[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = ex2(__uint_as_float(x[c][2 * i])), b = ex2(__uint_as_float(x[c][2 * i + 1]));
-          l[c][i >> 1] = add2(l[c][i >> 1], pack2(a, b));
-          h[i] = pack_half2(a, b);
-        }
+        for (int i = 0; i < 4; ++i) h[i] = pack_half2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l[c][e] = add2(l[c][e], sum[c][e]);
         stsm_x4_trans(p_addr + c * (16 * kKeys * 2), h[0], h[1], h[2], h[3]);
       }
       fence_proxy_async_smem();
@@ -965,8 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       if (last_tile) {
         // ---- the piece: sums of weights over the keys, then O^T
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c >= nc) continue;
+        for (int c = 0; c < NC; ++c)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float2 v = unpack2(l[c][e]);
@@ -977,7 +1043,6 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
             }
             if (g == 0) *reinterpret_cast<float2*>(red + sw * kRows + 16 * c + 8 * e + t2) = v;
           }
-        }
         __syncwarp();
         named_bar_sync(1, kSmThreads);
         if (st < rows) {
@@ -990,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
         tc_fence_after();
         float* dst = p.part_o + slot * kD + 128 * hh + 32 * quarter + v_dim<VT>(lane);
 #pragma unroll 1
-        for (int c = 0; c < nc; ++c) {
+        for (int c = 0; c < NC; ++c) {
           uint32_t o[16];
           tmem_ld16(o_addr + 16 * c, o);
           tmem_ld_wait();
@@ -1004,6 +1069,16 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
         if (live && lane == 0) mbar_arrive(o_free);
         __syncwarp();
       }
+    };
+    for (int j = 0; j < n; ++j) {
+      live = live && warp_wait(s_full, j & 1, p.err, abort);
+      tc_fence_after();
+      const uint32_t info = tiles[j & (kTiles - 1)].info;
+      const int nc = ((info & 0xff) + 15) >> 4;
+      if (nc == 1) tile(std::integral_constant<int, 1>(), j, info);
+      else if (nc == 2) tile(std::integral_constant<int, 2>(), j, info);
+      else if (nc == 3) tile(std::integral_constant<int, 3>(), j, info);
+      else tile(std::integral_constant<int, 4>(), j, info);
     }
   }
   tc_fence_before();
