@@ -530,15 +530,26 @@ __device__ __forceinline__ bool bar_or(uint32_t id, uint32_t count, bool x) {
   return r != 0;
 }
 
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Out-of-line part of warp_wait: false once the wait gave up (after
 // kWaitTimeoutNs, which is recorded) or another role had to.
 template <bool kSleep>
 __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort) {
-  const uint64_t t0 = globaltimer();
+  uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
     if (kSleep) __nanosleep(100);
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    if ((i & 63u) == 0) {
+    if (__all_sync(0xffffffffu, kSleep ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity))) return true;
+    if ((i & 63u) == 0) {  // the clock is slow to read: not before the wait is long
+      if (i == 64) t0 = globaltimer();
       const bool late = globaltimer() - t0 > kWaitTimeoutNs;
       if (late) {
         record_error(err, PA_ERR_TIMEOUT);
@@ -908,122 +919,111 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       const Tile& tl = tiles[j & (kTiles - 1)];
       const int rows = info & 0xff, open = tl.open;
       const bool first_tile = (info >> 8) & 1, last_tile = (info >> 9) & 1;
-      const long long slot = tl.slot_row;
       uint32_t x[NC][8];  // [16 columns][(8 columns e, key g or g + 8, column 2t or 2t + 1): 4e + 2k + i], floats
-      uint64_t sum[NC][2];
-      // The weights against the present references.  If a sum of them passes 2^8
-      // (so no single one that is used does), once more with the references
-      // raised; the first tile of a piece raises them at once.  S^T stays in
-      // tensor memory until then.
-      bool raise = first_tile;
-      if (first_tile) named_bar_sync(1, kSmThreads);  // the piece before is done with the shared arrays
-#pragma unroll 1
-      for (;;) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) tmem_ld_frag2(s_addr + 16 * c, x[c]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          loaded(x[c]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint64_t m = first_tile ? 0ull : *reinterpret_cast<const uint64_t*>(nref + 16 * c + 8 * e + t2);
-            put2(x[c] + 4 * e, fma2(get2(x[c] + 4 * e), scale2, m));
-            put2(x[c] + 4 * e + 2, fma2(get2(x[c] + 4 * e + 2), scale2, m));
-          }
-        }
-        if (open < kKeys) {  // the edge: mask
-          const int ka = tile_key + key16(g), kb = tile_key + key16(g + 8), causal = tl.causal, row0 = tl.row0;
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int row = row0 + 16 * c + 8 * (i >> 2) + t2 + (i & 1);
-              if (((i & 2) ? kb : ka) >= open + (causal ? row / kGqa : 0)) x[c][i] = 0xff800000u;  // -inf
-            }
-        }
-        if (raise) {
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float u = fmaxf(__uint_as_float(x[c][4 * e]), __uint_as_float(x[c][4 * e + 2])),
-                    v = fmaxf(__uint_as_float(x[c][4 * e + 1]), __uint_as_float(x[c][4 * e + 3]));
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) {
-                u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-              }
-              if (g == 0) *reinterpret_cast<float2*>(red + sw * kRows + 16 * c + 8 * e + t2) = make_float2(u, v);
-            }
-          __syncwarp();
-          named_bar_sync(1, kSmThreads);
-          if (st < 16 * NC) {
-            float v = red[st];
-#pragma unroll
-            for (int i = 1; i < 8; ++i) v = fmaxf(v, red[i * kRows + st]);
-            // a row that sees no key yet keeps a reference of 0; it will see none later in the piece either
-            const float d = first_tile ? (v == -INFINITY ? 0.f : v) : fmaxf(v, 0.f);
-            nref[st] = first_tile ? -d : nref[st] - d;
-            ndelta[st] = -d;
-            alpha[st] = ex2(-d);
-          }
-          __syncwarp();
-          named_bar_sync(1, kSmThreads);
-#pragma unroll
-          for (int c = 0; c < NC; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint64_t d = *reinterpret_cast<const uint64_t*>(ndelta + 16 * c + 8 * e + t2);
-              put2(x[c] + 4 * e, add2(get2(x[c] + 4 * e), d));
-              put2(x[c] + 4 * e + 2, add2(get2(x[c] + 4 * e + 2), d));
-              l[c][e] = first_tile ? 0ull : mul2(l[c][e], *reinterpret_cast<const uint64_t*>(alpha + 16 * c + 8 * e + t2));
-            }
-          if (!first_tile) {  // O^T holds the tiles before: dims of this warp, every row
-            live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < NC; ++c) {
-              uint32_t o[16];
-              tmem_ld16(o_addr + 16 * c, o);
-              tmem_ld_wait();
-              loaded(o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[16 * c + i]);
-              tmem_st16(o_addr + 16 * c, o);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-          }
-        }
-        float top = 0.f;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[c][i] = __float_as_uint(ex2(__uint_as_float(x[c][i])));
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            sum[c][e] = add2(get2(x[c] + 4 * e), get2(x[c] + 4 * e + 2));
-            const float2 v = unpack2(sum[c][e]);
-            top = fmaxf(top, fmaxf(v.x, v.y));
-          }
-        }
-        if (raise || !bar_or(1, kSmThreads, top > 256.f)) break;
-        raise = true;
-      }
+      for (int c = 0; c < NC; ++c) tmem_ld_frag2(s_addr + 16 * c, x[c]);
+      tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (live && lane == 0) mbar_arrive(s_empty);
       __syncwarp();
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        loaded(x[c]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint64_t m = first_tile ? 0ull : *reinterpret_cast<const uint64_t*>(nref + 16 * c + 8 * e + t2);
+          put2(x[c] + 4 * e, fma2(get2(x[c] + 4 * e), scale2, m));
+          put2(x[c] + 4 * e + 2, fma2(get2(x[c] + 4 * e + 2), scale2, m));
+        }
+      }
+      if (open < kKeys) {  // the edge: mask
+        const int ka = tile_key + key16(g), kb = tile_key + key16(g + 8), causal = tl.causal, row0 = tl.row0;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = row0 + 16 * c + 8 * (i >> 2) + t2 + (i & 1);
+            if (((i & 2) ? kb : ka) >= open + (causal ? row / kGqa : 0)) x[c][i] = 0xff800000u;  // -inf
+          }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])));
+      // The references are raised when a logit passes them by 2^8, and at a piece's
+      // first tile.  The barrier also says that the others are done with the shared
+      // arrays.
+      if (bar_or(1, kSmThreads, first_tile || top > kLazyLog2)) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float u = fmaxf(__uint_as_float(x[c][4 * e]), __uint_as_float(x[c][4 * e + 2])),
+                  v = fmaxf(__uint_as_float(x[c][4 * e + 1]), __uint_as_float(x[c][4 * e + 3]));
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+              u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            }
+            if (g == 0) *reinterpret_cast<float2*>(red + sw * kRows + 16 * c + 8 * e + t2) = make_float2(u, v);
+          }
+        __syncwarp();
+        named_bar_sync(1, kSmThreads);
+        if (st < 16 * NC) {
+          float v = red[st];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) v = fmaxf(v, red[i * kRows + st]);
+          // a row that sees no key yet keeps a reference of 0; it will see none later in the piece either
+          const float d = first_tile ? (v == -INFINITY ? 0.f : v) : fmaxf(v, 0.f);
+          nref[st] = first_tile ? -d : nref[st] - d;
+          ndelta[st] = -d;
+          alpha[st] = ex2(-d);
+        }
+        __syncwarp();
+        named_bar_sync(1, kSmThreads);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t d = *reinterpret_cast<const uint64_t*>(ndelta + 16 * c + 8 * e + t2);
+            put2(x[c] + 4 * e, add2(get2(x[c] + 4 * e), d));
+            put2(x[c] + 4 * e + 2, add2(get2(x[c] + 4 * e + 2), d));
+            l[c][e] = first_tile ? 0ull : mul2(l[c][e], *reinterpret_cast<const uint64_t*>(alpha + 16 * c + 8 * e + t2));
+          }
+        if (!first_tile) {  // O^T holds the tiles before: dims of this warp, every row
+          live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < NC; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o_addr + 16 * c, o);
+            tmem_ld_wait();
+            loaded(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[16 * c + i]);
+            tmem_st16(o_addr + 16 * c, o);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+        }
+      }
+      uint32_t h[NC][4];
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float a0 = ex2(__uint_as_float(x[c][4 * e])), a1 = ex2(__uint_as_float(x[c][4 * e + 1])),
+                      b0 = ex2(__uint_as_float(x[c][4 * e + 2])), b1 = ex2(__uint_as_float(x[c][4 * e + 3]));
+          h[c][2 * e] = pack_half2(a0, a1);
+          h[c][2 * e + 1] = pack_half2(b0, b1);
+          l[c][e] = add2(l[c][e], add2(pack2(a0, a1), pack2(b0, b1)));
+        }
       if (j > 0) live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);  // P^T(j - 1) has been read
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        uint32_t h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = pack_half2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1]));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) l[c][e] = add2(l[c][e], sum[c][e]);
-        stsm_x4_trans(p_addr + c * (16 * kKeys * 2), h[0], h[1], h[2], h[3]);
+        stsm_x4_trans(p_addr + c * (16 * kKeys * 2), h[c][0], h[c][1], h[c][2], h[c][3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -1045,6 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
           }
         __syncwarp();
         named_bar_sync(1, kSmThreads);
+        const long long slot = tl.slot_row;
         if (st < rows) {
           float v = red[st];
 #pragma unroll
