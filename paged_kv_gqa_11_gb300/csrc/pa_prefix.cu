@@ -311,6 +311,9 @@ pa_status run_chunk(const Batch& b, uint32_t c0, uint32_t cn, const Group* group
   p.n_kv_heads = m.n_kv_heads = heads;
   p.n_q_heads = m.n_q_heads = heads * kGqa;
   p.page_size = (int)b.d.page_size;
+  p.page_shift = -1;
+  for (int i = 4; i < 31; ++i)
+    if (b.d.page_size == 1u << i) p.page_shift = i;
   p.table_stride = (int)b.table_stride;
   p.n_blocks = (int)b.d.n_blocks;
   p.n_seq = (int)cn;

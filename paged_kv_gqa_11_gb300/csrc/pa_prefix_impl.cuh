@@ -28,23 +28,21 @@
 // cost 32 x 48 cycles for up to 64 rows.
 //
 // Tensor memory (512 columns x 128 lanes): O^T dims 0-127 in columns 0-63 and
-// dims 128-255 in 64-127 (lane = dim, column = query row), S^T in 128-191
-// (lane = key), and five operand units of 64 columns.  A K unit is 128 keys x
-// 128 dims (lane = key, a column = two dims), a V unit 64 keys x 256 dims (lane
-// = dim, a column = two keys, dims 128-255 in its upper 32 columns); each is
-// worth eight MMAs, and they form a ring in the order in which the MMA warp
-// consumes them: K(0) | K(1) V(0) | K(2) V(1) | ... | V(n - 1), so that S of the
-// next tile is computed while the softmax of this one runs.
+// dims 128-255 in 64-127 (lane = dim, column = query row), two buffers of S^T
+// in 128-255 (lane = key), and four operand units of 64 columns.  A K unit is
+// 128 keys x 128 dims (lane = key, a column = two dims), a V unit 64 keys x 256
+// dims (lane = dim, a column = two keys, dims 128-255 in its upper 32 columns);
+// each is worth eight MMAs and is refilled as soon as they have read it.
 //
 // Warps, hand-offs on mbarriers, every wait bounded:
-//   0-7    K dequantisation: (half of the dims, lane quarter), thread = key;
+//   0-7    K dequantisation: (half of the dims, lane quarter), thread = key; and
+//          the query rows of every piece, eight by each warp;
 //   8-15   V dequantisation: (half of the tile's keys, lane quarter), by
 //          transposing ldmatrix;
 //   16-23  softmax: 16 keys each, all query rows, in mma fragments; P^T goes to
 //          shared memory by transposing stmatrix; they also rescale O^T (rarely:
 //          the reference maximum is raised only past 2^8) and write the pieces;
-//   24     MMA issue; 25 and 26 raw K and V copies (cp.async.bulk); 27 stages the
-//          query rows of the pieces after the first (the softmax warps stage it).
+//   24, 25 MMA issue, S^T and O^T; 26, 27 raw K and V copies (cp.async.bulk).
 //
 // The key order inside a group of 16 is key16 below: it is the order in which
 // a transposing ldmatrix delivers key pairs to the columns of a V unit, chosen so
@@ -74,11 +72,10 @@ constexpr int kStageKeys = 64;    // keys per copy stage and per V unit
 constexpr int kRows = 64;         // query rows per row tile
 constexpr int kMaxSeqs = 256;     // sequences per launch
 constexpr int kMaxGroups = 128;   // shared prefixes per launch (two sequences each at least)
-constexpr int kUnits = 5;         // operand units in tensor memory
-constexpr int kKWarp0 = 0, kVWarp0 = 8, kSmWarp0 = 16, kMmaWarp = 24, kCopyKWarp = 25, kCopyVWarp = 26, kQWarp = 27;
+constexpr int kKWarp0 = 0, kVWarp0 = 8, kSmWarp0 = 16, kSWarp = 24, kPvWarp = 25, kCopyKWarp = 26, kCopyVWarp = 27;
 constexpr int kThreads = 28 * 32;
 constexpr int kSmThreads = 256;
-constexpr uint32_t kTmemCols = 512, kOCol = 0, kSCol = 128, kUnitCol = 192;
+constexpr uint32_t kTmemCols = 512, kOCol = 0, kSCol = 128, kKCol = 256, kVCol = 384;
 constexpr float kLazyLog2 = 8.f;  // the reference maximum is raised past this
 
 struct Params {
@@ -90,6 +87,7 @@ struct Params {
   float2* part_ml;  // (reference maximum in log2 units, sum of weights) per slot row
   float* part_o;    // [slot row][256]
   int q_type, n_qtok, n_kv_heads, n_q_heads, page_size, table_stride, n_blocks;
+  int page_shift;  // log2 of page_size, or -1
   int n_seq, n_groups, n_ctas;
   int prefix_tiles, total_tiles;
   int suffix_row_tiles, suffix_rows;  // row tiles of a suffix segment; rows of its slot
@@ -180,11 +178,6 @@ __device__ __forceinline__ int pos_slot_row(const Params& p, const Pos& t, int c
   return p.suffix_base + (cta + (t.unit * p.n_kv_heads + t.head) * t.nrt + t.rt) * p.suffix_rows;
 }
 
-// Operand units are numbered in the order of consumption: the two of K(j), and
-// the two of V(j), of a CTA's n tiles.
-__device__ __forceinline__ uint32_t k_num(uint32_t j) { return j == 0 ? 0 : 4 * j - 2; }
-__device__ __forceinline__ uint32_t v_num(uint32_t j, uint32_t n) { return j + 1 == n ? 4 * j + 2 : 4 * j + 4; }
-
 // The row of a 16-key group at position p of the tile's key order.
 __host__ __device__ constexpr int key16(int p) {
   const int t = p >> 2, e = p & 3;
@@ -223,8 +216,9 @@ struct Smem {
   static constexpr int kRed = kVRing + kVStages * kVStage;
   static constexpr int kRef = kRed + 8 * kRows * 4, kDelta = kRef + kRows * 4, kAlpha = kDelta + kRows * 4;
   static constexpr int kTile = kAlpha + kRows * 4, kLeft = kTile + 16 * 32, kBar = kLeft + 64;
-  // K and V raw full / empty [stages], unit full / empty [5], s full / empty, p full, pv done, q full / empty [2], o free, drain, sink
-  static constexpr int kNBar = 2 * (kKStages + kVStages) + 2 * kUnits + 4 + 4 + 3;
+  // K and V raw full / empty [stages], K and V unit full / empty [2], s full / empty [2], q full / empty [2],
+  // p full, pv done, o free, drain [2], sink
+  static constexpr int kNBar = 2 * (kKStages + kVStages) + 8 + 4 + 4 + 6;
   static constexpr int kMisc = kBar + 8 * kNBar;  // abort, tmem base, the first tile's place
   static constexpr int kTotal = kMisc + 16 + 32;
   static constexpr int kLaunch = kTotal + 1024;  // the base is aligned to 1024 inside
@@ -417,69 +411,90 @@ __device__ __forceinline__ void dequant_v(uint32_t stage, int b, int n_keys, uin
   }
 }
 
+// ------------------------------------------------------------------ tiles
+
+// What the other roles need to know of a tile; the K copy warp writes it,
+// sixteen tiles deep (the roles are never that far apart: the copy stages and
+// operand units between them hold fewer tiles).
+struct alignas(16) Tile {
+  uint32_t info;  // query rows of the segment | first tile of a piece << 8 | last << 9 | suffix << 10
+  int open;       // keys of the tile that every row sees (<= 0: none; >= 128: no edge here); suffix row r sees
+                  // (row0 + r) / 6 more
+  int row0;       // first query row of the row tile
+  int slot_row;   // first slot row of the piece
+  int token;      // first token (row of heads) of the unit's queries
+  int head;       // KV head
+  int pad[2];
+};
+constexpr int kTiles = 16;
+
 // ------------------------------------------------------------------ query rows
 
-__device__ __forceinline__ float4 load4(int type, const uint8_t* base, long long i) {
-  if (type == PA_DT_F32) return *reinterpret_cast<const float4*>(base + 4 * i);
-  const uint2 v = *reinterpret_cast<const uint2*>(base + 2 * i);
-  if (type == PA_DT_F16) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x)),
-                 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-  }
-  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                     __uint_as_float(v.y & 0xffff0000u));
+// Eight query rows r8 .. r8 + 7 of a row tile by one warp as binary16 into the B
+// operand at dst, slots in K's dim order, rows past the segment's as zeros.  Lane:
+// row r8 + lane % 8, slots lane / 8 + 4 i.  begin starts asynchronous copies
+// of 16-bit rows to their places (fp32 rows are converted at once), end waits for
+// them and puts the pairs of a slot in order and bfloat16 into binary16.
+template <int KT>
+__device__ __forceinline__ uint4 q_slot(uint4 v) {  // Q4_0: the order of dequant_k's columns, 0, 2 | 1, 3
+  if (KT != PA_Q4_0) return v;
+  return make_uint4(prmt(v.x, v.y, 0x5410), prmt(v.x, v.y, 0x7632), prmt(v.z, v.w, 0x5410), prmt(v.z, v.w, 0x7632));
 }
 
-// Worker w of nw (warps) stages row groups w, w + nw, ... of eight of the
-// segment's query rows as binary16 into the B operand at dst, in K's dim order;
-// rows past the segment's, up to n (a multiple of 16), are zeros.  Lane: row
-// lane % 8, slots lane / 8 + 4 i; half of a row group's loads are in flight at once.
-template <int KT, int QT>
-__device__ __forceinline__ void stage_q_as(const Params& p, const Pos& t, uint32_t dst, int n, int w, int nw, int lane) {
-  const int rows = pos_rows(p, t), s4 = lane >> 3;
-  const long long tok0 = (long long)pos_seq(p, t) * p.n_qtok;
+template <int KT>
+__device__ __forceinline__ void stage_q_begin(const Params& p, const Tile& t, uint32_t dst, int r8, int lane) {
+  const int row = r8 + (lane & 7), rg = t.row0 + row, rows = t.info & 0xff;
+  const uint32_t to = dst + canon(row, lane >> 3, kD / 8);
+  if (row >= rows) {
 #pragma unroll 1
-  for (int r8 = 8 * w; r8 < n; r8 += 8 * nw) {
-    const int row = r8 + (lane & 7), rg = t.rt * kRows + row;
-    const uint32_t to = dst + canon(row, s4, kD / 8);
-    if (r8 >= rows) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sts128_zero(to + 512 * i);
-      continue;
+    for (int i = 0; i < 8; ++i) sts128_zero(to + 512 * i);
+    return;
+  }
+  const long long at = ((long long)(t.token + rg / kGqa) * p.n_q_heads + t.head * kGqa + rg % kGqa) * kD;
+  if (p.q_type == PA_DT_F32) {
+    const float* src = reinterpret_cast<const float*>(p.q) + at;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+      const float4 x = *reinterpret_cast<const float4*>(src + q_dim<KT>((lane >> 3) + 4 * i, 0)),
+                   y = *reinterpret_cast<const float4*>(src + q_dim<KT>((lane >> 3) + 4 * i, 1));
+      sts128(to + 512 * i,
+             q_slot<KT>(make_uint4(pack_half2(x.x, x.y), pack_half2(x.z, x.w), pack_half2(y.x, y.y), pack_half2(y.z, y.w))));
     }
-    const bool real = row < rows;
-    const long long at = ((tok0 + rg / kGqa) * p.n_q_heads + t.head * kGqa + rg % kGqa) * kD;
+  } else {
+    const uint8_t* src = p.q + 2 * at;
+#pragma unroll 2
+    for (int i = 0; i < 8; ++i) {
+      const int slot = (lane >> 3) + 4 * i;
+      if (KT == PA_Q4_0) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float4 a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int slot = s4 + 4 * (4 * h + i);
-        a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (real) {
-          a[i] = load4(QT, p.q, at + q_dim<KT>(slot, 0));
-          b[i] = load4(QT, p.q, at + q_dim<KT>(slot, 1));
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 v;
-        if (KT == PA_Q4_0)
-          v = make_uint4(pack_half2(a[i].x, a[i].z), pack_half2(a[i].y, a[i].w), pack_half2(b[i].x, b[i].z), pack_half2(b[i].y, b[i].w));
-        else
-          v = make_uint4(pack_half2(a[i].x, a[i].y), pack_half2(a[i].z, a[i].w), pack_half2(b[i].x, b[i].y), pack_half2(b[i].z, b[i].w));
-        sts128(to + 512 * (4 * h + i), v);
+        for (int h = 0; h < 2; ++h)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to + 512 * i + 8 * h),
+                       "l"(src + 2 * q_dim<KT>(slot, h))
+                       : "memory");
+      } else {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512 * i), "l"(src + 16 * slot) : "memory");
       }
     }
   }
 }
 
 template <int KT>
-__device__ __forceinline__ void stage_q(const Params& p, const Pos& t, uint32_t dst, int n, int w, int nw, int lane) {
-  if (p.q_type == PA_DT_F32) stage_q_as<KT, PA_DT_F32>(p, t, dst, n, w, nw, lane);
-  else if (p.q_type == PA_DT_F16) stage_q_as<KT, PA_DT_F16>(p, t, dst, n, w, nw, lane);
-  else stage_q_as<KT, PA_DT_BF16>(p, t, dst, n, w, nw, lane);
+__device__ __forceinline__ void stage_q_end(const Params& p, uint32_t dst, int r8, int lane) {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  const bool bf16 = p.q_type == PA_DT_BF16;
+  if (p.q_type == PA_DT_F32 || (KT != PA_Q4_0 && !bf16)) return;
+  const uint32_t to = dst + canon(r8 + (lane & 7), lane >> 3, kD / 8);
+#pragma unroll 2
+  for (int i = 0; i < 8; ++i) {
+    uint4 v = lds128(to + 512 * i);
+    if (bf16) {
+      uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) u[k] = pack_half2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
+      v = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    sts128(to + 512 * i, q_slot<KT>(v));
+  }
 }
 
 // ------------------------------------------------------------------ pairs of floats
@@ -570,93 +585,100 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t
   return warp_wait_slow<kSleep>(bar, parity, err, abort);
 }
 
-// What the softmax and the MMA warp need to know of a tile; the K copy warp
-// writes it, sixteen tiles deep (the roles are never that far apart: the copy
-// stages and operand units between them hold fewer tiles).
-struct alignas(16) Tile {
-  uint32_t info;  // query rows of the segment | first tile of a piece << 8 | last << 9
-  int open;      // keys of the tile that every row sees (<= 0: none; >= 128: no edge here)
-  int causal;    // row r sees (row0 + r) / 6 more than `open`
-  int row0;      // first query row of the row tile
-  int slot_row;  // first slot row of the piece
-  int pad[3];
-};
-constexpr int kTiles = 16;
-
 // The raw K (kIsV false) or V row groups of the CTA's tiles into a ring of NS
-// stages at ring, two stages per tile.  Lane g (0..7) looks after row group g of
-// the tile; its table entry is read a tile ahead.  Returns the number of
-// stages issued.
+// stages at ring, two stages per tile; returns the number of stages issued.
+// Lane g (0..7) looks after row group g of the tile, all in one pass: its
+// stage's wait, its copy; its table entry is read a tile ahead.  One warp in the
+// company of twenty others executes an instruction every ten cycles or so, so
+// what the tiles of a segment share is computed once per segment.
 template <int T, bool kIsV, int NS>
 __device__ __forceinline__ int copy_role(const Params& p, Pos pos, int n, uint32_t ring, uint32_t full, uint32_t empty,
                                          Tile* tiles, int* lefts, volatile int* abort, int lane) {
   constexpr int GB = pa_layout::group_bytes<T>(), RB = Fmt<T>::kRow;
   const uint8_t* pool = kIsV ? p.v_pool : p.k_pool;
-  int slot = 0, issued = 0;
-  uint32_t parity = 1;  // of the wait for a stage's previous use; flips when the ring wraps
-  int entry = -1, off = 0, left = 0;
-  auto look = [&](const Pos& t) {
-    const int k0 = pos_key0(p, t), k = k0 + kGroup * lane;
-    left = min(kKeys, pos_end(p, t) - k0);
-    entry = -1;
-    if (lane < kKeys / kGroup && kGroup * lane < left) {
-      const int page = k / p.page_size;
-      off = k - page * p.page_size;
-      entry = __ldg(p.table + (long long)pos_seq(p, t) * p.table_stride + page);
+  const long long block_rows = (long long)p.n_kv_heads * p.page_size;
+  const int half = (lane >> 2) & 1, lane_key = lane < 8 ? kGroup * lane : kKeys;  // lanes past 7 have no group
+  const int page_shift = p.page_shift;
+  // of the segment
+  const int32_t* row = nullptr;
+  int end = 0, key0 = 0, head_row = 0;
+  uint32_t info = 0;
+  int4 tile0 = make_int4(0, 0, 0, 0), tile1 = tile0;
+  auto enter = [&]() {
+    row = p.table + (long long)pos_seq(p, pos) * p.table_stride;
+    end = pos_end(p, pos);
+    key0 = pos_key0(p, pos);
+    head_row = pos.head * p.page_size;
+    if (!kIsV) {
+      info = (uint32_t)pos_rows(p, pos) | (pos.pre ? 0u : 1u << 10) | 1u << 8;
+      // prefix: the live keys; suffix: the new tokens' keys open one by one
+      tile0 = make_int4(0, pos.pre ? end : end - p.n_qtok + 1, pos.rt * kRows, pos_slot_row(p, pos, (int)blockIdx.x));
+      tile1 = make_int4(pos_seq(p, pos) * p.n_qtok, pos.head, 0, 0);
     }
   };
-  look(pos);
+  int entry = -1, off = 0;
+  auto look = [&]() {
+    entry = -1;
+    const int k = key0 + lane_key;
+    if (lane_key < kKeys && k < end) {
+      const int page = page_shift >= 0 ? k >> page_shift : k / p.page_size;
+      off = k - page * p.page_size;
+      entry = __ldg(row + page);
+    }
+  };
+  enter();
+  look();
+  int pair = 0;         // stages 2 pair, 2 pair + 1
+  uint32_t parity = 1;  // of the wait for the stages' previous use; flips when the ring wraps
   for (int j = 0; j < n; ++j) {
+    const int tb = entry;
+    const bool mine = lane_key < kKeys && key0 + lane_key < end, ok = mine && (uint32_t)tb < (uint32_t)p.n_blocks;
+    const uint8_t* src = pool + (tb * block_rows + (head_row + off)) * RB;
+    const bool last = j + 1 == n || pos.j + 1 == pos.nt;
     if (lane == 0) {
       if (kIsV) {
-        lefts[j & (kTiles - 1)] = left;
+        lefts[j & (kTiles - 1)] = end - key0;
       } else {
-        Tile& t = tiles[j & (kTiles - 1)];
-        t.info = (uint32_t)pos_rows(p, pos) | ((j == 0 || pos.j == 0) ? 1u << 8 : 0u) |
-                 ((j + 1 == n || pos.j + 1 == pos.nt) ? 1u << 9 : 0u);
-        // prefix: the tile's live keys; suffix: the new tokens' keys open one by one
-        t.open = pos.pre ? pos_end(p, pos) - pos_key0(p, pos) : pos_end(p, pos) - p.n_qtok + 1 - pos_key0(p, pos);
-        t.causal = !pos.pre;
-        t.row0 = pos.rt * kRows;
-        t.slot_row = pos_slot_row(p, pos, (int)blockIdx.x);
+        int4* t = reinterpret_cast<int4*>(tiles + (j & (kTiles - 1)));
+        t[0] = make_int4((int)(info | (last ? 1u << 9 : 0u)), tile0.y - key0, tile0.z, tile0.w);
+        t[1] = tile1;
       }
     }
-    const int tb = entry, head = pos.head;
-    const bool mine = lane < kKeys / kGroup && kGroup * lane < left, ok = mine && tb >= 0 && tb < p.n_blocks;
-    const uint8_t* src = pool + (((long long)tb * p.n_kv_heads + head) * p.page_size + off) * RB;
-    if (j + 1 < n) {
-      advance(p, pos);
-      look(pos);
-    }
+    info &= ~(1u << 8);
     const uint32_t good = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, mine && !ok);
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      const uint32_t fb = full + 8 * slot, dst = ring + slot * (4 * GB);
-      if (issued >= NS && !warp_wait<true>(empty + 8 * slot, parity, p.err, abort)) return issued;
-      if (bad) {  // rows of an entry outside the pool read as zeros
-        if (lane == 0) record_error(p.err, PA_ERR_BOUNDS);
-        for (int g = 0; g < 4; ++g) {
-          if (!((bad >> (4 * half + g)) & 1)) continue;
-          for (int i = lane; i < GB / 16; i += 32) sts128_zero(dst + g * GB + 16 * i);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
+    if (j + 1 < n) {  // the next tile's table entries
+      if (last) {
+        advance(p, pos);
+        enter();
+      } else {
+        ++pos.j;
+        key0 += kKeys;
       }
-      if (lane == 0) mbar_arrive_expect_tx(fb, __popc(good & (0xfu << (4 * half))) * GB);
+      look();
+    }
+    const uint32_t stage = 2 * pair + half, fb = full + 8 * stage, dst = ring + stage * (4 * GB) + (lane & 3) * GB;
+    if (j >= NS / 2 && !warp_wait<true>(empty + 8 * stage, parity, p.err, abort)) return 2 * j;
+    if (bad) {  // rows of an entry outside the pool read as zeros
+      if (lane == 0) record_error(p.err, PA_ERR_BOUNDS);
+      for (int g = 0; g < 8; ++g) {
+        if (!((bad >> g) & 1)) continue;
+        for (int i = lane; i < GB / 16; i += 32) sts128_zero(ring + (2 * pair + (g >> 2)) * (4 * GB) + (g & 3) * GB + 16 * i);
+      }
+      fence_proxy_async_smem();
       __syncwarp();
-      if (ok && (lane >> 2) == half)
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         dst + (lane & 3) * GB),
-                     "l"(src), "r"(GB), "r"(fb)
-                     : "memory");
-      ++issued;
-      if (++slot == NS) {
-        slot = 0;
-        parity ^= 1;
-      }
+    }
+    if (lane == 0 || lane == 4) mbar_arrive_expect_tx(fb, __popc(good & (0xfu << lane)) * GB);
+    __syncwarp();
+    if (ok)
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                   "l"(src), "r"(GB), "r"(fb)
+                   : "memory");
+    if (++pair == NS / 2) {
+      pair = 0;
+      parity ^= 1;
     }
   }
-  return issued;
+  return 2 * n;
 }
 
 // Eight MMAs of an operand unit (columns a, a + 8, ...), issued by the lane
@@ -704,19 +726,19 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
   uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  // Hand-offs (unit numbers: k_num / v_num; tile j, piece i of the CTA):
+  // Hand-offs (tile j, piece i of the CTA):
   //   kraw_*, vraw_* [(2 j + half) % stages]  copies <-> dequantisation (four warps read a stage)
-  //   unit_full / unit_empty [number % 5]     dequantisation (four warps) <-> MMA (commit)
-  //   s_full / s_empty                  S^T(j) in tensor memory / in the softmax registers
+  //   ku_*, vu_* [half]                 operand units: dequantisation (four warps) <-> MMA (commit)
+  //   s_full / s_empty [j & 1]          S^T(j) in tensor memory / in the softmax registers
   //   p_full / pv_done                  P^T(j) written / O^T holds tile j, P^T free
   //   q_full / q_empty [i & 1]          query rows of piece i staged / no longer needed
   //   o_free                            piece i's O^T has been read
   // A role whose wait expires stops: it arrives nowhere any more.
   const uint32_t kraw_full = base + SM::kBar, kraw_empty = kraw_full + 8 * NK, vraw_full = kraw_empty + 8 * NK,
-                 vraw_empty = vraw_full + 8 * NV, unit_full = vraw_empty + 8 * NV,
-                 unit_empty = unit_full + 8 * kUnits, s_full = unit_empty + 8 * kUnits, s_empty = s_full + 8,
-                 p_full = s_empty + 8, pv_done = p_full + 8, q_full = pv_done + 8, q_empty = q_full + 16,
-                 o_free = q_empty + 16, drain = o_free + 8, sink = drain + 8;
+                 vraw_empty = vraw_full + 8 * NV, ku_full = vraw_empty + 8 * NV, ku_empty = ku_full + 16,
+                 vu_full = ku_empty + 16, vu_empty = vu_full + 16, s_full = vu_empty + 16, s_empty = s_full + 16,
+                 q_full = s_empty + 16, q_empty = q_full + 16, p_full = q_empty + 16, pv_done = p_full + 8,
+                 o_free = pv_done + 8, drain = o_free + 8, sink = drain + 16;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + SM::kMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc + 8);
   Pos* start = reinterpret_cast<Pos*>(smem + SM::kMisc + 16);
@@ -734,20 +756,20 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       mbar_init(vraw_full + 8 * i, 1);
       mbar_init(vraw_empty + 8 * i, 4);
     }
-    for (int i = 0; i < kUnits; ++i) {
-      mbar_init(unit_full + 8 * i, 4);
-      mbar_init(unit_empty + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(ku_full + 8 * i, 4);
+      mbar_init(ku_empty + 8 * i, 1);
+      mbar_init(vu_full + 8 * i, 4);
+      mbar_init(vu_empty + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(s_empty + 8 * i, 8);
+      mbar_init(q_full + 8 * i, 8);
+      mbar_init(q_empty + 8 * i, 1);
+      mbar_init(drain + 8 * i, 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(s_empty, 8);
     mbar_init(p_full, 8);
     mbar_init(pv_done, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + 8 * i, 1);
-      mbar_init(q_empty + 8 * i, 1);
-    }
     mbar_init(o_free, 8);
-    mbar_init(drain, 1);
     mbar_init(sink, 1);
     fence_mbar_init();
   }
@@ -780,128 +802,129 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     const int r = key16(lane & 15);
     const uint32_t grp = base + SM::kRing + ((at >> 4) & 3) * pa_layout::group_bytes<KT>();
     const uint32_t t_lane = (uint32_t)(32 * quarter) << 16;
+    // The query rows of a piece are staged here too, eight by each of the warps,
+    // copied while the tile's K is converted.
+    uint32_t piece = 0;
     for (int j = 0; j < n; ++j) {
-      const uint32_t stage = 2 * j + (quarter >> 1), slot = stage % NK, unit = k_num(j) + kd, us = unit % kUnits;
+      const uint32_t stage = 2 * j + (quarter >> 1), slot = stage % NK;
       if (!warp_wait<true>(kraw_full + 8 * slot, (stage / NK) & 1, p.err, abort)) break;
-      if (unit >= kUnits && !warp_wait<true>(unit_empty + 8 * us, (unit / kUnits - 1) & 1, p.err, abort)) break;
+      const Tile& t = tiles[j & (kTiles - 1)];
+      const uint32_t info = t.info, q_dst = base + SM::kQ + (piece & 1) * SM::kQBytes;
+      const bool first_tile = (info >> 8) & 1, stage_q = first_tile && 8 * w < (int)(((info & 0xff) + 15) & ~15u);
+      if (first_tile && piece >= 2 && !warp_wait<true>(q_empty + 8 * (piece & 1), ((piece >> 1) - 1) & 1, p.err, abort)) break;
+      if (stage_q) stage_q_begin<KT>(p, t, q_dst, 8 * w, lane);
+      if (j > 0 && !warp_wait<true>(ku_empty + 8 * kd, (j - 1) & 1, p.err, abort)) break;
       tc_fence_after();
-      dequant_k<KT>(grp + slot * SM::kKStage, r, kd, kUnitCol + 64 * us + t_lane);
+      dequant_k<KT>(grp + slot * SM::kKStage, r, kd, kKCol + 64 * kd + t_lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(kraw_empty + 8 * slot);
       __syncwarp();
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(unit_full + 8 * us);
+      if (lane == 0) mbar_arrive(ku_full + 8 * kd);
+      __syncwarp();
+      if (first_tile) {
+        if (stage_q) stage_q_end<KT>(p, q_dst, 8 * w, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full + 8 * (piece & 1));
+        __syncwarp();
+        ++piece;
+      }
     }
   } else if (w < kSmWarp0) {
     // ---- V: keys 64 vh .. + 63 of the tile, block `quarter` of each half of the dims
     const int vh = (w - kVWarp0) >> 2, quarter = w & 3;
     const uint32_t t_lane = (uint32_t)(32 * quarter) << 16;
     for (int j = 0; j < n; ++j) {
-      const uint32_t stage = 2 * j + vh, slot = stage % NV, num = v_num(j, n) + vh, us = num % kUnits;
+      const uint32_t stage = 2 * j + vh, slot = stage % NV;
       if (!warp_wait<true>(vraw_full + 8 * slot, (stage / NV) & 1, p.err, abort)) break;
-      if (num >= kUnits && !warp_wait<true>(unit_empty + 8 * us, (num / kUnits - 1) & 1, p.err, abort)) break;
+      if (j > 0 && !warp_wait<true>(vu_empty + 8 * vh, (j - 1) & 1, p.err, abort)) break;
       tc_fence_after();
       dequant_v<VT>(base + SM::kVRing + slot * SM::kVStage, quarter, lefts[j & (kTiles - 1)] - kStageKeys * vh,
-                    kUnitCol + 64 * us + t_lane, lane);
+                    kVCol + 64 * vh + t_lane, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(vraw_empty + 8 * slot);
       __syncwarp();
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(unit_full + 8 * us);
+      if (lane == 0) mbar_arrive(vu_full + 8 * vh);
     }
-  } else if (w == kMmaWarp) {
-    // ---- MMA issue: the whole warp runs the loop and an elected lane issues, so
-    // that the operands stay in uniform registers: what comes from shared memory
-    // goes through a warp reduction, and an expired wait leaves the control flow
-    // as it is -- from then on all commits go to a barrier that nobody waits on.
-    const uint64_t qdesc = smem_desc(base + SM::kQ, 128, 4096), pdesc = smem_desc(base + SM::kP, 128, 2048);
+  } else if (w == kSWarp || w == kPvWarp) {
+    // ---- MMA issue, S^T and O^T by a warp each: the whole warp runs its loop and
+    // an elected lane issues, so that the operands stay in uniform registers: what
+    // comes from shared memory goes through a warp reduction, and an expired wait
+    // leaves the control flow as it is -- from then on all commits go to a barrier
+    // that nobody waits on.
+    const uint32_t leader = elect_one();
     bool dead = false;
     auto wait = [&](uint32_t bar, uint32_t parity) { dead |= !warp_wait(bar, parity, p.err, abort); };
     auto commit = [&](uint32_t bar) { tc_commit_warp(dead ? sink : bar); };
-    const uint32_t leader = elect_one();
-    uint32_t piece = 0, prev_info = 0;
+    auto info_of = [&](uint32_t j) { return __reduce_or_sync(0xffffffffu, tiles[j & (kTiles - 1)].info); };
     auto idesc_of = [](uint32_t info) { return idesc_f16_f32(128, 0) | (((info & 0xffu) + 15) >> 4 << 18); };
-    // O^T += V^T P^T of tile jj, of piece number pc (from 1)
-    auto pv = [&](uint32_t jj, uint32_t info, uint32_t pc) {
-      const bool first_tile = (info >> 8) & 1;
-      const uint32_t idesc = idesc_of(info);
-      wait(p_full, jj & 1);
-      if (first_tile && pc > 1) wait(o_free, pc & 1);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t num = v_num(jj, n) + h, us = num % kUnits;
-        wait(unit_full + 8 * us, (num / kUnits) & 1);
+    uint32_t piece = 0;
+    if (w == kSWarp) {
+      const uint64_t qdesc = smem_desc(base + SM::kQ, 128, 4096);
+      for (uint32_t j = 0; j < (uint32_t)n; ++j) {
+        const uint32_t b = j & 1;
+        wait(ku_full, b);
+        const uint32_t info = info_of(j);
+        if ((info >> 8) & 1) {
+          wait(q_full + 8 * (piece & 1), (piece >> 1) & 1);
+          ++piece;
+        }
+        if (j >= 2) wait(s_empty + 8 * b, ((j >> 1) - 1) & 1);
         tc_fence_after();
-        mma8<true>(kOCol, kUnitCol + 64 * us, pdesc + 64 * h, idesc, (h == 0 && first_tile) ? 0u : 1u, leader);
-        commit(unit_empty + 8 * us);
-      }
-      commit(pv_done);
-    };
-    for (uint32_t j = 0; j < (uint32_t)n; ++j) {
-      const uint32_t num0 = k_num(j);
-      wait(unit_full + 8 * (num0 % kUnits), (num0 / kUnits) & 1);
-      const uint32_t info = __reduce_or_sync(0xffffffffu, tiles[j & (kTiles - 1)].info);
-      const uint32_t prev_piece = piece;
-      if ((info >> 8) & 1) {
-        wait(q_full + 8 * (piece & 1), (piece >> 1) & 1);
-        ++piece;
-      }
-      if (j > 0) wait(s_empty, (j - 1) & 1);
-      const uint64_t qd = qdesc + (uint64_t)(((piece - 1) & 1) * (SM::kQBytes >> 4));
-      const uint32_t idesc = idesc_of(info);
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const uint32_t num = num0 + d, us = num % kUnits;
-        if (d) wait(unit_full + 8 * us, (num / kUnits) & 1);
+        const uint64_t qd = qdesc + (uint64_t)(((piece - 1) & 1) * (SM::kQBytes >> 4));
+        const uint32_t idesc = idesc_of(info), d = kSCol + 64 * b;
+        mma8<false>(d, kKCol, qd, idesc, 0u, leader);
+        commit(ku_empty);
+        wait(ku_full + 8, b);
         tc_fence_after();
-        mma8<false>(kSCol, kUnitCol + 64 * us, qd + 128 * d, idesc, (uint32_t)d, leader);
-        commit(unit_empty + 8 * us);
+        mma8<false>(d, kKCol + 64, qd + 128, idesc, 1u, leader);
+        commit(ku_empty + 8);
+        commit(s_full + 8 * b);
+        if ((info >> 9) & 1) commit(q_empty + 8 * ((piece - 1) & 1));
       }
-      commit(s_full);
-      if ((info >> 9) & 1) commit(q_empty + 8 * ((piece - 1) & 1));
-      if (j > 0) pv(j - 1, prev_info, prev_piece);
-      prev_info = info;
+      // the last commits have arrived before the CTA's barriers go away
+      for (int i = 0; i < 2; ++i) wait(ku_empty + 8 * i, (n - 1) & 1);
+      for (uint32_t j = n < 2 ? 0 : n - 2; j < (uint32_t)n; ++j) wait(s_full + 8 * (j & 1), (j >> 1) & 1);
+      for (uint32_t i = piece < 2 ? 0 : piece - 2; i < piece; ++i) wait(q_empty + 8 * (i & 1), (i >> 1) & 1);
+    } else {
+      const uint64_t pdesc = smem_desc(base + SM::kP, 128, 2048);
+      for (uint32_t j = 0; j < (uint32_t)n; ++j) {
+        const uint32_t b = j & 1;
+        wait(p_full, b);
+        const uint32_t info = info_of(j), first_tile = (info >> 8) & 1, idesc = idesc_of(info);
+        if (first_tile) {
+          if (piece > 0) wait(o_free, (piece - 1) & 1);
+          ++piece;
+        }
+        wait(vu_full, b);
+        tc_fence_after();
+        mma8<true>(kOCol, kVCol, pdesc, idesc, first_tile ^ 1u, leader);
+        commit(vu_empty);
+        wait(vu_full + 8, b);
+        tc_fence_after();
+        mma8<true>(kOCol, kVCol + 64, pdesc + 64, idesc, 1u, leader);
+        commit(vu_empty + 8);
+        commit(pv_done);
+      }
+      for (int i = 0; i < 2; ++i) wait(vu_empty + 8 * i, (n - 1) & 1);
+      wait(pv_done, (n - 1) & 1);
     }
-    pv(n - 1, prev_info, piece);
-    // the last commits have arrived before the CTA's barriers go away
-    for (uint32_t u = 4 * n < kUnits ? 0 : 4 * n - kUnits; u < 4u * n; ++u)
-      wait(unit_empty + 8 * (u % kUnits), (u / kUnits) & 1);
-    for (uint32_t i = piece < 2 ? 0 : piece - 2; i < piece; ++i) wait(q_empty + 8 * (i & 1), (i >> 1) & 1);
-    wait(pv_done, (n - 1) & 1);
     if (dead) {  // what was issued ends before shared and tensor memory are released
-      tc_commit_warp(drain);
-      mbar_wait(drain, 0, p.err, abort, /*honour_abort=*/false);
+      const uint32_t bar = drain + 8 * (w - kSWarp);
+      tc_commit_warp(bar);
+      mbar_wait(bar, 0, p.err, abort, /*honour_abort=*/false);
     }
     __syncwarp();
-  } else if (w == kQWarp) {
-    // ---- query rows of the pieces after the first: a piece ends with its segment
-    Pos pos = *start;
-    int piece = 0;
-    for (int j = pos.nt - pos.j; j < n; j += pos.nt) {
-      pos.j = pos.nt - 1;
-      advance(p, pos);
-      ++piece;
-      if (piece >= 2 && !warp_wait<true>(q_empty + 8 * (piece & 1), ((piece >> 1) - 1) & 1, p.err, abort)) break;
-      stage_q<KT>(p, pos, base + SM::kQ + (piece & 1) * SM::kQBytes, (pos_rows(p, pos) + 15) & ~15, 0, 1, lane);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full + 8 * (piece & 1));
-    }
   } else {
     // ---- softmax: keys 16 hh + 32 quarter .. + 15 of the tile, all query rows;
     // thread 4g + t holds keys g and g + 8 and columns 2t, 2t + 1 of every 8
     const int sw = w - kSmWarp0, hh = sw >> 2, quarter = w & 3, g = lane >> 2, t2 = 2 * (lane & 3), st = tid - 32 * kSmWarp0;
-    {
-      const Pos pos = *start;
-      stage_q<KT>(p, pos, base + SM::kQ, (pos_rows(p, pos) + 15) & ~15, sw, 8, lane);
-    }
-    fence_proxy_async_smem();
-    named_bar_sync(1, kSmThreads);
-    if (st == 0) mbar_arrive(q_full);
     float* red = reinterpret_cast<float*>(smem + SM::kRed);
     float* nref = reinterpret_cast<float*>(smem + SM::kRef);      // minus the reference maximum
     float* ndelta = reinterpret_cast<float*>(smem + SM::kDelta);  // minus what it was raised by
@@ -921,11 +944,11 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       const bool first_tile = (info >> 8) & 1, last_tile = (info >> 9) & 1;
       uint32_t x[NC][8];  // [16 columns][(8 columns e, key g or g + 8, column 2t or 2t + 1): 4e + 2k + i], floats
 #pragma unroll
-      for (int c = 0; c < NC; ++c) tmem_ld_frag2(s_addr + 16 * c, x[c]);
+      for (int c = 0; c < NC; ++c) tmem_ld_frag2(s_addr + 64 * (j & 1) + 16 * c, x[c]);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (live && lane == 0) mbar_arrive(s_empty);
+      if (live && lane == 0) mbar_arrive(s_empty + 8 * (j & 1));
       __syncwarp();
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -938,7 +961,8 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
         }
       }
       if (open < kKeys) {  // the edge: mask
-        const int ka = tile_key + key16(g), kb = tile_key + key16(g + 8), causal = tl.causal, row0 = tl.row0;
+        const int ka = tile_key + key16(g), kb = tile_key + key16(g + 8), row0 = tl.row0;
+        const bool causal = (info >> 10) & 1;
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -1072,7 +1096,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       }
     };
     for (int j = 0; j < n; ++j) {
-      live = live && warp_wait(s_full, j & 1, p.err, abort);
+      live = live && warp_wait(s_full + 8 * (j & 1), (j >> 1) & 1, p.err, abort);
       tc_fence_after();
       const uint32_t info = tiles[j & (kTiles - 1)].info;
       const int nc = ((info & 0xff) + 15) >> 4;
