@@ -18,7 +18,7 @@ import threading
 from . import _build
 
 __all__ = [
-    "PA_F16", "PA_Q4_0", "PA_Q8_0", "PaError", "Pool", "load", "row_bytes", "pa_append_rows", "pa_append_rows_f16", "pa_copy_blocks", "pa_decode",
+    "PA_F16", "PA_Q4_0", "PA_Q8_0", "PaError", "Pool", "load", "load_calls", "row_bytes", "pa_append_rows", "pa_append_rows_f16", "pa_copy_blocks", "pa_decode",
     "pa_decode_workspace_size", "pa_decode_plan", "pa_get_error", "pa_selftest_wait_timeout", "status_name",
     "library_path", "pa_decode_noalloc", "PA_DT_F32", "PA_DT_F16", "PA_DT_BF16", "RopeDesc", "dtype_number",
     "pa_norm_rope", "pa_append_rows_rope", "pa_read_rows", "pa_decode_prefix", "pa_decode_prefix_workspace_size",
@@ -122,6 +122,31 @@ def load():
         return L
 
 
+_calls = None
+
+
+def load_calls():
+    """The Python module over the calls that run once per layer and step
+    (csrc/pa_calls.cpp); raises if it has not been built (no fallback)."""
+    global _calls
+    load()
+    with _lock:
+        if _calls is None:
+            import importlib.machinery
+            import importlib.util
+
+            import torch  # noqa: F401  (its libraries, before the module that uses them)
+            path = _build.CALLS_PATH
+            if not os.path.exists(path):
+                raise RuntimeError(f"pa_calls is not built ({path} missing); run paged_kv_gqa_11_gb300._build.build()")
+            loader = importlib.machinery.ExtensionFileLoader("pa_calls", path)
+            m = importlib.util.module_from_spec(importlib.util.spec_from_loader("pa_calls", loader))
+            loader.exec_module(m)
+            m.set_error(PaError)
+            _calls = m
+        return _calls
+
+
 def row_bytes(t: int, head_dim: int = 256) -> int:
     return int(load().pa_row_bytes(t, head_dim))
 
@@ -168,6 +193,10 @@ class Pool:
     @property
     def handle(self):
         return self._h
+
+    @property
+    def address(self) -> int:
+        return self._h.value
 
     def close(self):
         if getattr(self, "_h", None):

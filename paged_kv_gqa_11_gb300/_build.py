@@ -16,6 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libpa.so")
+CALLS_PATH = os.path.join(OUT_DIR, "pa_calls.so")  # the Python module over it (csrc/pa_calls.cpp)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 TYPES = {"f16": 1, "q4_0": 2, "q8_0": 8}  # pa_type numbers
 # (source, object name, extra defines): the split-decode and shared-prefix
@@ -43,9 +44,9 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -58,6 +59,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(obj_dir, exist_ok=True)
     procs = []
     objs = []
+    tmp = LIB_PATH + f".tmp{os.getpid()}"
+    calls_obj = os.path.join(obj_dir, "pa_calls.o")
+    procs.append(_calls_compile(cuda, calls_obj))
     for src, name, defs in UNITS:
         path = os.path.join(CSRC, src)
         obj = os.path.join(obj_dir, name + ".o")
@@ -80,12 +84,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
             failed.append(" ".join(cmd))
     if failed:
         raise RuntimeError("libpa build failed:\n" + "\n".join(failed))
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
     link = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-Xcompiler", "-fPIC",
             "-Xlinker", "-rpath", "-Xlinker", os.path.join(cuda, "lib64"), *objs, "-o", tmp]
     subprocess.run(link, check=True)
     os.replace(tmp, LIB_PATH)
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    subprocess.run(["g++", "-shared", calls_obj, "-o", tmp, "-L", OUT_DIR, "-l:libpa.so", "-L", lib, "-ltorch_python", "-ltorch",
+                    "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], check=True)
+    os.replace(tmp, CALLS_PATH)
     return LIB_PATH
+
+
+def _calls_compile(cuda: str, obj: str):
+    """The Python module's compilation, against torch's own headers."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    abi = int(getattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", True))
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", INCLUDE, "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"], "-isystem",
+           os.path.join(cuda, "include"), "-c", os.path.join(CSRC, "pa_calls.cpp"), "-o", obj]
+    return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
 
 
 if __name__ == "__main__":

@@ -7,15 +7,12 @@ buffers and passes pointers.
 """
 from __future__ import annotations
 
-import contextlib
-
 import numpy as np
 import torch
 
-from . import (PA_ERR_INVALID, PA_OK, PaError, Pool, dtype_number, load, pa_append_rows, pa_append_rows_f16,
-               pa_append_rows_rope, pa_decode, pa_decode_prefix, pa_decode_prefix_workspace_size,
-               pa_decode_workspace_size, pa_get_error, pa_read_rows)
-from .rope import HEAD_DIM, Rope, check_index, check_table, heads_of, weight_type
+from . import (PA_ERR_INVALID, PA_OK, PaError, Pool, load, load_calls, pa_append_rows, pa_append_rows_f16, pa_decode,
+               pa_decode_workspace_size, pa_get_error)
+from .rope import Rope
 
 
 class PagedKVCache:
@@ -24,6 +21,7 @@ class PagedKVCache:
                  k_pool: torch.Tensor | None = None, v_pool: torch.Tensor | None = None):
         """k_pool, v_pool: pools that exist already (uint8, the pool's bytes), else zeroed ones are made."""
         load()
+        self._calls = load_calls()
         self.device = torch.device(device)
         self.pool = Pool(n_blocks, page_size, n_kv_heads, head_dim, k_type, v_type)
         self.page_size = page_size
@@ -71,31 +69,9 @@ class PagedKVCache:
         normalised (with a weight), rotated to row_pos and stored, values stored;
         returns the queries, normalised and rotated, as q_dtype (default:
         q's own)."""
-        n = row_seq.shape[0]
-        check_index(row_seq, n, "row_seq")
-        check_index(row_pos, n, "row_pos")
-        check_table(block_table)
-        if k.shape != (n, self.n_kv_heads, HEAD_DIM) or v.shape != k.shape or v.dtype != k.dtype:
-            raise PaError(PA_ERR_INVALID, "append_rope: k and v rows [n][n_kv_heads][256] of one type")
-        in_type = dtype_number(k.dtype)
-        q_type = in_type
-        if q is not None:
-            if q.dtype != k.dtype or q.shape[0] != n:
-                raise PaError(PA_ERR_INVALID, "append_rope: q of k's type and row count")
-            if q_out is None:
-                with self._on(stream):
-                    q_out = torch.empty(q.shape, dtype=q.dtype if q_dtype is None else q_dtype, device=q.device)
-            if q_out.shape != q.shape or (q_dtype is not None and q_out.dtype != q_dtype):
-                raise PaError(PA_ERR_INVALID, "append_rope: q_out of q's shape")
-            q_type = dtype_number(q_out.dtype)
-        elif q_out is not None:
-            raise PaError(PA_ERR_INVALID, "append_rope: q_out without q")
-        qs, hq = heads_of(q, "q")
-        pa_append_rows_rope(self.pool, self.k_pool, self.v_pool, rope.address, k, heads_of(k, "k")[0], v,
-                            heads_of(v, "v")[0], in_type, k_weight, weight_type(k_weight, q_weight), q, qs, hq,
-                            q_weight, q_out, heads_of(q_out, "q_out")[0], q_type, row_seq, row_pos, n, block_table,
-                            block_table.shape[1], block_table.shape[0], self.err, stream)
-        return q_out
+        return self._calls.append_rope(self.pool.address, self.n_kv_heads, self.k_pool, self.v_pool, rope.address, k, v,
+                                       row_seq, row_pos, block_table, k_weight, q, q_weight, q_out, q_dtype, self.err,
+                                       stream)
 
     # ------------------------------------------------------------ reading back
     def read_rows(self, row_seq: torch.Tensor, row_pos: torch.Tensor, block_table: torch.Tensor,
@@ -104,32 +80,10 @@ class PagedKVCache:
         """The cache's rows at (row_seq, row_pos) as values [n][n_kv_heads][256];
         returns (k, v).  With only one of k_out, v_out given, only that one is
         read."""
-        n = row_seq.shape[0]
-        check_index(row_seq, n, "row_seq")
-        check_index(row_pos, n, "row_pos")
-        check_table(block_table)
-        shape = (n, self.n_kv_heads, HEAD_DIM)
-        if k_out is None and v_out is None:
-            with self._on(stream):
-                k_out = torch.empty(shape, dtype=dtype, device=row_seq.device)
-                v_out = torch.empty(shape, dtype=dtype, device=row_seq.device)
-        some = k_out if k_out is not None else v_out
-        for x in (k_out, v_out):
-            if x is not None and (x.shape != shape or x.dtype != some.dtype or not x.is_contiguous()):
-                raise PaError(PA_ERR_INVALID, "read_rows: outputs [n][n_kv_heads][256] of one type")
-        pa_read_rows(self.pool, self.k_pool, self.v_pool, row_seq, row_pos, n, block_table, block_table.shape[1],
-                     block_table.shape[0], k_out, v_out, dtype_number(some.dtype), self.err, stream)
-        return k_out, v_out
+        return self._calls.read_rows(self.pool.address, self.n_kv_heads, self.k_pool, self.v_pool, row_seq, row_pos,
+                                     block_table, dtype, k_out, v_out, self.err, stream)
 
     # ------------------------------------------------------------ decode
-    def _on(self, stream):
-        """Allocations for a call on `stream` come from that stream's memory."""
-        if stream is None:
-            return contextlib.nullcontext()
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=self.device)
-        return torch.cuda.stream(stream)
-
     def workspace(self, n_seq: int, n_qtok: int) -> torch.Tensor:
         dev = self.device.index if self.device.index is not None else torch.cuda.current_device()
         key = (n_seq, n_qtok, dev)
@@ -163,36 +117,15 @@ class PagedKVCache:
         """decode for sequences that share prefixes: the batch is runs of
         group_sizes[g] sequences, whose first prefix_lens[g] positions hold the
         same rows; those are read once for the run.  q: [n_seq][n_qtok][heads][256]
-        fp32, binary16 or bfloat16; out: q's shape, of q's type unless given.
+        fp32, binary16 or bfloat16; out: q's shape, of q's type unless given;
+        seq_lens_host, group_sizes, prefix_lens: host arrays of 32-bit whole
+        numbers (numpy).
         The workspace is taken from torch's allocator for each call, so calls on
         several streams, and captured ones, each have their own.  Returns
         (out, lse)."""
-        n_seq, _, hq, d = q.shape
-        if q.shape[1] != n_qtok or d != HEAD_DIM or not q.is_contiguous():
-            raise PaError(PA_ERR_INVALID, "decode_prefix: q [n_seq][n_qtok][heads][256], contiguous")
-        check_table(block_table)
-        sl = np.ascontiguousarray(seq_lens_host, dtype=np.int32)
-        gs = np.ascontiguousarray(group_sizes, dtype=np.uint32)
-        pl = np.ascontiguousarray(prefix_lens, dtype=np.int32)
-        if sl.shape != (n_seq,) or gs.ndim != 1 or gs.shape != pl.shape:
-            raise PaError(PA_ERR_INVALID, "decode_prefix: a length per sequence, a size and a prefix per group")
-        with self._on(stream):
-            if out is None:
-                out = torch.empty_like(q)
-            if lse is None and want_lse:
-                lse = torch.empty((n_seq, n_qtok, hq), dtype=torch.float32, device=self.device)
-            if workspace is None:
-                dev = self.device.index if self.device.index is not None else torch.cuda.current_device()
-                nbytes = pa_decode_prefix_workspace_size(self.pool, n_seq, len(gs), n_qtok, dev)
-                if nbytes == 0 and n_seq:
-                    raise PaError(PA_ERR_INVALID, "pa_decode_prefix_workspace_size")
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        if out.shape != q.shape or not out.is_contiguous():
-            raise PaError(PA_ERR_INVALID, "decode_prefix: out of q's shape, contiguous")
-        pa_decode_prefix(self.pool, q, dtype_number(q.dtype), self.k_pool, self.v_pool, block_table,
-                         block_table.shape[1], seq_lens_dev, sl, n_seq, gs, pl, len(gs), n_qtok, hq, scale, out,
-                         dtype_number(out.dtype), lse, workspace, workspace.numel(), self.err, stream)
-        return out, lse
+        return self._calls.decode_prefix(self.pool.address, q, self.k_pool, self.v_pool, block_table, seq_lens_dev,
+                                         seq_lens_host, group_sizes, prefix_lens, n_qtok, scale, out, lse, want_lse,
+                                         workspace, self.err, stream)
 
     def check(self, stream=None) -> int:
         """Synchronise, read and reset the device error word."""
