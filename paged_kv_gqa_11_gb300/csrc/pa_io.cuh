@@ -13,27 +13,54 @@
 
 namespace pa_dev {
 
+// Pairs of floats in 64 bits, for the paired fp32 instructions.
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+
 // Bytes of one value of a pa_dtype; 0 if there is no such type.
 inline int dtype_bytes(int32_t t) {
   return t == PA_DT_F32 ? 4 : t == PA_DT_F16 || t == PA_DT_BF16 ? 2 : 0;
 }
 
-// src 16-byte aligned.  Plain loads, not the read-only path: the rows may be
-// overwritten in place by the same kernel.
+// Eight values from the 16 (32 for fp32) bytes that hold them.
 template <typename T>
-__device__ __forceinline__ void load8(const uint8_t* src, float (&x)[8]);
+__device__ __forceinline__ void unpack8(const uint4* v, float (&x)[8]);
 
 template <>
-__device__ __forceinline__ void load8<float>(const uint8_t* src, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(src)[0], b = reinterpret_cast<const float4*>(src)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+__device__ __forceinline__ void unpack8<float>(const uint4* v, float (&x)[8]) {
+  const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
 }
 
 template <>
-__device__ __forceinline__ void load8<__half>(const uint8_t* src, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(src);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void unpack8<__half>(const uint4* v, float (&x)[8]) {
+  const uint32_t w[4] = {v->x, v->y, v->z, v->w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
@@ -43,14 +70,23 @@ __device__ __forceinline__ void load8<__half>(const uint8_t* src, float (&x)[8])
 }
 
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const uint8_t* src, float (&x)[8]) {
-  const uint4 v = *reinterpret_cast<const uint4*>(src);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void unpack8<__nv_bfloat16>(const uint4* v, float (&x)[8]) {
+  const uint32_t w[4] = {v->x, v->y, v->z, v->w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+}
+
+// src 16-byte aligned.  Plain loads, not the read-only path: the rows may be
+// overwritten in place by the same kernel.
+template <typename T>
+__device__ __forceinline__ void load8(const uint8_t* src, float (&x)[8]) {
+  uint4 v[sizeof(T) / 2];
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(src)[i];
+  unpack8<T>(v, x);
 }
 
 // Eight values packed in 16 bytes.
@@ -92,28 +128,6 @@ __device__ __forceinline__ void store8<float>(uint8_t* dst, const float (&x)[8])
 
 __host__ __device__ constexpr int row_bytes_of(int type) {
   return type == PA_F16 ? pa_layout::Fmt<PA_F16>::kRow : type == PA_Q8_0 ? pa_layout::Fmt<PA_Q8_0>::kRow : pa_layout::Fmt<PA_Q4_0>::kRow;
-}
-
-// Values 8 lane .. 8 lane + 7 of row r of the group at grp.
-__device__ __forceinline__ void read_row(int type, bool is_v, const uint8_t* grp, int r, int lane, float (&x)[8]) {
-  if (type == PA_F16) {
-    load8<__half>(grp + pa_layout::chunk_offset(0, pa_layout::Fmt<PA_F16>::kRowQ, r, lane), x);
-    return;
-  }
-  const int b = lane >> 2;
-  const float d = __half2float(
-      *reinterpret_cast<const __half*>(grp + (is_v ? pa_layout::v_scale_offset(r, b) : pa_layout::k_scale_offset(r, b))));
-  if (type == PA_Q8_0) {
-    const uint2 w = *reinterpret_cast<const uint2*>(grp + pa_layout::chunk_offset(256, pa_layout::Fmt<PA_Q8_0>::kRowQ, r, lane >> 1) +
-                                                    8 * (lane & 1));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)(int8_t)(((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xffu) * d;
-  } else {
-    const uint2 w = *reinterpret_cast<const uint2*>(grp + pa_layout::chunk_offset(256, pa_layout::Fmt<PA_Q4_0>::kRowQ, r, b) + 8 * (lane & 1));
-    const int sh = lane & 2 ? 4 : 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)((int)(((i < 4 ? w.x : w.y) >> (8 * (i & 3) + sh)) & 15u) - 8) * d;
-  }
 }
 
 }  // namespace pa_dev

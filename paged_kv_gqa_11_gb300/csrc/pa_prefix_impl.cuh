@@ -58,6 +58,7 @@
 #include <type_traits>
 
 #include "pa_decode_impl.cuh"
+#include "pa_io.cuh"
 
 namespace pa_prefix {
 
@@ -497,18 +498,8 @@ __device__ __forceinline__ void stage_q_end(const Params& p, uint32_t dst, int r
   }
 }
 
-// ------------------------------------------------------------------ pairs of floats
+// ------------------------------------------------------------------ the roles' common parts
 
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
 // The pair of floats in two registers.
 __device__ __forceinline__ uint64_t get2(const uint32_t* r) { return pack2(__uint_as_float(r[0]), __uint_as_float(r[1])); }
 __device__ __forceinline__ void put2(uint32_t* r, uint64_t v) {
@@ -516,23 +507,6 @@ __device__ __forceinline__ void put2(uint32_t* r, uint64_t v) {
   r[0] = __float_as_uint(f.x);
   r[1] = __float_as_uint(f.y);
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-// ------------------------------------------------------------------ the roles' common parts
 
 __device__ __forceinline__ bool bar_or(uint32_t id, uint32_t count, bool x) {
   uint32_t r;

@@ -10,19 +10,21 @@
 // An angle p w_i of a far position loses its fraction in 32 bits, and 64-bit
 // floating arithmetic is slow on this part, so the host turns every frequency
 // into 64-bit fixed-point turns (2^64 = one revolution): p times that, modulo
-// 2^64, is the phase, exact to p * 2^-53 revolutions; its top 32 bits go
-// through sincospif.
+// 2^64, is the phase, exact to p * 2^-53 revolutions.
 //
-// One warp works on one head at a time: lane l holds values 8l .. 8l+7 (16
+// One warp works on a few heads at a time: lane l holds values 8l .. 8l+7 (16
 // bytes of a 16-bit row), the sum of squares is a shuffle reduction in fp32,
-// the rotation partner half a rotation away comes by shuffles, and the cosines
-// stay in registers for all the heads of the row that the warp walks.
+// the rotation partner half a rotation away comes by shuffles of the loaded words,
+// and the cosines and sines, times the weights, stay in registers for all the
+// heads of the row that the warp walks.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "pa.h"
 #include "pa_device.cuh"
@@ -87,55 +89,65 @@ __device__ __forceinline__ bool place_of(const int32_t* table, int table_stride,
   return true;
 }
 
+// Four whole numbers -128 .. 255 as bytes.
+__device__ __forceinline__ uint32_t bytes4(int a, int b, int c, int d) {
+  return prmt(prmt((uint32_t)a, (uint32_t)b, 0x0040), prmt((uint32_t)c, (uint32_t)d, 0x0040), 0x5410);
+}
+
 // Store a head's values (lane l: 8l .. 8l+7) as row r of the group at grp.  The
 // quantisers are ggml's reference rule in fp32, every operation rounded on its
 // own, a block of 32 values being four neighbouring lanes:
 //   Q8_0: d = max|x| / 127, id = d ? 1/d : 0, q = round-half-away(x * id);
 //   Q4_0: m = the x of largest |x| (the first on ties), d = m / -8,
 //         q = min(15, trunc(x * id + 8.5)).
+// round-half-away(y) is trunc(y + copysign(1/2 - 2^-25, y)): the sum of a tie k +
+// 1/2 rounds up to k + 1, the one of the largest float below it stays below.
 __device__ __forceinline__ void store_row(int type, bool is_v, const float (&x)[8], uint8_t* grp, int r, int lane) {
   if (type == PA_F16) {
     *reinterpret_cast<uint4*>(grp + chunk_offset(0, Fmt<PA_F16>::kRowQ, r, lane)) = pack8<__half>(x);
     return;
   }
   const int b = lane >> 2;
-  float amax = 0.f, m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (fabsf(x[i]) > amax) {
-      amax = fabsf(x[i]);
-      m = x[i];
-    }
-#pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {  // the first of equals: the lower lane's
-    const float oa = __shfl_xor_sync(0xffffffffu, amax, o), om = __shfl_xor_sync(0xffffffffu, m, o);
-    if (oa > amax || (oa == amax && (lane & o))) {
-      amax = oa;
-      m = om;
-    }
-  }
   float d;
+  int q[8];
   if (type == PA_Q8_0) {
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     d = __fdiv_rn(amax, 127.f);
     const float id = d != 0.f ? __fdiv_rn(1.f, d) : 0.f;
-    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float y = __fmul_rn(x[i], id);
+      q[i] = __float2int_rz(__fadd_rn(y, copysignf(0.49999997f, y)));
+    }
+    *reinterpret_cast<uint2*>(grp + chunk_offset(256, Fmt<PA_Q8_0>::kRowQ, r, lane >> 1) + 8 * (lane & 1)) =
+        make_uint2(bytes4(q[0], q[1], q[2], q[3]), bytes4(q[4], q[5], q[6], q[7]));
+  } else {
+    float amax = 0.f, m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      w[i >> 2] |= ((uint32_t)(uint8_t)(int8_t)(int)roundf(__fmul_rn(x[i], id))) << (8 * (i & 3));
-    *reinterpret_cast<uint2*>(grp + chunk_offset(256, Fmt<PA_Q8_0>::kRowQ, r, lane >> 1) + 8 * (lane & 1)) =
-        make_uint2(w[0], w[1]);
-  } else {
+      if (fabsf(x[i]) > amax) {
+        amax = fabsf(x[i]);
+        m = x[i];
+      }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {  // the first of equals: the lower lane's
+      const float om = __shfl_xor_sync(0xffffffffu, m, o);
+      if (fabsf(om) > fabsf(m) || (fabsf(om) == fabsf(m) && (lane & o))) m = om;
+    }
     d = __fdiv_rn(m, -8.f);
     const float id = d != 0.f ? __fdiv_rn(1.f, d) : 0.f;
-    uint32_t w[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i >> 2] |= (uint32_t)min((int)truncf(__fadd_rn(__fmul_rn(x[i], id), 8.5f)), 15) << (8 * (i & 3));
+    for (int i = 0; i < 8; ++i) q[i] = min(__float2int_rz(__fadd_rn(__fmul_rn(x[i], id), 8.5f)), 15);
+    const uint32_t w0 = bytes4(q[0], q[1], q[2], q[3]), w1 = bytes4(q[4], q[5], q[6], q[7]);
     // lanes 0, 1 of a block hold its low nibbles, lanes 2, 3 the high ones
-    const uint32_t h0 = __shfl_xor_sync(0xffffffffu, w[0], 2), h1 = __shfl_xor_sync(0xffffffffu, w[1], 2);
+    const uint32_t h0 = __shfl_xor_sync(0xffffffffu, w0, 2), h1 = __shfl_xor_sync(0xffffffffu, w1, 2);
     if (!(lane & 2))
       *reinterpret_cast<uint2*>(grp + chunk_offset(256, Fmt<PA_Q4_0>::kRowQ, r, b) + 8 * (lane & 1)) =
-          make_uint2(w[0] | (h0 << 4), w[1] | (h1 << 4));
+          make_uint2(w0 | (h0 << 4), w1 | (h1 << 4));
   }
   if ((lane & 3) == 0)
     *reinterpret_cast<uint16_t*>(grp + (is_v ? v_scale_offset(r, b) : k_scale_offset(r, b))) =
@@ -144,74 +156,183 @@ __device__ __forceinline__ void store_row(int type, bool is_v, const float (&x)[
 
 // ------------------------------------------------------------------ norm and rotation
 
-// A row's cosines and sines for this lane's values.
+// What a lane multiplies its values and their partners by: the cosines and
+// (signed) sines of its row, times the weights of one kind of head; two values
+// to an element, for the paired fp32 instructions.
 struct Turn {
-  float c[8], s[8];
+  uint64_t c[4], s[4];
 };
 
-__device__ __forceinline__ void make_turn(const RopeParams& p, const uint64_t* turns, int pos, int lane, Turn* t) {
-  const int half = p.rot >> 1;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int d = 8 * lane + i;
-    float c = 1.f, s = 0.f;
-    if (d < p.rot) {
-      const int pair = p.interleaved ? d >> 1 : d < half ? d : d - half;
-      const uint64_t phase = (uint64_t)(int64_t)pos * turns[pair];
-      const float x = (float)(int32_t)(uint32_t)(phase >> 32) * (1.f / 2147483648.f);  // half-turns
-      sincospif(x, &s, &c);
-      c *= p.factor;
-      s *= p.factor;
-      if (p.interleaved ? !(d & 1) : d < half) s = -s;  // the first of a pair takes -sin
-    }
-    t->c[i] = c;
-    t->s[i] = s;
-  }
+// cos and sin of `phase` / 2^32 revolutions: the nearest quarter turn apart, the
+// rest (at most pi / 4) by Taylor's series, whose next terms, t^10 / 10! and
+// t^11 / 11!, are below 2^-25.
+__device__ __forceinline__ void cos_sin(uint32_t phase, float* c, float* s) {
+  const uint32_t near = phase + 0x20000000u, quarter = near >> 30;
+  const float t = (float)((int32_t)(near & 0x3fffffffu) - 0x20000000) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float u = t * t;
+  float a = fmaf(u, 2.7557319e-6f, -1.9841270e-4f);
+  a = fmaf(u, a, 8.3333333e-3f);
+  a = fmaf(u, a, -1.6666667e-1f);
+  a = fmaf(t * u, a, t);
+  float b = fmaf(u, 2.4801587e-5f, -1.3888889e-3f);
+  b = fmaf(u, b, 4.1666667e-2f);
+  b = fmaf(u, b, -0.5f);
+  b = fmaf(u, b, 1.f);
+  const float x = (quarter & 1) ? a : b, y = (quarter & 1) ? b : a;
+  *c = __uint_as_float(__float_as_uint(x) ^ (((quarter + 1) & 2) << 30));
+  *s = __uint_as_float(__float_as_uint(y) ^ ((quarter & 2) << 30));
 }
 
-__device__ __forceinline__ void norm_turn(const RopeParams& p, float (&x)[8], const float (&w)[8], bool norm,
-                                          const Turn& t, int lane) {
-  if (norm) {
-    float ss = 0.f;
+// The lane that holds the partners of this lane's values (itself when they are
+// its own, or when there is nothing to turn).
+__device__ __forceinline__ int partner_lane(const RopeParams& p, int lane) {
+  const int h = p.rot >> 4;  // lanes of half a rotation
+  return p.interleaved || lane >= 2 * h ? lane : lane < h ? lane + h : lane - h;
+}
+
+// A lane computes four of the angles of its row: its own four pairs, or half of
+// the eight that it shares with its partner lane.
+__device__ __forceinline__ Turn make_turn(const RopeParams& p, const uint64_t* turns, int pos, int lane, int from) {
+  float c[8], s[8];
+  const bool turned = 8 * lane < p.rot, second = from < lane;
+  float ac[4], as[4];
+  const int pair0 = p.interleaved ? 4 * lane : second ? 8 * from + 4 : 8 * lane;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = rsqrtf(ss * (1.f / kD) + p.eps);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+  for (int j = 0; j < 4; ++j) {
+    ac[j] = 1.f;
+    as[j] = 0.f;
+    if (turned) {
+      const uint64_t phase = (uint64_t)(int64_t)pos * turns[pair0 + j];
+      cos_sin((uint32_t)(phase >> 32), &ac[j], &as[j]);
+      ac[j] *= p.factor;
+      as[j] *= p.factor;
+    }
   }
-  if (p.rot == 0) return;
   if (p.interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const float a = x[i], b = x[i + 1];
-      x[i] = fmaf(a, t.c[i], b * t.s[i]);
-      x[i + 1] = fmaf(b, t.c[i + 1], a * t.s[i + 1]);
+    for (int i = 0; i < 8; ++i) {
+      c[i] = ac[i >> 1];
+      s[i] = (i & 1) ? as[i >> 1] : -as[i >> 1];  // the first of a pair takes -sin
     }
   } else {
-    const int h = p.rot >> 4;  // lanes of half a rotation
-    const int from = lane < h ? lane + h : lane < 2 * h ? lane - h : lane;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_sync(0xffffffffu, x[i], from);
-      x[i] = fmaf(x[i], t.c[i], o * t.s[i]);
+    for (int j = 0; j < 4; ++j) {
+      const float oc = __shfl_sync(0xffffffffu, ac[j], from), os = __shfl_sync(0xffffffffu, as[j], from);
+      c[j] = second ? oc : ac[j];
+      c[j + 4] = second ? ac[j] : oc;
+      s[j] = second ? os : -as[j];
+      s[j + 4] = second ? as[j] : -os;
     }
+  }
+  Turn t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    t.c[i] = pack2(c[2 * i], c[2 * i + 1]);
+    t.s[i] = pack2(s[2 * i], s[2 * i + 1]);
+  }
+  return t;
+}
+
+// The turn times a weight vector (value i's own, and its partner's).
+__device__ __forceinline__ Turn weighted(const RopeParams& p, const Turn& t, const void* w, int lane, int from) {
+  if (!w) return t;
+  float x[8];
+  if (p.w_type == PA_DT_F32) load8<float>(static_cast<const uint8_t*>(w) + 32 * lane, x);
+  else if (p.w_type == PA_DT_F16) load8<__half>(static_cast<const uint8_t*>(w) + 16 * lane, x);
+  else load8<__nv_bfloat16>(static_cast<const uint8_t*>(w) + 16 * lane, x);
+  Turn r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] += p.w_offset;
+  float o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = p.interleaved ? x[i ^ 1] : __shfl_sync(0xffffffffu, x[i], from);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.c[i] = mul2(t.c[i], pack2(x[2 * i], x[2 * i + 1]));
+    r.s[i] = mul2(t.s[i], pack2(o[2 * i], o[2 * i + 1]));
+  }
+  return r;
+}
+
+// A lane's eight values as loaded.
+template <typename T>
+struct Raw {
+  uint4 v[sizeof(T) / 2];
+
+  __device__ __forceinline__ void load(const uint8_t* src) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(src)[i];
+  }
+  __device__ __forceinline__ Raw from_lane(int l) const {
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      r.v[i] = make_uint4(__shfl_sync(0xffffffffu, v[i].x, l), __shfl_sync(0xffffffffu, v[i].y, l),
+                          __shfl_sync(0xffffffffu, v[i].z, l), __shfl_sync(0xffffffffu, v[i].w, l));
+    return r;
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const { unpack8<T>(v, x); }
+  __device__ __forceinline__ void get(uint64_t (&x)[4]) const {
+    float f[8];
+    get(f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = pack2(f[2 * i], f[2 * i + 1]);
+  }
+};
+
+// 1 / sqrt(mean(x^2) + eps) of N heads; the heads' shuffles interleave, so that
+// their latencies overlap.
+template <typename T, int N>
+__device__ __forceinline__ void inverse_norms(const RopeParams& p, const Raw<T> (&raw)[N], float (&r)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    uint64_t x[4];
+    raw[k].get(x);
+    uint64_t sq = mul2(x[0], x[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) sq = fma2(x[i], x[i], sq);
+    const float2 h = unpack2(sq);
+    r[k] = h.x + h.y;
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) r[k] += __shfl_xor_sync(0xffffffffu, r[k], m);
+#pragma unroll
+  for (int k = 0; k < N; ++k) r[k] = rsqrtf(r[k] * (1.f / kD) + p.eps);
+}
+
+// y = r (x c + partner s), the weights inside c and s.
+template <typename T>
+__device__ __forceinline__ void turn_head(const RopeParams& p, const Raw<T>& raw, const Turn& t, float r, int from, float (&y)[8]) {
+  uint64_t x[4], o[4];
+  raw.get(x);
+  if (p.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpack2(x[i]);
+      o[i] = pack2(v.y, v.x);
+    }
+  } else {
+    raw.from_lane(from).get(o);
+  }
+  const uint64_t rr = pack2(r, r);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack2(mul2(fma2(x[i], t.c[i], mul2(o[i], t.s[i])), rr));
+    y[2 * i] = v.x;
+    y[2 * i + 1] = v.y;
   }
 }
 
-__device__ __forceinline__ void load_weight(const RopeParams& p, const void* w, int lane, float (&out)[8]) {
-  if (!w) return;
-  if (p.w_type == PA_DT_F32) load8<float>(static_cast<const uint8_t*>(w) + 32 * lane, out);
-  else if (p.w_type == PA_DT_F16) load8<__half>(static_cast<const uint8_t*>(w) + 16 * lane, out);
-  else load8<__nv_bfloat16>(static_cast<const uint8_t*>(w) + 16 * lane, out);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] += p.w_offset;
-}
+// Heads whose loads are in flight at once, warps that few rows are split into,
+// and resident CTAs that the registers allow (20 warps an SM).  4096 rows of bf16:
+// 26.7 us (4.4 TB/s); batches of two 28.4, of eight 32.8 (107 registers).
+constexpr int kBatch = 4, kWarpsPerSm = 48, kMinCtas = 5;
 
 // kAppend: keys and values go into the pools; else keys go to k_out.
 template <typename In, typename Out, bool kAppend>
-__global__ void __launch_bounds__(32 * kWarps) pa_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(32 * kWarps, kMinCtas) pa_rope_kernel(const __grid_constant__ RopeParams p) {
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
   __shared__ uint64_t turns[kMaxPairs];
   const int lane = threadIdx.x & 31;
@@ -222,42 +343,68 @@ __global__ void __launch_bounds__(32 * kWarps) pa_rope_kernel(const __grid_const
   if (row >= p.n_rows) return;
   const int chunk = (int)(item - row * p.chunks);
   const int h0 = chunk * p.per, h1 = min(h0 + p.per, p.hq + p.hk + p.hv);
-  const int pos = __ldg(p.row_pos + row);
-  Turn t;
-  if (h0 < p.hq + p.hk) make_turn(p, turns, pos, lane, &t);
-  float wq[8], wk[8];
-  if (h0 < p.hq) load_weight(p, p.wq, lane, wq);
-  if (h0 < p.hq + p.hk && h1 > p.hq) load_weight(p, p.wk, lane, wk);
+  const int pos = __ldg(p.row_pos + row), from = partner_lane(p, lane);
   Place at{};
   bool placed = false;
   if (kAppend && h1 > p.hq) {
     placed = place_of(p.table, p.table_stride, p.n_seq, p.n_blocks, p.page_size, p.hk, __ldg(p.row_seq + row), pos, &at);
     if (!placed && lane == 0) record_error(p.err, PA_ERR_BOUNDS);
   }
-  for (int h = h0; h < h1; ++h) {
-    float x[8];
-    if (h < p.hq) {
-      load8<In>(p.q + row * p.q_stride + (long long)h * kD * sizeof(In) + 8 * sizeof(In) * lane, x);
-      norm_turn(p, x, wq, p.wq != nullptr, t, lane);
-      store8<Out>(p.q_out + row * p.q_out_stride + (long long)h * kD * sizeof(Out) + 8 * sizeof(Out) * lane, x);
-    } else if (h < p.hq + p.hk) {
-      const int hh = h - p.hq;
-      load8<In>(p.k + row * p.k_stride + (long long)hh * kD * sizeof(In) + 8 * sizeof(In) * lane, x);
-      norm_turn(p, x, wk, p.wk != nullptr, t, lane);
-      if constexpr (kAppend) {
-        if (placed)
-          store_row(p.k_type, false, x, p.k_pool + (at.grp_row + (long long)hh * p.page_size) * row_bytes_of(p.k_type),
-                    at.r, lane);
-      } else {
-        store8<Out>(p.k_out + row * p.k_out_stride + (long long)hh * kD * sizeof(Out) + 8 * sizeof(Out) * lane, x);
+  // Heads a .. b - 1 of one kind, kBatch at a time: normalised (norm) and turned
+  // by t, or as they are (no t), to `put` with their number.
+  auto heads = [&](const uint8_t* src, int a, int b, const Turn* t, bool norm, auto&& put) {
+    constexpr int kHead = kD * (int)sizeof(In);
+    src += a * kHead + 8 * (int)sizeof(In) * lane;
+    auto batch = [&](auto count) {
+      constexpr int N = decltype(count)::value;
+      Raw<In> raw[N];
+      float r[N], y[8];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        raw[i].load(src + i * kHead);
+        r[i] = 1.f;
       }
-    } else if constexpr (kAppend) {
-      const int hh = h - p.hq - p.hk;
-      load8<In>(p.v + row * p.v_stride + (long long)hh * kD * sizeof(In) + 8 * sizeof(In) * lane, x);
-      if (placed)
-        store_row(p.v_type, true, x, p.v_pool + (at.grp_row + (long long)hh * p.page_size) * row_bytes_of(p.v_type),
-                  at.r, lane);
+      if (norm) inverse_norms<In, N>(p, raw, r);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        if (t) turn_head<In>(p, raw[i], *t, r[i], from, y);
+        else raw[i].get(y);
+        put(a + i, y);
+      }
+      a += N;
+      src += N * kHead;
+    };
+    while (a + kBatch <= b) batch(std::integral_constant<int, kBatch>());
+    while (a < b) batch(std::integral_constant<int, 1>());
+  };
+  const int qk = p.hq + p.hk;
+  if (h0 < qk) {
+    const Turn t = make_turn(p, turns, pos, lane, from);
+    if (h0 < p.hq) {
+      const Turn tq = weighted(p, t, p.wq, lane, from);
+      uint8_t* out = p.q_out + row * p.q_out_stride + 8 * (int)sizeof(Out) * lane;
+      heads(p.q + row * p.q_stride, h0, min(h1, p.hq), &tq, p.wq != nullptr,
+            [&](int h, const float (&y)[8]) { store8<Out>(out + h * kD * (int)sizeof(Out), y); });
     }
+    if (h1 > p.hq) {
+      const Turn tk = weighted(p, t, p.wk, lane, from);
+      heads(p.k + row * p.k_stride, max(h0, p.hq) - p.hq, min(h1, qk) - p.hq, &tk, p.wk != nullptr,
+            [&](int h, const float (&y)[8]) {
+              if constexpr (kAppend) {
+                if (placed)
+                  store_row(p.k_type, false, y, p.k_pool + (at.grp_row + (long long)h * p.page_size) * row_bytes_of(p.k_type),
+                            at.r, lane);
+              } else {
+                store8<Out>(p.k_out + row * p.k_out_stride + (h * kD + 8 * lane) * (int)sizeof(Out), y);
+              }
+            });
+    }
+  }
+  if constexpr (kAppend) {
+    if (h1 > qk && placed)
+      heads(p.v + row * p.v_stride, max(h0, qk) - qk, h1 - qk, nullptr, false, [&](int h, const float (&y)[8]) {
+        store_row(p.v_type, true, y, p.v_pool + (at.grp_row + (long long)h * p.page_size) * row_bytes_of(p.v_type), at.r, lane);
+      });
   }
 }
 
@@ -274,31 +421,120 @@ struct ReadParams {
   int32_t* err;
   long long n_rows;
   int n_heads, page_size, table_stride, n_seq, n_blocks, k_type, v_type;
+  int pools, rows;  // pools read; rows of a warp
 };
 
-// One warp per (row, head): its K row, then its V row.
+constexpr int kReadRows = 8;  // rows of a warp, looked up by a lane each
+
+// A lane's eight values of a stored row: the quants as exact binary16 pairs and
+// their scale, or binary16 values.
+template <int T>
+struct Stored {
+  uint32_t h[4];
+  uint32_t d;  // the scale twice
+
+  uint4 raw;
+  __device__ __forceinline__ void load(const uint8_t* grp, int r, int lane, bool is_v) {
+    if (T == PA_F16) {
+      raw = *reinterpret_cast<const uint4*>(grp + chunk_offset(0, Fmt<T>::kRowQ, r, lane));
+      return;
+    }
+    const int b = lane >> 2;
+    const uint2 w = *reinterpret_cast<const uint2*>(
+        grp + chunk_offset(256, Fmt<T>::kRowQ, r, T == PA_Q8_0 ? lane >> 1 : b) + 8 * (lane & 1));
+    raw = make_uint4(w.x, w.y, 0u, 0u);
+    d = *reinterpret_cast<const uint16_t*>(grp + (is_v ? v_scale_offset(r, b) : k_scale_offset(r, b)));
+  }
+  // The values as Out, the exact products rounded once.
+  template <typename Out>
+  __device__ __forceinline__ void store(uint8_t* dst, int lane) {
+    float x[8];
+    if (T == PA_F16) {
+      if (sizeof(Out) == 2 && std::is_same<Out, __half>::value) {
+        *reinterpret_cast<uint4*>(dst) = raw;
+        return;
+      }
+      unpack8<__half>(&raw, x);
+      store8<Out>(dst, x);
+      return;
+    }
+    // bytes 0 .. 255 under 0x64 are the binary16 numbers 1024 + byte
+    const uint32_t bias = T == PA_Q8_0 ? 0xe480e480u : 0xe408e408u;  // -1152, -1032
+    uint32_t w[2] = {raw.x, raw.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w[i] = T == PA_Q8_0 ? w[i] ^ 0x80808080u : (w[i] >> ((lane & 2) << 1)) & 0x0f0f0f0fu;
+      h[2 * i] = hadd2(prmt(w[i], 0x64646464u, 0x4140), bias);
+      h[2 * i + 1] = hadd2(prmt(w[i], 0x64646464u, 0x4342), bias);
+    }
+    const uint32_t d2 = d | (d << 16);
+    if (std::is_same<Out, __half>::value) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(hmul2(h[0], d2), hmul2(h[1], d2), hmul2(h[2], d2), hmul2(h[3], d2));
+      return;
+    }
+    const float df = __half2float(__ushort_as_half((unsigned short)d));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+      x[2 * i] = f.x * df;
+      x[2 * i + 1] = f.y * df;
+    }
+    store8<Out>(dst, x);
+  }
+};
+
+// The heads of one row of one pool, four in flight at a time.
+template <int T, typename Out>
+__device__ __forceinline__ void read_heads(const uint8_t* pool, bool is_v, long long grp_row, int r, bool placed, int n_heads,
+                                           int page_size, uint8_t* dst, int lane) {
+  const uint8_t* grp = pool + grp_row * Fmt<T>::kRow;
+  const long long step = (long long)page_size * Fmt<T>::kRow;
+  dst += 8 * lane * (int)sizeof(Out);
+  if (!placed) {
+    const float zero[8] = {};
+    for (int h = 0; h < n_heads; ++h) store8<Out>(dst + h * kD * (int)sizeof(Out), zero);
+    return;
+  }
+  for (int h = 0; h < n_heads; h += 4) {
+    Stored<T> s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (h + i < n_heads) s[i].load(grp + (h + i) * step, r, lane, is_v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (h + i < n_heads) s[i].template store<Out>(dst + (h + i) * kD * (int)sizeof(Out), lane);
+  }
+}
+
+// A warp per kRows rows of K or of V; their places are looked up at once, a lane
+// for each: the three dependent loads of a lookup take longer than a row's copy.
+template <int T, typename Out>
+__device__ __forceinline__ void read_warp(const ReadParams& p, bool is_v, long long row0, int rows, int lane) {
+  Place at{};
+  bool placed = false;
+  if (lane < rows)
+    placed = place_of(p.table, p.table_stride, p.n_seq, p.n_blocks, p.page_size, p.n_heads, __ldg(p.row_seq + row0 + lane),
+                      __ldg(p.row_pos + row0 + lane), &at);
+  if (lane < rows && !placed) record_error(p.err, PA_ERR_BOUNDS);
+  for (int i = 0; i < rows; ++i)
+    read_heads<T, Out>(is_v ? p.v_pool : p.k_pool, is_v, __shfl_sync(0xffffffffu, at.grp_row, i), __shfl_sync(0xffffffffu, at.r, i),
+                       __shfl_sync(0xffffffffu, (int)placed, i) != 0, p.n_heads, p.page_size,
+                       (is_v ? p.v_out : p.k_out) + (row0 + i) * p.n_heads * kD * (long long)sizeof(Out), lane);
+}
+
 template <typename Out>
 __global__ void __launch_bounds__(32 * kWarps) pa_read_kernel(const __grid_constant__ ReadParams p) {
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31;
   const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const long long row = item / p.n_heads;
-  if (row >= p.n_rows) return;
-  const int head = (int)(item - row * p.n_heads);
-  Place at{};
-  const bool placed = place_of(p.table, p.table_stride, p.n_seq, p.n_blocks, p.page_size, p.n_heads,
-                               __ldg(p.row_seq + row), __ldg(p.row_pos + row), &at);
-  if (!placed && lane == 0) record_error(p.err, PA_ERR_BOUNDS);
-  const long long gr = at.grp_row + (long long)head * p.page_size, o = (item * kD + 8 * lane) * (long long)sizeof(Out);
-  float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (p.k_out) {
-    if (placed) read_row(p.k_type, false, p.k_pool + gr * row_bytes_of(p.k_type), at.r, lane, x);
-    store8<Out>(p.k_out + o, x);
-  }
-  if (p.v_out) {
-    if (placed) read_row(p.v_type, true, p.v_pool + gr * row_bytes_of(p.v_type), at.r, lane, x);
-    store8<Out>(p.v_out + o, x);
-  }
+  const long long batch = item / p.pools;
+  const long long row0 = batch * p.rows;
+  if (row0 >= p.n_rows) return;
+  const bool is_v = p.pools == 1 ? p.k_out == nullptr : item - batch * p.pools != 0;
+  const int rows = (int)min((long long)p.rows, p.n_rows - row0), type = is_v ? p.v_type : p.k_type;
+  if (type == PA_F16) read_warp<PA_F16, Out>(p, is_v, row0, rows, lane);
+  else if (type == PA_Q8_0) read_warp<PA_Q8_0, Out>(p, is_v, row0, rows, lane);
+  else read_warp<PA_Q4_0, Out>(p, is_v, row0, rows, lane);
 }
 
 // ------------------------------------------------------------------ host side
@@ -345,18 +581,23 @@ pa_status sm_count(int* sms) {
   return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, device) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// Few rows: a warp per head, so that a step of one token spreads over the SMs;
+// many rows: a warp walks more heads of its row and computes the row's angles
+// once for them.
+void split_heads(int heads, long long rows, int sms, int* chunks, int* per) {
+  long long want = (kWarpsPerSm * (long long)sms + rows - 1) / rows;
+  if (want > heads) want = heads;
+  *per = (int)((heads + want - 1) / want);
+  if (*per > kBatch) *per = (*per + kBatch - 1) / kBatch * kBatch;  // whole batches of loads
+  *chunks = (heads + *per - 1) / *per;
+}
+
 template <typename In, typename Out, bool kAppend>
 pa_status launch_rope(RopeParams& p, cudaStream_t cs) {
   int sms = 0;
   const pa_status st = sm_count(&sms);
   if (st != PA_OK) return st;
-  // Few rows: a warp per head, so that a step of one token spreads over the
-  // SMs; many rows: a warp walks more heads of its row and computes the row's
-  // angles once for them.
-  const int heads = p.hq + p.hk + p.hv;
-  const long long want = (32ll * sms + p.n_rows - 1) / p.n_rows;
-  p.per = (int)((heads + (want < heads ? want : heads) - 1) / (want < heads ? want : heads));
-  p.chunks = (heads + p.per - 1) / p.per;
+  split_heads(p.hq + p.hk + p.hv, p.n_rows, sms, &p.chunks, &p.per);
   const long long items = p.n_rows * p.chunks, grid = (items + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffll) return PA_ERR_UNSUPPORTED;
   pa_rope_kernel<In, Out, kAppend><<<(unsigned)grid, 32 * kWarps, 0, cs>>>(p);
@@ -510,7 +751,12 @@ extern "C" pa_status pa_read_rows(const pa_pool* pool, const void* k_pool, const
   p.n_blocks = (int)d.n_blocks;
   p.k_type = d.k_type;
   p.v_type = d.v_type;
-  const long long grid = ((long long)n_rows * d.n_kv_heads + kWarps - 1) / kWarps;
+  int sms = 0;
+  const pa_status st = sm_count(&sms);
+  if (st != PA_OK) return st;
+  p.pools = (k_out != nullptr) + (v_out != nullptr);
+  p.rows = (int)std::min<long long>(kReadRows, ((long long)n_rows * p.pools + 32ll * sms - 1) / (32ll * sms));  // 1 while warps are few
+  const long long grid = (((long long)n_rows + p.rows - 1) / p.rows * p.pools + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffll) return PA_ERR_UNSUPPORTED;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (out_type == PA_DT_F32) pa_read_kernel<float><<<(unsigned)grid, 32 * kWarps, 0, cs>>>(p);
