@@ -6,7 +6,7 @@
 // row groups (16 keys; the rest joins the suffixes, so a suffix's row groups
 // are whole too), and read as a shared prefix when that takes fewer key tiles
 // than leaving it in every sequence's own keys.  The tiles, prefixes first, are
-// cut into equal contiguous ranges, one CTA per SM.
+// cut into contiguous ranges of equal cost, one CTA per SM (cost_of).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,10 +38,10 @@ struct MergeParams {
   float* lse;
   int32_t* err;
   int out_type, n_qtok, n_kv_heads, n_q_heads, n_ctas;
-  int prefix_tiles, total_tiles, suffix_row_tiles, suffix_rows, suffix_base;
-  int32_t len[kMaxSeqs], start[kMaxSeqs], seq_tile[kMaxSeqs];
+  int weigh, prefix_len, total_len, suffix_row_tiles, suffix_rows, suffix_base;
+  int32_t len[kMaxSeqs], start[kMaxSeqs], seq_at[kMaxSeqs];
   int16_t group[kMaxSeqs];  // a sequence's group, or -1
-  int32_t group_first[kMaxGroups], group_seqs[kMaxGroups], group_keys[kMaxGroups], group_tile[kMaxGroups],
+  int32_t group_first[kMaxGroups], group_seqs[kMaxGroups], group_keys[kMaxGroups], group_at[kMaxGroups],
       group_seg[kMaxGroups];
 };
 
@@ -51,8 +51,11 @@ struct Pieces {
   int n, step;
 };
 
-__device__ __forceinline__ Pieces pieces_of(const MergeParams& p, int tile, int nt, int seg, int step, int base, int r) {
-  const int c0 = cta_of(tile, p.total_tiles, p.n_ctas), c1 = cta_of(tile + nt - 1, p.total_tiles, p.n_ctas);
+__device__ __forceinline__ Pieces pieces_of(const MergeParams& p, int at, int unit_rows, int in_unit, int nt, int seg,
+                                            int step, int base, int r) {
+  const Cost c = cost_of(p.weigh, unit_rows);
+  at += in_unit * (c.lead + nt * c.tile) + c.lead;
+  const int c0 = cta_of(at, p.total_len, p.n_ctas), c1 = cta_of(at + (nt - 1) * c.tile, p.total_len, p.n_ctas);
   return Pieces{base + (long long)(c0 + seg) * step + r, c1 - c0 + 1, step};
 }
 
@@ -73,14 +76,14 @@ __global__ void __launch_bounds__(kMergeThreads) pa_prefix_merge_kernel(const __
   {
     const int nt = ceil_div(p.len[s] - p.start[s], kKeys), rg = t * kGqa + hl, rt = rg / kRows;
     const int seg = (s * p.n_kv_heads + head) * p.suffix_row_tiles + rt;
-    a = pieces_of(p, p.prefix_tiles + p.seq_tile[s] + (head * p.suffix_row_tiles + rt) * nt, nt, seg, p.suffix_rows,
+    a = pieces_of(p, p.prefix_len + p.seq_at[s], kGqa * p.n_qtok, head * p.suffix_row_tiles + rt, nt, seg, p.suffix_rows,
                   p.suffix_base, rg % kRows);
   }
   const int g = p.group[s];
   if (g >= 0) {
-    const int nt = ceil_div(p.group_keys[g], kKeys), nrt = ceil_div(kGqa * p.n_qtok * p.group_seqs[g], kRows);
+    const int nt = ceil_div(p.group_keys[g], kKeys), rows = kGqa * p.n_qtok * p.group_seqs[g], nrt = ceil_div(rows, kRows);
     const int rg = ((s - p.group_first[g]) * p.n_qtok + t) * kGqa + hl, rt = rg / kRows;
-    b = pieces_of(p, p.group_tile[g] + (head * nrt + rt) * nt, nt, p.group_seg[g] + head * nrt + rt, kRows, 0, rg % kRows);
+    b = pieces_of(p, p.group_at[g], rows, head * nrt + rt, nt, p.group_seg[g] + head * nrt + rt, kRows, 0, rg % kRows);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
@@ -280,20 +283,36 @@ pa_status run_chunk(const Batch& b, uint32_t c0, uint32_t cn, const Group* group
     p.group_first[ng] = m.group_first[ng] = g.first;
     p.group_seqs[ng] = m.group_seqs[ng] = g.n;
     p.group_keys[ng] = m.group_keys[ng] = keys;
-    p.group_tile[ng] = m.group_tile[ng] = (int32_t)tiles;
+    p.group_tile[ng] = (int32_t)tiles;
     p.group_seg[ng] = m.group_seg[ng] = (int32_t)segs;
     tiles += (int64_t)heads * nrt * ceil_div(keys, kKeys);
     segs += (int64_t)heads * nrt;
-    if (tiles >= (1ll << 30)) return PA_ERR_UNSUPPORTED;
+    if (tiles >= (1ll << 27)) return PA_ERR_UNSUPPORTED;
     ++ng;
   }
-  const int64_t prefix_tiles = tiles;
   for (uint32_t i = 0; i < cn; ++i) {
-    p.seq_tile[i] = m.seq_tile[i] = (int32_t)(tiles - prefix_tiles);
+    p.seq_tile[i] = (int32_t)tiles;
     tiles += (int64_t)heads * srt * ceil_div(p.len[i] - p.start[i], kKeys);
-    if (tiles >= (1ll << 30)) return PA_ERR_UNSUPPORTED;
+    if (tiles >= (1ll << 27)) return PA_ERR_UNSUPPORTED;
   }
   const int ctas = (int)std::min<int64_t>(tiles, b.sms);
+  // every CTA must have a tile: with weights its range is longer than a lead and
+  // a tile
+  const int weigh = tiles > 3 * ctas;
+  int64_t at = 0;
+  for (int k = 0; k < ng; ++k) {
+    const int rows = kGqa * T * p.group_seqs[k];
+    const Cost c = cost_of(weigh, rows);
+    p.group_at[k] = m.group_at[k] = (int32_t)at;
+    at += (int64_t)heads * ceil_div(rows, kRows) * (c.lead + ceil_div(p.group_keys[k], kKeys) * c.tile);
+  }
+  const int64_t prefix_len = at;
+  const Cost c = cost_of(weigh, kGqa * T);
+  for (uint32_t i = 0; i < cn; ++i) {
+    p.seq_at[i] = m.seq_at[i] = (int32_t)(at - prefix_len);
+    at += (int64_t)heads * srt * (c.lead + ceil_div(p.len[i] - p.start[i], kKeys) * c.tile);
+  }
+  if (at >= (1ll << 30)) return PA_ERR_UNSUPPORTED;
   const int64_t base = (ctas + segs) * kRows,
                 rows = base + (ctas + (int64_t)heads * cn * srt) * suffix_rows_of(b.n_qtok);
   const WsLayout lay = layout_of(rows);
@@ -319,8 +338,10 @@ pa_status run_chunk(const Batch& b, uint32_t c0, uint32_t cn, const Group* group
   p.n_seq = (int)cn;
   p.n_groups = ng;
   p.n_ctas = m.n_ctas = ctas;
-  p.prefix_tiles = m.prefix_tiles = (int32_t)prefix_tiles;
-  p.total_tiles = m.total_tiles = (int32_t)tiles;
+  p.weigh = m.weigh = weigh;
+  p.total_tiles = (int)tiles;
+  p.prefix_len = m.prefix_len = (int32_t)prefix_len;
+  p.total_len = m.total_len = (int32_t)at;
   p.suffix_row_tiles = m.suffix_row_tiles = srt;
   p.suffix_rows = m.suffix_rows = suffix_rows_of(b.n_qtok);
   p.suffix_base = m.suffix_base = (int32_t)base;

@@ -10,10 +10,11 @@
 //
 //   segment  = (group, KV head, tile of 64 query rows) over the prefix's keys,
 //              or (sequence, KV head, row tile) over the suffix's; cut into key
-//              tiles of 128; all tiles of the batch are laid end to end and cut
-//              into one contiguous range per CTA (one CTA per SM).  A range's
-//              share of a segment is a piece; every piece leaves (m, l) and O in
-//              the workspace for the merge.
+//              tiles of 128; all tiles of the batch are laid end to end by
+//              their cost, every segment after a lead that stands for the cost
+//              of a piece, and cut into one equal contiguous range per CTA (one
+//              CTA per SM).  A range's share of a segment is a piece; every
+//              piece leaves (m, l) and O in the workspace for the merge.
 //   S^T      = K Q^T    tcgen05.mma M = 128 keys, N = query rows (16 to 64),
 //   O^T     += V^T P^T  tcgen05.mma M = 128 dims (twice), N = query rows,
 //              K = keys.
@@ -77,6 +78,7 @@ constexpr int kKWarp0 = 0, kVWarp0 = 8, kSmWarp0 = 16, kSWarp = 24, kPvWarp = 25
 constexpr int kThreads = 28 * 32;
 constexpr int kSmThreads = 256;
 constexpr uint32_t kTmemCols = 512, kOCol = 0, kSCol = 128, kKCol = 256, kVCol = 384;
+constexpr int kLead = 7, kTileCost = 6;
 constexpr float kLazyLog2 = 8.f;  // the reference maximum is raised past this
 
 struct Params {
@@ -90,21 +92,36 @@ struct Params {
   int q_type, n_qtok, n_kv_heads, n_q_heads, page_size, table_stride, n_blocks;
   int page_shift;  // log2 of page_size, or -1
   int n_seq, n_groups, n_ctas;
-  int prefix_tiles, total_tiles;
+  int weigh;                  // 0: tiles take a place each
+  int prefix_len, total_len;  // places of the prefixes, of all
+  int total_tiles;
   int suffix_row_tiles, suffix_rows;  // row tiles of a suffix segment; rows of its slot
   int suffix_base;                    // first slot row of the suffixes
   float scale_log2;
   int32_t len[kMaxSeqs], start[kMaxSeqs];  // a suffix's keys are start .. len - 1
-  int32_t seq_tile[kMaxSeqs + 1];          // suffix tiles before a sequence
+  int32_t seq_at[kMaxSeqs];                // places of the suffixes before a sequence's
+  int32_t seq_tile[kMaxSeqs];              // tiles before a sequence's suffix
   int32_t group_first[kMaxGroups], group_seqs[kMaxGroups], group_keys[kMaxGroups];
-  int32_t group_tile[kMaxGroups + 1], group_seg[kMaxGroups];  // tiles and segments before a group
+  int32_t group_at[kMaxGroups], group_tile[kMaxGroups], group_seg[kMaxGroups];  // places, tiles, segments before a group
 };
 
 // ------------------------------------------------------------------ the walk
 
 __host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// The CTA whose range holds tile x: CTA i takes tiles i T / G .. (i + 1) T / G - 1.
+// A segment of nt tiles takes lead + nt * cost places, a tile stands at the first
+// of its own.  CTA i has the places i T / G .. (i + 1) T / G - 1 and the tiles
+// that stand there; cta_of is the CTA of place x.
+struct Cost {
+  int lead, tile;
+};
+
+// By the query rows of the unit, in half microseconds: a tile of 16 rows takes
+// 1.5 us, one of 64 2.5; a piece 2 us more than its tiles.
+__host__ __device__ constexpr Cost cost_of(int weigh, int rows) {
+  return weigh ? Cost{kLead, kTileCost + (rows >= kRows ? 2 : rows / 32)} : Cost{0, 1};
+}
+
 __host__ __device__ inline int cta_of(int x, int total, int ctas) {
   return (int)((((long long)x + 1) * ctas - 1) / total);
 }
@@ -114,6 +131,7 @@ struct Pos {
   int head, rt, j;  // KV head, row tile, key tile
   int nt, nrt;     // key tiles of the segment, row tiles of the (unit, head)
   bool pre;
+  int tile;        // number of the tile (set by locate)
 };
 
 __device__ __forceinline__ void pos_sizes(const Params& p, Pos& t) {
@@ -124,26 +142,6 @@ __device__ __forceinline__ void pos_sizes(const Params& p, Pos& t) {
     t.nt = ceil_div(p.len[t.unit] - p.start[t.unit], kKeys);
     t.nrt = p.suffix_row_tiles;
   }
-}
-
-__device__ __forceinline__ Pos locate(const Params& p, int x) {
-  Pos t;
-  t.pre = x < p.prefix_tiles;
-  const int32_t* cum = t.pre ? p.group_tile : p.seq_tile;
-  if (!t.pre) x -= p.prefix_tiles;
-  int lo = 0, hi = (t.pre ? p.n_groups : p.n_seq) - 1;  // the last unit whose first tile is <= x
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cum[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  t.unit = lo;
-  x -= cum[lo];
-  pos_sizes(p, t);
-  const int seg = x / t.nt;
-  t.j = x - seg * t.nt;
-  t.head = seg / t.nrt;
-  t.rt = seg - t.head * t.nrt;
-  return t;
 }
 
 __device__ __forceinline__ void advance(const Params& p, Pos& t) {
@@ -160,6 +158,34 @@ __device__ __forceinline__ void advance(const Params& p, Pos& t) {
   }
   if (!t.pre && t.unit >= p.n_seq) return;  // past the last tile
   pos_sizes(p, t);
+}
+
+// The first tile at place x or after it.
+__device__ __forceinline__ Pos locate(const Params& p, int x) {
+  Pos t;
+  t.pre = x < p.prefix_len;
+  const int32_t* cum = t.pre ? p.group_at : p.seq_at;
+  if (!t.pre) x -= p.prefix_len;
+  int lo = 0, hi = (t.pre ? p.n_groups : p.n_seq) - 1;  // the last unit whose first tile is <= x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cum[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  t.unit = lo;
+  x -= cum[lo];
+  pos_sizes(p, t);
+  const Cost c = cost_of(p.weigh, kGqa * p.n_qtok * (t.pre ? p.group_seqs[t.unit] : 1));
+  const int len = c.lead + t.nt * c.tile;
+  int seg = x / len;
+  t.j = (max(x - seg * len - c.lead, 0) + c.tile - 1) / c.tile;
+  t.tile = (t.pre ? p.group_tile : p.seq_tile)[t.unit] + seg * t.nt + t.j;
+  t.head = seg / t.nrt;
+  t.rt = seg - t.head * t.nrt;
+  if (t.j == t.nt) {  // past the segment's last tile
+    --t.j;
+    advance(p, t);
+  }
+  return t;
 }
 
 __device__ __forceinline__ int pos_seq(const Params& p, const Pos& t) { return t.pre ? p.group_first[t.unit] : t.unit; }
@@ -192,7 +218,7 @@ struct Smem {
   static constexpr int kKStage = 4 * pa_layout::group_bytes<KT>(), kVStage = 4 * pa_layout::group_bytes<VT>();
   static constexpr int kQBytes = kRows * kD * 2, kPBytes = kRows * kKeys * 2;
   static constexpr int kQ = 0, kP = 2 * kQBytes, kRing = kP + kPBytes;
-  static constexpr int kTail = 8 * kRows * 4 + 3 * kRows * 4 + 16 * 32 + 64 + 512;  // red, references, tiles, barriers
+  static constexpr int kTail = 8 * kRows * 4 + 2 * kRows * 4 + 16 * 32 + 64 + 512;  // red, references, tiles, barriers
   // K and V stages in rings of their own, both of an even number of stages: a
   // warp reads every second stage of its ring, and so sees every use of those it
   // reads (a parity wait must never be two phases ahead of its barrier).  Two
@@ -215,13 +241,13 @@ struct Smem {
   static_assert(2 * (kKStage + kVStage) <= kRoom, "a tile of stages does not fit");
   static constexpr int kVRing = kRing + kKStages * kKStage;
   static constexpr int kRed = kVRing + kVStages * kVStage;
-  static constexpr int kRef = kRed + 8 * kRows * 4, kDelta = kRef + kRows * 4, kAlpha = kDelta + kRows * 4;
+  static constexpr int kRef = kRed + 8 * kRows * 4, kAlpha = kRef + kRows * 4;
   static constexpr int kTile = kAlpha + kRows * 4, kLeft = kTile + 16 * 32, kBar = kLeft + 64;
   // K and V raw full / empty [stages], K and V unit full / empty [2], s full / empty [2], q full / empty [2],
-  // p full, pv done, o free, drain [2], sink
-  static constexpr int kNBar = 2 * (kKStages + kVStages) + 8 + 4 + 4 + 6;
+  // p full, pv done, o free [2], drain [2], sink
+  static constexpr int kNBar = 2 * (kKStages + kVStages) + 8 + 4 + 4 + 7;
   static constexpr int kMisc = kBar + 8 * kNBar;  // abort, tmem base, the first tile's place
-  static constexpr int kTotal = kMisc + 16 + 32;
+  static constexpr int kTotal = kMisc + 16 + sizeof(Pos) + 12;
   static constexpr int kLaunch = kTotal + 1024;  // the base is aligned to 1024 inside
   static_assert(kTotal - kBar <= 512 && kLaunch <= 232448, "shared memory");
 };
@@ -240,6 +266,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(a));
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(a));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // 16 lanes x 16 columns in the mma fragment distribution: thread 4g + t gets
@@ -418,7 +456,7 @@ __device__ __forceinline__ void dequant_v(uint32_t stage, int b, int n_keys, uin
 // sixteen tiles deep (the roles are never that far apart: the copy stages and
 // operand units between them hold fewer tiles).
 struct alignas(16) Tile {
-  uint32_t info;  // query rows of the segment | first tile of a piece << 8 | last << 9 | suffix << 10
+  uint32_t info;  // query rows of the segment | first tile of a piece << 8 | last << 9 | suffix << 10 | odd piece << 11
   int open;       // keys of the tile that every row sees (<= 0: none; >= 128: no edge here); suffix row r sees
                   // (row0 + r) / 6 more
   int row0;       // first query row of the row tile
@@ -428,6 +466,11 @@ struct alignas(16) Tile {
   int pad[2];
 };
 constexpr int kTiles = 16;
+
+// Where a piece's O^T lies in its 64 columns: pieces of up to 32 rows take the
+// halves in turn, so that one is written out while the next accumulates.
+__device__ __forceinline__ bool is_wide(uint32_t info) { return (info & 0xff) > 32; }
+__device__ __forceinline__ uint32_t o_half(uint32_t info) { return !is_wide(info) && ((info >> 11) & 1) ? 32u : 0u; }
 
 // ------------------------------------------------------------------ query rows
 
@@ -559,17 +602,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t
   return warp_wait_slow<kSleep>(bar, parity, err, abort);
 }
 
-// The raw K (kIsV false) or V row groups of the CTA's tiles into a ring of NS
-// stages at ring, two stages per tile; returns the number of stages issued.
+// The raw K or V row groups of the CTA's tiles into a ring of ns stages at ring,
+// two stages per tile; returns the number of stages issued.  gb, rb: bytes of a
+// group and of a row.  One function for both, with what differs as arguments: the
+// roles' code competes for the instruction caches.
 // Lane g (0..7) looks after row group g of the tile, all in one pass: its
 // stage's wait, its copy; its table entry is read a tile ahead.  One warp in the
 // company of twenty others executes an instruction every ten cycles or so, so
 // what the tiles of a segment share is computed once per segment.
-template <int T, bool kIsV, int NS>
-__device__ __forceinline__ int copy_role(const Params& p, Pos pos, int n, uint32_t ring, uint32_t full, uint32_t empty,
-                                         Tile* tiles, int* lefts, volatile int* abort, int lane) {
-  constexpr int GB = pa_layout::group_bytes<T>(), RB = Fmt<T>::kRow;
-  const uint8_t* pool = kIsV ? p.v_pool : p.k_pool;
+__device__ __forceinline__ int copy_role(const Params& p, Pos pos, int n, bool is_v, int gb, int rb, int ns, uint32_t ring,
+                                         uint32_t full, uint32_t empty, Tile* tiles, int* lefts, volatile int* abort,
+                                         int lane) {
+  const uint8_t* pool = is_v ? p.v_pool : p.k_pool;
   const long long block_rows = (long long)p.n_kv_heads * p.page_size;
   const int half = (lane >> 2) & 1, lane_key = lane < 8 ? kGroup * lane : kKeys;  // lanes past 7 have no group
   const int page_shift = p.page_shift;
@@ -578,76 +622,76 @@ __device__ __forceinline__ int copy_role(const Params& p, Pos pos, int n, uint32
   int end = 0, key0 = 0, head_row = 0;
   uint32_t info = 0;
   int4 tile0 = make_int4(0, 0, 0, 0), tile1 = tile0;
-  auto enter = [&]() {
-    row = p.table + (long long)pos_seq(p, pos) * p.table_stride;
-    end = pos_end(p, pos);
-    key0 = pos_key0(p, pos);
-    head_row = pos.head * p.page_size;
-    if (!kIsV) {
-      info = (uint32_t)pos_rows(p, pos) | (pos.pre ? 0u : 1u << 10) | 1u << 8;
-      // prefix: the live keys; suffix: the new tokens' keys open one by one
-      tile0 = make_int4(0, pos.pre ? end : end - p.n_qtok + 1, pos.rt * kRows, pos_slot_row(p, pos, (int)blockIdx.x));
-      tile1 = make_int4(pos_seq(p, pos) * p.n_qtok, pos.head, 0, 0);
-    }
-  };
+  uint32_t odd = 1;
   int entry = -1, off = 0;
-  auto look = [&]() {
-    entry = -1;
-    const int k = key0 + lane_key;
-    if (lane_key < kKeys && k < end) {
-      const int page = page_shift >= 0 ? k >> page_shift : k / p.page_size;
-      off = k - page * p.page_size;
-      entry = __ldg(row + page);
-    }
-  };
-  enter();
-  look();
   int pair = 0;         // stages 2 pair, 2 pair + 1
   uint32_t parity = 1;  // of the wait for the stages' previous use; flips when the ring wraps
-  for (int j = 0; j < n; ++j) {
-    const int tb = entry;
-    const bool mine = lane_key < kKeys && key0 + lane_key < end, ok = mine && (uint32_t)tb < (uint32_t)p.n_blocks;
-    const uint8_t* src = pool + (tb * block_rows + (head_row + off)) * RB;
-    const bool last = j + 1 == n || pos.j + 1 == pos.nt;
-    if (lane == 0) {
-      if (kIsV) {
-        lefts[j & (kTiles - 1)] = end - key0;
-      } else {
-        int4* t = reinterpret_cast<int4*>(tiles + (j & (kTiles - 1)));
-        t[0] = make_int4((int)(info | (last ? 1u << 9 : 0u)), tile0.y - key0, tile0.z, tile0.w);
-        t[1] = tile1;
+  bool last = true;
+  for (int j = -1; j < n; ++j) {  // issues tile j, looks tile j + 1 up
+    const int left = end - key0, tb = entry;
+    const bool mine = lane_key < min(kKeys, left), ok = mine && (uint32_t)tb < (uint32_t)p.n_blocks;
+    const uint8_t* src = pool + (tb * block_rows + (head_row + off)) * rb;
+    if (j >= 0) {
+      last = j + 1 == n || pos.j + 1 == pos.nt;
+      if (lane == 0) {
+        if (is_v) {
+          lefts[j & (kTiles - 1)] = left;
+        } else {
+          int4* t = reinterpret_cast<int4*>(tiles + (j & (kTiles - 1)));
+          t[0] = make_int4((int)(info | (last ? 1u << 9 : 0u)), tile0.y - key0, tile0.z, tile0.w);
+          t[1] = tile1;
+        }
       }
-    }
-    info &= ~(1u << 8);
-    const uint32_t good = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, mine && !ok);
-    if (j + 1 < n) {  // the next tile's table entries
+      info &= ~(1u << 8);
       if (last) {
-        advance(p, pos);
-        enter();
+        if (j + 1 < n) advance(p, pos);
       } else {
         ++pos.j;
         key0 += kKeys;
       }
-      look();
     }
-    const uint32_t stage = 2 * pair + half, fb = full + 8 * stage, dst = ring + stage * (4 * GB) + (lane & 3) * GB;
-    if (j >= NS / 2 && !warp_wait<true>(empty + 8 * stage, parity, p.err, abort)) return 2 * j;
+    if (j + 1 < n) {
+      if (last) {
+        odd ^= 1;
+        row = p.table + (long long)pos_seq(p, pos) * p.table_stride;
+        end = pos_end(p, pos);
+        key0 = pos_key0(p, pos);
+        head_row = pos.head * p.page_size;
+        info = (uint32_t)pos_rows(p, pos) | (pos.pre ? 0u : 1u << 10) | 1u << 8 | odd << 11;
+        // prefix: the live keys; suffix: the new tokens' keys open one by one
+        tile0 = make_int4(0, pos.pre ? end : end - p.n_qtok + 1, pos.rt * kRows, pos_slot_row(p, pos, (int)blockIdx.x));
+        tile1 = make_int4(pos_seq(p, pos) * p.n_qtok, pos.head, 0, 0);
+      }
+      const int k = key0 + lane_key;
+      entry = -1;
+      if (lane_key < kKeys && k < end) {
+        const int page = page_shift >= 0 ? k >> page_shift : k / p.page_size;
+        off = k - page * p.page_size;
+        entry = __ldg(row + page);
+      }
+    }
+    if (j < 0) continue;
+    const uint32_t good = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, mine && !ok);
+    const uint32_t stage = 2 * pair + half, fb = full + 8 * stage, dst = ring + stage * (4 * gb) + (lane & 3) * gb;
+    if (j >= ns / 2 && !warp_wait<true>(empty + 8 * stage, parity, p.err, abort)) return 2 * j;
     if (bad) {  // rows of an entry outside the pool read as zeros
       if (lane == 0) record_error(p.err, PA_ERR_BOUNDS);
+#pragma unroll 1
       for (int g = 0; g < 8; ++g) {
         if (!((bad >> g) & 1)) continue;
-        for (int i = lane; i < GB / 16; i += 32) sts128_zero(ring + (2 * pair + (g >> 2)) * (4 * GB) + (g & 3) * GB + 16 * i);
+#pragma unroll 1
+        for (int i = lane; i < gb / 16; i += 32) sts128_zero(ring + (2 * pair + (g >> 2)) * (4 * gb) + (g & 3) * gb + 16 * i);
       }
       fence_proxy_async_smem();
       __syncwarp();
     }
-    if (lane == 0 || lane == 4) mbar_arrive_expect_tx(fb, __popc(good & (0xfu << lane)) * GB);
+    if (lane == 0 || lane == 4) mbar_arrive_expect_tx(fb, __popc(good & (0xfu << lane)) * gb);
     __syncwarp();
     if (ok)
       asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                   "l"(src), "r"(GB), "r"(fb)
+                   "l"(src), "r"(gb), "r"(fb)
                    : "memory");
-    if (++pair == NS / 2) {
+    if (++pair == ns / 2) {
       pair = 0;
       parity ^= 1;
     }
@@ -706,20 +750,19 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
   //   s_full / s_empty [j & 1]          S^T(j) in tensor memory / in the softmax registers
   //   p_full / pv_done                  P^T(j) written / O^T holds tile j, P^T free
   //   q_full / q_empty [i & 1]          query rows of piece i staged / no longer needed
-  //   o_free                            piece i's O^T has been read
+  //   o_free [i & 1]                    piece i's O^T has been read
   // A role whose wait expires stops: it arrives nowhere any more.
   const uint32_t kraw_full = base + SM::kBar, kraw_empty = kraw_full + 8 * NK, vraw_full = kraw_empty + 8 * NK,
                  vraw_empty = vraw_full + 8 * NV, ku_full = vraw_empty + 8 * NV, ku_empty = ku_full + 16,
                  vu_full = ku_empty + 16, vu_empty = vu_full + 16, s_full = vu_empty + 16, s_empty = s_full + 16,
                  q_full = s_empty + 16, q_empty = q_full + 16, p_full = q_empty + 16, pv_done = p_full + 8,
-                 o_free = pv_done + 8, drain = o_free + 8, sink = drain + 16;
+                 o_free = pv_done + 8, drain = o_free + 16, sink = drain + 16;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + SM::kMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc + 8);
   Pos* start = reinterpret_cast<Pos*>(smem + SM::kMisc + 16);
+  int* tiles_at = reinterpret_cast<int*>(smem + SM::kMisc + 16 + sizeof(Pos));  // the CTA's first tile, the next CTA's
   Tile* tiles = reinterpret_cast<Tile*>(smem + SM::kTile);
   int* lefts = reinterpret_cast<int*>(smem + SM::kLeft);
-  const int first = (int)((long long)blockIdx.x * p.total_tiles / p.n_ctas),
-            n = (int)((long long)(blockIdx.x + 1) * p.total_tiles / p.n_ctas) - first;  // at least 1
   if (tid == 0) {
     *abort = 0;
     for (int i = 0; i < NK; ++i) {
@@ -739,15 +782,26 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       mbar_init(s_empty + 8 * i, 8);
       mbar_init(q_full + 8 * i, 8);
       mbar_init(q_empty + 8 * i, 1);
+      mbar_init(o_free + 8 * i, 8);
       mbar_init(drain + 8 * i, 1);
     }
     mbar_init(p_full, 8);
     mbar_init(pv_done, 1);
-    mbar_init(o_free, 8);
     mbar_init(sink, 1);
     fence_mbar_init();
   }
-  if (tid == 32) *start = locate(p, first);
+  if (w == 1 || w == 2) {
+    const int x = (int)((long long)(blockIdx.x + w - 1) * p.total_len / p.n_ctas);
+    if (x < p.total_len) {
+      const Pos t = locate(p, x);
+      if (lane == 0) {
+        if (w == 1) *start = t;
+        tiles_at[w - 1] = t.tile;
+      }
+    } else if (lane == 0) {
+      tiles_at[1] = p.total_tiles;
+    }
+  }
   if (w == 0) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
@@ -755,6 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  const int n = tiles_at[1] - tiles_at[0];  // at least 1
   // nothing that another kernel wrote is read before this
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0) asm volatile("griddepcontrol.launch_dependents;");
@@ -763,13 +818,17 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
   // to prove uniform.
   const bool whole = *tmem_slot == 0;
   if (!whole && tid == 0) record_error(p.err, PA_ERR_CUDA);
-  int issued_k = 0, issued_v = 0;  // copy stages (the copy warps')
+  // the copy warps': K's or V's
+  const bool is_v = w == kCopyVWarp;
+  const int ns = is_v ? NV : NK;
+  const uint32_t raw_full = is_v ? vraw_full : kraw_full;
+  int issued = 0;
 
   if (!whole) {
-  } else if (w == kCopyKWarp) {
-    issued_k = copy_role<KT, false, NK>(p, *start, n, base + SM::kRing, kraw_full, kraw_empty, tiles, lefts, abort, lane);
-  } else if (w == kCopyVWarp) {
-    issued_v = copy_role<VT, true, NV>(p, *start, n, base + SM::kVRing, vraw_full, vraw_empty, tiles, lefts, abort, lane);
+  } else if (w == kCopyKWarp || is_v) {
+    issued = copy_role(p, *start, n, is_v, is_v ? SM::kVStage / 4 : SM::kKStage / 4, is_v ? Fmt<VT>::kRow : Fmt<KT>::kRow, ns,
+                       base + (is_v ? SM::kVRing : SM::kRing), raw_full, is_v ? vraw_empty : kraw_empty, tiles, lefts, abort,
+                       lane);
   } else if (w < kVWarp0) {
     // ---- K: thread = key (position 32 * quarter + lane), dims 128 kd .. + 127
     const int kd = w >> 2, quarter = w & 3, at = 32 * quarter + lane;
@@ -853,12 +912,13 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
         tc_fence_after();
         const uint64_t qd = qdesc + (uint64_t)(((piece - 1) & 1) * (SM::kQBytes >> 4));
         const uint32_t idesc = idesc_of(info), d = kSCol + 64 * b;
-        mma8<false>(d, kKCol, qd, idesc, 0u, leader);
-        commit(ku_empty);
-        wait(ku_full + 8, b);
-        tc_fence_after();
-        mma8<false>(d, kKCol + 64, qd + 128, idesc, 1u, leader);
-        commit(ku_empty + 8);
+#pragma unroll 1
+        for (uint32_t h = 0; h < 2; ++h) {
+          if (h) wait(ku_full + 8, b);
+          tc_fence_after();
+          mma8<false>(d, kKCol + 64 * h, qd + 128 * h, idesc, h, leader);
+          commit(ku_empty + 8 * h);
+        }
         commit(s_full + 8 * b);
         if ((info >> 9) & 1) commit(q_empty + 8 * ((piece - 1) & 1));
       }
@@ -868,22 +928,24 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       for (uint32_t i = piece < 2 ? 0 : piece - 2; i < piece; ++i) wait(q_empty + 8 * (i & 1), (i >> 1) & 1);
     } else {
       const uint64_t pdesc = smem_desc(base + SM::kP, 128, 2048);
+      uint32_t wide = 0;  // the piece before
       for (uint32_t j = 0; j < (uint32_t)n; ++j) {
         const uint32_t b = j & 1;
         wait(p_full, b);
         const uint32_t info = info_of(j), first_tile = (info >> 8) & 1, idesc = idesc_of(info);
         if (first_tile) {
-          if (piece > 0) wait(o_free, (piece - 1) & 1);
+          if (piece > 1) wait(o_free + 8 * (piece & 1), ((piece >> 1) - 1) & 1);
+          if (piece > 0 && (wide | (uint32_t)is_wide(info))) wait(o_free + 8 * ((piece - 1) & 1), ((piece - 1) >> 1) & 1);
+          wide = is_wide(info);
           ++piece;
         }
-        wait(vu_full, b);
-        tc_fence_after();
-        mma8<true>(kOCol, kVCol, pdesc, idesc, first_tile ^ 1u, leader);
-        commit(vu_empty);
-        wait(vu_full + 8, b);
-        tc_fence_after();
-        mma8<true>(kOCol, kVCol + 64, pdesc + 64, idesc, 1u, leader);
-        commit(vu_empty + 8);
+#pragma unroll 1
+        for (uint32_t h = 0; h < 2; ++h) {
+          wait(vu_full + 8 * h, b);
+          tc_fence_after();
+          mma8<true>(kOCol + o_half(info), kVCol + 64 * h, pdesc + 64 * h, idesc, h | (first_tile ^ 1u), leader);
+          commit(vu_empty + 8 * h);
+        }
         commit(pv_done);
       }
       for (int i = 0; i < 2; ++i) wait(vu_empty + 8 * i, (n - 1) & 1);
@@ -901,195 +963,213 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     const int sw = w - kSmWarp0, hh = sw >> 2, quarter = w & 3, g = lane >> 2, t2 = 2 * (lane & 3), st = tid - 32 * kSmWarp0;
     float* red = reinterpret_cast<float*>(smem + SM::kRed);
     float* nref = reinterpret_cast<float*>(smem + SM::kRef);      // minus the reference maximum
-    float* ndelta = reinterpret_cast<float*>(smem + SM::kDelta);  // minus what it was raised by
     float* alpha = reinterpret_cast<float*>(smem + SM::kAlpha);
     const uint32_t s_addr = kSCol + ((uint32_t)(32 * quarter + 16 * hh) << 16);
     const uint32_t o_addr = kOCol + 64 * hh + ((uint32_t)(32 * quarter) << 16);
     const int tile_key = 16 * (2 * quarter + hh);
     const uint32_t p_addr = base + SM::kP + canon(8 * (lane >> 4) + (lane & 7), 4 * quarter + 2 * hh + ((lane >> 3) & 1), kKeys / 8);
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
-    uint64_t l[4][2];  // sums of weights over this thread's keys: rows (16c + 8e + 2t, + 1)
+    uint64_t l[4][2] = {};  // sums of weights over this thread's keys: rows (16c + 8e + 2t, + 1)
     bool live = true;  // a warp whose wait expired keeps to the group's barriers but arrives nowhere
-    // One tile, its query rows NC times 16.
-    auto tile = [&](auto width, const int j, const uint32_t info) {
-      constexpr int NC = decltype(width)::value;
+    // Logits of 16 rows in log2 units, less their references (none: zero ones).
+    // Thread: [8 columns e, key g or g + 8, column 2t or 2t + 1] at 4e + 2k + i.  Row r
+    // of the tile's edge sees key k when r >= 6 (k - open + 1) (suffix) or k < open.
+    auto logits = [&](uint32_t (&x)[8], const int j, const int c, const bool refs, const bool edge, const int la, const int lb) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint64_t m = refs ? *reinterpret_cast<const uint64_t*>(nref + 16 * c + 8 * e + t2) : 0ull;
+        put2(x + 4 * e, fma2(get2(x + 4 * e), scale2, m));
+        put2(x + 4 * e + 2, fma2(get2(x + 4 * e + 2), scale2, m));
+      }
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (16 * c + 8 * (i >> 2) + (i & 1) < ((i & 2) ? lb : la)) x[i] = 0xff800000u;  // -inf
+      }
+    };
+    auto tile = [&](const int j, const uint32_t info) {
+      const int nc = ((info & 0xff) + 15) >> 4;  // query rows in sixteens
       const Tile& tl = tiles[j & (kTiles - 1)];
-      const int rows = info & 0xff, open = tl.open;
-      const bool first_tile = (info >> 8) & 1, last_tile = (info >> 9) & 1;
-      uint32_t x[NC][8];  // [16 columns][(8 columns e, key g or g + 8, column 2t or 2t + 1): 4e + 2k + i], floats
-#pragma unroll
-      for (int c = 0; c < NC; ++c) tmem_ld_frag2(s_addr + 64 * (j & 1) + 16 * c, x[c]);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (live && lane == 0) mbar_arrive(s_empty + 8 * (j & 1));
-      __syncwarp();
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        loaded(x[c]);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint64_t m = first_tile ? 0ull : *reinterpret_cast<const uint64_t*>(nref + 16 * c + 8 * e + t2);
-          put2(x[c] + 4 * e, fma2(get2(x[c] + 4 * e), scale2, m));
-          put2(x[c] + 4 * e + 2, fma2(get2(x[c] + 4 * e + 2), scale2, m));
+      const bool first_tile = (info >> 8) & 1;
+      const uint32_t s_at = s_addr + 64 * (j & 1);
+      const bool edge = tl.open < kKeys;
+      int la = 0, lb = 0;
+      if (edge) {
+        const int ka = tile_key + key16(g) - tl.open, kb = tile_key + key16(g + 8) - tl.open;
+        if ((info >> 10) & 1) {
+          la = kGqa * (ka + 1) - tl.row0 - t2;
+          lb = kGqa * (kb + 1) - tl.row0 - t2;
+        } else {
+          la = ka < 0 ? -kRows : kRows;
+          lb = kb < 0 ? -kRows : kRows;
         }
       }
-      if (open < kKeys) {  // the edge: mask
-        const int ka = tile_key + key16(g), kb = tile_key + key16(g + 8), row0 = tl.row0;
-        const bool causal = (info >> 10) & 1;
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = row0 + 16 * c + 8 * (i >> 2) + t2 + (i & 1);
-            if (((i & 2) ? kb : ka) >= open + (causal ? row / kGqa : 0)) x[c][i] = 0xff800000u;  // -inf
-          }
-      }
-      float top = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])));
-      // The references are raised when a logit passes them by 2^8, and at a piece's
-      // first tile.  The barrier also says that the others are done with the shared
-      // arrays.
-      if (bar_or(1, kSmThreads, first_tile || top > kLazyLog2)) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float u = fmaxf(__uint_as_float(x[c][4 * e]), __uint_as_float(x[c][4 * e + 2])),
-                  v = fmaxf(__uint_as_float(x[c][4 * e + 1]), __uint_as_float(x[c][4 * e + 3]));
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-              u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
-              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-            }
-            if (g == 0) *reinterpret_cast<float2*>(red + sw * kRows + 16 * c + 8 * e + t2) = make_float2(u, v);
-          }
-        __syncwarp();
-        named_bar_sync(1, kSmThreads);
-        if (st < 16 * NC) {
-          float v = red[st];
-#pragma unroll
-          for (int i = 1; i < 8; ++i) v = fmaxf(v, red[i * kRows + st]);
-          // a row that sees no key yet keeps a reference of 0; it will see none later in the piece either
-          const float d = first_tile ? (v == -INFINITY ? 0.f : v) : fmaxf(v, 0.f);
-          nref[st] = first_tile ? -d : nref[st] - d;
-          ndelta[st] = -d;
-          alpha[st] = ex2(-d);
-        }
-        __syncwarp();
-        named_bar_sync(1, kSmThreads);
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint64_t d = *reinterpret_cast<const uint64_t*>(ndelta + 16 * c + 8 * e + t2);
-            put2(x[c] + 4 * e, add2(get2(x[c] + 4 * e), d));
-            put2(x[c] + 4 * e + 2, add2(get2(x[c] + 4 * e + 2), d));
-            l[c][e] = first_tile ? 0ull : mul2(l[c][e], *reinterpret_cast<const uint64_t*>(alpha + 16 * c + 8 * e + t2));
-          }
-        if (!first_tile) {  // O^T holds the tiles before: dims of this warp, every row
-          live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);
-          tc_fence_after();
+      // The references are set at a piece's first tile and raised when a logit passes
+      // them by 2^8; then the tile's weights are computed again.
+      bool raise = first_tile;
+      uint64_t ls[4][2];
+      for (;;) {
+        if (raise) {
+          named_bar_sync(1, kSmThreads);  // the others are done with the shared arrays
 #pragma unroll 1
-          for (int c = 0; c < NC; ++c) {
-            uint32_t o[16];
-            tmem_ld16(o_addr + 16 * c, o);
+          for (int c = 0; c < nc; ++c) {
+            uint32_t x[8];
+            tmem_ld_frag2(s_at + 16 * c, x);
             tmem_ld_wait();
-            loaded(o);
+            loaded(x);
+            logits(x, j, c, !first_tile, edge, la, lb);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[16 * c + i]);
-            tmem_st16(o_addr + 16 * c, o);
+            for (int e = 0; e < 2; ++e) {
+              float u = fmaxf(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 2])),
+                    v = fmaxf(__uint_as_float(x[4 * e + 1]), __uint_as_float(x[4 * e + 3]));
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) {
+                u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+              }
+              if (g == 0) *reinterpret_cast<float2*>(red + sw * kRows + 16 * c + 8 * e + t2) = make_float2(u, v);
+            }
           }
-          tmem_st_wait();
-          tc_fence_before();
+          __syncwarp();
+          named_bar_sync(1, kSmThreads);
+          if (st < 16 * nc) {
+            float v = red[st];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) v = fmaxf(v, red[i * kRows + st]);
+            // a row that sees no key yet keeps a reference of 0; it will see none later in the piece either
+            const float d = first_tile ? (v == -INFINITY ? 0.f : v) : fmaxf(v, 0.f);
+            nref[st] = first_tile ? -d : nref[st] - d;
+            alpha[st] = ex2(-d);
+          }
+          __syncwarp();
+          named_bar_sync(1, kSmThreads);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              l[c][e] = first_tile ? 0ull : mul2(l[c][e], *reinterpret_cast<const uint64_t*>(alpha + 16 * c + 8 * e + t2));
+          if (!first_tile) {  // O^T holds the tiles before: dims of this warp, every row
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 2 * nc; ++c) {
+              uint32_t o[8];
+              tmem_ld8(o_addr + o_half(info) + 8 * c, o);
+              tmem_ld_wait();
+              loaded(o);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[8 * c + i]);
+              tmem_st8(o_addr + o_half(info) + 8 * c, o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
         }
-      }
-      uint32_t h[NC][4];
+        float top = -INFINITY;
+        uint32_t xs[2][8];
+        tmem_ld_frag2(s_at, xs[0]);
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
+        for (int c = 0; c < 4; ++c) {
+          ls[c][0] = ls[c][1] = 0ull;
+          if (c >= nc) continue;
+          uint32_t (&x)[8] = xs[c & 1];
+          tmem_ld_wait();
+          loaded(x);
+          if (c + 1 < 4 && c + 1 < nc) tmem_ld_frag2(s_at + 16 * (c + 1), xs[(c + 1) & 1]);
+          logits(x, j, c, true, edge, la, lb);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float a0 = ex2(__uint_as_float(x[c][4 * e])), a1 = ex2(__uint_as_float(x[c][4 * e + 1])),
-                      b0 = ex2(__uint_as_float(x[c][4 * e + 2])), b1 = ex2(__uint_as_float(x[c][4 * e + 3]));
-          h[c][2 * e] = pack_half2(a0, a1);
-          h[c][2 * e + 1] = pack_half2(b0, b1);
-          l[c][e] = add2(l[c][e], add2(pack2(a0, a1), pack2(b0, b1)));
+          for (int i = 0; i < 8; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float a0 = ex2(__uint_as_float(x[4 * e])), a1 = ex2(__uint_as_float(x[4 * e + 1])),
+                        b0 = ex2(__uint_as_float(x[4 * e + 2])), b1 = ex2(__uint_as_float(x[4 * e + 3]));
+            h[2 * e] = pack_half2(a0, a1);
+            h[2 * e + 1] = pack_half2(b0, b1);
+            ls[c][e] = add2(pack2(a0, a1), pack2(b0, b1));
+          }
+          if (c == 0 && j > 0) live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);  // P^T(j - 1) has been read
+          stsm_x4_trans(p_addr + c * (16 * kKeys * 2), h[0], h[1], h[2], h[3]);
         }
-      if (j > 0) live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);  // P^T(j - 1) has been read
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        stsm_x4_trans(p_addr + c * (16 * kKeys * 2), h[c][0], h[c][1], h[c][2], h[c][3]);
+        if (raise) break;
+        raise = bar_or(1, kSmThreads, top > kLazyLog2);
+        if (!raise) break;
       }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l[c][e] = add2(l[c][e], ls[c][e]);
+      tc_fence_before();
       fence_proxy_async_smem();
       __syncwarp();
-      if (live && lane == 0) mbar_arrive(p_full);
+      if (live && lane == 0) {
+        mbar_arrive(p_full);
+        mbar_arrive(s_empty + 8 * (j & 1));
+      }
       __syncwarp();
-      if (last_tile) {
-        // ---- the piece: sums of weights over the keys, then O^T
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float2 v = unpack2(l[c][e]);
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-              v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-              v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-            }
-            if (g == 0) *reinterpret_cast<float2*>(red + sw * kRows + 16 * c + 8 * e + t2) = v;
-          }
-        __syncwarp();
-        named_bar_sync(1, kSmThreads);
-        const long long slot = tl.slot_row;
-        if (st < rows) {
-          float v = red[st];
-#pragma unroll
-          for (int i = 1; i < 8; ++i) v += red[i * kRows + st];
-          p.part_ml[slot + st] = make_float2(-nref[st], v);
-        }
-        live = live && warp_wait(pv_done, j & 1, p.err, abort);
+    };
+    for (int j = 0; j <= n; ++j) {
+      if (j < n) {
+        live = live && warp_wait(s_full + 8 * (j & 1), (j >> 1) & 1, p.err, abort);
         tc_fence_after();
-        float* dst = p.part_o + slot * kD + 128 * hh + 32 * quarter + v_dim<VT>(lane);
+        const uint32_t info = tiles[j & (kTiles - 1)].info;
+        tile(j, info);
+      } else {
+        live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);
+      }
+      // ---- a piece's O^T, once the weights of the tile after it are on their way
+      const Tile& t = tiles[(j - 1) & (kTiles - 1)];
+      const uint32_t info = j > 0 ? t.info : 0u;
+      if ((info >> 9) & 1) {
+        const int rows = info & 0xff;
+        const uint32_t from = o_addr + o_half(info);
+        float* dst = p.part_o + (long long)t.slot_row * kD + 128 * hh + 32 * quarter + v_dim<VT>(lane);
+        tc_fence_after();
 #pragma unroll 1
-        for (int c = 0; c < NC; ++c) {
+        for (int r = 0; r < rows; r += 16) {
           uint32_t o[16];
-          tmem_ld16(o_addr + 16 * c, o);
+          tmem_ld16(from + r, o);
           tmem_ld_wait();
           loaded(o);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            if (16 * c + i < rows) dst[(16 * c + i) * kD] = __uint_as_float(o[i]);
+            if (r + i < rows) dst[(r + i) * kD] = __uint_as_float(o[i]);
         }
         tc_fence_before();
         __syncwarp();
-        if (live && lane == 0) mbar_arrive(o_free);
+        if (live && lane == 0) mbar_arrive(o_free + 8 * ((info >> 11) & 1));
         __syncwarp();
       }
-    };
-    for (int j = 0; j < n; ++j) {
-      live = live && warp_wait(s_full + 8 * (j & 1), (j >> 1) & 1, p.err, abort);
-      tc_fence_after();
-      const uint32_t info = tiles[j & (kTiles - 1)].info;
-      const int nc = ((info & 0xff) + 15) >> 4;
-      if (nc == 1) tile(std::integral_constant<int, 1>(), j, info);
-      else if (nc == 2) tile(std::integral_constant<int, 2>(), j, info);
-      else if (nc == 3) tile(std::integral_constant<int, 3>(), j, info);
-      else tile(std::integral_constant<int, 4>(), j, info);
+      // ---- a piece's sums of weights, after its last tile
+      if (j == n) break;
+      const Tile& tl = tiles[j & (kTiles - 1)];
+      if ((tl.info >> 9) & 1) {
+        named_bar_sync(1, kSmThreads);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint64_t v = l[c][e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) v = add2(v, __shfl_xor_sync(0xffffffffu, v, o));
+            if (g == 0) *reinterpret_cast<uint64_t*>(red + sw * kRows + 16 * c + 8 * e + t2) = v;
+          }
+        __syncwarp();
+        named_bar_sync(1, kSmThreads);
+        if (st < (int)(tl.info & 0xff)) {
+          float v = red[st];
+#pragma unroll
+          for (int i = 1; i < 8; ++i) v += red[i * kRows + st];
+          p.part_ml[(long long)tl.slot_row + st] = make_float2(-nref[st], v);
+        }
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
   // after an expired wait, copies that nobody waited for must still land
-  if (w == kCopyKWarp && *abort) {
-    for (int i = max(0, issued_k - NK); i < issued_k; ++i)
-      mbar_wait(kraw_full + 8 * (i % NK), (uint32_t)((i / NK) & 1), p.err, abort, false, kWaitTimeoutNs / 8);
-  }
-  if (w == kCopyVWarp && *abort) {
-    for (int i = max(0, issued_v - NV); i < issued_v; ++i)
-      mbar_wait(vraw_full + 8 * (i % NV), (uint32_t)((i / NV) & 1), p.err, abort, false, kWaitTimeoutNs / 8);
+  if ((w == kCopyKWarp || is_v) && *abort) {
+    for (int i = max(0, issued - ns); i < issued; ++i)
+      mbar_wait(raw_full + 8 * (i % ns), (uint32_t)((i / ns) & 1), p.err, abort, false, kWaitTimeoutNs / 8);
   }
   if (w == 0) {
     tc_fence_after();
