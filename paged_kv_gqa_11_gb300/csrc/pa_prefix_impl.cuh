@@ -217,8 +217,8 @@ template <int KT, int VT>
 struct Smem {
   static constexpr int kKStage = 4 * pa_layout::group_bytes<KT>(), kVStage = 4 * pa_layout::group_bytes<VT>();
   static constexpr int kQBytes = kRows * kD * 2, kPBytes = kRows * kKeys * 2;
-  static constexpr int kQ = 0, kP = 2 * kQBytes, kRing = kP + kPBytes;
-  static constexpr int kTail = 8 * kRows * 4 + 2 * kRows * 4 + 16 * 32 + 64 + 512;  // red, references, tiles, barriers
+  static constexpr int kQ = 0, kP = kQBytes, kRing = kP + 2 * kPBytes;
+  static constexpr int kTail = 8 * kRows * 4 + 2 * kRows * 4 + 17 * 32 + 64 + 640;  // red, references, tiles, barriers
   // K and V stages in rings of their own, both of an even number of stages: a
   // warp reads every second stage of its ring, and so sees every use of those it
   // reads (a parity wait must never be two phases ahead of its barrier).  Two
@@ -242,14 +242,14 @@ struct Smem {
   static constexpr int kVRing = kRing + kKStages * kKStage;
   static constexpr int kRed = kVRing + kVStages * kVStage;
   static constexpr int kRef = kRed + 8 * kRows * 4, kAlpha = kRef + kRows * 4;
-  static constexpr int kTile = kAlpha + kRows * 4, kLeft = kTile + 16 * 32, kBar = kLeft + 64;
+  static constexpr int kTile = kAlpha + kRows * 4, kOpening = kTile + 16 * 32, kLeft = kOpening + 32, kBar = kLeft + 64;
   // K and V raw full / empty [stages], K and V unit full / empty [2], s full / empty [2], q full / empty [2],
-  // p full, pv done, o free [2], drain [2], sink
-  static constexpr int kNBar = 2 * (kKStages + kVStages) + 8 + 4 + 4 + 7;
+  // p full, pv done, o free [2] each, drain [2], sink
+  static constexpr int kNBar = 2 * (kKStages + kVStages) + 8 + 4 + 4 + 9;
   static constexpr int kMisc = kBar + 8 * kNBar;  // abort, tmem base, the first tile's place
   static constexpr int kTotal = kMisc + 16 + sizeof(Pos) + 12;
   static constexpr int kLaunch = kTotal + 1024;  // the base is aligned to 1024 inside
-  static_assert(kTotal - kBar <= 512 && kLaunch <= 232448, "shared memory");
+  static_assert(kTotal - kBar <= 640 && kLaunch <= 232448, "shared memory");
 };
 
 // Canonical K-major byte offset (core matrices of 8 rows x 16 bytes) of row r,
@@ -467,10 +467,12 @@ struct alignas(16) Tile {
 };
 constexpr int kTiles = 16;
 
-// Where a piece's O^T lies in its 64 columns: pieces of up to 32 rows take the
-// halves in turn, so that one is written out while the next accumulates.
+// Where a piece's rows lie among the 64 of Q and the 64 columns of O^T: pieces
+// of up to 32 rows take the halves in turn, so that one is staged while the other
+// is used, and written out while the next accumulates.  A piece waits for the one
+// before the last, and for the last if either is wider.
 __device__ __forceinline__ bool is_wide(uint32_t info) { return (info & 0xff) > 32; }
-__device__ __forceinline__ uint32_t o_half(uint32_t info) { return !is_wide(info) && ((info >> 11) & 1) ? 32u : 0u; }
+__device__ __forceinline__ uint32_t row0_of(uint32_t info) { return !is_wide(info) && ((info >> 11) & 1) ? 32u : 0u; }
 
 // ------------------------------------------------------------------ query rows
 
@@ -562,24 +564,12 @@ __device__ __forceinline__ bool bar_or(uint32_t id, uint32_t count, bool x) {
   return r != 0;
 }
 
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Out-of-line part of warp_wait: false once the wait gave up (after
 // kWaitTimeoutNs, which is recorded) or another role had to.
-template <bool kSleep>
-__device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort) {
+static __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort) {
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
-    if (kSleep) __nanosleep(100);
-    if (__all_sync(0xffffffffu, kSleep ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity))) return true;
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     if ((i & 63u) == 0) {  // the clock is slow to read: not before the wait is long
       if (i == 64) t0 = globaltimer();
       const bool late = globaltimer() - t0 > kWaitTimeoutNs;
@@ -593,13 +583,10 @@ __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, int32
 }
 
 // A bounded wait of the whole warp, which branches as one (the vote keeps it
-// free of the convergence barriers of a wait per lane).  Polls cost issue slots
-// that the other warps need: the roles that run ahead of the MMAs sleep between
-// theirs, the ones in the MMA - softmax loop do not.
-template <bool kSleep = false>
+// free of the convergence barriers of a wait per lane).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  return warp_wait_slow<kSleep>(bar, parity, err, abort);
+  return warp_wait_slow(bar, parity, err, abort);
 }
 
 // The raw K or V row groups of the CTA's tiles into a ring of ns stages at ring,
@@ -673,7 +660,7 @@ __device__ __forceinline__ int copy_role(const Params& p, Pos pos, int n, bool i
     if (j < 0) continue;
     const uint32_t good = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, mine && !ok);
     const uint32_t stage = 2 * pair + half, fb = full + 8 * stage, dst = ring + stage * (4 * gb) + (lane & 3) * gb;
-    if (j >= ns / 2 && !warp_wait<true>(empty + 8 * stage, parity, p.err, abort)) return 2 * j;
+    if (j >= ns / 2 && !warp_wait(empty + 8 * stage, parity, p.err, abort)) return 2 * j;
     if (bad) {  // rows of an entry outside the pool read as zeros
       if (lane == 0) record_error(p.err, PA_ERR_BOUNDS);
 #pragma unroll 1
@@ -748,19 +735,20 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
   //   kraw_*, vraw_* [(2 j + half) % stages]  copies <-> dequantisation (four warps read a stage)
   //   ku_*, vu_* [half]                 operand units: dequantisation (four warps) <-> MMA (commit)
   //   s_full / s_empty [j & 1]          S^T(j) in tensor memory / in the softmax registers
-  //   p_full / pv_done                  P^T(j) written / O^T holds tile j, P^T free
+  //   p_full / pv_done [j & 1]          P^T(j) written / O^T holds tile j, P^T(j) is free
   //   q_full / q_empty [i & 1]          query rows of piece i staged / no longer needed
   //   o_free [i & 1]                    piece i's O^T has been read
   // A role whose wait expires stops: it arrives nowhere any more.
   const uint32_t kraw_full = base + SM::kBar, kraw_empty = kraw_full + 8 * NK, vraw_full = kraw_empty + 8 * NK,
                  vraw_empty = vraw_full + 8 * NV, ku_full = vraw_empty + 8 * NV, ku_empty = ku_full + 16,
                  vu_full = ku_empty + 16, vu_empty = vu_full + 16, s_full = vu_empty + 16, s_empty = s_full + 16,
-                 q_full = s_empty + 16, q_empty = q_full + 16, p_full = q_empty + 16, pv_done = p_full + 8,
-                 o_free = pv_done + 8, drain = o_free + 16, sink = drain + 16;
+                 q_full = s_empty + 16, q_empty = q_full + 16, p_full = q_empty + 16, pv_done = p_full + 16,
+                 o_free = pv_done + 16, drain = o_free + 16, sink = drain + 16;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + SM::kMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc + 8);
   Pos* start = reinterpret_cast<Pos*>(smem + SM::kMisc + 16);
   int* tiles_at = reinterpret_cast<int*>(smem + SM::kMisc + 16 + sizeof(Pos));  // the CTA's first tile, the next CTA's
+  Tile* opening = reinterpret_cast<Tile*>(smem + SM::kOpening);                 // of the first tile, what its query rows need
   Tile* tiles = reinterpret_cast<Tile*>(smem + SM::kTile);
   int* lefts = reinterpret_cast<int*>(smem + SM::kLeft);
   if (tid == 0) {
@@ -782,11 +770,11 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       mbar_init(s_empty + 8 * i, 8);
       mbar_init(q_full + 8 * i, 8);
       mbar_init(q_empty + 8 * i, 1);
+      mbar_init(p_full + 8 * i, 8);
+      mbar_init(pv_done + 8 * i, 1);
       mbar_init(o_free + 8 * i, 8);
       mbar_init(drain + 8 * i, 1);
     }
-    mbar_init(p_full, 8);
-    mbar_init(pv_done, 1);
     mbar_init(sink, 1);
     fence_mbar_init();
   }
@@ -795,7 +783,10 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     if (x < p.total_len) {
       const Pos t = locate(p, x);
       if (lane == 0) {
-        if (w == 1) *start = t;
+        if (w == 1) {
+          *start = t;
+          *opening = Tile{(uint32_t)pos_rows(p, t) | 1u << 8, 0, t.rt * kRows, 0, pos_seq(p, t) * p.n_qtok, t.head, {0, 0}};
+        }
         tiles_at[w - 1] = t.tile;
       }
     } else if (lane == 0) {
@@ -838,15 +829,24 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     // The query rows of a piece are staged here too, eight by each of the warps,
     // copied while the tile's K is converted.
     uint32_t piece = 0;
+    bool wide = false;  // the piece before
     for (int j = 0; j < n; ++j) {
       const uint32_t stage = 2 * j + (quarter >> 1), slot = stage % NK;
-      if (!warp_wait<true>(kraw_full + 8 * slot, (stage / NK) & 1, p.err, abort)) break;
-      const Tile& t = tiles[j & (kTiles - 1)];
-      const uint32_t info = t.info, q_dst = base + SM::kQ + (piece & 1) * SM::kQBytes;
+      // the first piece's rows do not wait for its keys
+      if (j > 0 && !warp_wait(kraw_full + 8 * slot, (stage / NK) & 1, p.err, abort)) break;
+      const Tile& t = j > 0 ? tiles[j & (kTiles - 1)] : *opening;
+      const uint32_t info = t.info, q_dst = base + SM::kQ + row0_of(info) * (kD * 2);
       const bool first_tile = (info >> 8) & 1, stage_q = first_tile && 8 * w < (int)(((info & 0xff) + 15) & ~15u);
-      if (first_tile && piece >= 2 && !warp_wait<true>(q_empty + 8 * (piece & 1), ((piece >> 1) - 1) & 1, p.err, abort)) break;
+      if (first_tile) {
+        if (piece > 1 && !warp_wait(q_empty + 8 * (piece & 1), ((piece >> 1) - 1) & 1, p.err, abort)) break;
+        if (piece > 0 && (wide || is_wide(info)) &&
+            !warp_wait(q_empty + 8 * ((piece - 1) & 1), ((piece - 1) >> 1) & 1, p.err, abort))
+          break;
+        wide = is_wide(info);
+      }
       if (stage_q) stage_q_begin<KT>(p, t, q_dst, 8 * w, lane);
-      if (j > 0 && !warp_wait<true>(ku_empty + 8 * kd, (j - 1) & 1, p.err, abort)) break;
+      if (!(j > 0 ? warp_wait(ku_empty + 8 * kd, (j - 1) & 1, p.err, abort) : warp_wait(kraw_full + 8 * slot, 0, p.err, abort)))
+        break;
       tc_fence_after();
       dequant_k<KT>(grp + slot * SM::kKStage, r, kd, kKCol + 64 * kd + t_lane);
       __syncwarp();
@@ -872,8 +872,8 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     const uint32_t t_lane = (uint32_t)(32 * quarter) << 16;
     for (int j = 0; j < n; ++j) {
       const uint32_t stage = 2 * j + vh, slot = stage % NV;
-      if (!warp_wait<true>(vraw_full + 8 * slot, (stage / NV) & 1, p.err, abort)) break;
-      if (j > 0 && !warp_wait<true>(vu_empty + 8 * vh, (j - 1) & 1, p.err, abort)) break;
+      if (!warp_wait(vraw_full + 8 * slot, (stage / NV) & 1, p.err, abort)) break;
+      if (j > 0 && !warp_wait(vu_empty + 8 * vh, (j - 1) & 1, p.err, abort)) break;
       tc_fence_after();
       dequant_v<VT>(base + SM::kVRing + slot * SM::kVStage, quarter, lefts[j & (kTiles - 1)] - kStageKeys * vh,
                     kVCol + 64 * vh + t_lane, lane);
@@ -910,7 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
         }
         if (j >= 2) wait(s_empty + 8 * b, ((j >> 1) - 1) & 1);
         tc_fence_after();
-        const uint64_t qd = qdesc + (uint64_t)(((piece - 1) & 1) * (SM::kQBytes >> 4));
+        const uint64_t qd = qdesc + row0_of(info) * (kD * 2 / 16);
         const uint32_t idesc = idesc_of(info), d = kSCol + 64 * b;
 #pragma unroll 1
         for (uint32_t h = 0; h < 2; ++h) {
@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       uint32_t wide = 0;  // the piece before
       for (uint32_t j = 0; j < (uint32_t)n; ++j) {
         const uint32_t b = j & 1;
-        wait(p_full, b);
+        wait(p_full + 8 * b, (j >> 1) & 1);
         const uint32_t info = info_of(j), first_tile = (info >> 8) & 1, idesc = idesc_of(info);
         if (first_tile) {
           if (piece > 1) wait(o_free + 8 * (piece & 1), ((piece >> 1) - 1) & 1);
@@ -943,13 +943,13 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
         for (uint32_t h = 0; h < 2; ++h) {
           wait(vu_full + 8 * h, b);
           tc_fence_after();
-          mma8<true>(kOCol + o_half(info), kVCol + 64 * h, pdesc + 64 * h, idesc, h | (first_tile ^ 1u), leader);
+          mma8<true>(kOCol + row0_of(info), kVCol + 64 * h, pdesc + (b * (SM::kPBytes >> 4) + 64 * h), idesc, h | (first_tile ^ 1u), leader);
           commit(vu_empty + 8 * h);
         }
-        commit(pv_done);
+        commit(pv_done + 8 * b);
       }
       for (int i = 0; i < 2; ++i) wait(vu_empty + 8 * i, (n - 1) & 1);
-      wait(pv_done, (n - 1) & 1);
+      for (uint32_t j = n < 2 ? 0 : n - 2; j < (uint32_t)n; ++j) wait(pv_done + 8 * (j & 1), (j >> 1) & 1);
     }
     if (dead) {  // what was issued ends before shared and tensor memory are released
       const uint32_t bar = drain + 8 * (w - kSWarp);
@@ -991,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       const int nc = ((info & 0xff) + 15) >> 4;  // query rows in sixteens
       const Tile& tl = tiles[j & (kTiles - 1)];
       const bool first_tile = (info >> 8) & 1;
-      const uint32_t s_at = s_addr + 64 * (j & 1);
+      const uint32_t s_at = s_addr + 64 * (j & 1), p_to = p_addr + (j & 1) * SM::kPBytes;
       const bool edge = tl.open < kKeys;
       int la = 0, lb = 0;
       if (edge) {
@@ -1049,32 +1049,31 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
             for (int e = 0; e < 2; ++e)
               l[c][e] = first_tile ? 0ull : mul2(l[c][e], *reinterpret_cast<const uint64_t*>(alpha + 16 * c + 8 * e + t2));
           if (!first_tile) {  // O^T holds the tiles before: dims of this warp, every row
+            live = live && warp_wait(pv_done + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, p.err, abort);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 2 * nc; ++c) {
               uint32_t o[8];
-              tmem_ld8(o_addr + o_half(info) + 8 * c, o);
+              tmem_ld8(o_addr + row0_of(info) + 8 * c, o);
               tmem_ld_wait();
               loaded(o);
 #pragma unroll
               for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha[8 * c + i]);
-              tmem_st8(o_addr + o_half(info) + 8 * c, o);
+              tmem_st8(o_addr + row0_of(info) + 8 * c, o);
             }
             tmem_st_wait();
             tc_fence_before();
           }
         }
         float top = -INFINITY;
-        uint32_t xs[2][8];
-        tmem_ld_frag2(s_at, xs[0]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           ls[c][0] = ls[c][1] = 0ull;
           if (c >= nc) continue;
-          uint32_t (&x)[8] = xs[c & 1];
+          uint32_t x[8];
+          tmem_ld_frag2(s_at + 16 * c, x);
           tmem_ld_wait();
           loaded(x);
-          if (c + 1 < 4 && c + 1 < nc) tmem_ld_frag2(s_at + 16 * (c + 1), xs[(c + 1) & 1]);
           logits(x, j, c, true, edge, la, lb);
 #pragma unroll
           for (int i = 0; i < 8; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
@@ -1087,8 +1086,8 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
             h[2 * e + 1] = pack_half2(b0, b1);
             ls[c][e] = add2(pack2(a0, a1), pack2(b0, b1));
           }
-          if (c == 0 && j > 0) live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);  // P^T(j - 1) has been read
-          stsm_x4_trans(p_addr + c * (16 * kKeys * 2), h[0], h[1], h[2], h[3]);
+          if (c == 0 && j > 1) live = live && warp_wait(pv_done + 8 * (j & 1), ((j >> 1) - 1) & 1, p.err, abort);  // of P^T(j - 2)
+          stsm_x4_trans(p_to + c * (16 * kKeys * 2), h[0], h[1], h[2], h[3]);
         }
         if (raise) break;
         raise = bar_or(1, kSmThreads, top > kLazyLog2);
@@ -1102,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       fence_proxy_async_smem();
       __syncwarp();
       if (live && lane == 0) {
-        mbar_arrive(p_full);
+        mbar_arrive(p_full + 8 * (j & 1));
         mbar_arrive(s_empty + 8 * (j & 1));
       }
       __syncwarp();
@@ -1111,17 +1110,15 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       if (j < n) {
         live = live && warp_wait(s_full + 8 * (j & 1), (j >> 1) & 1, p.err, abort);
         tc_fence_after();
-        const uint32_t info = tiles[j & (kTiles - 1)].info;
-        tile(j, info);
-      } else {
-        live = live && warp_wait(pv_done, (j - 1) & 1, p.err, abort);
+        tile(j, tiles[j & (kTiles - 1)].info);
       }
       // ---- a piece's O^T, once the weights of the tile after it are on their way
       const Tile& t = tiles[(j - 1) & (kTiles - 1)];
       const uint32_t info = j > 0 ? t.info : 0u;
       if ((info >> 9) & 1) {
         const int rows = info & 0xff;
-        const uint32_t from = o_addr + o_half(info);
+        const uint32_t from = o_addr + row0_of(info);
+        live = live && warp_wait(pv_done + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, p.err, abort);
         float* dst = p.part_o + (long long)t.slot_row * kD + 128 * hh + 32 * quarter + v_dim<VT>(lane);
         tc_fence_after();
 #pragma unroll 1
