@@ -38,6 +38,7 @@ struct MergeParams {
   float* lse;
   int32_t* err;
   int out_type, n_qtok, n_kv_heads, n_q_heads, n_ctas;
+  uint64_t len_inv;  // 2^64 / total_len, rounded up
   int weigh, prefix_len, total_len, suffix_row_tiles, suffix_rows, suffix_base;
   int32_t len[kMaxSeqs], start[kMaxSeqs], seq_at[kMaxSeqs];
   int16_t group[kMaxSeqs];  // a sequence's group, or -1
@@ -51,26 +52,45 @@ struct Pieces {
   int n, step;
 };
 
+// cta_of by the reciprocal: a 64-bit division per row and thread costs more than
+// the row's sums.  The product's excess is below x n_ctas / total_len < n_ctas, so
+// the quotient is at most one too large.
+__device__ __forceinline__ int merge_cta_of(const MergeParams& p, int x) {
+  const uint64_t num = ((uint64_t)x + 1) * (uint32_t)p.n_ctas - 1, q = __umul64hi(num, p.len_inv);
+  return (int)q - (q * (uint32_t)p.total_len > num);
+}
+
 __device__ __forceinline__ Pieces pieces_of(const MergeParams& p, int at, int unit_rows, int in_unit, int nt, int seg,
                                             int step, int base, int r) {
   const Cost c = cost_of(p.weigh, unit_rows);
   at += in_unit * (c.lead + nt * c.tile) + c.lead;
-  const int c0 = cta_of(at, p.total_len, p.n_ctas), c1 = cta_of(at + (nt - 1) * c.tile, p.total_len, p.n_ctas);
+  const int c0 = merge_cta_of(p, at), c1 = merge_cta_of(p, at + (nt - 1) * c.tile);
   return Pieces{base + (long long)(c0 + seg) * step + r, c1 - c0 + 1, step};
 }
 
-// One CTA per output row: kGroups groups of 64 threads (a float4 of the dims
-// each) take every kGroups-th piece of the row's suffix and prefix; then the
-// groups' states are joined.  With M the largest reference maximum and w_i =
-// 2^(m_i - M): out = sum w_i O_i / sum w_i l_i, lse = (M + log2 sum w_i l_i) ln 2.
-// The order is fixed, so the result does not depend on timing.
-constexpr int kMergeGroups = 4, kMergeThreads = 64 * kMergeGroups, kAhead = 4;
+// One CTA per output row: G groups of 64 threads (a float4 of the dims each) take
+// every G-th piece of the row's suffix and prefix, kAhead pieces' loads at once;
+// then the groups' states are joined.  With M the largest reference maximum and
+// w_i = 2^(m_i - M): out = sum w_i O_i / sum w_i l_i, lse = (M + log2 sum w_i l_i)
+// ln 2.  The order is fixed, so the result does not depend on timing.
+//
+// G by the rows: the more there are, the fewer threads for each, so that all of
+// them are resident at once (merge_groups).  Whole calls with 1, 2, 4 and 8
+// groups, us: 192 rows 31.9, 28.2, 25.7, 25.0; 408 rows 25.1, 23.7, 22.5, 22.8;
+// 768 rows 36.6, 35.0, 35.9, 37.4; 1536 rows 40.8, 42.1, 44.5, 47.3.
+int merge_groups(int64_t rows, int sms) {
+  int g = 8;
+  while (g > 1 && rows * g * 64 > (int64_t)sms * 768) g /= 2;
+  return g;
+}
 
-__global__ void __launch_bounds__(kMergeThreads) pa_prefix_merge_kernel(const __grid_constant__ MergeParams p) {
-  __shared__ float sm[kMergeGroups], sw[kMergeGroups];
-  __shared__ float4 so[kMergeGroups][64];
+template <int G>
+__global__ void __launch_bounds__(64 * G) pa_prefix_merge_kernel(const __grid_constant__ MergeParams p) {
+  constexpr int kAhead = G == 1 ? 8 : G == 8 ? 2 : 4;
+  __shared__ float sm[G], sw[G];
+  __shared__ float4 so[G][64];
   const int col = threadIdx.x & 63, grp = threadIdx.x >> 6;
-  const int h = blockIdx.x % p.n_q_heads, st = blockIdx.x / p.n_q_heads, t = st % p.n_qtok, s = st / p.n_qtok;
+  const int h = blockIdx.x, t = blockIdx.y, s = blockIdx.z;
   const int head = h / kGqa, hl = h % kGqa;
   Pieces a, b{0, 0, 0};
   {
@@ -92,12 +112,12 @@ __global__ void __launch_bounds__(kMergeThreads) pa_prefix_merge_kernel(const __
   const int np = len_ok ? a.n + b.n : 0;
   float M = -INFINITY, W = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = grp; i0 < np; i0 += kMergeGroups * kAhead) {
+  for (int i0 = grp; i0 < np; i0 += G * kAhead) {
     float2 ml[kAhead];
     float4 x[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int i = i0 + kMergeGroups * k;
+      const int i = i0 + G * k;
       ml[k] = make_float2(-INFINITY, 0.f);
       x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < np) {
@@ -132,11 +152,11 @@ __global__ void __launch_bounds__(kMergeThreads) pa_prefix_merge_kernel(const __
   if (grp != 0) return;
   float Mr = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kMergeGroups; ++i) Mr = fmaxf(Mr, sm[i]);
+  for (int i = 0; i < G; ++i) Mr = fmaxf(Mr, sm[i]);
   W = 0.f;
   O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < kMergeGroups; ++i) {
+  for (int i = 0; i < G; ++i) {
     const float f = sw[i] > 0.f ? exp2f(sm[i] - Mr) : 0.f;
     W = fmaf(f, sw[i], W);
     const float4 v = so[i][col];
@@ -144,7 +164,7 @@ __global__ void __launch_bounds__(kMergeThreads) pa_prefix_merge_kernel(const __
   }
   const float inv = W > 0.f ? 1.f / W : 0.f;
   O = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
-  const long long row = blockIdx.x;
+  const long long row = ((long long)s * p.n_qtok + t) * p.n_q_heads + h;
   if (p.out_type == PA_DT_F32) {
     reinterpret_cast<float4*>(p.out)[row * 64 + col] = O;
   } else if (p.out_type == PA_DT_F16) {
@@ -340,6 +360,7 @@ pa_status run_chunk(const Batch& b, uint32_t c0, uint32_t cn, const Group* group
   p.n_ctas = m.n_ctas = ctas;
   p.weigh = m.weigh = weigh;
   p.total_tiles = (int)tiles;
+  m.len_inv = ~0ull / (uint64_t)at + 1;
   p.prefix_len = m.prefix_len = (int32_t)prefix_len;
   p.total_len = m.total_len = (int32_t)at;
   p.suffix_row_tiles = m.suffix_row_tiles = srt;
@@ -365,10 +386,15 @@ pa_status run_chunk(const Batch& b, uint32_t c0, uint32_t cn, const Group* group
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, ki.fn, p) != cudaSuccess) return PA_ERR_CUDA;
-  cfg.gridDim = dim3(cn * (unsigned)(T * heads * kGqa));
-  cfg.blockDim = dim3(kMergeThreads);
+  cfg.gridDim = dim3((unsigned)(heads * kGqa), (unsigned)T, cn);
+  const int wide = merge_groups((int64_t)cn * T * heads * kGqa, b.sms);
+  cfg.blockDim = dim3(64 * wide);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, pa_prefix_merge_kernel, m) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const auto merge = wide == 8   ? pa_prefix_merge_kernel<8>
+                     : wide == 4 ? pa_prefix_merge_kernel<4>
+                     : wide == 2 ? pa_prefix_merge_kernel<2>
+                                   : pa_prefix_merge_kernel<1>;
+  return cudaLaunchKernelEx(&cfg, merge, m) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace

@@ -78,7 +78,7 @@ constexpr int kKWarp0 = 0, kVWarp0 = 8, kSmWarp0 = 16, kSWarp = 24, kPvWarp = 25
 constexpr int kThreads = 28 * 32;
 constexpr int kSmThreads = 256;
 constexpr uint32_t kTmemCols = 512, kOCol = 0, kSCol = 128, kKCol = 256, kVCol = 384;
-constexpr int kLead = 7, kTileCost = 6;
+constexpr int kLead = 12, kTileCost = 9;
 constexpr float kLazyLog2 = 8.f;  // the reference maximum is raised past this
 
 struct Params {
@@ -116,8 +116,10 @@ struct Cost {
   int lead, tile;
 };
 
-// By the query rows of the unit, in half microseconds: a tile of 16 rows takes
-// 1.5 us, one of 64 2.5; a piece 2 us more than its tiles.
+// By the query rows of the unit: what tiles of up to 31, 63 and 64 rows and the
+// pieces took, fitted over batches of short and long suffixes.  Equal tiles and no
+// lead: 64 sequences of 128 + 4096 keys 175 us instead of 90, 8 of 98304 + 16 in
+// Q8_0 70 instead of 48.
 __host__ __device__ constexpr Cost cost_of(int weigh, int rows) {
   return weigh ? Cost{kLead, kTileCost + (rows >= kRows ? 2 : rows / 32)} : Cost{0, 1};
 }
@@ -1010,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       uint64_t ls[4][2];
       for (;;) {
         if (raise) {
-          named_bar_sync(1, kSmThreads);  // the others are done with the shared arrays
+          if (j > 0) named_bar_sync(1, kSmThreads);  // the others are done with the shared arrays
 #pragma unroll 1
           for (int c = 0; c < nc; ++c) {
             uint32_t x[8];
