@@ -114,6 +114,34 @@ def test_stress_inputs(kind, t):
     against_oracle(w, np.array([2], np.uint32), np.array([rows], np.int32), what=kind)
 
 
+@pytest.mark.parametrize("kt,vt,t,ps,groups", [
+    (Q4, Q4, 1, 16, [(14, 1500), (2, 1000), (5, 130), (1, 300), (12, 2100), (6, 0)]),
+    (Q8, Q4, 2, 48, [(9, 1500), (2, 1000), (5, 130), (1, 300), (7, 2100), (6, 0)]),
+    (F16, F16, 1, 64, [(8, 2500), (3, 1000), (6, 1200)]),
+    (Q8, Q8, 11, 16, [(3, 900), (1, 20), (4, 400)]),
+    (Q4, Q8, 1, 16, [(30, 128)] + [(2, 16 + 16 * i) for i in range(25)]),
+])
+def test_ctas_of_many_pieces(kt, vt, t, ps, groups):
+    """Several tiles and pieces to a CTA: wide and narrow ones in turn, pieces
+    of one tile, and all numbers of threads that the merge gives a row."""
+    own = [t + (97 * i) % 800 for i in range(sum(b for b, _ in groups))]
+    w, gs, pl = prefix_workload(groups, own, ps, kt, vt, n_qtok=t, seed=t)
+    against_oracle(w, gs, pl, torch.float16)
+
+
+@pytest.mark.parametrize("kind", ["rising", "late", "scales"])
+@pytest.mark.parametrize("t", [1, 4])
+def test_references_raised_inside_a_piece(kind, t):
+    """The stress inputs again, long enough that a CTA's piece has several tiles:
+    weights already in O are scaled down, tiles whose weights overflow are redone."""
+    base = W.stress_workload(kind, 78, [12000], 16, Q8, Q4, t)
+    n, rows, pages = 12000, 6000, 750
+    table = np.stack([np.arange(pages), np.concatenate([np.arange(rows // 16), pages + np.arange(pages - rows // 16)])]).astype(np.int32)
+    w = W.Workload(kind, np.array([n, n], np.int32), t, 16, 2 * pages, Q8, Q4, table, np.concatenate([base.k_rows] * 2),
+                   np.concatenate([base.v_rows] * 2), np.concatenate([base.q, base.q]), base.scale)
+    against_oracle(w, np.array([2], np.uint32), np.array([rows], np.int32), what=kind)
+
+
 def test_page_size_and_placement_change_nothing():
     outs = []
     for ps in (16, 48, 256):
