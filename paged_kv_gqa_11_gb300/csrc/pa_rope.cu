@@ -325,14 +325,17 @@ __device__ __forceinline__ void turn_head(const RopeParams& p, const Raw<T>& raw
   }
 }
 
-// Heads whose loads are in flight at once, warps that few rows are split into,
-// and resident CTAs that the registers allow (20 warps an SM).  4096 rows of bf16:
-// 26.7 us (4.4 TB/s); batches of two 28.4, of eight 32.8 (107 registers).
-constexpr int kBatch = 4, kWarpsPerSm = 48, kMinCtas = 5;
+// Heads that are loaded at once (the next ones are prefetched meanwhile), warps
+// that few rows are split into, and resident CTAs that the registers allow: 28
+// warps an SM, 20 for the append, whose quantisers would spill.  4096 rows of bf16:
+// 22.8 us (5.1 TB/s) with 28 warps and the prefetch, 23.3 with 20, 27.0 without the
+// prefetch; 8192 rows appended as Q8_0 and Q4_0: 61.9 us, 64.5 and more with over
+// 20, 68.0 without; batches of two or eight heads are slower.
+constexpr int kBatch = 4, kWarpsPerSm = 48;
 
 // kAppend: keys and values go into the pools; else keys go to k_out.
 template <typename In, typename Out, bool kAppend>
-__global__ void __launch_bounds__(32 * kWarps, kMinCtas) pa_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(32 * kWarps, kAppend ? 5 : 7) pa_rope_kernel(const __grid_constant__ RopeParams p) {
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
   __shared__ uint64_t turns[kMaxPairs];
   const int lane = threadIdx.x & 31;
@@ -344,6 +347,17 @@ __global__ void __launch_bounds__(32 * kWarps, kMinCtas) pa_rope_kernel(const __
   const int chunk = (int)(item - row * p.chunks);
   const int h0 = chunk * p.per, h1 = min(h0 + p.per, p.hq + p.hk + p.hv);
   const int pos = __ldg(p.row_pos + row), from = partner_lane(p, lane);
+  if (p.per > kBatch) {  // many rows: the first heads are on their way before the position is known
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i;
+      if (h >= h1) break;
+      const uint8_t* src = h < p.hq          ? p.q + row * p.q_stride + h * kD * (int)sizeof(In)
+                           : h < p.hq + p.hk ? p.k + row * p.k_stride + (h - p.hq) * kD * (int)sizeof(In)
+                                             : p.v + row * p.v_stride + (h - p.hq - p.hk) * kD * (int)sizeof(In);
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(src + 8 * (int)sizeof(In) * lane));
+    }
+  }
   Place at{};
   bool placed = false;
   if (kAppend && h1 > p.hq) {
@@ -363,6 +377,11 @@ __global__ void __launch_bounds__(32 * kWarps, kMinCtas) pa_rope_kernel(const __
       for (int i = 0; i < N; ++i) {
         raw[i].load(src + i * kHead);
         r[i] = 1.f;
+      }
+      if (N == kBatch) {  // the next batch is on its way while this one is worked on
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (a + N + i < b) asm volatile("prefetch.global.L1 [%0];" ::"l"(src + (N + i) * kHead));
       }
       if (norm) inverse_norms<In, N>(p, raw, r);
 #pragma unroll
