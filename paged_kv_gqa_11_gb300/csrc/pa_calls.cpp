@@ -167,7 +167,8 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& body) {
     if (n != want) refuse("wrong number of arguments");
     return body();
   } catch (const Refused& r) {
-    PyObject* e = PyObject_CallFunction(g_error ? g_error : PyExc_RuntimeError, g_error ? "is" : "is", r.status, r.what.c_str());
+    PyErr_Clear();  // of a conversion whose result was then refused
+    PyObject* e = PyObject_CallFunction(g_error ? g_error : PyExc_RuntimeError, "is", r.status, r.what.c_str());
     if (e) {
       PyErr_SetObject(reinterpret_cast<PyObject*>(Py_TYPE(e)), e);
       Py_DECREF(e);

@@ -27,6 +27,7 @@ using pa_split::kLog2e;
 namespace {
 
 constexpr uint32_t kMaxQTok = 96;
+constexpr int64_t kMaxLen = 0x7fffffff - 2 * kKeys;  // a tile past the last key is still a 32-bit number
 
 // ------------------------------------------------------------------ merge
 
@@ -434,6 +435,7 @@ extern "C" pa_status pa_decode_prefix(const pa_pool* pool, const void* q, int32_
     if (group_sizes[g] == 0 || end > n_seq || prefix_lens[g] < 0) return PA_ERR_INVALID;
     for (; at < end; ++at) {
       const int64_t L = seq_lens_host[at];
+      if (L > kMaxLen) return PA_ERR_UNSUPPORTED;
       if (L < (int64_t)n_qtok || L > (int64_t)table_stride * b.d.page_size || prefix_lens[g] > L - (int64_t)n_qtok)
         return PA_ERR_INVALID;
     }

@@ -24,9 +24,10 @@
 // is.  K and V are then the A operands, and those may lie in tensor memory:
 // a dequantising warp goes from raw quants in shared memory through registers
 // into tensor memory, and the binary16 K and V never touch shared memory,
-// whose bandwidth a kernel with both operands there runs out of first.  An
-// MMA of up to 64 columns takes about 48 cycles whatever N is, so 128 keys
-// cost 32 x 48 cycles for up to 64 rows.
+// whose bandwidth a kernel with both operands there runs out of first.  An MMA
+// with A in tensor memory takes N / 2 cycles (measured: 24.6 with 48 columns, 32.4
+// with 64; 44 to 48 with A in shared memory, whatever N), so 128 keys cost 32 of
+// them, about 1000 cycles for 64 rows.
 //
 // Tensor memory (512 columns x 128 lanes): O^T dims 0-127 in columns 0-63 and
 // dims 128-255 in 64-127 (lane = dim, column = query row), two buffers of S^T
@@ -42,8 +43,23 @@
 //          transposing ldmatrix;
 //   16-23  softmax: 16 keys each, all query rows, in mma fragments; P^T goes to
 //          shared memory by transposing stmatrix; they also rescale O^T (rarely:
-//          the reference maximum is raised only past 2^8) and write the pieces;
+//          the reference maximum is raised only past 2^8) and write the pieces,
+//          each while the tile after it is multiplied;
 //   24, 25 MMA issue, S^T and O^T; 26, 27 raw K and V copies (cp.async.bulk).
+//
+// What bounds it.  Neither the tensor core (11 % of a call of 8 x (32768 + 1024)
+// keys in Q4_0, 25 us, by the counter; 30 % where tiles of 64 rows follow one another)
+// nor the memory, but for binary16 (8 x 98304 keys: 72 us, 5.6 TB/s).  A tile of 64
+// rows takes about 1.8 us, and
+// three chains are equally long there: the softmax of a tile (latencies: 2,400
+// cycles, and 600 to the next), the dequantisation of V plus half of its MMAs, and
+// of K plus half of its.  Seven warps on a scheduler, each in code of its own,
+// wait for instructions as much as for anything else: one softmax body for all
+// widths instead of four and one copy function instead of two took 64 x (8192 +
+// 300) keys from 61 to 49 us, while unrolled dequantisation and operand units of
+// half the size (more hand-offs) were slower by 8 to 30 per cent.  A call's first
+// output starts some 8 us after its first instruction (table, keys, their
+// conversion, two products, the merge), which is what short ones consist of.
 //
 // The key order inside a group of 16 is key16 below: it is the order in which
 // a transposing ldmatrix delivers key pairs to the columns of a V unit, chosen so
@@ -55,8 +71,6 @@
 // of the rounding of Q that fp32 queries meet anyway; keeping K exact would take
 // a second product and half again the dequantisation.
 #pragma once
-
-#include <type_traits>
 
 #include "pa_decode_impl.cuh"
 #include "pa_io.cuh"
@@ -79,7 +93,7 @@ constexpr int kThreads = 28 * 32;
 constexpr int kSmThreads = 256;
 constexpr uint32_t kTmemCols = 512, kOCol = 0, kSCol = 128, kKCol = 256, kVCol = 384;
 constexpr int kLead = 12, kTileCost = 9;
-constexpr float kLazyLog2 = 8.f;  // the reference maximum is raised past this
+constexpr float kLazyLog2 = 8.f;  // logits may pass their reference by this
 
 struct Params {
   const uint8_t* q;
@@ -945,7 +959,8 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
         for (uint32_t h = 0; h < 2; ++h) {
           wait(vu_full + 8 * h, b);
           tc_fence_after();
-          mma8<true>(kOCol + row0_of(info), kVCol + 64 * h, pdesc + (b * (SM::kPBytes >> 4) + 64 * h), idesc, h | (first_tile ^ 1u), leader);
+          mma8<true>(kOCol + row0_of(info), kVCol + 64 * h, pdesc + (b * (SM::kPBytes >> 4) + 64 * h), idesc,
+                     h | (first_tile ^ 1u), leader);
           commit(vu_empty + 8 * h);
         }
         commit(pv_done + 8 * b);
@@ -976,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     // Logits of 16 rows in log2 units, less their references (none: zero ones).
     // Thread: [8 columns e, key g or g + 8, column 2t or 2t + 1] at 4e + 2k + i.  Row r
     // of the tile's edge sees key k when r >= 6 (k - open + 1) (suffix) or k < open.
-    auto logits = [&](uint32_t (&x)[8], const int j, const int c, const bool refs, const bool edge, const int la, const int lb) {
+    auto logits = [&](uint32_t (&x)[8], const int c, const bool refs, const bool edge, const int la, const int lb) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint64_t m = refs ? *reinterpret_cast<const uint64_t*>(nref + 16 * c + 8 * e + t2) : 0ull;
@@ -989,6 +1004,9 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
           if (16 * c + 8 * (i >> 2) + (i & 1) < ((i & 2) ? lb : la)) x[i] = 0xff800000u;  // -inf
       }
     };
+    // S^T is read twice in a first tile (maxima, then weights) and once in others:
+    // kept in registers it made them spill.  The rows' sixteens are skipped, not
+    // compiled for each number of them.
     auto tile = [&](const int j, const uint32_t info) {
       const int nc = ((info & 0xff) + 15) >> 4;  // query rows in sixteens
       const Tile& tl = tiles[j & (kTiles - 1)];
@@ -1019,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
             tmem_ld_frag2(s_at + 16 * c, x);
             tmem_ld_wait();
             loaded(x);
-            logits(x, j, c, !first_tile, edge, la, lb);
+            logits(x, c, !first_tile, edge, la, lb);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float u = fmaxf(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 2])),
@@ -1076,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
           tmem_ld_frag2(s_at + 16 * c, x);
           tmem_ld_wait();
           loaded(x);
-          logits(x, j, c, true, edge, la, lb);
+          logits(x, c, true, edge, la, lb);
 #pragma unroll
           for (int i = 0; i < 8; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
           uint32_t h[4];

@@ -327,10 +327,12 @@ __device__ __forceinline__ void turn_head(const RopeParams& p, const Raw<T>& raw
 
 // Heads that are loaded at once (the next ones are prefetched meanwhile), warps
 // that few rows are split into, and resident CTAs that the registers allow: 28
-// warps an SM, 20 for the append, whose quantisers would spill.  4096 rows of bf16:
-// 22.8 us (5.1 TB/s) with 28 warps and the prefetch, 23.3 with 20, 27.0 without the
-// prefetch; 8192 rows appended as Q8_0 and Q4_0: 61.9 us, 64.5 and more with over
-// 20, 68.0 without; batches of two or eight heads are slower.
+// warps an SM, 20 for the append, whose quantisers would spill.  4096 rows of bf16,
+// one launch after another: 22.8 us with 28 warps and the prefetch, 23.3 with 20,
+// 27.0 without the prefetch (21.7 us, 5.4 TB/s, as programmatic dependents); 8192
+// rows appended as Q8_0 and Q4_0 and read back: 61.9 us, 64.5 and more with over 20
+// warps, 68.0 without the prefetch (60.5 as dependents); batches of two or eight
+// heads are slower.
 constexpr int kBatch = 4, kWarpsPerSm = 48;
 
 // kAppend: keys and values go into the pools; else keys go to k_out.

@@ -292,3 +292,32 @@ def test_a_serving_step_from_projections():
     e = np.exp(z - z.max(-1, keepdims=True))
     want = np.einsum("nhgl,nlhd->nhgd", e / e.sum(-1, keepdims=True), v).reshape(n, 1, 24, 256)
     assert_close(out.float().cpu().numpy(), want)
+
+
+def test_refusals_of_the_python_call():
+    """Arguments of the wrong type, shape, place or device: PaError, nothing written, and the next call works."""
+    w, gs, pl = prefix_workload([(2, 100), (1, 3)], [40, 50, 30], 16, Q8, Q4)
+    cache, tab = device_cache(w)
+    q, sl = to_dev(w.q).half(), to_dev(w.seq_lens)
+    want, want_lse = cache.decode_prefix(q, tab, sl, w.seq_lens, gs, pl, 1, w.scale)
+    out = torch.full_like(q, 7.0)
+    good = dict(q=q, block_table=tab, seq_lens_dev=sl, seq_lens_host=w.seq_lens, group_sizes=gs, prefix_lens=pl, n_qtok=1, scale=w.scale, out=out)
+    bad = [
+        dict(q=q.double()), dict(q=q[:, :, ::2]), dict(q=q.cpu()), dict(q=q[0]), dict(q=q[..., :128].contiguous()), dict(q=None), dict(q=w.q),
+        dict(block_table=tab.long()), dict(block_table=tab.T), dict(block_table=tab[:2]), dict(block_table=tab.cpu()), dict(block_table=tab[:, :1].contiguous()),
+        dict(seq_lens_dev=sl.long()), dict(seq_lens_dev=sl[:2]), dict(seq_lens_dev=w.seq_lens),
+        dict(seq_lens_host=w.seq_lens.astype(np.int64)), dict(seq_lens_host=w.seq_lens[:2]), dict(seq_lens_host=sl), dict(seq_lens_host=w.seq_lens * 0),
+        dict(seq_lens_host=np.repeat(w.seq_lens, 2)[::2]), dict(seq_lens_host=w.seq_lens.astype(np.float32)),
+        dict(group_sizes=gs + 1), dict(group_sizes=gs[:1]), dict(group_sizes=np.array([3, 0], np.uint32)), dict(prefix_lens=pl + 1000),
+        dict(prefix_lens=pl - 200), dict(prefix_lens=pl[:1]), dict(n_qtok=2), dict(n_qtok="1"), dict(scale="x"), dict(scale=0.0), dict(scale=float("nan")),
+        dict(scale=float("inf")), dict(scale=-1.0), dict(out=out[:2]), dict(out=out.double()), dict(out=out.cpu()), dict(out=torch.empty(3, 1, 24, 512, device="cuda")[..., ::2]),
+        dict(lse=torch.empty(3, 1, 24, device="cuda").half()), dict(lse=torch.empty(3, 24, device="cuda")), dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
+        dict(workspace=torch.empty(1 << 24, dtype=torch.uint8)), dict(stream="s"), dict(stream=object()),
+    ]
+    for change in bad:
+        with pytest.raises(PaError):
+            cache.decode_prefix(**{**good, **change})
+    torch.cuda.synchronize()
+    assert (out == 7).all() and cache.check() == PA_OK
+    got, lse = cache.decode_prefix(**good)
+    assert got is out and torch.equal(out, want) and torch.equal(lse, want_lse)

@@ -290,3 +290,40 @@ def test_unknown_types_are_refused():
     r = Rope(inv_freq(64))
     with pytest.raises(PaError):
         r.apply(torch.zeros(1, 1, 256, dtype=torch.float64, device="cuda"), None, torch.zeros(1, dtype=torch.int32, device="cuda"))
+
+
+def test_refusals_of_the_python_calls():
+    r = Rope(inv_freq(64))
+    dev = "cuda"
+    x = torch.zeros(3, 32, 256, dtype=torch.float16, device=dev)
+    pos = torch.zeros(3, dtype=torch.int32, device=dev)
+    q, k, v = x[:, :24], x[:, 24:28], x[:, 28:]
+    for args, kw in [((None, None, pos), {}), ((q.cpu(), None, pos), {}), ((q, k.float(), pos), {}), ((q, k[:2], pos), {}), ((q, k, pos.long()), {}),
+                     ((q, k, pos[:2]), {}), ((q, k, pos.cpu()), {}), ((q[0], None, pos), {}), ((q[..., :128], None, pos), {}),
+                     ((q[:, ::2], None, pos), {}), ((q[:, :, ::1].transpose(0, 1), None, pos), {}), ((q[:1].expand(3, 24, 256), None, pos), {}),
+                     ((q, None, pos), dict(k_out=torch.empty_like(k))), ((q, None, pos), dict(q_out=torch.empty_like(k))),
+                     ((q, None, pos), dict(q_out=torch.empty_like(q), out_dtype=torch.float32)), ((q, None, pos), dict(out_dtype=torch.float64)),
+                     ((q, None, pos), dict(out_dtype="half")), ((q, None, pos), dict(q_weight=x[0, 0, :128])), ((q, None, pos), dict(q_weight=x[0, 0].double())),
+                     ((q, k, pos), dict(q_weight=x[0, 0], k_weight=x[0, 0].float())), ((q, None, pos), dict(stream="s"))]:
+        with pytest.raises(PaError):
+            r.apply(*args, **kw)
+    c = PagedKVCache(8, 16, Q8, Q8)
+    seq = torch.zeros(3, dtype=torch.int32, device=dev)
+    tab = torch.zeros(1, 4, dtype=torch.int32, device=dev)
+    for args, kw in [((k, v[:, :2], seq, pos, tab), {}), ((k, v.float(), seq, pos, tab), {}), ((q, q, seq, pos, tab), {}), ((k, v, seq[:2], pos, tab), {}),
+                     ((k, v, seq, pos, tab.long()), {}), ((k, v, seq, pos, tab[0]), {}), ((k, v, seq.cpu(), pos, tab), {}),
+                     ((k, v, seq, pos, tab), dict(q_out=torch.empty_like(q))), ((k, v, seq, pos, tab), dict(q=q.float())),
+                     ((k, v, seq, pos, tab), dict(q=q, q_out=torch.empty_like(q), q_dtype=torch.float32))]:
+        with pytest.raises(PaError):
+            c.append_rope(r, *args, **kw)
+    for args, kw in [((seq, pos[:2], tab), {}), ((seq[None], pos, tab), {}), ((seq, pos, tab.cpu()), {}), ((seq, pos, tab), dict(dtype=torch.int8)),
+                     ((seq, pos, tab), dict(k_out=torch.empty(3, 4, 128, device=dev))), ((seq, pos, tab), dict(k_out=torch.empty(2, 4, 256, device=dev))),
+                     ((seq, pos, tab), dict(k_out=torch.empty(3, 4, 256, device=dev), v_out=torch.empty(3, 4, 256, device=dev).half()))]:
+        with pytest.raises(PaError):
+            c.read_rows(*args, **kw)
+    torch.cuda.synchronize()
+    assert c.check() == PA_OK and not c.k_pool.any() and not c.v_pool.any()
+    # no rows: empty outputs, nothing launched
+    none = torch.empty(0, dtype=torch.int32, device=dev)
+    assert r.apply(q[:0], k[:0], none)[0].shape == (0, 24, 256) and c.read_rows(none, none, tab)[0].shape == (0, 4, 256)
+    assert c.append_rope(r, k[:0], v[:0], none, none, tab, q=q[:0]).shape == (0, 24, 256)
