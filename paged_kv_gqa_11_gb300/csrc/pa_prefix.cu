@@ -78,7 +78,9 @@ __device__ __forceinline__ Pieces pieces_of(const MergeParams& p, int at, int un
 // G by the rows: the more there are, the fewer threads for each, so that all of
 // them are resident at once (merge_groups).  Whole calls with 1, 2, 4 and 8
 // groups, us: 192 rows 31.9, 28.2, 25.7, 25.0; 408 rows 25.1, 23.7, 22.5, 22.8;
-// 768 rows 36.6, 35.0, 35.9, 37.4; 1536 rows 40.8, 42.1, 44.5, 47.3.
+// 768 rows 36.6, 35.0, 35.9, 37.4; 1536 rows 40.8, 42.1, 44.5, 47.3.  Pieces at once:
+// 192 rows of 34 pieces 25.2 us with two, 23.7 with five, 25.7 with eight; 768 rows of
+// 15 35.5 with four, 34.1 with eight.
 int merge_groups(int64_t rows, int sms) {
   int g = 8;
   while (g > 1 && rows * g * 64 > (int64_t)sms * 768) g /= 2;
@@ -87,7 +89,7 @@ int merge_groups(int64_t rows, int sms) {
 
 template <int G>
 __global__ void __launch_bounds__(64 * G) pa_prefix_merge_kernel(const __grid_constant__ MergeParams p) {
-  constexpr int kAhead = G == 1 ? 8 : G == 8 ? 2 : 4;
+  constexpr int kAhead = G <= 2 ? 8 : 5;
   __shared__ float sm[G], sw[G];
   __shared__ float4 so[G][64];
   const int col = threadIdx.x & 63, grp = threadIdx.x >> 6;
@@ -108,9 +110,8 @@ __global__ void __launch_bounds__(64 * G) pa_prefix_merge_kernel(const __grid_co
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
-  const bool len_ok = __ldg(p.seq_lens + s) == p.len[s];
-  if (!len_ok && threadIdx.x == 0) record_error(p.err, PA_ERR_BOUNDS);
-  const int np = len_ok ? a.n + b.n : 0;
+  const int len_dev = __ldg(p.seq_lens + s);  // compared once the pieces are on their way
+  const int np = a.n + b.n;
   float M = -INFINITY, W = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = grp; i0 < np; i0 += G * kAhead) {
@@ -162,6 +163,11 @@ __global__ void __launch_bounds__(64 * G) pa_prefix_merge_kernel(const __grid_co
     W = fmaf(f, sw[i], W);
     const float4 v = so[i][col];
     O = make_float4(fmaf(f, v.x, O.x), fmaf(f, v.y, O.y), fmaf(f, v.z, O.z), fmaf(f, v.w, O.w));
+  }
+  if (len_dev != p.len[s]) {
+    if (threadIdx.x == 0) record_error(p.err, PA_ERR_BOUNDS);
+    W = 0.f;
+    O = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const float inv = W > 0.f ? 1.f / W : 0.f;
   O = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);

@@ -48,8 +48,8 @@
 //   24, 25 MMA issue, S^T and O^T; 26, 27 raw K and V copies (cp.async.bulk).
 //
 // What bounds it.  Neither the tensor core (11 % of a call of 8 x (32768 + 1024)
-// keys in Q4_0, 25 us, by the counter; 30 % where tiles of 64 rows follow one another)
-// nor the memory, but for binary16 (8 x 98304 keys: 72 us, 5.6 TB/s).  A tile of 64
+// keys in Q4_0, 24 us, by the counter; 30 % where tiles of 64 rows follow one another)
+// nor the memory, but for binary16 (8 x 98304 keys: 70 us, 5.7 TB/s).  A tile of 64
 // rows takes about 1.8 us, and
 // three chains are equally long there: the softmax of a tile (latencies: 2,400
 // cycles, and 600 to the next), the dequantisation of V plus half of its MMAs, and
