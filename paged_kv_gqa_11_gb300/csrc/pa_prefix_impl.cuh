@@ -314,7 +314,13 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[N]) {
                       "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
-// 16 lanes x 8 columns, the same distribution, stored.
+// 16 lanes x 16 columns and 16 lanes x 8 columns, the same distribution, stored.
+__device__ __forceinline__ void tmem_st_frag2(uint32_t a, const uint32_t (&u)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(u[0]), "r"(u[1]),
+               "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_frag1(uint32_t a, const uint32_t (&r)[4]) {
   asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]),
                "r"(r[3])
@@ -338,7 +344,7 @@ __device__ __forceinline__ void dequant_k(uint32_t grp, int r, int kd, uint32_t 
   const int r7 = r & 7;
   uint2 sc = make_uint2(0u, 0u);
   if (T != PA_F16) sc = lds64(grp + 16 * r + 8 * kd);  // four block scales
-#pragma unroll 1
+#pragma unroll 2
   for (int i = 0; i < 4; ++i) {
     const int b = 4 * kd + i;
     uint32_t out[16];
@@ -989,19 +995,13 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     uint64_t l[4][2] = {};  // sums of weights over this thread's keys: rows (16c + 8e + 2t, + 1)
     bool live = true;  // a warp whose wait expired keeps to the group's barriers but arrives nowhere
     // Logits of 16 rows in log2 units, less their references (none: zero ones).
-    // Thread: [8 columns e, key g or g + 8, column 2t or 2t + 1] at 4e + 2k + i.  Row r
-    // of the tile's edge sees key k when r >= 6 (k - open + 1) (suffix) or k < open.
-    auto logits = [&](uint32_t (&x)[8], const int c, const bool refs, const bool edge, const int la, const int lb) {
+    // Thread: [8 columns e, key g or g + 8, column 2t or 2t + 1] at 4e + 2k + i.
+    auto logits = [&](uint32_t (&x)[8], const int c, const bool refs) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint64_t m = refs ? *reinterpret_cast<const uint64_t*>(nref + 16 * c + 8 * e + t2) : 0ull;
         put2(x + 4 * e, fma2(get2(x + 4 * e), scale2, m));
         put2(x + 4 * e + 2, fma2(get2(x + 4 * e + 2), scale2, m));
-      }
-      if (edge) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (16 * c + 8 * (i >> 2) + (i & 1) < ((i & 2) ? lb : la)) x[i] = 0xff800000u;  // -inf
       }
     };
     // S^T is read twice in a first tile (maxima, then weights) and once in others:
@@ -1012,17 +1012,28 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       const Tile& tl = tiles[j & (kTiles - 1)];
       const bool first_tile = (info >> 8) & 1;
       const uint32_t s_at = s_addr + 64 * (j & 1), p_to = p_addr + (j & 1) * SM::kPBytes;
-      const bool edge = tl.open < kKeys;
-      int la = 0, lb = 0;
-      if (edge) {
+      if (tl.open < kKeys) {
+        // The edge: what a row does not see becomes -inf in tensor memory, so that
+        // the code of the other tiles has no mask in it.  Row r sees key k when r >= 6
+        // (k - open + 1) (suffix) or k < open.
         const int ka = tile_key + key16(g) - tl.open, kb = tile_key + key16(g + 8) - tl.open;
-        if ((info >> 10) & 1) {
-          la = kGqa * (ka + 1) - tl.row0 - t2;
-          lb = kGqa * (kb + 1) - tl.row0 - t2;
-        } else {
-          la = ka < 0 ? -kRows : kRows;
-          lb = kb < 0 ? -kRows : kRows;
+        const bool causal = (info >> 10) & 1;
+        int la = causal ? kGqa * (ka + 1) - tl.row0 - t2 : ka < 0 ? -kRows : kRows,
+            lb = causal ? kGqa * (kb + 1) - tl.row0 - t2 : kb < 0 ? -kRows : kRows;
+#pragma unroll 1
+        for (int c = 0; c < nc; ++c) {
+          uint32_t x[8];
+          tmem_ld_frag2(s_at + 16 * c, x);
+          tmem_ld_wait();
+          loaded(x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (8 * (i >> 2) + (i & 1) < ((i & 2) ? lb : la)) x[i] = 0xff800000u;  // -inf
+          tmem_st_frag2(s_at + 16 * c, x);
+          la -= 16;
+          lb -= 16;
         }
+        tmem_st_wait();
       }
       // The references are set at a piece's first tile and raised when a logit passes
       // them by 2^8; then the tile's weights are computed again.
@@ -1037,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
             tmem_ld_frag2(s_at + 16 * c, x);
             tmem_ld_wait();
             loaded(x);
-            logits(x, c, !first_tile, edge, la, lb);
+            logits(x, c, !first_tile);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               float u = fmaxf(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 2])),
@@ -1094,7 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
           tmem_ld_frag2(s_at + 16 * c, x);
           tmem_ld_wait();
           loaded(x);
-          logits(x, c, true, edge, la, lb);
+          logits(x, c, true);
 #pragma unroll
           for (int i = 0; i < 8; i += 2) top = fmaxf(top, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
           uint32_t h[4];
