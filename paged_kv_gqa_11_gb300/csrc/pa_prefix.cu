@@ -53,10 +53,10 @@ struct Pieces {
   int n, step;
 };
 
-// cta_of by the reciprocal: a 64-bit division per row and thread costs more than
-// the row's sums.  The product's excess is below x n_ctas / total_len < n_ctas, so
-// the quotient is at most one too large.
-__device__ __forceinline__ int merge_cta_of(const MergeParams& p, int x) {
+// The CTA of place x, by a reciprocal: a 64-bit division per row and thread costs
+// more than the row's sums.  The reciprocal is less than 1 too large, so the quotient
+// is by less than num / 2^64: at most one.
+__device__ __forceinline__ int cta_of(const MergeParams& p, int x) {
   const uint64_t num = ((uint64_t)x + 1) * (uint32_t)p.n_ctas - 1, q = __umul64hi(num, p.len_inv);
   return (int)q - (q * (uint32_t)p.total_len > num);
 }
@@ -65,7 +65,7 @@ __device__ __forceinline__ Pieces pieces_of(const MergeParams& p, int at, int un
                                             int step, int base, int r) {
   const Cost c = cost_of(p.weigh, unit_rows);
   at += in_unit * (c.lead + nt * c.tile) + c.lead;
-  const int c0 = merge_cta_of(p, at), c1 = merge_cta_of(p, at + (nt - 1) * c.tile);
+  const int c0 = cta_of(p, at), c1 = cta_of(p, at + (nt - 1) * c.tile);
   return Pieces{base + (long long)(c0 + seg) * step + r, c1 - c0 + 1, step};
 }
 

@@ -48,18 +48,18 @@
 //   24, 25 MMA issue, S^T and O^T; 26, 27 raw K and V copies (cp.async.bulk).
 //
 // What bounds it.  Neither the tensor core (11 % of a call of 8 x (32768 + 1024)
-// keys in Q4_0, 24 us, by the counter; 30 % where tiles of 64 rows follow one another)
-// nor the memory, but for binary16 (8 x 98304 keys: 70 us, 5.7 TB/s).  A tile of 64
-// rows takes about 1.8 us, and
-// three chains are equally long there: the softmax of a tile (latencies: 2,400
-// cycles, and 600 to the next), the dequantisation of V plus half of its MMAs, and
-// of K plus half of its.  Seven warps on a scheduler, each in code of its own,
-// wait for instructions as much as for anything else: one softmax body for all
-// widths instead of four and one copy function instead of two took 64 x (8192 +
-// 300) keys from 61 to 49 us, while unrolled dequantisation and operand units of
-// half the size (more hand-offs) were slower by 8 to 30 per cent.  A call's first
-// output starts some 8 us after its first instruction (table, keys, their
-// conversion, two products, the merge), which is what short ones consist of.
+// keys in Q4_0, 23 us, by the counter; a third where tiles of 64 rows follow one
+// another) nor the memory, but for binary16 (8 x 98304 keys: 69.5 us, 5.8 TB/s).  A
+// tile of 64 rows takes about 1.6 us, and three chains are about equally long there:
+// the softmax of a tile and the step to the next, the dequantisation of V plus half
+// of its MMAs, and of K plus half of its.  Seven warps on a scheduler, each in code of
+// its own, wait for instructions as much as for anything else: one softmax body for
+// all widths instead of four and one copy function instead of two took 64 x (8192 +
+// 300) keys from 61 to 49 us, the masks' own loop from 41 to 39.5; unrolling
+// the dequantisation by four makes it 50, and operand units of half the size (more
+// hand-offs) cost 8 per cent.  A call's first output starts some 8 us after its
+// first instruction (table, keys, their conversion, two products, the merge), which
+// is what short ones consist of.
 //
 // The key order inside a group of 16 is key16 below: it is the order in which
 // a transposing ldmatrix delivers key pairs to the columns of a V unit, chosen so
@@ -124,22 +124,18 @@ struct Params {
 __host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // A segment of nt tiles takes lead + nt * cost places, a tile stands at the first
-// of its own.  CTA i has the places i T / G .. (i + 1) T / G - 1 and the tiles
-// that stand there; cta_of is the CTA of place x.
+// of its own.  CTA i of G has the places i T / G .. (i + 1) T / G - 1 and the tiles
+// that stand there: place x is CTA ((x + 1) G - 1) / T's.
 struct Cost {
   int lead, tile;
 };
 
 // By the query rows of the unit: what tiles of up to 31, 63 and 64 rows and the
 // pieces took, fitted over batches of short and long suffixes.  Equal tiles and no
-// lead: 64 sequences of 128 + 4096 keys 175 us instead of 90, 8 of 98304 + 16 in
-// Q8_0 70 instead of 48.
+// lead: 64 sequences of 128 + 4096 keys 175 us, 8 of 98304 + 16 in Q8_0 70 us;
+// by cost, on the same kernel, 102 and 57.
 __host__ __device__ constexpr Cost cost_of(int weigh, int rows) {
   return weigh ? Cost{kLead, kTileCost + (rows >= kRows ? 2 : rows / 32)} : Cost{0, 1};
-}
-
-__host__ __device__ inline int cta_of(int x, int total, int ctas) {
-  return (int)((((long long)x + 1) * ctas - 1) / total);
 }
 
 struct Pos {
@@ -182,7 +178,7 @@ __device__ __forceinline__ Pos locate(const Params& p, int x) {
   t.pre = x < p.prefix_len;
   const int32_t* cum = t.pre ? p.group_at : p.seq_at;
   if (!t.pre) x -= p.prefix_len;
-  int lo = 0, hi = (t.pre ? p.n_groups : p.n_seq) - 1;  // the last unit whose first tile is <= x
+  int lo = 0, hi = (t.pre ? p.n_groups : p.n_seq) - 1;  // the last unit whose first place is <= x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (cum[mid] <= x) lo = mid; else hi = mid - 1;
@@ -329,8 +325,9 @@ __device__ __forceinline__ void tmem_st_frag1(uint32_t a, const uint32_t (&r)[4]
 
 // ------------------------------------------------------------------ dequantisation
 //
-// The loops are rolled: the roles' code runs side by side on every scheduler,
-// and the instruction cache is the first thing that it runs out of.
+// The loops are rolled (K two steps at a time): the roles' code runs side by side
+// on every scheduler, and the instruction cache is the first thing that it runs out
+// of.
 
 constexpr uint32_t kM1152 = pa_split::kHalf2_m1152, kM1032 = pa_split::kHalf2_m1032, kR16 = pa_split::kHalf2_1_16,
                    kM72 = pa_split::kHalf2_m72, kMagic = pa_split::kMagic64;
