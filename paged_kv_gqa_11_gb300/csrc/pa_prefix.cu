@@ -131,16 +131,17 @@ __global__ void __launch_bounds__(64 * G) pa_prefix_merge_kernel(const __grid_co
     float mr = M;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (ml[k].y > 0.f) mr = fmaxf(mr, ml[k].x);
-    const float f0 = W > 0.f ? exp2f(M - mr) : 0.f;
+      if (ml[k].y != 0.f) mr = fmaxf(mr, ml[k].x);
+    const float f0 = W != 0.f ? exp2f(M - mr) : 0.f;
     W *= f0;
     O = make_float4(O.x * f0, O.y * f0, O.z * f0, O.w * f0);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      // a piece in which the row sees nothing carries no weight, whatever its reference
-      const float f = ml[k].y > 0.f ? exp2f(ml[k].x - mr) : 0.f;
+      // a piece in which the row sees nothing (a sum of 0, not one that is NaN) carries no
+      // weight, whatever its reference
+      const float f = ml[k].y != 0.f ? exp2f(ml[k].x - mr) : 0.f;
       W = fmaf(f, ml[k].y, W);
-      if (ml[k].y > 0.f)
+      if (ml[k].y != 0.f)
         O = make_float4(fmaf(f, x[k].x, O.x), fmaf(f, x[k].y, O.y), fmaf(f, x[k].z, O.z), fmaf(f, x[k].w, O.w));
     }
     M = mr;
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(64 * G) pa_prefix_merge_kernel(const __grid_co
   O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < G; ++i) {
-    const float f = sw[i] > 0.f ? exp2f(sm[i] - Mr) : 0.f;
+    const float f = sw[i] != 0.f ? exp2f(sm[i] - Mr) : 0.f;
     W = fmaf(f, sw[i], W);
     const float4 v = so[i][col];
     O = make_float4(fmaf(f, v.x, O.x), fmaf(f, v.y, O.y), fmaf(f, v.z, O.z), fmaf(f, v.w, O.w));
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(64 * G) pa_prefix_merge_kernel(const __grid_co
     W = 0.f;
     O = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  const float inv = W > 0.f ? 1.f / W : 0.f;
+  const float inv = W != 0.f ? 1.f / W : 0.f;  // NaN where a sum of weights is
   O = make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
   const long long row = ((long long)s * p.n_qtok + t) * p.n_q_heads + h;
   if (p.out_type == PA_DT_F32) {
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(64 * G) pa_prefix_merge_kernel(const __grid_co
     reinterpret_cast<uint2*>(p.out)[row * 64 + col] =
         make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
   }
-  if (col == 0 && p.lse) p.lse[row] = W > 0.f ? (Mr + log2f(W)) * kLn2 : -INFINITY;
+  if (col == 0 && p.lse) p.lse[row] = W != 0.f ? (Mr + log2f(W)) * kLn2 : -INFINITY;
 }
 
 // ------------------------------------------------------------------ host side
