@@ -440,8 +440,7 @@ pa_status pa_decode_noalloc(const pa_pool* pool, const float* q, const void* k_p
  * q, out:   device [n_seq][n_qtok][n_q_heads][head_dim] of q_type / out_type (a
  *           pa_dtype), 16-byte aligned.  Queries of fp32 are rounded to
  *           binary16, as in pa_decode; quantised K (scale * quant) is too, so a
- *           logit is off by about 2^-12 |q| |k| scale at most, and a stored key
- *           past binary16's range (65504) is infinite here.
+ *           logit is off by about 2^-12 |q| |k| scale at most.
  *           A row whose logits are not all numbers (a NaN in its query or in a key
  *           that it sees) is NaN, its lse too.
  * prefix_lens: at most seq_lens_host - n_qtok of every sequence of the group

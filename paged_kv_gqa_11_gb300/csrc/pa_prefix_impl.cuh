@@ -65,6 +65,10 @@
 // a transposing ldmatrix delivers key pairs to the columns of a V unit, chosen so
 // that both its rows and the K threads' row reads fall in different banks.
 //
+// Range.  A stored key may have values past binary16's 65504 (scale * quant goes to
+// 8.3 * 10^6): the values of such a key are taken 2^-8 of what they are, its logits 2^8
+// times (dequant_k).  That costs the ordinary case a vote on the scales, 0 to 1 per cent.
+//
 // Precision.  Q, K, V (scale * quant, rounded once) and P are binary16, products
 // are accumulated in fp32, m, l and O are fp32, and l sums the weights before
 // their rounding.  Rounding K costs a logit 2^-12 |q| |k| scale at most, the size
@@ -230,7 +234,7 @@ struct Smem {
   static constexpr int kKStage = 4 * pa_layout::group_bytes<KT>(), kVStage = 4 * pa_layout::group_bytes<VT>();
   static constexpr int kQBytes = kRows * kD * 2, kPBytes = kRows * kKeys * 2;
   static constexpr int kQ = 0, kP = kQBytes, kRing = kP + 2 * kPBytes;
-  static constexpr int kTail = 8 * kRows * 4 + 2 * kRows * 4 + 17 * 32 + 64 + 640;  // red, references, tiles, barriers
+  static constexpr int kTail = 8 * kRows * 4 + 2 * kRows * 4 + 17 * 32 + 64 + 64 + 640;  // red, references, tiles, wide keys, barriers
   // K and V stages in rings of their own, both of an even number of stages: a
   // warp reads every second stage of its ring, and so sees every use of those it
   // reads (a parity wait must never be two phases ahead of its barrier).  Two
@@ -254,7 +258,8 @@ struct Smem {
   static constexpr int kVRing = kRing + kKStages * kKStage;
   static constexpr int kRed = kVRing + kVStages * kVStage;
   static constexpr int kRef = kRed + 8 * kRows * 4, kAlpha = kRef + kRows * 4;
-  static constexpr int kTile = kAlpha + kRows * 4, kOpening = kTile + 16 * 32, kLeft = kOpening + 32, kBar = kLeft + 64;
+  static constexpr int kTile = kAlpha + kRows * 4, kOpening = kTile + 16 * 32, kLeft = kOpening + 32, kWide = kLeft + 64,
+                       kBar = kWide + 16 * 4;
   // K and V raw full / empty [stages], K and V unit full / empty [2], s full / empty [2], q full / empty [2],
   // p full, pv done, o free [2] each, drain [2], sink
   static constexpr int kNBar = 2 * (kKStages + kVStages) + 8 + 4 + 4 + 9;
@@ -330,17 +335,34 @@ __device__ __forceinline__ void tmem_st_frag1(uint32_t a, const uint32_t (&r)[4]
 // of.
 
 constexpr uint32_t kM1152 = pa_split::kHalf2_m1152, kM1032 = pa_split::kHalf2_m1032, kR16 = pa_split::kHalf2_1_16,
-                   kM72 = pa_split::kHalf2_m72, kMagic = pa_split::kMagic64;
+                   kM72 = pa_split::kHalf2_m72, kMagic = pa_split::kMagic64, kR256 = 0x1c001c00u;  // 2^-8 twice
 
 // This thread's key, dims 128 kd .. + 127, from raw shared memory into a K
 // unit's 64 columns at taddr, 32 dims (16 columns) at a time.  grp: the key's row
-// group, r its row there.
+// group, r its row there.  Returns the warp's wide keys (lane = bit): those with a
+// scale times which the largest quant (128, in Q4_0 8) is past binary16's range.
+// Their values are made 2^-8 of what they are, both halves of the dims alike, and the
+// softmax multiplies their logits by 2^8.
 template <int T>
-__device__ __forceinline__ void dequant_k(uint32_t grp, int r, int kd, uint32_t taddr) {
+__device__ __forceinline__ uint32_t dequant_k(uint32_t grp, int r, int kd, uint32_t taddr) {
   const uint32_t row = grp + Fmt<T>::kScales + r * Fmt<T>::kRowQ;
   const int r7 = r & 7;
   uint2 sc = make_uint2(0u, 0u);
-  if (T != PA_F16) sc = lds64(grp + 16 * r + 8 * kd);  // four block scales
+  uint32_t wide = 0;
+  if constexpr (T != PA_F16) {
+    const uint4 d = lds128(grp + 16 * r);  // the row's eight block scales
+    sc = kd ? make_uint2(d.z, d.w) : make_uint2(d.x, d.y);
+    auto larger = [](uint32_t x, uint32_t y) {  // of two pairs of scales, by magnitude
+      const __half2 m = __hmax2(__habs2(*reinterpret_cast<const __half2*>(&x)), __habs2(*reinterpret_cast<const __half2*>(&y)));
+      return *reinterpret_cast<const uint32_t*>(&m);
+    };
+    // 2^9 (Q4_0: 2^13) is 0x6000 (0x7000): from there on the sum has bit 15
+    const bool mine = (larger(larger(d.x, d.y), larger(d.z, d.w)) + (T == PA_Q8_0 ? 0x20002000u : 0x10001000u)) & 0x80008000u;
+    if (__any_sync(0xffffffffu, mine)) {
+      wide = __ballot_sync(0xffffffffu, mine);
+      if (mine) sc = make_uint2(hmul2(sc.x, kR256), hmul2(sc.y, kR256));
+    }
+  }
 #pragma unroll 2
   for (int i = 0; i < 4; ++i) {
     const int b = 4 * kd + i;
@@ -383,6 +405,7 @@ __device__ __forceinline__ void dequant_k(uint32_t grp, int r, int kd, uint32_t 
     }
     tmem_st16(taddr + 16 * i, out);
   }
+  return wide;
 }
 
 // The four dims at load 0 and at load 1 of an 8-position slot of K's dim order,
@@ -475,7 +498,8 @@ __device__ __forceinline__ void dequant_v(uint32_t stage, int b, int n_keys, uin
 // sixteen tiles deep (the roles are never that far apart: the copy stages and
 // operand units between them hold fewer tiles).
 struct alignas(16) Tile {
-  uint32_t info;  // query rows of the segment | first tile of a piece << 8 | last << 9 | suffix << 10 | odd piece << 11
+  uint32_t info;  // query rows of the segment | first tile of a piece << 8 | last << 9 | suffix << 10 | odd piece << 11 |
+                  // 1 << 12 + q: wide keys in quarter q of the lanes (set by the K warps, before S^T)
   int open;       // keys of the tile that every row sees (<= 0: none; >= 128: no edge here); suffix row r sees
                   // (row0 + r) / 6 more
   int row0;       // first query row of the row tile
@@ -770,6 +794,9 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
   Tile* opening = reinterpret_cast<Tile*>(smem + SM::kOpening);                 // of the first tile, what its query rows need
   Tile* tiles = reinterpret_cast<Tile*>(smem + SM::kTile);
   int* lefts = reinterpret_cast<int*>(smem + SM::kLeft);
+  // wide keys (dequant_k) of each quarter of the lanes, where the tile says so; four tiles
+  // deep: K(j + 4) follows S^T(j + 3), and that the end of softmax(j + 1)
+  uint32_t* wide_keys = reinterpret_cast<uint32_t*>(smem + SM::kWide);
   if (tid == 0) {
     *abort = 0;
     for (int i = 0; i < NK; ++i) {
@@ -867,7 +894,11 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       if (!(j > 0 ? warp_wait(ku_empty + 8 * kd, (j - 1) & 1, p.err, abort) : warp_wait(kraw_full + 8 * slot, 0, p.err, abort)))
         break;
       tc_fence_after();
-      dequant_k<KT>(grp + slot * SM::kKStage, r, kd, kKCol + 64 * kd + t_lane);
+      const uint32_t wide_lanes = dequant_k<KT>(grp + slot * SM::kKStage, r, kd, kKCol + 64 * kd + t_lane);
+      if (KT != PA_F16 && wide_lanes != 0 && kd == 0 && lane == 0) {
+        wide_keys[4 * (j & 3) + quarter] = wide_lanes;
+        atomicOr(&tiles[j & (kTiles - 1)].info, 1u << (12 + quarter));
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(kraw_empty + 8 * slot);
       __syncwarp();
@@ -1009,10 +1040,13 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       const Tile& tl = tiles[j & (kTiles - 1)];
       const bool first_tile = (info >> 8) & 1;
       const uint32_t s_at = s_addr + 64 * (j & 1), p_to = p_addr + (j & 1) * SM::kPBytes;
-      if (tl.open < kKeys) {
+      const bool has_wide = KT != PA_F16 && info >> (12 + quarter) & 1;
+      if (tl.open < kKeys || has_wide) {
         // The edge: what a row does not see becomes -inf in tensor memory, so that
         // the code of the other tiles has no mask in it.  Row r sees key k when r >= 6
-        // (k - open + 1) (suffix) or k < open.
+        // (k - open + 1) (suffix) or k < open.  And the logits of wide keys.
+        const uint32_t wide = has_wide ? wide_keys[4 * (j & 3) + quarter] >> (16 * hh) : 0u;
+        const float fa = wide >> g & 1 ? 256.f : 1.f, fb = wide >> (g + 8) & 1 ? 256.f : 1.f;
         const int ka = tile_key + key16(g) - tl.open, kb = tile_key + key16(g + 8) - tl.open;
         const bool causal = (info >> 10) & 1;
         int la = causal ? kGqa * (ka + 1) - tl.row0 - t2 : ka < 0 ? -kRows : kRows,
@@ -1025,7 +1059,8 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
           loaded(x);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (8 * (i >> 2) + (i & 1) < ((i & 2) ? lb : la)) x[i] = 0xff800000u;  // -inf
+            x[i] = 8 * (i >> 2) + (i & 1) < ((i & 2) ? lb : la) ? 0xff800000u  // -inf
+                                                                : __float_as_uint(__uint_as_float(x[i]) * ((i & 2) ? fb : fa));
           tmem_st_frag2(s_at + 16 * c, x);
           la -= 16;
           lb -= 16;

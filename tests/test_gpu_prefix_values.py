@@ -1,11 +1,12 @@
 """Shared-prefix decode at the edges of its number types: what is not finite
-shows in the outputs."""
+shows in the outputs, and stored keys of any size count as what they are."""
 import numpy as np
 import pytest
 import torch
 
+import oracle
 import workloads as W
-from gpu_helpers import device_cache, to_dev
+from gpu_helpers import assert_close, assert_lse_close, device_cache, to_dev
 from paged_kv_gqa_11_gb300 import PA_OK
 from rope_helpers import prefix_workload
 
@@ -59,3 +60,74 @@ def test_a_nan_query_row_is_nan(dtype):
     mark[1, 0, 7] = True
     assert out[mark].isnan().all() and lse[mark].isnan().all()
     assert torch.equal(out[~mark], want[~mark]) and torch.equal(lse[~mark], want_lse[~mark])
+
+
+# ------------------------------------------------------------------ the range of stored keys
+
+def attend64(w, k, v, q):
+    """The definition in float64 on given rows [n][heads][256] (stored order) -> (out, lse, max of scale sum |q||k|)."""
+    out, lse, at, most = np.zeros(w.q.shape), np.zeros(w.q.shape[:3]), 0, 0.0
+    t = w.n_qtok
+    for s, n in enumerate(w.seq_lens.tolist()):
+        for h in range(24):
+            kh, vh = k[at:at + n, h // 6], v[at:at + n, h // 6]
+            for i in range(t):
+                m = n - t + 1 + i
+                z = w.scale * (kh[:m] @ q[s, i, h])
+                most = max(most, w.scale * (np.abs(kh[:m]) @ np.abs(q[s, i, h])).max())
+                p = np.exp(z - z.max())
+                lse[s, i, h] = z.max() + np.log(p.sum())
+                out[s, i, h] = p @ vh[:m] / p.sum()
+        at += n
+    return out, lse, most
+
+
+def wide_keys(w, kt, every, seed):
+    """w with K rows encoded anew: dims 64 .. 95 of every `every`-th row are about 5 * 10^4 N(0, 1) (past binary16's range, in scales within it), with
+    queries of about 10^-5 there, so that the logits stay ordinary."""
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((len(w.k_rows), 4, 256)).astype(np.float32)
+    pos = np.concatenate([np.arange(n) for n in w.seq_lens])
+    x = x[np.minimum(pos, len(x) - 1)]  # rows by position: the prefix's copies are alike
+    x[pos % every == 0, :, 64:96] *= np.float32(5e4)
+    q = w.q.copy()
+    q[..., 64:96] *= np.float32(1e-5)
+    return W.Workload(w.name, w.seq_lens, w.n_qtok, w.page_size, w.n_blocks, kt, w.v_type, w.table, W.encode_rows(x, kt), w.v_rows, q, w.scale)
+
+
+@pytest.mark.parametrize("kt", [Q8, Q4])
+@pytest.mark.parametrize("t", [1, 4])
+@pytest.mark.parametrize("every", [1, 7, 901])
+def test_keys_past_binary16(kt, t, every):
+    """Scale * quant past 65504: finite in the pool, and the product with a small
+    query an ordinary logit -- every key so, some of them, a few."""
+    w, gs, pl = prefix_workload([(3, 1500), (1, 20)], [200, 40, 1000, 30], 16, kt, Q8, n_qtok=t)
+    w = wide_keys(w, kt, every, seed=t)
+    q = to_dev(w.q).half()
+    out, lse = decode(w, gs, pl, q)
+    k, v = oracle.dequant_rows(w.k_rows, kt), oracle.dequant_rows(w.v_rows, Q8)
+    assert np.abs(k).max() > 65504
+    want, want_lse, _ = attend64(w, k, v, q.double().cpu().numpy())
+    assert_close(out.cpu().numpy(), want)
+    assert_lse_close(lse.cpu().numpy(), want_lse)
+
+
+def test_wide_keys_leave_the_others_alone():
+    """A sequence with such keys in a batch changes no bit of the other sequences."""
+    w, gs, pl = prefix_workload([(2, 700), (3, 500)], [100, 40, 300, 30, 60], 16, Q8, Q8)
+    q = to_dev(w.q).half()
+    want, want_lse = decode(w, gs, pl, q)
+    k = w.k_rows.copy().reshape(len(w.k_rows), 4, 8, 34)
+    at = int(w.seq_lens[:4].sum()) + 520  # the fifth sequence's own row
+    k[at, :, 3, :2] = np.array([3000.0], np.float16).view(np.uint8)
+    bad = W.Workload(w.name, w.seq_lens, 1, 16, w.n_blocks, Q8, Q8, w.table, k.reshape(w.k_rows.shape), w.v_rows, w.q, w.scale)
+    out, lse = decode(bad, gs, pl, q)
+    assert torch.equal(out[:4], want[:4]) and torch.equal(lse[:4], want_lse[:4])
+    kd, vd = oracle.dequant_rows(bad.k_rows, Q8), oracle.dequant_rows(w.v_rows, Q8)
+    ref, ref_lse, _ = attend64(bad, kd, vd, q.double().cpu().numpy())
+    # the key's logits are tens of thousands: a row sees it alone or not at all (2^-11 of |q||k| scale is some tens)
+    z = np.abs(np.einsum("hgd,hd->hg", q[4, 0].double().cpu().numpy().reshape(4, 6, 256), kd[at]).reshape(24)) / 16
+    sharp = z > 500
+    assert sharp.sum() > 20
+    assert_close(out.cpu().numpy()[4, 0][sharp], ref[4, 0][sharp])
+    assert (np.abs(lse.cpu().numpy() - ref_lse)[4, 0] <= 2.0 ** -11 * 16 * z + 0.01).all()
