@@ -442,7 +442,8 @@ pa_status pa_decode_noalloc(const pa_pool* pool, const float* q, const void* k_p
  *           binary16, as in pa_decode; quantised K (scale * quant) is too, so a
  *           logit is off by about 2^-12 |q| |k| scale at most.
  *           A row whose logits are not all numbers (a NaN in its query or in a key
- *           that it sees) is NaN, its lse too.
+ *           that it sees) is NaN, its lse too; so is one of fp32 or bfloat16 with a
+ *           value that rounds past binary16's 65504.
  * prefix_lens: at most seq_lens_host - n_qtok of every sequence of the group
  *           (PA_ERR_INVALID otherwise): the new tokens are each sequence's own.
  * workspace: ws_bytes >= pa_decode_prefix_workspace_size(), 256-byte aligned.

@@ -337,6 +337,12 @@ __device__ __forceinline__ void tmem_st_frag1(uint32_t a, const uint32_t (&r)[4]
 constexpr uint32_t kM1152 = pa_split::kHalf2_m1152, kM1032 = pa_split::kHalf2_m1032, kR16 = pa_split::kHalf2_1_16,
                    kM72 = pa_split::kHalf2_m72, kMagic = pa_split::kMagic64, kR256 = 0x1c001c00u;  // 2^-8 twice
 
+// The larger of two pairs of binary16 numbers, by magnitude.
+__device__ __forceinline__ uint32_t larger2(uint32_t x, uint32_t y) {
+  const __half2 m = __hmax2(__habs2(*reinterpret_cast<const __half2*>(&x)), __habs2(*reinterpret_cast<const __half2*>(&y)));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
 // This thread's key, dims 128 kd .. + 127, from raw shared memory into a K
 // unit's 64 columns at taddr, 32 dims (16 columns) at a time.  grp: the key's row
 // group, r its row there.  Returns the warp's wide keys (lane = bit): those with a
@@ -352,12 +358,8 @@ __device__ __forceinline__ uint32_t dequant_k(uint32_t grp, int r, int kd, uint3
   if constexpr (T != PA_F16) {
     const uint4 d = lds128(grp + 16 * r);  // the row's eight block scales
     sc = kd ? make_uint2(d.z, d.w) : make_uint2(d.x, d.y);
-    auto larger = [](uint32_t x, uint32_t y) {  // of two pairs of scales, by magnitude
-      const __half2 m = __hmax2(__habs2(*reinterpret_cast<const __half2*>(&x)), __habs2(*reinterpret_cast<const __half2*>(&y)));
-      return *reinterpret_cast<const uint32_t*>(&m);
-    };
     // 2^9 (Q4_0: 2^13) is 0x6000 (0x7000): from there on the sum has bit 15
-    const bool mine = (larger(larger(d.x, d.y), larger(d.z, d.w)) + (T == PA_Q8_0 ? 0x20002000u : 0x10001000u)) & 0x80008000u;
+    const bool mine = (larger2(larger2(d.x, d.y), larger2(d.z, d.w)) + (T == PA_Q8_0 ? 0x20002000u : 0x10001000u)) & 0x80008000u;
     if (__any_sync(0xffffffffu, mine)) {
       wide = __ballot_sync(0xffffffffu, mine);
       if (mine) sc = make_uint2(hmul2(sc.x, kR256), hmul2(sc.y, kR256));
@@ -530,6 +532,14 @@ __device__ __forceinline__ uint4 q_slot(uint4 v) {  // Q4_0: the order of dequan
   return make_uint4(prmt(v.x, v.y, 0x5410), prmt(v.x, v.y, 0x7632), prmt(v.z, v.w, 0x5410), prmt(v.z, v.w, 0x7632));
 }
 
+// Of a row of converted queries: top, the largest of this lane's values.  If one came out
+// infinite the row gets a NaN (at its slot to): an infinite logit of either sign would
+// pass for a key unseen or weigh alone.
+__device__ __forceinline__ void q_range(uint32_t top, uint32_t to) {
+  if ((top + 0x04000400u) & 0x80008000u)  // an exponent of all ones carries into bit 15
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"((unsigned short)0x7fff) : "memory");
+}
+
 template <int KT>
 __device__ __forceinline__ void stage_q_begin(const Params& p, const Tile& t, uint32_t dst, int r8, int lane) {
   const int row = r8 + (lane & 7), rg = t.row0 + row, rows = t.info & 0xff;
@@ -542,13 +552,16 @@ __device__ __forceinline__ void stage_q_begin(const Params& p, const Tile& t, ui
   const long long at = ((long long)(t.token + rg / kGqa) * p.n_q_heads + t.head * kGqa + rg % kGqa) * kD;
   if (p.q_type == PA_DT_F32) {
     const float* src = reinterpret_cast<const float*>(p.q) + at;
+    uint32_t top = 0;
 #pragma unroll 2
     for (int i = 0; i < 8; ++i) {
       const float4 x = *reinterpret_cast<const float4*>(src + q_dim<KT>((lane >> 3) + 4 * i, 0)),
                    y = *reinterpret_cast<const float4*>(src + q_dim<KT>((lane >> 3) + 4 * i, 1));
-      sts128(to + 512 * i,
-             q_slot<KT>(make_uint4(pack_half2(x.x, x.y), pack_half2(x.z, x.w), pack_half2(y.x, y.y), pack_half2(y.z, y.w))));
+      const uint4 v = make_uint4(pack_half2(x.x, x.y), pack_half2(x.z, x.w), pack_half2(y.x, y.y), pack_half2(y.z, y.w));
+      top = larger2(larger2(larger2(top, v.x), v.y), larger2(v.z, v.w));
+      sts128(to + 512 * i, q_slot<KT>(v));
     }
+    q_range(top, to);
   } else {
     const uint8_t* src = p.q + 2 * at;
 #pragma unroll 2
@@ -573,6 +586,7 @@ __device__ __forceinline__ void stage_q_end(const Params& p, uint32_t dst, int r
   const bool bf16 = p.q_type == PA_DT_BF16;
   if (p.q_type == PA_DT_F32 || (KT != PA_Q4_0 && !bf16)) return;
   const uint32_t to = dst + canon(r8 + (lane & 7), lane >> 3, kD / 8);
+  uint32_t top = 0;
 #pragma unroll 2
   for (int i = 0; i < 8; ++i) {
     uint4 v = lds128(to + 512 * i);
@@ -581,9 +595,11 @@ __device__ __forceinline__ void stage_q_end(const Params& p, uint32_t dst, int r
 #pragma unroll
       for (int k = 0; k < 4; ++k) u[k] = pack_half2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
       v = make_uint4(u[0], u[1], u[2], u[3]);
+      top = larger2(larger2(larger2(top, v.x), v.y), larger2(v.z, v.w));
     }
     sts128(to + 512 * i, q_slot<KT>(v));
   }
+  if (bf16) q_range(top, to);
 }
 
 // ------------------------------------------------------------------ the roles' common parts

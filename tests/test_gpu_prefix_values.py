@@ -131,3 +131,37 @@ def test_wide_keys_leave_the_others_alone():
     assert sharp.sum() > 20
     assert_close(out.cpu().numpy()[4, 0][sharp], ref[4, 0][sharp])
     assert (np.abs(lse.cpu().numpy() - ref_lse)[4, 0] <= 2.0 ** -11 * 16 * z + 0.01).all()
+
+
+# ------------------------------------------------------------------ the range of queries
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("value", [1e5, -3e38, 65536.0])
+@pytest.mark.parametrize("kt", [F16, Q4])
+def test_queries_past_binary16_are_not_a_number(dtype, value, kt):
+    """A finite query value that binary16 has no number for makes its row NaN, whatever
+    the keys' signs; the other rows stay as they are."""
+    w, gs, pl = prefix_workload([(4, 2000), (1, 30)], [40, 50, 30, 400, 20], 16, kt, Q8)
+    if kt == F16:  # all of a dim's keys of one sign: every logit would be -inf or inf
+        k = np.ascontiguousarray(w.k_rows).view(np.float16).copy()
+        k[..., 9] = np.abs(k[..., 9]) + np.float16(0.125)
+        w = W.Workload(w.name, w.seq_lens, 1, 16, w.n_blocks, kt, Q8, w.table, k.view(np.uint8), w.v_rows, w.q, w.scale)
+    q = to_dev(w.q).to(dtype)
+    want, want_lse = decode(w, gs, pl, q)
+    q[2, 0, 23, 9] = value
+    out, lse = decode(w, gs, pl, q)
+    mark = torch.zeros(5, 1, 24, dtype=torch.bool, device="cuda")
+    mark[2, 0, 23] = True
+    assert out[mark].isnan().all() and lse[mark].isnan().all()
+    assert torch.equal(out[~mark], want[~mark]) and torch.equal(lse[~mark], want_lse[~mark])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_largest_queries(dtype):
+    """Just inside the range (65280 has a bfloat16): an ordinary row."""
+    w, gs, pl = prefix_workload([(3, 600)], [40, 50, 30], 16, Q8, Q8)
+    q = to_dev(w.q).to(dtype)
+    q[1, 0, 5, :] = 0
+    q[1, 0, 5, 200] = 65280.0
+    out, lse = decode(w, gs, pl, q)
+    assert out.isfinite().all() and lse.isfinite().all()
