@@ -183,6 +183,11 @@ __device__ __forceinline__ void cos_sin(uint32_t phase, float* c, float* s) {
   *s = __uint_as_float(__float_as_uint(y) ^ ((quarter & 2) << 30));
 }
 
+// Values from rot_dim on have no partner: theirs is read as a zero and their sine is one
+// of the other sign, so that x c + partner s is x c - 0, which is x c for infinities and
+// zeros of either sign too.  Whole lanes are turned or not (rot_dim is a multiple of 16).
+__device__ __forceinline__ bool is_turned(const RopeParams& p, int lane) { return 8 * lane < p.rot; }
+
 // The lane that holds the partners of this lane's values (itself when they are
 // its own, or when there is nothing to turn).
 __device__ __forceinline__ int partner_lane(const RopeParams& p, int lane) {
@@ -194,7 +199,7 @@ __device__ __forceinline__ int partner_lane(const RopeParams& p, int lane) {
 // the eight that it shares with its partner lane.
 __device__ __forceinline__ Turn make_turn(const RopeParams& p, const uint64_t* turns, int pos, int lane, int from) {
   float c[8], s[8];
-  const bool turned = 8 * lane < p.rot, second = from < lane;
+  const bool turned = is_turned(p, lane), second = from < lane;
   float ac[4], as[4];
   const int pair0 = p.interleaved ? 4 * lane : second ? 8 * from + 4 : 8 * lane;
 #pragma unroll
@@ -212,7 +217,7 @@ __device__ __forceinline__ Turn make_turn(const RopeParams& p, const uint64_t* t
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       c[i] = ac[i >> 1];
-      s[i] = (i & 1) ? as[i >> 1] : -as[i >> 1];  // the first of a pair takes -sin
+      s[i] = (i & 1) ? as[i >> 1] : -as[i >> 1];  // the first of a pair takes -sin; not turned: -0, +0
     }
   } else {
 #pragma unroll
@@ -245,7 +250,10 @@ __device__ __forceinline__ Turn weighted(const RopeParams& p, const Turn& t, con
   for (int i = 0; i < 8; ++i) x[i] += p.w_offset;
   float o[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = p.interleaved ? x[i ^ 1] : __shfl_sync(0xffffffffu, x[i], from);
+  for (int i = 0; i < 8; ++i) {
+    o[i] = p.interleaved ? x[i ^ 1] : __shfl_sync(0xffffffffu, x[i], from);
+    if (!is_turned(p, lane)) o[i] = 1.f;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     r.c[i] = mul2(t.c[i], pack2(x[2 * i], x[2 * i + 1]));
@@ -269,6 +277,12 @@ struct Raw {
     for (int i = 0; i < (int)sizeof(T) / 2; ++i)
       r.v[i] = make_uint4(__shfl_sync(0xffffffffu, v[i].x, l), __shfl_sync(0xffffffffu, v[i].y, l),
                           __shfl_sync(0xffffffffu, v[i].z, l), __shfl_sync(0xffffffffu, v[i].w, l));
+    return r;
+  }
+  __device__ __forceinline__ Raw masked(uint32_t m) const {
+    Raw r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = make_uint4(v[i].x & m, v[i].y & m, v[i].z & m, v[i].w & m);
     return r;
   }
   __device__ __forceinline__ void get(float (&x)[8]) const { unpack8<T>(v, x); }
@@ -302,19 +316,22 @@ __device__ __forceinline__ void inverse_norms(const RopeParams& p, const Raw<T> 
   for (int k = 0; k < N; ++k) r[k] = rsqrtf(r[k] * (1.f / kD) + p.eps);
 }
 
-// y = r (x c + partner s), the weights inside c and s.
+// y = r (x c + partner s), the weights inside c and s; mask: all ones in a lane that is
+// turned, else 0.
 template <typename T>
-__device__ __forceinline__ void turn_head(const RopeParams& p, const Raw<T>& raw, const Turn& t, float r, int from, float (&y)[8]) {
+__device__ __forceinline__ void turn_head(const RopeParams& p, const Raw<T>& raw, const Turn& t, float r, int from, uint32_t mask,
+                                          float (&y)[8]) {
   uint64_t x[4], o[4];
   raw.get(x);
   if (p.interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 v = unpack2(x[i]);
-      o[i] = pack2(v.y, v.x);
+      o[i] = pack2(__uint_as_float(__float_as_uint(v.y) & mask),
+                   __uint_as_float((__float_as_uint(v.x) & mask) | (~mask & 0x80000000u)));
     }
   } else {
-    raw.from_lane(from).get(o);
+    raw.from_lane(from).masked(mask).get(o);
   }
   const uint64_t rr = pack2(r, r);
 #pragma unroll
@@ -350,6 +367,7 @@ __global__ void __launch_bounds__(32 * kWarps, kAppend ? 5 : 7) pa_rope_kernel(c
   const int chunk = (int)(item - row * p.chunks);
   const int h0 = chunk * p.per, h1 = min(h0 + p.per, p.hq + p.hk + p.hv);
   const int pos = __ldg(p.row_pos + row), from = partner_lane(p, lane);
+  const uint32_t mask = is_turned(p, lane) ? ~0u : 0u;
   if (p.per > kBatch) {  // many rows: the first heads are on their way before the position is known
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -389,7 +407,7 @@ __global__ void __launch_bounds__(32 * kWarps, kAppend ? 5 : 7) pa_rope_kernel(c
       if (norm) inverse_norms<In, N>(p, raw, r);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        if (t) turn_head<In>(p, raw[i], *t, r[i], from, y);
+        if (t) turn_head<In>(p, raw[i], *t, r[i], from, mask, y);
         else raw[i].get(y);
         put(a + i, y);
       }
