@@ -19,7 +19,8 @@ class PagedKVCache:
     def __init__(self, n_blocks: int, page_size: int, k_type: int, v_type: int | None = None,
                  n_kv_heads: int = 4, head_dim: int = 256, device: torch.device | str = "cuda",
                  k_pool: torch.Tensor | None = None, v_pool: torch.Tensor | None = None):
-        """k_pool, v_pool: pools that exist already (uint8, the pool's bytes), else zeroed ones are made."""
+        """k_pool, v_pool: pools that exist already (uint8 on the cache's device, the pool's bytes, 16-byte aligned),
+        else zeroed ones are made."""
         load()
         self._calls = load_calls()
         self.device = torch.device(device)
@@ -42,7 +43,13 @@ class PagedKVCache:
             return torch.zeros(n, dtype=torch.uint8, device=self.device)
         if given.dtype != torch.uint8 or given.numel() != n or not given.is_contiguous():
             raise PaError(PA_ERR_INVALID, f"pool buffer: uint8, {n} bytes")
+        # the calls pass its address on to kernels
+        if not given.is_cuda or given.device.index != self._device_index() or given.data_ptr() % 16:
+            raise PaError(PA_ERR_INVALID, f"pool buffer: on {self.device}, 16-byte aligned")
         return given
+
+    def _device_index(self) -> int:
+        return self.device.index if self.device.index is not None else torch.cuda.current_device()
 
     # ------------------------------------------------------------ append
     def append(self, k_rows: torch.Tensor, v_rows: torch.Tensor, row_seq: torch.Tensor, row_pos: torch.Tensor,
@@ -85,7 +92,7 @@ class PagedKVCache:
 
     # ------------------------------------------------------------ decode
     def workspace(self, n_seq: int, n_qtok: int) -> torch.Tensor:
-        dev = self.device.index if self.device.index is not None else torch.cuda.current_device()
+        dev = self._device_index()
         key = (n_seq, n_qtok, dev)
         if self._ws is None or self._ws_key != key:
             nbytes = pa_decode_workspace_size(self.pool, n_seq, n_qtok, dev)
