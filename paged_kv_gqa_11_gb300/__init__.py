@@ -129,6 +129,8 @@ def load_calls():
     """The Python module over the calls that run once per layer and step
     (csrc/pa_calls.cpp); raises if it has not been built (no fallback)."""
     global _calls
+    if _calls is not None:
+        return _calls
     load()
     with _lock:
         if _calls is None:

@@ -24,8 +24,11 @@ class Rope:
             raise PaError(PA_ERR_INVALID, "Rope: at most 128 pairs")
         self.desc = RopeDesc(2 * len(f), int(bool(interleaved)), eps, weight_offset, attn_factor,
                              (C.c_double * 128)(*f))
-        self.address = C.addressof(self.desc)
-        self._norm_rope = load_calls().norm_rope
+
+    @property
+    def address(self) -> int:
+        """Of the constants, as the calls take them: in a copy, of the copy's own."""
+        return C.addressof(self.desc)
 
     @classmethod
     def from_theta(cls, rot_dim: int, theta: float, **kw) -> "Rope":
@@ -40,4 +43,4 @@ class Rope:
         of one projection are fine), normalised where a weight is given and
         rotated to row_pos (int32 [n]).  Returns (q_out, k_out), of out_dtype (by
         default the inputs' type); an output may be its input."""
-        return self._norm_rope(self.address, q, k, row_pos, q_weight, k_weight, q_out, k_out, out_dtype, stream)
+        return load_calls().norm_rope(self.address, q, k, row_pos, q_weight, k_weight, q_out, k_out, out_dtype, stream)
