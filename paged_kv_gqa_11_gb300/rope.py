@@ -32,7 +32,9 @@ class Rope:
 
     @classmethod
     def from_theta(cls, rot_dim: int, theta: float, **kw) -> "Rope":
-        """The usual frequencies theta^(-2 i / rot_dim)."""
+        """The usual frequencies theta^(-2 i / rot_dim); rot_dim is even, 0 to 256."""
+        if rot_dim % 2 or not 0 <= rot_dim <= 256:
+            raise PaError(PA_ERR_INVALID, "Rope: rot_dim is even, 0 to 256")
         return cls([float(theta) ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)], **kw)
 
     def apply(self, q: torch.Tensor | None, k: torch.Tensor | None, row_pos: torch.Tensor,

@@ -6,7 +6,8 @@ import pickle
 
 import pytest
 
-from paged_kv_gqa_11_gb300 import RopeDesc, _build
+import paged_kv_gqa_11_gb300 as pa
+from paged_kv_gqa_11_gb300 import PaError, RopeDesc, _build
 from paged_kv_gqa_11_gb300.rope import Rope
 
 
@@ -40,3 +41,9 @@ def test_a_copy_is_changed_alone():
     b.desc.eps = 0.5
     assert constants(b.address)[2] == 0.5 and constants(a.address)[2] != 0.5
 
+
+@pytest.mark.parametrize("rot_dim", [-2, 1, 33, 65, 257, 258])
+def test_widths_that_no_pairs_fill_are_refused(rot_dim):
+    with pytest.raises(PaError) as e:
+        Rope.from_theta(rot_dim, 1e6)
+    assert e.value.status == pa.PA_ERR_INVALID
