@@ -22,7 +22,6 @@ class PagedKVCache:
         """k_pool, v_pool: pools that exist already (uint8 on the cache's device, the pool's bytes, 16-byte aligned),
         else zeroed ones are made."""
         load()
-        self._calls = load_calls()
         self.device = torch.device(device)
         self.pool = Pool(n_blocks, page_size, n_kv_heads, head_dim, k_type, v_type)
         self.page_size = page_size
@@ -76,7 +75,7 @@ class PagedKVCache:
         normalised (with a weight), rotated to row_pos and stored, values stored;
         returns the queries, normalised and rotated, as q_dtype (default:
         q's own)."""
-        return self._calls.append_rope(self.pool.address, self.n_kv_heads, self.k_pool, self.v_pool, rope.address, k, v,
+        return load_calls().append_rope(self.pool.address, self.n_kv_heads, self.k_pool, self.v_pool, rope.address, k, v,
                                        row_seq, row_pos, block_table, k_weight, q, q_weight, q_out, q_dtype, self.err,
                                        stream)
 
@@ -87,7 +86,7 @@ class PagedKVCache:
         """The cache's rows at (row_seq, row_pos) as values [n][n_kv_heads][256];
         returns (k, v).  With only one of k_out, v_out given, only that one is
         read."""
-        return self._calls.read_rows(self.pool.address, self.n_kv_heads, self.k_pool, self.v_pool, row_seq, row_pos,
+        return load_calls().read_rows(self.pool.address, self.n_kv_heads, self.k_pool, self.v_pool, row_seq, row_pos,
                                      block_table, dtype, k_out, v_out, self.err, stream)
 
     # ------------------------------------------------------------ decode
@@ -130,7 +129,7 @@ class PagedKVCache:
         The workspace is taken from torch's allocator for each call, so calls on
         several streams, and captured ones, each have their own.  Returns
         (out, lse)."""
-        return self._calls.decode_prefix(self.pool.address, q, self.k_pool, self.v_pool, block_table, seq_lens_dev,
+        return load_calls().decode_prefix(self.pool.address, q, self.k_pool, self.v_pool, block_table, seq_lens_dev,
                                          seq_lens_host, group_sizes, prefix_lens, n_qtok, scale, out, lse, want_lse,
                                          workspace, self.err, stream)
 
