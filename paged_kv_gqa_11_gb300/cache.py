@@ -70,7 +70,8 @@ class PagedKVCache:
                     block_table: torch.Tensor, k_weight: torch.Tensor | None = None, q: torch.Tensor | None = None,
                     q_weight: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
                     q_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor | None:
-        """Rows straight from a projection: k and v [n][n_kv_heads][256], and if
+        """Rows straight from a projection (stream, here and in read_rows and
+        decode_prefix: as in Rope.apply): k and v [n][n_kv_heads][256], and if
         given q [n][heads][256] (parts of one tensor are fine).  Keys are
         normalised (with a weight), rotated to row_pos and stored, values stored;
         returns the queries, normalised and rotated, as q_dtype (default:

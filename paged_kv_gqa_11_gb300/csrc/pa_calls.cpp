@@ -11,15 +11,19 @@
 //
 // Nothing is kept from one call for the next.  Memory that a call needs comes
 // from torch's allocator on the stream that the call runs on, so calls on several
-// streams, and captured ones, each have their own.
+// streams, and captured ones, each have their own.  What stands on a stream passed in
+// is ordered there: the caller lets it wait for what makes the arguments, and waits for
+// it before using the results elsewhere.
 #include <Python.h>
 
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ATen.h>
 
+#include <initializer_list>
 #include <optional>
 #include <string>
 
@@ -98,6 +102,7 @@ void* ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 struct Place {
   std::optional<c10::cuda::CUDAGuard> device;
   std::optional<c10::cuda::CUDAStreamGuard> stream_guard;
+  std::optional<c10::cuda::CUDAStream> other, current;  // a stream passed in that is not the current one, and that
   pa_stream_t stream;
 
   Place(int dev, PyObject* s) {
@@ -121,7 +126,28 @@ struct Place {
       refuse("stream: a torch stream or its address");
     }
     stream = reinterpret_cast<pa_stream_t>(v);
-    stream_guard.emplace(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(v), static_cast<c10::DeviceIndex>(dev)));
+    const auto device_index = static_cast<c10::DeviceIndex>(dev);
+    const auto passed = c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(v), device_index);
+    const auto now = c10::cuda::getCurrentCUDAStream(device_index);
+    if (passed.stream() != now.stream()) {
+      other = passed;
+      current = now;
+    }
+    stream_guard.emplace(passed);
+  }
+
+  // Tensors that the call reads or writes: torch's allocator gives their memory out again
+  // only after what is on the stream by then.
+  void uses(std::initializer_list<const at::Tensor*> tensors) const {
+    if (!other) return;
+    for (const at::Tensor* t : tensors)
+      if (t->defined()) c10::cuda::CUDACachingAllocator::recordStream(t->storage().data_ptr(), *other);
+  }
+
+  // A result made on the stream passed in, which the caller will use on the current one.
+  const at::Tensor& made(const at::Tensor& t) const {
+    if (other) c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), *current);
+    return t;
   }
 };
 
@@ -199,8 +225,9 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const auto want = dtype_arg(a[8]);
     const at::ScalarType type = want ? *want : qo.defined() ? qo.scalar_type() : ko.defined() ? ko.scalar_type() : some.scalar_type();
     const Place place(dev, a[9]);
-    if (q.defined() && !qo.defined()) qo = like(q, type);
-    if (k.defined() && !ko.defined()) ko = like(k, type);
+    place.uses({&q, &k, &pos, &wq, &wk, &qo, &ko});
+    if (q.defined() && !qo.defined()) qo = place.made(like(q, type));
+    if (k.defined() && !ko.defined()) ko = place.made(like(k, type));
     int64_t s[4] = {0, 0, 0, 0}, h[2] = {0, 0};
     const at::Tensor *in[2] = {&q, &k}, *out[2] = {&qo, &ko};
     for (int i = 0; i < 2; ++i) {
@@ -245,10 +272,11 @@ PyObject* append_rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     on(dev, table, "block_table"); on(dev, wk, "k_weight"); on(dev, q, "q"); on(dev, wq, "q_weight"); on(dev, qo, "q_out"); on(dev, err, "err");
     const auto want = dtype_arg(a[14]);
     const Place place(dev, a[16]);
+    place.uses({&kp, &vp, &k, &v, &seq, &pos, &table, &wk, &q, &wq, &qo, &err});
     int64_t qs = 0, qos = 0, hq = 0;
     if (q.defined()) {
       check(q.dim() == 3 && q.size(0) == n && q.scalar_type() == k.scalar_type(), "q of k's type and row count");
-      if (!qo.defined()) qo = like(q, want ? *want : q.scalar_type());
+      if (!qo.defined()) qo = place.made(like(q, want ? *want : q.scalar_type()));
       same_shape(q, qo, "q_out of q's shape");
       check(!want || qo.scalar_type() == *want, "q_out of q_dtype");
       qs = row_stride(q, "q");
@@ -286,10 +314,11 @@ PyObject* read_rows(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     on(dev, ko, "k_out"); on(dev, vo, "v_out"); on(dev, err, "err");
     const auto want = dtype_arg(a[7]);
     const Place place(dev, a[11]);
+    place.uses({&kp, &vp, &seq, &pos, &table, &ko, &vo, &err});
     if (!ko.defined() && !vo.defined()) {
       const auto opt = kp.options().dtype(want ? *want : at::kHalf);
-      ko = at::empty({n, heads, kD}, opt);
-      vo = at::empty({n, heads, kD}, opt);
+      ko = place.made(at::empty({n, heads, kD}, opt));
+      vo = place.made(at::empty({n, heads, kD}, opt));
     }
     const at::Tensor& some = ko.defined() ? ko : vo;
     for (const at::Tensor* x : {&ko, &vo})
@@ -348,8 +377,9 @@ PyObject* decode_prefix(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     on(dev, lse, "lse"); on(dev, ws, "workspace"); on(dev, err, "err");
     check(n <= UINT32_MAX && g <= UINT32_MAX && t <= UINT32_MAX && hq <= UINT32_MAX && table.size(1) <= INT32_MAX, "sizes");
     const Place place(dev, a[16]);
-    if (!out.defined()) out = like(q, q.scalar_type());
-    if (!lse.defined() && PyObject_IsTrue(a[13]) == 1) lse = at::empty({n, t, hq}, q.options().dtype(at::kFloat));
+    place.uses({&q, &kp, &vp, &table, &lens_dev, &out, &lse, &ws, &err});
+    if (!out.defined()) out = place.made(like(q, q.scalar_type()));
+    if (!lse.defined() && PyObject_IsTrue(a[13]) == 1) lse = place.made(at::empty({n, t, hq}, q.options().dtype(at::kFloat)));
     same_shape(q, out, "out of q's shape");
     check(out.is_contiguous(), "out: contiguous");
     check(!lse.defined() || (lse.scalar_type() == at::kFloat && lse.is_contiguous() && lse.dim() == 3 && lse.size(0) == n && lse.size(1) == t &&

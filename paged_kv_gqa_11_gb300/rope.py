@@ -44,5 +44,8 @@ class Rope:
         """q [n][heads][256] and k [n][kv heads][256] (either may be None; parts
         of one projection are fine), normalised where a weight is given and
         rotated to row_pos (int32 [n]).  Returns (q_out, k_out), of out_dtype (by
-        default the inputs' type); an output may be its input."""
+        default the inputs' type); an output may be its input.  stream: the
+        current one, unless given; the caller orders a given one after what makes
+        the arguments and before what uses the results, and may drop its tensors
+        once the call returns."""
         return load_calls().norm_rope(self.address, q, k, row_pos, q_weight, k_weight, q_out, k_out, out_dtype, stream)
