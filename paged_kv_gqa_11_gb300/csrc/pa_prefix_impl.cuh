@@ -731,6 +731,7 @@ __device__ __forceinline__ int copy_role(const Params& p, Pos pos, int n, bool i
       fence_proxy_async_smem();
       __syncwarp();
     }
+    __syncwarp();  // the tile's record, written by lane 0, comes before lane 4's arrival too
     if (lane == 0 || lane == 4) mbar_arrive_expect_tx(fb, __popc(good & (0xfu << lane)) * gb);
     __syncwarp();
     if (ok)
