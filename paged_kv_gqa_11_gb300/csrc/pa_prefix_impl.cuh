@@ -263,7 +263,7 @@ struct Smem {
   // K and V raw full / empty [stages], K and V unit full / empty [2], s full / empty [2], q full / empty [2],
   // p full, pv done, o free [2] each, drain [2], sink
   static constexpr int kNBar = 2 * (kKStages + kVStages) + 8 + 4 + 4 + 9;
-  static constexpr int kMisc = kBar + 8 * kNBar;  // abort, tmem base, the first tile's place
+  static constexpr int kMisc = kBar + 8 * kNBar;  // abort, tmem base, the softmax's leave, the first tile's place
   static constexpr int kTotal = kMisc + 16 + sizeof(Pos) + 12;
   static constexpr int kLaunch = kTotal + 1024;  // the base is aligned to 1024 inside
   static_assert(kTotal - kBar <= 640 && kLaunch <= 232448, "shared memory");
@@ -805,7 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
                  q_full = s_empty + 16, q_empty = q_full + 16, p_full = q_empty + 16, pv_done = p_full + 16,
                  o_free = pv_done + 16, drain = o_free + 16, sink = drain + 16;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + SM::kMisc);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc + 8);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc + 4);
+  volatile int* leave = reinterpret_cast<volatile int*>(smem + SM::kMisc + 8);  // of even, odd tiles
   Pos* start = reinterpret_cast<Pos*>(smem + SM::kMisc + 16);
   int* tiles_at = reinterpret_cast<int*>(smem + SM::kMisc + 16 + sizeof(Pos));  // the CTA's first tile, the next CTA's
   Tile* opening = reinterpret_cast<Tile*>(smem + SM::kOpening);                 // of the first tile, what its query rows need
@@ -815,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
   // deep: K(j + 4) follows S^T(j + 3), and that the end of softmax(j + 1)
   uint32_t* wide_keys = reinterpret_cast<uint32_t*>(smem + SM::kWide);
   if (tid == 0) {
-    *abort = 0;
+    *abort = leave[0] = leave[1] = 0;
     for (int i = 0; i < NK; ++i) {
       mbar_init(kraw_full + 8 * i, 1);
       mbar_init(kraw_empty + 8 * i, 4);
@@ -1038,7 +1039,11 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     const uint32_t p_addr = base + SM::kP + canon(8 * (lane >> 4) + (lane & 7), 4 * quarter + 2 * hh + ((lane >> 3) & 1), kKeys / 8);
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     uint64_t l[4][2] = {};  // sums of weights over this thread's keys: rows (16c + 8e + 2t, + 1)
-    bool live = true;  // a warp whose wait expired keeps to the group's barriers but arrives nowhere
+    // A warp whose wait expired arrives nowhere any more and, before it would read another
+    // tile's record, says so: it sets the tile's `leave` and comes to the barrier at which
+    // the eight warps meet first in every tile, a vote.  After that all of them leave; until
+    // then all walk the same records, and so the same barriers.
+    bool live = true;
     // Logits of 16 rows in log2 units, less their references (none: zero ones).
     // Thread: [8 columns e, key g or g + 8, column 2t or 2t + 1] at 4e + 2k + i.
     auto logits = [&](uint32_t (&x)[8], const int c, const bool refs) {
@@ -1052,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     // S^T is read twice in a first tile (maxima, then weights) and once in others:
     // kept in registers it made them spill.  The rows' sixteens are skipped, not
     // compiled for each number of them.
-    auto tile = [&](const int j, const uint32_t info) {
+    auto tile = [&](const int j, const uint32_t info) -> bool {  // false: one of the warps has given up
       const int nc = ((info & 0xff) + 15) >> 4;  // query rows in sixteens
       const Tile& tl = tiles[j & (kTiles - 1)];
       const bool first_tile = (info >> 8) & 1;
@@ -1090,7 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       uint64_t ls[4][2];
       for (;;) {
         if (raise) {
-          if (j > 0) named_bar_sync(1, kSmThreads);  // the others are done with the shared arrays
+          if (j > 0 && bar_or(1, kSmThreads, false)) return false;  // the others are done with the shared arrays
 #pragma unroll 1
           for (int c = 0; c < nc; ++c) {
             uint32_t x[8];
@@ -1111,7 +1116,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
             }
           }
           __syncwarp();
-          named_bar_sync(1, kSmThreads);
+          if (bar_or(1, kSmThreads, false)) return false;  // the first meeting of tile 0
           if (st < 16 * nc) {
             float v = red[st];
 #pragma unroll
@@ -1166,12 +1171,17 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
             h[2 * e + 1] = pack_half2(b0, b1);
             ls[c][e] = add2(pack2(a0, a1), pack2(b0, b1));
           }
-          if (c == 0 && j > 1) live = live && warp_wait(pv_done + 8 * (j & 1), ((j >> 1) - 1) & 1, p.err, abort);  // of P^T(j - 2)
+          if (c == 0 && j > 1 && live && !warp_wait(pv_done + 8 * (j & 1), ((j >> 1) - 1) & 1, p.err, abort)) {  // of P^T(j - 2)
+            live = false;
+            leave[j & 1] = 1;
+            top = INFINITY;
+          }
           stsm_x4_trans(p_to + c * (16 * kKeys * 2), h[0], h[1], h[2], h[3]);
         }
         if (raise) break;
         raise = bar_or(1, kSmThreads, top > kLazyLog2);
         if (!raise) break;
+        if (leave[j & 1]) return false;
       }
 #pragma unroll
       for (int c = 0; c < 4; ++c)
@@ -1185,12 +1195,18 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
         mbar_arrive(s_empty + 8 * (j & 1));
       }
       __syncwarp();
+      return true;
     };
     for (int j = 0; j <= n; ++j) {
       if (j < n) {
         live = live && warp_wait(s_full + 8 * (j & 1), (j >> 1) & 1, p.err, abort);
+        if (!live) {
+          leave[j & 1] = 1;
+          bar_or(1, kSmThreads, true);
+          break;
+        }
         tc_fence_after();
-        tile(j, tiles[j & (kTiles - 1)].info);
+        if (!tile(j, tiles[j & (kTiles - 1)].info)) break;
       }
       // ---- a piece's O^T, once the weights of the tile after it are on their way
       const Tile& t = tiles[(j - 1) & (kTiles - 1)];
