@@ -958,12 +958,14 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     // an elected lane issues, so that the operands stay in uniform registers: what
     // comes from shared memory goes through a warp reduction, and an expired wait
     // leaves the control flow as it is -- from then on all commits go to a barrier
-    // that nobody waits on.
+    // that nobody waits on, and the MMAs are of 16 rows: the tile's record may not be
+    // there, and a shape that there is none of would be a fault.  (The choice stands
+    // before the reduction; behind it, or on the issuing lane, it costs 4 to 9 per cent.)
     const uint32_t leader = elect_one();
     bool dead = false;
     auto wait = [&](uint32_t bar, uint32_t parity) { dead |= !warp_wait(bar, parity, p.err, abort); };
     auto commit = [&](uint32_t bar) { tc_commit_warp(dead ? sink : bar); };
-    auto info_of = [&](uint32_t j) { return __reduce_or_sync(0xffffffffu, tiles[j & (kTiles - 1)].info); };
+    auto info_of = [&](uint32_t j) { return __reduce_or_sync(0xffffffffu, dead ? 16u : tiles[j & (kTiles - 1)].info); };
     auto idesc_of = [](uint32_t info) { return idesc_f16_f32(128, 0) | (((info & 0xffu) + 15) >> 4 << 18); };
     uint32_t piece = 0;
     if (w == kSWarp) {

@@ -3,7 +3,8 @@
 The roles of pa_prefix_impl.cuh -- copies, conversions, MMA issue, softmax -- run as
 generators over the kernel's barriers, in random order, with random waits expiring and a
 copy that never lands.  Whatever happens, every role comes to its end (a barrier that
-only some of the softmax warps reach would hold a GPU for good), no wait passes a phase
+only some of the softmax warps reach would hold a GPU for good), no MMA goes by a tile
+record that may not be there, no wait passes a phase
 that it does not mean, and a record is not overwritten while a live role needs it."""
 import random
 
@@ -33,8 +34,8 @@ class Bar:
             self.left = self.count
 
 
-def simulate(seed, agree=True):
-    """agree: the softmax warps leave together."""
+def simulate(seed, agree=True, own_shape=True):
+    """agree: the softmax warps leave together; own_shape: after an expired wait MMAs go by no tile's record."""
     rnd = random.Random(seed)
     n, nk, nv = rnd.randint(1, 14), rnd.choice([2, 4, 6, 8, 10]), rnd.choice([2, 4, 6, 8, 10])
     first = [True] + [rnd.random() < 0.35 for _ in range(n)]
@@ -140,8 +141,9 @@ def simulate(seed, agree=True):
                 dead = True
 
         def issue(j, bars_to):
-            if not dead:
+            if not (dead and own_shape):
                 record(j)
+            if not dead:
                 bars_to[0].extend(bars_to[1])
 
         for j in range(n):
@@ -287,7 +289,7 @@ def test_every_role_ends():
     assert 8 < clean < 190  # some runs without an expired wait, many with
 
 
-@pytest.mark.parametrize("without", ["agree"])
+@pytest.mark.parametrize("without", ["agree", "own_shape"])
 def test_the_model_sees_what_each_rule_is_for(without):
     faults = 0
     for seed in range(100):
