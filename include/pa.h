@@ -438,12 +438,18 @@ pa_status pa_decode_noalloc(const pa_pool* pool, const float* q, const void* k_p
  * a prefix length of 0 shares nothing.
  *
  * q, out:   device [n_seq][n_qtok][n_q_heads][head_dim] of q_type / out_type (a
- *           pa_dtype), 16-byte aligned.  Queries of fp32 are rounded to
- *           binary16, as in pa_decode; quantised K (scale * quant) is too, so a
- *           logit is off by about 2^-12 |q| |k| scale at most.
- *           A row whose logits are not all numbers (a NaN in its query or in a key
- *           that it sees) is NaN, its lse too; so is one of fp32 or bfloat16 with a
- *           value that rounds past binary16's 65504.
+ *           pa_dtype), 16-byte aligned.
+ *
+ * Precision and range.  Queries of fp32 and bfloat16 are rounded to binary16 (fp32
+ * as in pa_decode), and so is quantised K (scale * quant), which pa_decode keeps
+ * exact: a logit is off by 2^-11 |q| |k| scale at most for each of the two that is
+ * rounded.  Where that is not small against 1 (logits of hundreds), pa_decode is the
+ * call to make.  V (scale * quant) and the softmax weights are rounded to binary16,
+ * sums are fp32.  Stored keys may be of any size that a pool holds; a stored V value
+ * past 65504 is infinite.  A row with a NaN logit (a NaN in its query or in a key that
+ * it sees) is NaN, its lse too; so is a row with a query value of fp32 or bfloat16
+ * that rounds past 65504.
+ *
  * prefix_lens: at most seq_lens_host - n_qtok of every sequence of the group
  *           (PA_ERR_INVALID otherwise): the new tokens are each sequence's own.
  * workspace: ws_bytes >= pa_decode_prefix_workspace_size(), 256-byte aligned.

@@ -127,6 +127,10 @@ class PagedKVCache:
         fp32, binary16 or bfloat16; out: q's shape, of q's type unless given;
         seq_lens_host, group_sizes, prefix_lens: host arrays of 32-bit whole
         numbers (numpy).
+        Queries and keys are rounded to binary16 (decode keeps quantised keys
+        exact): a logit is off by 2^-11 |q| |k| scale at most for each, so decode
+        is the call for logits of hundreds.  A query value of fp32 or bfloat16
+        past 65504 makes its row NaN, a stored V value past 65504 is infinite.
         The workspace is taken from torch's allocator for each call, so calls on
         several streams, and captured ones, each have their own.  Returns
         (out, lse)."""

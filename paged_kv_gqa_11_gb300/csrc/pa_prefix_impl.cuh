@@ -71,9 +71,9 @@
 //
 // Precision.  Q, K, V (scale * quant, rounded once) and P are binary16, products
 // are accumulated in fp32, m, l and O are fp32, and l sums the weights before
-// their rounding.  Rounding K costs a logit 2^-12 |q| |k| scale at most, the size
-// of the rounding of Q that fp32 queries meet anyway; keeping K exact would take
-// a second product and half again the dequantisation.
+// their rounding.  Rounding K costs a logit 2^-11 |q| |k| scale at most, as much as the
+// rounding of Q that fp32 queries meet anyway; keeping K exact would take a second
+// product and half again the dequantisation.
 #pragma once
 
 #include "pa_decode_impl.cuh"

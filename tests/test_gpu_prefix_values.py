@@ -165,3 +165,83 @@ def test_the_largest_queries(dtype):
     q[1, 0, 5, 200] = 65280.0
     out, lse = decode(w, gs, pl, q)
     assert out.isfinite().all() and lse.isfinite().all()
+
+
+# ------------------------------------------------------------------ precision
+
+def bounds(w, k, v, q, want, key_step):
+    """How far out and lse may lie from `want`, the float64 result on the rows k and v
+    (per element of out; one number for lse).
+
+    Logits: products of binary16 numbers are exact in fp32; the sum over 256 dims is 16
+    steps of 16 dims, each off by 2^-23 of sum |q||k| at most; scale (its conversion to log2
+    units), the difference from the reference and ex2 are off by 2^-21 of the logit and
+    2^-21 -- d below -- and the stored keys' own rounding by key_step * scale sum |q||k|.
+    Weights p e^(+-d), renormalised: off by e^(2 d) - 1 relative.  The weights' rounding
+    (2^-11, or half of 2^-24 for weights below 2^-14, against a sum of 1 at least) and V's
+    (2^-11) come on top."""
+    out, lse, most = want
+    absolute, _, _ = attend64(w, k, np.abs(v), q)
+    d = (2.0 ** -19 + 2.0 ** -21 + key_step) * most + 2.0 ** -21
+    few = w.seq_lens.max() * 2.0 ** -25 * np.abs(v).max()
+    return (np.expm1(2 * d) + 2.0 ** -10 * 1.01) * (absolute + np.abs(out)) + few, d + 2.0 ** -11 + 2.0 ** -22 * np.abs(lse).max()
+
+
+@pytest.mark.parametrize("kt,vt", [(Q8, Q4), (Q4, Q8), (F16, F16)])
+@pytest.mark.parametrize("t", [1, 4])
+def test_large_logits(kt, vt, t):
+    """Logits of standard deviation 16.  Against the keys as they are: within the stated
+    2^-11 |q||k| scale of every logit.  Against the keys rounded to binary16: within the
+    rounding of the rest, so that nothing but the stated rounding is lost."""
+    base = W.stress_workload("bigq", 77, [2000], 16, kt, vt, t)
+    n, rows, pages = 2000, 1008, 125
+    table = np.stack([np.arange(pages), np.concatenate([np.arange(rows // 16), pages + np.arange(pages - rows // 16)])]).astype(np.int32)
+    w = W.Workload("bigq", np.array([n, n], np.int32), t, 16, 2 * pages, kt, vt, table, np.concatenate([base.k_rows] * 2),
+                   np.concatenate([base.v_rows] * 2), np.concatenate([base.q, base.q]), base.scale)
+    out, lse = decode(w, np.array([2], np.uint32), np.array([rows], np.int32), to_dev(w.q).half())
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    k, v = oracle.dequant_rows(w.k_rows, kt), oracle.dequant_rows(w.v_rows, vt)
+    for keys, step in ((k, 0.0 if kt == F16 else 2.0 ** -11), (k.astype(np.float16).astype(np.float64), 0.0)):
+        want = attend64(w, keys, v, w.q.astype(np.float64))
+        b, bl = bounds(w, keys, v, w.q, want, step)
+        assert (np.abs(out - want[0]) <= b).all(), (step, np.max(np.abs(out - want[0]) / b))
+        assert (np.abs(lse - want[1]) <= bl).all(), (step, np.abs(lse - want[1]).max() / bl)
+
+
+def test_the_rounding_of_a_key():
+    """The worst product of a scale and a quant lies 2^-11 (and not 2^-12) of itself from
+    binary16; with all values of a key so, a logit does.  Sequences of one key: lse is the logit."""
+    d = (np.arange(1024, 2048) / 1024.0)[:, None] * np.arange(1.0, 128.0)[None, :]
+    e = (d.astype(np.float16).astype(np.float64) - d) / d
+    i, j = np.unravel_index(np.argmax(np.abs(e)), e.shape)
+    assert 2.0 ** -12 * 1.9 < abs(e[i, j]) <= 2.0 ** -11
+    row = np.zeros((2, 4, 8, 34), np.uint8)
+    row[..., :2] = np.array([(1024 + i) / 1024.0], np.float16).view(np.uint8)
+    row[..., 2:] = j + 1
+    w = W.Workload("one", np.array([1, 1], np.int32), 1, 16, 2, Q8, Q8, np.array([[0], [1]], np.int32), row.reshape(2, 4, 272), row.reshape(2, 4, 272),
+                   np.ones((2, 1, 24, 256), np.float32), 1 / 16)
+    _, lse = decode(w, np.array([2], np.uint32), np.array([0], np.int32), to_dev(w.q).half())
+    logit = 16.0 * d[i, j]
+    off = np.abs(lse.double().cpu().numpy() - logit)
+    assert (off <= (2.0 ** -11 + 2.0 ** -18) * logit).all() and (off > 2.0 ** -12 * 1.9 * logit).all()
+
+
+def test_values_past_binary16_are_seen():
+    """A stored V value past 65504 is infinite: the rows that see it are not finite in
+    that dim, whatever its weight, and no other element changes."""
+    w, gs, pl = prefix_workload([(2, 700), (1, 500)], [100, 40, 300], 16, Q8, Q8)
+    q = to_dev(w.q).half()
+    want, want_lse = decode(w, gs, pl, q)
+    v = w.v_rows.copy().reshape(len(w.v_rows), 4, 8, 34)
+    at = int(w.seq_lens[:1].sum()) + 720  # the second sequence's own row
+    v[at, 1, 3, :2] = np.array([3000.0], np.float16).view(np.uint8)
+    quants = v[at, 1, 3, 2:].view(np.int8).astype(np.int32)
+    bad = W.Workload(w.name, w.seq_lens, 1, 16, w.n_blocks, Q8, Q8, w.table, w.k_rows, v.reshape(w.v_rows.shape), w.q, w.scale)
+    out, lse = decode(bad, gs, pl, q)
+    past = np.zeros((3, 1, 24, 256), bool)
+    past[1, 0, 6:12, 96:128] = np.abs(3000 * quants) > 65504
+    block = np.zeros_like(past)
+    block[1, 0, 6:12, 96:128] = True
+    got = out.cpu().numpy()
+    assert past.sum() > 60 and not np.isfinite(got[past]).any() and np.isfinite(got[~past]).all()
+    assert np.array_equal(got[~block], want.cpu().numpy()[~block]) and torch.equal(lse, want_lse)
