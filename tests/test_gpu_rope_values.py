@@ -3,10 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-import workloads as W
 from gpu_helpers import to_dev
-from paged_kv_gqa_11_gb300 import PA_OK
-from paged_kv_gqa_11_gb300.cache import PagedKVCache
 from paged_kv_gqa_11_gb300.rope import Rope
 from rope_helpers import inv_freq
 
@@ -62,3 +59,22 @@ def test_infinite_values_in_the_rotated_part_touch_their_pair_only():
         rest = [i for i in range(256) if i not in pair]
         assert torch.equal(got[:, :, rest], plain[:, :, rest])
         assert not got[:, :, pair].isfinite().any()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_cosines_and_sines(inter):
+    """Pairs (1, 0) turn into (cos, sin), exactly: both within 5 u of float64's (u = 2^-24).
+    The phase's cut to 32 bits is u / 32 of an angle, its three fp32 roundings 3 u pi / 4, the
+    series' remainder u / 2, its evaluation below 1.5 u; float64 itself is off by 2^-30 at
+    angles below 2^24."""
+    rng = np.random.default_rng(2)
+    pos = np.concatenate([np.arange(-64, 64), rng.integers(-(1 << 24), 1 << 24, 8000)]).astype(np.int32)
+    freq = [1.0, np.pi / 4, np.pi / 8, 0.5] + [float(x) for x in rng.uniform(0, 1, 60)] + [1e-3 ** (i / 64) for i in range(64)]
+    x = torch.zeros(len(pos), 1, 256, device="cuda")
+    (x[..., 0::2] if inter else x[..., :128]).fill_(1.0)
+    y, _ = Rope(freq, interleaved=inter).apply(x, None, to_dev(pos))
+    y = y[:, 0].double().cpu().numpy()
+    c, s = (y[:, 0::2], y[:, 1::2]) if inter else (y[:, :128], y[:, 128:])
+    ang = pos.astype(np.float64)[:, None] * np.array(freq)
+    worst = max(np.abs(c - np.cos(ang)).max(), np.abs(s - np.sin(ang)).max())
+    assert worst < 5 * 2.0 ** -24 + 2.0 ** -28, worst * 2 ** 24
