@@ -76,11 +76,12 @@ void block_table(const at::Tensor& t) {
   check(t.scalar_type() == at::kInt && t.dim() == 2 && t.is_contiguous(), "block_table: int32 [n_seq][pages], contiguous");
 }
 
-// Elements between rows of [n][heads][256] whose heads are packed.
+// Elements between rows of [n][heads][256] whose heads are packed (a single row's own
+// length, whatever stride its tensor has there).
 int64_t row_stride(const at::Tensor& x, const char* name) {
   if (x.dim() != 3 || x.size(2) != kD || x.stride(2) != 1 || (x.size(1) > 1 && x.stride(1) != kD))
     refuse(std::string(name) + ": rows [n][heads][256] of packed heads");
-  return x.size(0) > 1 ? x.stride(0) : std::max<int64_t>(x.stride(0), x.size(1) * kD);
+  return x.size(0) > 1 ? x.stride(0) : x.size(1) * kD;
 }
 
 void same_shape(const at::Tensor& a, const at::Tensor& b, const char* what) { check(a.sizes() == b.sizes(), what); }

@@ -78,3 +78,16 @@ def test_cosines_and_sines(inter):
     ang = pos.astype(np.float64)[:, None] * np.array(freq)
     worst = max(np.abs(c - np.cos(ang)).max(), np.abs(s - np.sin(ang)).max())
     assert worst < 5 * 2.0 ** -24 + 2.0 ** -28, worst * 2 ** 24
+
+
+def test_a_single_row_of_any_stride():
+    """One row of a buffer whose rows are no whole 16 bytes long: its stride is never used."""
+    buf = torch.from_numpy(np.random.default_rng(6).standard_normal((8, 28 * 256 + 4)).astype(np.float32)).cuda().half()
+    row = buf[:, :28 * 256].unflatten(1, (28, 256))[2:3]
+    assert row.stride(0) % 8 and row.data_ptr() % 16 == 0
+    pos, w, r = torch.tensor([9], dtype=torch.int32, device="cuda"), torch.rand(256, device="cuda").half(), Rope(inv_freq(64))
+    want = r.apply(row[:, :24].contiguous(), row[:, 24:].contiguous(), pos, w, w)
+    got = r.apply(row[:, :24], row[:, 24:], pos, w, w)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    r.apply(row[:, :24], row[:, 24:], pos, w, w, q_out=row[:, :24], k_out=row[:, 24:])
+    assert torch.equal(row[:, :24], want[0]) and torch.equal(row[:, 24:], want[1])
