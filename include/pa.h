@@ -273,7 +273,9 @@ pa_status pa_norm_rope(const pa_rope_desc* rope, const void* q, int64_t q_stride
  *           table entry is out of range (the padding of a batch: row_seq -1) is
  *           not stored and sets *err = PA_ERR_BOUNDS; its query is still
  *           written.  Rows with the same (seq, pos) in one call race.  Values
- *           are finite. */
+ *           are finite, and in the range of their format: up to 65504 in F16, 65504
+ *           times 127 in Q8_0 and times 8 in Q4_0 (past it they are stored as
+ *           infinite). */
 pa_status pa_append_rows_rope(const pa_pool* pool, void* k_pool, void* v_pool, const pa_rope_desc* rope,
                               const void* k_rows, int64_t k_stride, const void* v_rows, int64_t v_stride,
                               int32_t in_type, const void* k_weight, int32_t w_type, const void* q, int64_t q_stride,
@@ -436,6 +438,13 @@ pa_status pa_decode_noalloc(const pa_pool* pool, const float* q, const void* k_p
  * the same blocks; a page that the prefix ends in may be each sequence's own
  * copy).  The result is that of pa_decode on the same batch, up to rounding;
  * a prefix length of 0 shares nothing.
+ *
+ * When it pays, GPU time against pa_decode on the same batch: from two sequences
+ * with 1000 shared rows on in quantised pools (8.1 against 9.3 us), from four in F16
+ * (8.4 against 9.1), the more the longer the prefix and the more sequences (8 of
+ * 32768 + 1024 rows in Q4_0: 22.9 against 56); with four query tokens nearly always
+ * (8 of 500 + 100 rows: 11.8 against 16.1).  With one token, shorter prefixes are even,
+ * and sequences that share nothing take the same within an eighth, either way.
  *
  * q, out:   device [n_seq][n_qtok][n_q_heads][head_dim] of q_type / out_type (a
  *           pa_dtype), 16-byte aligned.

@@ -48,8 +48,8 @@
 //   24, 25 MMA issue, S^T and O^T; 26, 27 raw K and V copies (cp.async.bulk).
 //
 // What bounds it.  Neither the tensor core (11 % of a call of 8 x (32768 + 1024)
-// keys in Q4_0, 23 us, by the counter; a third where tiles of 64 rows follow one
-// another) nor the memory, but for binary16 (8 x 98304 keys: 69.5 us, 5.8 TB/s).  A
+// keys in Q4_0, 22.9 us, by the counter; a third where tiles of 64 rows follow one
+// another) nor the memory, but for binary16 (8 x 98304 keys: 70 us, 5.8 TB/s).  A
 // tile of 64 rows takes about 1.6 us, and three chains are about equally long there:
 // the softmax of a tile and the step to the next, the dequantisation of V plus half
 // of its MMAs, and of K plus half of its.  Seven warps on a scheduler, each in code of
@@ -68,12 +68,15 @@
 // Range.  A stored key may have values past binary16's 65504 (scale * quant goes to
 // 8.3 * 10^6): the values of such a key are taken 2^-8 of what they are, its logits 2^8
 // times (dequant_k).  That costs the ordinary case a vote on the scales, 0 to 1 per cent.
+// A query value that rounds past 65504 makes its row NaN; a V value past it is infinite.
 //
 // Precision.  Q, K, V (scale * quant, rounded once) and P are binary16, products
 // are accumulated in fp32, m, l and O are fp32, and l sums the weights before
 // their rounding.  Rounding K costs a logit 2^-11 |q| |k| scale at most, as much as the
 // rounding of Q that fp32 queries meet anyway; keeping K exact would take a second
-// product and half again the dequantisation.
+// product and half again the dequantisation.  On N(0, 1) data the roundings of P, of V and
+// of K move the output by 2.1, 1.6 to 2.1 and 1.7 to 2.2 x 10^-4 of its norm, a binary16
+// output's own by 2.1.
 #pragma once
 
 #include "pa_decode_impl.cuh"
@@ -136,8 +139,8 @@ struct Cost {
 
 // By the query rows of the unit: what tiles of up to 31, 63 and 64 rows and the
 // pieces took, fitted over batches of short and long suffixes.  Equal tiles and no
-// lead: 64 sequences of 128 + 4096 keys 175 us, 8 of 98304 + 16 in Q8_0 70 us;
-// by cost, on the same kernel, 102 and 57.
+// lead: 64 sequences of 128 + 4096 keys in Q4_0 155 us, 8 of 98304 + 16 in Q8_0 61 us;
+// by cost 94.6 and 45.5.
 __host__ __device__ constexpr Cost cost_of(int weigh, int rows) {
   return weigh ? Cost{kLead, kTileCost + (rows >= kRows ? 2 : rows / 32)} : Cost{0, 1};
 }

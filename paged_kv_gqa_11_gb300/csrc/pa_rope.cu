@@ -347,12 +347,14 @@ __device__ __forceinline__ void turn_head(const RopeParams& p, const Raw<T>& raw
 
 // Heads that are loaded at once (the next ones are prefetched meanwhile), warps
 // that few rows are split into, and resident CTAs that the registers allow: 28
-// warps an SM, 20 for the append, whose quantisers would spill.  4096 rows of bf16,
-// one launch after another: 22.8 us with 28 warps and the prefetch, 23.3 with 20,
-// 27.0 without the prefetch (21.7 us, 5.4 TB/s, as programmatic dependents); 8192
+// warps an SM, 20 for the append, whose quantisers would spill more.  4096 rows of
+// bf16, one launch after another: 22.8 us with 28 warps and the prefetch, 23.3 with 20,
+// 27.0 without the prefetch (20.9 us, 5.6 TB/s, as programmatic dependents); 8192
 // rows appended as Q8_0 and Q4_0 and read back: 61.9 us, 64.5 and more with over 20
-// warps, 68.0 without the prefetch (60.5 as dependents); batches of two or eight
-// heads are slower.
+// warps, 68.0 without the prefetch (60.4 as dependents); batches of two or eight
+// heads are slower.  At 72 registers 16-bit rows spill 76 to 116 bytes a thread, fp32
+// rows 240 to 328; the append spills with fp32 rows only (38 to 64).  28 warps was
+// chosen with bf16 rows; 4096 of fp32 take 43.8 us, 0.79 of what their bytes need.
 constexpr int kBatch = 4, kWarpsPerSm = 48;
 
 // kAppend: keys and values go into the pools; else keys go to k_out.
