@@ -99,3 +99,31 @@ def test_results_dropped_before_the_current_stream_has_read_them():
     later, _ = r.apply(xs[1], None, pos, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(copy, want) and not torch.equal(later, want)
+
+
+def test_a_stream_passed_in_while_capturing():
+    """A branch of a captured graph: forked from the capturing stream, joined to it, the
+    call's inputs and results dropped inside."""
+    rng = np.random.default_rng(6)
+    xs = [torch.from_numpy(rng.standard_normal((64, 32, 256)).astype(np.float32)).cuda().half() for _ in range(2)]
+    pos, w = torch.arange(64, dtype=torch.int32, device="cuda"), torch.rand(256, device="cuda").half()
+    r, side = Rope(inv_freq(64)), torch.cuda.Stream()
+    want = [r.apply(x * 2, None, pos, w)[0] + 1 for x in xs]
+    x = xs[0].clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        now = torch.cuda.current_stream()
+        twice = x * 2
+        side.wait_stream(now)
+        y, _ = r.apply(twice, None, pos, w, stream=side)
+        del twice
+        scratch = torch.zeros_like(x)  # would take the dropped block
+        now.wait_stream(side)
+        out = y + 1
+        del y, scratch
+    for src, ref in zip(xs, want):
+        x.copy_(src)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
