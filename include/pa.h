@@ -478,6 +478,49 @@ pa_status pa_decode_prefix(const pa_pool* pool, const void* q, int32_t q_type, c
 size_t pa_decode_prefix_workspace_size(const pa_pool* pool, uint32_t n_seq, uint32_t n_groups, uint32_t n_qtok,
                                        int device);
 
+/* ------------------------------------------------------------------ attention over a window
+ * The pages describe no counterpart of this call; it exists for users of this library.
+ *
+ * Causal attention of each sequence's newest tokens over the cache, for ragged batches:
+ * sequence s has n_new[s] >= 0 of them, one (a decode step), a few (verification) or many
+ * (a chunk of prompt, a whole one), at positions L - n_new[s] .. L - 1 of its L =
+ * seq_lens[s] cached rows.  The token at position p attends to the keys x <= p with
+ * x > p - window (the window holds its own key) or x < sinks (first keys that stay
+ * visible); window 0 stands for none: all keys up to p.
+ *
+ * q, out:   device rows of n_q_heads heads of 256 values, of q_type / out_type (a
+ *           pa_dtype), a row per token: the first sequence's n_new[0], then the next's.
+ *           q_stride and out_stride are values between rows (at least heads * 256, a
+ *           multiple of 16 bytes), so q may be a part of a projection.  Rows after
+ *           the last sequence's are neither read nor written.
+ * lse:      device fp32 [tokens][n_q_heads], or NULL.
+ * n_new:    host int32 [n_seq]; n_new[s] <= L.  seq_lens_dev, seq_lens_host: as pa_decode
+ *           (the host's drive every read; a sequence whose device length is another gives
+ *           out = 0, lse = -inf and *err = PA_ERR_BOUNDS).
+ * block_table: only entries for pages that hold a row group (16 rows) with a key that
+ *           some new token sees are read, so the pages outside window and sinks may
+ *           have been released.  An entry outside the pool: as pa_decode.
+ * workspace: ws_bytes >= pa_attend_window_workspace_size() for the largest n_new,
+ *           256-byte aligned; contents as pa_decode's.
+ *
+ * Precision and range: as pa_decode_prefix, whose arithmetic it is.  An infinite or NaN
+ * value of V (a stored one past 65504 is infinite) in a row that one of the tokens
+ * sees can also reach others of the same sequence that do not see it (those up to 11
+ * tokens away); in a row that none of them sees it has no effect, and K's never have.
+ *
+ * Launches: one, and a merge when a (64 query rows, KV head) is shared by CTAs; 448 times
+ * 64 query rows at a time.  Both are programmatic dependent launches (pa_decode). */
+pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_t q_stride, int32_t q_type, const void* k_pool,
+                           const void* v_pool, const int32_t* block_table, uint32_t table_stride,
+                           const int32_t* seq_lens_dev, const int32_t* seq_lens_host, const int32_t* n_new,
+                           uint32_t n_seq, uint32_t n_q_heads, uint32_t window, uint32_t sinks, float scale, void* out,
+                           int64_t out_stride, int32_t out_type, float* lse, void* workspace, size_t ws_bytes,
+                           int32_t* err, pa_stream_t stream);
+
+/* Scratch bytes pa_attend_window needs for up to max_new new tokens of a sequence, any
+ * number of sequences, on CUDA device `device`.  0 for an unsupported pool. */
+size_t pa_attend_window_workspace_size(const pa_pool* pool, uint32_t max_new, int device);
+
 /* ------------------------------------------------------------------ errors */
 
 /* Device-detected failures are reported, not trapped (lucebox PR #555,

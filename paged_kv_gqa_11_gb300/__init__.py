@@ -22,6 +22,7 @@ __all__ = [
     "pa_decode_workspace_size", "pa_decode_plan", "pa_get_error", "pa_selftest_wait_timeout", "status_name",
     "library_path", "pa_decode_noalloc", "PA_DT_F32", "PA_DT_F16", "PA_DT_BF16", "RopeDesc", "dtype_number",
     "pa_norm_rope", "pa_append_rows_rope", "pa_read_rows", "pa_decode_prefix", "pa_decode_prefix_workspace_size",
+    "pa_attend_window", "pa_attend_window_workspace_size",
 ]
 
 PA_F16, PA_Q4_0, PA_Q8_0 = 1, 2, 8
@@ -36,7 +37,7 @@ EXPORTS = ["pa_pool_create", "pa_pool_destroy", "pa_pool_get_desc", "pa_row_byte
            "pa_cow_blocks", "pa_copy_blocks", "pa_append_rows", "pa_append_rows_f16",
            "pa_decode", "pa_decode_split", "pa_decode_merge", "pa_decode_workspace_size", "pa_decode_plan", "pa_get_error", "pa_status_string",
            "pa_selftest_wait_timeout", "pa_decode_noalloc", "pa_norm_rope", "pa_append_rows_rope", "pa_read_rows",
-           "pa_decode_prefix", "pa_decode_prefix_workspace_size"]
+           "pa_decode_prefix", "pa_decode_prefix_workspace_size", "pa_attend_window", "pa_attend_window_workspace_size"]
 
 
 class PaError(RuntimeError):
@@ -112,6 +113,9 @@ def load():
             "pa_decode_prefix": (C.c_int, [vp, vp, i32, vp, vp, vp, u32, vp, vp, u32, vp, vp, u32, u32, u32, C.c_float,
                                            vp, i32, vp, vp, sz, vp, vp]),
             "pa_decode_prefix_workspace_size": (sz, [vp, u32, u32, u32, C.c_int]),
+            "pa_attend_window": (C.c_int, [vp, vp, i64, i32, vp, vp, vp, u32, vp, vp, vp, u32, u32, u32, u32, C.c_float, vp,
+                                           i64, i32, vp, vp, sz, vp, vp]),
+            "pa_attend_window_workspace_size": (sz, [vp, u32, C.c_int]),
         }
         sig["pa_decode_split"] = sig["pa_decode_merge"] = sig["pa_decode"]
         for name, (res, args) in sig.items():
@@ -389,4 +393,21 @@ def pa_decode_prefix(pool: Pool, q, q_type: int, k_pool, v_pool, block_table, ta
                                  _ptr(workspace), ws_bytes, _ptr(err), _stream(stream))
     if check:
         _check(rc, "pa_decode_prefix")
+    return rc
+
+
+def pa_attend_window_workspace_size(pool: Pool, max_new: int, device: int = 0) -> int:
+    return int(load().pa_attend_window_workspace_size(pool.handle, max_new, device))
+
+
+def pa_attend_window(pool: Pool, q, q_stride: int, q_type: int, k_pool, v_pool, block_table, table_stride: int, seq_lens_dev,
+                     seq_lens_host, n_new, n_seq: int, n_q_heads: int, window: int, sinks: int, scale: float, out,
+                     out_stride: int, out_type: int, lse, workspace, ws_bytes: int, err, stream=None, check: bool = True) -> int:
+    """seq_lens_host, n_new: host int32 buffers that stay alive for the call; strides in elements between rows."""
+    rc = load().pa_attend_window(pool.handle, _ptr(q), q_stride, q_type, _ptr(k_pool), _ptr(v_pool), _ptr(block_table),
+                                 table_stride, _ptr(seq_lens_dev), _ptr(seq_lens_host), _ptr(n_new), n_seq, n_q_heads, window,
+                                 sinks, scale, _ptr(out), out_stride, out_type, _ptr(lse), _ptr(workspace), ws_bytes, _ptr(err),
+                                 _stream(stream))
+    if check:
+        _check(rc, "pa_attend_window")
     return rc

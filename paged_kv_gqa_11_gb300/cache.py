@@ -138,6 +138,24 @@ class PagedKVCache:
                                          seq_lens_host, group_sizes, prefix_lens, n_qtok, scale, out, lse, want_lse,
                                          workspace, self.err, stream)
 
+    # ------------------------------------------------------------ attention over a window
+    def attend_window(self, q: torch.Tensor, block_table: torch.Tensor, seq_lens_dev: torch.Tensor, seq_lens_host: np.ndarray,
+                      n_new, window: int = 0, sinks: int = 0, scale: float = 1.0 / 16.0, out: torch.Tensor | None = None,
+                      lse: torch.Tensor | None = None, want_lse: bool = True, workspace: torch.Tensor | None = None, stream=None):
+        """Causal attention of each sequence's newest n_new[s] tokens (0, 1, a
+        few, a whole prompt), which are in the cache already: the token at
+        position p sees the `window` keys up to its own (0: all) and the first
+        `sinks`.  q: rows [tokens][heads][256] of fp32, binary16 or bfloat16, one
+        sequence's after the other's (a part of a projection is fine); out: q's
+        shape, of q's type unless given.  seq_lens_host, n_new: host arrays of
+        32-bit whole numbers (numpy).  Pages that no new token sees are not read;
+        they may have been released.  Rows of q after the last sequence's are left
+        alone: those of a given out and lse stay, those of new ones are zeros.
+        Precision, workspace and streams: as decode_prefix.  Returns (out, lse)."""
+        return load_calls().attend_window(self.pool.address, q, self.k_pool, self.v_pool, block_table, seq_lens_dev,
+                                          seq_lens_host, n_new, window, sinks, scale, out, lse, want_lse, workspace, self.err,
+                                          stream)
+
     def check(self, stream=None) -> int:
         """Synchronise, read and reset the device error word."""
         return pa_get_error(self.err, stream)

@@ -23,6 +23,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ATen.h>
 
+#include <algorithm>
 #include <initializer_list>
 #include <optional>
 #include <string>
@@ -399,6 +400,82 @@ PyObject* decode_prefix(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
+uint32_t count_arg(PyObject* o, const char* name) {
+  const long long v = PyLong_AsLongLong(o);
+  if (PyErr_Occurred() || v < 0 || v > UINT32_MAX) {
+    PyErr_Clear();
+    refuse(std::string(name) + ": a whole number from 0 on");
+  }
+  return (uint32_t)v;
+}
+
+float float_arg(PyObject* o, const char* name) {
+  const double v = PyFloat_AsDouble(o);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse(std::string(name) + ": a number");
+  }
+  return (float)v;
+}
+
+// (pool, q, k_pool, v_pool, table, seq_lens_dev, seq_lens_host, n_new, window, sinks, scale, out, lse, want_lse, workspace,
+//  err, stream) -> (out, lse)
+PyObject* attend_window(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded(n_args, 17, [&]() -> PyObject* {
+    const auto* pool = static_cast<const pa_pool*>(address(a[0], "pool"));
+    const at::Tensor &q = tensor(a[1], "q"), &kp = tensor(a[2], "k_pool"), &vp = tensor(a[3], "v_pool"), &table = tensor(a[4], "block_table"),
+                     &lens_dev = tensor(a[5], "seq_lens_dev"), &err = tensor(a[15], "err");
+    const Ints lens(a[6], "seq_lens_host"), n_new(a[7], "n_new");
+    const uint32_t window = count_arg(a[8], "window"), sinks = count_arg(a[9], "sinks");
+    const float scale = float_arg(a[10], "scale");
+    at::Tensor out = tensor(a[11], "out", true), lse = tensor(a[12], "lse", true), ws = tensor(a[14], "workspace", true);
+    const int dev = kp.get_device();
+    block_table(table);
+    const int64_t n = table.size(0);
+    index(lens_dev, n, "seq_lens_dev");
+    check(lens.size() == n && n_new.size() == n, "a table row, a length and a number of new tokens per sequence");
+    const int64_t qs = row_stride(q, "q"), rows = q.size(0), hq = q.size(1);
+    const auto* fresh = static_cast<const int32_t*>(n_new.b.buf);
+    int64_t tokens = 0;
+    int32_t most = 0;
+    for (int64_t i = 0; i < n; ++i) {
+      check(fresh[i] >= 0, "n_new: from 0 on");
+      tokens += fresh[i];
+      most = std::max(most, fresh[i]);
+    }
+    check(tokens <= rows, "q: a row per new token");
+    on(dev, q, "q"); on(dev, vp, "v_pool"); on(dev, table, "block_table"); on(dev, lens_dev, "seq_lens_dev"); on(dev, out, "out");
+    on(dev, lse, "lse"); on(dev, ws, "workspace"); on(dev, err, "err");
+    check(n <= UINT32_MAX && hq <= UINT32_MAX && table.size(1) <= INT32_MAX, "sizes");
+    const Place place(dev, a[16]);
+    place.uses({&q, &kp, &vp, &table, &lens_dev, &out, &lse, &ws, &err});
+    if (!out.defined()) {
+      out = place.made(at::empty({rows, hq, kD}, q.options()));
+      if (tokens < rows) out.narrow(0, tokens, rows - tokens).zero_();
+    }
+    const int want = PyObject_IsTrue(a[13]);
+    if (want < 0) PyErr_Clear();
+    if (!lse.defined() && want == 1) {
+      lse = place.made(at::empty({rows, hq}, q.options().dtype(at::kFloat)));
+      if (tokens < rows) lse.narrow(0, tokens, rows - tokens).zero_();
+    }
+    same_shape(q, out, "out of q's shape");
+    check(!lse.defined() || (lse.scalar_type() == at::kFloat && lse.is_contiguous() && lse.dim() == 2 && lse.size(0) == rows && lse.size(1) == hq),
+          "lse: float32 [tokens][heads], contiguous");
+    if (tokens > 0 && !ws.defined())
+      ws = at::empty({(int64_t)pa_attend_window_workspace_size(pool, (uint32_t)most, dev)}, kp.options().dtype(at::kByte));
+    check(!ws.defined() || ws.is_contiguous(), "workspace: contiguous");
+    const int qt = dtype_of(q), ot = dtype_of(out);
+    const int64_t os = row_stride(out, "out");
+    status(pa_attend_window(pool, ptr(q), qs, qt, ptr(kp), ptr(vp), table.data_ptr<int32_t>(), (uint32_t)table.size(1),
+                            lens_dev.data_ptr<int32_t>(), static_cast<const int32_t*>(lens.b.buf), fresh, (uint32_t)n, (uint32_t)hq, window,
+                            sinks, scale, ptr(out), os, ot, lse.defined() ? lse.data_ptr<float>() : nullptr, ptr(ws),
+                            ws.defined() ? (size_t)ws.nbytes() : 0, err.data_ptr<int32_t>(), place.stream),
+           "pa_attend_window");
+    return pair(out, lse);
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* e) {
   Py_INCREF(e);
   Py_XDECREF(g_error);
@@ -411,6 +488,7 @@ PyMethodDef g_methods[] = {
     {"append_rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(append_rope)), METH_FASTCALL, ""},
     {"read_rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(read_rows)), METH_FASTCALL, ""},
     {"decode_prefix", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(decode_prefix)), METH_FASTCALL, ""},
+    {"attend_window", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(attend_window)), METH_FASTCALL, ""},
     {"set_error", set_error, METH_O, ""},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -103,6 +103,7 @@ constexpr int kLead = 12, kTileCost = 9;
 constexpr float kLazyLog2 = 8.f;  // logits may pass their reference by this
 
 struct Params {
+  static constexpr bool kWindow = false;
   const uint8_t* q;
   const uint8_t* k_pool;
   const uint8_t* v_pool;
@@ -124,6 +125,7 @@ struct Params {
   int32_t seq_tile[kMaxSeqs];              // tiles before a sequence's suffix
   int32_t group_first[kMaxGroups], group_seqs[kMaxGroups], group_keys[kMaxGroups];
   int32_t group_at[kMaxGroups], group_tile[kMaxGroups], group_seg[kMaxGroups];  // places, tiles, segments before a group
+  using Live = int;  // live keys of a tile
 };
 
 // ------------------------------------------------------------------ the walk
@@ -207,7 +209,9 @@ __device__ __forceinline__ Pos locate(const Params& p, int x) {
   return t;
 }
 
+__device__ __forceinline__ int pos_row0(const Params&, const Pos& t) { return t.rt * kRows; }
 __device__ __forceinline__ int pos_seq(const Params& p, const Pos& t) { return t.pre ? p.group_first[t.unit] : t.unit; }
+__device__ __forceinline__ int pos_token(const Params& p, const Pos& t) { return pos_seq(p, t) * p.n_qtok; }
 __device__ __forceinline__ int pos_key0(const Params& p, const Pos& t) {
   return (t.pre ? 0 : p.start[t.unit]) + t.j * kKeys;
 }
@@ -232,12 +236,14 @@ __host__ __device__ constexpr int key16(int p) {
 
 // ------------------------------------------------------------------ shared memory
 
-template <int KT, int VT>
+template <int KT, int VT, bool kWindow = false>
 struct Smem {
   static constexpr int kKStage = 4 * pa_layout::group_bytes<KT>(), kVStage = 4 * pa_layout::group_bytes<VT>();
   static constexpr int kQBytes = kRows * kD * 2, kPBytes = kRows * kKeys * 2;
   static constexpr int kQ = 0, kP = kQBytes, kRing = kP + 2 * kPBytes;
-  static constexpr int kTail = 8 * kRows * 4 + 2 * kRows * 4 + 17 * 32 + 64 + 64 + 640;  // red, references, tiles, wide keys, barriers
+  static constexpr int kLiveBytes = kWindow ? 16 * 16 : 64, kInvBytes = kWindow ? kRows * 4 : 0;
+  // red, references, tiles, live keys, wide keys, reciprocal sums, barriers
+  static constexpr int kTail = 8 * kRows * 4 + 2 * kRows * 4 + 17 * 32 + kLiveBytes + 64 + kInvBytes + 640;
   // K and V stages in rings of their own, both of an even number of stages: a
   // warp reads every second stage of its ring, and so sees every use of those it
   // reads (a parity wait must never be two phases ahead of its barrier).  Two
@@ -261,8 +267,8 @@ struct Smem {
   static constexpr int kVRing = kRing + kKStages * kKStage;
   static constexpr int kRed = kVRing + kVStages * kVStage;
   static constexpr int kRef = kRed + 8 * kRows * 4, kAlpha = kRef + kRows * 4;
-  static constexpr int kTile = kAlpha + kRows * 4, kOpening = kTile + 16 * 32, kLeft = kOpening + 32, kWide = kLeft + 64,
-                       kBar = kWide + 16 * 4;
+  static constexpr int kTile = kAlpha + kRows * 4, kOpening = kTile + 16 * 32, kLeft = kOpening + 32,
+                       kWide = kLeft + kLiveBytes, kInv = kWide + 16 * 4, kBar = kInv + kInvBytes;
   // K and V raw full / empty [stages], K and V unit full / empty [2], s full / empty [2], q full / empty [2],
   // p full, pv done, o free [2] each, drain [2], sink
   static constexpr int kNBar = 2 * (kKStages + kVStages) + 8 + 4 + 4 + 9;
@@ -427,12 +433,25 @@ __host__ __device__ constexpr int v_dim(int l) {
   return T == PA_F16 ? l : 16 * (l >> 4) + 2 * (l & 7) + ((l >> 3) & 1);
 }
 
+// The live keys of a stage: its first n, or (of a window) those before a and from b to
+// c - 1.
+struct FirstKeys {
+  int n;
+  __device__ __forceinline__ bool all() const { return n >= kStageKeys; }
+  __device__ __forceinline__ bool has(int k) const { return k < n; }
+};
+struct WindowKeys {
+  int a, b, c;
+  __host__ __device__ __forceinline__ bool all() const { return c >= kStageKeys && (b <= 0 || a >= b || a >= kStageKeys); }
+  __host__ __device__ __forceinline__ bool has(int k) const { return k < c && (k < a || k >= b); }
+};
+
 // 64 keys x 32 dims twice (blocks b and b + 4) of a V stage into a V unit's 32
 // lanes at taddr (lane field included): columns 0-31 and 32-63, eight for every
-// 16 keys.  n_keys: live keys of the stage; the others' values become zeros,
+// 16 keys.  keys: the live keys of the stage; the others' values become zeros,
 // whatever bytes lie there.
-template <int T>
-__device__ __forceinline__ void dequant_v(uint32_t stage, int b, int n_keys, uint32_t taddr, int lane) {
+template <int T, class Keys>
+__device__ __forceinline__ void dequant_v(uint32_t stage, int b, const Keys keys, uint32_t taddr, int lane) {
   constexpr int GB = pa_layout::group_bytes<T>(), RQ = Fmt<T>::kRowQ;
   // ldmatrix: matrices 0 and 2 hold rows 0..7 of a group, 1 and 3 rows 8 + (i ^ 4)
   const int mi = lane >> 3, i = lane & 7, r7 = (mi & 1) ? i ^ 4 : i, t = lane & 3;
@@ -442,10 +461,10 @@ __device__ __forceinline__ void dequant_v(uint32_t stage, int b, int n_keys, uin
 #pragma unroll 1
   for (int g = 0; g < 4; ++g) {
     uint32_t ma = 0xffffffffu, mb = 0xffffffffu;  // live keys of the pairs
-    if (n_keys < kStageKeys) {
-      const int left = n_keys - 16 * g, ka = 2 * t, kb = 8 + ((2 * t) ^ 4);
-      ma = (ka < left ? 0xffffu : 0u) | (ka + 1 < left ? 0xffff0000u : 0u);
-      mb = (kb < left ? 0xffffu : 0u) | (kb + 1 < left ? 0xffff0000u : 0u);
+    if (!keys.all()) {
+      const int ka = 16 * g + 2 * t, kb = 16 * g + 8 + ((2 * t) ^ 4);
+      ma = (keys.has(ka) ? 0xffffu : 0u) | (keys.has(ka + 1) ? 0xffff0000u : 0u);
+      mb = (keys.has(kb) ? 0xffffu : 0u) | (keys.has(kb + 1) ? 0xffff0000u : 0u);
     }
     [[maybe_unused]] uint32_t xq[4];
 #pragma unroll
@@ -543,8 +562,11 @@ __device__ __forceinline__ void q_range(uint32_t top, uint32_t to) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"((unsigned short)0x7fff) : "memory");
 }
 
-template <int KT>
-__device__ __forceinline__ void stage_q_begin(const Params& p, const Tile& t, uint32_t dst, int r8, int lane) {
+// Where query head h of token t has its values, counted in values.
+__device__ __forceinline__ long long query_at(const Params& p, int t, int h) { return ((long long)t * p.n_q_heads + h) * kD; }
+
+template <int KT, class P>
+__device__ __forceinline__ void stage_q_begin(const P& p, const Tile& t, uint32_t dst, int r8, int lane) {
   const int row = r8 + (lane & 7), rg = t.row0 + row, rows = t.info & 0xff;
   const uint32_t to = dst + canon(row, lane >> 3, kD / 8);
   if (row >= rows) {
@@ -552,7 +574,7 @@ __device__ __forceinline__ void stage_q_begin(const Params& p, const Tile& t, ui
     for (int i = 0; i < 8; ++i) sts128_zero(to + 512 * i);
     return;
   }
-  const long long at = ((long long)(t.token + rg / kGqa) * p.n_q_heads + t.head * kGqa + rg % kGqa) * kD;
+  const long long at = query_at(p, t.token + rg / kGqa, t.head * kGqa + rg % kGqa);
   if (p.q_type == PA_DT_F32) {
     const float* src = reinterpret_cast<const float*>(p.q) + at;
     uint32_t top = 0;
@@ -583,8 +605,8 @@ __device__ __forceinline__ void stage_q_begin(const Params& p, const Tile& t, ui
   }
 }
 
-template <int KT>
-__device__ __forceinline__ void stage_q_end(const Params& p, uint32_t dst, int r8, int lane) {
+template <int KT, class P>
+__device__ __forceinline__ void stage_q_end(const P& p, uint32_t dst, int r8, int lane) {
   asm volatile("cp.async.wait_all;" ::: "memory");
   const bool bf16 = p.q_type == PA_DT_BF16;
   if (p.q_type == PA_DT_F32 || (KT != PA_Q4_0 && !bf16)) return;
@@ -650,6 +672,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int32_t
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return warp_wait_slow(bar, parity, err, abort);
 }
+
+__device__ __forceinline__ FirstKeys live_keys(const Params&, int left, int from) { return FirstKeys{left - from}; }
+__device__ __forceinline__ bool has_edge(const Params&, const Tile& t) { return t.open < kKeys; }
 
 // The raw K or V row groups of the CTA's tiles into a ring of ns stages at ring,
 // two stages per tile; returns the number of stages issued.  gb, rb: bytes of a
@@ -785,9 +810,9 @@ __device__ __forceinline__ uint32_t elect_one() {
 
 // ------------------------------------------------------------------ the kernel
 
-template <int KT, int VT>
-__global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_constant__ Params p) {
-  using SM = Smem<KT, VT>;
+template <int KT, int VT, class P>
+__global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_constant__ P p) {
+  using SM = Smem<KT, VT, P::kWindow>;
   constexpr int NK = SM::kKStages, NV = SM::kVStages;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -814,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
   int* tiles_at = reinterpret_cast<int*>(smem + SM::kMisc + 16 + sizeof(Pos));  // the CTA's first tile, the next CTA's
   Tile* opening = reinterpret_cast<Tile*>(smem + SM::kOpening);                 // of the first tile, what its query rows need
   Tile* tiles = reinterpret_cast<Tile*>(smem + SM::kTile);
-  int* lefts = reinterpret_cast<int*>(smem + SM::kLeft);
+  auto* lefts = reinterpret_cast<typename P::Live*>(smem + SM::kLeft);
   // wide keys (dequant_k) of each quarter of the lanes, where the tile says so; four tiles
   // deep: K(j + 4) follows S^T(j + 3), and that the end of softmax(j + 1)
   uint32_t* wide_keys = reinterpret_cast<uint32_t*>(smem + SM::kWide);
@@ -852,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       if (lane == 0) {
         if (w == 1) {
           *start = t;
-          *opening = Tile{(uint32_t)pos_rows(p, t) | 1u << 8, 0, t.rt * kRows, 0, pos_seq(p, t) * p.n_qtok, t.head, {0, 0}};
+          *opening = Tile{(uint32_t)pos_rows(p, t) | 1u << 8, 0, pos_row0(p, t), 0, pos_token(p, t), t.head, {0, 0}};
         }
         tiles_at[w - 1] = t.tile;
       }
@@ -946,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       if (!warp_wait(vraw_full + 8 * slot, (stage / NV) & 1, p.err, abort)) break;
       if (j > 0 && !warp_wait(vu_empty + 8 * vh, (j - 1) & 1, p.err, abort)) break;
       tc_fence_after();
-      dequant_v<VT>(base + SM::kVRing + slot * SM::kVStage, quarter, lefts[j & (kTiles - 1)] - kStageKeys * vh,
+      dequant_v<VT>(base + SM::kVRing + slot * SM::kVStage, quarter, live_keys(p, lefts[j & (kTiles - 1)], kStageKeys * vh),
                     kVCol + 64 * vh + t_lane, lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(vraw_empty + 8 * slot);
@@ -1068,16 +1093,26 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
       const bool first_tile = (info >> 8) & 1;
       const uint32_t s_at = s_addr + 64 * (j & 1), p_to = p_addr + (j & 1) * SM::kPBytes;
       const bool has_wide = KT != PA_F16 && info >> (12 + quarter) & 1;
-      if (tl.open < kKeys || has_wide) {
+      if (has_edge(p, tl) || has_wide) {
         // The edge: what a row does not see becomes -inf in tensor memory, so that
         // the code of the other tiles has no mask in it.  Row r sees key k when r >= 6
         // (k - open + 1) (suffix) or k < open.  And the logits of wide keys.
         const uint32_t wide = has_wide ? wide_keys[4 * (j & 3) + quarter] >> (16 * hh) : 0u;
         const float fa = wide >> g & 1 ? 256.f : 1.f, fb = wide >> (g + 8) & 1 ? 256.f : 1.f;
-        const int ka = tile_key + key16(g) - tl.open, kb = tile_key + key16(g + 8) - tl.open;
-        const bool causal = (info >> 10) & 1;
-        int la = causal ? kGqa * (ka + 1) - tl.row0 - t2 : ka < 0 ? -kRows : kRows,
-            lb = causal ? kGqa * (kb + 1) - tl.row0 - t2 : kb < 0 ? -kRows : kRows;
+        int la, lb;                   // the first row that sees the key, less this thread's column
+        [[maybe_unused]] int ua, ub;  // of a window: the first one after those that see it
+        if constexpr (P::kWindow) {
+          const int2 a = rows_that_see(p, tl, tile_key + key16(g)), b = rows_that_see(p, tl, tile_key + key16(g + 8));
+          la = a.x - t2;
+          ua = a.y - t2;
+          lb = b.x - t2;
+          ub = b.y - t2;
+        } else {
+          const int ka = tile_key + key16(g) - tl.open, kb = tile_key + key16(g + 8) - tl.open;
+          const bool causal = (info >> 10) & 1;
+          la = causal ? kGqa * (ka + 1) - tl.row0 - t2 : ka < 0 ? -kRows : kRows;
+          lb = causal ? kGqa * (kb + 1) - tl.row0 - t2 : kb < 0 ? -kRows : kRows;
+        }
 #pragma unroll 1
         for (int c = 0; c < nc; ++c) {
           uint32_t x[8];
@@ -1085,12 +1120,20 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
           tmem_ld_wait();
           loaded(x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            x[i] = 8 * (i >> 2) + (i & 1) < ((i & 2) ? lb : la) ? 0xff800000u  // -inf
-                                                                : __float_as_uint(__uint_as_float(x[i]) * ((i & 2) ? fb : fa));
+          for (int i = 0; i < 8; ++i) {
+            const int r = 8 * (i >> 2) + (i & 1);
+            bool hidden = r < ((i & 2) ? lb : la);
+            if constexpr (P::kWindow) hidden |= r >= ((i & 2) ? ub : ua);
+            x[i] = hidden ? 0xff800000u  // -inf
+                          : __float_as_uint(__uint_as_float(x[i]) * ((i & 2) ? fb : fa));
+          }
           tmem_st_frag2(s_at + 16 * c, x);
           la -= 16;
           lb -= 16;
+          if constexpr (P::kWindow) {
+            ua -= 16;
+            ub -= 16;
+          }
         }
         tmem_st_wait();
       }
@@ -1228,6 +1271,12 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
           tmem_ld16(from + r, o);
           tmem_ld_wait();
           loaded(o);
+          if constexpr (P::kWindow) {
+            if (t.slot_row < 0) {  // the whole segment: the result
+              write_out(p, t, r, rows, reinterpret_cast<const float*>(smem + SM::kInv), 128 * hh + 32 * quarter + v_dim<VT>(lane), o);
+              continue;
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (r + i < rows) dst[(r + i) * kD] = __uint_as_float(o[i]);
@@ -1257,7 +1306,16 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
           float v = red[st];
 #pragma unroll
           for (int i = 1; i < 8; ++i) v += red[i * kRows + st];
-          p.part_ml[(long long)tl.slot_row + st] = make_float2(-nref[st], v);
+          bool result = false;
+          if constexpr (P::kWindow) {
+            result = tl.slot_row < 0;
+            if (result) reinterpret_cast<float*>(smem + SM::kInv)[st] = finish_row(p, tl, st, -nref[st], v);
+          }
+          if (!result) p.part_ml[(long long)tl.slot_row + st] = make_float2(-nref[st], v);
+        }
+        if constexpr (P::kWindow) {
+          __syncwarp();
+          named_bar_sync(1, kSmThreads);
         }
       }
     }
@@ -1275,10 +1333,12 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
   }
 }
 
-struct KernelInfo {
-  void (*fn)(Params);
+template <class P>
+struct KernelOf {
+  void (*fn)(P);
   int smem;
 };
+using KernelInfo = KernelOf<Params>;
 
 #define PA_DECLARE_PREFIX(k, v) bool lookup_prefix_kernel_##k##_##v(KernelInfo* out);
 PA_DECLARE_PREFIX(1, 1) PA_DECLARE_PREFIX(1, 2) PA_DECLARE_PREFIX(1, 8)

@@ -12,7 +12,7 @@
 namespace pa_prefix {
 
 bool PA_PREFIX_NAME(PA_KT, PA_VT)(KernelInfo* out) {
-  *out = KernelInfo{pa_prefix_kernel<PA_KT, PA_VT>, Smem<PA_KT, PA_VT>::kLaunch};
+  *out = KernelInfo{pa_prefix_kernel<PA_KT, PA_VT, Params>, Smem<PA_KT, PA_VT>::kLaunch};
   return true;
 }
 

@@ -1,0 +1,168 @@
+// Checks the plan of the windowed attention on the host: the units, the ranges and the cuts
+// that pa_window.cu makes, and what pa_window_impl.cuh derives from them for a tile (key
+// order, masks, live keys, slots), against the definition, over random batches.
+#include <cstdio>
+#include <cstdlib>
+#include <map>
+#include <random>
+#include <set>
+#include <tuple>
+
+#include "pa_window.cu"
+
+static long long bad = 0;
+#define CHECK(x)                                         \
+  do {                                                   \
+    if (!(x)) {                                          \
+      if (++bad <= 20) std::printf("line %d: %s (batch %d)\n", __LINE__, #x, batch); \
+    }                                                    \
+  } while (0)
+
+int main(int argc, char** argv) {
+  const int batches = argc > 1 ? std::atoi(argv[1]) : 300;
+  std::mt19937 rng(7);
+  auto pick = [&](long long lo, long long hi) { return (int)(lo + (long long)(rng() % (unsigned long long)(hi - lo + 1))); };
+  static WindowParams p;
+  static MergeParams m;
+  for (int batch = 0; batch < batches; ++batch) {
+    const bool big = batch % 50 == 49;  // more units than one launch takes
+    const int n_seq = big ? pick(300, 700) : pick(1, 12), max_ctas = pick(1, 3) == 1 ? pick(1, 7) : 152;
+    const int win[] = {1, 2, 15, 16, 17, pick(1, 300), pick(1, 3000), kAllKeys}, snk[] = {0, 0, 1, 4, 16, 17, pick(0, 300), kAllKeys};
+    p.window = win[pick(0, 7)];
+    p.sinks = snk[pick(0, 7)];
+    p.n_kv_heads = pick(1, 4);
+    std::vector<int32_t> lens(n_seq), fresh(n_seq);
+    uint32_t most = 0;
+    long long tokens = 0;
+    for (int i = 0; i < n_seq; ++i) {
+      fresh[i] = pick(0, 3) == 0 ? 0 : pick(0, 2) == 0 && !big ? pick(1, 120) : pick(1, 8);
+      lens[i] = fresh[i] + (pick(0, 2) == 0 ? pick(0, 5) : pick(0, big ? 300 : 4000));
+      most = std::max(most, (uint32_t)fresh[i]);
+      tokens += fresh[i];
+    }
+    p.slot_rows = m.slot_rows = slot_rows_of(most);
+    std::map<std::tuple<int, int, int>, int> rows_seen;  // (sequence, head, query row) -> times
+    Cursor at{0, 0, 0};
+    int launches = 0;
+    while (at.seq < (uint32_t)n_seq) {
+      const Cursor before = at;
+      const Plan plan = plan_chunk(p, m, lens.data(), fresh.data(), n_seq, max_ctas, &at);
+      CHECK(at.seq > before.seq || at.rt > before.rt);
+      if (at.seq == before.seq && at.rt == before.rt) return 1;
+      if (p.n_units == 0) continue;
+      ++launches;
+      CHECK(p.n_units <= kMaxUnits && p.n_ctas >= 1 && p.n_ctas <= max_ctas && plan.cuts < kMaxCtas);
+      std::map<std::pair<int, int>, std::pair<int, int>> pieces;  // (unit, head) -> (first CTA, pieces) where cut
+      int tile = 0;
+      std::set<int> slots;
+      std::vector<int> next_j((size_t)p.n_units * p.n_kv_heads, 0);
+      for (int cta = 0; cta < p.n_ctas; ++cta) {
+        const int x0 = (int)((long long)cta * p.total_len / p.n_ctas), x1 = (int)((long long)(cta + 1) * p.total_len / p.n_ctas);
+        Pos t = locate(p, x0);
+        const int end = x1 < p.total_len ? locate(p, x1).tile : p.total_tiles;
+        CHECK(t.tile == tile && end > tile);
+        for (bool fresh_seg = t.j == 0; tile < end; ++tile) {
+          CHECK(t.unit < p.n_units && t.head < p.n_kv_heads);
+          const Unit& u = p.unit[t.unit];
+          CHECK(next_j[(size_t)t.unit * p.n_kv_heads + t.head]++ == t.j);
+          const Span s = span_of(u, p.window, p.sinks);
+          const int key0 = t.j * kKeys, last_pos = u.pos + (unit_row0(u) + unit_rows(u) - 1) / kGqa;
+          const bool ends = t.j + 1 == t.nt, last = ends || tile + 1 == end;
+          if (last) {
+            const int slot = slot_of(fresh_seg, ends, cta, p.slot_rows);
+            CHECK((slot < 0) == (fresh_seg && ends));
+            if (slot >= 0) {
+              CHECK(slots.insert(slot).second && slot + unit_rows(u) <= 2 * p.n_ctas * p.slot_rows && slot % p.slot_rows == 0);
+              auto& pc = pieces[{t.unit, t.head}];
+              if (pc.second == 0) pc.first = cta;
+              CHECK(pc.first + pc.second == cta && slot == (2 * cta + (pc.second == 0 ? 1 : 0)) * p.slot_rows);
+              ++pc.second;
+            }
+          }
+          // every tile of a few heads, the masks of a few tiles
+          if (t.head == 0 && (big ? pick(0, 30) == 0 : true)) {
+            const int last_lo = last_pos >= p.window ? last_pos - p.window + 1 : 0;
+            const bool inner = sees_all(s, key0, u.pos, last_lo, p.sinks);
+            Tile tl{};
+            tl.open = u.pos;
+            tl.row0 = unit_row0(u);
+            tl.pad[0] = key0;
+            tl.pad[1] = s.shift;
+            const WindowKeys live = live_keys(p, live_of(s, key0, p.sinks), 0);
+            bool all_live = true;
+            for (int k = 0; k < kKeys; ++k) {
+              const int v = key0 + k, key = v < s.s16 ? v : v + s.shift;
+              const int2 see = rows_that_see(p, tl, k);
+              bool any = false, all = true;
+              for (int r = 0; r < unit_rows(u); ++r) {
+                const int pos = u.pos + (unit_row0(u) + r) / kGqa;
+                const bool sees = v < s.end && key <= pos && ((long long)key > (long long)pos - p.window || key < p.sinks);
+                if (v < s.end) CHECK(sees == (r >= see.x && r < see.y));
+                else CHECK(!(r >= see.x && r < see.y));
+                any |= sees;
+                all &= sees;
+              }
+              CHECK(live.has(k) == any || (live.has(k) && v < s.end && key <= last_pos));
+              if (any) CHECK(live.has(k));
+              if (!live.has(k)) all_live = false;
+              if (inner) CHECK(all);
+              if (live.has(k)) CHECK(key < u.len);
+            }
+            for (int h = 0; h < 2; ++h) {
+              const WindowKeys half = live_keys(p, live_of(s, key0, p.sinks), kStageKeys * h);
+              bool every = true;
+              for (int k = 0; k < kStageKeys; ++k) {
+                every &= half.has(k);
+                CHECK(half.has(k) == live.has(kStageKeys * h + k));
+              }
+              CHECK(!half.all() || every);
+            }
+            (void)all_live;
+          }
+          if (t.j == 0) {
+            for (int r = 0; r < unit_rows(u); ++r) {
+              const int tok = u.token + (unit_row0(u) + r) / kGqa;
+              ++rows_seen[{u.seq, t.head, tok * kGqa + (unit_row0(u) + r) % kGqa}];
+            }
+            // a row's visible keys are all in the order, and its first one in the first tile of any piece with one
+            for (int r = 0; r < unit_rows(u); r += 7) {
+              const int pos = u.pos + (unit_row0(u) + r) / kGqa, lo = pos >= p.window ? pos - p.window + 1 : 0;
+              CHECK(lo >= s.lo && pos - s.shift < s.end && (s.shift == 0 || lo >= s.s16 + s.shift));
+              CHECK(lo - s.shift - (s.lo - s.shift) < kKeys - kGroup);
+            }
+          }
+          if (tile + 1 < end) {
+            const int unit = t.unit, head = t.head;
+            advance(p, t);
+            if (t.unit != unit || t.head != head) fresh_seg = true;
+          }
+        }
+      }
+      CHECK(tile == p.total_tiles);
+      for (size_t i = 0; i < next_j.size(); ++i)
+        CHECK(next_j[i] == tiles_of(p.unit[i / p.n_kv_heads], p.window, p.sinks));
+      CHECK((int)pieces.size() == plan.cuts);
+      for (int i = 0; i < plan.cuts; ++i) {
+        const Cut& c = m.cut[i];
+        bool found = false;
+        for (const auto& [key, pc] : pieces) {
+          const Unit& u = p.unit[key.first];
+          if (u.seq == c.seq && u.token == c.token && u.rows_row0 == c.rows_row0 && key.second == c.head) {
+            found = true;
+            CHECK(pc.first == c.cta && pc.second == c.n && u.len == c.len && unit_rows(u) <= plan.rows);
+          }
+        }
+        CHECK(found);
+      }
+    }
+    long long rows = 0;
+    for (const auto& r : rows_seen) {
+      CHECK(r.second == 1);
+      ++rows;
+    }
+    CHECK(rows == tokens * kGqa * p.n_kv_heads);
+    if (big) CHECK(launches >= 1);
+  }
+  std::printf("mismatches %lld\n", bad);
+  return bad != 0;
+}
