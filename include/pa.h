@@ -169,6 +169,29 @@ pa_status pa_cow_blocks(pa_pool* pool, const pa_block* handles, uint32_t n, pa_b
 pa_status pa_copy_blocks(const pa_pool* pool, void* k_pool, void* v_pool, const int32_t* src,
                          const int32_t* dst, uint32_t n, int32_t* err, pa_stream_t stream);
 
+/* Bring the live blocks to the front of the pool: with m of them, those at m or behind
+ * move, in order, into the free places before m (the lowest first).  Writes a
+ * pair of handles for each into old_handles (ascending by index) and new_handles
+ * (host arrays of `capacity`), *n_moves of them; a moved block keeps its references, its old
+ * handle is stale from then on.  The free blocks are the last n_blocks - m, handed out from m
+ * on.  The caller puts the new handles in the old ones' place and moves the rows
+ * (pa_move_blocks, whose src and dst are the handles' indices: their low 32
+ * bits) before the blocks are used again.  PA_ERR_INVALID when capacity is less than *n_moves
+ * (which is written): nothing changes. */
+pa_status pa_compact_blocks(pa_pool* pool, uint32_t capacity, pa_block* old_handles, pa_block* new_handles,
+                            uint32_t* n_moves);
+
+/* Device half of a compaction: copy whole blocks from src[i] to dst[i], i < n, as
+ * pa_copy_blocks, and rewrite tables in the same launch: table_out[e] is dst[i]
+ * where table[e] is a src[i], else table[e] (whatever it is), e < n_entries.
+ * src, dst, table, table_out: device int32; table_out may be table (other overlaps
+ * race), n_entries 0 for none.  With entries, src ascends (*err = PA_ERR_INVALID
+ * where it does not, and then the tables are not to be used).  No block may be
+ * both in src and in dst: such pairs race. */
+pa_status pa_move_blocks(const pa_pool* pool, void* k_pool, void* v_pool, const int32_t* src, const int32_t* dst,
+                         uint32_t n, const int32_t* table, int32_t* table_out, uint64_t n_entries, int32_t* err,
+                         pa_stream_t stream);
+
 /* ------------------------------------------------------------------ append
  * New rows are uploaded once, packed, and a kernel scatters them into their
  * page slots (colibri PR #372, Summary: one packed transfer of the newly
@@ -294,6 +317,38 @@ pa_status pa_append_rows_rope(const pa_pool* pool, void* k_pool, void* v_pool, c
 pa_status pa_read_rows(const pa_pool* pool, const void* k_pool, const void* v_pool, const int32_t* row_seq,
                        const int32_t* row_pos, uint32_t n_rows, const int32_t* block_table, uint32_t table_stride,
                        uint32_t n_seq, void* k_out, void* v_out, int32_t out_type, int32_t* err, pa_stream_t stream);
+
+/* Rows of the cache moved to other places: row i of sequence src_seq[i], position
+ * src_pos[i] (through src_table) to dst_seq[i], dst_pos[i] (through dst_table,
+ * which may be src_table), K and V.  For dropping the middle of a context, keeping the accepted
+ * ones of drafted tokens, giving a fork its own copy of a page's first rows, or changing the
+ * frequencies of a live cache.
+ *
+ * All rows are read before any is written, so that rows may land where others come
+ * from.  Two rows with the same destination race.  disjoint 1: the caller vouches
+ * that no row's destination is another row's source (its own is fine); one launch less.
+ *
+ * rope:     host, or NULL: rows are copied byte for byte.  Else keys are turned by
+ *           the difference of dst_pos's angles under rope and src_pos's under rope_from
+ *           (NULL: rope), and multiplied by the ratio of their attn_factors where they
+ *           are turned; eps and weight_offset are not used.  rope_from has rope's
+ *           rot_dim and interleaved.  A turned key is dequantised, turned in fp32 and stored by
+ *           the rule of pa_append_rows_f16 in blocks of 32 values; blocks from rot_dim
+ *           on, keys whose position and rope stay, and V are copied byte for byte.
+ * src_table, dst_table: device int32 [n_seq][stride] each.
+ * workspace: 16-byte aligned scratch of ws_bytes >= pa_move_rows_workspace_size(); not
+ *           used with disjoint.
+ * A row of which one place is out of range is not moved and sets *err = PA_ERR_BOUNDS. */
+pa_status pa_move_rows(const pa_pool* pool, void* k_pool, void* v_pool, const pa_rope_desc* rope,
+                       const pa_rope_desc* rope_from, const int32_t* src_seq, const int32_t* src_pos,
+                       const int32_t* dst_seq, const int32_t* dst_pos, uint32_t n_rows, const int32_t* src_table,
+                       uint32_t src_stride, uint32_t src_n_seq, const int32_t* dst_table, uint32_t dst_stride,
+                       uint32_t dst_n_seq, int32_t disjoint, void* workspace, size_t ws_bytes, int32_t* err,
+                       pa_stream_t stream);
+
+/* Scratch bytes pa_move_rows needs for n_rows rows that are not disjoint: 0 while they are few
+ * (256 rows of 4 KV heads), else as many as the rows have. */
+size_t pa_move_rows_workspace_size(const pa_pool* pool, uint32_t n_rows);
 
 /* ------------------------------------------------------------------ decode
  * Single-step GQA decode attention over a paged cache: split-K flash decoding

@@ -22,7 +22,7 @@ __all__ = [
     "pa_decode_workspace_size", "pa_decode_plan", "pa_get_error", "pa_selftest_wait_timeout", "status_name",
     "library_path", "pa_decode_noalloc", "PA_DT_F32", "PA_DT_F16", "PA_DT_BF16", "RopeDesc", "dtype_number",
     "pa_norm_rope", "pa_append_rows_rope", "pa_read_rows", "pa_decode_prefix", "pa_decode_prefix_workspace_size",
-    "pa_attend_window", "pa_attend_window_workspace_size",
+    "pa_attend_window", "pa_attend_window_workspace_size", "pa_move_rows", "pa_move_rows_workspace_size", "pa_move_blocks",
 ]
 
 PA_F16, PA_Q4_0, PA_Q8_0 = 1, 2, 8
@@ -37,7 +37,8 @@ EXPORTS = ["pa_pool_create", "pa_pool_destroy", "pa_pool_get_desc", "pa_row_byte
            "pa_cow_blocks", "pa_copy_blocks", "pa_append_rows", "pa_append_rows_f16",
            "pa_decode", "pa_decode_split", "pa_decode_merge", "pa_decode_workspace_size", "pa_decode_plan", "pa_get_error", "pa_status_string",
            "pa_selftest_wait_timeout", "pa_decode_noalloc", "pa_norm_rope", "pa_append_rows_rope", "pa_read_rows",
-           "pa_decode_prefix", "pa_decode_prefix_workspace_size", "pa_attend_window", "pa_attend_window_workspace_size"]
+           "pa_decode_prefix", "pa_decode_prefix_workspace_size", "pa_attend_window", "pa_attend_window_workspace_size",
+           "pa_compact_blocks", "pa_move_blocks", "pa_move_rows", "pa_move_rows_workspace_size"]
 
 
 class PaError(RuntimeError):
@@ -116,6 +117,10 @@ def load():
             "pa_attend_window": (C.c_int, [vp, vp, i64, i32, vp, vp, vp, u32, vp, vp, vp, u32, u32, u32, u32, C.c_float, vp,
                                            i64, i32, vp, vp, sz, vp, vp]),
             "pa_attend_window_workspace_size": (sz, [vp, u32, C.c_int]),
+            "pa_compact_blocks": (C.c_int, [vp, u32, vp, vp, C.POINTER(u32)]),
+            "pa_move_blocks": (C.c_int, [vp, vp, vp, vp, vp, u32, vp, vp, C.c_uint64, vp, vp]),
+            "pa_move_rows": (C.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp, u32, vp, u32, u32, vp, u32, u32, i32, vp, sz, vp, vp]),
+            "pa_move_rows_workspace_size": (sz, [vp, u32]),
         }
         sig["pa_decode_split"] = sig["pa_decode_merge"] = sig["pa_decode"]
         for name, (res, args) in sig.items():
@@ -260,6 +265,21 @@ class Pool:
         if rc != PA_OK:
             return rc, [], []
         return rc, list(out[:len(handles)]), [(src[i], dst[i]) for i in range(nc.value)]
+
+
+    def compact(self) -> list[tuple[int, int]]:
+        """Brings the live blocks to the front; returns the moved blocks' (old handle, new handle), ascending by
+        the old index.  The caller then moves their rows (pa_move_blocks, by the handles' low 32 bits) and
+        puts the new handles in the old ones' place."""
+        n = C.c_uint32(0)
+        while True:
+            k = n.value
+            old, new = (C.c_uint64 * max(k, 1))(), (C.c_uint64 * max(k, 1))()
+            rc = int(load().pa_compact_blocks(self._h, k, old, new, C.byref(n)))
+            if rc == PA_OK:
+                return list(zip(old[:n.value], new[:n.value]))
+            if n.value <= k:  # not for the arrays' size
+                raise PaError(rc, "pa_compact_blocks")
 
 
 def pa_append_rows(pool: Pool, k_pool, v_pool, k_rows, v_rows, row_seq, row_pos, n_rows: int, block_table,
@@ -411,3 +431,23 @@ def pa_attend_window(pool: Pool, q, q_stride: int, q_type: int, k_pool, v_pool, 
     if check:
         _check(rc, "pa_attend_window")
     return rc
+
+
+def pa_move_blocks(pool: Pool, k_pool, v_pool, src, dst, n: int, table, table_out, n_entries: int, err, stream=None) -> None:
+    """Copy whole blocks src[i] -> dst[i] in both pools and write tables with the new indices (src ascending)."""
+    _check(load().pa_move_blocks(pool.handle, _ptr(k_pool), _ptr(v_pool), _ptr(src), _ptr(dst), n, _ptr(table),
+                                 _ptr(table_out), n_entries, _ptr(err), _stream(stream)), "pa_move_blocks")
+
+
+def pa_move_rows_workspace_size(pool: Pool, n_rows: int) -> int:
+    return int(load().pa_move_rows_workspace_size(pool.handle, n_rows))
+
+
+def pa_move_rows(pool: Pool, k_pool, v_pool, rope: int | None, rope_from: int | None, src_seq, src_pos, dst_seq, dst_pos,
+                 n_rows: int, src_table, src_stride: int, src_n_seq: int, dst_table, dst_stride: int, dst_n_seq: int,
+                 disjoint: bool, workspace, ws_bytes: int, err, stream=None) -> None:
+    """Rows moved to other places, keys turned to them (rope, rope_from: addresses of RopeDescs, or None)."""
+    _check(load().pa_move_rows(pool.handle, _ptr(k_pool), _ptr(v_pool), rope, rope_from, _ptr(src_seq), _ptr(src_pos),
+                               _ptr(dst_seq), _ptr(dst_pos), n_rows, _ptr(src_table), src_stride, src_n_seq,
+                               _ptr(dst_table), dst_stride, dst_n_seq, int(disjoint), _ptr(workspace), ws_bytes, _ptr(err),
+                               _stream(stream)), "pa_move_rows")

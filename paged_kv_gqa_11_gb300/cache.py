@@ -90,6 +90,29 @@ class PagedKVCache:
         return load_calls().read_rows(self.pool.address, self.n_kv_heads, self.k_pool, self.v_pool, row_seq, row_pos,
                                      block_table, dtype, k_out, v_out, self.err, stream)
 
+    # ------------------------------------------------------------ moving
+    def move_rows(self, src_seq: torch.Tensor, src_pos: torch.Tensor, dst_seq: torch.Tensor, dst_pos: torch.Tensor,
+                  block_table: torch.Tensor, dst_table: torch.Tensor | None = None, rope: Rope | None = None,
+                  rope_from: Rope | None = None, disjoint: bool = False, workspace: torch.Tensor | None = None, stream=None) -> None:
+        """Rows (src_seq, src_pos) moved to (dst_seq, dst_pos), int32 [n] each, through
+        block_table (the destinations through dst_table, if given).  All rows are
+        read before any is written; disjoint: no row's destination is another's
+        source (the caller's word; a launch less).  With a rope, keys are turned from
+        their old position's angles (under rope_from, or rope) to the new one's
+        and stored anew; without one, rows keep their bytes.  Workspace and
+        stream: as decode_prefix."""
+        load_calls().move_rows(self.pool.address, self.k_pool, self.v_pool, rope.address if rope is not None else 0,
+                               rope_from.address if rope_from is not None else 0, src_seq, src_pos, dst_seq, dst_pos, block_table,
+                               dst_table, disjoint, workspace, self.err, stream)
+
+    def move_blocks(self, src: torch.Tensor, dst: torch.Tensor, block_table: torch.Tensor | None = None,
+                    table_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+        """Whole blocks src[i] copied to dst[i] (int32 [n]; none in both; src ascending if
+        there is a table), and the table with dst[i] for every src[i] (into table_out, which
+        may be the table, or a new tensor), which is returned: the device half of
+        Pool.compact."""
+        return load_calls().move_blocks(self.pool.address, self.k_pool, self.v_pool, src, dst, block_table, table_out, self.err, stream)
+
     # ------------------------------------------------------------ decode
     def workspace(self, n_seq: int, n_qtok: int) -> torch.Tensor:
         dev = self._device_index()

@@ -476,6 +476,78 @@ PyObject* attend_window(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
+// (pool, k_pool, v_pool, rope, rope_from, src_seq, src_pos, dst_seq, dst_pos, table, dst_table, disjoint, workspace, err,
+//  stream) -> None
+PyObject* move_rows(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded(n_args, 15, [&]() -> PyObject* {
+    const auto* pool = static_cast<const pa_pool*>(address(a[0], "pool"));
+    const at::Tensor &kp = tensor(a[1], "k_pool"), &vp = tensor(a[2], "v_pool"), &from_seq = tensor(a[5], "src_seq"),
+                     &from = tensor(a[6], "src_pos"), &to_seq = tensor(a[7], "dst_seq"), &to = tensor(a[8], "dst_pos"),
+                     &table = tensor(a[9], "block_table"), &other = tensor(a[10], "dst_table", true), &err = tensor(a[13], "err");
+    const auto* rope = static_cast<const pa_rope_desc*>(address(a[3], "rope"));
+    const auto* was = static_cast<const pa_rope_desc*>(address(a[4], "rope_from"));
+    at::Tensor ws = tensor(a[12], "workspace", true);
+    const int dev = kp.get_device();
+    const int64_t n = from_seq.dim() == 1 ? from_seq.size(0) : 0;
+    index(from_seq, n, "src_seq"); index(from, n, "src_pos"); index(to_seq, n, "dst_seq"); index(to, n, "dst_pos");
+    block_table(table);
+    if (other.defined()) block_table(other);
+    const at::Tensor& dst_table = other.defined() ? other : table;
+    on(dev, vp, "v_pool"); on(dev, from_seq, "src_seq"); on(dev, from, "src_pos"); on(dev, to_seq, "dst_seq"); on(dev, to, "dst_pos");
+    on(dev, table, "block_table"); on(dev, other, "dst_table"); on(dev, ws, "workspace"); on(dev, err, "err");
+    const int disjoint = PyObject_IsTrue(a[11]);
+    if (disjoint < 0) {
+      PyErr_Clear();
+      refuse("disjoint: true or false");
+    }
+    check(n <= UINT32_MAX && table.size(0) <= INT32_MAX && table.size(1) <= INT32_MAX && dst_table.size(0) <= INT32_MAX &&
+              dst_table.size(1) <= INT32_MAX,
+          "rows and tables");
+    const Place place(dev, a[14]);
+    place.uses({&kp, &vp, &from_seq, &from, &to_seq, &to, &table, &other, &ws, &err});
+    if (!disjoint && !ws.defined()) {
+      const size_t bytes = pa_move_rows_workspace_size(pool, (uint32_t)n);
+      if (bytes > 0) ws = at::empty({(int64_t)bytes}, kp.options().dtype(at::kByte));
+    }
+    check(!ws.defined() || ws.is_contiguous(), "workspace: contiguous");
+    status(pa_move_rows(pool, ptr(kp), ptr(vp), rope, was, from_seq.data_ptr<int32_t>(), from.data_ptr<int32_t>(), to_seq.data_ptr<int32_t>(),
+                        to.data_ptr<int32_t>(), (uint32_t)n, table.data_ptr<int32_t>(), (uint32_t)table.size(1), (uint32_t)table.size(0),
+                        dst_table.data_ptr<int32_t>(), (uint32_t)dst_table.size(1), (uint32_t)dst_table.size(0), disjoint, ptr(ws),
+                        ws.defined() ? (size_t)ws.nbytes() : 0, err.data_ptr<int32_t>(), place.stream),
+           "pa_move_rows");
+    Py_RETURN_NONE;
+  });
+}
+
+// (pool, k_pool, v_pool, src, dst, table, table_out, err, stream) -> table_out
+PyObject* move_blocks(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded(n_args, 9, [&]() -> PyObject* {
+    const auto* pool = static_cast<const pa_pool*>(address(a[0], "pool"));
+    const at::Tensor &kp = tensor(a[1], "k_pool"), &vp = tensor(a[2], "v_pool"), &src = tensor(a[3], "src"), &dst = tensor(a[4], "dst"),
+                     &table = tensor(a[5], "block_table", true), &err = tensor(a[7], "err");
+    at::Tensor out = tensor(a[6], "table_out", true);
+    const int dev = kp.get_device();
+    const int64_t n = src.dim() == 1 ? src.size(0) : 0;
+    index(src, n, "src"); index(dst, n, "dst");
+    if (table.defined()) block_table(table);
+    check(table.defined() || !out.defined(), "table_out without block_table");
+    on(dev, vp, "v_pool"); on(dev, src, "src"); on(dev, dst, "dst"); on(dev, table, "block_table"); on(dev, out, "table_out"); on(dev, err, "err");
+    check(n <= INT32_MAX, "blocks");
+    const Place place(dev, a[8]);
+    place.uses({&kp, &vp, &src, &dst, &table, &out, &err});
+    if (table.defined() && !out.defined()) out = place.made(at::empty(table.sizes(), table.options()));
+    if (out.defined()) {
+      same_shape(table, out, "table_out of the table's shape");
+      check(out.scalar_type() == at::kInt && out.is_contiguous(), "table_out: int32, contiguous");
+    }
+    status(pa_move_blocks(pool, ptr(kp), ptr(vp), src.data_ptr<int32_t>(), dst.data_ptr<int32_t>(), (uint32_t)n,
+                          table.defined() ? table.data_ptr<int32_t>() : nullptr, out.defined() ? out.data_ptr<int32_t>() : nullptr,
+                          table.defined() ? (uint64_t)table.numel() : 0, err.data_ptr<int32_t>(), place.stream),
+           "pa_move_blocks");
+    return wrap(out);
+  });
+}
+
 PyObject* set_error(PyObject*, PyObject* e) {
   Py_INCREF(e);
   Py_XDECREF(g_error);
@@ -489,6 +561,8 @@ PyMethodDef g_methods[] = {
     {"read_rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(read_rows)), METH_FASTCALL, ""},
     {"decode_prefix", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(decode_prefix)), METH_FASTCALL, ""},
     {"attend_window", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(attend_window)), METH_FASTCALL, ""},
+    {"move_rows", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(move_rows)), METH_FASTCALL, ""},
+    {"move_blocks", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(move_blocks)), METH_FASTCALL, ""},
     {"set_error", set_error, METH_O, ""},
     {nullptr, nullptr, 0, nullptr}};
 

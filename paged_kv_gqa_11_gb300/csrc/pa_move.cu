@@ -1,0 +1,539 @@
+// Rows and blocks of a cache moved within its pools (pa_move_rows, pa_move_blocks,
+// pa_copy_blocks).
+//
+// Mathematics.  A key at position p was turned by the angles p f of its pairs; at position
+// p' under frequencies f' it is to be turned by p' f' - p f more.  The difference is taken
+// in 64-bit fixed-point turns, like the angles themselves (pa_row_ops.cuh), so far
+// positions lose nothing.  A turned block of 32 values is dequantised, turned and quantised
+// again by the rule of the append; all other bytes of a row stay what they are.
+//
+// Rows that land where others still have to be read: all reads come before all writes.  Few
+// rows stay in the registers of one cluster of CTAs between the two (its hardware barrier
+// is the only thing between them: one launch); more go through the workspace, in the pools'
+// formats, by two launches.  Where the caller vouches that no row's place is another row's
+// source, one launch reads and writes at once.
+//
+// Bound: the memory.  A warp moves a row's heads four at a time, all loads first.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "pa_row_ops.cuh"
+
+using namespace pa_rows_io;
+
+namespace {
+
+struct MoveParams {
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  uint8_t* ws;
+  const int32_t* src_seq;
+  const int32_t* src_pos;
+  const int32_t* dst_seq;
+  const int32_t* dst_pos;
+  const int32_t* src_table;
+  const int32_t* dst_table;
+  int32_t* err;
+  long long n_rows;
+  int n_heads, page_size, src_stride, src_seqs, dst_stride, dst_seqs, n_blocks, k_type, v_type;
+  int rows;         // of a warp
+  int rot, interleaved;
+  int still;        // a row that keeps its position is not turned
+  float factor;
+  uint64_t from[kMaxPairs], to[kMaxPairs];
+};
+
+// A row on its way: both places (head 0's group, in rows of the pool, and the row in it),
+// and whether its key is turned.
+struct Move {
+  long long src, dst;
+  int src_r, dst_r;
+  int src_pos, dst_pos;
+  bool ok, turned, same;  // same: both places are one
+};
+
+__device__ __forceinline__ Move move_of(const MoveParams& p, long long row) {
+  Move m{};
+  Place a{}, b{};
+  m.src_pos = __ldg(p.src_pos + row);
+  m.dst_pos = __ldg(p.dst_pos + row);
+  const bool has = place_of(p.src_table, p.src_stride, p.src_seqs, p.n_blocks, p.page_size, p.n_heads, __ldg(p.src_seq + row), m.src_pos, &a);
+  m.ok = place_of(p.dst_table, p.dst_stride, p.dst_seqs, p.n_blocks, p.page_size, p.n_heads, __ldg(p.dst_seq + row), m.dst_pos, &b) && has;
+  m.src = a.grp_row;
+  m.src_r = a.r;
+  m.dst = b.grp_row;
+  m.dst_r = b.r;
+  m.same = a.grp_row == b.grp_row && a.r == b.r;
+  m.turned = p.rot > 0 && !(p.still && m.src_pos == m.dst_pos);
+  return m;
+}
+
+__device__ __forceinline__ Move from_lane(const Move& m, int l) {
+  Move r;
+  r.src = __shfl_sync(0xffffffffu, m.src, l);
+  r.dst = __shfl_sync(0xffffffffu, m.dst, l);
+  r.src_r = __shfl_sync(0xffffffffu, m.src_r, l);
+  r.dst_r = __shfl_sync(0xffffffffu, m.dst_r, l);
+  r.src_pos = __shfl_sync(0xffffffffu, m.src_pos, l);
+  r.dst_pos = __shfl_sync(0xffffffffu, m.dst_pos, l);
+  const int f = __shfl_sync(0xffffffffu, (int)m.ok | (int)m.turned << 1 | (int)m.same << 2, l);
+  r.ok = f & 1;
+  r.turned = f >> 1 & 1;
+  r.same = f >> 2 & 1;
+  return r;
+}
+
+template <int T>
+__device__ __forceinline__ Packed get(const uint8_t* row, const Lane& at) {
+  if (T == PA_F16) return Packed{*reinterpret_cast<const uint4*>(row + at.body), 0u};
+  const uint2 w = *reinterpret_cast<const uint2*>(row + at.body);
+  return Packed{make_uint4(w.x, w.y, 0u, 0u), *reinterpret_cast<const uint16_t*>(row + at.scale)};
+}
+
+// The eight values of lane l that x holds.
+template <int T>
+__device__ __forceinline__ void values(const Packed& x, int l, float (&y)[8]) {
+  if (T == PA_F16) {
+    unpack8<__half>(&x.w, y);
+    return;
+  }
+  const float d = __half2float(__ushort_as_half((unsigned short)x.d));
+  const uint32_t w[2] = {x.w.x, x.w.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // bytes 0 .. 255 under 0x64 are the binary16 numbers 1024 + byte
+    const uint32_t u = T == PA_Q8_0 ? w[i] ^ 0x80808080u : (w[i] >> ((l & 2) << 1)) & 0x0f0f0f0fu;
+    const uint32_t bias = T == PA_Q8_0 ? 0xe480e480u : 0xe408e408u;  // -1152, -1032
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t h = hadd2(prmt(u, 0x64646464u, k ? 0x4342 : 0x4140), bias);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      y[4 * i + 2 * k] = f.x * d;
+      y[4 * i + 2 * k + 1] = f.y * d;
+    }
+  }
+}
+
+// A head's row turned by t: its turned blocks quantised anew, the others as they are.
+template <int T>
+__device__ __forceinline__ Packed turned(const MoveParams& p, const Packed& x, const Turn& t, int from, int lane) {
+  float a[8], b[8];
+  values<T>(x, lane, a);
+  if (p.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = a[i ^ 1];
+  } else {
+    Packed o;
+    o.w.x = __shfl_sync(0xffffffffu, x.w.x, from);
+    o.w.y = __shfl_sync(0xffffffffu, x.w.y, from);
+    o.w.z = T == PA_F16 ? __shfl_sync(0xffffffffu, x.w.z, from) : 0u;
+    o.w.w = T == PA_F16 ? __shfl_sync(0xffffffffu, x.w.w, from) : 0u;
+    o.d = T == PA_F16 ? 0u : __shfl_sync(0xffffffffu, x.d, from);
+    values<T>(o, from, b);
+  }
+  const bool mine = is_turned(p.rot, lane);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = unpack2(fma2(pack2(a[2 * i], a[2 * i + 1]), t.c[i], mul2(pack2(b[2 * i], b[2 * i + 1]), t.s[i])));
+    a[2 * i] = mine ? v.x : a[2 * i];
+    a[2 * i + 1] = mine ? v.y : a[2 * i + 1];
+  }
+  const Packed q = quantised(T, a, lane);
+  return 32 * (lane >> 2) < p.rot ? q : x;
+}
+
+__device__ __forceinline__ Turn turn_of(const MoveParams& p, const uint64_t* from_turns, const uint64_t* to_turns, const Move& m, int lane,
+                                        int from) {
+  return make_turn(
+      p.rot, p.interleaved, p.factor,
+      [&](int i) { return (uint64_t)(int64_t)m.dst_pos * to_turns[i] - (uint64_t)(int64_t)m.src_pos * from_turns[i]; }, lane, from);
+}
+
+// A row between its places in the pools: at ws, heads one after the other, each its chunks,
+// then its scales.
+__device__ __forceinline__ Lane lane_in_ws(int type, int lane) {
+  if (type == PA_F16) return Lane{16 * lane, 0};
+  return type == PA_Q8_0 ? Lane{8 * lane, Fmt<PA_Q8_0>::kRowQ + 2 * (lane >> 2)}
+                         : Lane{16 * (lane >> 2) + 8 * (lane & 1), Fmt<PA_Q4_0>::kRowQ + 2 * (lane >> 2)};
+}
+
+enum Phase { kDirect, kGather, kScatter };
+
+// The heads of one row of one pool.
+template <int T, int kPhase>
+__device__ __forceinline__ void move_heads(const MoveParams& p, uint8_t* pool, bool is_v, const Move& m, uint8_t* ws, const Turn* t,
+                                           int from, int lane) {
+  const long long step = (long long)p.page_size * Fmt<T>::kRow;
+  const uint8_t* src = kPhase == kScatter ? ws : pool + m.src * Fmt<T>::kRow;
+  uint8_t* dst = kPhase == kGather ? ws : pool + m.dst * Fmt<T>::kRow;
+  const long long src_step = kPhase == kScatter ? Fmt<T>::kRow : step, dst_step = kPhase == kGather ? Fmt<T>::kRow : step;
+  const Lane a = kPhase == kScatter ? lane_in_ws(T, lane) : lane_of(T, is_v, m.src_r, lane),
+             b = kPhase == kGather ? lane_in_ws(T, lane) : lane_of(T, is_v, m.dst_r, lane);
+  for (int h = 0; h < p.n_heads; h += 4) {
+    Packed x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (h + i < p.n_heads) x[i] = get<T>(src + (h + i) * src_step, a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (h + i >= p.n_heads) break;
+      if (kPhase != kScatter && t) x[i] = turned<T>(p, x[i], *t, from, lane);
+      put(T, x[i], dst + (h + i) * dst_step, b, lane);
+    }
+  }
+}
+
+template <int kPhase>
+__device__ __forceinline__ void move_row(const MoveParams& p, bool is_v, const Move& m, long long row, const uint64_t* from_turns,
+                                         const uint64_t* to_turns, int lane) {
+  const bool turns = !is_v && m.turned;
+  if (!m.ok || (m.same && !turns)) return;
+  const int type = is_v ? p.v_type : p.k_type, from = partner_lane(p.rot, p.interleaved, lane);
+  uint8_t* pool = is_v ? p.v_pool : p.k_pool;
+  const long long k_row = (long long)p.n_heads * row_bytes_of(p.k_type), v_row = (long long)p.n_heads * row_bytes_of(p.v_type);
+  uint8_t* ws = kPhase == kDirect ? nullptr : p.ws + (is_v ? p.n_rows * k_row + row * v_row : row * k_row);
+  Turn t;
+  if (kPhase != kScatter && turns) t = turn_of(p, from_turns, to_turns, m, lane, from);
+  const Turn* tp = turns ? &t : nullptr;
+  if (type == PA_F16) move_heads<PA_F16, kPhase>(p, pool, is_v, m, ws, tp, from, lane);
+  else if (type == PA_Q8_0) move_heads<PA_Q8_0, kPhase>(p, pool, is_v, m, ws, tp, from, lane);
+  else move_heads<PA_Q4_0, kPhase>(p, pool, is_v, m, ws, tp, from, lane);
+}
+
+__device__ __forceinline__ void load_turns(const MoveParams& p, uint64_t* from_turns, uint64_t* to_turns) {
+  for (int i = threadIdx.x; i < p.rot / 2; i += blockDim.x) {
+    from_turns[i] = p.from[i];
+    to_turns[i] = p.to[i];
+  }
+  __syncthreads();
+}
+
+template <int kPhase>
+__global__ void __launch_bounds__(32 * kWarps) pa_move_kernel(const __grid_constant__ MoveParams p) {
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
+  __shared__ uint64_t from_turns[kMaxPairs], to_turns[kMaxPairs];
+  const int lane = threadIdx.x & 31;
+  load_turns(p, from_turns, to_turns);
+  const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const long long row0 = (item >> 1) * p.rows;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing that another kernel wrote is read before this
+  if (row0 >= p.n_rows) return;
+  const bool is_v = item & 1;
+  const int rows = (int)min((long long)p.rows, p.n_rows - row0);
+  Move m{};
+  if (lane < rows) {
+    m = move_of(p, row0 + lane);
+    if (!m.ok && !is_v && kPhase != kScatter) record_error(p.err, PA_ERR_BOUNDS);
+  }
+  for (int i = 0; i < rows; ++i) move_row<kPhase>(p, is_v, from_lane(m, i), row0 + i, from_turns, to_turns, lane);
+}
+
+// Few rows: every warp of a cluster reads up to kItems (row, pool, four heads), all warps
+// meet, every warp writes.
+constexpr int kItems = 4, kSmallWarps = 16, kMaxCluster = 8;
+
+template <int T>
+__device__ __forceinline__ void read_item(const MoveParams& p, const uint8_t* pool, bool is_v, const Move& m, int h0, const Turn* t,
+                                          int from, int lane, Packed (&x)[4]) {
+  const long long step = (long long)p.page_size * Fmt<T>::kRow;
+  const uint8_t* src = pool + m.src * Fmt<T>::kRow + h0 * step;
+  const Lane a = lane_of(T, is_v, m.src_r, lane);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (h0 + i < p.n_heads) x[i] = get<T>(src + i * step, a);
+  if (t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (h0 + i < p.n_heads) x[i] = turned<T>(p, x[i], *t, from, lane);
+  }
+}
+
+__global__ void __launch_bounds__(32 * kSmallWarps) pa_move_few_kernel(const __grid_constant__ MoveParams p) {
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
+  __shared__ uint64_t from_turns[kMaxPairs], to_turns[kMaxPairs];
+  const int lane = threadIdx.x & 31, from = partner_lane(p.rot, p.interleaved, lane);
+  load_turns(p, from_turns, to_turns);
+  const int quads = (p.n_heads + 3) / 4, warp = (int)blockIdx.x * kSmallWarps + (threadIdx.x >> 5), warps = (int)gridDim.x * kSmallWarps;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing that another kernel wrote is read before this
+  const int items = (int)p.n_rows * 2 * quads;
+  Packed x[kItems][4];
+  long long dst[kItems];
+  int dst_r[kItems];
+  uint32_t go = 0;  // items that are written
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int item = warp + k * warps;
+    if (item >= items) break;
+    const int row = item / (2 * quads), rest = item - row * 2 * quads, h0 = 4 * (rest >> 1);
+    const bool is_v = rest & 1;
+    const Move m = move_of(p, row);
+    if (!m.ok && rest == 0 && lane == 0) record_error(p.err, PA_ERR_BOUNDS);
+    const bool turns = !is_v && m.turned;
+    if (!m.ok || (m.same && !turns)) continue;
+    go |= 1u << k;
+    dst[k] = m.dst;
+    dst_r[k] = m.dst_r;
+    Turn t;
+    if (turns) t = turn_of(p, from_turns, to_turns, m, lane, from);
+    const Turn* tp = turns ? &t : nullptr;
+    const int type = is_v ? p.v_type : p.k_type;
+    const uint8_t* pool = is_v ? p.v_pool : p.k_pool;
+    if (type == PA_F16) read_item<PA_F16>(p, pool, is_v, m, h0, tp, from, lane, x[k]);
+    else if (type == PA_Q8_0) read_item<PA_Q8_0>(p, pool, is_v, m, h0, tp, from, lane, x[k]);
+    else read_item<PA_Q4_0>(p, pool, is_v, m, h0, tp, from, lane, x[k]);
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    if (!(go >> k & 1)) continue;
+    const int item = warp + k * warps, rest = item % (2 * quads), h0 = 4 * (rest >> 1);
+    const bool is_v = rest & 1;
+    const int type = is_v ? p.v_type : p.k_type;
+    const long long rb = row_bytes_of(type), step = (long long)p.page_size * rb;
+    uint8_t* to = (is_v ? p.v_pool : p.k_pool) + dst[k] * rb + h0 * step;
+    const Lane b = lane_of(type, is_v, dst_r[k], lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (h0 + i < p.n_heads) put(type, x[k][i], to + i * step, b, lane);
+  }
+}
+
+// ------------------------------------------------------------------ blocks
+
+// Whole blocks (every KV head's page, K and V) from src[i] to dst[i], and the tables' entries
+// src[i] as dst[i].  Chunks of 16 KB, 64 bytes a thread in flight; behind them the
+// tables' entries, each found in src (ascending) by bisection.
+struct BlockParams {
+  uint8_t* k_pool;
+  uint8_t* v_pool;
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* table;
+  int32_t* table_out;
+  int32_t* err;
+  long long k_bytes, v_bytes;  // of a block
+  long long entries;
+  long long chunks;            // of all pairs
+  int n, k_chunks, v_chunks;   // pairs; chunks of a block
+  int n_blocks;
+};
+
+constexpr int kBlockThreads = 256, kChunk = 16 * 4 * kBlockThreads;
+
+__global__ void __launch_bounds__(kBlockThreads) pa_move_blocks_kernel(const __grid_constant__ BlockParams p) {
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing that another kernel wrote is read before this
+  const int per = p.k_chunks + p.v_chunks;
+  const long long parts = p.chunks + (p.entries + kBlockThreads - 1) / kBlockThreads;
+  for (long long part = blockIdx.x; part < parts; part += gridDim.x) {
+    if (part >= p.chunks) {
+      const long long e = (part - p.chunks) * kBlockThreads + threadIdx.x;
+      if (e >= p.entries) continue;
+      const int x = __ldcg(p.table + e);
+      int lo = 0, hi = p.n;  // the first pair with src >= x
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(p.src + mid) < x) lo = mid + 1; else hi = mid;
+      }
+      int to = x;
+      if (lo < p.n && __ldg(p.src + lo) == x && (uint32_t)x < (uint32_t)p.n_blocks) {
+        const int d = __ldg(p.dst + lo);
+        if ((uint32_t)d < (uint32_t)p.n_blocks) to = d;
+      }
+      p.table_out[e] = to;
+      continue;
+    }
+    const long long pair = part / per;
+    const int c = (int)(part - pair * per), cv = c - p.k_chunks;
+    const bool is_v = cv >= 0;
+    const int s = __ldg(p.src + pair), d = __ldg(p.dst + pair);
+    if (c == 0 && threadIdx.x == 0 && p.table && pair > 0 && __ldg(p.src + pair - 1) >= s) record_error(p.err, PA_ERR_INVALID);
+    if ((uint32_t)s >= (uint32_t)p.n_blocks || (uint32_t)d >= (uint32_t)p.n_blocks) {
+      if (c == 0 && threadIdx.x == 0) record_error(p.err, PA_ERR_BOUNDS);
+      continue;
+    }
+    const long long size = is_v ? p.v_bytes : p.k_bytes, from = (long long)(is_v ? cv : c) * kChunk + 16 * threadIdx.x;
+    uint8_t* pool = is_v ? p.v_pool : p.k_pool;
+    const uint8_t* a = pool + s * size + from;
+    uint8_t* b = pool + d * size + from;
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (from + 16 * kBlockThreads * i < size) x[i] = *reinterpret_cast<const uint4*>(a + 16 * kBlockThreads * i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (from + 16 * kBlockThreads * i < size) *reinterpret_cast<uint4*>(b + 16 * kBlockThreads * i) = x[i];
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+// Rows that one cluster moves at once.
+bool is_few(long long n_rows, int n_heads) {
+  return n_rows * 2 * ((n_heads + 3) / 4) <= (long long)kItems * kSmallWarps * kMaxCluster;
+}
+
+pa_status launch_few(const MoveParams& p, cudaStream_t cs) {
+  const long long items = p.n_rows * 2 * ((p.n_heads + 3) / 4);
+  const unsigned ctas = (unsigned)((items + kItems * kSmallWarps - 1) / (kItems * kSmallWarps));
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(32 * kSmallWarps);
+  cfg.stream = cs;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, pa_move_few_kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status launch_blocks(const BlockParams& p, cudaStream_t cs) {
+  int sms = 0;
+  const pa_status st = sm_count(&sms);
+  if (st != PA_OK) return st;
+  const long long parts = p.chunks + (p.entries + kBlockThreads - 1) / kBlockThreads;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(parts, 8ll * sms));
+  cfg.blockDim = dim3(kBlockThreads);
+  cfg.stream = cs;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pa_move_blocks_kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status move_blocks(const pa_pool* pool, void* k_pool, void* v_pool, const int32_t* src, const int32_t* dst, uint32_t n,
+                      const int32_t* table, int32_t* table_out, uint64_t entries, int32_t* err, pa_stream_t stream) {
+  pa_pool_desc d;
+  if (pa_pool_get_desc(pool, &d) != PA_OK) return PA_ERR_INVALID;
+  if (n == 0 && entries == 0) return PA_OK;
+  if (!k_pool || !v_pool || (n && (!src || !dst)) || !err || (entries && (!table || !table_out))) return PA_ERR_INVALID;
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return PA_ERR_INVALID;
+  const size_t bk = (size_t)d.n_kv_heads * d.page_size * pa_row_bytes(d.k_type, d.head_dim);
+  const size_t bv = (size_t)d.n_kv_heads * d.page_size * pa_row_bytes(d.v_type, d.head_dim);
+  if (bk == 0 || bv == 0 || ((bk | bv) & 15)) return PA_ERR_UNSUPPORTED;
+  if (n > 0x7fffffffu || entries > (uint64_t(1) << 40) || (bk + bv) / kChunk > 0x3fffffffu) return PA_ERR_UNSUPPORTED;
+  BlockParams p{};
+  p.k_pool = static_cast<uint8_t*>(k_pool);
+  p.v_pool = static_cast<uint8_t*>(v_pool);
+  p.src = src;
+  p.dst = dst;
+  p.table = entries ? table : nullptr;
+  p.table_out = table_out;
+  p.err = err;
+  p.k_bytes = (long long)bk;
+  p.v_bytes = (long long)bv;
+  p.entries = (long long)entries;
+  p.n = (int)n;
+  p.k_chunks = (int)((bk + kChunk - 1) / kChunk);
+  p.v_chunks = (int)((bv + kChunk - 1) / kChunk);
+  p.chunks = (long long)n * (p.k_chunks + p.v_chunks);
+  p.n_blocks = (int)d.n_blocks;
+  return launch_blocks(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t move_workspace(const pa_pool_desc& d, uint64_t n_rows) {
+  return (size_t)n_rows * d.n_kv_heads * (pa_row_bytes(d.k_type, d.head_dim) + pa_row_bytes(d.v_type, d.head_dim));
+}
+
+}  // namespace
+
+extern "C" pa_status pa_copy_blocks(const pa_pool* pool, void* k_pool, void* v_pool, const int32_t* src,
+                                    const int32_t* dst, uint32_t n, int32_t* err, pa_stream_t stream) {
+  return move_blocks(pool, k_pool, v_pool, src, dst, n, nullptr, nullptr, 0, err, stream);
+}
+
+extern "C" pa_status pa_move_blocks(const pa_pool* pool, void* k_pool, void* v_pool, const int32_t* src,
+                                    const int32_t* dst, uint32_t n, const int32_t* table, int32_t* table_out,
+                                    uint64_t n_entries, int32_t* err, pa_stream_t stream) {
+  return move_blocks(pool, k_pool, v_pool, src, dst, n, table, table_out, n_entries, err, stream);
+}
+
+extern "C" size_t pa_move_rows_workspace_size(const pa_pool* pool, uint32_t n_rows) {
+  pa_pool_desc d;
+  if (pa_pool_get_desc(pool, &d) != PA_OK || is_few(n_rows, (int)d.n_kv_heads)) return 0;
+  return move_workspace(d, n_rows);
+}
+
+extern "C" pa_status pa_move_rows(const pa_pool* pool, void* k_pool, void* v_pool, const pa_rope_desc* rope,
+                                  const pa_rope_desc* rope_from, const int32_t* src_seq, const int32_t* src_pos,
+                                  const int32_t* dst_seq, const int32_t* dst_pos, uint32_t n_rows,
+                                  const int32_t* src_table, uint32_t src_stride, uint32_t src_n_seq,
+                                  const int32_t* dst_table, uint32_t dst_stride, uint32_t dst_n_seq, int32_t disjoint,
+                                  void* workspace, size_t ws_bytes, int32_t* err, pa_stream_t stream) {
+  pa_pool_desc d;
+  if (pa_pool_get_desc(pool, &d) != PA_OK) return PA_ERR_INVALID;
+  if (d.head_dim != (uint32_t)kD) return PA_ERR_UNSUPPORTED;
+  if (!rope && rope_from) return PA_ERR_INVALID;
+  for (const pa_rope_desc* r : {rope, rope_from}) {
+    if (!r) continue;
+    const pa_status st = check_rope(r);
+    if (st != PA_OK) return st;
+  }
+  if (rope_from && (rope_from->rot_dim != rope->rot_dim || rope_from->interleaved != rope->interleaved)) return PA_ERR_INVALID;
+  if (n_rows == 0) return PA_OK;
+  if (!k_pool || !v_pool || !src_seq || !src_pos || !dst_seq || !dst_pos || !src_table || !dst_table || !err || src_stride == 0 ||
+      dst_stride == 0 || src_n_seq == 0 || dst_n_seq == 0)
+    return PA_ERR_INVALID;
+  if (src_stride > 0x7fffffffu || dst_stride > 0x7fffffffu || src_n_seq > 0x7fffffffu || dst_n_seq > 0x7fffffffu) return PA_ERR_INVALID;
+  if (!aligned16(k_pool) || !aligned16(v_pool)) return PA_ERR_INVALID;
+  MoveParams p{};
+  p.factor = 1.f;
+  p.still = 1;
+  if (rope) {
+    const pa_rope_desc* was = rope_from ? rope_from : rope;
+    const double factor = (double)rope->attn_factor / (double)was->attn_factor;
+    if (!std::isfinite(factor) || !std::isfinite((float)factor)) return PA_ERR_INVALID;  // nothing brings back what a factor of 0 made
+    p.rot = (int)rope->rot_dim;
+    p.interleaved = rope->interleaved;
+    p.factor = (float)factor;
+    p.still = factor == 1.0;
+    for (int i = 0; i < p.rot / 2; ++i) {
+      p.from[i] = turns_of(was->inv_freq[i]);
+      p.to[i] = turns_of(rope->inv_freq[i]);
+      if (p.from[i] != p.to[i]) p.still = 0;
+    }
+  }
+  p.k_pool = static_cast<uint8_t*>(k_pool);
+  p.v_pool = static_cast<uint8_t*>(v_pool);
+  p.src_seq = src_seq;
+  p.src_pos = src_pos;
+  p.dst_seq = dst_seq;
+  p.dst_pos = dst_pos;
+  p.src_table = src_table;
+  p.dst_table = dst_table;
+  p.err = err;
+  p.n_rows = n_rows;
+  p.n_heads = (int)d.n_kv_heads;
+  p.page_size = (int)d.page_size;
+  p.src_stride = (int)src_stride;
+  p.src_seqs = (int)src_n_seq;
+  p.dst_stride = (int)dst_stride;
+  p.dst_seqs = (int)dst_n_seq;
+  p.n_blocks = (int)d.n_blocks;
+  p.k_type = d.k_type;
+  p.v_type = d.v_type;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (!disjoint && is_few(n_rows, p.n_heads)) return launch_few(p, cs);
+  if (!disjoint) {
+    if (!workspace || !aligned16(workspace) || ws_bytes < move_workspace(d, n_rows)) return PA_ERR_INVALID;
+    p.ws = static_cast<uint8_t*>(workspace);
+  }
+  int sms = 0;
+  pa_status st = sm_count(&sms);
+  if (st != PA_OK) return st;
+  p.rows = (int)std::min<long long>(8, (2ll * n_rows + 32ll * sms - 1) / (32ll * sms));  // 1 while warps are few
+  const long long grid = (((long long)n_rows + p.rows - 1) / p.rows * 2 + kWarps - 1) / kWarps;
+  if (grid > 0x7fffffffll) return PA_ERR_UNSUPPORTED;
+  if (disjoint) return launch(pa_move_kernel<kDirect>, p, (unsigned)grid, cs);
+  st = launch(pa_move_kernel<kGather>, p, (unsigned)grid, cs);
+  return st == PA_OK ? launch(pa_move_kernel<kScatter>, p, (unsigned)grid, cs) : st;
+}

@@ -14,6 +14,8 @@
 //   * an allocated block has a reference count (1 after alloc); share adds
 //     references, release drops them and frees the block at 0, and cow
 //     swaps a shared block for a fresh one the caller copies into;
+//   * compact moves the live blocks to the front: a moved block keeps its
+//     references under a new handle, its old place's generation is bumped;
 //   * every call checks everything first and then commits, so a failed call
 //     leaves the pool exactly as it was.
 #include <cstring>
@@ -203,6 +205,36 @@ extern "C" pa_status pa_cow_blocks(pa_pool* pool, const pa_block* handles, uint3
     }
   }
   *n_copies = k;
+  return PA_OK;
+}
+
+extern "C" pa_status pa_compact_blocks(pa_pool* pool, uint32_t capacity, pa_block* old_handles, pa_block* new_handles,
+                                       uint32_t* n_moves) {
+  if (!pool || !n_moves || (capacity && (!old_handles || !new_handles))) return PA_ERR_INVALID;
+  std::lock_guard<std::mutex> lk(pool->mu);
+  const uint32_t live = pool->desc.n_blocks - (uint32_t)pool->stack.size();
+  uint32_t moves = 0;
+  for (uint32_t i = live; i < pool->desc.n_blocks; ++i) moves += pool->ref[i] > 0;
+  *n_moves = moves;
+  if (moves > capacity) return PA_ERR_INVALID;
+  if (moves > 0) {
+    // live blocks behind the first `live` places, in order, into the free ones among those
+    uint32_t to = 0, k = 0;
+    for (uint32_t from = live; from < pool->desc.n_blocks; ++from) {
+      if (pool->ref[from] == 0) continue;
+      while (pool->ref[to] > 0) ++to;
+      old_handles[k] = ((uint64_t)pool->gen[from] << 32) | from;
+      new_handles[k] = ((uint64_t)pool->gen[to] << 32) | to;
+      ++k;
+      pool->ref[to] = pool->ref[from];
+      pool->ref[from] = 0;
+      const uint32_t g = pool->gen[from] + 1;
+      pool->gen[from] = g ? g : 1;
+    }
+  }
+  // the free blocks are the last ones now, the lowest handed out first
+  pool->stack.clear();
+  for (uint32_t i = pool->desc.n_blocks; i > live; --i) pool->stack.push_back(i - 1);
   return PA_OK;
 }
 

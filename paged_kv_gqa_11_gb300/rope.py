@@ -8,6 +8,7 @@ way into one.
 from __future__ import annotations
 
 import ctypes as C
+import math
 
 import torch
 
@@ -36,6 +37,35 @@ class Rope:
         if rot_dim % 2 or not 0 <= rot_dim <= 256:
             raise PaError(PA_ERR_INVALID, "Rope: rot_dim is even, 0 to 256")
         return cls([float(theta) ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)], **kw)
+
+    @classmethod
+    def scaled(cls, rot_dim: int, theta: float, factor: float, method: str = "base", length: int | None = None, fast: float = 32.0,
+               slow: float = 1.0, **kw) -> "Rope":
+        """Frequencies for contexts `factor` times longer than those that f_i =
+        theta^(-2 i / rot_dim) were made for (factor at least 1):
+
+          "linear"  f_i / factor;
+          "base"    of the base theta factor^(rot_dim / (rot_dim - 2)): the first pair
+                    keeps its frequency, the last has 1 / factor of it;
+          "ramp"    by how often a pair turns in the original `length`, r_i = length f_i /
+                    (2 pi): f_i from `fast` turns on, f_i / factor up to `slow`, linear
+                    in r_i between; attn_factor 0.1 ln(factor) + 1 unless given.
+
+        Keys that a cache holds under other frequencies: PagedKVCache.move_rows."""
+        if rot_dim % 2 or not 4 <= rot_dim <= 256:
+            raise PaError(PA_ERR_INVALID, "Rope: rot_dim is even, 4 to 256")
+        if not (math.isfinite(factor) and factor >= 1.0):
+            raise PaError(PA_ERR_INVALID, "Rope: factor is at least 1")
+        if method == "base":
+            return cls.from_theta(rot_dim, float(theta) * factor ** (rot_dim / (rot_dim - 2)), **kw)
+        f = [float(theta) ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)]
+        if method == "linear":
+            return cls([x / factor for x in f], **kw)
+        if method != "ramp" or length is None or length <= 0 or not fast > slow:
+            raise PaError(PA_ERR_INVALID, 'Rope: "linear", "base", or "ramp" with a length and fast > slow')
+        kw.setdefault("attn_factor", 0.1 * math.log(factor) + 1.0)
+        keep = [min(1.0, max(0.0, (length * x / (2.0 * math.pi) - slow) / (fast - slow))) for x in f]
+        return cls([x * (k + (1.0 - k) / factor) for x, k in zip(f, keep)], **kw)
 
     def apply(self, q: torch.Tensor | None, k: torch.Tensor | None, row_pos: torch.Tensor,
               q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
