@@ -555,16 +555,18 @@ size_t pa_decode_prefix_workspace_size(const pa_pool* pool, uint32_t n_seq, uint
  * block_table: only entries for pages that hold a row group (16 rows) with a key that
  *           some new token sees are read, so the pages outside window and sinks may
  *           have been released.  An entry outside the pool: as pa_decode.
- * workspace: ws_bytes >= pa_attend_window_workspace_size() for the largest n_new,
- *           256-byte aligned; contents as pa_decode's.
+ * workspace: ws_bytes >= pa_attend_window_workspace_size(), 256-byte aligned; contents as
+ *           pa_decode's.
  *
  * Precision and range: as pa_decode_prefix, whose arithmetic it is.  An infinite or NaN
  * value of V (a stored one past 65504 is infinite) in a row that one of the tokens
- * sees can also reach others of the same sequence that do not see it (those up to 11
+ * sees can also reach others of the same sequence that do not see it (those up to 40
  * tokens away); in a row that none of them sees it has no effect, and K's never have.
  *
- * Launches: one, and a merge when a (64 query rows, KV head) is shared by CTAs; 448 times
- * 64 query rows at a time.  Both are programmatic dependent launches (pa_decode). */
+ * Launches: one for the sequences of fewer than 64 new tokens (448 times 64 query rows at a
+ * time), and a merge when a (64 query rows, KV head) is shared by CTAs; for those of more,
+ * one that turns their keys into binary16, and one over 256 times 128 query rows at a
+ * time, with its merge.  All are programmatic dependent launches (pa_decode). */
 pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_t q_stride, int32_t q_type, const void* k_pool,
                            const void* v_pool, const int32_t* block_table, uint32_t table_stride,
                            const int32_t* seq_lens_dev, const int32_t* seq_lens_host, const int32_t* n_new,
@@ -572,9 +574,12 @@ pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_t q_stride,
                            int64_t out_stride, int32_t out_type, float* lse, void* workspace, size_t ws_bytes,
                            int32_t* err, pa_stream_t stream);
 
-/* Scratch bytes pa_attend_window needs for up to max_new new tokens of a sequence, any
- * number of sequences, on CUDA device `device`.  0 for an unsupported pool. */
-size_t pa_attend_window_workspace_size(const pa_pool* pool, uint32_t max_new, int device);
+/* Scratch bytes pa_attend_window needs for these lengths on CUDA device `device`; more new
+ * tokens, longer sequences and windows, or more sequences need no less.  Sequences of 64 new
+ * tokens and more take 16 KB for each KV head and 16 keys that they see.  0 for an unsupported
+ * pool or lengths that the call refuses. */
+size_t pa_attend_window_workspace_size(const pa_pool* pool, const int32_t* seq_lens_host, const int32_t* n_new,
+                                       uint32_t n_seq, uint32_t window, uint32_t sinks, int device);
 
 /* ------------------------------------------------------------------ errors */
 

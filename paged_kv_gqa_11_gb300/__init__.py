@@ -116,7 +116,7 @@ def load():
             "pa_decode_prefix_workspace_size": (sz, [vp, u32, u32, u32, C.c_int]),
             "pa_attend_window": (C.c_int, [vp, vp, i64, i32, vp, vp, vp, u32, vp, vp, vp, u32, u32, u32, u32, C.c_float, vp,
                                            i64, i32, vp, vp, sz, vp, vp]),
-            "pa_attend_window_workspace_size": (sz, [vp, u32, C.c_int]),
+            "pa_attend_window_workspace_size": (sz, [vp, vp, vp, u32, u32, u32, C.c_int]),
             "pa_compact_blocks": (C.c_int, [vp, u32, vp, vp, C.POINTER(u32)]),
             "pa_move_blocks": (C.c_int, [vp, vp, vp, vp, vp, u32, vp, vp, C.c_uint64, vp, vp]),
             "pa_move_rows": (C.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp, u32, vp, u32, u32, vp, u32, u32, i32, vp, sz, vp, vp]),
@@ -416,8 +416,12 @@ def pa_decode_prefix(pool: Pool, q, q_type: int, k_pool, v_pool, block_table, ta
     return rc
 
 
-def pa_attend_window_workspace_size(pool: Pool, max_new: int, device: int = 0) -> int:
-    return int(load().pa_attend_window_workspace_size(pool.handle, max_new, device))
+def pa_attend_window_workspace_size(pool: Pool, seq_lens_host, n_new, window: int = 0, sinks: int = 0, device: int = 0) -> int:
+    import numpy as np
+    sl, nn = (np.ascontiguousarray(x, dtype=np.int32) for x in (seq_lens_host, n_new))
+    if sl.ndim != 1 or sl.shape != nn.shape:
+        raise PaError(PA_ERR_INVALID, "a length and a number of new tokens per sequence")
+    return int(load().pa_attend_window_workspace_size(pool.handle, sl.ctypes.data, nn.ctypes.data, len(sl), window, sinks, device))
 
 
 def pa_attend_window(pool: Pool, q, q_stride: int, q_type: int, k_pool, v_pool, block_table, table_stride: int, seq_lens_dev,

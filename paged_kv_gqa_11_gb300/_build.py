@@ -27,7 +27,7 @@ TYPES = {"f16": 1, "q4_0": 2, "q8_0": 8}  # pa_type numbers
 # windowed kernels are one source each, compiled once per (K, V) format pair.
 UNITS = [("pa_pool.cpp", "pa_pool", []), ("pa_append.cu", "pa_append", []), ("pa_decode.cu", "pa_decode", []),
          ("pa_rope.cu", "pa_rope", []), ("pa_prefix.cu", "pa_prefix", []), ("pa_window.cu", "pa_window", []),
-         ("pa_move.cu", "pa_move", [])]
+         ("pa_prompt.cu", "pa_prompt", []), ("pa_move.cu", "pa_move", [])]
 UNITS += [("pa_decode_kern.cu", f"pa_decode_kern_{k}_{v}", [f"-DPA_KT={TYPES[k]}", f"-DPA_VT={TYPES[v]}"])
           for k in TYPES for v in TYPES]
 UNITS += [("pa_prefix_kern.cu", f"pa_prefix_kern_{k}_{v}", [f"-DPA_KT={TYPES[k]}", f"-DPA_VT={TYPES[v]}"])

@@ -23,7 +23,6 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ATen.h>
 
-#include <algorithm>
 #include <initializer_list>
 #include <optional>
 #include <string>
@@ -437,11 +436,9 @@ PyObject* attend_window(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int64_t qs = row_stride(q, "q"), rows = q.size(0), hq = q.size(1);
     const auto* fresh = static_cast<const int32_t*>(n_new.b.buf);
     int64_t tokens = 0;
-    int32_t most = 0;
     for (int64_t i = 0; i < n; ++i) {
       check(fresh[i] >= 0, "n_new: from 0 on");
       tokens += fresh[i];
-      most = std::max(most, fresh[i]);
     }
     check(tokens <= rows, "q: a row per new token");
     on(dev, q, "q"); on(dev, vp, "v_pool"); on(dev, table, "block_table"); on(dev, lens_dev, "seq_lens_dev"); on(dev, out, "out");
@@ -463,7 +460,9 @@ PyObject* attend_window(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     check(!lse.defined() || (lse.scalar_type() == at::kFloat && lse.is_contiguous() && lse.dim() == 2 && lse.size(0) == rows && lse.size(1) == hq),
           "lse: float32 [tokens][heads], contiguous");
     if (tokens > 0 && !ws.defined())
-      ws = at::empty({(int64_t)pa_attend_window_workspace_size(pool, (uint32_t)most, dev)}, kp.options().dtype(at::kByte));
+      ws = at::empty({(int64_t)pa_attend_window_workspace_size(pool, static_cast<const int32_t*>(lens.b.buf), fresh, (uint32_t)n, window,
+                                                               sinks, dev)},
+                     kp.options().dtype(at::kByte));
     check(!ws.defined() || ws.is_contiguous(), "workspace: contiguous");
     const int qt = dtype_of(q), ot = dtype_of(out);
     const int64_t os = row_stride(out, "out");

@@ -1,0 +1,640 @@
+// Windowed attention of many new tokens, on the fifth-generation tensor core (sm_103a).
+//
+// The mathematics is that of pa_window_impl.cuh.  A prompt's tokens share their keys: a key
+// tile meets dozens of row tiles.  So the keys and values that any new token sees are
+// first turned into binary16 once, in the workspace (pa_prompt_prepare_kernel; a chunk's stay
+// in L2), in the order in which the MMAs take them:
+//   K   per (sequence, head) four planes of 64 dims, each [8 keys][8 dims'][8 keys' rows of 16 bytes]: a
+//       run of row groups of a plane is one contiguous piece, an MMA's B operand;
+//   V   transposed, [8 keys][8 dims][8 rows of 16 bytes = 8 keys]: likewise a run of groups is.
+// and the attention is a dense one over tiles of 128 query rows (a unit) x 128 keys:
+//   S = Q K^T   tcgen05.mma M = 128 rows, N = keys of the tile, K = 256 dims; Q and K in shared memory;
+//   O += P V    M = 128 rows, N = 256 dims, K = keys; P in tensor memory (in its S's place), V in shared memory.
+// Tensor memory: O in columns 0-255, two buffers of S in 256-383 and 384-511; P as pairs
+// of binary16 in the first 64 columns of its S.
+//
+// Shared memory: Q (64 KB) and a ring of nine stages of 16 KB: a quarter of a K tile (64 dims of
+// its keys) or of a V tile (32 keys), each worth 256 cycles of MMA; so about 2000 cycles are
+// on their way while one is used.
+//
+// Warps, hand-offs on mbarriers, every wait bounded:
+//   0-7    softmax: (half of the keys, lane quarter), thread = row;
+//   8-11   query rows into Q, and a finished piece's O to its place;
+//   12     MMA issue; 13 copies.
+// S of tile j + 1 is multiplied while the softmax of tile j runs, and that of j + 1 while PV of
+// j and S of j + 2 are.  At a piece's end PV comes before the next piece's S, whose
+// query rows are on their way meanwhile.
+//
+// Ranges, cuts and slots are those of pa_window_impl.cuh, with units of 128 rows.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "pa_prompt.cuh"
+#include "pa_row_ops.cuh"
+
+namespace pa_prefix {
+
+namespace {
+
+using pa_rows_io::Lane;
+
+// ------------------------------------------------------------------ keys and values into the workspace
+
+// A warp takes eight rows (half a row group) of one head of one pool: lane l their dims 8 l ..
+// + 7, which is one core matrix of the MMA's operand, 128 bytes.
+
+// A lane's eight values of a row in binary16 (scale * quant, rounded once); wide: the row's
+// scales as they are may overflow (dequant_k), the values are 2^-8 of what they are.
+template <int T>
+__device__ __forceinline__ uint4 half_values(const uint8_t* grp, int r, int lane, bool is_v, bool* wide) {
+  const Lane at = pa_rows_io::lane_of(T, is_v, r, lane);
+  if (T == PA_F16) return *reinterpret_cast<const uint4*>(grp + at.body);
+  const uint2 raw = *reinterpret_cast<const uint2*>(grp + at.body);
+  uint32_t d = *reinterpret_cast<const uint16_t*>(grp + at.scale);
+  d |= d << 16;
+  if (!is_v) {
+    *wide = __any_sync(0xffffffffu, ((d & 0x7fffu) + (T == PA_Q8_0 ? 0x2000u : 0x1000u)) & 0x8000u);
+    if (*wide) d = hmul2(d, kR256);
+  }
+  const uint32_t w[2] = {raw.x, raw.y};
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // bytes 0 .. 255 under 0x64 are the binary16 numbers 1024 + byte
+    const uint32_t u = T == PA_Q8_0 ? w[i] ^ 0x80808080u : (w[i] >> ((lane & 2) << 1)) & 0x0f0f0f0fu;
+    const uint32_t bias = T == PA_Q8_0 ? 0xe480e480u : 0xe408e408u;  // -1152, -1032
+    h[2 * i] = hmul2(hadd2(prmt(u, 0x64646464u, 0x4140), bias), d);
+    h[2 * i + 1] = hmul2(hadd2(prmt(u, 0x64646464u, 0x4342), bias), d);
+  }
+  return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+template <int T>
+__device__ __forceinline__ void prepare_rows(const PrepareParams& p, const PromptSeq& s, bool is_v, int head, int group, int half,
+                                             const uint8_t* grp, int first, int lane) {
+  uint4 x[8];
+  uint32_t wide_rows = 0;
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    bool wide = false;
+    x[r] = grp ? half_values<T>(grp, 8 * half + r, lane, is_v, &wide) : make_uint4(0u, 0u, 0u, 0u);
+    wide_rows |= (uint32_t)wide << r;
+    const int key = first + r;  // values of keys that no new token sees are zeros, whatever lies there
+    if (is_v && (key >= s.len || (key >= p.sinks && key < s.lo))) x[r] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  const long long reg = (long long)s.group0 * p.n_kv_heads + (long long)head * s.groups;
+  if (is_v) {
+    uint8_t* to = p.v + (reg + group) * kGroupBytes + half * (kGroupBytes / 2) + 128 * lane;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {  // dims 2 d and 2 d + 1 of the lane's eight
+      uint32_t w[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) w[r] = d == 0 ? x[r].x : d == 1 ? x[r].y : d == 2 ? x[r].z : x[r].w;
+      uint4* o = reinterpret_cast<uint4*>(to + 32 * d);
+      o[0] = make_uint4(prmt(w[0], w[1], 0x5410), prmt(w[2], w[3], 0x5410), prmt(w[4], w[5], 0x5410), prmt(w[6], w[7], 0x5410));
+      o[1] = make_uint4(prmt(w[0], w[1], 0x7632), prmt(w[2], w[3], 0x7632), prmt(w[4], w[5], 0x7632), prmt(w[6], w[7], 0x7632));
+    }
+  } else {
+    // plane lane / 8, [8 keys][8 slots][8 rows]
+    uint8_t* to = p.k + reg * kGroupBytes + (((long long)(lane >> 3) * s.groups + group) * 2 + half) * 1024 + (lane & 7) * 128;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) reinterpret_cast<uint4*>(to)[r] = x[r];
+    if (p.wide && lane == 0) p.wide[(reg + group) * 2 + half] = (uint8_t)wide_rows;
+  }
+}
+
+constexpr int kPrepareWarps = 4;
+
+__global__ void __launch_bounds__(32 * kPrepareWarps) pa_prompt_prepare_kernel(const __grid_constant__ PrepareParams p) {
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const long long items = (long long)p.groups * 4 * p.n_kv_heads, step = (long long)gridDim.x * kPrepareWarps;
+  for (long long i = (long long)blockIdx.x * kPrepareWarps + (threadIdx.x >> 5); i < items; i += step) {
+    const int half = (int)(i & 1), is_v = (int)(i >> 1 & 1);
+    const long long g = i >> 2;
+    const int head = (int)(g % p.n_kv_heads), at = (int)(g / p.n_kv_heads);
+    int lo = 0, hi = p.n_seqs - 1;  // the last sequence whose first group is <= at
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.seq[mid].at <= at) lo = mid; else hi = mid - 1;
+    }
+    const PromptSeq& s = p.seq[lo];
+    const int group = at - s.at, v = group * kGroup, first = v < s.s16 ? v : v + s.shift;
+    const int page = first / p.page_size, off = first - page * p.page_size;
+    const int entry = __ldg(p.table + (long long)s.seq * p.table_stride + page);
+    const bool ok = (uint32_t)entry < (uint32_t)p.n_blocks;
+    if (!ok && lane == 0) record_error(p.err, PA_ERR_BOUNDS);  // its rows read as zeros
+    const int type = is_v ? p.v_type : p.k_type;
+    const uint8_t* grp =
+        ok ? (is_v ? p.v_pool : p.k_pool) + (((long long)entry * p.n_kv_heads + head) * p.page_size + off) * row_bytes_of(type) : nullptr;
+    if (type == PA_F16) prepare_rows<PA_F16>(p, s, is_v, head, group, half, grp, first + 8 * half, lane);
+    else if (type == PA_Q8_0) prepare_rows<PA_Q8_0>(p, s, is_v, head, group, half, grp, first + 8 * half, lane);
+    else prepare_rows<PA_Q4_0>(p, s, is_v, head, group, half, grp, first + 8 * half, lane);
+  }
+}
+
+// ------------------------------------------------------------------ the attention
+
+constexpr int kStageBytes = 16384, kNStages = 9;
+constexpr int kPSmWarps = 8, kAuxWarp0 = 8, kMmaWarp = 12, kCopyWarp = 13, kPThreads = 14 * 32;
+constexpr uint32_t kPOCol = 0, kPSCol = 256;
+
+struct PSmem {
+  static constexpr int kQ = 0, kRing = kPromptRows * kD * 2, kRed = kRing + kNStages * kStageBytes;
+  static constexpr int kSum = kRed + 2 * kPromptRows * 4;        // [piece & 1][half of the keys][row]
+  static constexpr int kRef = kSum + 4 * kPromptRows * 4;        // [piece & 1][row]
+  static constexpr int kBar = kRef + 2 * kPromptRows * 4;
+  static constexpr int kNBar = 2 * kNStages + 2 + 2 + 2 + 2 + 1 + 2 + 2;
+  static constexpr int kMisc = kBar + 8 * kNBar;                 // abort, tmem base, the softmax's leave [2]
+  static constexpr int kTotal = kMisc + 16;
+  static constexpr int kLaunch = kTotal + 1024;
+  static_assert(kLaunch <= 232448, "shared memory");
+};
+
+// A piece of the CTA's range: tiles j0 .. j1 - 1 of a (unit, head).
+struct Piece {
+  int unit, head, j0, j1, nt;
+  bool first, last;  // of the segment's tiles
+};
+
+// The roles walk the CTA's pieces each on its own.
+struct Walk {
+  Pos pos;
+  int left;  // tiles of the range from here on
+  __device__ __forceinline__ bool next(const PromptParams& p, Piece& x) {
+    if (left == 0) return false;
+    x.unit = pos.unit;
+    x.head = pos.head;
+    x.nt = pos.nt;
+    x.j0 = pos.j;
+    x.j1 = min(pos.nt, pos.j + left);
+    x.first = pos.j == 0;
+    x.last = x.j1 == pos.nt;
+    left -= x.j1 - x.j0;
+    pos.j = x.j1 - 1;
+    if (left > 0) advance(p, pos);
+    return true;
+  }
+};
+
+// Keys of tile j of a unit, up to 128, and the same in whole steps of an MMA.
+__device__ __forceinline__ int tile_keys(const Span& s, int j) { return min(kKeys, s.end - j * kKeys); }
+__device__ __forceinline__ int whole16(int n) { return (n + 15) & ~15; }
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_constant__ PromptParams p) {
+  using SM = PSmem;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
+  const uint32_t base = smem_u32(smem);
+  const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+  // Hand-offs (tile j, piece i of the CTA):
+  //   full / empty [stage]        copies <-> MMA (commit)
+  //   q_full / q_empty            query rows of piece i in Q / its last S done
+  //   s_full [j & 1]              S(j) in tensor memory
+  //   p_full [j & 1]              P(j) in its place
+  //   pv_done [j & 1]             O holds tile j
+  //   l_full [i & 1]              piece i's sums and references in shared memory
+  //   o_free                      piece i's O has been read
+  // A role whose wait expires stops: it arrives nowhere any more.
+  const uint32_t full = base + SM::kBar, empty = full + 8 * kNStages, q_full = empty + 8 * kNStages, q_empty = q_full + 8,
+                 s_full = q_empty + 8, p_full = s_full + 16, pv_done = p_full + 16, o_free = pv_done + 16, l_full = o_free + 8,
+                 drain = l_full + 16, sink = drain + 8;
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + SM::kMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc + 4);
+  volatile int* leave = reinterpret_cast<volatile int*>(smem + SM::kMisc + 8);  // of even, odd tiles
+  if (tid == 0) {
+    *abort = leave[0] = leave[1] = 0;
+    for (int i = 0; i < kNStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    mbar_init(q_full, 4);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, kPSmWarps);
+      mbar_init(pv_done + 8 * i, 1);
+      mbar_init(l_full + 8 * i, kPSmWarps);
+    }
+    mbar_init(o_free, 4);
+    mbar_init(drain, 1);
+    mbar_init(sink, 1);
+    fence_mbar_init();
+  }
+  Walk walk;
+  {
+    const int x0 = (int)((long long)blockIdx.x * p.total_len / p.n_ctas), x1 = (int)((long long)(blockIdx.x + 1) * p.total_len / p.n_ctas);
+    walk.pos = locate(p, x0);
+    walk.left = (x1 < p.total_len ? locate(p, x1).tile : p.total_tiles) - walk.pos.tile;
+  }
+  const int n = walk.left;  // at least 1
+  if (w == 0) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // nothing that another kernel wrote is read before this
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tid == 0) asm volatile("griddepcontrol.launch_dependents;");
+  const bool whole = *tmem_slot == 0;  // all of tensor memory is this CTA's, so its columns start at 0
+  if (!whole && tid == 0) record_error(p.err, PA_ERR_CUDA);
+  int issued = 0;
+  Piece x;
+
+  if (!whole) {
+  } else if (w == kCopyWarp) {
+    // ---- copies: of a piece K(0), then K(j + 1) before V(j); a stage each 64 dims or 32 keys
+    bool live = true;
+    auto stage = [&](uint32_t bytes) -> int {  // the next stage, once it is free; -1: the wait expired
+      const int s = issued % kNStages, use = issued / kNStages;
+      if (live && use > 0 && !warp_wait(empty + 8 * s, (use - 1) & 1, p.err, abort)) live = false;
+      if (!live) return -1;
+      if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
+      __syncwarp();
+      ++issued;
+      return s;
+    };
+    while (live && walk.next(p, x)) {
+      const PromptUnit& u = p.unit[x.unit];
+      const Span s = span_of(u, p.window, p.sinks);
+      const long long reg = (long long)u.group0 * p.n_kv_heads + (long long)x.head * u.groups;
+      // places v .. end - 1: one run of the sequence's groups, or two (sinks, window)
+      auto copy = [&](const uint8_t* from, uint32_t to, int v, int end, int unit_bytes, uint32_t bar) {
+        int a = v, stop = s.shift != u.shift0 && v < s.s16 ? min(end, s.s16) : end;
+        while (a < end) {
+          if (lane == 0)
+            bulk_copy(to + ((a - v) >> 4) * unit_bytes, from + (long long)group_of(u, s, a) * unit_bytes, ((stop - a) >> 4) * unit_bytes, bar);
+          a = stop;
+          stop = end;
+        }
+        __syncwarp();
+      };
+      auto keys = [&](int j) {
+        const int v = j * kKeys, n16 = whole16(tile_keys(s, j));
+        for (int q = 0; q < 4 && live; ++q) {
+          const int st = stage((uint32_t)n16 * 128);
+          if (st >= 0) copy(p.k + reg * kGroupBytes + (long long)q * u.groups * 2048, base + SM::kRing + st * kStageBytes, v, v + n16, 2048, full + 8 * st);
+        }
+      };
+      auto vals = [&](int j) {
+        const int v = j * kKeys, n16 = whole16(tile_keys(s, j));
+        for (int q = 0; q < n16 && live; q += 32) {
+          const int m = min(32, n16 - q), st = stage((uint32_t)m * 512);
+          if (st >= 0) copy(p.v + reg * kGroupBytes, base + SM::kRing + st * kStageBytes, v + q, v + q + m, kGroupBytes, full + 8 * st);
+        }
+      };
+      keys(x.j0);
+      for (int j = x.j0; j < x.j1 && live; ++j) {
+        if (j + 1 < x.j1) keys(j + 1);
+        vals(j);
+      }
+    }
+  } else if (w == kMmaWarp) {
+    // ---- MMA issue by the whole warp, an elected lane issuing.  After an expired wait no
+    // further MMA is issued; what was ends before the CTA does.
+    bool dead = false;
+    int used = 0;
+    uint32_t piece = 0;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (!dead) dead = !warp_wait(bar, parity, p.err, abort);
+      return !dead;
+    };
+    const uint64_t qdesc = smem_desc(base + SM::kQ, 128, 4096);
+    const uint32_t pv_idesc = idesc_f16_f32(128, kD);
+    int j = 0;  // the CTA's tile
+    while (!dead && walk.next(p, x)) {
+      const Span s = span_of(p.unit[x.unit], p.window, p.sinks);
+      auto score = [&](int t, int jj) {  // S of the segment's tile t, the CTA's jj
+        const uint32_t idesc = idesc_f16_f32(128, 0) | (uint32_t)(whole16(tile_keys(s, t)) >> 3) << 17, d = kPSCol + 128 * (jj & 1);
+        for (int q = 0; q < 4; ++q) {
+          const int st = used % kNStages;
+          if (!wait(full + 8 * st, (used / kNStages) & 1)) return;
+          tc_fence_after();
+          const uint64_t kdesc = smem_desc(base + SM::kRing + st * kStageBytes, 128, 1024);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tc_mma_f16_warp(d, qdesc + 64 * q + 16 * i, kdesc + 16 * i, idesc, q | i);
+          tc_commit_warp(empty + 8 * st);
+          ++used;
+        }
+        tc_commit_warp(s_full + 8 * (jj & 1));
+        if (t + 1 == x.j1) tc_commit_warp(q_empty);
+      };
+      if (!wait(q_full, piece & 1)) break;
+      tc_fence_after();
+      score(x.j0, j);
+      for (int t = x.j0; t < x.j1 && !dead; ++t, ++j) {
+        if (t + 1 < x.j1) score(t + 1, j + 1);
+        if (!wait(p_full + 8 * (j & 1), (j >> 1) & 1)) break;
+        if (t == x.j0 && piece > 0 && !wait(o_free, (piece - 1) & 1)) break;
+        tc_fence_after();
+        const int n16 = whole16(tile_keys(s, t));
+        for (int q = 0; q < n16; q += 32) {
+          const int st = used % kNStages;
+          if (!wait(full + 8 * st, (used / kNStages) & 1)) break;
+          tc_fence_after();
+          const uint64_t vdesc = smem_desc(base + SM::kRing + st * kStageBytes, kGroupBytes / 2, 128);
+          const uint32_t a = kPSCol + 128 * (j & 1) + q / 2;
+          tc_mma_f16_tmem_a_warp(kPOCol, a, vdesc, pv_idesc, (t - x.j0) | q);
+          if (q + 16 < n16) tc_mma_f16_tmem_a_warp(kPOCol, a + 8, vdesc + (kGroupBytes >> 4), pv_idesc, 1);
+          tc_commit_warp(empty + 8 * st);
+          ++used;
+        }
+        if (dead) break;
+        tc_commit_warp(pv_done + 8 * (j & 1));
+      }
+      ++piece;
+    }
+    // what was issued, and every commit, ends before the CTA's memory is given back
+    tc_commit_warp(drain);
+    mbar_wait(drain, 0, p.err, abort, /*honour_abort=*/false);
+    __syncwarp();
+  } else if (w >= kAuxWarp0) {
+    // ---- query rows of a piece into Q, and the O of the piece before to its place
+    const int quarter = w & 3;
+    bool live = true;
+    uint32_t piece = 0;
+    int tiles = 0;  // of the pieces so far
+    Piece before{};
+    const float* sums = reinterpret_cast<const float*>(smem + SM::kSum);
+    const float* refs = reinterpret_cast<const float*>(smem + SM::kRef);
+    for (;;) {
+      const bool more = walk.next(p, x);
+      if (more) {
+        const PromptUnit& u = p.unit[x.unit];
+        if (piece > 0 && !(live = live && warp_wait(q_empty, (piece - 1) & 1, p.err, abort))) break;
+        Tile t{};
+        t.info = (uint32_t)unit_rows(u);
+        t.row0 = unit_row0(u);
+        t.token = u.token;
+        t.head = x.head;
+#pragma unroll 1
+        for (int r8 = 8 * quarter; r8 < kPromptRows; r8 += 32) stage_q_begin<PA_F16>(p, t, base + SM::kQ, r8, lane);
+#pragma unroll 1
+        for (int r8 = 8 * quarter; r8 < kPromptRows; r8 += 32) stage_q_end<PA_F16>(p, base + SM::kQ, r8, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        __syncwarp();
+      }
+      if (piece > 0) {
+        const uint32_t i = piece - 1, j = (uint32_t)tiles - 1;  // the piece, its last tile
+        if (!(live = live && warp_wait(l_full + 8 * (i & 1), (i >> 1) & 1, p.err, abort) &&
+                     warp_wait(pv_done + 8 * (j & 1), (j >> 1) & 1, p.err, abort)))
+          break;
+        tc_fence_after();
+        const PromptUnit& u = p.unit[before.unit];
+        const int row = 32 * quarter + lane, rows = unit_rows(u), rg = unit_row0(u) + row, tok = rg / kGqa;
+        const float l = sums[(i & 1) * 256 + row] + sums[(i & 1) * 256 + 128 + row], m = refs[(i & 1) * 128 + row];
+        const uint32_t from = kPOCol + ((uint32_t)(32 * quarter) << 16);
+        const bool mine = row < rows;
+        if (before.first && before.last) {  // the whole segment: the result
+          const bool other = __ldg(p.lens + u.seq) != u.len;
+          if (other && row == 0) record_error(p.err, PA_ERR_BOUNDS);
+          const float sum = other ? 0.f : l, inv = sum != 0.f ? 1.f / sum : 0.f;
+          const int h = before.head * kGqa + rg - tok * kGqa;
+          if (mine && p.lse) p.lse[(long long)(u.token + tok) * p.n_q_heads + h] = sum != 0.f ? (m + log2f(sum)) * pa_split::kLn2 : -INFINITY;
+          const int bytes = p.out_type == PA_DT_F32 ? 4 : 2;
+          uint8_t* to = p.out + ((u.token + tok) * p.out_stride + h * kD) * bytes;
+#pragma unroll 1
+          for (int c = 0; c < kD; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(from + c, o);
+            tmem_ld_wait();
+            loaded(o);
+            float y[2][8];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) y[k >> 3][k & 7] = inv != 0.f ? __uint_as_float(o[k]) * inv : 0.f;
+            if (mine) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint8_t* d = to + (c + 8 * k) * bytes;
+                if (p.out_type == PA_DT_F32) store8<float>(d, y[k]);
+                else if (p.out_type == PA_DT_F16) store8<__half>(d, y[k]);
+                else store8<__nv_bfloat16>(d, y[k]);
+              }
+            }
+            __syncwarp();  // the next load is the whole warp's
+          }
+        } else {
+          const long long slot = slot_of(before.first, before.last, (int)blockIdx.x, p.slot_rows) + row;
+          if (mine) p.part_ml[slot] = make_float2(m, l);
+          float4* to = reinterpret_cast<float4*>(p.part_o + slot * kD);
+#pragma unroll 1
+          for (int c = 0; c < kD; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(from + c, o);
+            tmem_ld_wait();
+            loaded(o);
+            if (mine) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                to[c / 4 + k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                                            __uint_as_float(o[4 * k + 3]));
+            }
+            __syncwarp();
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
+        __syncwarp();
+      }
+      if (!more) break;
+      before = x;
+      tiles += x.j1 - x.j0;
+      ++piece;
+    }
+  } else {
+    // ---- softmax: keys 64 half .. + 63 of a tile, row 32 quarter + lane
+    const int half = w >> 2, quarter = w & 3, row = 32 * quarter + lane;
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    float* red = reinterpret_cast<float*>(smem + SM::kRed);
+    float* sums = reinterpret_cast<float*>(smem + SM::kSum);
+    float* refs = reinterpret_cast<float*>(smem + SM::kRef);
+    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+    // A warp whose wait expired arrives nowhere any more and says so (the tile's `leave`) before
+    // the barrier at which the eight warps meet first in every tile; after it all of them
+    // leave, until then all walk the same tiles, and so the same barriers.
+    bool live = true, gone = false;
+    uint32_t piece = 0;
+    int j = 0;  // the CTA's tile
+    while (!gone && walk.next(p, x)) {
+      const PromptUnit& u = p.unit[x.unit];
+      const Span s = span_of(u, p.window, p.sinks);
+      const int last_pos = u.pos + (unit_row0(u) + unit_rows(u) - 1) / kGqa;
+      const int last_lo = last_pos >= p.window ? last_pos - p.window + 1 : 0;
+      const RowKeys mine = row_keys(u, s, row, p.window);
+      const long long reg = (long long)u.group0 * p.n_kv_heads + (long long)x.head * u.groups;
+      float ref = 0.f;
+      uint64_t l2 = 0;  // sums of weights over this thread's keys, in two
+      for (int t = x.j0; t < x.j1; ++t, ++j) {
+        const int v0 = t * kKeys + 64 * half, n = tile_keys(s, t);
+        uint64_t wide = 0;  // of this thread's keys (all rows': the same)
+        if (p.wide) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int v = v0 + 16 * g;
+            if (v < s.end)
+              wide |= (uint64_t)__ldg(reinterpret_cast<const uint16_t*>(p.wide) + reg + group_of(u, s, v)) << (16 * g);
+          }
+        }
+        live = live && warp_wait(s_full + 8 * (j & 1), (j >> 1) & 1, p.err, abort);
+        if (!live) leave[j & 1] = 1;
+        tc_fence_after();
+        const uint32_t s_at = kPSCol + 128 * (j & 1) + lanes;
+        uint32_t a[2][32];
+        if (64 * half < n) {  // whole warps
+          tmem_ld32(s_at + 64 * half, a[0]);
+          tmem_ld32(s_at + 64 * half + 32, a[1]);
+          tmem_ld_wait();
+          loaded(a[0]);
+          loaded(a[1]);
+        }
+        if (wide) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (wide >> k & 1) a[k >> 5][k & 31] = __float_as_uint(__uint_as_float(a[k >> 5][k & 31]) * 256.f);
+        }
+        if (!sees_all(s, t * kKeys, u.pos, last_lo, p.sinks) || 64 * half >= n) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (!mine.has(v0 + k, p.sinks)) a[k >> 5][k & 31] = 0xff800000u;  // -inf
+        }
+        const uint64_t nref = pack2(-ref, -ref);
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) {
+          uint32_t* r = &a[k >> 5][k & 31];
+          put2(r, fma2(get2(r), scale2, nref));
+          top = fmaxf(top, fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+        }
+        const bool first_tile = t == x.j0;
+        const bool raise = bar_or(1, 32 * kPSmWarps, first_tile || top > kLazyLog2);
+        if (leave[j & 1]) {
+          gone = true;
+          break;
+        }
+        if (raise) {
+          red[half * kPromptRows + row] = top;
+          __syncwarp();
+          named_bar_sync(1, 32 * kPSmWarps);
+          const float m = fmaxf(red[row], red[kPromptRows + row]);
+          // a row that sees no key yet keeps a reference of 0; it will see none later in the piece either
+          const float d = first_tile ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);
+          ref += d;
+          const uint64_t nd = pack2(-d, -d);
+#pragma unroll
+          for (int k = 0; k < 64; k += 2) {
+            uint32_t* r = &a[k >> 5][k & 31];
+            put2(r, add2(get2(r), nd));
+          }
+          if (first_tile) {
+            l2 = 0;
+          } else if (__any_sync(0xffffffffu, d != 0.f)) {  // O holds the tiles before: half of the dims
+            const float f = ex2(-d);
+            l2 = mul2(l2, pack2(f, f));
+            if (!warp_wait(pv_done + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1, p.err, abort)) {
+              live = false;
+              leave[(j + 1) & 1] = 1;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < kD / 2; c += 8) {
+              uint32_t o[8];
+              tmem_ld8(kPOCol + 128 * half + c + lanes, o);
+              tmem_ld_wait();
+              loaded(o);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st8(kPOCol + 128 * half + c + lanes, o);
+            }
+          }
+        }
+        uint32_t h[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const uint32_t* r = &a[k >> 4][2 * (k & 15)];
+          const float e0 = ex2(__uint_as_float(r[0])), e1 = ex2(__uint_as_float(r[1]));
+          l2 = add2(l2, pack2(e0, e1));
+          h[k] = pack_half2(e0, e1);
+        }
+        tmem_st32(s_at + 32 * half, h);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (live && lane == 0) mbar_arrive(p_full + 8 * (j & 1));
+        __syncwarp();
+      }
+      if (gone) break;
+      const float2 l = unpack2(l2);
+      sums[(piece & 1) * 256 + half * 128 + row] = l.x + l.y;
+      if (half == 0) refs[(piece & 1) * 128 + row] = ref;
+      __syncwarp();
+      if (live && lane == 0) mbar_arrive(l_full + 8 * (piece & 1));
+      __syncwarp();
+      ++piece;
+    }
+  }
+  (void)n;
+  tc_fence_before();
+  __syncthreads();
+  // after an expired wait, copies that nobody waited for must still land
+  if (w == kCopyWarp && *abort) {
+    for (int i = max(0, issued - kNStages); i < issued; ++i)
+      mbar_wait(full + 8 * (i % kNStages), (uint32_t)((i / kNStages) & 1), p.err, abort, false, kWaitTimeoutNs / 8);
+  }
+  if (w == 0) {
+    tc_fence_after();
+    tmem_dealloc(*tmem_slot, kTmemCols);
+  }
+}
+
+}  // namespace
+
+__device__ __forceinline__ long long query_at(const PromptParams& p, int t, int h) { return t * p.q_stride + h * kD; }
+
+namespace {
+
+template <class P>
+pa_status launch_one(void (*kernel)(P), const P& p, int grid, int threads, int smem, cudaStream_t cs) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = cs;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+pa_status launch_prepare(const PrepareParams& p, int sms, cudaStream_t cs) {
+  const long long items = (long long)p.groups * 4 * p.n_kv_heads, ctas = (items + kPrepareWarps - 1) / kPrepareWarps;
+  return launch_one(pa_prompt_prepare_kernel, p, (int)(ctas < 16ll * sms ? ctas : 16ll * sms), 32 * kPrepareWarps, 0, cs);
+}
+
+pa_status launch_prompt(const PromptParams& p, cudaStream_t cs) {
+  return launch_one(pa_prompt_kernel, p, p.n_ctas, kPThreads, PSmem::kLaunch, cs);
+}
+
+pa_status prompt_ready() {
+  return cudaFuncSetAttribute(pa_prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem::kLaunch) == cudaSuccess ? PA_OK
+                                                                                                                            : PA_ERR_CUDA;
+}
+
+}  // namespace pa_prefix

@@ -1,0 +1,107 @@
+// Windowed attention of many new tokens (chunks of prompt, whole prompts): parameters of its
+// kernels (pa_prompt.cu) for the host side (pa_window.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "pa_window_impl.cuh"
+
+namespace pa_prefix {
+
+constexpr int kPromptRows = 128;              // query rows of a unit
+constexpr int kGroupBytes = kGroup * kD * 2;  // a group's keys (or values) in binary16
+
+// A unit of a prompt, and where its sequence's keys lie in the workspace: the row groups
+// group0 .. group0 + groups - 1, of position v (v < s16), else v + shift0.
+struct PromptUnit : Unit {
+  int32_t groups, group0, shift0;
+};
+
+// The key order of all new tokens of a sequence: that of a unit from its first to its last.
+struct SeqSpan : Span {
+  int groups;
+};
+
+inline SeqSpan seq_span(int len, int n_new, int window, int sinks) {
+  SeqSpan s;
+  const int first = len - n_new;
+  s.lo = first >= window ? first - window + 1 : 0;
+  s.s16 = (sinks + kGroup - 1) & ~(kGroup - 1);
+  const int group = s.lo & ~(kGroup - 1);
+  s.shift = group > s.s16 ? group - s.s16 : 0;
+  s.end = len - s.shift;
+  s.groups = ceil_div(s.end, kGroup);
+  return s;
+}
+
+struct PromptParams {
+  static constexpr int kUnitRows = kPromptRows, kMaxUnits = 256;
+  const uint8_t* q;
+  const int32_t* lens;  // device lengths, only compared
+  const uint8_t* k;     // the workspace's keys and values, and which keys are wide (or NULL: none can be)
+  const uint8_t* v;
+  const uint8_t* wide;
+  int32_t* err;
+  float2* part_ml;
+  float* part_o;
+  uint8_t* out;
+  float* lse;
+  long long q_stride, out_stride;
+  int q_type, out_type, n_kv_heads, n_q_heads;
+  int n_units, n_ctas, weigh;
+  int total_len, total_tiles;
+  int window, sinks;
+  int slot_rows;
+  float scale_log2;
+  PromptUnit unit[kMaxUnits];
+};
+
+// What a piece takes before its first tile, in tiles' eighths.
+__host__ __device__ __forceinline__ Cost cost_of(const PromptParams& p, const Unit&) { return p.weigh ? Cost{10, 8} : Cost{0, 1}; }
+
+// The places of a unit's order that a row sees: v <= hi with v >= lo or v < sinks (a row behind
+// the unit's: none).
+struct RowKeys {
+  int lo, hi;
+  __host__ __device__ __forceinline__ bool has(int v, int sinks) const { return v <= hi && (v >= lo || v < sinks); }
+};
+
+__host__ __device__ __forceinline__ RowKeys row_keys(const Unit& u, const Span& s, int row, int window) {
+  const int pos = u.pos + (unit_row0(u) + row) / kGqa;
+  return RowKeys{(pos >= window ? pos - window + 1 : 0) - s.shift, row < unit_rows(u) ? pos - s.shift : -1};
+}
+
+// The group of place v of a unit's order among its sequence's.
+__host__ __device__ __forceinline__ int group_of(const PromptUnit& u, const Span& s, int v) {
+  return (v < s.s16 ? v : v + s.shift - u.shift0) >> 4;
+}
+
+// A sequence's keys on their way into the workspace.
+struct PromptSeq {
+  int32_t seq, len;
+  int32_t lo;  // first key of its first new token's window
+  int32_t s16, shift, groups, group0;
+  int32_t at;  // groups of the launch's sequences before it
+};
+
+struct PrepareParams {
+  static constexpr int kMaxPromptSeqs = 128;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const int32_t* table;
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* wide;
+  int32_t* err;
+  int k_type, v_type, n_kv_heads, page_size, table_stride, n_blocks;
+  int sinks;
+  int n_seqs, groups;
+  PromptSeq seq[kMaxPromptSeqs];
+};
+
+// Launches (programmatic dependents of what runs before them on the stream).
+pa_status launch_prepare(const PrepareParams& p, int sms, cudaStream_t cs);
+pa_status launch_prompt(const PromptParams& p, cudaStream_t cs);
+pa_status prompt_ready();  // raises the kernel's limits on the current device
+
+}  // namespace pa_prefix

@@ -1,6 +1,7 @@
 // Attention over a sliding window and first keys: the plan, the merge of the segments that
-// are cut, and the host side of pa_attend_window.  The kernel over the keys is in
-// pa_window_impl.cuh and pa_prefix_impl.cuh, compiled once per (K format, V format) pair.
+// are cut, and the host side of pa_attend_window.  The kernel over the keys for sequences with few
+// new tokens is in pa_window_impl.cuh and pa_prefix_impl.cuh, compiled once per (K format,
+// V format) pair; the kernels for those with many are in pa_prompt.cu.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -10,6 +11,7 @@
 
 #include "pa_io.cuh"
 #include "pa_merge.cuh"
+#include "pa_prompt.cuh"
 #include "pa_window_impl.cuh"
 
 using namespace pa_dev;
@@ -22,6 +24,7 @@ constexpr int64_t kMaxLen = 0x7fffffff - 2 * kKeys;  // a tile past the last key
 constexpr uint32_t kMaxNew = 1u << 24;               // new tokens of a sequence
 constexpr int kMaxCtas = 256;
 constexpr int64_t kMaxPlaces = 1ll << 30;
+constexpr int32_t kPromptTokens = 64;  // sequences of so many new tokens or more are the prompts' kernel's
 
 // ------------------------------------------------------------------ merge
 
@@ -79,7 +82,7 @@ int type_slot(int t) { return t == PA_F16 ? 0 : t == PA_Q4_0 ? 1 : 2; }
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int g_sms[kMaxDevices];
-bool g_ready[kMaxDevices][3][3];  // the kernel's shared-memory limit is raised
+bool g_ready[kMaxDevices][3][3];  // the kernels' shared-memory limits are raised
 
 // CTAs of a launch on the device (one per SM), and, with a kernel, its limit raised there
 // (the device must be current for that).
@@ -94,29 +97,81 @@ pa_status device_ready(int device, int kt, int vt, const WindowKernel* ki, int* 
   *ctas = std::min(g_sms[device], kMaxCtas);
   if (ki) {
     bool& r = g_ready[device][type_slot(kt)][type_slot(vt)];
-    if (!r && cudaFuncSetAttribute(ki->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ki->smem) != cudaSuccess)
+    if (!r && (cudaFuncSetAttribute(ki->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ki->smem) != cudaSuccess ||
+               prompt_ready() != PA_OK))
       return PA_ERR_CUDA;
     r = true;
   }
   return PA_OK;
 }
 
-struct WsLayout {
-  size_t o, total;  // (m, l) at 0, O at o
+// What a batch needs, its lengths checked.
+struct Batch {
+  const int32_t* lens;
+  const int32_t* n_new;
+  uint32_t n_seq;
+  int window, sinks, heads;
+  uint64_t tokens;
+  uint32_t most;        // new tokens of the largest sequence of few
+  uint32_t prompts;     // sequences of many
+  int64_t groups;       // row groups of their keys
+  bool many(uint32_t s) const { return is_many(n_new[s]); }
+  static bool is_many(int32_t n) { return n >= kPromptTokens; }
 };
 
-// Two slots for each CTA, of the rows of the largest unit.
+pa_status check_batch(const pa_pool_desc& d, uint64_t max_len, Batch* b) {
+  b->tokens = 0;
+  b->most = b->prompts = 0;
+  b->groups = 0;
+  for (uint32_t i = 0; i < b->n_seq; ++i) {
+    const int64_t len = b->lens[i], n = b->n_new[i];
+    if (n < 0 || len < n || len > (int64_t)max_len) return PA_ERR_INVALID;
+    if (n > kMaxNew || len > kMaxLen) return PA_ERR_UNSUPPORTED;
+    if (n == 0) continue;
+    b->tokens += (uint64_t)n;
+    // one unit fits a launch: its window is at most that long
+    const int64_t keys = std::min<int64_t>(len, (int64_t)b->window + (int64_t)b->sinks + 4 * kKeys);
+    if (d.n_kv_heads * (kLead + (keys / kKeys + 1) * (kTileCost + 2)) >= kMaxPlaces) return PA_ERR_UNSUPPORTED;
+    if (b->many(i)) {
+      ++b->prompts;
+      b->groups += seq_span((int)len, (int)n, b->window, b->sinks).groups;
+    } else {
+      b->most = std::max(b->most, (uint32_t)n);
+    }
+  }
+  return b->tokens > 0x7fffffffu || b->groups > 0x7fffffff / 16 ? PA_ERR_UNSUPPORTED : PA_OK;
+}
+
+// The workspace: two slots of (m, l) and O for each CTA, of the rows of the largest unit, for
+// the kernel of few tokens and for that of many; the many's keys, values and which keys are wide.
+struct WsLayout {
+  size_t o, prompt_ml, prompt_o, k, v, wide, total;  // the first (m, l) at 0
+};
+
 int slot_rows_of(uint32_t max_new) { return (int)std::min<uint64_t>(kRows, (uint64_t)kGqa * max_new); }
 
-WsLayout layout_of(int ctas, uint32_t max_new) {
-  const size_t rows = 2 * (size_t)ctas * slot_rows_of(max_new);
+WsLayout layout_of(int ctas, const Batch& b) {
+  const size_t rows = 2 * (size_t)ctas * slot_rows_of(b.most), many = b.prompts ? 2 * (size_t)ctas * kPromptRows : 0;
+  const size_t keys = (size_t)b.groups * b.heads * kGroupBytes;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t from = at;
+    at += (bytes + 255) & ~size_t(255);
+    return from;
+  };
   WsLayout w;
-  w.o = (rows * sizeof(float2) + 255) & ~size_t(255);
-  w.total = w.o + rows * kD * sizeof(float);
+  take(rows * sizeof(float2));
+  w.o = take(rows * kD * sizeof(float));
+  w.prompt_ml = take(many * sizeof(float2));
+  w.prompt_o = take(many * kD * sizeof(float));
+  w.k = take(keys);
+  w.v = take(keys);
+  w.wide = take((size_t)b.groups * b.heads * 2);
+  w.total = at;
   return w;
 }
 
-// The units of the batch in order: sequence s's rows 64 rt .. of 6 n.
+// The units of the batch in order: rows P::kUnitRows rt .. of the 6 n of sequence s.
 struct Cursor {
   uint32_t seq;
   int rt;
@@ -131,27 +186,30 @@ struct Plan {
   int cuts, rows;  // cut segments, rows of the largest
 };
 
-Plan plan_chunk(WindowParams& p, MergeParams& m, const int32_t* lens, const int32_t* n_new, uint32_t n_seq, int max_ctas, Cursor* at) {
+template <class P>
+Plan plan_chunk(P& p, MergeParams& m, const Batch& b, bool many, int max_ctas, Cursor* at) {
+  const int32_t* const lens = b.lens;
+  const int32_t* const n_new = b.n_new;
   const int heads = p.n_kv_heads;
   int64_t tiles = 0;
   p.n_units = 0;
-  for (; at->seq < n_seq && p.n_units < kMaxUnits; at->token += n_new[at->seq++], at->rt = 0) {
-    const int rows = kGqa * n_new[at->seq];
-    for (; at->rt * kRows < rows && p.n_units < kMaxUnits; ++at->rt) {
-      const int row = at->rt * kRows;
+  for (; at->seq < b.n_seq && p.n_units < P::kMaxUnits; at->token += n_new[at->seq++], at->rt = 0) {
+    const int rows = b.many(at->seq) == many ? kGqa * n_new[at->seq] : 0;
+    for (; at->rt * P::kUnitRows < rows && p.n_units < P::kMaxUnits; ++at->rt) {
+      const int row = at->rt * P::kUnitRows;
       Unit& u = p.unit[p.n_units];
       u.seq = (int32_t)at->seq;
       u.token = at->token + row / kGqa;
       u.len = lens[at->seq];
       u.pos = u.len - n_new[at->seq] + row / kGqa;
-      u.rows_row0 = std::min(kRows, rows - row) | (row % kGqa) << 8;
+      u.rows_row0 = std::min(P::kUnitRows, rows - row) | (row % kGqa) << 8;
       u.tile = (int32_t)tiles;
       const int64_t more = tiles + (int64_t)heads * tiles_of(u, p.window, p.sinks);
       if (p.n_units > 0 && more > (kMaxPlaces >> 5)) break;  // the next launch's
       tiles = more;
       ++p.n_units;
     }
-    if (at->rt * kRows < rows) break;
+    if (at->rt * P::kUnitRows < rows) break;
   }
   if (p.n_units == 0) return Plan{0, 0};
   p.total_tiles = (int)tiles;
@@ -161,7 +219,7 @@ Plan plan_chunk(WindowParams& p, MergeParams& m, const int32_t* lens, const int3
   int64_t places = 0;
   for (int i = 0; i < p.n_units; ++i) {
     Unit& u = p.unit[i];
-    const Cost c = cost_of(p.weigh, unit_rows(u));
+    const Cost c = cost_of(p, u);
     u.at = (int32_t)places;
     places += (int64_t)heads * (c.lead + (int64_t)tiles_of(u, p.window, p.sinks) * c.tile);
   }
@@ -183,32 +241,71 @@ Plan plan_chunk(WindowParams& p, MergeParams& m, const int32_t* lens, const int3
   return Plan{cuts, rows};
 }
 
-pa_status launch_chunk(const WindowParams& p, const MergeParams& m, const Plan& plan, const WindowKernel& ki, int max_ctas,
-                       cudaStream_t cs) {
-  if (p.n_units == 0) return PA_OK;
-  // Both are programmatic dependents of what runs before them on the stream: their set-up
-  // overlaps its tail, and they wait for it before they read.
+// Every launch is a programmatic dependent of what runs before it on the stream: its set-up
+// overlaps the other's tail, and it waits for it before it reads.
+struct Launch {
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)p.n_ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)ki.smem;
-  cfg.stream = cs;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, ki.fn, p) != cudaSuccess) return PA_ERR_CUDA;
+  explicit Launch(cudaStream_t cs) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = cs;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
+
+pa_status launch_few(const WindowParams& p, const WindowKernel& ki, cudaStream_t cs) {
+  Launch l(cs);
+  l.cfg.gridDim = dim3((unsigned)p.n_ctas);
+  l.cfg.blockDim = dim3(kThreads);
+  l.cfg.dynamicSmemBytes = (size_t)ki.smem;
+  return cudaLaunchKernelEx(&l.cfg, ki.fn, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status launch_merge(const MergeParams& m, const Plan& plan, int max_ctas, cudaStream_t cs) {
   if (plan.cuts == 0) return PA_OK;
+  Launch l(cs);
   const int wide = merge_groups((int64_t)plan.cuts * plan.rows, max_ctas);
-  cfg.gridDim = dim3((unsigned)plan.cuts, (unsigned)plan.rows);
-  cfg.blockDim = dim3(64 * wide);
-  cfg.dynamicSmemBytes = 0;
+  l.cfg.gridDim = dim3((unsigned)plan.cuts, (unsigned)plan.rows);
+  l.cfg.blockDim = dim3(64 * wide);
   const auto merge = wide == 8   ? pa_window_merge_kernel<8>
                      : wide == 4 ? pa_window_merge_kernel<4>
                      : wide == 2 ? pa_window_merge_kernel<2>
                                  : pa_window_merge_kernel<1>;
-  return cudaLaunchKernelEx(&cfg, merge, m) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return cudaLaunchKernelEx(&l.cfg, merge, m) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// The keys of the batch's sequences of many tokens into the workspace.
+pa_status prepare_prompts(PrepareParams& r, const Batch& b, int sms, cudaStream_t cs) {
+  int group0 = 0;
+  for (uint32_t i = 0; i < b.n_seq;) {
+    r.n_seqs = r.groups = 0;
+    for (; i < b.n_seq && r.n_seqs < PrepareParams::kMaxPromptSeqs; ++i) {
+      if (!b.many(i)) continue;
+      const SeqSpan s = seq_span(b.lens[i], b.n_new[i], b.window, b.sinks);
+      r.seq[r.n_seqs++] = PromptSeq{(int32_t)i, b.lens[i], s.lo, s.s16, s.shift, s.groups, group0, r.groups};
+      r.groups += s.groups;
+      group0 += s.groups;
+    }
+    if (r.n_seqs == 0) break;
+    const pa_status st = launch_prepare(r, sms, cs);
+    if (st != PA_OK) return st;
+  }
+  return PA_OK;
+}
+
+// Where the units' sequences have their keys; (seq, group0): of the launches before.
+void place_prompts(PromptParams& p, const Batch& b, uint32_t* seq, int* group0) {
+  for (int i = 0; i < p.n_units; ++i) {
+    PromptUnit& u = p.unit[i];
+    for (; *seq < (uint32_t)u.seq; ++*seq)
+      if (b.many(*seq)) *group0 += seq_span(b.lens[*seq], b.n_new[*seq], b.window, b.sinks).groups;
+    const SeqSpan s = seq_span(u.len, b.n_new[u.seq], b.window, b.sinks);
+    u.groups = s.groups;
+    u.group0 = *group0;
+    u.shift0 = s.shift;
+  }
 }
 
 pa_status check_pool(const pa_pool* pool, pa_pool_desc* d, WindowKernel* ki) {
@@ -216,14 +313,44 @@ pa_status check_pool(const pa_pool* pool, pa_pool_desc* d, WindowKernel* ki) {
   return d->head_dim == (uint32_t)kD && lookup_kernel(d->k_type, d->v_type, ki) ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
+// The window as the kernels take it: at most as long as any sequence.
+int clamp_keys(uint32_t n) { return (int)std::min<uint32_t>(n, kAllKeys); }
+
+// What both kernels' parameters, and the merge's, have in common.
+template <class P>
+void fill(P& p, MergeParams& m, const Batch& b, const pa_pool_desc& d, const void* q, int64_t q_stride, int32_t q_type,
+          const int32_t* lens_dev, float scale, void* out, int64_t out_stride, int32_t out_type, float* lse, uint8_t* ws, size_t ml,
+          size_t o, int slot_rows, int32_t* err) {
+  p.q = static_cast<const uint8_t*>(q);
+  p.lens = m.lens = lens_dev;
+  p.err = m.err = err;
+  m.part_ml = p.part_ml = reinterpret_cast<float2*>(ws + ml);
+  m.part_o = p.part_o = reinterpret_cast<float*>(ws + o);
+  p.out = m.out = static_cast<uint8_t*>(out);
+  p.lse = m.lse = lse;
+  p.q_stride = q_stride;
+  p.out_stride = m.out_stride = out_stride;
+  p.q_type = q_type;
+  p.out_type = m.out_type = out_type;
+  p.n_kv_heads = (int)d.n_kv_heads;
+  p.n_q_heads = m.n_q_heads = (int)d.n_kv_heads * kGqa;
+  p.window = b.window;
+  p.sinks = b.sinks;
+  p.slot_rows = m.slot_rows = slot_rows;
+  p.scale_log2 = scale * kLog2e;
+}
+
 }  // namespace
 
-extern "C" size_t pa_attend_window_workspace_size(const pa_pool* pool, uint32_t max_new, int device) {
+extern "C" size_t pa_attend_window_workspace_size(const pa_pool* pool, const int32_t* seq_lens_host, const int32_t* n_new,
+                                                  uint32_t n_seq, uint32_t window, uint32_t sinks, int device) {
   pa_pool_desc d;
   WindowKernel ki;
   int ctas = 0;
-  if (check_pool(pool, &d, &ki) != PA_OK || device_ready(device, d.k_type, d.v_type, nullptr, &ctas) != PA_OK) return 0;
-  return layout_of(ctas, max_new).total;
+  if (check_pool(pool, &d, &ki) != PA_OK || (n_seq && (!seq_lens_host || !n_new))) return 0;
+  Batch b{seq_lens_host, n_new, n_seq, clamp_keys(window ? window : ~0u), clamp_keys(sinks), (int)d.n_kv_heads};
+  if (check_batch(d, ~0u, &b) != PA_OK || device_ready(device, d.k_type, d.v_type, nullptr, &ctas) != PA_OK) return 0;
+  return layout_of(ctas, b).total;
 }
 
 extern "C" pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_t q_stride, int32_t q_type, const void* k_pool,
@@ -241,23 +368,11 @@ extern "C" pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_
   if (n_seq == 0) return PA_OK;
   if (!seq_lens_host || !n_new) return PA_ERR_INVALID;
   if (!(scale > 0.f) || !std::isfinite(scale)) return PA_ERR_INVALID;
-  const int w = window == 0 ? kAllKeys : (int)std::min<uint32_t>(window, kAllKeys), s = (int)std::min<uint32_t>(sinks, kAllKeys);
   // every length is checked before the first launch
-  uint64_t tokens = 0;
-  uint32_t most = 0;
-  for (uint32_t i = 0; i < n_seq; ++i) {
-    const int64_t len = seq_lens_host[i], n = n_new[i];
-    if (n < 0 || len < n || len > (int64_t)table_stride * d.page_size) return PA_ERR_INVALID;
-    if (n > kMaxNew || len > kMaxLen) return PA_ERR_UNSUPPORTED;
-    tokens += (uint64_t)n;
-    most = std::max(most, (uint32_t)n);
-    if (n > 0) {  // one unit fits a launch: its window is at most that long
-      const int64_t keys = std::min<int64_t>(len, (int64_t)w + (int64_t)s + 4 * kKeys);
-      if (d.n_kv_heads * (kLead + (keys / kKeys + 1) * (kTileCost + 2)) >= kMaxPlaces) return PA_ERR_UNSUPPORTED;
-    }
-  }
-  if (tokens == 0) return PA_OK;
-  if (tokens > 0x7fffffffu) return PA_ERR_UNSUPPORTED;
+  Batch b{seq_lens_host, n_new, n_seq, clamp_keys(window ? window : ~0u), clamp_keys(sinks), (int)d.n_kv_heads};
+  st = check_batch(d, (uint64_t)table_stride * d.page_size, &b);
+  if (st != PA_OK) return st;
+  if (b.tokens == 0) return PA_OK;
   if (!q || !k_pool || !v_pool || !block_table || !seq_lens_dev || !out || !workspace || !err || table_stride == 0 ||
       table_stride > 0x7fffffffu)
     return PA_ERR_INVALID;
@@ -272,43 +387,59 @@ extern "C" pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_
   if (cudaGetDevice(&device) != cudaSuccess) return PA_ERR_CUDA;
   st = device_ready(device, d.k_type, d.v_type, &ki, &ctas);
   if (st != PA_OK) return st;
-  const WsLayout lay = layout_of(ctas, most);
+  const WsLayout lay = layout_of(ctas, b);
   if (ws_bytes < lay.total) return PA_ERR_INVALID;
-  static thread_local WindowParams p;  // kept off the stack
-  static thread_local MergeParams m;
-  p.q = static_cast<const uint8_t*>(q);
-  p.k_pool = static_cast<const uint8_t*>(k_pool);
-  p.v_pool = static_cast<const uint8_t*>(v_pool);
-  p.table = block_table;
-  p.lens = m.lens = seq_lens_dev;
-  p.err = m.err = err;
-  m.part_ml = p.part_ml = static_cast<float2*>(workspace);
-  m.part_o = p.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + lay.o);
-  p.out = m.out = static_cast<uint8_t*>(out);
-  p.lse = m.lse = lse;
-  p.q_stride = q_stride;
-  p.out_stride = m.out_stride = out_stride;
-  p.q_type = q_type;
-  p.out_type = m.out_type = out_type;
-  p.n_kv_heads = (int)d.n_kv_heads;
-  p.n_q_heads = m.n_q_heads = (int)n_q_heads;
-  p.page_size = (int)d.page_size;
-  p.page_shift = -1;
-  for (int i = 4; i < 31; ++i)
-    if (d.page_size == 1u << i) p.page_shift = i;
-  p.table_stride = (int)table_stride;
-  p.n_blocks = (int)d.n_blocks;
-  p.window = w;
-  p.sinks = s;
-  p.slot_rows = m.slot_rows = slot_rows_of(most);
-  p.scale_log2 = scale * kLog2e;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  static thread_local MergeParams m;  // kept off the stack
   // Launches in order on the stream, sharing the workspace: each one's kernel waits for the
   // one before to complete.
-  Cursor at{0, 0, 0};
-  while (at.seq < n_seq) {
-    const Plan plan = plan_chunk(p, m, seq_lens_host, n_new, n_seq, ctas, &at);
-    st = launch_chunk(p, m, plan, ki, ctas, reinterpret_cast<cudaStream_t>(stream));
-    if (st != PA_OK) return st;
+  if (b.most > 0) {
+    static thread_local WindowParams p;
+    fill(p, m, b, d, q, q_stride, q_type, seq_lens_dev, scale, out, out_stride, out_type, lse, ws, 0, lay.o, slot_rows_of(b.most), err);
+    p.k_pool = static_cast<const uint8_t*>(k_pool);
+    p.v_pool = static_cast<const uint8_t*>(v_pool);
+    p.table = block_table;
+    p.page_size = (int)d.page_size;
+    p.page_shift = -1;
+    for (int i = 4; i < 31; ++i)
+      if (d.page_size == 1u << i) p.page_shift = i;
+    p.table_stride = (int)table_stride;
+    p.n_blocks = (int)d.n_blocks;
+    for (Cursor at{0, 0, 0}; at.seq < n_seq;) {
+      const Plan plan = plan_chunk(p, m, b, false, ctas, &at);
+      if (p.n_units == 0) break;
+      if ((st = launch_few(p, ki, cs)) != PA_OK || (st = launch_merge(m, plan, ctas, cs)) != PA_OK) return st;
+    }
+  }
+  if (b.prompts > 0) {
+    static thread_local PromptParams p;
+    static thread_local PrepareParams r;
+    fill(p, m, b, d, q, q_stride, q_type, seq_lens_dev, scale, out, out_stride, out_type, lse, ws, lay.prompt_ml, lay.prompt_o, kPromptRows,
+         err);
+    p.k = r.k = ws + lay.k;
+    p.v = r.v = ws + lay.v;
+    p.wide = r.wide = d.k_type == PA_F16 ? nullptr : ws + lay.wide;
+    r.k_pool = static_cast<const uint8_t*>(k_pool);
+    r.v_pool = static_cast<const uint8_t*>(v_pool);
+    r.table = block_table;
+    r.err = err;
+    r.k_type = d.k_type;
+    r.v_type = d.v_type;
+    r.n_kv_heads = (int)d.n_kv_heads;
+    r.page_size = (int)d.page_size;
+    r.table_stride = (int)table_stride;
+    r.n_blocks = (int)d.n_blocks;
+    r.sinks = b.sinks;
+    if ((st = prepare_prompts(r, b, ctas, cs)) != PA_OK) return st;
+    uint32_t seq = 0;
+    int group0 = 0;
+    for (Cursor at{0, 0, 0}; at.seq < n_seq;) {
+      const Plan plan = plan_chunk(p, m, b, true, ctas, &at);
+      if (p.n_units == 0) break;
+      place_prompts(p, b, &seq, &group0);
+      if ((st = launch_prompt(p, cs)) != PA_OK || (st = launch_merge(m, plan, ctas, cs)) != PA_OK) return st;
+    }
   }
   return PA_OK;
 }

@@ -31,7 +31,6 @@
 
 namespace pa_prefix {
 
-constexpr int kMaxUnits = 448;  // units per launch
 constexpr int kAllKeys = 0x7fffffff - 2 * kKeys;  // a window as long as any sequence: that of a call without one
 
 struct Unit {
@@ -45,6 +44,7 @@ struct Unit {
 
 struct WindowParams {
   static constexpr bool kWindow = true;
+  static constexpr int kUnitRows = kRows, kMaxUnits = 448;  // query rows of a unit, units per launch
   using Live = int4;  // of a tile: its live keys are those before x and from y to z - 1
   const uint8_t* q;
   const uint8_t* k_pool;
@@ -88,12 +88,18 @@ __host__ __device__ inline Span span_of(const Unit& u, int window, int sinks) {
 }
 
 // ------------------------------------------------------------------ the walk
+//
+// P: WindowParams, or those of the prompts' kernel.
 
-__host__ __device__ __forceinline__ void pos_sizes(const WindowParams& p, Pos& t) {
+__host__ __device__ __forceinline__ Cost cost_of(const WindowParams& p, const Unit& u) { return cost_of(p.weigh, unit_rows(u)); }
+
+template <class P>
+__host__ __device__ __forceinline__ void pos_sizes(const P& p, Pos& t) {
   t.nt = ceil_div(span_of(p.unit[t.unit], p.window, p.sinks).end, kKeys);
 }
 
-__host__ __device__ __forceinline__ void advance(const WindowParams& p, Pos& t) {
+template <class P>
+__host__ __device__ __forceinline__ void advance(const P& p, Pos& t) {
   if (++t.j < t.nt) return;
   t.j = 0;
   if (++t.head < p.n_kv_heads) return;
@@ -103,7 +109,8 @@ __host__ __device__ __forceinline__ void advance(const WindowParams& p, Pos& t) 
 }
 
 // The first tile at place x or after it.
-__host__ __device__ __forceinline__ Pos locate(const WindowParams& p, int x) {
+template <class P>
+__host__ __device__ __forceinline__ Pos locate(const P& p, int x) {
   Pos t;
   t.pre = false;
   t.rt = 0;
@@ -116,7 +123,7 @@ __host__ __device__ __forceinline__ Pos locate(const WindowParams& p, int x) {
   t.unit = lo;
   x -= p.unit[lo].at;
   pos_sizes(p, t);
-  const Cost c = cost_of(p.weigh, unit_rows(p.unit[lo]));
+  const Cost c = cost_of(p, p.unit[lo]);
   const int len = c.lead + t.nt * c.tile;
   t.head = x / len;
   t.j = ((x > t.head * len + c.lead ? x - t.head * len - c.lead : 0) + c.tile - 1) / c.tile;

@@ -193,7 +193,7 @@ def test_streams_graphs_and_repeats():
     want, want_lse = call(q)
     q2 = q.flip(0).contiguous()
     want2, _ = call(q2)
-    ws = torch.full((pa_attend_window_workspace_size(cache.pool, 60),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((pa_attend_window_workspace_size(cache.pool, w.seq_lens, n_new, 1500, 4),), 255, dtype=torch.uint8, device="cuda")
     got, got_lse = call(q, workspace=ws)
     assert torch.equal(got, want) and torch.equal(got_lse, want_lse)
     streams = [torch.cuda.Stream() for _ in range(2)]
@@ -255,3 +255,158 @@ def test_refusals():
     torch.cuda.synchronize()
     assert cache.check() == PA_OK
     PagedKVCache(1, 16, Q8, Q8)
+
+
+@pytest.mark.parametrize("kt,vt", [(F16, F16), (Q4, Q8), (Q8, Q4)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (16, 1), (100, 4), (128, 16), (129, 130), (600, 17), (2000, 0)])
+def test_prompts(kt, vt, window, sinks):
+    """Sequences of many new tokens beside those of few: from the first token on, after others, of odd lengths, with
+    pages that no power of two counts."""
+    n_new = [64, 1, 150, 0, 300, 63, 65]
+    lens = [64, 700, 151, 0, 1100, 63, 1500]
+    w = window_batch(lens, n_new, 48, kt, vt, seed=window + sinks)
+    against_definition(w, n_new, window, sinks, torch.bfloat16, what=f"window {window}, sinks {sinks}")
+
+
+@pytest.mark.parametrize("qt,ot", [(torch.float32, torch.float16), (torch.float16, torch.float32), (torch.bfloat16, torch.bfloat16)])
+def test_prompts_in_rows_of_any_type(qt, ot):
+    n_new = [70, 90]
+    w = window_batch([500, 90], n_new, 16, Q8, Q8)
+    x = torch.full((170, 32, 256), float("nan"), device="cuda").to(qt)
+    x[:160, :24] = to_dev(w.q).to(qt)
+    big = torch.full((170, 30, 256), 7.0, device="cuda").to(ot)
+    lse = torch.full((170, 24), 7.0, device="cuda")
+    cache, tab = device_cache(w)
+    out, _ = attend(w, n_new, 128, 4, cache=cache, tab=tab, q=x[:, :24], out=big[:, 3:27], lse=lse)
+    want, want_lse = attend64(w, n_new, 128, 4, x[:160, :24].float().cpu().numpy())
+    assert_close(out[:160].float().cpu().numpy(), want)
+    assert_lse_close(lse[:160].cpu().numpy(), want_lse)
+    assert (out[160:] == 7).all() and (lse[160:] == 7).all() and (big[:, :3] == 7).all() and (big[:, 27:] == 7).all()
+
+
+def test_prompts_of_one_launch_and_several():
+    against_definition(window_batch([6000], [5800], 64, Q8, Q8), [5800], 80, 4, torch.float16)  # more than 256 units
+    n_new = [64 + i % 3 for i in range(140)]  # more sequences than a launch prepares
+    against_definition(window_batch([n + 5 * (i % 7) for i, n in enumerate(n_new)], n_new, 16, F16, F16), n_new, 0, 0, torch.float16)
+    against_definition(window_batch([12000], [64], 16, Q4, Q4), [64], 0, 0, torch.bfloat16)  # long segments, cut by many CTAs
+
+
+@pytest.mark.parametrize("size", [100.0, 60000.0])
+def test_prompts_with_large_logits(size):
+    """Later keys that raise the reference by far."""
+    n_new = [200]
+    w = window_batch([900], n_new, 16, F16, F16)
+    k = W.encode_rows(np.sign(np.random.default_rng(1).standard_normal((900, 4, 256))).astype(np.float32) * (size / 60000.0), F16)
+    k[[3, 650, 790, 890]] = W.encode_rows(np.full((4, 4, 256), size / 2000.0, np.float32), F16)
+    w = W.Workload(w.name, w.seq_lens, 1, 16, w.n_blocks, F16, F16, w.table, k, w.v_rows, np.abs(w.q), w.scale)
+    against_definition(w, n_new, 600, 4, torch.float16)
+    against_definition(w, n_new, 0, 0, torch.float16)
+
+
+@pytest.mark.parametrize("kt", [Q4, Q8])
+@pytest.mark.parametrize("n", [3, 80])
+def test_stored_keys_past_binary16(kt, n):
+    """Scales times quants of up to 8.3 10^6 in a few keys, whose logits the small queries keep in range."""
+    n_new = [n]
+    w = window_batch([400], n_new, 16, kt, Q8)
+    k = w.k_rows.copy()
+    size = 34 if kt == Q8 else 18
+    for row in (0, 7, 130, 200, 399):
+        scales = k[row].reshape(4, 8, size)[..., :2].copy().view(np.float16)
+        k[row].reshape(4, 8, size)[..., :2] = (scales / np.abs(scales).max() * 60000).astype(np.float16).view(np.uint8).reshape(4, 8, 2)
+    w = W.Workload(w.name, w.seq_lens, 1, 16, w.n_blocks, kt, Q8, w.table, k, w.v_rows, (w.q * 1e-5).astype(np.float32), w.scale)
+    # queries this small are subnormal in binary16: powers of two keep them exact
+    q = np.sign(w.q).astype(np.float32) * 2.0 ** -20
+    w = W.Workload(w.name, w.seq_lens, 1, 16, w.n_blocks, kt, Q8, w.table, k, w.v_rows, q, w.scale)
+    against_definition(w, n_new, 300, 4)
+    against_definition(w, n_new, 0, 0)
+
+
+@pytest.mark.parametrize("kt,vt", [(F16, F16), (Q8, Q4)])
+def test_prompts_and_what_no_token_sees(kt, vt):
+    """Rows before the windows and behind the sequences, in row groups that are read, that hold NaN and infinities."""
+    n_new, window, sinks = [100, 64], 60, 5
+    w = window_batch([1000, 333], n_new, 16, kt, vt)
+    cache, tab = device_cache(w)
+    want, want_lse = attend(w, n_new, window, sinks, cache=cache, tab=tab)
+    row = 0
+    k, v = w.k_rows.copy(), w.v_rows.copy()
+    for n, length in zip(n_new, w.seq_lens):
+        x = np.arange(length)
+        dead = ~((x > length - n - window) | (x < sinks))
+        for rows, t in ((k, kt), (v, vt)):
+            part = rows[row: row + length]
+            if t == F16:
+                part[dead] = 0xff
+            else:
+                size = 34 if t == Q8 else 18
+                for b in range(8):
+                    part[dead, :, size * b] = 0
+                    part[dead, :, size * b + 1] = 0x7c | (b & 1) << 1
+        row += length
+    bad = W.Workload(w.name, w.seq_lens, 1, 16, w.n_blocks, kt, vt, w.table, k, v, w.q, w.scale)
+    cache, tab = device_cache(bad)
+    # the last pages' other rows too
+    for i, length in enumerate(w.seq_lens):
+        rest = np.arange(length, -(-int(length) // 16) * 16)
+        nan = lambda t: np.full((len(rest), 4, W.row_bytes(t)), 0xff, np.uint8)  # noqa: E731
+        dev = lambda x: to_dev(np.ascontiguousarray(x, dtype=np.int32))  # noqa: E731
+        if len(rest):
+            cache.append(to_dev(nan(kt)), to_dev(nan(vt)), dev(np.full(len(rest), i)), dev(rest), tab)
+    out, lse = attend(w, n_new, window, sinks, cache=cache, tab=tab)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_prompts_with_bad_entries_and_lengths():
+    n_new = [100, 1, 64]
+    w = window_batch([500, 300, 400], n_new, 16, Q8, Q8)
+    cache, tab = device_cache(w)
+    lens = w.seq_lens.copy()
+    lens[0] -= 1
+    q = to_dev(w.q)
+    for window in (0, 50):
+        ref, ref_lse = attend(w, n_new, window, 0, cache=cache, tab=tab)
+        out, lse = cache.attend_window(q, tab, to_dev(lens), w.seq_lens, np.array(n_new, np.int32), window, 0, w.scale)
+        torch.cuda.synchronize()
+        assert cache.check() == PA_ERR_BOUNDS and cache.check() == PA_OK
+        assert (out[:100] == 0).all() and (lse[:100] == -float("inf")).all()
+        assert torch.equal(out[100:], ref[100:]) and torch.equal(lse[100:], ref_lse[100:])
+    holes = w.table.copy()
+    holes[2, 3] = -7  # 16 rows of zeros
+    out, lse = cache.attend_window(q, to_dev(holes), to_dev(w.seq_lens), w.seq_lens, np.array(n_new, np.int32), 0, 0, w.scale)
+    torch.cuda.synchronize()
+    assert cache.check() == PA_ERR_BOUNDS
+    k, v = w.k_rows.copy(), w.v_rows.copy()
+    k[800 + 48: 800 + 64] = 0
+    v[800 + 48: 800 + 64] = 0
+    zero = W.Workload(w.name, w.seq_lens, 1, 16, w.n_blocks, Q8, Q8, w.table, k, v, w.q, w.scale)
+    ref, ref_lse = attend64(zero, n_new, 0, 0)
+    assert_close(out.cpu().numpy(), ref)
+    assert_lse_close(lse.cpu().numpy(), ref_lse)
+
+
+def test_prompts_repeat_bit_for_bit():
+    """Again, captured and replayed with other queries, on another stream at once."""
+    n_new = [300, 80, 1]
+    w = window_batch([2500, 900, 77], n_new, 16, Q8, Q4)
+    cache, tab = device_cache(w)
+    q, sl, nn = to_dev(w.q).half(), to_dev(w.seq_lens), np.array(n_new, np.int32)
+    call = lambda q, **kw: cache.attend_window(q, tab, sl, w.seq_lens, nn, 1500, 4, w.scale, **kw)  # noqa: E731
+    q2 = q.flip(0).contiguous()
+    want, want2 = call(q)[0], call(q2)[0]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    res = [(i, call(q2 if i % 2 else q, stream=side if i % 2 else None)[0]) for i in range(6)]
+    g = torch.cuda.CUDAGraph()
+    x = q.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        y, _ = call(x)
+    for i, r in res:
+        assert torch.equal(r, want2 if i % 2 else want)
+    for src, ref in ((q, want), (q2, want2), (q, want)):
+        x.copy_(src)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref)
+    assert cache.check() == PA_OK

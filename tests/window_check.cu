@@ -18,15 +18,84 @@ static long long bad = 0;
     }                                                    \
   } while (0)
 
-int main(int argc, char** argv) {
-  const int batches = argc > 1 ? std::atoi(argv[1]) : 300;
+template <class P>
+constexpr bool kPrompt = false;
+template <>
+constexpr bool kPrompt<PromptParams> = true;
+
+static bool sees(const Unit& u, int row, int key, int window, int sinks) {
+  const long long pos = u.pos + (unit_row0(u) + row) / kGqa;
+  return key <= pos && (key > pos - window || key < sinks);
+}
+
+// A tile of the kernel for few tokens: its masks, live keys.
+static void masks(const WindowParams& p, const Unit& u, const Span& s, int key0, int last_pos, int batch) {
+  const int last_lo = last_pos >= p.window ? last_pos - p.window + 1 : 0;
+  const bool inner = sees_all(s, key0, u.pos, last_lo, p.sinks);
+  Tile tl{};
+  tl.open = u.pos;
+  tl.row0 = unit_row0(u);
+  tl.pad[0] = key0;
+  tl.pad[1] = s.shift;
+  const WindowKeys live = live_keys(p, live_of(s, key0, p.sinks), 0);
+  for (int k = 0; k < kKeys; ++k) {
+    const int v = key0 + k, key = v < s.s16 ? v : v + s.shift;
+    const int2 see = rows_that_see(p, tl, k);
+    bool any = false, all = true;
+    for (int r = 0; r < unit_rows(u); ++r) {
+      const bool yes = v < s.end && sees(u, r, key, p.window, p.sinks);
+      CHECK(yes == (r >= see.x && r < see.y));
+      any |= yes;
+      all &= yes;
+    }
+    CHECK(live.has(k) == any || (live.has(k) && v < s.end && key <= last_pos));
+    if (any) CHECK(live.has(k));
+    if (inner) CHECK(all);
+    if (live.has(k)) CHECK(key < u.len);
+  }
+  for (int h = 0; h < 2; ++h) {
+    const WindowKeys half = live_keys(p, live_of(s, key0, p.sinks), kStageKeys * h);
+    bool every = true;
+    for (int k = 0; k < kStageKeys; ++k) {
+      every &= half.has(k);
+      CHECK(half.has(k) == live.has(kStageKeys * h + k));
+    }
+    CHECK(!half.all() || every);
+  }
+}
+
+// A tile of the prompts' kernel: its masks, and where its keys lie among the sequence's.
+static void masks(const PromptParams& p, const PromptUnit& u, const Span& s, int key0, int last_pos, int batch) {
+  const int last_lo = last_pos >= p.window ? last_pos - p.window + 1 : 0;
+  const bool inner = sees_all(s, key0, u.pos, last_lo, p.sinks);
+  const int n = std::min(kKeys, s.end - key0);
+  for (int k = 0; k < kKeys; ++k) {
+    const int v = key0 + k, key = v < s.s16 ? v : v + s.shift;
+    for (int r = 0; r < kPromptRows; r += 1 + r % 5) {
+      const bool yes = row_keys(u, s, r, p.window).has(v, p.sinks);
+      if (r >= unit_rows(u)) {
+        CHECK(!yes);
+        continue;
+      }
+      CHECK(yes == (v < s.end && sees(u, r, key, p.window, p.sinks)));
+      if (inner) CHECK(yes);
+    }
+    if (k >= ((n + 15) & ~15)) continue;  // not copied
+    const int g = group_of(u, s, v), at = 16 * g, s16 = s.s16;
+    CHECK(g >= 0 && g < u.groups);
+    CHECK((at < s16 ? at : at + u.shift0) == (key & ~15));
+  }
+}
+
+template <class P>
+static int check(int batches, bool many) {
   std::mt19937 rng(7);
   auto pick = [&](long long lo, long long hi) { return (int)(lo + (long long)(rng() % (unsigned long long)(hi - lo + 1))); };
-  static WindowParams p;
+  static P p;
   static MergeParams m;
   for (int batch = 0; batch < batches; ++batch) {
     const bool big = batch % 50 == 49;  // more units than one launch takes
-    const int n_seq = big ? pick(300, 700) : pick(1, 12), max_ctas = pick(1, 3) == 1 ? pick(1, 7) : 152;
+    const int n_seq = big ? (many ? pick(70, 150) : pick(300, 700)) : pick(1, 12), max_ctas = pick(1, 3) == 1 ? pick(1, 7) : 152;
     const int win[] = {1, 2, 15, 16, 17, pick(1, 300), pick(1, 3000), kAllKeys}, snk[] = {0, 0, 1, 4, 16, 17, pick(0, 300), kAllKeys};
     p.window = win[pick(0, 7)];
     p.sinks = snk[pick(0, 7)];
@@ -35,23 +104,28 @@ int main(int argc, char** argv) {
     uint32_t most = 0;
     long long tokens = 0;
     for (int i = 0; i < n_seq; ++i) {
-      fresh[i] = pick(0, 3) == 0 ? 0 : pick(0, 2) == 0 && !big ? pick(1, 120) : pick(1, 8);
+      fresh[i] = pick(0, 3) == 0 ? 0 : pick(0, 2) == 0 && !big ? pick(1, 120) : many && pick(0, 5) ? pick(64, 700) : pick(1, 8);
       lens[i] = fresh[i] + (pick(0, 2) == 0 ? pick(0, 5) : pick(0, big ? 300 : 4000));
       most = std::max(most, (uint32_t)fresh[i]);
       tokens += fresh[i];
     }
-    p.slot_rows = m.slot_rows = slot_rows_of(most);
+    for (int32_t& n : fresh) tokens -= Batch::is_many(n) != many ? n : 0;  // the other kernel's
+    const Batch b{lens.data(), fresh.data(), (uint32_t)n_seq, p.window, p.sinks, p.n_kv_heads};
+    p.slot_rows = m.slot_rows = many ? kPromptRows : slot_rows_of(most);
+    uint32_t prompt_seq = 0;
+    int group0 = 0;
     std::map<std::tuple<int, int, int>, int> rows_seen;  // (sequence, head, query row) -> times
     Cursor at{0, 0, 0};
     int launches = 0;
     while (at.seq < (uint32_t)n_seq) {
       const Cursor before = at;
-      const Plan plan = plan_chunk(p, m, lens.data(), fresh.data(), n_seq, max_ctas, &at);
+      const Plan plan = plan_chunk(p, m, b, many, max_ctas, &at);
       CHECK(at.seq > before.seq || at.rt > before.rt);
       if (at.seq == before.seq && at.rt == before.rt) return 1;
-      if (p.n_units == 0) continue;
+      if (p.n_units == 0) break;
       ++launches;
-      CHECK(p.n_units <= kMaxUnits && p.n_ctas >= 1 && p.n_ctas <= max_ctas && plan.cuts < kMaxCtas);
+      if constexpr (kPrompt<P>) place_prompts(p, b, &prompt_seq, &group0);
+      CHECK(p.n_units <= P::kMaxUnits && p.n_ctas >= 1 && p.n_ctas <= max_ctas && plan.cuts < kMaxCtas);
       std::map<std::pair<int, int>, std::pair<int, int>> pieces;  // (unit, head) -> (first CTA, pieces) where cut
       int tile = 0;
       std::set<int> slots;
@@ -63,7 +137,7 @@ int main(int argc, char** argv) {
         CHECK(t.tile == tile && end > tile);
         for (bool fresh_seg = t.j == 0; tile < end; ++tile) {
           CHECK(t.unit < p.n_units && t.head < p.n_kv_heads);
-          const Unit& u = p.unit[t.unit];
+          const auto& u = p.unit[t.unit];
           CHECK(next_j[(size_t)t.unit * p.n_kv_heads + t.head]++ == t.j);
           const Span s = span_of(u, p.window, p.sinks);
           const int key0 = t.j * kKeys, last_pos = u.pos + (unit_row0(u) + unit_rows(u) - 1) / kGqa;
@@ -79,46 +153,8 @@ int main(int argc, char** argv) {
               ++pc.second;
             }
           }
-          // every tile of a few heads, the masks of a few tiles
-          if (t.head == 0 && (big ? pick(0, 30) == 0 : true)) {
-            const int last_lo = last_pos >= p.window ? last_pos - p.window + 1 : 0;
-            const bool inner = sees_all(s, key0, u.pos, last_lo, p.sinks);
-            Tile tl{};
-            tl.open = u.pos;
-            tl.row0 = unit_row0(u);
-            tl.pad[0] = key0;
-            tl.pad[1] = s.shift;
-            const WindowKeys live = live_keys(p, live_of(s, key0, p.sinks), 0);
-            bool all_live = true;
-            for (int k = 0; k < kKeys; ++k) {
-              const int v = key0 + k, key = v < s.s16 ? v : v + s.shift;
-              const int2 see = rows_that_see(p, tl, k);
-              bool any = false, all = true;
-              for (int r = 0; r < unit_rows(u); ++r) {
-                const int pos = u.pos + (unit_row0(u) + r) / kGqa;
-                const bool sees = v < s.end && key <= pos && ((long long)key > (long long)pos - p.window || key < p.sinks);
-                if (v < s.end) CHECK(sees == (r >= see.x && r < see.y));
-                else CHECK(!(r >= see.x && r < see.y));
-                any |= sees;
-                all &= sees;
-              }
-              CHECK(live.has(k) == any || (live.has(k) && v < s.end && key <= last_pos));
-              if (any) CHECK(live.has(k));
-              if (!live.has(k)) all_live = false;
-              if (inner) CHECK(all);
-              if (live.has(k)) CHECK(key < u.len);
-            }
-            for (int h = 0; h < 2; ++h) {
-              const WindowKeys half = live_keys(p, live_of(s, key0, p.sinks), kStageKeys * h);
-              bool every = true;
-              for (int k = 0; k < kStageKeys; ++k) {
-                every &= half.has(k);
-                CHECK(half.has(k) == live.has(kStageKeys * h + k));
-              }
-              CHECK(!half.all() || every);
-            }
-            (void)all_live;
-          }
+          // the masks of a head's tiles
+          if (t.head == 0 && (big ? pick(0, 30) == 0 : true)) masks(p, u, s, key0, last_pos, batch);
           if (t.j == 0) {
             for (int r = 0; r < unit_rows(u); ++r) {
               const int tok = u.token + (unit_row0(u) + r) / kGqa;
@@ -163,6 +199,12 @@ int main(int argc, char** argv) {
     CHECK(rows == tokens * kGqa * p.n_kv_heads);
     if (big) CHECK(launches >= 1);
   }
+  return 0;
+}
+
+int main(int argc, char** argv) {
+  const int batches = argc > 1 ? std::atoi(argv[1]) : 300;
+  if (check<WindowParams>(batches, false) || check<PromptParams>(batches, true)) return 1;
   std::printf("mismatches %lld\n", bad);
   return bad != 0;
 }
