@@ -3,29 +3,38 @@
 // The mathematics is that of pa_window_impl.cuh.  A prompt's tokens share their keys: a key
 // tile meets dozens of row tiles.  So the keys and values that any new token sees are
 // first turned into binary16 once, in the workspace (pa_prompt_prepare_kernel; a chunk's stay
-// in L2), in the order in which the MMAs take them:
-//   K   per (sequence, head) four planes of 64 dims, each [8 keys][8 dims'][8 keys' rows of 16 bytes]: a
-//       run of row groups of a plane is one contiguous piece, an MMA's B operand;
-//   V   transposed, [8 keys][8 dims][8 rows of 16 bytes = 8 keys]: likewise a run of groups is.
-// and the attention is a dense one over tiles of 128 query rows (a unit) x 128 keys:
-//   S = Q K^T   tcgen05.mma M = 128 rows, N = keys of the tile, K = 256 dims; Q and K in shared memory;
-//   O += P V    M = 128 rows, N = 256 dims, K = keys; P in tensor memory (in its S's place), V in shared memory.
+// in L2), in the order in which the MMAs take them, and the attention is a dense one over tiles
+// of 256 query rows (a unit) x 128 keys, by pairs of CTAs (clusters of two, cta_group::2):
+//   S = Q K^T   tcgen05.mma M = 256 rows, N = 128 keys, K = 256 dims; Q and K in shared memory;
+//   O += P V    M = 256 rows, N = 256 dims, K = keys; P in tensor memory (in its S's place), V in shared memory.
+// A CTA holds 128 of the rows (Q, S, P and O), 64 of the tile's keys of K and 128 of the dims
+// of V; the tensor cores read each other's half.
+//
+// Why pairs.  An SM takes in 30 bytes a cycle from L2 (all of them 8.9 TB/s, measured).
+// A CTA of its own reads 128 KB for 128 rows x 128 keys, 4300 cycles for 2048 of MMA
+// (4096 tokens, no window: 312 us); one of a pair 64 KB.  (Bulk copies to both CTAs
+// at once, multicast, run at 12 bytes a cycle.)
+//
+// The workspace's layout, per (sequence, head); a core matrix is 8 rows x 16 bytes:
+//   K   two planes of 128 dims, each [8 keys][16 slots of 8 dims] core matrices (rows = keys);
+//   V   two planes of 128 dims, each [8 keys][16 slots of 8 dims] core matrices, transposed (rows = dims);
+// a run of row groups of a plane is one contiguous piece, and an MMA's B operand.
+//
 // Tensor memory: O in columns 0-255, two buffers of S in 256-383 and 384-511; P as pairs
 // of binary16 in the first 64 columns of its S.
 //
-// Shared memory: Q (64 KB) and a ring of nine stages of 16 KB: a quarter of a K tile (64 dims of
-// its keys) or of a V tile (32 keys), each worth 256 cycles of MMA; so about 2000 cycles are
-// on their way while one is used.
+// Shared memory: Q twice (64 KB each, this piece's and the next one's) and a ring of five stages
+// of 16 KB: of K 64 keys x 128 dims, of V 64 keys x 128 dims, each worth 512 cycles of MMA.
 //
 // Warps, hand-offs on mbarriers, every wait bounded:
 //   0-7    softmax: (half of the keys, lane quarter), thread = row;
 //   8-11   query rows into Q, and a finished piece's O to its place;
-//   12     MMA issue; 13 copies.
+//   12     MMA issue (the pair's first CTA; the second's tells it of the second's copies); 13 copies.
 // S of tile j + 1 is multiplied while the softmax of tile j runs, and that of j + 1 while PV of
-// j and S of j + 2 are.  At a piece's end PV comes before the next piece's S, whose
-// query rows are on their way meanwhile.
+// j and S of j + 2 are.
 //
-// Ranges, cuts and slots are those of pa_window_impl.cuh, with units of 128 rows.
+// Ranges, cuts and slots are those of pa_window_impl.cuh, with units of 256 rows and ranges of
+// pairs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -84,8 +93,9 @@ __device__ __forceinline__ void prepare_rows(const PrepareParams& p, const Promp
     if (is_v && (key >= s.len || (key >= p.sinks && key < s.lo))) x[r] = make_uint4(0u, 0u, 0u, 0u);
   }
   const long long reg = (long long)s.group0 * p.n_kv_heads + (long long)head * s.groups;
+  const long long plane = (((long long)(lane >> 4) * s.groups + group) * 2 + half) * 2048 + (lane & 15) * 128;  // of the lane's dims
   if (is_v) {
-    uint8_t* to = p.v + (reg + group) * kGroupBytes + half * (kGroupBytes / 2) + 128 * lane;
+    uint8_t* to = p.v + reg * kGroupBytes + plane;
 #pragma unroll
     for (int d = 0; d < 4; ++d) {  // dims 2 d and 2 d + 1 of the lane's eight
       uint32_t w[8];
@@ -96,8 +106,7 @@ __device__ __forceinline__ void prepare_rows(const PrepareParams& p, const Promp
       o[1] = make_uint4(prmt(w[0], w[1], 0x7632), prmt(w[2], w[3], 0x7632), prmt(w[4], w[5], 0x7632), prmt(w[6], w[7], 0x7632));
     }
   } else {
-    // plane lane / 8, [8 keys][8 slots][8 rows]
-    uint8_t* to = p.k + reg * kGroupBytes + (((long long)(lane >> 3) * s.groups + group) * 2 + half) * 1024 + (lane & 7) * 128;
+    uint8_t* to = p.k + reg * kGroupBytes + plane;
 #pragma unroll
     for (int r = 0; r < 8; ++r) reinterpret_cast<uint4*>(to)[r] = x[r];
     if (p.wide && lane == 0) p.wide[(reg + group) * 2 + half] = (uint8_t)wide_rows;
@@ -137,21 +146,85 @@ __global__ void __launch_bounds__(32 * kPrepareWarps) pa_prompt_prepare_kernel(c
 
 // ------------------------------------------------------------------ the attention
 
-constexpr int kStageBytes = 16384, kNStages = 9;
+constexpr int kStageBytes = 16384, kNStages = 5;
+constexpr int kCtaRows = kPromptRows / 2, kPlaneGroup = kGroupBytes / 2;  // rows of a CTA; bytes of a group in a plane
 constexpr int kPSmWarps = 8, kAuxWarp0 = 8, kMmaWarp = 12, kCopyWarp = 13, kPThreads = 14 * 32;
 constexpr uint32_t kPOCol = 0, kPSCol = 256;
 
 struct PSmem {
-  static constexpr int kQ = 0, kRing = kPromptRows * kD * 2, kRed = kRing + kNStages * kStageBytes;
-  static constexpr int kSum = kRed + 2 * kPromptRows * 4;        // [piece & 1][half of the keys][row]
-  static constexpr int kRef = kSum + 4 * kPromptRows * 4;        // [piece & 1][row]
-  static constexpr int kBar = kRef + 2 * kPromptRows * 4;
-  static constexpr int kNBar = 2 * kNStages + 2 + 2 + 2 + 2 + 1 + 2 + 2;
-  static constexpr int kMisc = kBar + 8 * kNBar;                 // abort, tmem base, the softmax's leave [2]
+  static constexpr int kQBytes = kCtaRows * kD * 2;
+  static constexpr int kQ = 0, kRing = 2 * kQBytes, kRed = kRing + kNStages * kStageBytes;
+  static constexpr int kSum = kRed + 2 * kCtaRows * 4;        // [piece & 1][half of the keys][row]
+  static constexpr int kRef = kSum + 4 * kCtaRows * 4;        // [piece & 1][row]
+  static constexpr int kBar = kRef + 2 * kCtaRows * 4;
+  static constexpr int kNBar = 2 * kNStages + 2 + 2 + 2 + 2 + 2 + 1 + 2 + 1;
+  static constexpr int kMisc = kBar + 8 * kNBar + 8 * (kNBar & 1);  // abort, tmem base, the softmax's leave [2]
   static constexpr int kTotal = kMisc + 16;
   static constexpr int kLaunch = kTotal + 1024;
   static_assert(kLaunch <= 232448, "shared memory");
 };
+
+// ------------------------------------------------------------------ pairs of CTAs
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// All threads of both CTAs.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// An arrival at the first CTA's barrier of this address.
+__device__ __forceinline__ void arrive_first(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\tmbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// warp_wait for a barrier at which the other CTA's threads arrive.
+__device__ __forceinline__ bool warp_wait_pair(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort) {
+  if (!warp_wait(bar, parity, err, abort)) return false;
+  return __all_sync(0xffffffffu, try_wait_cluster(bar, parity));  // the phase is over: this orders what came before it
+}
+
+// One arrival at both CTAs' barriers of this address when every MMA issued so far has
+// completed.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_pair_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 
 // A piece of the CTA's range: tiles j0 .. j1 - 1 of a (unit, head).
 struct Piece {
@@ -189,6 +262,46 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const uint8_t* src, uint
                : "memory");
 }
 
+// Eight query rows r8 .. r8 + 7 of a CTA's by one warp as binary16 into Q, rows from `rows` on
+// as zeros (stage_q_begin's layout and range).  Lane: row r8 + lane % 8, slots lane / 8 + 4 i.
+__device__ __forceinline__ void load_queries(const PromptParams& p, int token, int row0, int rows, int head, uint32_t dst, int r8, int lane) {
+  const int row = r8 + (lane & 7), rg = row0 + row;
+  const uint32_t to = dst + canon(row, lane >> 3, kD / 8);
+  const long long at = (token + rg / kGqa) * p.q_stride + (head * kGqa + rg % kGqa) * kD + 8 * (lane >> 3);
+  uint4 v[8];
+  if (row >= rows) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  } else if (p.q_type == PA_DT_F32) {
+    const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 x = __ldg(src + 8 * i), y = __ldg(src + 8 * i + 1);
+      v[i] = make_uint4(pack_half2(x.x, x.y), pack_half2(x.z, x.w), pack_half2(y.x, y.y), pack_half2(y.z, y.w));
+    }
+  } else {
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + 2 * at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __ldg(src + 4 * i);
+    if (p.q_type == PA_DT_BF16) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) u[k] = pack_half2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
+        v[i] = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    }
+  }
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    top = larger2(larger2(larger2(top, v[i].x), v[i].y), larger2(v[i].z, v[i].w));
+    sts128(to + 512 * i, v[i]);
+  }
+  if (p.q_type != PA_DT_F16) q_range(top, to);
+}
+
 __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_constant__ PromptParams p) {
   using SM = PSmem;
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -196,65 +309,71 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
   uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-  // Hand-offs (tile j, piece i of the CTA):
-  //   full / empty [stage]        copies <-> MMA (commit)
-  //   q_full / q_empty            query rows of piece i in Q / its last S done
+  const uint32_t rank = cluster_rank();
+  const int pair = (int)(blockIdx.x >> 1), cta_row0 = kCtaRows * (int)rank;  // this CTA's rows of a unit
+  // Hand-offs (tile j, piece i of the pair's range).  What the MMAs complete is told both
+  // CTAs (commit_pair), what they wait for is told the first one:
+  //   full [stage]                copies -> MMA: the first CTA's own, and the second's word of its own
+  //   empty [stage]               MMA -> copies
+  //   q_full / q_empty [i & 1]    query rows of piece i in Q / its last S done
   //   s_full [j & 1]              S(j) in tensor memory
   //   p_full [j & 1]              P(j) in its place
   //   pv_done [j & 1]             O holds tile j
-  //   l_full [i & 1]              piece i's sums and references in shared memory
   //   o_free                      piece i's O has been read
+  // and within a CTA:
+  //   l_full [i & 1]              piece i's sums and references in shared memory
   // A role whose wait expires stops: it arrives nowhere any more.
-  const uint32_t full = base + SM::kBar, empty = full + 8 * kNStages, q_full = empty + 8 * kNStages, q_empty = q_full + 8,
-                 s_full = q_empty + 8, p_full = s_full + 16, pv_done = p_full + 16, o_free = pv_done + 16, l_full = o_free + 8,
-                 drain = l_full + 16, sink = drain + 8;
+  const uint32_t full = base + SM::kBar, empty = full + 8 * kNStages, q_full = empty + 8 * kNStages, q_empty = q_full + 16,
+                 s_full = q_empty + 16, p_full = s_full + 16, pv_done = p_full + 16, o_free = pv_done + 16, l_full = o_free + 8,
+                 drain = l_full + 16;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + SM::kMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc + 4);
   volatile int* leave = reinterpret_cast<volatile int*>(smem + SM::kMisc + 8);  // of even, odd tiles
   if (tid == 0) {
     *abort = leave[0] = leave[1] = 0;
     for (int i = 0; i < kNStages; ++i) {
-      mbar_init(full + 8 * i, 1);
+      mbar_init(full + 8 * i, rank == 0 ? 2 : 1);
       mbar_init(empty + 8 * i, 1);
     }
-    mbar_init(q_full, 4);
-    mbar_init(q_empty, 1);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 8);
+      mbar_init(q_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, kPSmWarps);
+      mbar_init(p_full + 8 * i, 2 * kPSmWarps);
       mbar_init(pv_done + 8 * i, 1);
       mbar_init(l_full + 8 * i, kPSmWarps);
     }
-    mbar_init(o_free, 4);
+    mbar_init(o_free, 8);
     mbar_init(drain, 1);
-    mbar_init(sink, 1);
     fence_mbar_init();
   }
   Walk walk;
   {
-    const int x0 = (int)((long long)blockIdx.x * p.total_len / p.n_ctas), x1 = (int)((long long)(blockIdx.x + 1) * p.total_len / p.n_ctas);
+    const int x0 = (int)((long long)pair * p.total_len / p.n_ctas), x1 = (int)((long long)(pair + 1) * p.total_len / p.n_ctas);
     walk.pos = locate(p, x0);
-    walk.left = (x1 < p.total_len ? locate(p, x1).tile : p.total_tiles) - walk.pos.tile;
+    walk.left = (x1 < p.total_len ? locate(p, x1).tile : p.total_tiles) - walk.pos.tile;  // at least 1
   }
-  const int n = walk.left;  // at least 1
   if (w == 0) {
-    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-    tmem_relinquish();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // the other CTA's barriers are there
   tc_fence_after();
   // nothing that another kernel wrote is read before this
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0) asm volatile("griddepcontrol.launch_dependents;");
-  const bool whole = *tmem_slot == 0;  // all of tensor memory is this CTA's, so its columns start at 0
+  // All of tensor memory is the pair's, so its columns start at 0 in both.
+  const bool whole = *tmem_slot == 0;
   if (!whole && tid == 0) record_error(p.err, PA_ERR_CUDA);
   int issued = 0;
   Piece x;
 
   if (!whole) {
   } else if (w == kCopyWarp) {
-    // ---- copies: of a piece K(0), then K(j + 1) before V(j); a stage each 64 dims or 32 keys
+    // ---- copies: K(0), then K(j + 1) before V(j); a stage each 128 dims of K (64 keys: the CTA's) or
+    // 64 keys of V (128 dims: the CTA's)
     bool live = true;
     auto stage = [&](uint32_t bytes) -> int {  // the next stage, once it is free; -1: the wait expired
       const int s = issued % kNStages, use = issued / kNStages;
@@ -265,195 +384,230 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       ++issued;
       return s;
     };
-    while (live && walk.next(p, x)) {
-      const PromptUnit& u = p.unit[x.unit];
-      const Span s = span_of(u, p.window, p.sinks);
-      const long long reg = (long long)u.group0 * p.n_kv_heads + (long long)x.head * u.groups;
-      // places v .. end - 1: one run of the sequence's groups, or two (sinks, window)
-      auto copy = [&](const uint8_t* from, uint32_t to, int v, int end, int unit_bytes, uint32_t bar) {
-        int a = v, stop = s.shift != u.shift0 && v < s.s16 ? min(end, s.s16) : end;
-        while (a < end) {
-          if (lane == 0)
-            bulk_copy(to + ((a - v) >> 4) * unit_bytes, from + (long long)group_of(u, s, a) * unit_bytes, ((stop - a) >> 4) * unit_bytes, bar);
-          a = stop;
-          stop = end;
-        }
-        __syncwarp();
-      };
-      auto keys = [&](int j) {
-        const int v = j * kKeys, n16 = whole16(tile_keys(s, j));
-        for (int q = 0; q < 4 && live; ++q) {
-          const int st = stage((uint32_t)n16 * 128);
-          if (st >= 0) copy(p.k + reg * kGroupBytes + (long long)q * u.groups * 2048, base + SM::kRing + st * kStageBytes, v, v + n16, 2048, full + 8 * st);
-        }
-      };
-      auto vals = [&](int j) {
-        const int v = j * kKeys, n16 = whole16(tile_keys(s, j));
-        for (int q = 0; q < n16 && live; q += 32) {
-          const int m = min(32, n16 - q), st = stage((uint32_t)m * 512);
-          if (st >= 0) copy(p.v + reg * kGroupBytes, base + SM::kRing + st * kStageBytes, v + q, v + q + m, kGroupBytes, full + 8 * st);
-        }
-      };
-      keys(x.j0);
-      for (int j = x.j0; j < x.j1 && live; ++j) {
-        if (j + 1 < x.j1) keys(j + 1);
-        vals(j);
+    // places v .. end - 1 of a plane: one run of the sequence's groups, or two (sinks, window)
+    auto copy = [&](const PromptUnit& u, const Span& s, const uint8_t* plane, int v, int end, int st) {
+      int a = v, stop = s.shift != u.shift0 && v < s.s16 ? min(end, s.s16) : end;
+      while (a < end) {
+        if (lane == 0)
+          bulk_copy(base + SM::kRing + st * kStageBytes + ((a - v) >> 4) * kPlaneGroup, plane + (long long)group_of(u, s, a) * kPlaneGroup,
+                    ((stop - a) >> 4) * kPlaneGroup, full + 8 * st);
+        a = stop;
+        stop = end;
       }
+      __syncwarp();
+    };
+    auto keys = [&](const Piece& x, const Span& s, int j) {
+      const PromptUnit& u = p.unit[x.unit];
+      const uint8_t* k = p.k + ((long long)u.group0 * p.n_kv_heads + (long long)x.head * u.groups) * kGroupBytes;
+      const int v = j * kKeys + 64 * (int)rank, end = max(v, min(v + 64, j * kKeys + whole16(tile_keys(s, j))));
+      for (int h = 0; h < 2 && live; ++h) {
+        const int st = stage((uint32_t)(end - v) * 256);
+        if (st >= 0) copy(u, s, k + (long long)h * u.groups * kPlaneGroup, v, end, st);
+      }
+    };
+    auto vals = [&](const Piece& x, const Span& s, int j) {
+      const PromptUnit& u = p.unit[x.unit];
+      const uint8_t* k = p.v + ((long long)u.group0 * p.n_kv_heads + (long long)x.head * u.groups) * kGroupBytes + (long long)rank * u.groups * kPlaneGroup;
+      const int v = j * kKeys, n16 = whole16(tile_keys(s, j));
+      for (int q = 0; q < n16 && live; q += 64) {
+        const int m = min(64, n16 - q), st = stage((uint32_t)m * 256);
+        if (st >= 0) copy(u, s, k, v + q, v + q + m, st);
+      }
+    };
+    bool more = walk.next(p, x);
+    Span s = span_of(p.unit[x.unit], p.window, p.sinks);
+    keys(x, s, x.j0);
+    while (more && live) {
+      for (int j = x.j0; j + 1 < x.j1 && live; ++j) {
+        keys(x, s, j + 1);
+        vals(x, s, j);
+      }
+      const Piece before = x;
+      const Span was = s;
+      more = walk.next(p, x);
+      if (more && live) {
+        s = span_of(p.unit[x.unit], p.window, p.sinks);
+        keys(x, s, x.j0);
+      }
+      vals(before, was, before.j1 - 1);
+    }
+  } else if (w == kMmaWarp && rank != 0) {
+    // ---- the second CTA's copies, told the first one
+    int used = 0;
+    bool live = true;
+    auto pass = [&](int n) {
+      for (int i = 0; i < n && live; ++i, ++used) {
+        const int st = used % kNStages;
+        live = warp_wait(full + 8 * st, (used / kNStages) & 1, p.err, abort);
+        if (live && lane == 0) arrive_first(full + 8 * st);
+        __syncwarp();
+      }
+    };
+    while (live && walk.next(p, x)) {
+      const Span s = span_of(p.unit[x.unit], p.window, p.sinks);
+      for (int t = x.j0; t < x.j1 && live; ++t) pass(2 + (whole16(tile_keys(s, t)) > 64 ? 2 : 1));
     }
   } else if (w == kMmaWarp) {
     // ---- MMA issue by the whole warp, an elected lane issuing.  After an expired wait no
-    // further MMA is issued; what was ends before the CTA does.
+    // further MMA is issued; what was ends before the pair does.
     bool dead = false;
     int used = 0;
-    uint32_t piece = 0;
+    uint32_t scored = 0, piece = 0;  // pieces whose S, whose PV has begun
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (!dead) dead = !warp_wait(bar, parity, p.err, abort);
+      if (!dead) dead = !warp_wait_pair(bar, parity, p.err, abort);
       return !dead;
     };
-    const uint64_t qdesc = smem_desc(base + SM::kQ, 128, 4096);
-    const uint32_t pv_idesc = idesc_f16_f32(128, kD);
-    int j = 0;  // the CTA's tile
-    while (!dead && walk.next(p, x)) {
-      const Span s = span_of(p.unit[x.unit], p.window, p.sinks);
-      auto score = [&](int t, int jj) {  // S of the segment's tile t, the CTA's jj
-        const uint32_t idesc = idesc_f16_f32(128, 0) | (uint32_t)(whole16(tile_keys(s, t)) >> 3) << 17, d = kPSCol + 128 * (jj & 1);
-        for (int q = 0; q < 4; ++q) {
-          const int st = used % kNStages;
-          if (!wait(full + 8 * st, (used / kNStages) & 1)) return;
-          tc_fence_after();
-          const uint64_t kdesc = smem_desc(base + SM::kRing + st * kStageBytes, 128, 1024);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tc_mma_f16_warp(d, qdesc + 64 * q + 16 * i, kdesc + 16 * i, idesc, q | i);
-          tc_commit_warp(empty + 8 * st);
-          ++used;
-        }
-        tc_commit_warp(s_full + 8 * (jj & 1));
-        if (t + 1 == x.j1) tc_commit_warp(q_empty);
-      };
-      if (!wait(q_full, piece & 1)) break;
+    auto next_stage = [&]() -> uint32_t {  // its barriers' place, 0 .. kNStages - 1; waits for it
+      const int st = used % kNStages;
+      wait(full + 8 * st, (used / kNStages) & 1);
       tc_fence_after();
-      score(x.j0, j);
-      for (int t = x.j0; t < x.j1 && !dead; ++t, ++j) {
-        if (t + 1 < x.j1) score(t + 1, j + 1);
+      ++used;
+      return (uint32_t)st;
+    };
+    const uint32_t s_idesc = idesc_f16_f32(256, kKeys), pv_idesc = idesc_f16_f32(256, kD);
+    // S of tile t of a piece, the range's j
+    auto score = [&](const Piece& x, int t, int j) {
+      if (t == x.j0) {
+        if (!wait(q_full + 8 * (scored & 1), (scored >> 1) & 1)) return;
+        ++scored;
+      }
+      const uint64_t qdesc = smem_desc(base + SM::kQ + ((scored - 1) & 1) * SM::kQBytes, 128, 4096);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t st = next_stage();
+        if (dead) return;
+        const uint64_t kdesc = smem_desc(base + SM::kRing + st * kStageBytes, 128, 2048);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mma_pair(kPSCol + 128 * (j & 1), qdesc + 128 * h + 16 * i, kdesc + 16 * i, s_idesc, h | i);
+        commit_pair(empty + 8 * st);
+      }
+      commit_pair(s_full + 8 * (j & 1));
+      if (t + 1 == x.j1) commit_pair(q_empty + 8 * ((scored - 1) & 1));
+    };
+    int j = 0;  // the range's tile
+    bool more = walk.next(p, x);
+    score(x, x.j0, 0);
+    while (more && !dead) {
+      const Piece now = x;
+      const Span s = span_of(p.unit[now.unit], p.window, p.sinks);
+      for (int t = now.j0; t < now.j1 && !dead; ++t, ++j) {
+        if (t + 1 < now.j1) {
+          score(now, t + 1, j + 1);
+        } else {
+          more = walk.next(p, x);
+          if (more) score(x, x.j0, j + 1);
+        }
         if (!wait(p_full + 8 * (j & 1), (j >> 1) & 1)) break;
-        if (t == x.j0 && piece > 0 && !wait(o_free, (piece - 1) & 1)) break;
+        if (t == now.j0 && piece > 0 && !wait(o_free, (piece - 1) & 1)) break;
         tc_fence_after();
         const int n16 = whole16(tile_keys(s, t));
-        for (int q = 0; q < n16; q += 32) {
-          const int st = used % kNStages;
-          if (!wait(full + 8 * st, (used / kNStages) & 1)) break;
-          tc_fence_after();
-          const uint64_t vdesc = smem_desc(base + SM::kRing + st * kStageBytes, kGroupBytes / 2, 128);
+        for (int q = 0; q < n16 && !dead; q += 64) {
+          const uint32_t st = next_stage();
+          if (dead) break;
+          const uint64_t vdesc = smem_desc(base + SM::kRing + st * kStageBytes, 2048, 128);
           const uint32_t a = kPSCol + 128 * (j & 1) + q / 2;
-          tc_mma_f16_tmem_a_warp(kPOCol, a, vdesc, pv_idesc, (t - x.j0) | q);
-          if (q + 16 < n16) tc_mma_f16_tmem_a_warp(kPOCol, a + 8, vdesc + (kGroupBytes >> 4), pv_idesc, 1);
-          tc_commit_warp(empty + 8 * st);
-          ++used;
+          for (int i = 0; i < 4 && q + 16 * i < n16; ++i)
+            mma_pair_tmem_a(kPOCol, a + 8 * i, vdesc + (uint64_t)(i * (kPlaneGroup >> 4)), pv_idesc, (t - now.j0) | q | i);
+          commit_pair(empty + 8 * st);
         }
         if (dead) break;
-        tc_commit_warp(pv_done + 8 * (j & 1));
+        commit_pair(pv_done + 8 * (j & 1));
       }
       ++piece;
     }
-    // what was issued, and every commit, ends before the CTA's memory is given back
-    tc_commit_warp(drain);
+    // what was issued, and every commit, ends before the pair's memory is given back
+    commit_pair(drain);
     mbar_wait(drain, 0, p.err, abort, /*honour_abort=*/false);
     __syncwarp();
   } else if (w >= kAuxWarp0) {
-    // ---- query rows of a piece into Q, and the O of the piece before to its place
+    // ---- query rows of a piece into Q, two pieces ahead of its results; a finished piece's O to its place
     const int quarter = w & 3;
     bool live = true;
-    uint32_t piece = 0;
-    int tiles = 0;  // of the pieces so far
-    Piece before{};
+    uint32_t loads = 0;  // pieces whose rows are in Q
+    Walk ahead = walk;
+    auto load = [&]() {  // the next piece's rows, if there is one
+      Piece y;
+      if (!live || !ahead.next(p, y)) return;
+      if (loads > 1 && !(live = warp_wait(q_empty + 8 * (loads & 1), ((loads >> 1) - 1) & 1, p.err, abort))) return;
+      const PromptUnit& u = p.unit[y.unit];
+      const int rows = unit_rows(u) - cta_row0;  // of this CTA
+#pragma unroll 1
+      for (int r8 = 8 * quarter; r8 < kCtaRows; r8 += 32)
+        load_queries(p, u.token, unit_row0(u) + cta_row0, rows, y.head, base + SM::kQ + (loads & 1) * SM::kQBytes, r8, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_first(q_full + 8 * (loads & 1));
+      __syncwarp();
+      ++loads;
+    };
+    load();
+    load();
     const float* sums = reinterpret_cast<const float*>(smem + SM::kSum);
     const float* refs = reinterpret_cast<const float*>(smem + SM::kRef);
-    for (;;) {
-      const bool more = walk.next(p, x);
-      if (more) {
-        const PromptUnit& u = p.unit[x.unit];
-        if (piece > 0 && !(live = live && warp_wait(q_empty, (piece - 1) & 1, p.err, abort))) break;
-        Tile t{};
-        t.info = (uint32_t)unit_rows(u);
-        t.row0 = unit_row0(u);
-        t.token = u.token;
-        t.head = x.head;
-#pragma unroll 1
-        for (int r8 = 8 * quarter; r8 < kPromptRows; r8 += 32) stage_q_begin<PA_F16>(p, t, base + SM::kQ, r8, lane);
-#pragma unroll 1
-        for (int r8 = 8 * quarter; r8 < kPromptRows; r8 += 32) stage_q_end<PA_F16>(p, base + SM::kQ, r8, lane);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-        __syncwarp();
-      }
-      if (piece > 0) {
-        const uint32_t i = piece - 1, j = (uint32_t)tiles - 1;  // the piece, its last tile
-        if (!(live = live && warp_wait(l_full + 8 * (i & 1), (i >> 1) & 1, p.err, abort) &&
-                     warp_wait(pv_done + 8 * (j & 1), (j >> 1) & 1, p.err, abort)))
-          break;
-        tc_fence_after();
-        const PromptUnit& u = p.unit[before.unit];
-        const int row = 32 * quarter + lane, rows = unit_rows(u), rg = unit_row0(u) + row, tok = rg / kGqa;
-        const float l = sums[(i & 1) * 256 + row] + sums[(i & 1) * 256 + 128 + row], m = refs[(i & 1) * 128 + row];
-        const uint32_t from = kPOCol + ((uint32_t)(32 * quarter) << 16);
-        const bool mine = row < rows;
-        if (before.first && before.last) {  // the whole segment: the result
-          const bool other = __ldg(p.lens + u.seq) != u.len;
-          if (other && row == 0) record_error(p.err, PA_ERR_BOUNDS);
-          const float sum = other ? 0.f : l, inv = sum != 0.f ? 1.f / sum : 0.f;
-          const int h = before.head * kGqa + rg - tok * kGqa;
-          if (mine && p.lse) p.lse[(long long)(u.token + tok) * p.n_q_heads + h] = sum != 0.f ? (m + log2f(sum)) * pa_split::kLn2 : -INFINITY;
-          const int bytes = p.out_type == PA_DT_F32 ? 4 : 2;
-          uint8_t* to = p.out + ((u.token + tok) * p.out_stride + h * kD) * bytes;
-#pragma unroll 1
-          for (int c = 0; c < kD; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(from + c, o);
-            tmem_ld_wait();
-            loaded(o);
-            float y[2][8];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) y[k >> 3][k & 7] = inv != 0.f ? __uint_as_float(o[k]) * inv : 0.f;
-            if (mine) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                uint8_t* d = to + (c + 8 * k) * bytes;
-                if (p.out_type == PA_DT_F32) store8<float>(d, y[k]);
-                else if (p.out_type == PA_DT_F16) store8<__half>(d, y[k]);
-                else store8<__nv_bfloat16>(d, y[k]);
-              }
-            }
-            __syncwarp();  // the next load is the whole warp's
-          }
-        } else {
-          const long long slot = slot_of(before.first, before.last, (int)blockIdx.x, p.slot_rows) + row;
-          if (mine) p.part_ml[slot] = make_float2(m, l);
-          float4* to = reinterpret_cast<float4*>(p.part_o + slot * kD);
-#pragma unroll 1
-          for (int c = 0; c < kD; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(from + c, o);
-            tmem_ld_wait();
-            loaded(o);
-            if (mine) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                to[c / 4 + k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
-                                            __uint_as_float(o[4 * k + 3]));
-            }
-            __syncwarp();
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o_free);
-        __syncwarp();
-      }
-      if (!more) break;
-      before = x;
+    int tiles = 0;  // of the pieces so far
+    for (uint32_t i = 0; live && walk.next(p, x); ++i) {
       tiles += x.j1 - x.j0;
-      ++piece;
+      const uint32_t j = (uint32_t)tiles - 1;  // the piece's last tile
+      if (!(live = warp_wait(l_full + 8 * (i & 1), (i >> 1) & 1, p.err, abort) &&
+                   warp_wait(pv_done + 8 * (j & 1), (j >> 1) & 1, p.err, abort)))
+        break;
+      tc_fence_after();
+      const PromptUnit& u = p.unit[x.unit];
+      const int row = 32 * quarter + lane, rg = unit_row0(u) + cta_row0 + row, tok = rg / kGqa;
+      const float l = sums[(i & 1) * 256 + row] + sums[(i & 1) * 256 + 128 + row], m = refs[(i & 1) * 128 + row];
+      const uint32_t from = kPOCol + ((uint32_t)(32 * quarter) << 16);
+      const bool mine = cta_row0 + row < unit_rows(u);
+      if (x.first && x.last) {  // the whole segment: the result
+        const bool other = __ldg(p.lens + u.seq) != u.len;
+        if (other && row == 0) record_error(p.err, PA_ERR_BOUNDS);
+        const float sum = other ? 0.f : l, inv = sum != 0.f ? 1.f / sum : 0.f;
+        const int h = x.head * kGqa + rg - tok * kGqa;
+        if (mine && p.lse) p.lse[(long long)(u.token + tok) * p.n_q_heads + h] = sum != 0.f ? (m + log2f(sum)) * pa_split::kLn2 : -INFINITY;
+        const int bytes = p.out_type == PA_DT_F32 ? 4 : 2;
+        uint8_t* to = p.out + ((u.token + tok) * p.out_stride + h * kD) * bytes;
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(from + c, o);
+          tmem_ld_wait();
+          loaded(o);
+          float y[2][8];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) y[k >> 3][k & 7] = inv != 0.f ? __uint_as_float(o[k]) * inv : 0.f;
+          if (mine) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint8_t* d = to + (c + 8 * k) * bytes;
+              if (p.out_type == PA_DT_F32) store8<float>(d, y[k]);
+              else if (p.out_type == PA_DT_F16) store8<__half>(d, y[k]);
+              else store8<__nv_bfloat16>(d, y[k]);
+            }
+          }
+          __syncwarp();  // the next load is the whole warp's
+        }
+      } else {
+        const long long slot = slot_of(x.first, x.last, pair, p.slot_rows) + cta_row0 + row;
+        if (mine) p.part_ml[slot] = make_float2(m, l);
+        float4* to = reinterpret_cast<float4*>(p.part_o + slot * kD);
+#pragma unroll 1
+        for (int c = 0; c < kD; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(from + c, o);
+          tmem_ld_wait();
+          loaded(o);
+          if (mine) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              to[c / 4 + k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
+                                          __uint_as_float(o[4 * k + 3]));
+          }
+          __syncwarp();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_first(o_free);
+      __syncwarp();
+      load();
     }
   } else {
     // ---- softmax: keys 64 half .. + 63 of a tile, row 32 quarter + lane
@@ -474,7 +628,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       const Span s = span_of(u, p.window, p.sinks);
       const int last_pos = u.pos + (unit_row0(u) + unit_rows(u) - 1) / kGqa;
       const int last_lo = last_pos >= p.window ? last_pos - p.window + 1 : 0;
-      const RowKeys mine = row_keys(u, s, row, p.window);
+      const RowKeys mine = row_keys(u, s, cta_row0 + row, p.window);
       const long long reg = (long long)u.group0 * p.n_kv_heads + (long long)x.head * u.groups;
       float ref = 0.f;
       uint64_t l2 = 0;  // sums of weights over this thread's keys, in two
@@ -526,10 +680,10 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
           break;
         }
         if (raise) {
-          red[half * kPromptRows + row] = top;
+          red[half * kCtaRows + row] = top;
           __syncwarp();
           named_bar_sync(1, 32 * kPSmWarps);
-          const float m = fmaxf(red[row], red[kPromptRows + row]);
+          const float m = fmaxf(red[row], red[kCtaRows + row]);
           // a row that sees no key yet keeps a reference of 0; it will see none later in the piece either
           const float d = first_tile ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);
           ref += d;
@@ -573,7 +727,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (live && lane == 0) mbar_arrive(p_full + 8 * (j & 1));
+        if (live && lane == 0) arrive_first(p_full + 8 * (j & 1));
         __syncwarp();
       }
       if (gone) break;
@@ -586,7 +740,6 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       ++piece;
     }
   }
-  (void)n;
   tc_fence_before();
   __syncthreads();
   // after an expired wait, copies that nobody waited for must still land
@@ -594,21 +747,21 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
     for (int i = max(0, issued - kNStages); i < issued; ++i)
       mbar_wait(full + 8 * (i % kNStages), (uint32_t)((i / kNStages) & 1), p.err, abort, false, kWaitTimeoutNs / 8);
   }
+  __syncwarp();
+  cluster_sync();  // no MMA, arrival or copy is on its way to either CTA any more
   if (w == 0) {
     tc_fence_after();
-    tmem_dealloc(*tmem_slot, kTmemCols);
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "r"(kTmemCols) : "memory");
   }
 }
 
 }  // namespace
 
-__device__ __forceinline__ long long query_at(const PromptParams& p, int t, int h) { return t * p.q_stride + h * kD; }
-
 namespace {
 
 template <class P>
-pa_status launch_one(void (*kernel)(P), const P& p, int grid, int threads, int smem, cudaStream_t cs) {
-  cudaLaunchAttribute attr[1];
+pa_status launch_one(void (*kernel)(P), const P& p, int grid, int cluster, int threads, int smem, cudaStream_t cs) {
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
@@ -616,8 +769,11 @@ pa_status launch_one(void (*kernel)(P), const P& p, int grid, int threads, int s
   cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = cs;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -625,11 +781,11 @@ pa_status launch_one(void (*kernel)(P), const P& p, int grid, int threads, int s
 
 pa_status launch_prepare(const PrepareParams& p, int sms, cudaStream_t cs) {
   const long long items = (long long)p.groups * 4 * p.n_kv_heads, ctas = (items + kPrepareWarps - 1) / kPrepareWarps;
-  return launch_one(pa_prompt_prepare_kernel, p, (int)(ctas < 16ll * sms ? ctas : 16ll * sms), 32 * kPrepareWarps, 0, cs);
+  return launch_one(pa_prompt_prepare_kernel, p, (int)(ctas < 16ll * sms ? ctas : 16ll * sms), 1, 32 * kPrepareWarps, 0, cs);
 }
 
 pa_status launch_prompt(const PromptParams& p, cudaStream_t cs) {
-  return launch_one(pa_prompt_kernel, p, p.n_ctas, kPThreads, PSmem::kLaunch, cs);
+  return launch_one(pa_prompt_kernel, p, 2 * p.n_ctas, 2, kPThreads, PSmem::kLaunch, cs);
 }
 
 pa_status prompt_ready() {

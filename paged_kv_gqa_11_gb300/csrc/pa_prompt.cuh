@@ -8,7 +8,7 @@
 
 namespace pa_prefix {
 
-constexpr int kPromptRows = 128;              // query rows of a unit
+constexpr int kPromptRows = 256;              // query rows of a unit: 128 for each CTA of a pair
 constexpr int kGroupBytes = kGroup * kD * 2;  // a group's keys (or values) in binary16
 
 // A unit of a prompt, and where its sequence's keys lie in the workspace: the row groups
@@ -48,7 +48,7 @@ struct PromptParams {
   float* lse;
   long long q_stride, out_stride;
   int q_type, out_type, n_kv_heads, n_q_heads;
-  int n_units, n_ctas, weigh;
+  int n_units, n_ctas, weigh;  // n_ctas: pairs of CTAs
   int total_len, total_tiles;
   int window, sinks;
   int slot_rows;

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(64 * G) pa_window_merge_kernel(const __grid_co
   const int r = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
-  if (r >= (c.rows_row0 & 0xff)) return;
+  if (r >= (c.rows_row0 & 0xffff)) return;
   const bool other = __ldg(p.lens + c.seq) != c.len;
   const long long slot = 2ll * c.cta * p.slot_rows + r;
   Merged m;
@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(64 * G) pa_window_merge_kernel(const __grid_co
   if (!merge_pieces<G>(p.part_ml, p.part_o, c.n, [&](int i) { return slot + (i == 0 ? 1ll : 2ll * i) * p.slot_rows; }, grp, col, &m))
     return;
   if (other && threadIdx.x == 0) record_error(p.err, PA_ERR_BOUNDS);
-  const int rg = (c.rows_row0 >> 8) + r, h = c.head * kGqa + rg % kGqa;
+  const int rg = (c.rows_row0 >> 16) + r, h = c.head * kGqa + rg % kGqa;
   const long long token = c.token + rg / kGqa;
   store_merged(m, other, p.out, p.out_type, token * p.out_stride + h * kD, col, p.lse ? p.lse + token * p.n_q_heads + h : nullptr);
 }
@@ -151,7 +151,7 @@ struct WsLayout {
 int slot_rows_of(uint32_t max_new) { return (int)std::min<uint64_t>(kRows, (uint64_t)kGqa * max_new); }
 
 WsLayout layout_of(int ctas, const Batch& b) {
-  const size_t rows = 2 * (size_t)ctas * slot_rows_of(b.most), many = b.prompts ? 2 * (size_t)ctas * kPromptRows : 0;
+  const size_t rows = 2 * (size_t)ctas * slot_rows_of(b.most), many = b.prompts ? 2 * (size_t)(ctas / 2) * kPromptRows : 0;
   const size_t keys = (size_t)b.groups * b.heads * kGroupBytes;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -202,7 +202,7 @@ Plan plan_chunk(P& p, MergeParams& m, const Batch& b, bool many, int max_ctas, C
       u.token = at->token + row / kGqa;
       u.len = lens[at->seq];
       u.pos = u.len - n_new[at->seq] + row / kGqa;
-      u.rows_row0 = std::min(P::kUnitRows, rows - row) | (row % kGqa) << 8;
+      u.rows_row0 = std::min(P::kUnitRows, rows - row) | (row % kGqa) << 16;
       u.tile = (int32_t)tiles;
       const int64_t more = tiles + (int64_t)heads * tiles_of(u, p.window, p.sinks);
       if (p.n_units > 0 && more > (kMaxPlaces >> 5)) break;  // the next launch's
@@ -435,7 +435,7 @@ extern "C" pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_
     uint32_t seq = 0;
     int group0 = 0;
     for (Cursor at{0, 0, 0}; at.seq < n_seq;) {
-      const Plan plan = plan_chunk(p, m, b, true, ctas, &at);
+      const Plan plan = plan_chunk(p, m, b, true, ctas / 2, &at);  // ranges of pairs of CTAs
       if (p.n_units == 0) break;
       place_prompts(p, b, &seq, &group0);
       if ((st = launch_prompt(p, cs)) != PA_OK || (st = launch_merge(m, plan, ctas, cs)) != PA_OK) return st;

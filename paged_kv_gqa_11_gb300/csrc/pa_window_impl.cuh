@@ -38,7 +38,7 @@ struct Unit {
   int32_t token;      // of its first row, among all queries
   int32_t pos;        // that token's position
   int32_t len;        // of the sequence
-  int32_t rows_row0;  // query rows | first row among its token's six << 8
+  int32_t rows_row0;  // query rows | first row among its token's six << 16
   int32_t at, tile;   // places, tiles before the unit
 };
 
@@ -67,8 +67,8 @@ struct WindowParams {
   Unit unit[kMaxUnits];
 };
 
-__host__ __device__ inline int unit_rows(const Unit& u) { return u.rows_row0 & 0xff; }
-__host__ __device__ inline int unit_row0(const Unit& u) { return u.rows_row0 >> 8; }
+__host__ __device__ inline int unit_rows(const Unit& u) { return u.rows_row0 & 0xffff; }
+__host__ __device__ inline int unit_row0(const Unit& u) { return u.rows_row0 >> 16; }
 
 // The key order of a unit.
 struct Span {
