@@ -37,12 +37,16 @@ struct Merged {
 
 // The pieces 0 .. np - 1 of a row, whose slot rows row_of gives; true for the threads that
 // have the result (group 0: thread col has the dims 4 col .. + 3).
-template <int G, class RowOf>
+// kRowsPerCta: rows that the CTA's threads merge at once, this thread's being in_cta.
+template <int G, int kRowsPerCta = 1, class RowOf>
 __device__ __forceinline__ bool merge_pieces(const float2* part_ml, const float* part_o, int np, RowOf&& row_of, int grp, int col,
-                                             Merged* out) {
-  constexpr int kAhead = G <= 2 ? 8 : 5;
-  __shared__ float sm[G], sw[G];
-  __shared__ float4 so[G][64];
+                                             Merged* out, int in_cta = 0) {
+  constexpr int kAhead = kRowsPerCta > 1 && G == 1 ? 2 : G <= 2 ? 8 : 5;
+  __shared__ float sms[kRowsPerCta][G], sws[kRowsPerCta][G];
+  __shared__ float4 sos[kRowsPerCta][G][64];
+  float* sm = sms[in_cta];
+  float* sw = sws[in_cta];
+  float4(*so)[64] = sos[in_cta];
   float M = -INFINITY, W = 0.f;
   float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = grp; i0 < np; i0 += G * kAhead) {
@@ -76,6 +80,10 @@ __device__ __forceinline__ bool merge_pieces(const float2* part_ml, const float*
         O = make_float4(fmaf(f, x[k].x, O.x), fmaf(f, x[k].y, O.y), fmaf(f, x[k].z, O.z), fmaf(f, x[k].w, O.w));
     }
     M = mr;
+  }
+  if (G == 1) {
+    *out = Merged{M, W, O};
+    return true;
   }
   if (col == 0) {
     sm[grp] = M;

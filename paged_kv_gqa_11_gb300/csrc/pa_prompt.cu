@@ -28,7 +28,7 @@
 //
 // Warps, hand-offs on mbarriers, every wait bounded:
 //   0-7    softmax: (half of the keys, lane quarter), thread = row;
-//   8-11   query rows into Q, and a finished piece's O to its place;
+//   8-11   query rows into Q (the first piece's: 0-7), and a finished piece's O to its place;
 //   12     MMA issue (the pair's first CTA; the second's tells it of the second's copies); 13 copies.
 // S of tile j + 1 is multiplied while the softmax of tile j runs, and that of j + 1 while PV of
 // j and S of j + 2 are.
@@ -47,6 +47,8 @@ namespace pa_prefix {
 namespace {
 
 using pa_rows_io::Lane;
+
+constexpr int kPlaneGroup = kGroupBytes / 2;  // bytes of a group in a plane
 
 // ------------------------------------------------------------------ keys and values into the workspace
 
@@ -81,7 +83,7 @@ __device__ __forceinline__ uint4 half_values(const uint8_t* grp, int r, int lane
 
 template <int T>
 __device__ __forceinline__ void prepare_rows(const PrepareParams& p, const PromptSeq& s, bool is_v, int head, int group, int half,
-                                             const uint8_t* grp, int first, int lane) {
+                                             const uint8_t* grp, int first, uint4* stage, int lane) {
   uint4 x[8];
   uint32_t wide_rows = 0;
 #pragma unroll
@@ -93,31 +95,47 @@ __device__ __forceinline__ void prepare_rows(const PrepareParams& p, const Promp
     if (is_v && (key >= s.len || (key >= p.sinks && key < s.lo))) x[r] = make_uint4(0u, 0u, 0u, 0u);
   }
   const long long reg = (long long)s.group0 * p.n_kv_heads + (long long)head * s.groups;
-  const long long plane = (((long long)(lane >> 4) * s.groups + group) * 2 + half) * 2048 + (lane & 15) * 128;  // of the lane's dims
-  if (is_v) {
-    uint8_t* to = p.v + reg * kGroupBytes + plane;
+  if (is_v) {  // eight dims x eight keys, transposed
+    uint32_t y[8][4];
 #pragma unroll
     for (int d = 0; d < 4; ++d) {  // dims 2 d and 2 d + 1 of the lane's eight
       uint32_t w[8];
 #pragma unroll
       for (int r = 0; r < 8; ++r) w[r] = d == 0 ? x[r].x : d == 1 ? x[r].y : d == 2 ? x[r].z : x[r].w;
-      uint4* o = reinterpret_cast<uint4*>(to + 32 * d);
-      o[0] = make_uint4(prmt(w[0], w[1], 0x5410), prmt(w[2], w[3], 0x5410), prmt(w[4], w[5], 0x5410), prmt(w[6], w[7], 0x5410));
-      o[1] = make_uint4(prmt(w[0], w[1], 0x7632), prmt(w[2], w[3], 0x7632), prmt(w[4], w[5], 0x7632), prmt(w[6], w[7], 0x7632));
-    }
-  } else {
-    uint8_t* to = p.k + reg * kGroupBytes + plane;
 #pragma unroll
-    for (int r = 0; r < 8; ++r) reinterpret_cast<uint4*>(to)[r] = x[r];
-    if (p.wide && lane == 0) p.wide[(reg + group) * 2 + half] = (uint8_t)wide_rows;
+      for (int k = 0; k < 4; ++k) {
+        y[2 * d][k] = prmt(w[2 * k], w[2 * k + 1], 0x5410);
+        y[2 * d + 1][k] = prmt(w[2 * k], w[2 * k + 1], 0x7632);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) x[r] = make_uint4(y[r][0], y[r][1], y[r][2], y[r][3]);
+  } else if (p.wide && lane == 0) {
+    p.wide[(reg + group) * 2 + half] = (uint8_t)wide_rows;
   }
+  // The lane's core matrix, by way of shared memory (chunk r of lane l at r ^ (l & 7)), so that a
+  // store writes 512 bytes in a row: lanes 0 - 15 are the first plane's 2 KB, the others the second's.
+#pragma unroll
+  for (int r = 0; r < 8; ++r) stage[8 * lane + (r ^ (lane & 7))] = x[r];
+  __syncwarp();
+  uint8_t* to = (is_v ? p.v : p.k) + reg * kGroupBytes + (long long)(2 * group + half) * 2048;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = 32 * i + lane, l = c >> 3;  // chunk c of the 4 KB, of lane l
+    *reinterpret_cast<uint4*>(to + (i >> 2) * (long long)s.groups * kPlaneGroup + ((c & 127) << 4)) = stage[8 * l + ((c & 7) ^ (l & 7))];
+  }
+  __syncwarp();
 }
 
 constexpr int kPrepareWarps = 4;
 
-__global__ void __launch_bounds__(32 * kPrepareWarps) pa_prompt_prepare_kernel(const __grid_constant__ PrepareParams p) {
-  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
+__global__ void __launch_bounds__(32 * kPrepareWarps, 8) pa_prompt_prepare_kernel(const __grid_constant__ PrepareParams p) {
+  // In this order: when the attention starts, all that came before this kernel is complete,
+  // and it may read its queries before it waits for this kernel's keys.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
+  __shared__ uint4 stages[kPrepareWarps][256];
+  uint4* stage = stages[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31;
   const long long items = (long long)p.groups * 4 * p.n_kv_heads, step = (long long)gridDim.x * kPrepareWarps;
   for (long long i = (long long)blockIdx.x * kPrepareWarps + (threadIdx.x >> 5); i < items; i += step) {
@@ -138,16 +156,16 @@ __global__ void __launch_bounds__(32 * kPrepareWarps) pa_prompt_prepare_kernel(c
     const int type = is_v ? p.v_type : p.k_type;
     const uint8_t* grp =
         ok ? (is_v ? p.v_pool : p.k_pool) + (((long long)entry * p.n_kv_heads + head) * p.page_size + off) * row_bytes_of(type) : nullptr;
-    if (type == PA_F16) prepare_rows<PA_F16>(p, s, is_v, head, group, half, grp, first + 8 * half, lane);
-    else if (type == PA_Q8_0) prepare_rows<PA_Q8_0>(p, s, is_v, head, group, half, grp, first + 8 * half, lane);
-    else prepare_rows<PA_Q4_0>(p, s, is_v, head, group, half, grp, first + 8 * half, lane);
+    if (type == PA_F16) prepare_rows<PA_F16>(p, s, is_v, head, group, half, grp, first + 8 * half, stage, lane);
+    else if (type == PA_Q8_0) prepare_rows<PA_Q8_0>(p, s, is_v, head, group, half, grp, first + 8 * half, stage, lane);
+    else prepare_rows<PA_Q4_0>(p, s, is_v, head, group, half, grp, first + 8 * half, stage, lane);
   }
 }
 
 // ------------------------------------------------------------------ the attention
 
 constexpr int kStageBytes = 16384, kNStages = 5;
-constexpr int kCtaRows = kPromptRows / 2, kPlaneGroup = kGroupBytes / 2;  // rows of a CTA; bytes of a group in a plane
+constexpr int kCtaRows = kPromptRows / 2;  // rows of a CTA
 constexpr int kPSmWarps = 8, kAuxWarp0 = 8, kMmaWarp = 12, kCopyWarp = 13, kPThreads = 14 * 32;
 constexpr uint32_t kPOCol = 0, kPSCol = 256;
 
@@ -158,8 +176,8 @@ struct PSmem {
   static constexpr int kRef = kSum + 4 * kCtaRows * 4;        // [piece & 1][row]
   static constexpr int kBar = kRef + 2 * kCtaRows * 4;
   static constexpr int kNBar = 2 * kNStages + 2 + 2 + 2 + 2 + 2 + 1 + 2 + 1;
-  static constexpr int kMisc = kBar + 8 * kNBar + 8 * (kNBar & 1);  // abort, tmem base, the softmax's leave [2]
-  static constexpr int kTotal = kMisc + 16;
+  static constexpr int kMisc = kBar + 8 * kNBar + 8 * (kNBar & 1);  // abort, tmem base, the softmax's leave [quarter][2]
+  static constexpr int kTotal = kMisc + 48;
   static constexpr int kLaunch = kTotal + 1024;
   static_assert(kLaunch <= 232448, "shared memory");
 };
@@ -177,27 +195,16 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// An arrival at the first CTA's barrier of this address.
-__device__ __forceinline__ void arrive_first(uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\tmbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-// warp_wait for a barrier at which the other CTA's threads arrive.
-__device__ __forceinline__ bool warp_wait_pair(uint32_t bar, uint32_t parity, int32_t* err, volatile int* abort) {
-  if (!warp_wait(bar, parity, err, abort)) return false;
-  return __all_sync(0xffffffffu, try_wait_cluster(bar, parity));  // the phase is over: this orders what came before it
+// An arrival at the first CTA's barrier of this address.  What it stands for -- a finished
+// bulk copy, tensor memory behind a tcgen05 fence, shared memory behind a proxy fence -- is
+// read by the tensor cores alone, not through this thread's own memory order, so the
+// arrival has the CTA's scope (the cluster's takes about 1000 cycles in the arriving thread:
+// 361 us for 4096 tokens without a window).
+__device__ __forceinline__ void arrive_first(uint32_t bar, uint32_t rank) {
+  if (rank == 0)
+    mbar_arrive(bar);
+  else
+    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\tmbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(bar) : "memory");
 }
 
 // One arrival at both CTAs' barriers of this address when every MMA issued so far has
@@ -210,23 +217,41 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       : "memory");
 }
 
-__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// MMAs of one stage, issued by the lane whose leader is set; one statement, so that what they
+// share is moved to uniform registers once (mma8).  acc 0: the first overwrites D.
+//   scores: D += Q K^T over 128 dims, eight steps of 16 (two slots of a row each);
+//   values: D += P V over 64 keys, four steps of 16 (a row group each), or only the first `steps`.
+#define PA_MMA(A, AOFF, BOFF, P) \
+  A "\n\tadd.u64 b1, %2, " #BOFF ";\n\t@e tcgen05.mma.cta_group::2.kind::f16 [%0], " AOFF ", b1, %3, " P ";\n\t"
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t leader) {
+#define PA_STEP(OFF, P) PA_MMA("add.u64 a1, %1, " #OFF ";", "a1", OFF, P)
+  asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 a1, b1;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t" PA_STEP(0, "p")
+                   PA_STEP(16, "1") PA_STEP(32, "1") PA_STEP(48, "1") PA_STEP(64, "1") PA_STEP(80, "1") PA_STEP(96, "1") PA_STEP(112, "1") "}" ::"r"(d),
+               "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
+               : "memory");
+#undef PA_STEP
 }
 
-__device__ __forceinline__ void mma_pair_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, int steps, uint32_t leader) {
+#define PA_STEP(AOFF, BOFF, P) PA_MMA("add.u32 a1, %1, " #AOFF ";", "[a1]", BOFF, P)
+  if (steps == 4) {
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t" PA_STEP(
+                     0, 0, "p") PA_STEP(8, 256, "1") PA_STEP(16, 512, "1") PA_STEP(24, 768, "1") "}" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
+                 : "memory");
+  } else {
+    for (int i = 0; i < steps; ++i)
+      asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t" PA_STEP(
+                       0, 0, "p") "}" ::"r"(d),
+                   "r"(a + 8 * i), "l"(b + 256 * i), "r"(idesc), "r"(acc | (uint32_t)i), "r"(leader)
+                   : "memory");
+  }
+#undef PA_STEP
 }
+#undef PA_MMA
+static_assert(kPlaneGroup == 16 * 256, "a step of values in a descriptor");
 
-// A piece of the CTA's range: tiles j0 .. j1 - 1 of a (unit, head).
+// A piece of the pair's range: tiles j0 .. j1 - 1 of a (unit, head).
 struct Piece {
   int unit, head, j0, j1, nt;
   bool first, last;  // of the segment's tiles
@@ -262,44 +287,120 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const uint8_t* src, uint
                : "memory");
 }
 
-// Eight query rows r8 .. r8 + 7 of a CTA's by one warp as binary16 into Q, rows from `rows` on
-// as zeros (stage_q_begin's layout and range).  Lane: row r8 + lane % 8, slots lane / 8 + 4 i.
-__device__ __forceinline__ void load_queries(const PromptParams& p, int token, int row0, int rows, int head, uint32_t dst, int r8, int lane) {
-  const int row = r8 + (lane & 7), rg = row0 + row;
-  const uint32_t to = dst + canon(row, lane >> 3, kD / 8);
-  const long long at = (token + rg / kGqa) * p.q_stride + (head * kGqa + rg % kGqa) * kD + 8 * (lane >> 3);
-  uint4 v[8];
-  if (row >= rows) {
+// Rows r0 .. r1 - 1 (whole eights) of a CTA's query rows by one warp as binary16 into Q, rows from `rows`
+// on as zeros (stage_q_begin's layout and range).  Lane: row r8 + lane % 8, slots lane / 8 + 4 i.
+// 16-bit rows are copied asynchronously, all at once (begin), and bfloat16 converted where it
+// lies (end).
+__device__ __forceinline__ void load_queries_begin(const PromptParams& p, int token, int row0, int rows, int head, uint32_t q, int r0, int r1, int lane) {
+#pragma unroll 1
+  for (int r8 = r0; r8 < r1; r8 += 8) {
+    const int row = r8 + (lane & 7), rg = row0 + row;
+    const uint32_t to = q + canon(row, lane >> 3, kD / 8);
+    const long long at = (token + rg / kGqa) * p.q_stride + (head * kGqa + rg % kGqa) * kD + 8 * (lane >> 3);
+    if (row >= rows) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-  } else if (p.q_type == PA_DT_F32) {
-    const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + at);
+      for (int i = 0; i < 8; ++i) sts128_zero(to + 512 * i);
+    } else if (p.q_type == PA_DT_F32) {
+      const float4* src = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.q) + at);
+      uint32_t top = 0;
+#pragma unroll 4
+      for (int i = 0; i < 8; ++i) {
+        const float4 x = __ldg(src + 8 * i), y = __ldg(src + 8 * i + 1);
+        const uint4 v = make_uint4(pack_half2(x.x, x.y), pack_half2(x.z, x.w), pack_half2(y.x, y.y), pack_half2(y.z, y.w));
+        top = larger2(larger2(larger2(top, v.x), v.y), larger2(v.z, v.w));
+        sts128(to + 512 * i, v);
+      }
+      q_range(top, to);
+    } else {
+      const uint8_t* src = p.q + 2 * at;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512 * i), "l"(src + 64 * i) : "memory");
+    }
+  }
+}
+
+__device__ __forceinline__ void load_queries_end(const PromptParams& p, uint32_t q, int r0, int r1, int lane) {
+  if (p.q_type == PA_DT_F32) return;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (p.q_type != PA_DT_BF16) return;
+#pragma unroll 1
+  for (int r8 = r0; r8 < r1; r8 += 8) {
+    const uint32_t to = q + canon(r8 + (lane & 7), lane >> 3, kD / 8);
+    uint4 v[8];
+    __nv_bfloat162 top = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = lds128(to + 512 * i);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float4 x = __ldg(src + 8 * i), y = __ldg(src + 8 * i + 1);
-      v[i] = make_uint4(pack_half2(x.x, x.y), pack_half2(x.z, x.w), pack_half2(y.x, y.y), pack_half2(y.z, y.w));
+      uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        top = __hmax2(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u[k])));
+        u[k] = pack_half2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
+      }
+      sts128(to + 512 * i, make_uint4(u[0], u[1], u[2], u[3]));
     }
-  } else {
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + 2 * at);
+    // the bfloat16 numbers from 65536 on round to binary16's infinity, those before do not (q_range)
+    if (fmaxf(__low2float(top), __high2float(top)) >= 65536.f)
+      asm volatile("st.shared.b16 [%0], %1;" ::"r"(to), "h"((unsigned short)0x7fff) : "memory");
+  }
+}
+
+// This warp's 32 rows of O (lane = row), times f (0: zeros), to rows of global memory by way of
+// shared memory at `stage` (16 KB of the warp's own), so that a store writes whole rows.
+// to: where this lane's row goes (or NULL), of type Out.  done(): O has been read.
+template <typename Out, class Done>
+__device__ __forceinline__ void write_rows(uint32_t from, float f, uint32_t stage, int lane, uint8_t* to, Done&& done) {
+  constexpr int kPass = 512 / (int)sizeof(Out), kPer = 16 / (int)sizeof(Out);  // columns of a pass (512 bytes of each row), of a chunk
+  const uint32_t row = stage + 512 * lane;
+  const uint64_t f2 = pack2(f, f);
+  const bool zero = f == 0.f;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kD; c0 += kPass) {
+#pragma unroll 1
+    for (int c = 0; c < kPass; c += 64) {
+      uint32_t o[2][32];
+      tmem_ld32(from + c0 + c, o[0]);
+      tmem_ld32(from + c0 + c + 32, o[1]);
+      tmem_ld_wait();
+      loaded(o[0]);
+      loaded(o[1]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __ldg(src + 4 * i);
-    if (p.q_type == PA_DT_BF16) {
+      for (int h = 0; h < 2; ++h) {
+        if (zero) {  // whatever O holds
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          for (int k = 0; k < 32; ++k) o[h][k] = 0u;
+        }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) u[k] = pack_half2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xffff0000u));
-        v[i] = make_uint4(u[0], u[1], u[2], u[3]);
+        for (int k = 0; k < 32; k += 2) put2(o[h] + k, mul2(get2(o[h] + k), f2));
+        // chunk x of row r lies at x ^ (r & 7)
+#pragma unroll
+        for (int k = 0; k < 32; k += kPer) {
+          uint4 v;
+          if constexpr (sizeof(Out) == 4) {
+            v = make_uint4(o[h][k], o[h][k + 1], o[h][k + 2], o[h][k + 3]);
+          } else {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[h][k + e]);
+            v = pack8<Out>(y);
+          }
+          sts128(row + ((((c + 32 * h + k) / kPer) ^ (lane & 7)) << 4), v);
+        }
       }
     }
+    __syncwarp();
+    if (c0 + kPass == kD) done();
+    const unsigned long long mine = reinterpret_cast<unsigned long long>(to ? to + c0 * sizeof(Out) : nullptr);
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      uint8_t* at = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, mine, r));
+      const uint4 v = lds128(stage + 512 * r + ((lane ^ (r & 7)) << 4));
+      if (at) *reinterpret_cast<uint4*>(at + 16 * lane) = v;
+    }
+    __syncwarp();
   }
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    top = larger2(larger2(larger2(top, v[i].x), v[i].y), larger2(v[i].z, v[i].w));
-    sts128(to + 512 * i, v[i]);
-  }
-  if (p.q_type != PA_DT_F16) q_range(top, to);
 }
 
 __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_constant__ PromptParams p) {
@@ -328,9 +429,10 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
                  drain = l_full + 16;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + SM::kMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::kMisc + 4);
-  volatile int* leave = reinterpret_cast<volatile int*>(smem + SM::kMisc + 8);  // of even, odd tiles
+  volatile int* leave = reinterpret_cast<volatile int*>(smem + SM::kMisc + 8) + 2 * (w & 3);  // of even, odd tiles
+  if (tid < 128 && lane == 0) leave[0] = leave[1] = 0;
   if (tid == 0) {
-    *abort = leave[0] = leave[1] = 0;
+    *abort = 0;
     for (int i = 0; i < kNStages; ++i) {
       mbar_init(full + 8 * i, rank == 0 ? 2 : 1);
       mbar_init(empty + 8 * i, 1);
@@ -353,6 +455,13 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
     walk.pos = locate(p, x0);
     walk.left = (x1 < p.total_len ? locate(p, x1).tile : p.total_tiles) - walk.pos.tile;  // at least 1
   }
+  // The kernel before this one (the keys', or a launch of the same call) lets it start only when
+  // what came before that is complete: queries may be read at once.  Keys are read, and anything
+  // is written, behind the wait (the copies' and the results' warps).
+  if (w < kPSmWarps) {  // the first piece's rows
+    const PromptUnit& u = p.unit[walk.pos.unit];
+    load_queries_begin(p, u.token, unit_row0(u) + cta_row0, unit_rows(u) - cta_row0, walk.pos.head, base + SM::kQ, 16 * w, 16 * w + 16, lane);
+  }
   if (w == 0) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -361,9 +470,6 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
   __syncthreads();
   cluster_sync();  // the other CTA's barriers are there
   tc_fence_after();
-  // nothing that another kernel wrote is read before this
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (tid == 0) asm volatile("griddepcontrol.launch_dependents;");
   // All of tensor memory is the pair's, so its columns start at 0 in both.
   const bool whole = *tmem_slot == 0;
   if (!whole && tid == 0) record_error(p.err, PA_ERR_CUDA);
@@ -416,6 +522,8 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
     };
     bool more = walk.next(p, x);
     Span s = span_of(p.unit[x.unit], p.window, p.sinks);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (lane == 0) asm volatile("griddepcontrol.launch_dependents;");
     keys(x, s, x.j0);
     while (more && live) {
       for (int j = x.j0; j + 1 < x.j1 && live; ++j) {
@@ -439,7 +547,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       for (int i = 0; i < n && live; ++i, ++used) {
         const int st = used % kNStages;
         live = warp_wait(full + 8 * st, (used / kNStages) & 1, p.err, abort);
-        if (live && lane == 0) arrive_first(full + 8 * st);
+        if (live && lane == 0) arrive_first(full + 8 * st, rank);
         __syncwarp();
       }
     };
@@ -450,19 +558,23 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
   } else if (w == kMmaWarp) {
     // ---- MMA issue by the whole warp, an elected lane issuing.  After an expired wait no
     // further MMA is issued; what was ends before the pair does.
+    const uint32_t leader = elect_one();
     bool dead = false;
-    int used = 0;
+    uint32_t stage = 0, phase = 0;  // the next stage, and its use's parity
     uint32_t scored = 0, piece = 0;  // pieces whose S, whose PV has begun
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (!dead) dead = !warp_wait_pair(bar, parity, p.err, abort);
+      if (!dead) dead = !warp_wait(bar, parity, p.err, abort);
       return !dead;
     };
-    auto next_stage = [&]() -> uint32_t {  // its barriers' place, 0 .. kNStages - 1; waits for it
-      const int st = used % kNStages;
-      wait(full + 8 * st, (used / kNStages) & 1);
+    auto next_stage = [&]() -> uint32_t {  // waits for it
+      const uint32_t st = stage;
+      wait(full + 8 * st, phase);
       tc_fence_after();
-      ++used;
-      return (uint32_t)st;
+      if (++stage == kNStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+      return st;
     };
     const uint32_t s_idesc = idesc_f16_f32(256, kKeys), pv_idesc = idesc_f16_f32(256, kD);
     // S of tile t of a piece, the range's j
@@ -476,8 +588,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
         const uint32_t st = next_stage();
         if (dead) return;
         const uint64_t kdesc = smem_desc(base + SM::kRing + st * kStageBytes, 128, 2048);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mma_pair(kPSCol + 128 * (j & 1), qdesc + 128 * h + 16 * i, kdesc + 16 * i, s_idesc, h | i);
+        mma_scores(kPSCol + 128 * (j & 1), qdesc + 128 * h, kdesc, s_idesc, h, leader);
         commit_pair(empty + 8 * st);
       }
       commit_pair(s_full + 8 * (j & 1));
@@ -505,8 +616,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
           if (dead) break;
           const uint64_t vdesc = smem_desc(base + SM::kRing + st * kStageBytes, 2048, 128);
           const uint32_t a = kPSCol + 128 * (j & 1) + q / 2;
-          for (int i = 0; i < 4 && q + 16 * i < n16; ++i)
-            mma_pair_tmem_a(kPOCol, a + 8 * i, vdesc + (uint64_t)(i * (kPlaneGroup >> 4)), pv_idesc, (t - now.j0) | q | i);
+          mma_values(kPOCol, a, vdesc, pv_idesc, (uint32_t)((t - now.j0) | q), min(64, n16 - q) >> 4, leader);
           commit_pair(empty + 8 * st);
         }
         if (dead) break;
@@ -530,83 +640,60 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       if (loads > 1 && !(live = warp_wait(q_empty + 8 * (loads & 1), ((loads >> 1) - 1) & 1, p.err, abort))) return;
       const PromptUnit& u = p.unit[y.unit];
       const int rows = unit_rows(u) - cta_row0;  // of this CTA
-#pragma unroll 1
-      for (int r8 = 8 * quarter; r8 < kCtaRows; r8 += 32)
-        load_queries(p, u.token, unit_row0(u) + cta_row0, rows, y.head, base + SM::kQ + (loads & 1) * SM::kQBytes, r8, lane);
+      const uint32_t q = base + SM::kQ + (loads & 1) * SM::kQBytes;
+      load_queries_begin(p, u.token, unit_row0(u) + cta_row0, rows, y.head, q, 32 * quarter, 32 * quarter + 32, lane);
+      load_queries_end(p, q, 32 * quarter, 32 * quarter + 32, lane);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_first(q_full + 8 * (loads & 1));
+      if (lane == 0) arrive_first(q_full + 8 * (loads & 1), rank);
       __syncwarp();
       ++loads;
     };
+    Piece first_piece;  // its rows are the softmax warps' to load, who have nothing else to do yet
+    ahead.next(p, first_piece);
+    loads = 1;
     load();
-    load();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const float* sums = reinterpret_cast<const float*>(smem + SM::kSum);
     const float* refs = reinterpret_cast<const float*>(smem + SM::kRef);
     int tiles = 0;  // of the pieces so far
     for (uint32_t i = 0; live && walk.next(p, x); ++i) {
       tiles += x.j1 - x.j0;
-      const uint32_t j = (uint32_t)tiles - 1;  // the piece's last tile
+      const uint32_t j = (uint32_t)tiles - 1;  // the piece's last tile: after its PV, its S is done too
       if (!(live = warp_wait(l_full + 8 * (i & 1), (i >> 1) & 1, p.err, abort) &&
                    warp_wait(pv_done + 8 * (j & 1), (j >> 1) & 1, p.err, abort)))
         break;
       tc_fence_after();
       const PromptUnit& u = p.unit[x.unit];
-      const int row = 32 * quarter + lane, rg = unit_row0(u) + cta_row0 + row, tok = rg / kGqa;
+      const int row = 32 * quarter + lane, row0 = unit_row0(u) + cta_row0, rows = unit_rows(u) - cta_row0;
       const float l = sums[(i & 1) * 256 + row] + sums[(i & 1) * 256 + 128 + row], m = refs[(i & 1) * 128 + row];
       const uint32_t from = kPOCol + ((uint32_t)(32 * quarter) << 16);
-      const bool mine = cta_row0 + row < unit_rows(u);
+      // by way of this warp's own query rows, whose last product is done and which load() below overwrites
+      const uint32_t stage = base + SM::kQ + (i & 1) * SM::kQBytes + 32 * quarter * 512;
+      auto done = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_first(o_free, rank);
+        __syncwarp();
+      };
       if (x.first && x.last) {  // the whole segment: the result
         const bool other = __ldg(p.lens + u.seq) != u.len;
         if (other && row == 0) record_error(p.err, PA_ERR_BOUNDS);
         const float sum = other ? 0.f : l, inv = sum != 0.f ? 1.f / sum : 0.f;
-        const int h = x.head * kGqa + rg - tok * kGqa;
-        if (mine && p.lse) p.lse[(long long)(u.token + tok) * p.n_q_heads + h] = sum != 0.f ? (m + log2f(sum)) * pa_split::kLn2 : -INFINITY;
+        const int rg = row0 + row, tok = rg / kGqa;
+        if (row < rows && p.lse)
+          p.lse[(long long)(u.token + tok) * p.n_q_heads + x.head * kGqa + rg - tok * kGqa] =
+              sum != 0.f ? (m + log2f(sum)) * pa_split::kLn2 : -INFINITY;
         const int bytes = p.out_type == PA_DT_F32 ? 4 : 2;
-        uint8_t* to = p.out + ((u.token + tok) * p.out_stride + h * kD) * bytes;
-#pragma unroll 1
-        for (int c = 0; c < kD; c += 16) {
-          uint32_t o[16];
-          tmem_ld16(from + c, o);
-          tmem_ld_wait();
-          loaded(o);
-          float y[2][8];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) y[k >> 3][k & 7] = inv != 0.f ? __uint_as_float(o[k]) * inv : 0.f;
-          if (mine) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint8_t* d = to + (c + 8 * k) * bytes;
-              if (p.out_type == PA_DT_F32) store8<float>(d, y[k]);
-              else if (p.out_type == PA_DT_F16) store8<__half>(d, y[k]);
-              else store8<__nv_bfloat16>(d, y[k]);
-            }
-          }
-          __syncwarp();  // the next load is the whole warp's
-        }
+        uint8_t* to = row < rows ? p.out + ((u.token + tok) * p.out_stride + (x.head * kGqa + rg - tok * kGqa) * kD) * bytes : nullptr;
+        if (p.out_type == PA_DT_F32) write_rows<float>(from, inv, stage, lane, to, done);
+        else if (p.out_type == PA_DT_F16) write_rows<__half>(from, inv, stage, lane, to, done);
+        else write_rows<__nv_bfloat16>(from, inv, stage, lane, to, done);
       } else {
         const long long slot = slot_of(x.first, x.last, pair, p.slot_rows) + cta_row0 + row;
-        if (mine) p.part_ml[slot] = make_float2(m, l);
-        float4* to = reinterpret_cast<float4*>(p.part_o + slot * kD);
-#pragma unroll 1
-        for (int c = 0; c < kD; c += 16) {
-          uint32_t o[16];
-          tmem_ld16(from + c, o);
-          tmem_ld_wait();
-          loaded(o);
-          if (mine) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              to[c / 4 + k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]), __uint_as_float(o[4 * k + 2]),
-                                          __uint_as_float(o[4 * k + 3]));
-          }
-          __syncwarp();
-        }
+        if (row < rows) p.part_ml[slot] = make_float2(m, l);
+        write_rows<float>(from, 1.f, stage, lane, row < rows ? reinterpret_cast<uint8_t*>(p.part_o + slot * kD) : nullptr, done);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_first(o_free);
-      __syncwarp();
       load();
     }
   } else {
@@ -617,9 +704,20 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
     float* sums = reinterpret_cast<float*>(smem + SM::kSum);
     float* refs = reinterpret_cast<float*>(smem + SM::kRef);
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
-    // A warp whose wait expired arrives nowhere any more and says so (the tile's `leave`) before
-    // the barrier at which the eight warps meet first in every tile; after it all of them
-    // leave, until then all walk the same tiles, and so the same barriers.
+    {
+      load_queries_end(p, base + SM::kQ, 16 * w, 16 * w + 16, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      named_bar_sync(1 + quarter, 64);
+      if (half == 0 && lane == 0) arrive_first(q_full, rank);
+      __syncwarp();
+    }
+    if (p.wide) asm volatile("griddepcontrol.wait;" ::: "memory");  // which keys are wide
+    // The two warps of a quarter share its rows, and meet in every tile (barrier 1 + quarter).  A
+    // warp whose wait expired arrives nowhere any more and says so (the tile's `leave`) before
+    // they meet first; after it both leave, until then both walk the same tiles, and so the
+    // same barriers.
+    const uint32_t meet = 1 + quarter;
     bool live = true, gone = false;
     uint32_t piece = 0;
     int j = 0;  // the CTA's tile
@@ -633,7 +731,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       float ref = 0.f;
       uint64_t l2 = 0;  // sums of weights over this thread's keys, in two
       for (int t = x.j0; t < x.j1; ++t, ++j) {
-        const int v0 = t * kKeys + 64 * half, n = tile_keys(s, t);
+        const int v0 = t * kKeys + 64 * half;
         uint64_t wide = 0;  // of this thread's keys (all rows': the same)
         if (p.wide) {
 #pragma unroll
@@ -648,22 +746,21 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
         tc_fence_after();
         const uint32_t s_at = kPSCol + 128 * (j & 1) + lanes;
         uint32_t a[2][32];
-        if (64 * half < n) {  // whole warps
-          tmem_ld32(s_at + 64 * half, a[0]);
-          tmem_ld32(s_at + 64 * half + 32, a[1]);
-          tmem_ld_wait();
-          loaded(a[0]);
-          loaded(a[1]);
-        }
+        tmem_ld32(s_at + 64 * half, a[0]);
+        tmem_ld32(s_at + 64 * half + 32, a[1]);
+        tmem_ld_wait();
+        loaded(a[0]);
+        loaded(a[1]);
         if (wide) {
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (wide >> k & 1) a[k >> 5][k & 31] = __float_as_uint(__uint_as_float(a[k >> 5][k & 31]) * 256.f);
+          for (int k = 0; k < 64; ++k) a[k >> 5][k & 31] = __float_as_uint(__uint_as_float(a[k >> 5][k & 31]) * (wide >> k & 1 ? 256.f : 1.f));
         }
-        if (!sees_all(s, t * kKeys, u.pos, last_lo, p.sinks) || 64 * half >= n) {
+        if (!sees_all(s, t * kKeys, u.pos, last_lo, p.sinks)) {  // what the row does not see becomes -inf
+          const uint64_t seen = mine.bits(v0, p.sinks);
+          const uint32_t word[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
 #pragma unroll
           for (int k = 0; k < 64; ++k)
-            if (!mine.has(v0 + k, p.sinks)) a[k >> 5][k & 31] = 0xff800000u;  // -inf
+            if (!(word[k >> 5] >> (k & 31) & 1)) a[k >> 5][k & 31] = 0xff800000u;
         }
         const uint64_t nref = pack2(-ref, -ref);
         float top = -INFINITY;
@@ -674,7 +771,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
           top = fmaxf(top, fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
         }
         const bool first_tile = t == x.j0;
-        const bool raise = bar_or(1, 32 * kPSmWarps, first_tile || top > kLazyLog2);
+        const bool raise = bar_or(meet, 64, first_tile || top > kLazyLog2);
         if (leave[j & 1]) {
           gone = true;
           break;
@@ -682,7 +779,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
         if (raise) {
           red[half * kCtaRows + row] = top;
           __syncwarp();
-          named_bar_sync(1, 32 * kPSmWarps);
+          named_bar_sync(meet, 64);
           const float m = fmaxf(red[row], red[kCtaRows + row]);
           // a row that sees no key yet keeps a reference of 0; it will see none later in the piece either
           const float d = first_tile ? (m == -INFINITY ? 0.f : m) : fmaxf(m, 0.f);
@@ -727,7 +824,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (live && lane == 0) arrive_first(p_full + 8 * (j & 1));
+        if (live && lane == 0) arrive_first(p_full + 8 * (j & 1), rank);
         __syncwarp();
       }
       if (gone) break;

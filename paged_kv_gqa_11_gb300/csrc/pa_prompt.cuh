@@ -56,14 +56,19 @@ struct PromptParams {
   PromptUnit unit[kMaxUnits];
 };
 
-// What a piece takes before its first tile, in tiles' eighths.
-__host__ __device__ __forceinline__ Cost cost_of(const PromptParams& p, const Unit&) { return p.weigh ? Cost{10, 8} : Cost{0, 1}; }
+// What a piece takes, and a tile.
+__host__ __device__ __forceinline__ Cost cost_of(const PromptParams& p, const Unit&) { return p.weigh ? Cost{40, 8} : Cost{0, 1}; }
 
 // The places of a unit's order that a row sees: v <= hi with v >= lo or v < sinks (a row behind
 // the unit's: none).
 struct RowKeys {
   int lo, hi;
   __host__ __device__ __forceinline__ bool has(int v, int sinks) const { return v <= hi && (v >= lo || v < sinks); }
+  // has(v + k, sinks) in bit k, k < 64.
+  __host__ __device__ __forceinline__ uint64_t bits(int v, int sinks) const {
+    return below(hi - v + 1) & (~below(lo - v) | below(sinks - v));
+  }
+  static __host__ __device__ __forceinline__ uint64_t below(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
 };
 
 __host__ __device__ __forceinline__ RowKeys row_keys(const Unit& u, const Span& s, int row, int window) {

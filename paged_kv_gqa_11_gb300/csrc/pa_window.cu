@@ -44,22 +44,27 @@ struct MergeParams {
   Cut cut[kMaxCtas];
 };
 
-// A CTA per row of a cut segment (pa_merge.cuh).
+// Rows of a cut segment by groups of G times 64 threads (pa_merge.cuh), kMergeRows / G of them to a
+// CTA.
+constexpr int kMergeRows = 8;
+
 template <int G>
-__global__ void __launch_bounds__(64 * G) pa_window_merge_kernel(const __grid_constant__ MergeParams p) {
-  const int col = threadIdx.x & 63, grp = threadIdx.x >> 6;
+__global__ void __launch_bounds__(64 * kMergeRows) pa_window_merge_kernel(const __grid_constant__ MergeParams p) {
+  const int col = threadIdx.x & 63, grp = (threadIdx.x >> 6) % G, in_cta = (threadIdx.x >> 6) / G;
   const Cut& c = p.cut[blockIdx.x];
-  const int r = blockIdx.y;
+  const int r = (int)blockIdx.y * (kMergeRows / G) + in_cta;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
-  if (r >= (c.rows_row0 & 0xffff)) return;
+  const bool mine = r < (c.rows_row0 & 0xffff);
   const bool other = __ldg(p.lens + c.seq) != c.len;
   const long long slot = 2ll * c.cta * p.slot_rows + r;
   Merged m;
   // the first piece ends its CTA's range (the second slot), the others begin theirs
-  if (!merge_pieces<G>(p.part_ml, p.part_o, c.n, [&](int i) { return slot + (i == 0 ? 1ll : 2ll * i) * p.slot_rows; }, grp, col, &m))
+  if (!merge_pieces<G, kMergeRows / G>(p.part_ml, p.part_o, mine ? c.n : 0,
+                                       [&](int i) { return slot + (i == 0 ? 1ll : 2ll * i) * p.slot_rows; }, grp, col, &m, in_cta) ||
+      !mine)
     return;
-  if (other && threadIdx.x == 0) record_error(p.err, PA_ERR_BOUNDS);
+  if (other && col == 0) record_error(p.err, PA_ERR_BOUNDS);
   const int rg = (c.rows_row0 >> 16) + r, h = c.head * kGqa + rg % kGqa;
   const long long token = c.token + rg / kGqa;
   store_merged(m, other, p.out, p.out_type, token * p.out_stride + h * kD, col, p.lse ? p.lse + token * p.n_q_heads + h : nullptr);
@@ -214,14 +219,19 @@ Plan plan_chunk(P& p, MergeParams& m, const Batch& b, bool many, int max_ctas, C
   if (p.n_units == 0) return Plan{0, 0};
   p.total_tiles = (int)tiles;
   p.n_ctas = (int)std::min<int64_t>(tiles, max_ctas);
-  // every CTA must have a tile: with weights its range is longer than a lead and a tile
-  p.weigh = tiles > 3 * p.n_ctas;
+  // Every CTA must have a tile: with weights its range is at least as long as a lead and a tile.
   int64_t places = 0;
-  for (int i = 0; i < p.n_units; ++i) {
-    Unit& u = p.unit[i];
-    const Cost c = cost_of(p, u);
-    u.at = (int32_t)places;
-    places += (int64_t)heads * (c.lead + (int64_t)tiles_of(u, p.window, p.sinks) * c.tile);
+  for (p.weigh = tiles > 3 * p.n_ctas;; p.weigh = 0) {
+    places = 0;
+    int most = 0;
+    for (int i = 0; i < p.n_units; ++i) {
+      Unit& u = p.unit[i];
+      const Cost c = cost_of(p, u);
+      u.at = (int32_t)places;
+      places += (int64_t)heads * (c.lead + (int64_t)tiles_of(u, p.window, p.sinks) * c.tile);
+      most = std::max(most, c.lead + c.tile);
+    }
+    if (!p.weigh || places / p.n_ctas >= most) break;
   }
   p.total_len = (int)places;
   int cuts = 0, rows = 0, unit = -1, head = -1;
@@ -267,8 +277,8 @@ pa_status launch_merge(const MergeParams& m, const Plan& plan, int max_ctas, cud
   if (plan.cuts == 0) return PA_OK;
   Launch l(cs);
   const int wide = merge_groups((int64_t)plan.cuts * plan.rows, max_ctas);
-  l.cfg.gridDim = dim3((unsigned)plan.cuts, (unsigned)plan.rows);
-  l.cfg.blockDim = dim3(64 * wide);
+  l.cfg.gridDim = dim3((unsigned)plan.cuts, (unsigned)ceil_div(plan.rows, kMergeRows / wide));
+  l.cfg.blockDim = dim3(64 * kMergeRows);
   const auto merge = wide == 8   ? pa_window_merge_kernel<8>
                      : wide == 4 ? pa_window_merge_kernel<4>
                      : wide == 2 ? pa_window_merge_kernel<2>

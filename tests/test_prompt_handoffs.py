@@ -126,7 +126,7 @@ def simulate(seed, agree=True):
             yield ("drain", 0)
 
     def aux(c, a):
-        loads = done = 0
+        loads, done = 1, 0
 
         def load():
             nonlocal loads
@@ -141,7 +141,7 @@ def simulate(seed, agree=True):
             yield None
             return True
 
-        if not (yield from load()) or not (yield from load()):
+        if not (yield from load()):
             return
         for i, m in enumerate(pieces):
             done += m
@@ -157,40 +157,40 @@ def simulate(seed, agree=True):
             if not (yield from load()):
                 return
 
-    meeting = [{"here": [], "generation": 0, "any": False, "results": {}} for _ in range(2)]
-    leave = [[0, 0], [0, 0]]
-    raises = [[rnd.random() < 0.3 for _ in range(n)] for _ in range(2)]
+    meeting = [{"here": [], "generation": 0, "any": False, "results": {}} for _ in range(8)]  # of a CTA's quarter
+    leave = [[0, 0] for _ in range(8)]
+    raises = [[rnd.random() < 0.3 for _ in range(n)] for _ in range(8)]
 
     def meet(c, form, x=False):
         m = meeting[c]
         g = m["generation"]
         m["here"].append(form)
         m["any"] |= x
-        if len(m["here"]) == 8:
+        if len(m["here"]) == 2:
             if len(set(m["here"])) > 1:
                 raise Fault("one barrier in two forms")
             m["results"][g] = m["any"]
             m.update(here=[], generation=g + 1, any=False)
         while m["generation"] == g:
-            yield ("meet", c)
+            yield ("meet", c >> 2)
         return m["results"][g]
 
     def softmax(c, w):
-        live = True
+        live, g = True, 4 * c + (w & 3)
         for j, (i, t, m) in enumerate(tiles):
             live = live and (yield from wait(s_full[c][j & 1], j >> 1, c))
             if not live:
                 if not agree:
                     return
-                leave[c][j & 1] = 1
-            up = yield from meet(c, "or", t == 0 or raises[c][j])
-            if leave[c][j & 1]:
+                leave[g][j & 1] = 1
+            up = yield from meet(g, "or", t == 0 or raises[g][j])
+            if leave[g][j & 1]:
                 return
             if up:
-                yield from meet(c, "sync")
+                yield from meet(g, "sync")
                 if t > 0 and not (yield from wait(pv_done[c][(j - 1) & 1], (j - 1) >> 1, c)):
                     live = False
-                    leave[c][(j + 1) & 1] = 1
+                    leave[g][(j + 1) & 1] = 1
             yield None
             if live:
                 p_full[j & 1].arrive()
@@ -202,7 +202,14 @@ def simulate(seed, agree=True):
                     l_full[c][i & 1].arrive()
                 yield None
 
-    roles = {"mma": mma(), "forward": forward()}
+    def first_rows():  # the first piece's, by the softmax warps
+        for c in range(2):
+            for a in range(4):
+                queries[c, a, 0] = 0
+                yield None
+                q_full[0].arrive()
+
+    roles = {"mma": mma(), "forward": forward(), "first rows": first_rows()}
     for c in range(2):
         roles[f"copy {c}"] = copy(c)
         for a in range(4):

@@ -78,6 +78,7 @@ static void masks(const PromptParams& p, const PromptUnit& u, const Span& s, int
         continue;
       }
       CHECK(yes == (v < s.end && sees(u, r, key, p.window, p.sinks)));
+      CHECK(yes == (row_keys(u, s, r, p.window).bits(v & ~63, p.sinks) >> (v & 63) & 1));
       if (inner) CHECK(yes);
     }
     if (k >= ((n + 15) & ~15)) continue;  // not copied
