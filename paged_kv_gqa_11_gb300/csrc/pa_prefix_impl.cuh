@@ -870,7 +870,17 @@ __global__ void __launch_bounds__(kThreads, 1) pa_prefix_kernel(const __grid_con
     mbar_init(sink, 1);
     fence_mbar_init();
   }
-  if (w == 1 || w == 2) {
+  if constexpr (P::kWindow) {
+    if (w == 1) {
+      const Pos t = start_of(p, (int)blockIdx.x);
+      if (lane == 0) {
+        *start = t;
+        *opening = Tile{(uint32_t)pos_rows(p, t) | 1u << 8, 0, pos_row0(p, t), 0, pos_token(p, t), t.head, {0, 0}};
+        tiles_at[0] = t.tile;
+        tiles_at[1] = p.start[blockIdx.x + 1].tile;
+      }
+    }
+  } else if (w == 1 || w == 2) {
     const int x = (int)((long long)(blockIdx.x + w - 1) * p.total_len / p.n_ctas);
     if (x < p.total_len) {
       const Pos t = locate(p, x);

@@ -34,7 +34,8 @@
 // j and S of j + 2 are.
 //
 // Ranges, cuts and slots are those of pa_window_impl.cuh, with units of 256 rows and ranges of
-// pairs.
+// pairs; or, where that is no longer than with cuts and their merge, every pair has whole
+// segments, the largest dealt first, each to the pair with least.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -190,10 +191,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
-// All threads of both CTAs.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+// A meeting of all threads of both CTAs, in its two halves.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // An arrival at the first CTA's barrier of this address.  What it stands for -- a finished
 // bulk copy, tensor memory behind a tcgen05 fence, shared memory behind a proxy fence -- is
@@ -260,8 +260,29 @@ struct Piece {
 // The roles walk the CTA's pieces each on its own.
 struct Walk {
   Pos pos;
-  int left;  // tiles of the range from here on
+  int left;         // tiles of the range from here on
+  int item, items;  // of the list
+  __device__ __forceinline__ Walk(const PromptParams& p, int pair) {
+    left = item = items = 0;
+    if (p.listed) {
+      item = p.first[pair];
+      items = p.first[pair + 1];
+    } else {
+      pos = start_of(p, pair);
+      left = p.start[pair + 1].tile - pos.tile;  // at least 1
+    }
+  }
   __device__ __forceinline__ bool next(const PromptParams& p, Piece& x) {
+    if (p.listed) {
+      if (item == items) return false;
+      const int seg = p.list[item++];
+      x.unit = seg / p.n_kv_heads;
+      x.head = seg - x.unit * p.n_kv_heads;
+      x.j0 = 0;
+      x.j1 = x.nt = ceil_div(span_of(p.unit[x.unit], p.window, p.sinks).end, kKeys);
+      x.first = x.last = true;
+      return true;
+    }
     if (left == 0) return false;
     x.unit = pos.unit;
     x.head = pos.head;
@@ -349,51 +370,52 @@ __device__ __forceinline__ void load_queries_end(const PromptParams& p, uint32_t
 
 // This warp's 32 rows of O (lane = row), times f (0: zeros), to rows of global memory by way of
 // shared memory at `stage` (16 KB of the warp's own), so that a store writes whole rows.
-// to: where this lane's row goes (or NULL), of type Out.  done(): O has been read.
-template <typename Out, class Done>
-__device__ __forceinline__ void write_rows(uint32_t from, float f, uint32_t stage, int lane, uint8_t* to, Done&& done) {
-  constexpr int kPass = 512 / (int)sizeof(Out), kPer = 16 / (int)sizeof(Out);  // columns of a pass (512 bytes of each row), of a chunk
-  const uint32_t row = stage + 512 * lane;
+// to: where this lane's row goes (or NULL), of `type`.  done(): O has been read.  One body for
+// all types, 32 columns at a time: a piece's end meets cold instruction caches as it is.
+template <class Done>
+__device__ __forceinline__ void write_rows(uint32_t from, float f, uint32_t stage, int lane, uint8_t* to, int type, Done&& done) {
+  const bool wide = type == PA_DT_F32;
+  const int passes = wide ? 2 : 1, steps = wide ? 4 : 8;  // of 512 bytes of each row, of 32 columns
+  const uint32_t row = stage + 512 * lane, r7 = lane & 7;
   const uint64_t f2 = pack2(f, f);
-  const bool zero = f == 0.f;
 #pragma unroll 1
-  for (int c0 = 0; c0 < kD; c0 += kPass) {
+  for (int pass = 0; pass < passes; ++pass) {
 #pragma unroll 1
-    for (int c = 0; c < kPass; c += 64) {
-      uint32_t o[2][32];
-      tmem_ld32(from + c0 + c, o[0]);
-      tmem_ld32(from + c0 + c + 32, o[1]);
+    for (int i = 0; i < steps; ++i) {
+      uint32_t o[32];
+      tmem_ld32(from + 32 * (steps * pass + i), o);
       tmem_ld_wait();
-      loaded(o[0]);
-      loaded(o[1]);
+      loaded(o);
+      if (f == 0.f) {  // whatever O holds
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (zero) {  // whatever O holds
+        for (int k = 0; k < 32; ++k) o[k] = 0u;
+      }
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[h][k] = 0u;
-        }
+      for (int k = 0; k < 32; k += 2) put2(o + k, mul2(get2(o + k), f2));
+      // chunk x of row r lies at x ^ (r & 7)
+      if (wide) {
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) put2(o[h] + k, mul2(get2(o[h] + k), f2));
-        // chunk x of row r lies at x ^ (r & 7)
+        for (int k = 0; k < 8; ++k) sts128(row + (((8 * i + k) ^ r7) << 4), make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+      } else {
+        uint32_t h[16];
+        if (type == PA_DT_F16) {
 #pragma unroll
-        for (int k = 0; k < 32; k += kPer) {
-          uint4 v;
-          if constexpr (sizeof(Out) == 4) {
-            v = make_uint4(o[h][k], o[h][k + 1], o[h][k + 2], o[h][k + 3]);
-          } else {
-            float y[8];
+          for (int k = 0; k < 16; ++k) h[k] = pack_half2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[h][k + e]);
-            v = pack8<Out>(y);
+          for (int k = 0; k < 16; ++k) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+            h[k] = *reinterpret_cast<const uint32_t*>(&b);
           }
-          sts128(row + ((((c + 32 * h + k) / kPer) ^ (lane & 7)) << 4), v);
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sts128(row + (((4 * i + k) ^ r7) << 4), make_uint4(h[4 * k], h[4 * k + 1], h[4 * k + 2], h[4 * k + 3]));
       }
     }
     __syncwarp();
-    if (c0 + kPass == kD) done();
-    const unsigned long long mine = reinterpret_cast<unsigned long long>(to ? to + c0 * sizeof(Out) : nullptr);
-#pragma unroll 8
+    if (pass + 1 == passes) done();
+    const unsigned long long mine = reinterpret_cast<unsigned long long>(to ? to + 512 * pass : nullptr);
+#pragma unroll 4
     for (int r = 0; r < 32; ++r) {
       uint8_t* at = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, mine, r));
       const uint4 v = lds128(stage + 512 * r + ((lane ^ (r & 7)) << 4));
@@ -449,18 +471,16 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
     mbar_init(drain, 1);
     fence_mbar_init();
   }
-  Walk walk;
-  {
-    const int x0 = (int)((long long)pair * p.total_len / p.n_ctas), x1 = (int)((long long)(pair + 1) * p.total_len / p.n_ctas);
-    walk.pos = locate(p, x0);
-    walk.left = (x1 < p.total_len ? locate(p, x1).tile : p.total_tiles) - walk.pos.tile;  // at least 1
-  }
+  Walk walk(p, pair);
   // The kernel before this one (the keys', or a launch of the same call) lets it start only when
   // what came before that is complete: queries may be read at once.  Keys are read, and anything
   // is written, behind the wait (the copies' and the results' warps).
   if (w < kPSmWarps) {  // the first piece's rows
-    const PromptUnit& u = p.unit[walk.pos.unit];
-    load_queries_begin(p, u.token, unit_row0(u) + cta_row0, unit_rows(u) - cta_row0, walk.pos.head, base + SM::kQ, 16 * w, 16 * w + 16, lane);
+    Walk ahead = walk;
+    Piece y;
+    ahead.next(p, y);
+    const PromptUnit& u = p.unit[y.unit];
+    load_queries_begin(p, u.token, unit_row0(u) + cta_row0, unit_rows(u) - cta_row0, y.head, base + SM::kQ, 16 * w, 16 * w + 16, lane);
   }
   if (w == 0) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(kTmemCols) : "memory");
@@ -468,11 +488,13 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // the other CTA's barriers are there
+  cluster_arrive();  // this CTA's barriers are there
   tc_fence_after();
   // All of tensor memory is the pair's, so its columns start at 0 in both.
   const bool whole = *tmem_slot == 0;
   if (!whole && tid == 0) record_error(p.err, PA_ERR_CUDA);
+  if (w < kPSmWarps) load_queries_end(p, base + SM::kQ, 16 * w, 16 * w + 16, lane);
+  cluster_wait();  // and the other's
   int issued = 0;
   Piece x;
 
@@ -676,24 +698,27 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
         if (lane == 0) arrive_first(o_free, rank);
         __syncwarp();
       };
+      float f = 1.f;
+      uint8_t* to = nullptr;
+      int type = PA_DT_F32;
       if (x.first && x.last) {  // the whole segment: the result
         const bool other = __ldg(p.lens + u.seq) != u.len;
         if (other && row == 0) record_error(p.err, PA_ERR_BOUNDS);
-        const float sum = other ? 0.f : l, inv = sum != 0.f ? 1.f / sum : 0.f;
-        const int rg = row0 + row, tok = rg / kGqa;
-        if (row < rows && p.lse)
-          p.lse[(long long)(u.token + tok) * p.n_q_heads + x.head * kGqa + rg - tok * kGqa] =
-              sum != 0.f ? (m + log2f(sum)) * pa_split::kLn2 : -INFINITY;
-        const int bytes = p.out_type == PA_DT_F32 ? 4 : 2;
-        uint8_t* to = row < rows ? p.out + ((u.token + tok) * p.out_stride + (x.head * kGqa + rg - tok * kGqa) * kD) * bytes : nullptr;
-        if (p.out_type == PA_DT_F32) write_rows<float>(from, inv, stage, lane, to, done);
-        else if (p.out_type == PA_DT_F16) write_rows<__half>(from, inv, stage, lane, to, done);
-        else write_rows<__nv_bfloat16>(from, inv, stage, lane, to, done);
-      } else {
+        const float sum = other ? 0.f : l;
+        const int rg = row0 + row, tok = rg / kGqa, h = x.head * kGqa + rg - tok * kGqa;
+        f = sum != 0.f ? 1.f / sum : 0.f;
+        type = p.out_type;
+        if (row < rows) {
+          if (p.lse) p.lse[(long long)(u.token + tok) * p.n_q_heads + h] = sum != 0.f ? (m + log2f(sum)) * pa_split::kLn2 : -INFINITY;
+          to = p.out + ((u.token + tok) * p.out_stride + h * kD) * (type == PA_DT_F32 ? 4 : 2);
+        }
+      } else if (row < rows) {
         const long long slot = slot_of(x.first, x.last, pair, p.slot_rows) + cta_row0 + row;
-        if (row < rows) p.part_ml[slot] = make_float2(m, l);
-        write_rows<float>(from, 1.f, stage, lane, row < rows ? reinterpret_cast<uint8_t*>(p.part_o + slot * kD) : nullptr, done);
+        p.part_ml[slot] = make_float2(m, l);
+        to = reinterpret_cast<uint8_t*>(p.part_o + slot * kD);
       }
+      __syncwarp();
+      write_rows(from, f, stage, lane, to, type, done);
       load();
     }
   } else {
@@ -705,7 +730,6 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
     float* refs = reinterpret_cast<float*>(smem + SM::kRef);
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     {
-      load_queries_end(p, base + SM::kQ, 16 * w, 16 * w + 16, lane);
       fence_proxy_async_smem();
       __syncwarp();
       named_bar_sync(1 + quarter, 64);
@@ -745,16 +769,25 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
         if (!live) leave[j & 1] = 1;
         tc_fence_after();
         const uint32_t s_at = kPSCol + 128 * (j & 1) + lanes;
+        if (wide) {  // rare, and so in a loop of its own, in tensor memory
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 8) {
+            uint32_t y[8];
+            tmem_ld8(s_at + 64 * half + c, y);
+            tmem_ld_wait();
+            loaded(y);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * ((wide >> c) >> k & 1 ? 256.f : 1.f));
+            tmem_st8(s_at + 64 * half + c, y);
+          }
+          tmem_st_wait();
+        }
         uint32_t a[2][32];
         tmem_ld32(s_at + 64 * half, a[0]);
         tmem_ld32(s_at + 64 * half + 32, a[1]);
         tmem_ld_wait();
         loaded(a[0]);
         loaded(a[1]);
-        if (wide) {
-#pragma unroll
-          for (int k = 0; k < 64; ++k) a[k >> 5][k & 31] = __float_as_uint(__uint_as_float(a[k >> 5][k & 31]) * (wide >> k & 1 ? 256.f : 1.f));
-        }
         if (!sees_all(s, t * kKeys, u.pos, last_lo, p.sinks)) {  // what the row does not see becomes -inf
           const uint64_t seen = mine.bits(v0, p.sinks);
           const uint32_t word[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
@@ -845,7 +878,8 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       mbar_wait(full + 8 * (i % kNStages), (uint32_t)((i / kNStages) & 1), p.err, abort, false, kWaitTimeoutNs / 8);
   }
   __syncwarp();
-  cluster_sync();  // no MMA, arrival or copy is on its way to either CTA any more
+  cluster_arrive();
+  cluster_wait();  // no MMA, arrival or copy is on its way to either CTA any more
   if (w == 0) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(*tmem_slot), "r"(kTmemCols) : "memory");

@@ -53,11 +53,22 @@ struct PromptParams {
   int window, sinks;
   int slot_rows;
   float scale_log2;
+  Start start[kMaxCtas / 2 + 1];
+  // Or whole segments for each pair (listed): list[first[i]] .. list[first[i + 1] - 1], unit *
+  // n_kv_heads + head.
+  static constexpr int kMaxListed = 1024;
+  int listed;
+  uint16_t first[kMaxCtas / 2 + 1];
+  uint16_t list[kMaxListed];
   PromptUnit unit[kMaxUnits];
 };
 
-// What a piece takes, and a tile.
-__host__ __device__ __forceinline__ Cost cost_of(const PromptParams& p, const Unit&) { return p.weigh ? Cost{40, 8} : Cost{0, 1}; }
+// What a piece takes, and a tile; and the cuts of a launch (a merge, and rows in fp32 by way of the
+// workspace) in the same places, 0.15 us each.
+constexpr int kPromptLead = 40, kPromptTile = 8, kPromptMerge = 70;
+__host__ __device__ __forceinline__ Cost cost_of(const PromptParams& p, const Unit&) {
+  return p.weigh ? Cost{kPromptLead, kPromptTile} : Cost{0, 1};
+}
 
 // The places of a unit's order that a row sees: v <= hi with v >= lo or v < sinks (a row behind
 // the unit's: none).

@@ -22,7 +22,6 @@ namespace {
 
 constexpr int64_t kMaxLen = 0x7fffffff - 2 * kKeys;  // a tile past the last key is still a 32-bit number
 constexpr uint32_t kMaxNew = 1u << 24;               // new tokens of a sequence
-constexpr int kMaxCtas = 256;
 constexpr int64_t kMaxPlaces = 1ll << 30;
 constexpr int32_t kPromptTokens = 64;  // sequences of so many new tokens or more are the prompts' kernel's
 
@@ -235,8 +234,10 @@ Plan plan_chunk(P& p, MergeParams& m, const Batch& b, bool many, int max_ctas, C
   }
   p.total_len = (int)places;
   int cuts = 0, rows = 0, unit = -1, head = -1;
-  for (int c = 1; c < p.n_ctas; ++c) {
+  p.start[p.n_ctas] = Start{0, 0, p.total_tiles};
+  for (int c = 0; c < p.n_ctas; ++c) {
     const Pos t = locate(p, (int)((long long)c * p.total_len / p.n_ctas));
+    p.start[c] = Start{t.unit | t.head << 16, t.j, t.tile};
     if (t.j == 0) continue;  // the range begins with a segment
     if (t.unit == unit && t.head == head) {
       ++m.cut[cuts - 1].n;
@@ -318,9 +319,59 @@ void place_prompts(PromptParams& p, const Batch& b, uint32_t* seq, int* group0) 
   }
 }
 
+// Whole segments for each pair instead of p's ranges, if the longest pair's share is no longer
+// than the ranges with their merge.
+bool list_segments(PromptParams& p, const Plan& plan) {
+  p.listed = 0;
+  const int segs = p.n_units * p.n_kv_heads;
+  if (segs > PromptParams::kMaxListed || segs < p.n_ctas) return false;
+  struct Seg {
+    int32_t cost;
+    uint16_t unit;
+  };
+  static thread_local Seg seg[PromptParams::kMaxUnits];
+  int64_t total = 0;
+  for (int i = 0; i < p.n_units; ++i) {
+    seg[i] = Seg{kPromptLead + kPromptTile * tiles_of(p.unit[i], p.window, p.sinks), (uint16_t)i};
+    total += (int64_t)p.n_kv_heads * seg[i].cost;
+  }
+  std::sort(seg, seg + p.n_units, [](const Seg& a, const Seg& b) { return a.cost > b.cost || (a.cost == b.cost && a.unit < b.unit); });
+  // a heap of (load, pair), the least first
+  static thread_local uint64_t heap[kMaxCtas];
+  static thread_local uint16_t owner[PromptParams::kMaxListed];
+  for (int i = 0; i < p.n_ctas; ++i) heap[i] = (uint64_t)i;
+  const auto more = [](uint64_t a, uint64_t b) { return a > b; };
+  int k = 0;
+  uint64_t longest = 0;
+  for (int i = 0; i < p.n_units; ++i)
+    for (int h = 0; h < p.n_kv_heads; ++h) {
+      std::pop_heap(heap, heap + p.n_ctas, more);
+      uint64_t& top = heap[p.n_ctas - 1];
+      owner[k++] = (uint16_t)(top & 0xffff);
+      top += (uint64_t)seg[i].cost << 16;
+      longest = std::max(longest, top >> 16);
+      std::push_heap(heap, heap + p.n_ctas, more);
+    }
+  if ((int64_t)longest > total / p.n_ctas + (plan.cuts ? kPromptMerge : 0)) return false;
+  uint16_t at[kMaxCtas / 2 + 1] = {};
+  for (int i = 0; i < segs; ++i) ++at[owner[i]];
+  uint16_t sum = 0;
+  for (int i = 0; i < p.n_ctas; ++i) {
+    p.first[i] = sum;
+    sum = (uint16_t)(sum + at[i]);
+    at[i] = p.first[i];
+  }
+  p.first[p.n_ctas] = sum;
+  k = 0;
+  for (int i = 0; i < p.n_units; ++i)
+    for (int h = 0; h < p.n_kv_heads; ++h) p.list[at[owner[k++]]++] = (uint16_t)(seg[i].unit * p.n_kv_heads + h);
+  p.listed = 1;
+  return true;
+}
+
 pa_status check_pool(const pa_pool* pool, pa_pool_desc* d, WindowKernel* ki) {
   if (!pool || pa_pool_get_desc(pool, d) != PA_OK) return PA_ERR_INVALID;
-  return d->head_dim == (uint32_t)kD && lookup_kernel(d->k_type, d->v_type, ki) ? PA_OK : PA_ERR_UNSUPPORTED;
+  return d->head_dim == (uint32_t)kD && d->n_kv_heads <= 0x7fff && lookup_kernel(d->k_type, d->v_type, ki) ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
 // The window as the kernels take it: at most as long as any sequence.
@@ -445,8 +496,9 @@ extern "C" pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_
     uint32_t seq = 0;
     int group0 = 0;
     for (Cursor at{0, 0, 0}; at.seq < n_seq;) {
-      const Plan plan = plan_chunk(p, m, b, true, ctas / 2, &at);  // ranges of pairs of CTAs
+      Plan plan = plan_chunk(p, m, b, true, ctas / 2, &at);  // ranges of pairs of CTAs
       if (p.n_units == 0) break;
+      if (list_segments(p, plan)) plan.cuts = 0;
       place_prompts(p, b, &seq, &group0);
       if ((st = launch_prompt(p, cs)) != PA_OK || (st = launch_merge(m, plan, ctas, cs)) != PA_OK) return st;
     }

@@ -42,6 +42,14 @@ struct Unit {
   int32_t at, tile;   // places, tiles before the unit
 };
 
+// Where a CTA's range begins: j-th tile of (unit, head), the launch's tile-th; one more for the
+// end.  The host finds them: a search among the units in the kernel takes 2 us of cold loads.
+struct Start {
+  int32_t unit_head;  // unit | head << 16
+  int32_t j, tile;
+};
+constexpr int kMaxCtas = 256;
+
 struct WindowParams {
   static constexpr bool kWindow = true;
   static constexpr int kUnitRows = kRows, kMaxUnits = 448;  // query rows of a unit, units per launch
@@ -64,6 +72,7 @@ struct WindowParams {
   int window, sinks;
   int slot_rows;  // rows of a slot
   float scale_log2;
+  Start start[kMaxCtas + 1];
   Unit unit[kMaxUnits];
 };
 
@@ -132,6 +141,21 @@ __host__ __device__ __forceinline__ Pos locate(const P& p, int x) {
     --t.j;
     advance(p, t);
   }
+  return t;
+}
+
+template <class P>
+__device__ __forceinline__ Pos start_of(const P& p, int cta) {
+  const Start& s = p.start[cta];
+  Pos t;
+  t.pre = false;
+  t.rt = 0;
+  t.nrt = 1;
+  t.unit = s.unit_head & 0xffff;
+  t.head = s.unit_head >> 16;
+  t.j = s.j;
+  t.tile = s.tile;
+  pos_sizes(p, t);
   return t;
 }
 

@@ -26,4 +26,4 @@ def test_window_plan_matches_its_definition(tmp_path):
     assert done.returncode == 0, done.stderr
     out = subprocess.run([exe, "400"], capture_output=True, text=True)
     assert out.returncode == 0, out.stdout + out.stderr
-    assert "mismatches 0" in out.stdout, out.stdout
+    assert "mismatches 0," in out.stdout, out.stdout

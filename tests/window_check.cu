@@ -10,7 +10,7 @@
 
 #include "pa_window.cu"
 
-static long long bad = 0;
+static long long bad = 0, listed = 0;
 #define CHECK(x)                                         \
   do {                                                   \
     if (!(x)) {                                          \
@@ -96,7 +96,7 @@ static int check(int batches, bool many) {
   static MergeParams m;
   for (int batch = 0; batch < batches; ++batch) {
     const bool big = batch % 50 == 49;  // more units than one launch takes
-    const int n_seq = big ? (many ? pick(70, 150) : pick(300, 700)) : pick(1, 12), max_ctas = pick(1, 3) == 1 ? pick(1, 7) : 152;
+    const int n_seq = big ? (many ? pick(70, 150) : pick(300, 700)) : pick(1, 12), max_ctas = pick(1, 3) == 1 ? pick(1, 7) : many ? 76 : 152;
     const int win[] = {1, 2, 15, 16, 17, pick(1, 300), pick(1, 3000), kAllKeys}, snk[] = {0, 0, 1, 4, 16, 17, pick(0, 300), kAllKeys};
     p.window = win[pick(0, 7)];
     p.sinks = snk[pick(0, 7)];
@@ -125,7 +125,16 @@ static int check(int batches, bool many) {
       if (at.seq == before.seq && at.rt == before.rt) return 1;
       if (p.n_units == 0) break;
       ++launches;
-      if constexpr (kPrompt<P>) place_prompts(p, b, &prompt_seq, &group0);
+      if constexpr (kPrompt<P>) {
+        place_prompts(p, b, &prompt_seq, &group0);
+        if (list_segments(p, plan)) {  // every segment once, some for every pair
+          std::set<int> once;
+          CHECK(p.first[0] == 0 && p.first[p.n_ctas] == p.n_units * p.n_kv_heads);
+          for (int i = 0; i < p.n_ctas; ++i) CHECK(p.first[i] < p.first[i + 1]);
+          for (int i = 0; i < p.first[p.n_ctas]; ++i) CHECK(p.list[i] < p.n_units * p.n_kv_heads && once.insert(p.list[i]).second);
+          ++listed;
+        }
+      }
       CHECK(p.n_units <= P::kMaxUnits && p.n_ctas >= 1 && p.n_ctas <= max_ctas && plan.cuts < kMaxCtas);
       std::map<std::pair<int, int>, std::pair<int, int>> pieces;  // (unit, head) -> (first CTA, pieces) where cut
       int tile = 0;
@@ -136,6 +145,8 @@ static int check(int batches, bool many) {
         Pos t = locate(p, x0);
         const int end = x1 < p.total_len ? locate(p, x1).tile : p.total_tiles;
         CHECK(t.tile == tile && end > tile);
+        CHECK(p.start[cta].tile == t.tile && p.start[cta].j == t.j && p.start[cta].unit_head == (t.unit | t.head << 16) &&
+              p.start[cta + 1].tile == end);
         for (bool fresh_seg = t.j == 0; tile < end; ++tile) {
           CHECK(t.unit < p.n_units && t.head < p.n_kv_heads);
           const auto& u = p.unit[t.unit];
@@ -206,6 +217,6 @@ static int check(int batches, bool many) {
 int main(int argc, char** argv) {
   const int batches = argc > 1 ? std::atoi(argv[1]) : 300;
   if (check<WindowParams>(batches, false) || check<PromptParams>(batches, true)) return 1;
-  std::printf("mismatches %lld\n", bad);
-  return bad != 0;
+  std::printf("mismatches %lld, %lld launches of whole segments\n", bad, listed);
+  return bad != 0 || listed == 0;
 }
