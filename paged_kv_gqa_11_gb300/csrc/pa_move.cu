@@ -92,38 +92,45 @@ __device__ __forceinline__ Packed get(const uint8_t* row, const Lane& at) {
   return Packed{make_uint4(w.x, w.y, 0u, 0u), *reinterpret_cast<const uint16_t*>(row + at.scale)};
 }
 
-// The eight values of lane l that x holds.
+// The eight values of lane l that x holds, in pairs.
 template <int T>
-__device__ __forceinline__ void values(const Packed& x, int l, float (&y)[8]) {
+__device__ __forceinline__ void values(const Packed& x, int l, uint64_t (&y)[4]) {
   if (T == PA_F16) {
-    unpack8<__half>(&x.w, y);
+    float f[8];
+    unpack8<__half>(&x.w, f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = pack2(f[2 * i], f[2 * i + 1]);
     return;
   }
   const float d = __half2float(__ushort_as_half((unsigned short)x.d));
+  const uint64_t d2 = pack2(d, d);
+  // bytes 0 .. 255 under 0x4b0000 are the fp32 numbers 2^23 + byte
+  const float bias = T == PA_Q8_0 ? -8388736.f : -8388616.f;  // -(2^23 + 128), -(2^23 + 8)
+  const uint64_t b2 = pack2(bias, bias);
   const uint32_t w[2] = {x.w.x, x.w.y};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    // bytes 0 .. 255 under 0x64 are the binary16 numbers 1024 + byte
     const uint32_t u = T == PA_Q8_0 ? w[i] ^ 0x80808080u : (w[i] >> ((l & 2) << 1)) & 0x0f0f0f0fu;
-    const uint32_t bias = T == PA_Q8_0 ? 0xe480e480u : 0xe408e408u;  // -1152, -1032
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t h = hadd2(prmt(u, 0x64646464u, k ? 0x4342 : 0x4140), bias);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      y[4 * i + 2 * k] = f.x * d;
-      y[4 * i + 2 * k + 1] = f.y * d;
-    }
+    for (int k = 0; k < 2; ++k)
+      y[2 * i + k] = mul2(add2(pack2(__uint_as_float(prmt(u, 0x4b000000u, k ? 0x7442 : 0x7440)),
+                                     __uint_as_float(prmt(u, 0x4b000000u, k ? 0x7443 : 0x7441))),
+                               b2),
+                          d2);
   }
 }
 
 // A head's row turned by t: its turned blocks quantised anew, the others as they are.
 template <int T>
 __device__ __forceinline__ Packed turned(const MoveParams& p, const Packed& x, const Turn& t, int from, int lane) {
-  float a[8], b[8];
+  uint64_t a[4], b[4];
   values<T>(x, lane, a);
   if (p.interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = a[i ^ 1];
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpack2(a[i]);
+      b[i] = pack2(v.y, v.x);
+    }
   } else {
     Packed o;
     o.w.x = __shfl_sync(0xffffffffu, x.w.x, from);
@@ -133,22 +140,31 @@ __device__ __forceinline__ Packed turned(const MoveParams& p, const Packed& x, c
     o.d = T == PA_F16 ? 0u : __shfl_sync(0xffffffffu, x.d, from);
     values<T>(o, from, b);
   }
-  const bool mine = is_turned(p.rot, lane);
+  float y[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 v = unpack2(fma2(pack2(a[2 * i], a[2 * i + 1]), t.c[i], mul2(pack2(b[2 * i], b[2 * i + 1]), t.s[i])));
-    a[2 * i] = mine ? v.x : a[2 * i];
-    a[2 * i + 1] = mine ? v.y : a[2 * i + 1];
+    const float2 v = unpack2(fma2(a[i], t.c[i], mul2(b[i], t.s[i])));
+    y[2 * i] = v.x;
+    y[2 * i + 1] = v.y;
   }
-  const Packed q = quantised(T, a, lane);
+  if ((p.rot & 16) && !is_turned(p.rot, lane)) {  // the second half of the last turned block
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpack2(a[i]);
+      y[2 * i] = v.x;
+      y[2 * i + 1] = v.y;
+    }
+  }
+  __syncwarp();
+  const Packed q = quantised(T, y, lane);
   return 32 * (lane >> 2) < p.rot ? q : x;
 }
 
-__device__ __forceinline__ Turn turn_of(const MoveParams& p, const uint64_t* from_turns, const uint64_t* to_turns, const Move& m, int lane,
-                                        int from) {
+__device__ __forceinline__ Turn turn_of(const MoveParams& p, const uint64_t* from_turns, const uint64_t* to_turns, int src_pos, int dst_pos,
+                                        int lane, int from) {
   return make_turn(
       p.rot, p.interleaved, p.factor,
-      [&](int i) { return (uint64_t)(int64_t)m.dst_pos * to_turns[i] - (uint64_t)(int64_t)m.src_pos * from_turns[i]; }, lane, from);
+      [&](int i) { return (uint64_t)(int64_t)dst_pos * to_turns[i] - (uint64_t)(int64_t)src_pos * from_turns[i]; }, lane, from);
 }
 
 // A row between its places in the pools: at ws, heads one after the other, each its chunks,
@@ -161,45 +177,98 @@ __device__ __forceinline__ Lane lane_in_ws(int type, int lane) {
 
 enum Phase { kDirect, kGather, kScatter };
 
-// The heads of one row of one pool.
+// Four heads of a row on their way: where they come from and go to.
+struct Ends {
+  const uint8_t* src;
+  uint8_t* dst;
+  Lane a, b;
+};
+
 template <int T, int kPhase>
-__device__ __forceinline__ void move_heads(const MoveParams& p, uint8_t* pool, bool is_v, const Move& m, uint8_t* ws, const Turn* t,
-                                           int from, int lane) {
-  const long long step = (long long)p.page_size * Fmt<T>::kRow;
-  const uint8_t* src = kPhase == kScatter ? ws : pool + m.src * Fmt<T>::kRow;
-  uint8_t* dst = kPhase == kGather ? ws : pool + m.dst * Fmt<T>::kRow;
-  const long long src_step = kPhase == kScatter ? Fmt<T>::kRow : step, dst_step = kPhase == kGather ? Fmt<T>::kRow : step;
-  const Lane a = kPhase == kScatter ? lane_in_ws(T, lane) : lane_of(T, is_v, m.src_r, lane),
-             b = kPhase == kGather ? lane_in_ws(T, lane) : lane_of(T, is_v, m.dst_r, lane);
-  for (int h = 0; h < p.n_heads; h += 4) {
-    Packed x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (h + i < p.n_heads) x[i] = get<T>(src + (h + i) * src_step, a);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (h + i >= p.n_heads) break;
-      if (kPhase != kScatter && t) x[i] = turned<T>(p, x[i], *t, from, lane);
-      put(T, x[i], dst + (h + i) * dst_step, b, lane);
-    }
-  }
+__device__ __forceinline__ Ends ends_of(const MoveParams& p, uint8_t* pool, bool is_v, const Move& m, uint8_t* ws, int lane) {
+  Ends e;
+  e.src = kPhase == kScatter ? ws : pool + m.src * Fmt<T>::kRow;
+  e.dst = kPhase == kGather ? ws : pool + m.dst * Fmt<T>::kRow;
+  e.a = kPhase == kScatter ? lane_in_ws(T, lane) : lane_of(T, is_v, m.src_r, lane);
+  e.b = kPhase == kGather ? lane_in_ws(T, lane) : lane_of(T, is_v, m.dst_r, lane);
+  return e;
 }
 
-template <int kPhase>
-__device__ __forceinline__ void move_row(const MoveParams& p, bool is_v, const Move& m, long long row, const uint64_t* from_turns,
-                                         const uint64_t* to_turns, int lane) {
-  const bool turns = !is_v && m.turned;
-  if (!m.ok || (m.same && !turns)) return;
-  const int type = is_v ? p.v_type : p.k_type, from = partner_lane(p.rot, p.interleaved, lane);
+// A warp's rows of one pool, the next four heads' loads (of the row, or of the next row) before the
+// last ones are worked on.
+template <int T, int kPhase>
+__device__ __forceinline__ void move_rows_of(const MoveParams& p, bool is_v, const Move& moves, int rows, long long row0, const uint64_t* from_turns,
+                                             const uint64_t* to_turns, int lane) {
+  const long long step = (long long)p.page_size * Fmt<T>::kRow;
+  const long long src_step = kPhase == kScatter ? Fmt<T>::kRow : step, dst_step = kPhase == kGather ? Fmt<T>::kRow : step;
   uint8_t* pool = is_v ? p.v_pool : p.k_pool;
   const long long k_row = (long long)p.n_heads * row_bytes_of(p.k_type), v_row = (long long)p.n_heads * row_bytes_of(p.v_type);
-  uint8_t* ws = kPhase == kDirect ? nullptr : p.ws + (is_v ? p.n_rows * k_row + row * v_row : row * k_row);
+  const int from = partner_lane(p.rot, p.interleaved, lane);
+  const int quads = (p.n_heads + 3) >> 2;
+  // the rows that have something to do
+  const bool turns_mine = !is_v && moves.turned;
+  uint32_t todo = __ballot_sync(0xffffffffu, lane < rows && moves.ok && !(moves.same && !turns_mine));
+  if (kPhase != kScatter) {  // the first eight rows' first four heads are on their way at once: lane = (row, head)
+    const int r = lane >> 2, h = lane & 3;
+    const long long src = __shfl_sync(0xffffffffu, moves.src, r);
+    const int src_r = __shfl_sync(0xffffffffu, moves.src_r, r);
+    if (todo >> r & 1 && h < p.n_heads) {
+      const uint8_t* grp = pool + src * Fmt<T>::kRow + h * step;
+#pragma unroll
+      for (int i = 0; i < Fmt<T>::kRowQ; i += 128)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(grp + Fmt<T>::kScales + src_r * Fmt<T>::kRowQ + i));
+    }
+  }
+  Ends next{};
+  Packed ahead[4] = {};
+  int next_row = -1, next_quad = 0;
+  Move next_move{};
+  auto fetch = [&]() {  // the next four heads
+    if (next_row >= 0 && ++next_quad < quads) {
+    } else {
+      if (todo == 0) {
+        next_row = -1;
+        return;
+      }
+      next_row = __ffs(todo) - 1;
+      todo &= todo - 1;
+      next_quad = 0;
+      next_move = from_lane(moves, next_row);
+      const long long row = row0 + next_row;
+      next = ends_of<T, kPhase>(p, pool, is_v, next_move, kPhase == kDirect ? nullptr : p.ws + (is_v ? p.n_rows * k_row + row * v_row : row * k_row), lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * next_quad + i < p.n_heads) ahead[i] = get<T>(next.src + (4 * next_quad + i) * src_step, next.a);
+  };
+  fetch();
   Turn t;
-  if (kPhase != kScatter && turns) t = turn_of(p, from_turns, to_turns, m, lane, from);
-  const Turn* tp = turns ? &t : nullptr;
-  if (type == PA_F16) move_heads<PA_F16, kPhase>(p, pool, is_v, m, ws, tp, from, lane);
-  else if (type == PA_Q8_0) move_heads<PA_Q8_0, kPhase>(p, pool, is_v, m, ws, tp, from, lane);
-  else move_heads<PA_Q4_0, kPhase>(p, pool, is_v, m, ws, tp, from, lane);
+  int turned_row = -1, turned_by = 0;
+  while (next_row >= 0) {
+    Packed x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = ahead[i];
+    uint8_t* dst = next.dst;
+    const Lane b = next.b;
+    const int row = next_row, h = 4 * next_quad;
+    const bool turn = kPhase != kScatter && !is_v && next_move.turned;
+    const int src_pos = next_move.src_pos, dst_pos = next_move.dst_pos;
+    fetch();
+    if (turn && turned_row != row) {
+      const int by = dst_pos - src_pos;  // positions are 0 and more
+      if (turned_row < 0 || !p.still || by != turned_by) t = turn_of(p, from_turns, to_turns, src_pos, dst_pos, lane, from);
+      turned_row = row;
+      turned_by = by;
+    }
+    // heads that are not there are turned all the same: nothing stands between the four
+    if (turn) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = turned<T>(p, x[i], t, from, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (h + i < p.n_heads) put(T, x[i], dst + (h + i) * dst_step, b, lane);
+  }
 }
 
 __device__ __forceinline__ void load_turns(const MoveParams& p, uint64_t* from_turns, uint64_t* to_turns) {
@@ -216,18 +285,22 @@ __global__ void __launch_bounds__(32 * kWarps) pa_move_kernel(const __grid_const
   __shared__ uint64_t from_turns[kMaxPairs], to_turns[kMaxPairs];
   const int lane = threadIdx.x & 31;
   load_turns(p, from_turns, to_turns);
-  const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const long long row0 = (item >> 1) * p.rows;
+  // K's rows first, V's in CTAs of their own: where keys are turned in place those have nothing to do
+  const long long half = gridDim.x >> 1;
+  const bool is_v = blockIdx.x >= half;
+  const long long row0 = ((long long)(blockIdx.x - (is_v ? half : 0)) * kWarps + (threadIdx.x >> 5)) * p.rows;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing that another kernel wrote is read before this
   if (row0 >= p.n_rows) return;
-  const bool is_v = item & 1;
   const int rows = (int)min((long long)p.rows, p.n_rows - row0);
   Move m{};
   if (lane < rows) {
     m = move_of(p, row0 + lane);
     if (!m.ok && !is_v && kPhase != kScatter) record_error(p.err, PA_ERR_BOUNDS);
   }
-  for (int i = 0; i < rows; ++i) move_row<kPhase>(p, is_v, from_lane(m, i), row0 + i, from_turns, to_turns, lane);
+  const int type = is_v ? p.v_type : p.k_type;
+  if (type == PA_F16) move_rows_of<PA_F16, kPhase>(p, is_v, m, rows, row0, from_turns, to_turns, lane);
+  else if (type == PA_Q8_0) move_rows_of<PA_Q8_0, kPhase>(p, is_v, m, rows, row0, from_turns, to_turns, lane);
+  else move_rows_of<PA_Q4_0, kPhase>(p, is_v, m, rows, row0, from_turns, to_turns, lane);
 }
 
 // Few rows: every warp of a cluster reads up to kItems (row, pool, four heads), all warps
@@ -235,18 +308,18 @@ __global__ void __launch_bounds__(32 * kWarps) pa_move_kernel(const __grid_const
 constexpr int kItems = 4, kSmallWarps = 16, kMaxCluster = 8;
 
 template <int T>
-__device__ __forceinline__ void read_item(const MoveParams& p, const uint8_t* pool, bool is_v, const Move& m, int h0, const Turn* t,
-                                          int from, int lane, Packed (&x)[4]) {
+__device__ __forceinline__ void read_item(const MoveParams& p, const uint8_t* pool, bool is_v, const Move& m, int h0, bool turns,
+                                          const Turn& t, int from, int lane, Packed (&x)[4]) {
   const long long step = (long long)p.page_size * Fmt<T>::kRow;
   const uint8_t* src = pool + m.src * Fmt<T>::kRow + h0 * step;
   const Lane a = lane_of(T, is_v, m.src_r, lane);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (h0 + i < p.n_heads) x[i] = get<T>(src + i * step, a);
-  if (t) {
+  if (turns) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (h0 + i < p.n_heads) x[i] = turned<T>(p, x[i], *t, from, lane);
+      if (h0 + i < p.n_heads) x[i] = turned<T>(p, x[i], t, from, lane);
   }
 }
 
@@ -276,13 +349,12 @@ __global__ void __launch_bounds__(32 * kSmallWarps) pa_move_few_kernel(const __g
     dst[k] = m.dst;
     dst_r[k] = m.dst_r;
     Turn t;
-    if (turns) t = turn_of(p, from_turns, to_turns, m, lane, from);
-    const Turn* tp = turns ? &t : nullptr;
+    if (turns) t = turn_of(p, from_turns, to_turns, m.src_pos, m.dst_pos, lane, from);
     const int type = is_v ? p.v_type : p.k_type;
     const uint8_t* pool = is_v ? p.v_pool : p.k_pool;
-    if (type == PA_F16) read_item<PA_F16>(p, pool, is_v, m, h0, tp, from, lane, x[k]);
-    else if (type == PA_Q8_0) read_item<PA_Q8_0>(p, pool, is_v, m, h0, tp, from, lane, x[k]);
-    else read_item<PA_Q4_0>(p, pool, is_v, m, h0, tp, from, lane, x[k]);
+    if (type == PA_F16) read_item<PA_F16>(p, pool, is_v, m, h0, turns, t, from, lane, x[k]);
+    else if (type == PA_Q8_0) read_item<PA_Q8_0>(p, pool, is_v, m, h0, turns, t, from, lane, x[k]);
+    else read_item<PA_Q4_0>(p, pool, is_v, m, h0, turns, t, from, lane, x[k]);
   }
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 #pragma unroll
@@ -531,7 +603,7 @@ extern "C" pa_status pa_move_rows(const pa_pool* pool, void* k_pool, void* v_poo
   pa_status st = sm_count(&sms);
   if (st != PA_OK) return st;
   p.rows = (int)std::min<long long>(8, (2ll * n_rows + 32ll * sms - 1) / (32ll * sms));  // 1 while warps are few
-  const long long grid = (((long long)n_rows + p.rows - 1) / p.rows * 2 + kWarps - 1) / kWarps;
+  const long long grid = 2 * ((((long long)n_rows + p.rows - 1) / p.rows + kWarps - 1) / kWarps);
   if (grid > 0x7fffffffll) return PA_ERR_UNSUPPORTED;
   if (disjoint) return launch(pa_move_kernel<kDirect>, p, (unsigned)grid, cs);
   st = launch(pa_move_kernel<kGather>, p, (unsigned)grid, cs);
