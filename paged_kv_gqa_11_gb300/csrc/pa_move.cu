@@ -164,7 +164,13 @@ __device__ __forceinline__ Turn turn_of(const MoveParams& p, const uint64_t* fro
                                         int lane, int from) {
   return make_turn(
       p.rot, p.interleaved, p.factor,
-      [&](int i) { return (uint64_t)(int64_t)dst_pos * to_turns[i] - (uint64_t)(int64_t)src_pos * from_turns[i]; }, lane, from);
+      [&](int i) {  // the upper half of both products is all that the angle has (positions are 0 and more)
+        const uint64_t b = to_turns[i], a = from_turns[i];
+        const uint32_t hb = (uint32_t)dst_pos * (uint32_t)(b >> 32) + __umulhi((uint32_t)dst_pos, (uint32_t)b);
+        const uint32_t ha = (uint32_t)src_pos * (uint32_t)(a >> 32) + __umulhi((uint32_t)src_pos, (uint32_t)a);
+        return (uint64_t)(hb - ha) << 32;
+      },
+      lane, from);
 }
 
 // A row between its places in the pools: at ws, heads one after the other, each its chunks,
@@ -449,7 +455,8 @@ bool is_few(long long n_rows, int n_heads) {
 
 pa_status launch_few(const MoveParams& p, cudaStream_t cs) {
   const long long items = p.n_rows * 2 * ((p.n_heads + 3) / 4);
-  const unsigned ctas = (unsigned)((items + kItems * kSmallWarps - 1) / (kItems * kSmallWarps));
+  // an item to a warp while the cluster has room: a warp's items follow one another's loads
+  const unsigned ctas = (unsigned)std::min<long long>(kMaxCluster, (items + kSmallWarps - 1) / kSmallWarps);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
