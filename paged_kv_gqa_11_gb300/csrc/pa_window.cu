@@ -12,6 +12,7 @@
 #include "pa_io.cuh"
 #include "pa_merge.cuh"
 #include "pa_prompt.cuh"
+#include "pa_step.cuh"
 #include "pa_window_impl.cuh"
 
 using namespace pa_dev;
@@ -71,9 +72,14 @@ __global__ void __launch_bounds__(64 * kMergeRows) pa_window_merge_kernel(const 
 
 // ------------------------------------------------------------------ host side
 
-bool lookup_kernel(int kt, int vt, WindowKernel* out) {
+struct Kernels {  // of a (K format, V format) pair
+  WindowKernel few;
+  StepKernel step;
+};
+
+bool lookup_kernels(int kt, int vt, Kernels* out) {
 #define PA_PAIR(k, v) \
-  if (kt == k && vt == v) return lookup_window_kernel_##k##_##v(out);
+  if (kt == k && vt == v) return lookup_window_kernel_##k##_##v(&out->few) && lookup_step_kernel_##k##_##v(&out->step);
   PA_PAIR(1, 1) PA_PAIR(1, 2) PA_PAIR(1, 8)
   PA_PAIR(2, 1) PA_PAIR(2, 2) PA_PAIR(2, 8)
   PA_PAIR(8, 1) PA_PAIR(8, 2) PA_PAIR(8, 8)
@@ -90,7 +96,7 @@ bool g_ready[kMaxDevices][3][3];  // the kernels' shared-memory limits are raise
 
 // CTAs of a launch on the device (one per SM), and, with a kernel, its limit raised there
 // (the device must be current for that).
-pa_status device_ready(int device, int kt, int vt, const WindowKernel* ki, int* ctas) {
+pa_status device_ready(int device, int kt, int vt, const Kernels* ki, int* ctas) {
   if (device < 0 || device >= kMaxDevices) return PA_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_sms[device] == 0) {
@@ -101,7 +107,8 @@ pa_status device_ready(int device, int kt, int vt, const WindowKernel* ki, int* 
   *ctas = std::min(g_sms[device], kMaxCtas);
   if (ki) {
     bool& r = g_ready[device][type_slot(kt)][type_slot(vt)];
-    if (!r && (cudaFuncSetAttribute(ki->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ki->smem) != cudaSuccess ||
+    if (!r && (cudaFuncSetAttribute(ki->few.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ki->few.smem) != cudaSuccess ||
+               (ki->step.fn && cudaFuncSetAttribute(ki->step.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ki->step.smem) != cudaSuccess) ||
                prompt_ready() != PA_OK))
       return PA_ERR_CUDA;
     r = true;
@@ -119,6 +126,7 @@ struct Batch {
   uint32_t most;        // new tokens of the largest sequence of few
   uint32_t prompts;     // sequences of many
   int64_t groups;       // row groups of their keys
+  int64_t keys, longest;  // keys that the sequences of few read, and the longest's
   bool many(uint32_t s) const { return is_many(n_new[s]); }
   static bool is_many(int32_t n) { return n >= kPromptTokens; }
 };
@@ -126,7 +134,7 @@ struct Batch {
 pa_status check_batch(const pa_pool_desc& d, uint64_t max_len, Batch* b) {
   b->tokens = 0;
   b->most = b->prompts = 0;
-  b->groups = 0;
+  b->groups = b->keys = b->longest = 0;
   for (uint32_t i = 0; i < b->n_seq; ++i) {
     const int64_t len = b->lens[i], n = b->n_new[i];
     if (n < 0 || len < n || len > (int64_t)max_len) return PA_ERR_INVALID;
@@ -141,6 +149,9 @@ pa_status check_batch(const pa_pool_desc& d, uint64_t max_len, Batch* b) {
       b->groups += seq_span((int)len, (int)n, b->window, b->sinks).groups;
     } else {
       b->most = std::max(b->most, (uint32_t)n);
+      const int64_t seen = std::min<int64_t>(len, (int64_t)b->window + (int64_t)b->sinks + n - 1);
+      b->keys += seen;
+      b->longest = std::max(b->longest, seen);
     }
   }
   return b->tokens > 0x7fffffffu || b->groups > 0x7fffffff / 16 ? PA_ERR_UNSUPPORTED : PA_OK;
@@ -255,7 +266,7 @@ Plan plan_chunk(P& p, MergeParams& m, const Batch& b, bool many, int max_ctas, C
 // Every launch is a programmatic dependent of what runs before it on the stream: its set-up
 // overlaps the other's tail, and it waits for it before it reads.
 struct Launch {
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
   explicit Launch(cudaStream_t cs) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -285,6 +296,42 @@ pa_status launch_merge(const MergeParams& m, const Plan& plan, int max_ctas, cud
                      : wide == 2 ? pa_window_merge_kernel<2>
                                  : pa_window_merge_kernel<1>;
   return cudaLaunchKernelEx(&l.cfg, merge, m) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// CTAs of a segment of pa_step_kernel, or 0: the batch is the other kernel's.  The step kernel is taken where its
+// CTAs, two to an SM, fill four fifths of the device in each wave, no sequence has more than 5/4 of the mean
+// keys, and a segment has 128 keys for each CTA of its cluster and each wave (one wave of clusters of one: any number);
+// pa_step_impl.cuh has both sides' times.
+int step_cluster(const Batch& b, int sms) {
+  if (b.most != 1 || b.prompts) return 0;
+  const int64_t tokens = (int64_t)b.tokens, slots = 2 * sms;
+  if (b.longest * tokens > b.keys + b.keys / 4) return 0;
+  for (int c = 8; c >= 1; c /= 2) {
+    const int64_t n = tokens * b.heads * c, waves = (n + slots - 1) / slots;
+    if ((waves > 1 && c > 1) || n * 5 < waves * slots * 4) continue;
+    return waves * c == 1 || b.longest >= 128 * c * waves ? c : 0;
+  }
+  return 0;
+}
+
+// One token per sequence: kMaxStepSeqs sequences to a launch, a cluster to each of their heads.
+pa_status launch_steps(StepParams& p, const Batch& b, const StepKernel& ki, cudaStream_t cs) {
+  for (uint32_t s = 0, token = 0; s < b.n_seq;) {
+    int n = 0;
+    for (; s < b.n_seq && n < kMaxStepSeqs; ++s)
+      if (b.n_new[s]) p.seq[n++] = StepSeq{(int32_t)s, (int32_t)token++, b.lens[s]};
+    if (n == 0) break;
+    Launch l(cs);
+    l.attr[1].id = cudaLaunchAttributeClusterDimension;
+    l.attr[1].val.clusterDim.x = (unsigned)p.cluster;
+    l.attr[1].val.clusterDim.y = l.attr[1].val.clusterDim.z = 1;
+    l.cfg.numAttrs = 2;
+    l.cfg.gridDim = dim3((unsigned)(n * p.n_kv_heads * p.cluster));
+    l.cfg.blockDim = dim3(kStepThreads);
+    l.cfg.dynamicSmemBytes = (size_t)ki.smem;
+    if (cudaLaunchKernelEx(&l.cfg, ki.fn, p) != cudaSuccess) return PA_ERR_CUDA;
+  }
+  return PA_OK;
 }
 
 // The keys of the batch's sequences of many tokens into the workspace.
@@ -369,9 +416,9 @@ bool list_segments(PromptParams& p, const Plan& plan) {
   return true;
 }
 
-pa_status check_pool(const pa_pool* pool, pa_pool_desc* d, WindowKernel* ki) {
+pa_status check_pool(const pa_pool* pool, pa_pool_desc* d, Kernels* ki) {
   if (!pool || pa_pool_get_desc(pool, d) != PA_OK) return PA_ERR_INVALID;
-  return d->head_dim == (uint32_t)kD && d->n_kv_heads <= 0x7fff && lookup_kernel(d->k_type, d->v_type, ki) ? PA_OK : PA_ERR_UNSUPPORTED;
+  return d->head_dim == (uint32_t)kD && d->n_kv_heads <= 0x7fff && lookup_kernels(d->k_type, d->v_type, ki) ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
 // The window as the kernels take it: at most as long as any sequence.
@@ -379,26 +426,51 @@ int clamp_keys(uint32_t n) { return (int)std::min<uint32_t>(n, kAllKeys); }
 
 // What both kernels' parameters, and the merge's, have in common.
 template <class P>
-void fill(P& p, MergeParams& m, const Batch& b, const pa_pool_desc& d, const void* q, int64_t q_stride, int32_t q_type,
-          const int32_t* lens_dev, float scale, void* out, int64_t out_stride, int32_t out_type, float* lse, uint8_t* ws, size_t ml,
-          size_t o, int slot_rows, int32_t* err) {
+void fill(P& p, const Batch& b, const pa_pool_desc& d, const void* q, int64_t q_stride, int32_t q_type, const int32_t* lens_dev, float scale,
+          void* out, int64_t out_stride, int32_t out_type, float* lse, int32_t* err) {
   p.q = static_cast<const uint8_t*>(q);
-  p.lens = m.lens = lens_dev;
-  p.err = m.err = err;
-  m.part_ml = p.part_ml = reinterpret_cast<float2*>(ws + ml);
-  m.part_o = p.part_o = reinterpret_cast<float*>(ws + o);
-  p.out = m.out = static_cast<uint8_t*>(out);
-  p.lse = m.lse = lse;
+  p.lens = lens_dev;
+  p.err = err;
+  p.out = static_cast<uint8_t*>(out);
+  p.lse = lse;
   p.q_stride = q_stride;
-  p.out_stride = m.out_stride = out_stride;
+  p.out_stride = out_stride;
   p.q_type = q_type;
-  p.out_type = m.out_type = out_type;
+  p.out_type = out_type;
   p.n_kv_heads = (int)d.n_kv_heads;
-  p.n_q_heads = m.n_q_heads = (int)d.n_kv_heads * kGqa;
+  p.n_q_heads = (int)d.n_kv_heads * kGqa;
   p.window = b.window;
   p.sinks = b.sinks;
-  p.slot_rows = m.slot_rows = slot_rows;
   p.scale_log2 = scale * kLog2e;
+}
+
+// The same with the parts of cut segments, and the merge's parameters.
+template <class P>
+void fill_parts(P& p, MergeParams& m, uint8_t* ws, size_t ml, size_t o, int slot_rows) {
+  m.lens = p.lens;
+  m.err = p.err;
+  m.part_ml = p.part_ml = reinterpret_cast<float2*>(ws + ml);
+  m.part_o = p.part_o = reinterpret_cast<float*>(ws + o);
+  m.out = p.out;
+  m.lse = p.lse;
+  m.out_stride = p.out_stride;
+  m.out_type = p.out_type;
+  m.n_q_heads = p.n_q_heads;
+  m.slot_rows = p.slot_rows = slot_rows;
+}
+
+// The pools as the kernels that read them take them.
+template <class P>
+void fill_pools(P& p, const pa_pool_desc& d, const void* k_pool, const void* v_pool, const int32_t* table, uint32_t table_stride) {
+  p.k_pool = static_cast<const uint8_t*>(k_pool);
+  p.v_pool = static_cast<const uint8_t*>(v_pool);
+  p.table = table;
+  p.page_size = (int)d.page_size;
+  p.page_shift = -1;
+  for (int i = 4; i < 31; ++i)
+    if (d.page_size == 1u << i) p.page_shift = i;
+  p.table_stride = (int)table_stride;
+  p.n_blocks = (int)d.n_blocks;
 }
 
 }  // namespace
@@ -406,7 +478,7 @@ void fill(P& p, MergeParams& m, const Batch& b, const pa_pool_desc& d, const voi
 extern "C" size_t pa_attend_window_workspace_size(const pa_pool* pool, const int32_t* seq_lens_host, const int32_t* n_new,
                                                   uint32_t n_seq, uint32_t window, uint32_t sinks, int device) {
   pa_pool_desc d;
-  WindowKernel ki;
+  Kernels ki;
   int ctas = 0;
   if (check_pool(pool, &d, &ki) != PA_OK || (n_seq && (!seq_lens_host || !n_new))) return 0;
   Batch b{seq_lens_host, n_new, n_seq, clamp_keys(window ? window : ~0u), clamp_keys(sinks), (int)d.n_kv_heads};
@@ -421,7 +493,7 @@ extern "C" pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_
                                       void* out, int64_t out_stride, int32_t out_type, float* lse, void* workspace,
                                       size_t ws_bytes, int32_t* err, pa_stream_t stream) {
   pa_pool_desc d;
-  WindowKernel ki;
+  Kernels ki;
   pa_status st = check_pool(pool, &d, &ki);
   if (st != PA_OK) return st;
   if ((uint64_t)n_q_heads != (uint64_t)d.n_kv_heads * kGqa) return PA_ERR_UNSUPPORTED;
@@ -453,31 +525,31 @@ extern "C" pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   static thread_local MergeParams m;  // kept off the stack
+  if (const int cluster = ki.step.fn ? step_cluster(b, ctas) : 0) {
+    static thread_local StepParams p;
+    fill(p, b, d, q, q_stride, q_type, seq_lens_dev, scale, out, out_stride, out_type, lse, err);
+    fill_pools(p, d, k_pool, v_pool, block_table, table_stride);
+    p.cluster = cluster;
+    return launch_steps(p, b, ki.step, cs);
+  }
   // Launches in order on the stream, sharing the workspace: each one's kernel waits for the
   // one before to complete.
   if (b.most > 0) {
     static thread_local WindowParams p;
-    fill(p, m, b, d, q, q_stride, q_type, seq_lens_dev, scale, out, out_stride, out_type, lse, ws, 0, lay.o, slot_rows_of(b.most), err);
-    p.k_pool = static_cast<const uint8_t*>(k_pool);
-    p.v_pool = static_cast<const uint8_t*>(v_pool);
-    p.table = block_table;
-    p.page_size = (int)d.page_size;
-    p.page_shift = -1;
-    for (int i = 4; i < 31; ++i)
-      if (d.page_size == 1u << i) p.page_shift = i;
-    p.table_stride = (int)table_stride;
-    p.n_blocks = (int)d.n_blocks;
+    fill(p, b, d, q, q_stride, q_type, seq_lens_dev, scale, out, out_stride, out_type, lse, err);
+    fill_parts(p, m, ws, 0, lay.o, slot_rows_of(b.most));
+    fill_pools(p, d, k_pool, v_pool, block_table, table_stride);
     for (Cursor at{0, 0, 0}; at.seq < n_seq;) {
       const Plan plan = plan_chunk(p, m, b, false, ctas, &at);
       if (p.n_units == 0) break;
-      if ((st = launch_few(p, ki, cs)) != PA_OK || (st = launch_merge(m, plan, ctas, cs)) != PA_OK) return st;
+      if ((st = launch_few(p, ki.few, cs)) != PA_OK || (st = launch_merge(m, plan, ctas, cs)) != PA_OK) return st;
     }
   }
   if (b.prompts > 0) {
     static thread_local PromptParams p;
     static thread_local PrepareParams r;
-    fill(p, m, b, d, q, q_stride, q_type, seq_lens_dev, scale, out, out_stride, out_type, lse, ws, lay.prompt_ml, lay.prompt_o, kPromptRows,
-         err);
+    fill(p, b, d, q, q_stride, q_type, seq_lens_dev, scale, out, out_stride, out_type, lse, err);
+    fill_parts(p, m, ws, lay.prompt_ml, lay.prompt_o, kPromptRows);
     p.k = r.k = ws + lay.k;
     p.v = r.v = ws + lay.v;
     p.wide = r.wide = d.k_type == PA_F16 ? nullptr : ws + lay.wide;

@@ -410,3 +410,169 @@ def test_prompts_repeat_bit_for_bit():
         torch.cuda.synchronize()
         assert torch.equal(y, ref)
     assert cache.check() == PA_OK
+
+
+# One new token per sequence in batches that fill the device, K Q8_0: clusters of 1, 2, 4 and 8 CTAs, several waves and launches.
+STEPS = [(64, 1, 0), (64, 16, 1), (64, 17, 0), (70, 64, 5), (76, 100, 16), (61, 33, 40), (64, 1000, 130), (33, 500, 4), (16, 600, 17),
+         (8, 1030, 0), (8, 1500, 3), (300, 540, 3)]
+
+
+def step_batch(seqs, window, sinks, vt, seed=1, ps=48):
+    """Sequences longer than the window by less than it takes for one to stand out, and one without a new token."""
+    lens = [max(1, window) + sinks + (37 * i) % 90 for i in range(seqs)]
+    return window_batch(lens + [20], [1] * seqs + [0], ps, Q8, vt, seed=seed), [1] * seqs + [0]
+
+
+@pytest.mark.parametrize("vt", [Q4, Q8])
+@pytest.mark.parametrize("seqs,window,sinks", STEPS)
+def test_steps(seqs, window, sinks, vt):
+    w, n_new = step_batch(seqs, window, sinks, vt, seed=seqs + window)
+    against_definition(w, n_new, window, sinks, torch.bfloat16 if vt == Q4 else torch.float16, what=f"{seqs} x {window}, {sinks}")
+
+
+def test_steps_without_a_window():
+    """Idle sequences between the others, lengths from 60 to 70."""
+    n_new = [i % 5 != 3 for i in range(85)]
+    w = window_batch([60 + i % 11 for i in range(85)], n_new, 16, Q8, Q8)
+    against_definition(w, n_new, 0, 0)
+    w = window_batch([1] * 64, [1] * 64, 16, Q8, Q4)
+    against_definition(w, [1] * 64, 0, 0, torch.float16)
+
+
+@pytest.mark.parametrize("ot", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("qt", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("seqs", [64, 16])
+def test_steps_types_strides_and_rows_behind_the_last_sequence(seqs, qt, ot):
+    w, n_new = step_batch(seqs, 700, 4, Q4)
+    cache, tab = device_cache(w)
+    x = torch.full((seqs + 5, 32, 256), float("nan"), device="cuda").to(qt)
+    x[:seqs, :24] = to_dev(w.q).to(qt)
+    big = torch.full((seqs + 5, 30, 256), 7.0, device="cuda").to(ot)
+    lse = torch.full((seqs + 5, 24), 7.0, device="cuda")
+    out, _ = attend(w, n_new, 700, 4, cache=cache, tab=tab, q=x[:, :24], out=big[:, 3:27], lse=lse)
+    plain, plain_lse = attend(w, n_new, 700, 4, cache=cache, tab=tab, q=to_dev(w.q).to(qt), out=torch.empty(seqs, 24, 256, device="cuda"))
+    assert torch.equal(out[:seqs], plain.to(ot)) and torch.equal(lse[:seqs], plain_lse)
+    assert (out[seqs:] == 7).all() and (lse[seqs:] == 7).all() and (big[:, :3] == 7).all() and (big[:, 27:] == 7).all()
+
+
+@pytest.mark.parametrize("seqs,window,sinks", [(64, 100, 5), (33, 301, 0), (16, 600, 17), (64, 1, 0)])
+@pytest.mark.parametrize("vt", [Q4, Q8])
+def test_steps_and_what_no_token_sees(seqs, window, sinks, vt):
+    w, n_new = step_batch(seqs, window, sinks, vt, ps=16)
+    cache, tab = device_cache(w)
+    want, want_lse = attend(w, n_new, window, sinks, cache=cache, tab=tab)
+    k, v = w.k_rows.copy(), w.v_rows.copy()
+    holes, row = w.table.copy(), 0
+    for i, length in enumerate(w.seq_lens):
+        x = np.arange(length)
+        unseen = ~((x >= length - window) | (x < sinks)) if n_new[i] else x >= 0
+        for rows, size in ((k, 34), (v, 34 if vt == Q8 else 18)):
+            part = rows[row: row + length]
+            for b in range(8):  # scales that are infinite or NaN
+                part[unseen, :, size * b] = 0
+                part[unseen, :, size * b + 1] = 0x7c | (b & 1) << 1
+        seen_pages = {int(p) // 16 for p in x[~unseen]}
+        for p in range(holes.shape[1]):
+            if p not in seen_pages:
+                holes[i, p] = [-1, 2 ** 31 - 1, w.n_blocks][p % 3]
+        row += length
+    bad = W.Workload(w.name, w.seq_lens, 1, 16, w.n_blocks, Q8, vt, w.table, k, v, w.q, w.scale)
+    cache, _ = device_cache(bad)
+    out, lse = attend(w, n_new, window, sinks, cache=cache, tab=to_dev(holes))
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("seqs,window", [(64, 150), (16, 600)])
+def test_steps_with_bad_entries_and_lengths(seqs, window):
+    w, n_new = step_batch(seqs, window, 0, Q8, ps=16)
+    cache, tab = device_cache(w)
+    want, want_lse = attend(w, n_new, window, 0, cache=cache, tab=tab)
+    lens, nn, q = w.seq_lens.copy(), np.array(n_new, np.int32), to_dev(w.q)
+    lens[5] -= 1
+    out, lse = cache.attend_window(q, tab, to_dev(lens), w.seq_lens, nn, window, 0, w.scale)
+    torch.cuda.synchronize()
+    assert cache.check() == PA_ERR_BOUNDS and cache.check() == PA_OK
+    keep = torch.arange(seqs, device="cuda") != 5
+    assert (out[5] == 0).all() and (lse[5] == -float("inf")).all()
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
+    for entry in (-1, w.n_blocks, 2 ** 31 - 1):
+        holes = w.table.copy()
+        page = int(w.seq_lens[7] - 40) // 16
+        holes[7, page] = entry  # 16 rows of zeros
+        out, lse = cache.attend_window(q, to_dev(holes), to_dev(w.seq_lens), w.seq_lens, nn, window, 0, w.scale)
+        torch.cuda.synchronize()
+        assert cache.check() == PA_ERR_BOUNDS and cache.check() == PA_OK
+        k, v = w.k_rows.copy(), w.v_rows.copy()
+        at = int(w.seq_lens[:7].sum()) + 16 * page
+        k[at: at + 16] = 0
+        v[at: at + 16] = 0
+        zero = W.Workload(w.name, w.seq_lens, 1, 16, w.n_blocks, Q8, Q8, w.table, k, v, w.q, w.scale)
+        ref, ref_lse = attend64(zero, n_new, window, 0)
+        assert_close(out.cpu().numpy(), ref)
+        assert_lse_close(lse.cpu().numpy(), ref_lse)
+
+
+@pytest.mark.parametrize("seqs,window", [(64, 300), (16, 600)])
+@pytest.mark.parametrize("size", [100.0, 60000.0])
+def test_steps_with_large_logits(seqs, window, size):
+    """Later keys that raise a warp's reference until what came before is nothing, very negative first ones, keys past binary16."""
+    w, n_new = step_batch(seqs, window, 4, Q4, ps=16)
+    rng = np.random.default_rng(4)
+    x = np.sign(rng.standard_normal((len(w.k_rows), 4, 256))).astype(np.float32) * (size / 60000.0)
+    ends = np.cumsum(w.seq_lens)
+    for s in range(seqs):  # one large key somewhere in the window, in others all but it very negative
+        at = ends[s] - 1 - (s * 29) % window
+        if s % 3 == 2:
+            x[ends[s] - w.seq_lens[s]: ends[s]] = -size / 2000.0
+        x[at] = size / 2000.0
+    k = W.encode_rows(x, Q8)
+    w = W.Workload(w.name, w.seq_lens, 1, 16, w.n_blocks, Q8, Q4, w.table, k, w.v_rows, np.abs(w.q), w.scale)
+    against_definition(w, n_new, window, 4, torch.float16)
+    scales = k.reshape(len(k), 4, 8, 34)[..., :2].copy().view(np.float16)
+    scales[:] = 60000  # quants up to 127: keys of 7.6 10^6
+    k.reshape(len(k), 4, 8, 34)[..., :2] = scales.view(np.uint8).reshape(len(k), 4, 8, 2)
+    q = np.sign(w.q).astype(np.float32) * 2.0 ** -20
+    w = W.Workload(w.name, w.seq_lens, 1, 16, w.n_blocks, Q8, Q4, w.table, k, w.v_rows, q, w.scale)
+    against_definition(w, n_new, window, 4)
+
+
+def test_steps_past_the_queries_range():
+    """Queries past binary16's range give NaN in their rows, and there alone."""
+    w, n_new = step_batch(64, 100, 0, Q8)
+    cache, tab = device_cache(w)
+    q = to_dev(w.q).clone()
+    want, want_lse = attend(w, n_new, 100, 0, cache=cache, tab=tab, q=q)
+    q[3, 7, 200] = 70000.0
+    q[3, 23, 1] = float("inf")
+    q[60, 0, 255] = float("nan")
+    out, lse = attend(w, n_new, 100, 0, cache=cache, tab=tab, q=q)
+    hit = torch.zeros(64, 24, dtype=torch.bool, device="cuda")
+    hit[3, 7] = hit[3, 23] = hit[60, 0] = True
+    assert out[hit].isnan().all() and lse[hit].isnan().all()
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+
+
+def test_steps_streams_graphs_and_repeats():
+    w, n_new = step_batch(33, 600, 4, Q4)
+    cache, tab = device_cache(w)
+    q, sl, nn = to_dev(w.q).half(), to_dev(w.seq_lens), np.array(n_new, np.int32)
+    call = lambda q, **kw: cache.attend_window(q, tab, sl, w.seq_lens, nn, 600, 4, w.scale, **kw)  # noqa: E731
+    want, want_lse = call(q)
+    q2 = q.flip(0).contiguous()
+    want2, _ = call(q2)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    res = [(i, call(q2 if i % 2 else q, stream=streams[i % 2])[0]) for i in range(6)]
+    torch.cuda.synchronize()
+    for i, r in res:
+        assert torch.equal(r, want2 if i % 2 else want)
+    g = torch.cuda.CUDAGraph()
+    x = q.clone()
+    with torch.cuda.graph(g):
+        y, _ = call(x)
+    for src, ref in ((q, want), (q2, want2), (q, want)):
+        x.copy_(src)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, ref)
+    assert cache.check() == PA_OK

@@ -214,9 +214,44 @@ static int check(int batches, bool many) {
   return 0;
 }
 
+// The rule for pa_step_kernel: a cluster that its launch may have, the device well filled, never for other batches.
+int check_steps() {
+  struct Step {
+    int n_seq, keys, want;
+  };
+  const Step steps[] = {{64, 1, 1}, {64, 1024, 1}, {76, 64, 1}, {77, 4096, 0}, {60, 64, 0}, {33, 512, 2}, {33, 255, 0}, {16, 512, 4}, {16, 511, 0},
+                        {8, 1024, 8}, {8, 1023, 0}, {7, 4096, 0}, {1, 30000, 0}, {128, 256, 1}, {128, 255, 0}, {300, 512, 1}};
+  int batch = 0;
+  for (const Step& t : steps) {
+    ++batch;
+    std::vector<int32_t> lens(t.n_seq + 2, t.keys), n_new(t.n_seq + 2, 1);
+    lens[0] = 9, n_new[0] = 0;
+    n_new[t.n_seq + 1] = 0;
+    auto cluster = [&](int window) {
+      Batch b{lens.data(), n_new.data(), (uint32_t)lens.size(), clamp_keys(window ? window : ~0u), 0, 4};
+      pa_pool_desc d = {};
+      d.n_kv_heads = 4;
+      CHECK(check_batch(d, ~0u, &b) == PA_OK);
+      return step_cluster(b, 152);
+    };
+    CHECK(cluster(0) == t.want);
+    for (int i = 1; i <= t.n_seq; ++i) lens[i] += 7000 + i;  // a window makes sequences of different lengths equal
+    CHECK(cluster(t.keys) == t.want);
+    if (t.n_seq > 1) {
+      lens[1] += 20000;
+      CHECK(cluster(0) == 0);
+    }
+    n_new[1] = 2;
+    CHECK(cluster(t.keys) == 0);
+    n_new[1] = kPromptTokens;
+    CHECK(cluster(t.keys) == 0);
+  }
+  return 0;
+}
+
 int main(int argc, char** argv) {
   const int batches = argc > 1 ? std::atoi(argv[1]) : 300;
-  if (check<WindowParams>(batches, false) || check<PromptParams>(batches, true)) return 1;
+  if (check_steps() || check<WindowParams>(batches, false) || check<PromptParams>(batches, true)) return 1;
   std::printf("mismatches %lld, %lld launches of whole segments\n", bad, listed);
   return bad != 0 || listed == 0;
 }
