@@ -10,16 +10,18 @@
 // the third is multiplied by mma.sync:
 //   S (16 keys x 8 rows) = K Q^T: per block of 32 dims two MMAs of exact quants, then the block's scale in
 //                          fp32 on the four results: K is not rounded;
-//   O (dims x 8 rows)   += V^T P^T: V by transposing ldmatrix, scaled in binary16; P^T by movmatrix.
+//   O (dims x 8 rows)   += V^T P^T: V by transposing ldmatrix, scaled in binary16; P^T by movmatrix, in two parts
+//                          of binary16, so that only V is rounded (the second product is hidden: 29.1 and 29.2 us
+//                          without and with it).
 // The order of a contraction is free, so a thread's piece of K is whole words as they lie in the row,
 // and Q's fragments take the same order.  Two of the eight rows are idle.  A warp's and then a
 // cluster's states are joined in shared memory by log-sum-exp, in a fixed order: one launch, no workspace.
 //
-// What bounds it: a group is 800 instructions of dependent steps, 0.8 us for a warp that has its scheduler to
+// What bounds it: a group is 850 instructions of dependent steps, 0.8 us for a warp that has its scheduler to
 // itself; two CTAs on an SM hide each other's.  Eight warps to a CTA, one CTA on an SM, were slower
 // (64 sequences, 1024 keys: 41.8 against 31.4 us).  With K Q8_0, this kernel against the kernel of few
-// tokens, in us (sequences x keys): 64 x 64 7.8 / 11.0, 64 x 1024 31.5 / 43.3, 32 x 512 14.0 / 17.2, 16 x 4096
-// 32.2 / 37.5, 8 x 32768 93.1 / 104.5 (0.90 of the copy bandwidth), 256 x 512 75.6 / 86.0.  Short shares of
+// tokens, in us (sequences x keys, V Q8_0): 64 x 64 7.8 / 11.0, 64 x 1024 31.1 / 43.3, 32 x 512 13.9 / 17.2, 16 x 4096
+// 32.1 / 37.5, 8 x 32768 93.5 / 104.5 (0.90 of the copy bandwidth), 256 x 512 75.0 / 86.0.  Short shares of
 // a cluster lose (32 x 128 9.5 / 7.7, 8 x 512 10.0 / 9.6, 128 x 128 in two waves 18.2 / 16.6), Q4_0 keys gain
 // little (64 x 1024 32.8 / 33.8) and F16 ones lose (57.7 / 51.6: one CTA on an SM), so step_cluster
 // (pa_window.cu) has the rule and only pairs with K Q8_0 and quantised V have the kernel.
@@ -110,7 +112,7 @@ __device__ __forceinline__ void step_scores(uint32_t grp, const uint32_t (&q)[32
 // O += V^T P^T: tile i of O is dims 16 i + 2 g (c0, c1) and + 1 (c2, c3), rows
 // 2t, 2t + 1.  la, lb: live keys among the pairs (2t, 2t + 1) and + 8, as masks.
 template <int VT>
-__device__ __forceinline__ void step_values(uint32_t grp, float (&o)[16][4], uint32_t b0, uint32_t b1, uint32_t la, uint32_t lb, int lane) {
+__device__ __forceinline__ void step_values(uint32_t grp, float (&o)[16][4], const uint32_t (&b)[4], uint32_t la, uint32_t lb, int lane) {
   const int mi = lane >> 3, r = (mi & 1) * 8 + (lane & 7), r7 = lane & 7, t = lane & 3;
   const uint32_t row = grp + Fmt<VT>::kScales + r * Fmt<VT>::kRowQ;
 #pragma unroll
@@ -120,16 +122,21 @@ __device__ __forceinline__ void step_values(uint32_t grp, float (&o)[16][4], uin
     if constexpr (VT == PA_Q8_0) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int b = 2 * j + e;
+        const int blk = 2 * j + e;
         uint32_t x[4];
-        ldsm_x4_trans(row + (((2 * b + (mi >> 1)) ^ r7) << 4), x);
+        ldsm_x4_trans(row + (((2 * blk + (mi >> 1)) ^ r7) << 4), x);
+        uint32_t a[2][4];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {  // chunk 2 b + k: bytes 0, 2 are dim 2 g of a key pair, 1, 3 dim 2 g + 1
+        for (int k = 0; k < 2; ++k) {  // chunk 2 blk + k: bytes 0, 2 are dim 2 g of a key pair, 1, 3 dim 2 g + 1
           const uint32_t u = x[2 * k] ^ 0x80808080u, v = x[2 * k + 1] ^ 0x80808080u;
-          const uint32_t a[4] = {hmul2(step_q8(u, 0x4240), da[e]), hmul2(step_q8(u, 0x4341), da[e]), hmul2(step_q8(v, 0x4240), db[e]),
-                                 hmul2(step_q8(v, 0x4341), db[e])};
-          mma_16816(o[2 * b + k], a, b0, b1);
+          a[k][0] = hmul2(step_q8(u, 0x4240), da[e]);
+          a[k][1] = hmul2(step_q8(u, 0x4341), da[e]);
+          a[k][2] = hmul2(step_q8(v, 0x4240), db[e]);
+          a[k][3] = hmul2(step_q8(v, 0x4341), db[e]);
+          mma_16816(o[2 * blk + k], a[k], b[0], b[1]);
         }
+        mma_16816(o[2 * blk], a[0], b[2], b[3]);
+        mma_16816(o[2 * blk + 1], a[1], b[2], b[3]);
       }
     } else {
       uint32_t x[4];
@@ -145,8 +152,10 @@ __device__ __forceinline__ void step_values(uint32_t grp, float (&o)[16][4], uin
                                 hmul2(hfma2(and_or(u8, 0x00f000f0u, 0x64006400u), kR16, kM72), da[e]),
                                 hmul2(hfma2(and_or(v, 0x00f000f0u, 0x64006400u), kR16, kM72), db[e]),
                                 hmul2(hfma2(and_or(v8, 0x00f000f0u, 0x64006400u), kR16, kM72), db[e])};
-        mma_16816(o[2 * (2 * j + e)], lo, b0, b1);
-        mma_16816(o[2 * (2 * j + e) + 1], hi, b0, b1);
+        mma_16816(o[2 * (2 * j + e)], lo, b[0], b[1]);
+        mma_16816(o[2 * (2 * j + e) + 1], hi, b[0], b[1]);
+        mma_16816(o[2 * (2 * j + e)], lo, b[2], b[3]);
+        mma_16816(o[2 * (2 * j + e) + 1], hi, b[2], b[3]);
       }
     }
   }
@@ -172,7 +181,7 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t addr, uint32_t cta) {
 }
 
 template <int VT>
-__global__ void __launch_bounds__(kStepThreads) pa_step_kernel(const __grid_constant__ StepParams p) {
+__global__ void __launch_bounds__(kStepThreads, 2) pa_step_kernel(const __grid_constant__ StepParams p) {
   using SM = StepSmem<VT>;
   constexpr int NS = SM::kStages;
   extern __shared__ __align__(1024) uint8_t step_smem[];
@@ -283,8 +292,15 @@ __global__ void __launch_bounds__(kStepThreads) pa_step_kernel(const __grid_cons
     for (int k = 0; k < 4; ++k) s[k] = ex2(s[k]);
     l[0] += s[0] + s[2];
     l[1] += s[1] + s[3];
-    const uint32_t b0 = movmatrix_trans(pack_half2(s[0], s[1])), b1 = movmatrix_trans(pack_half2(s[2], s[3]));
-    step_values<VT>(grp + SM::kK, o, b0, b1, la, lb, lane);
+    uint32_t b[4];  // P in two parts of binary16
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t hi = pack_half2(s[2 * k], s[2 * k + 1]);
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+      b[k] = movmatrix_trans(hi);
+      b[2 + k] = movmatrix_trans(pack_half2(s[2 * k] - x.x, s[2 * k + 1] - x.y));
+    }
+    step_values<VT>(grp + SM::kK, o, b, la, lb, lane);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
