@@ -347,7 +347,7 @@ pa_status pa_move_rows(const pa_pool* pool, void* k_pool, void* v_pool, const pa
                        pa_stream_t stream);
 
 /* Scratch bytes pa_move_rows needs for n_rows rows that are not disjoint: 0 while they are few
- * (256 rows of 4 KV heads), else as many as the rows have. */
+ * (64 rows of 4 KV heads), else as many as the rows have. */
 size_t pa_move_rows_workspace_size(const pa_pool* pool, uint32_t n_rows);
 
 /* ------------------------------------------------------------------ decode
@@ -558,15 +558,17 @@ size_t pa_decode_prefix_workspace_size(const pa_pool* pool, uint32_t n_seq, uint
  * workspace: ws_bytes >= pa_attend_window_workspace_size(), 256-byte aligned; contents as
  *           pa_decode's.
  *
- * Precision and range: as pa_decode_prefix, whose arithmetic it is.  An infinite or NaN
+ * Precision and range: as pa_decode_prefix, whose arithmetic it is (single tokens of large
+ * batches with Q8_0 keys lose less: K and P are not rounded there).  An infinite or NaN
  * value of V (a stored one past 65504 is infinite) in a row that one of the tokens
- * sees can also reach others of the same sequence that do not see it (those up to 40
+ * sees can also reach others of the same sequence that do not see it (those up to 64
  * tokens away); in a row that none of them sees it has no effect, and K's never have.
  *
- * Launches: one for the sequences of fewer than 64 new tokens (448 times 64 query rows at a
- * time), and a merge when a (64 query rows, KV head) is shared by CTAs; for those of more,
- * one that turns their keys into binary16, and one over 256 times 128 query rows at a
- * time, with its merge.  All are programmatic dependent launches (pa_decode). */
+ * Launches: one for the sequences of fewer than 64 new tokens (448 times 64 query rows, or 256
+ * single tokens, at a time), and a merge when a (64 query rows, KV head) is shared by
+ * CTAs; for those of more, one that turns their keys into binary16 (128 sequences at a time),
+ * and one over 256 times 256 query rows at a time, with a merge when one of these is shared.  All are
+ * programmatic dependent launches (pa_decode). */
 pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_t q_stride, int32_t q_type, const void* k_pool,
                            const void* v_pool, const int32_t* block_table, uint32_t table_stride,
                            const int32_t* seq_lens_dev, const int32_t* seq_lens_host, const int32_t* n_new,

@@ -8,12 +8,19 @@
 // again by the rule of the append; all other bytes of a row stay what they are.
 //
 // Rows that land where others still have to be read: all reads come before all writes.  Few
-// rows stay in the registers of one cluster of CTAs between the two (its hardware barrier
+// rows (64 of 4 heads) stay in the registers of one cluster of CTAs between the two (its hardware barrier
 // is the only thing between them: one launch); more go through the workspace, in the pools'
 // formats, by two launches.  Where the caller vouches that no row's place is another row's
 // source, one launch reads and writes at once.
 //
-// Bound: the memory.  A warp moves a row's heads four at a time, all loads first.
+// Bound: the memory, where keys keep their bytes or rows are many; a turned key costs 300 instructions
+// a head (dequantised, turned, its maximum found, quantised), which a warp hides by having the
+// next four heads' loads on their way.  K's rows and V's are in CTAs of their own, so that rows
+// turned in place do not leave every second warp idle.  Measured, one GB300: 24 rows 3.4 us (one launch),
+// 12000 rows of Q8_0 down by 777, 64 values turned (two launches) 28.5, 65536 rows of Q8_0 keys turned in place
+// (all 256 values, 2.0 TB/s read and written: the arithmetic) 70.6; with rows of both pools in one
+// warp and no loads ahead 138.  Partly turned heads packed so that a warp turns only their blocks
+// were slower (more registers, 154, and more shuffles than the arithmetic that they saved).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -309,9 +316,10 @@ __global__ void __launch_bounds__(32 * kWarps) pa_move_kernel(const __grid_const
   else move_rows_of<PA_Q4_0, kPhase>(p, is_v, m, rows, row0, from_turns, to_turns, lane);
 }
 
-// Few rows: every warp of a cluster reads up to kItems (row, pool, four heads), all warps
-// meet, every warp writes.
-constexpr int kItems = 4, kSmallWarps = 16, kMaxCluster = 8;
+// Few rows: every warp of a cluster reads a (row, pool, four heads), all warps meet, every warp
+// writes.  Of rows of 4 heads in Q8_0: 24 rows 5.5 us; the others' two launches 6.9.  More than one
+// item to a warp, its loads one after the other, are slower than those (100 rows 9.2, 256 16.8).
+constexpr int kSmallWarps = 16, kMaxCluster = 8;
 
 template <int T>
 __device__ __forceinline__ void read_item(const MoveParams& p, const uint8_t* pool, bool is_v, const Move& m, int h0, bool turns,
@@ -329,60 +337,50 @@ __device__ __forceinline__ void read_item(const MoveParams& p, const uint8_t* po
   }
 }
 
-__global__ void __launch_bounds__(32 * kSmallWarps) pa_move_few_kernel(const __grid_constant__ MoveParams p) {
+__global__ void __launch_bounds__(32 * kSmallWarps, 1) pa_move_few_kernel(const __grid_constant__ MoveParams p) {
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
   __shared__ uint64_t from_turns[kMaxPairs], to_turns[kMaxPairs];
   const int lane = threadIdx.x & 31, from = partner_lane(p.rot, p.interleaved, lane);
   load_turns(p, from_turns, to_turns);
-  const int quads = (p.n_heads + 3) / 4, warp = (int)blockIdx.x * kSmallWarps + (threadIdx.x >> 5), warps = (int)gridDim.x * kSmallWarps;
+  const int quads = (p.n_heads + 3) / 4, item = (int)blockIdx.x * kSmallWarps + (threadIdx.x >> 5);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing that another kernel wrote is read before this
-  const int items = (int)p.n_rows * 2 * quads;
-  Packed x[kItems][4];
-  long long dst[kItems];
-  int dst_r[kItems];
-  uint32_t go = 0;  // items that are written
-#pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    const int item = warp + k * warps;
-    if (item >= items) break;
-    const int row = item / (2 * quads), rest = item - row * 2 * quads, h0 = 4 * (rest >> 1);
-    const bool is_v = rest & 1;
-    const Move m = move_of(p, row);
+  const int row = item / (2 * quads), rest = item - row * 2 * quads, h0 = 4 * (rest >> 1);
+  const bool is_v = rest & 1;
+  const int type = is_v ? p.v_type : p.k_type;
+  uint8_t* const pool = is_v ? p.v_pool : p.k_pool;
+  Packed x[4];
+  Move m{};
+  bool go = false;
+  if (row < (int)p.n_rows) {
+    m = move_of(p, row);
     if (!m.ok && rest == 0 && lane == 0) record_error(p.err, PA_ERR_BOUNDS);
     const bool turns = !is_v && m.turned;
-    if (!m.ok || (m.same && !turns)) continue;
-    go |= 1u << k;
-    dst[k] = m.dst;
-    dst_r[k] = m.dst_r;
-    Turn t;
-    if (turns) t = turn_of(p, from_turns, to_turns, m.src_pos, m.dst_pos, lane, from);
-    const int type = is_v ? p.v_type : p.k_type;
-    const uint8_t* pool = is_v ? p.v_pool : p.k_pool;
-    if (type == PA_F16) read_item<PA_F16>(p, pool, is_v, m, h0, turns, t, from, lane, x[k]);
-    else if (type == PA_Q8_0) read_item<PA_Q8_0>(p, pool, is_v, m, h0, turns, t, from, lane, x[k]);
-    else read_item<PA_Q4_0>(p, pool, is_v, m, h0, turns, t, from, lane, x[k]);
+    go = m.ok && (turns || !m.same);
+    if (go) {
+      Turn t;
+      if (turns) t = turn_of(p, from_turns, to_turns, m.src_pos, m.dst_pos, lane, from);
+      if (type == PA_F16) read_item<PA_F16>(p, pool, is_v, m, h0, turns, t, from, lane, x);
+      else if (type == PA_Q8_0) read_item<PA_Q8_0>(p, pool, is_v, m, h0, turns, t, from, lane, x);
+      else read_item<PA_Q4_0>(p, pool, is_v, m, h0, turns, t, from, lane, x);
+    }
   }
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (!go) return;
+  const long long rb = row_bytes_of(type), step = (long long)p.page_size * rb;
+  uint8_t* to = pool + m.dst * rb + h0 * step;
+  const Lane b = lane_of(type, is_v, m.dst_r, lane);
 #pragma unroll
-  for (int k = 0; k < kItems; ++k) {
-    if (!(go >> k & 1)) continue;
-    const int item = warp + k * warps, rest = item % (2 * quads), h0 = 4 * (rest >> 1);
-    const bool is_v = rest & 1;
-    const int type = is_v ? p.v_type : p.k_type;
-    const long long rb = row_bytes_of(type), step = (long long)p.page_size * rb;
-    uint8_t* to = (is_v ? p.v_pool : p.k_pool) + dst[k] * rb + h0 * step;
-    const Lane b = lane_of(type, is_v, dst_r[k], lane);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (h0 + i < p.n_heads) put(type, x[k][i], to + i * step, b, lane);
-  }
+  for (int i = 0; i < 4; ++i)
+    if (h0 + i < p.n_heads) put(type, x[i], to + i * step, b, lane);
 }
 
 // ------------------------------------------------------------------ blocks
 
 // Whole blocks (every KV head's page, K and V) from src[i] to dst[i], and the tables' entries
 // src[i] as dst[i].  Chunks of 16 KB, 64 bytes a thread in flight; behind them the
-// tables' entries, each found in src (ascending) by bisection.
+// tables' entries, each found in src (ascending) by bisection.  Bound: HBM (5000 blocks
+// of 64 rows, Q8_0 / Q4_0: 182 us, 5.9 TB/s read and written; 40 blocks of 16 rows: 2.1).
 struct BlockParams {
   uint8_t* k_pool;
   uint8_t* v_pool;
@@ -449,14 +447,11 @@ __global__ void __launch_bounds__(kBlockThreads) pa_move_blocks_kernel(const __g
 // ------------------------------------------------------------------ host side
 
 // Rows that one cluster moves at once.
-bool is_few(long long n_rows, int n_heads) {
-  return n_rows * 2 * ((n_heads + 3) / 4) <= (long long)kItems * kSmallWarps * kMaxCluster;
-}
+bool is_few(long long n_rows, int n_heads) { return n_rows * 2 * ((n_heads + 3) / 4) <= kSmallWarps * kMaxCluster; }
 
 pa_status launch_few(const MoveParams& p, cudaStream_t cs) {
   const long long items = p.n_rows * 2 * ((p.n_heads + 3) / 4);
-  // an item to a warp while the cluster has room: a warp's items follow one another's loads
-  const unsigned ctas = (unsigned)std::min<long long>(kMaxCluster, (items + kSmallWarps - 1) / kSmallWarps);
+  const unsigned ctas = (unsigned)((items + kSmallWarps - 1) / kSmallWarps);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

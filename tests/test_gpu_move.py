@@ -50,7 +50,7 @@ PAIRS = [(F16, F16), (Q4, Q8), (Q8, Q4), (F16, Q4)]
 
 
 @pytest.mark.parametrize("kt,vt", PAIRS)
-@pytest.mark.parametrize("rows", [1, 5, 255, 256, 257, 900])
+@pytest.mark.parametrize("rows", [1, 5, 63, 64, 65, 256, 900])
 @pytest.mark.parametrize("by", [1, 3, 16, 700])
 def test_rows_moved_down_over_one_another(kt, vt, rows, by):
     """Few rows (one cluster) and many (through the workspace), by less than a row group and more."""
