@@ -35,7 +35,14 @@
 //
 // Ranges, cuts and slots are those of pa_window_impl.cuh, with units of 256 rows and ranges of
 // pairs; or, where that is no longer than with cuts and their merge, every pair has whole
-// segments, the largest dealt first, each to the pair with least.
+// segments, the largest dealt first, each to the pair with least (4096 tokens, no window: 147 us
+// against 167; 2048 tokens, window 1024: 59 against 67).
+//
+// Measured: 4096 tokens without a window in F16 147 us (1402 TFLOP/s of the 206 GFLOP that are not
+// masked, 0.71 of cuBLAS's burst rate); 2048 tokens, window 1024, Q8_0 / Q4_0 59 us, of which 6 for
+// the keys' launch.  What bounds it: inside a piece of 32 tiles a tile takes 1250 cycles for 1024 of
+// MMA, the rest the softmax's 64 exponentials a thread and its hand-offs; each piece costs 40 / 8 of
+// a tile more, for its first S, its last PV and the results.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

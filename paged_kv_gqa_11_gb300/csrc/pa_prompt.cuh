@@ -64,7 +64,8 @@ struct PromptParams {
 };
 
 // What a piece takes, and a tile; and the cuts of a launch (a merge, and rows in fp32 by way of the
-// workspace) in the same places, 0.15 us each.
+// workspace) in the same places, 0.15 us each.  4096 tokens without a window, cut: a lead of 4 308 us, 16 237, 32 and
+// 40 167, 48 176.
 constexpr int kPromptLead = 40, kPromptTile = 8, kPromptMerge = 70;
 __host__ __device__ __forceinline__ Cost cost_of(const PromptParams& p, const Unit&) {
   return p.weigh ? Cost{kPromptLead, kPromptTile} : Cost{0, 1};

@@ -1,7 +1,8 @@
 // Attention over a sliding window and first keys: the plan, the merge of the segments that
 // are cut, and the host side of pa_attend_window.  The kernel over the keys for sequences with few
 // new tokens is in pa_window_impl.cuh and pa_prefix_impl.cuh, compiled once per (K format,
-// V format) pair; the kernels for those with many are in pa_prompt.cu.
+// V format) pair, that for large batches of single tokens in pa_step_impl.cuh, the kernels for
+// sequences with many tokens in pa_prompt.cu.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -24,7 +25,11 @@ namespace {
 constexpr int64_t kMaxLen = 0x7fffffff - 2 * kKeys;  // a tile past the last key is still a 32-bit number
 constexpr uint32_t kMaxNew = 1u << 24;               // new tokens of a sequence
 constexpr int64_t kMaxPlaces = 1ll << 30;
-constexpr int32_t kPromptTokens = 64;  // sequences of so many new tokens or more are the prompts' kernel's
+// Sequences of so many new tokens or more are the prompts' kernel's (Q8_0, 4 sequences of 4096 keys, 32 tokens
+// 45.8 us by the kernel of few, 64 tokens 75.7 by the prompts', 77.4 by the dense shared-prefix kernel with
+// nothing shared, whose arithmetic the kernel of few has; 2048 tokens, window 1024: 161 and 59).  The
+// prompts' kernel turns the keys into binary16 first, which fewer tokens do not pay for.
+constexpr int32_t kPromptTokens = 64;
 
 // ------------------------------------------------------------------ merge
 
@@ -126,7 +131,7 @@ struct Batch {
   uint32_t most;        // new tokens of the largest sequence of few
   uint32_t prompts;     // sequences of many
   int64_t groups;       // row groups of their keys
-  int64_t keys, longest;  // keys that the sequences of few read, and the longest's
+  int64_t few, keys, longest;  // sequences of few, keys that they read, and the longest's
   bool many(uint32_t s) const { return is_many(n_new[s]); }
   static bool is_many(int32_t n) { return n >= kPromptTokens; }
 };
@@ -134,7 +139,7 @@ struct Batch {
 pa_status check_batch(const pa_pool_desc& d, uint64_t max_len, Batch* b) {
   b->tokens = 0;
   b->most = b->prompts = 0;
-  b->groups = b->keys = b->longest = 0;
+  b->groups = b->few = b->keys = b->longest = 0;
   for (uint32_t i = 0; i < b->n_seq; ++i) {
     const int64_t len = b->lens[i], n = b->n_new[i];
     if (n < 0 || len < n || len > (int64_t)max_len) return PA_ERR_INVALID;
@@ -150,6 +155,7 @@ pa_status check_batch(const pa_pool_desc& d, uint64_t max_len, Batch* b) {
     } else {
       b->most = std::max(b->most, (uint32_t)n);
       const int64_t seen = std::min<int64_t>(len, (int64_t)b->window + (int64_t)b->sinks + n - 1);
+      ++b->few;
       b->keys += seen;
       b->longest = std::max(b->longest, seen);
     }
@@ -298,16 +304,17 @@ pa_status launch_merge(const MergeParams& m, const Plan& plan, int max_ctas, cud
   return cudaLaunchKernelEx(&l.cfg, merge, m) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// CTAs of a segment of pa_step_kernel, or 0: the batch is the other kernel's.  The step kernel is taken where its
+// CTAs of a segment of pa_step_kernel, or 0: the sequences of few tokens are the other kernel's.  The step
+// kernel is taken for single tokens where its
 // CTAs, two to an SM, fill four fifths of the device in each wave, no sequence has more than 5/4 of the mean
 // keys, and a segment has 128 keys for each CTA of its cluster and each wave (one wave of clusters of one: any number);
 // pa_step_impl.cuh has both sides' times.
 int step_cluster(const Batch& b, int sms) {
-  if (b.most != 1 || b.prompts) return 0;
-  const int64_t tokens = (int64_t)b.tokens, slots = 2 * sms;
-  if (b.longest * tokens > b.keys + b.keys / 4) return 0;
+  if (b.most != 1) return 0;
+  const int64_t slots = 2 * sms;
+  if (b.longest * b.few > b.keys + b.keys / 4) return 0;
   for (int c = 8; c >= 1; c /= 2) {
-    const int64_t n = tokens * b.heads * c, waves = (n + slots - 1) / slots;
+    const int64_t n = b.few * b.heads * c, waves = (n + slots - 1) / slots;
     if ((waves > 1 && c > 1) || n * 5 < waves * slots * 4) continue;
     return waves * c == 1 || b.longest >= 128 * c * waves ? c : 0;
   }
@@ -318,8 +325,8 @@ int step_cluster(const Batch& b, int sms) {
 pa_status launch_steps(StepParams& p, const Batch& b, const StepKernel& ki, cudaStream_t cs) {
   for (uint32_t s = 0, token = 0; s < b.n_seq;) {
     int n = 0;
-    for (; s < b.n_seq && n < kMaxStepSeqs; ++s)
-      if (b.n_new[s]) p.seq[n++] = StepSeq{(int32_t)s, (int32_t)token++, b.lens[s]};
+    for (; s < b.n_seq && n < kMaxStepSeqs; token += b.n_new[s++])
+      if (b.n_new[s] == 1) p.seq[n++] = StepSeq{(int32_t)s, (int32_t)token, b.lens[s]};
     if (n == 0) break;
     Launch l(cs);
     l.attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -525,16 +532,15 @@ extern "C" pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   static thread_local MergeParams m;  // kept off the stack
+  // Launches in order on the stream, sharing the workspace: each one's kernel waits for the
+  // one before to complete.
   if (const int cluster = ki.step.fn ? step_cluster(b, ctas) : 0) {
     static thread_local StepParams p;
     fill(p, b, d, q, q_stride, q_type, seq_lens_dev, scale, out, out_stride, out_type, lse, err);
     fill_pools(p, d, k_pool, v_pool, block_table, table_stride);
     p.cluster = cluster;
-    return launch_steps(p, b, ki.step, cs);
-  }
-  // Launches in order on the stream, sharing the workspace: each one's kernel waits for the
-  // one before to complete.
-  if (b.most > 0) {
+    if ((st = launch_steps(p, b, ki.step, cs)) != PA_OK) return st;
+  } else if (b.most > 0) {
     static thread_local WindowParams p;
     fill(p, b, d, q, q_stride, q_type, seq_lens_dev, scale, out, out_stride, out_type, lse, err);
     fill_parts(p, m, ws, 0, lay.o, slot_rows_of(b.most));

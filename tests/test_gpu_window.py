@@ -439,6 +439,16 @@ def test_steps_without_a_window():
     against_definition(w, [1] * 64, 0, 0, torch.float16)
 
 
+def test_steps_beside_prompts():
+    """Single tokens by their kernel, chunks of prompt between them by theirs."""
+    n_new = [1] * 20 + [100] + [1] * 30 + [0, 64] + [1] * 14
+    w = window_batch([150 + i % 9 for i in range(len(n_new))], n_new, 16, Q8, Q8)
+    against_definition(w, n_new, 90, 3, torch.float16)
+    n_new = [200] + [1] * 300
+    w = window_batch([600 if i == 0 else 560 + i % 9 for i in range(301)], n_new, 32, Q8, Q4)
+    against_definition(w, n_new, 540, 0, torch.bfloat16)
+
+
 @pytest.mark.parametrize("ot", [torch.float32, torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("qt", [torch.float32, torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("seqs", [64, 16])

@@ -240,10 +240,12 @@ int check_steps() {
     if (t.n_seq > 1) {
       lens[1] += 20000;
       CHECK(cluster(0) == 0);
+      lens[1] -= 20000;
     }
+    n_new[t.n_seq + 1] = kPromptTokens;  // whatever else the batch holds for other kernels
+    lens[t.n_seq + 1] = 30000;
+    CHECK(cluster(t.keys) == t.want);
     n_new[1] = 2;
-    CHECK(cluster(t.keys) == 0);
-    n_new[1] = kPromptTokens;
     CHECK(cluster(t.keys) == 0);
   }
   return 0;
