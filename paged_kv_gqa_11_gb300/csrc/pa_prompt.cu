@@ -29,7 +29,8 @@
 // Warps, hand-offs on mbarriers, every wait bounded:
 //   0-7    softmax: (half of the keys, lane quarter), thread = row;
 //   8-11   query rows into Q (the first piece's: 0-7), and a finished piece's O to its place;
-//   12     MMA issue (the pair's first CTA; the second's tells it of the second's copies); 13 copies.
+//   12     MMA issue (the pair's first CTA; the second's tells it of the second's copies);
+//   13, 14 copies of K and of V.
 // S of tile j + 1 is multiplied while the softmax of tile j runs, and that of j + 1 while PV of
 // j and S of j + 2 are.
 //
@@ -38,11 +39,13 @@
 // segments, the largest dealt first, each to the pair with least (4096 tokens, no window: 147 us
 // against 167; 2048 tokens, window 1024: 59 against 67).
 //
-// Measured: 4096 tokens without a window in F16 147 us (1402 TFLOP/s of the 206 GFLOP that are not
-// masked, 0.71 of cuBLAS's burst rate); 2048 tokens, window 1024, Q8_0 / Q4_0 59 us, of which 6 for
-// the keys' launch.  What bounds it: inside a piece of 32 tiles a tile takes 1250 cycles for 1024 of
-// MMA, the rest the softmax's 64 exponentials a thread and its hand-offs; each piece costs 40 / 8 of
-// a tile more, for its first S, its last PV and the results.
+// Measured: 4096 tokens without a window in F16 137 us (1504 TFLOP/s of the 206 GFLOP that are not
+// masked, 0.76 of cuBLAS's burst rate); 2048 tokens, window 1024, Q8_0 / Q4_0 57 us, of which 6 for
+// the keys' launch.  What bounds it: the copy engine's 32 bytes a cycle, 2040 cycles for a
+// tile's 64 KB beside 2048 of MMA (each alone runs at its rate, with all other traffic around it); the
+// engine and the MMAs wait for one another through a ring of five stages, 2300 cycles a tile.  A piece's end
+// costs 2 us: its O is read before the next piece's first PV.  V by cp.async (65 bytes a cycle and SM by
+// itself) with a proxy fence before its MMAs was slower (154 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -174,7 +177,7 @@ __global__ void __launch_bounds__(32 * kPrepareWarps, 8) pa_prompt_prepare_kerne
 
 constexpr int kStageBytes = 16384, kNStages = 5;
 constexpr int kCtaRows = kPromptRows / 2;  // rows of a CTA
-constexpr int kPSmWarps = 8, kAuxWarp0 = 8, kMmaWarp = 12, kCopyWarp = 13, kPThreads = 14 * 32;
+constexpr int kPSmWarps = 8, kAuxWarp0 = 8, kMmaWarp = 12, kCopyWarp = 13, kPThreads = 15 * 32;
 constexpr uint32_t kPOCol = 0, kPSCol = 256;
 
 struct PSmem {
@@ -503,20 +506,29 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
   if (w < kPSmWarps) load_queries_end(p, base + SM::kQ, 16 * w, 16 * w + 16, lane);
   cluster_wait();  // and the other's
   int issued = 0;
+  uint32_t slots = 0, parities = 0;  // stages that this warp copied into, and their last use's parity
   Piece x;
 
   if (!whole) {
-  } else if (w == kCopyWarp) {
+  } else if (w >= kCopyWarp) {
     // ---- copies: K(0), then K(j + 1) before V(j); a stage each 128 dims of K (64 keys: the CTA's) or
-    // 64 keys of V (128 dims: the CTA's)
+    // 64 keys of V (128 dims: the CTA's).  One warp copies K and one V, so that one's waits and set-up
+    // overlap the other's copies (a copy of 16 KB holds its warp for 470 cycles; one warp for both takes 2600
+    // cycles a tile, the copy engine alone 2040); both count all stages.  Each waits for its own stages alone,
+    // which means the phase that it says: consecutive ones of a warp are at most three apart, so
+    // when the earlier one's was free all that lie two uses back were.
+    const bool is_k = w == kCopyWarp;
     bool live = true;
-    auto stage = [&](uint32_t bytes) -> int {  // the next stage, once it is free; -1: the wait expired
+    auto stage = [&](bool mine, uint32_t bytes) -> int {  // the next stage, once it is free; -1: the other warp's, or the wait expired
       const int s = issued % kNStages, use = issued / kNStages;
-      if (live && use > 0 && !warp_wait(empty + 8 * s, (use - 1) & 1, p.err, abort)) live = false;
+      if (mine && live && use > 0 && !warp_wait(empty + 8 * s, (use - 1) & 1, p.err, abort)) live = false;
       if (!live) return -1;
+      ++issued;
+      if (!mine) return -1;
+      slots |= 1u << s;
+      parities = (parities & ~(1u << s)) | (uint32_t)(use & 1) << s;
       if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
       __syncwarp();
-      ++issued;
       return s;
     };
     // places v .. end - 1 of a plane: one run of the sequence's groups, or two (sinks, window)
@@ -536,7 +548,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       const uint8_t* k = p.k + ((long long)u.group0 * p.n_kv_heads + (long long)x.head * u.groups) * kGroupBytes;
       const int v = j * kKeys + 64 * (int)rank, end = max(v, min(v + 64, j * kKeys + whole16(tile_keys(s, j))));
       for (int h = 0; h < 2 && live; ++h) {
-        const int st = stage((uint32_t)(end - v) * 256);
+        const int st = stage(is_k, (uint32_t)(end - v) * 256);
         if (st >= 0) copy(u, s, k + (long long)h * u.groups * kPlaneGroup, v, end, st);
       }
     };
@@ -545,14 +557,14 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       const uint8_t* k = p.v + ((long long)u.group0 * p.n_kv_heads + (long long)x.head * u.groups) * kGroupBytes + (long long)rank * u.groups * kPlaneGroup;
       const int v = j * kKeys, n16 = whole16(tile_keys(s, j));
       for (int q = 0; q < n16 && live; q += 64) {
-        const int m = min(64, n16 - q), st = stage((uint32_t)m * 256);
+        const int m = min(64, n16 - q), st = stage(!is_k, (uint32_t)m * 256);
         if (st >= 0) copy(u, s, k, v + q, v + q + m, st);
       }
     };
     bool more = walk.next(p, x);
     Span s = span_of(p.unit[x.unit], p.window, p.sinks);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (lane == 0) asm volatile("griddepcontrol.launch_dependents;");
+    if (is_k && lane == 0) asm volatile("griddepcontrol.launch_dependents;");
     keys(x, s, x.j0);
     while (more && live) {
       for (int j = x.j0; j + 1 < x.j1 && live; ++j) {
@@ -761,17 +773,20 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       const long long reg = (long long)u.group0 * p.n_kv_heads + (long long)x.head * u.groups;
       float ref = 0.f;
       uint64_t l2 = 0;  // sums of weights over this thread's keys, in two
+      // which keys of a tile are wide (all rows': the same), read a tile ahead
+      uint16_t flags[4] = {};
+      auto read_flags = [&](int t) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int v = t * kKeys + 64 * half + 16 * g;
+          flags[g] = p.wide && t < x.j1 && v < s.end ? __ldg(reinterpret_cast<const uint16_t*>(p.wide) + reg + group_of(u, s, v)) : 0;
+        }
+      };
+      read_flags(x.j0);
       for (int t = x.j0; t < x.j1; ++t, ++j) {
         const int v0 = t * kKeys + 64 * half;
-        uint64_t wide = 0;  // of this thread's keys (all rows': the same)
-        if (p.wide) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int v = v0 + 16 * g;
-            if (v < s.end)
-              wide |= (uint64_t)__ldg(reinterpret_cast<const uint16_t*>(p.wide) + reg + group_of(u, s, v)) << (16 * g);
-          }
-        }
+        const uint64_t wide = (uint64_t)(flags[0] | (uint32_t)flags[1] << 16) | (uint64_t)(flags[2] | (uint32_t)flags[3] << 16) << 32;
+        if (p.wide) read_flags(t + 1);
         live = live && warp_wait(s_full + 8 * (j & 1), (j >> 1) & 1, p.err, abort);
         if (!live) leave[j & 1] = 1;
         tc_fence_after();
@@ -880,9 +895,9 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
   tc_fence_before();
   __syncthreads();
   // after an expired wait, copies that nobody waited for must still land
-  if (w == kCopyWarp && *abort) {
-    for (int i = max(0, issued - kNStages); i < issued; ++i)
-      mbar_wait(full + 8 * (i % kNStages), (uint32_t)((i / kNStages) & 1), p.err, abort, false, kWaitTimeoutNs / 8);
+  if (w >= kCopyWarp && *abort) {
+    for (int i = 0; i < kNStages; ++i)
+      if (slots >> i & 1) mbar_wait(full + 8 * i, parities >> i & 1, p.err, abort, false, kWaitTimeoutNs / 8);
   }
   __syncwarp();
   cluster_arrive();

@@ -1,6 +1,6 @@
 """The hand-offs of the prompts' attention kernel when a wait expires, as a model.
 
-The roles of both CTAs of a pair in pa_prompt.cu -- copies, word of the second's copies, MMA issue, query rows and results, softmax -- run as
+The roles of both CTAs of a pair in pa_prompt.cu -- copies of K and of V, word of the second's copies, MMA issue, query rows and results, softmax -- run as
 generators over the kernel's barriers, in random order, with random waits expiring and a
 copy that never lands.  Whatever happens, every role comes to its end (a barrier that only
 some of the softmax warps reach would hold a GPU for good), no wait passes a phase that it does
@@ -53,8 +53,10 @@ def simulate(seed, agree=True):
                 aborted[c] = True
                 return False
 
-    def copy(c):
+    def copy(c, kind):  # a warp's stages: K's or V's
         for i, what in enumerate(order):
+            if what[0] != kind:
+                continue
             s, use = i % STAGES, i // STAGES
             if use and not (yield from wait(empty[c][s], use - 1, c)):
                 return
@@ -211,7 +213,8 @@ def simulate(seed, agree=True):
 
     roles = {"mma": mma(), "forward": forward(), "first rows": first_rows()}
     for c in range(2):
-        roles[f"copy {c}"] = copy(c)
+        for kind in "kv":
+            roles[f"copy {c} {kind}"] = copy(c, kind)
         for a in range(4):
             roles[f"aux {c} {a}"] = aux(c, a)
         for w in range(8):
