@@ -37,15 +37,15 @@
 // Ranges, cuts and slots are those of pa_window_impl.cuh, with units of 256 rows and ranges of
 // pairs; or, where that is no longer than with cuts and their merge, every pair has whole
 // segments, the largest dealt first, each to the pair with least (4096 tokens, no window: 147 us
-// against 167; 2048 tokens, window 1024: 59 against 67).
+// against 167; 2048 tokens, window 1024: 59 against 67; both before K and V had a warp each).
 //
-// Measured: 4096 tokens without a window in F16 137 us (1504 TFLOP/s of the 206 GFLOP that are not
-// masked, 0.76 of cuBLAS's burst rate); 2048 tokens, window 1024, Q8_0 / Q4_0 57 us, of which 6 for
+// Measured: 4096 tokens without a window in F16 140 us (1472 TFLOP/s of the 206 GFLOP that are not
+// masked, 0.75 of cuBLAS's burst rate); 2048 tokens, window 1024, Q8_0 / Q4_0 58 us, of which 6 for
 // the keys' launch.  What bounds it: the copy engine's 32 bytes a cycle, 2040 cycles for a
 // tile's 64 KB beside 2048 of MMA (each alone runs at its rate, with all other traffic around it); the
 // engine and the MMAs wait for one another through a ring of five stages, 2300 cycles a tile.  A piece's end
 // costs 2 us: its O is read before the next piece's first PV.  V by cp.async (65 bytes a cycle and SM by
-// itself) with a proxy fence before its MMAs was slower (154 us).
+// itself) was slower, with a proxy fence before its MMAs (154 us) or in the copying warp (170).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
