@@ -378,9 +378,10 @@ __global__ void __launch_bounds__(32 * kSmallWarps, 1) pa_move_few_kernel(const 
 // ------------------------------------------------------------------ blocks
 
 // Whole blocks (every KV head's page, K and V) from src[i] to dst[i], and the tables' entries
-// src[i] as dst[i].  Chunks of 16 KB, 64 bytes a thread in flight; behind them the
-// tables' entries, each found in src (ascending) by bisection.  Bound: HBM (5000 blocks
-// of 64 rows, Q8_0 / Q4_0: 182 us, 5.9 TB/s read and written; 40 blocks of 16 rows: 2.1).
+// src[i] as dst[i].  All blocks' 16-byte pieces, laid end to end, one to a thread at a time, then the
+// tables' entries, each found in src (ascending) by bisection.  Bound: HBM (5000 blocks of 64 rows, Q8_0 /
+// Q4_0: 164 us, 6.5 TB/s read and written).  2048 threads an SM have as much on its way as
+// the memory takes; 2 or 4 pieces to a thread (fewer fit) took 176 and 185 us, parts of 16 KB inside a block 181.
 struct BlockParams {
   uint8_t* k_pool;
   uint8_t* v_pool;
@@ -389,23 +390,23 @@ struct BlockParams {
   const int32_t* table;
   int32_t* table_out;
   int32_t* err;
-  long long k_bytes, v_bytes;  // of a block
+  long long k_pieces, v_pieces;  // of a block
   long long entries;
-  long long chunks;            // of all pairs
-  int n, k_chunks, v_chunks;   // pairs; chunks of a block
-  int n_blocks;
+  long long pieces, parts;       // of all pairs; parts of kBlockThreads
+  int n, n_blocks;
+  int small;                     // pieces is a 31-bit number
 };
 
-constexpr int kBlockThreads = 256, kChunk = 16 * 4 * kBlockThreads;
+constexpr int kBlockThreads = 256;
 
-__global__ void __launch_bounds__(kBlockThreads) pa_move_blocks_kernel(const __grid_constant__ BlockParams p) {
+__global__ void __launch_bounds__(kBlockThreads, 8) pa_move_blocks_kernel(const __grid_constant__ BlockParams p) {
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing that another kernel wrote is read before this
-  const int per = p.k_chunks + p.v_chunks;
-  const long long parts = p.chunks + (p.entries + kBlockThreads - 1) / kBlockThreads;
+  const long long per = p.k_pieces + p.v_pieces;
+  const long long parts = p.parts + (p.entries + kBlockThreads - 1) / kBlockThreads;
   for (long long part = blockIdx.x; part < parts; part += gridDim.x) {
-    if (part >= p.chunks) {
-      const long long e = (part - p.chunks) * kBlockThreads + threadIdx.x;
+    if (part >= p.parts) {
+      const long long e = (part - p.parts) * kBlockThreads + threadIdx.x;
       if (e >= p.entries) continue;
       const int x = __ldcg(p.table + e);
       int lo = 0, hi = p.n;  // the first pair with src >= x
@@ -421,26 +422,19 @@ __global__ void __launch_bounds__(kBlockThreads) pa_move_blocks_kernel(const __g
       p.table_out[e] = to;
       continue;
     }
-    const long long pair = part / per;
-    const int c = (int)(part - pair * per), cv = c - p.k_chunks;
-    const bool is_v = cv >= 0;
+    const long long i = part * kBlockThreads + threadIdx.x;
+    if (i >= p.pieces) continue;
+    const long long pair = p.small ? (long long)((uint32_t)i / (uint32_t)per) : i / per, c = i - pair * per;
     const int s = __ldg(p.src + pair), d = __ldg(p.dst + pair);
-    if (c == 0 && threadIdx.x == 0 && p.table && pair > 0 && __ldg(p.src + pair - 1) >= s) record_error(p.err, PA_ERR_INVALID);
+    if (c == 0 && p.table && pair > 0 && __ldg(p.src + pair - 1) >= s) record_error(p.err, PA_ERR_INVALID);
     if ((uint32_t)s >= (uint32_t)p.n_blocks || (uint32_t)d >= (uint32_t)p.n_blocks) {
-      if (c == 0 && threadIdx.x == 0) record_error(p.err, PA_ERR_BOUNDS);
+      if (c == 0) record_error(p.err, PA_ERR_BOUNDS);
       continue;
     }
-    const long long size = is_v ? p.v_bytes : p.k_bytes, from = (long long)(is_v ? cv : c) * kChunk + 16 * threadIdx.x;
-    uint8_t* pool = is_v ? p.v_pool : p.k_pool;
-    const uint8_t* a = pool + s * size + from;
-    uint8_t* b = pool + d * size + from;
-    uint4 x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (from + 16 * kBlockThreads * i < size) x[i] = *reinterpret_cast<const uint4*>(a + 16 * kBlockThreads * i);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (from + 16 * kBlockThreads * i < size) *reinterpret_cast<uint4*>(b + 16 * kBlockThreads * i) = x[i];
+    const bool is_v = c >= p.k_pieces;
+    const long long size = is_v ? p.v_pieces : p.k_pieces, at = is_v ? c - p.k_pieces : c;
+    uint4* pool = reinterpret_cast<uint4*>(is_v ? p.v_pool : p.k_pool);
+    pool[d * size + at] = pool[s * size + at];
   }
 }
 
@@ -471,7 +465,7 @@ pa_status launch_blocks(const BlockParams& p, cudaStream_t cs) {
   int sms = 0;
   const pa_status st = sm_count(&sms);
   if (st != PA_OK) return st;
-  const long long parts = p.chunks + (p.entries + kBlockThreads - 1) / kBlockThreads;
+  const long long parts = p.parts + (p.entries + kBlockThreads - 1) / kBlockThreads;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -494,7 +488,7 @@ pa_status move_blocks(const pa_pool* pool, void* k_pool, void* v_pool, const int
   const size_t bk = (size_t)d.n_kv_heads * d.page_size * pa_row_bytes(d.k_type, d.head_dim);
   const size_t bv = (size_t)d.n_kv_heads * d.page_size * pa_row_bytes(d.v_type, d.head_dim);
   if (bk == 0 || bv == 0 || ((bk | bv) & 15)) return PA_ERR_UNSUPPORTED;
-  if (n > 0x7fffffffu || entries > (uint64_t(1) << 40) || (bk + bv) / kChunk > 0x3fffffffu) return PA_ERR_UNSUPPORTED;
+  if (n > 0x7fffffffu || entries > (uint64_t(1) << 40) || (bk + bv) / 16 > 0x7fffffffu) return PA_ERR_UNSUPPORTED;
   BlockParams p{};
   p.k_pool = static_cast<uint8_t*>(k_pool);
   p.v_pool = static_cast<uint8_t*>(v_pool);
@@ -503,13 +497,13 @@ pa_status move_blocks(const pa_pool* pool, void* k_pool, void* v_pool, const int
   p.table = entries ? table : nullptr;
   p.table_out = table_out;
   p.err = err;
-  p.k_bytes = (long long)bk;
-  p.v_bytes = (long long)bv;
+  p.k_pieces = (long long)(bk / 16);
+  p.v_pieces = (long long)(bv / 16);
   p.entries = (long long)entries;
   p.n = (int)n;
-  p.k_chunks = (int)((bk + kChunk - 1) / kChunk);
-  p.v_chunks = (int)((bv + kChunk - 1) / kChunk);
-  p.chunks = (long long)n * (p.k_chunks + p.v_chunks);
+  p.pieces = (long long)n * (p.k_pieces + p.v_pieces);
+  p.parts = (p.pieces + kBlockThreads - 1) / kBlockThreads;
+  p.small = p.pieces <= 0x7fffffff;
   p.n_blocks = (int)d.n_blocks;
   return launch_blocks(p, reinterpret_cast<cudaStream_t>(stream));
 }
