@@ -598,7 +598,8 @@ extern "C" pa_status pa_move_rows(const pa_pool* pool, void* k_pool, void* v_poo
   int sms = 0;
   pa_status st = sm_count(&sms);
   if (st != PA_OK) return st;
-  p.rows = (int)std::min<long long>(8, (2ll * n_rows + 32ll * sms - 1) / (32ll * sms));  // 1 while warps are few
+  // as few rows to a warp as give 32 warps an SM, up to 8 (12000 rows: 2 a warp 34.2 us, these 5 28.4, 8 33.5)
+  p.rows = (int)std::min<long long>(8, (2ll * n_rows + 32ll * sms - 1) / (32ll * sms));
   const long long grid = 2 * ((((long long)n_rows + p.rows - 1) / p.rows + kWarps - 1) / kWarps);
   if (grid > 0x7fffffffll) return PA_ERR_UNSUPPORTED;
   if (disjoint) return launch(pa_move_kernel<kDirect>, p, (unsigned)grid, cs);
