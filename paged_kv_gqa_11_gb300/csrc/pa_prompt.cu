@@ -102,8 +102,7 @@ __device__ __forceinline__ void prepare_rows(const PrepareParams& p, const Promp
     bool wide = false;
     x[r] = grp ? half_values<T>(grp, 8 * half + r, lane, is_v, &wide) : make_uint4(0u, 0u, 0u, 0u);
     wide_rows |= (uint32_t)wide << r;
-    const int key = first + r;  // values of keys that no new token sees are zeros, whatever lies there
-    if (is_v && (key >= s.len || (key >= p.sinks && key < s.lo))) x[r] = make_uint4(0u, 0u, 0u, 0u);
+    if (is_v && !has_value(s, group, first + r, p.sinks)) x[r] = make_uint4(0u, 0u, 0u, 0u);
   }
   const long long reg = (long long)s.group0 * p.n_kv_heads + (long long)head * s.groups;
   if (is_v) {  // eight dims x eight keys, transposed
@@ -159,7 +158,8 @@ __global__ void __launch_bounds__(32 * kPrepareWarps, 8) pa_prompt_prepare_kerne
       if (p.seq[mid].at <= at) lo = mid; else hi = mid - 1;
     }
     const PromptSeq& s = p.seq[lo];
-    const int group = at - s.at, v = group * kGroup, first = v < s.s16 ? v : v + s.shift;
+    const int group = at - s.at, first = first_key(s, group);
+    if (group == s.edge && !is_v) continue;  // of values only
     const int page = first / p.page_size, off = first - page * p.page_size;
     const int entry = __ldg(p.table + (long long)s.seq * p.table_stride + page);
     const bool ok = (uint32_t)entry < (uint32_t)p.n_blocks;
@@ -531,15 +531,14 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       __syncwarp();
       return s;
     };
-    // places v .. end - 1 of a plane: one run of the sequence's groups, or two (sinks, window)
-    auto copy = [&](const PromptUnit& u, const Span& s, const uint8_t* plane, int v, int end, int st) {
-      int a = v, stop = s.shift != u.shift0 && v < s.s16 ? min(end, s.s16) : end;
-      while (a < end) {
+    // places v .. end - 1 of a plane
+    auto copy = [&](const PromptUnit& u, const Span& s, int edge, const uint8_t* plane, int v, int end, int st) {
+      for (int a = v; a < end;) {
+        const Run r = run_of(u, s, edge, a, end);
         if (lane == 0)
-          bulk_copy(base + SM::kRing + st * kStageBytes + ((a - v) >> 4) * kPlaneGroup, plane + (long long)group_of(u, s, a) * kPlaneGroup,
-                    ((stop - a) >> 4) * kPlaneGroup, full + 8 * st);
-        a = stop;
-        stop = end;
+          bulk_copy(base + SM::kRing + st * kStageBytes + ((a - v) >> 4) * kPlaneGroup, plane + (long long)r.group * kPlaneGroup,
+                    ((r.stop - a) >> 4) * kPlaneGroup, full + 8 * st);
+        a = r.stop;
       }
       __syncwarp();
     };
@@ -549,7 +548,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       const int v = j * kKeys + 64 * (int)rank, end = max(v, min(v + 64, j * kKeys + whole16(tile_keys(s, j))));
       for (int h = 0; h < 2 && live; ++h) {
         const int st = stage(is_k, (uint32_t)(end - v) * 256);
-        if (st >= 0) copy(u, s, k + (long long)h * u.groups * kPlaneGroup, v, end, st);
+        if (st >= 0) copy(u, s, -1, k + (long long)h * u.groups * kPlaneGroup, v, end, st);
       }
     };
     auto vals = [&](const Piece& x, const Span& s, int j) {
@@ -558,7 +557,7 @@ __global__ void __launch_bounds__(kPThreads, 1) pa_prompt_kernel(const __grid_co
       const int v = j * kKeys, n16 = whole16(tile_keys(s, j));
       for (int q = 0; q < n16 && live; q += 64) {
         const int m = min(64, n16 - q), st = stage(!is_k, (uint32_t)m * 256);
-        if (st >= 0) copy(u, s, k, v + q, v + q + m, st);
+        if (st >= 0) copy(u, s, u.edge, k, v + q, v + q + m, st);
       }
     };
     bool more = walk.next(p, x);

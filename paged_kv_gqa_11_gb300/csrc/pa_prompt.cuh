@@ -12,14 +12,21 @@ constexpr int kPromptRows = 256;              // query rows of a unit: 128 for e
 constexpr int kGroupBytes = kGroup * kD * 2;  // a group's keys (or values) in binary16
 
 // A unit of a prompt, and where its sequence's keys lie in the workspace: the row groups
-// group0 .. group0 + groups - 1, of position v (v < s16), else v + shift0.
+// group0 .. group0 + groups - 1, of position v (v < s16), else v + shift0.  edge: the group that
+// stands for the values of the one in which the sinks end, or -1 (SeqSpan).
 struct PromptUnit : Unit {
-  int32_t groups, group0, shift0;
+  int32_t groups, group0, shift0, edge;
 };
 
 // The key order of all new tokens of a sequence: that of a unit from its first to its last.
+//
+// A value counts as a zero where no new token sees its key, but the sequence's first tokens may see
+// the keys behind the last sink in the sinks' last row group, which is in the order of every unit.  A
+// weight of 0 does not take an infinite or NaN value out of a product, so where some windows begin
+// in that group or before it and others behind it, the sequence has the group once more, the
+// last (edge), with zeros behind the last sink, for the units whose windows all begin behind it.
 struct SeqSpan : Span {
-  int groups;
+  int groups, edge;
 };
 
 inline SeqSpan seq_span(int len, int n_new, int window, int sinks) {
@@ -31,6 +38,7 @@ inline SeqSpan seq_span(int len, int n_new, int window, int sinks) {
   s.shift = group > s.s16 ? group - s.s16 : 0;
   s.end = len - s.shift;
   s.groups = ceil_div(s.end, kGroup);
+  s.edge = sinks < s.s16 && s.lo < s.s16 && len - window >= s.s16 ? s.groups++ : -1;  // len - window: the last token's first key
   return s;
 }
 
@@ -93,13 +101,41 @@ __host__ __device__ __forceinline__ int group_of(const PromptUnit& u, const Span
   return (v < s.s16 ? v : v + s.shift - u.shift0) >> 4;
 }
 
+// The run of the sequence's groups that the places v (the first of a row group) .. end - 1 begin with: up to `stop`, from
+// `group` on.  One run holds them all, or two (sinks, window), or three where `edge` (of values u.edge, of keys -1)
+// stands for the group in which the sinks end.
+struct Run {
+  int group, stop;
+};
+__host__ __device__ __forceinline__ Run run_of(const PromptUnit& u, const Span& s, int edge, int v, int end) {
+  Run r{group_of(u, s, v), end};
+  if (v < s.s16) {
+    const int last = s.s16 - kGroup;
+    if (edge >= 0 && v == last) r.group = edge;
+    const int stop = edge >= 0 && v < last ? last : edge >= 0 || s.shift != u.shift0 ? s.s16 : end;
+    r.stop = stop < end ? stop : end;
+  }
+  return r;
+}
+
 // A sequence's keys on their way into the workspace.
 struct PromptSeq {
   int32_t seq, len;
   int32_t lo;  // first key of its first new token's window
-  int32_t s16, shift, groups, group0;
+  int32_t s16, shift, groups, group0, edge;
   int32_t at;  // groups of the launch's sequences before it
 };
+
+// The position of a group's first key.
+__host__ __device__ __forceinline__ int first_key(const PromptSeq& s, int group) {
+  const int v = group == s.edge ? s.s16 - kGroup : group * kGroup;
+  return v < s.s16 ? v : v + s.shift;
+}
+
+// Whether a group has the value of `key`, one of its 16, or a zero in its place, whatever lies there.
+__host__ __device__ __forceinline__ bool has_value(const PromptSeq& s, int group, int key, int sinks) {
+  return key < s.len && (key < sinks || (key >= s.lo && group != s.edge));
+}
 
 struct PrepareParams {
   static constexpr int kMaxPromptSeqs = 128;

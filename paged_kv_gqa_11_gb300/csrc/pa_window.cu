@@ -349,7 +349,7 @@ pa_status prepare_prompts(PrepareParams& r, const Batch& b, int sms, cudaStream_
     for (; i < b.n_seq && r.n_seqs < PrepareParams::kMaxPromptSeqs; ++i) {
       if (!b.many(i)) continue;
       const SeqSpan s = seq_span(b.lens[i], b.n_new[i], b.window, b.sinks);
-      r.seq[r.n_seqs++] = PromptSeq{(int32_t)i, b.lens[i], s.lo, s.s16, s.shift, s.groups, group0, r.groups};
+      r.seq[r.n_seqs++] = PromptSeq{(int32_t)i, b.lens[i], s.lo, s.s16, s.shift, s.groups, group0, s.edge, r.groups};
       r.groups += s.groups;
       group0 += s.groups;
     }
@@ -370,6 +370,7 @@ void place_prompts(PromptParams& p, const Batch& b, uint32_t* seq, int* group0) 
     u.groups = s.groups;
     u.group0 = *group0;
     u.shift0 = s.shift;
+    u.edge = span_of(u, b.window, b.sinks).lo >= s.s16 ? s.edge : -1;
   }
 }
 
