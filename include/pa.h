@@ -577,9 +577,10 @@ pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_t q_stride,
                            int32_t* err, pa_stream_t stream);
 
 /* Scratch bytes pa_attend_window needs for these lengths on CUDA device `device`; more new
- * tokens, longer sequences and windows, or more sequences need no less.  Sequences of 64 new
- * tokens and more take 16 KB for each KV head and 16 keys that they see.  0 for an unsupported
- * pool or lengths that the call refuses. */
+ * tokens, longer sequences and windows, more first keys, or more sequences need no less, so that a
+ * caller may size it once for the largest.  Sequences of 64 new tokens and more take 16 KB for
+ * each KV head and 16 keys that they see, and up to three times 16 KB more for each head (131072 keys
+ * of 4 heads without a window: 512 MB).  0 for an unsupported pool or lengths that the call refuses. */
 size_t pa_attend_window_workspace_size(const pa_pool* pool, const int32_t* seq_lens_host, const int32_t* n_new,
                                        uint32_t n_seq, uint32_t window, uint32_t sinks, int device);
 

@@ -42,6 +42,13 @@ inline SeqSpan seq_span(int len, int n_new, int window, int sinks) {
   return s;
 }
 
+// The workspace's row groups for such a sequence: no fewer than it has, wherever in a row group its window
+// begins, and no fewer for more keys, new tokens, window or first keys.
+inline int64_t room_for(int64_t len, int64_t n_new, int64_t window, int64_t sinks) {
+  const int64_t all = (len + kGroup - 1) / kGroup, some = (sinks + kGroup - 1) / kGroup + (n_new + window + 2 * kGroup - 3) / kGroup;
+  return (all < some ? all : some) + 1;  // and edge
+}
+
 struct PromptParams {
   static constexpr int kUnitRows = kPromptRows, kMaxUnits = 256;
   const uint8_t* q;

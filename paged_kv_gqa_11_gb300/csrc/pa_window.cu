@@ -130,7 +130,7 @@ struct Batch {
   uint64_t tokens;
   uint32_t most;        // new tokens of the largest sequence of few
   uint32_t prompts;     // sequences of many
-  int64_t groups;       // row groups of their keys
+  int64_t groups;       // row groups for their keys
   int64_t few, keys, longest;  // sequences of few, keys that they read, and the longest's
   bool many(uint32_t s) const { return is_many(n_new[s]); }
   static bool is_many(int32_t n) { return n >= kPromptTokens; }
@@ -151,7 +151,7 @@ pa_status check_batch(const pa_pool_desc& d, uint64_t max_len, Batch* b) {
     if (d.n_kv_heads * (kLead + (keys / kKeys + 1) * (kTileCost + 2)) >= kMaxPlaces) return PA_ERR_UNSUPPORTED;
     if (b->many(i)) {
       ++b->prompts;
-      b->groups += seq_span((int)len, (int)n, b->window, b->sinks).groups;
+      b->groups += room_for(len, n, b->window, b->sinks);
     } else {
       b->most = std::max(b->most, (uint32_t)n);
       const int64_t seen = std::min<int64_t>(len, (int64_t)b->window + (int64_t)b->sinks + n - 1);
@@ -163,16 +163,19 @@ pa_status check_batch(const pa_pool_desc& d, uint64_t max_len, Batch* b) {
   return b->tokens > 0x7fffffffu || b->groups > 0x7fffffff / 16 ? PA_ERR_UNSUPPORTED : PA_OK;
 }
 
-// The workspace: two slots of (m, l) and O for each CTA, of the rows of the largest unit, for
-// the kernel of few tokens and for that of many; the many's keys, values and which keys are wide.
+// The workspace: two slots of (m, l) and O for each CTA, of the rows of the largest unit, the same for the
+// kernel of few tokens and, when that and its merge are done, that of many; the many's keys, values and which
+// keys are wide.  More of anything in a batch needs no less: the slots of a unit of many (256 rows for a pair of
+// CTAs) are larger than those of the largest of few (64 for a CTA), and the keys' room only grows (room_for).
 struct WsLayout {
-  size_t o, prompt_ml, prompt_o, k, v, wide, total;  // the first (m, l) at 0
+  size_t o, k, v, wide, total;  // the (m, l) at 0
 };
 
 int slot_rows_of(uint32_t max_new) { return (int)std::min<uint64_t>(kRows, (uint64_t)kGqa * max_new); }
 
 WsLayout layout_of(int ctas, const Batch& b) {
-  const size_t rows = 2 * (size_t)ctas * slot_rows_of(b.most), many = b.prompts ? 2 * (size_t)(ctas / 2) * kPromptRows : 0;
+  const size_t few = 2 * (size_t)ctas * slot_rows_of(b.most), many = b.prompts ? 2 * (size_t)(ctas / 2) * kPromptRows : 0;
+  const size_t rows = std::max(few, many);
   const size_t keys = (size_t)b.groups * b.heads * kGroupBytes;
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -183,8 +186,6 @@ WsLayout layout_of(int ctas, const Batch& b) {
   WsLayout w;
   take(rows * sizeof(float2));
   w.o = take(rows * kD * sizeof(float));
-  w.prompt_ml = take(many * sizeof(float2));
-  w.prompt_o = take(many * kD * sizeof(float));
   w.k = take(keys);
   w.v = take(keys);
   w.wide = take((size_t)b.groups * b.heads * 2);
@@ -454,10 +455,10 @@ void fill(P& p, const Batch& b, const pa_pool_desc& d, const void* q, int64_t q_
 
 // The same with the parts of cut segments, and the merge's parameters.
 template <class P>
-void fill_parts(P& p, MergeParams& m, uint8_t* ws, size_t ml, size_t o, int slot_rows) {
+void fill_parts(P& p, MergeParams& m, uint8_t* ws, size_t o, int slot_rows) {
   m.lens = p.lens;
   m.err = p.err;
-  m.part_ml = p.part_ml = reinterpret_cast<float2*>(ws + ml);
+  m.part_ml = p.part_ml = reinterpret_cast<float2*>(ws);
   m.part_o = p.part_o = reinterpret_cast<float*>(ws + o);
   m.out = p.out;
   m.lse = p.lse;
@@ -544,7 +545,7 @@ extern "C" pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_
   } else if (b.most > 0) {
     static thread_local WindowParams p;
     fill(p, b, d, q, q_stride, q_type, seq_lens_dev, scale, out, out_stride, out_type, lse, err);
-    fill_parts(p, m, ws, 0, lay.o, slot_rows_of(b.most));
+    fill_parts(p, m, ws, lay.o, slot_rows_of(b.most));
     fill_pools(p, d, k_pool, v_pool, block_table, table_stride);
     for (Cursor at{0, 0, 0}; at.seq < n_seq;) {
       const Plan plan = plan_chunk(p, m, b, false, ctas, &at);
@@ -556,7 +557,7 @@ extern "C" pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_
     static thread_local PromptParams p;
     static thread_local PrepareParams r;
     fill(p, b, d, q, q_stride, q_type, seq_lens_dev, scale, out, out_stride, out_type, lse, err);
-    fill_parts(p, m, ws, lay.prompt_ml, lay.prompt_o, kPromptRows);
+    fill_parts(p, m, ws, lay.o, kPromptRows);
     p.k = r.k = ws + lay.k;
     p.v = r.v = ws + lay.v;
     p.wide = r.wide = d.k_type == PA_F16 ? nullptr : ws + lay.wide;
