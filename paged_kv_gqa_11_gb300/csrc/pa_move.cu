@@ -171,12 +171,9 @@ __device__ __forceinline__ Turn turn_of(const MoveParams& p, const uint64_t* fro
                                         int lane, int from) {
   return make_turn(
       p.rot, p.interleaved, p.factor,
-      [&](int i) {  // the upper half of both products is all that the angle has (positions are 0 and more)
-        const uint64_t b = to_turns[i], a = from_turns[i];
-        const uint32_t hb = (uint32_t)dst_pos * (uint32_t)(b >> 32) + __umulhi((uint32_t)dst_pos, (uint32_t)b);
-        const uint32_t ha = (uint32_t)src_pos * (uint32_t)(a >> 32) + __umulhi((uint32_t)src_pos, (uint32_t)a);
-        return (uint64_t)(hb - ha) << 32;
-      },
+      // whole products (positions are 0 and more): of one frequency the difference is that of the distance, for all rows
+      // that are moved by it the same
+      [&](int i) { return (uint64_t)(uint32_t)dst_pos * to_turns[i] - (uint64_t)(uint32_t)src_pos * from_turns[i]; },
       lane, from);
 }
 
