@@ -19,12 +19,20 @@
 //
 // What bounds it: a group is 850 instructions of dependent steps, 0.8 us for a warp that has its scheduler to
 // itself; two CTAs on an SM hide each other's.  Eight warps to a CTA, one CTA on an SM, were slower
-// (64 sequences, 1024 keys: 41.8 against 31.4 us).  With K Q8_0, this kernel against the kernel of few
-// tokens, in us (sequences x keys, V Q8_0): 64 x 64 7.8 / 11.0, 64 x 1024 31.1 / 43.3, 32 x 512 13.9 / 17.2, 16 x 4096
-// 32.1 / 37.5, 8 x 32768 93.5 / 104.5 (0.90 of the copy bandwidth), 256 x 512 75.0 / 86.0.  Short shares of
-// a cluster lose (32 x 128 9.5 / 7.7, 8 x 512 10.0 / 9.6, 128 x 128 in two waves 18.2 / 16.6), Q4_0 keys gain
-// little (64 x 1024 32.8 / 33.8) and F16 ones lose (57.7 / 51.6: one CTA on an SM), so step_cluster
-// (pa_window.cu) has the rule and only pairs with K Q8_0 and quantised V have the kernel.
+// (64 sequences, 1024 keys: 41.8 against 31.4 us).
+//
+// Both sides of step_cluster's rule (pa_window.cu), in us: this kernel / the kernel of few tokens, sequences x keys of 4
+// heads, K and V Q8_0, eight caches in turn (at 256 and 1024 keys much of them stays in the L2):
+//   where the rule takes this kernel   61 x 256 15.9 / 19.2, 76 x 256 16.6 / 17.0, 61 x 1024 31.0 / 42.4, 76 x 1024 34.6 /
+//     42.4, 61 x 4096 90.6 / 110.3, 128 x 256 29.7 / 31.9, 128 x 1024 61.1 / 75.4, 128 x 4096 185 / 214; clusters of two 31 x 1024
+//     22.4 / 26.9, 38 x 1024 23.0 / 24.1, 31 x 4096 52.5 / 62.8; of four 16 x 1024 17.2 / 18.0, 16 x 4096 32.2 / 37.6; of eight
+//     8 x 4096 22.7 / 24.8; it loses at 38 x 256 (15.1 / 11.8: a segment to each SM suits the other) and 8 x 1024 (14.7 / 13.8);
+//   where it takes the other   77 x 256 24.4 / 21.4, 77 x 1024 50.9 / 50.0, 77 x 4096 155 / 135, 40 x 4096 86.7 / 77.0, 9 x 1024
+//     20.9 / 14.0, 19 x 1024 27.6 / 17.8; it loses between 48 and 60 sequences (60 x 256 15.8 / 19.2, 48 x 1024 30.2 / 35.5, 60 x 1024
+//     30.9 / 41.9, 60 x 4096 89.9 / 108), at 30 (30 x 1024 22.4 / 26.2) and at 100 to 121 (121 x 1024 60.7 / 71.9): the
+//     rule asks for four fifths of the device, and three would do at 1024 keys.
+// Q4_0 keys gain little (64 x 1024 32.8 / 33.8) and F16 ones lose (57.7 / 51.6: one CTA on an SM), so only pairs with K Q8_0 and
+// quantised V have the kernel.
 #pragma once
 
 #include "pa_io.cuh"

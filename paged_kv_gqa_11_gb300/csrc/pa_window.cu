@@ -94,14 +94,45 @@ bool lookup_kernels(int kt, int vt, Kernels* out) {
 
 int type_slot(int t) { return t == PA_F16 ? 0 : t == PA_Q4_0 ? 1 : 2; }
 
+// Every launch is a programmatic dependent of what runs before it on the stream: its set-up
+// overlaps the other's tail, and it waits for it before it reads.
+struct Launch {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = {};
+  explicit Launch(cudaStream_t cs) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = cs;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+};
+
+// A launch of pa_step_kernel over `segments` clusters.
+void set_steps(Launch& l, const StepKernel& ki, int cluster, int segments) {
+  l.attr[1].id = cudaLaunchAttributeClusterDimension;
+  l.attr[1].val.clusterDim.x = (unsigned)cluster;
+  l.attr[1].val.clusterDim.y = l.attr[1].val.clusterDim.z = 1;
+  l.cfg.numAttrs = 2;
+  l.cfg.gridDim = dim3((unsigned)(segments * cluster));
+  l.cfg.blockDim = dim3(kStepThreads);
+  l.cfg.dynamicSmemBytes = (size_t)ki.smem;
+}
+
+// Clusters of pa_step_kernel that the device holds at once, of 1, 2, 4 and 8 CTAs.
+struct StepFit {
+  int clusters[4];
+};
+
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int g_sms[kMaxDevices];
 bool g_ready[kMaxDevices][3][3];  // the kernels' shared-memory limits are raised
+StepFit g_fit[kMaxDevices][3][3];
 
 // CTAs of a launch on the device (one per SM), and, with a kernel, its limit raised there
-// (the device must be current for that).
-pa_status device_ready(int device, int kt, int vt, const Kernels* ki, int* ctas) {
+// (the device must be current for that) and what the device holds of the step kernel.
+pa_status device_ready(int device, int kt, int vt, const Kernels* ki, int* ctas, StepFit* fit = nullptr) {
   if (device < 0 || device >= kMaxDevices) return PA_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_sms[device] == 0) {
@@ -116,7 +147,16 @@ pa_status device_ready(int device, int kt, int vt, const Kernels* ki, int* ctas)
                (ki->step.fn && cudaFuncSetAttribute(ki->step.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, ki->step.smem) != cudaSuccess) ||
                prompt_ready() != PA_OK))
       return PA_ERR_CUDA;
+    StepFit& f = g_fit[device][type_slot(kt)][type_slot(vt)];
+    for (int i = 0; i < 4 && !r && ki->step.fn; ++i) {
+      Launch l(nullptr);
+      set_steps(l, ki->step, 1 << i, 1);
+      l.cfg.attrs = l.attr + 1;  // the cluster alone
+      l.cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&f.clusters[i], ki->step.fn, &l.cfg) != cudaSuccess) return PA_ERR_CUDA;
+    }
     r = true;
+    if (fit) *fit = f;
   }
   return PA_OK;
 }
@@ -270,20 +310,6 @@ Plan plan_chunk(P& p, MergeParams& m, const Batch& b, bool many, int max_ctas, C
   return Plan{cuts, rows};
 }
 
-// Every launch is a programmatic dependent of what runs before it on the stream: its set-up
-// overlaps the other's tail, and it waits for it before it reads.
-struct Launch {
-  cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = {};
-  explicit Launch(cudaStream_t cs) {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.stream = cs;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
-};
-
 pa_status launch_few(const WindowParams& p, const WindowKernel& ki, cudaStream_t cs) {
   Launch l(cs);
   l.cfg.gridDim = dim3((unsigned)p.n_ctas);
@@ -309,15 +335,19 @@ pa_status launch_merge(const MergeParams& m, const Plan& plan, int max_ctas, cud
 // kernel is taken for single tokens where its
 // CTAs, two to an SM, fill four fifths of the device in each wave, no sequence has more than 5/4 of the mean
 // keys, and a segment has 128 keys for each CTA of its cluster and each wave (one wave of clusters of one: any number);
-// pa_step_impl.cuh has both sides' times.
-int step_cluster(const Batch& b, int sms) {
+// and where, with clusters of several, the device holds all of them at once (fit; a cluster lies in one of its groups of
+// SMs, so that some SMs are left over: 74 clusters of 4 go on 152 SMs, not 76, and 36 of 8, not 38, of which the last two
+// wait all the same while one launch follows another).  Segments of 1024 / 4096 keys, us: 74 clusters of 4 20.1 / 36.2,
+// 75 27.5 / 53.5; 34 of 8 12.9 / 23.0, 36 17.3 / 30.7.  pa_step_impl.cuh has both sides' times.
+int step_cluster(const Batch& b, int sms, const StepFit* fit = nullptr) {
   if (b.most != 1) return 0;
   const int64_t slots = 2 * sms;
   if (b.longest * b.few > b.keys + b.keys / 4) return 0;
-  for (int c = 8; c >= 1; c /= 2) {
-    const int64_t n = b.few * b.heads * c, waves = (n + slots - 1) / slots;
+  for (int i = 3; i >= 0; --i) {
+    const int64_t c = 1 << i, n = b.few * b.heads * c, waves = (n + slots - 1) / slots;
     if ((waves > 1 && c > 1) || n * 5 < waves * slots * 4) continue;
-    return waves * c == 1 || b.longest >= 128 * c * waves ? c : 0;
+    if (fit && c > 1 && b.few * b.heads > fit->clusters[i] - (c == 8 ? 2 : 0)) continue;
+    return waves * c == 1 || b.longest >= 128 * c * waves ? (int)c : 0;
   }
   return 0;
 }
@@ -330,13 +360,7 @@ pa_status launch_steps(StepParams& p, const Batch& b, const StepKernel& ki, cuda
       if (b.n_new[s] == 1) p.seq[n++] = StepSeq{(int32_t)s, (int32_t)token, b.lens[s]};
     if (n == 0) break;
     Launch l(cs);
-    l.attr[1].id = cudaLaunchAttributeClusterDimension;
-    l.attr[1].val.clusterDim.x = (unsigned)p.cluster;
-    l.attr[1].val.clusterDim.y = l.attr[1].val.clusterDim.z = 1;
-    l.cfg.numAttrs = 2;
-    l.cfg.gridDim = dim3((unsigned)(n * p.n_kv_heads * p.cluster));
-    l.cfg.blockDim = dim3(kStepThreads);
-    l.cfg.dynamicSmemBytes = (size_t)ki.smem;
+    set_steps(l, ki, p.cluster, n * p.n_kv_heads);
     if (cudaLaunchKernelEx(&l.cfg, ki.fn, p) != cudaSuccess) return PA_ERR_CUDA;
   }
   return PA_OK;
@@ -527,7 +551,8 @@ extern "C" pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_
   }
   int device = 0, ctas = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return PA_ERR_CUDA;
-  st = device_ready(device, d.k_type, d.v_type, &ki, &ctas);
+  StepFit fit = {};
+  st = device_ready(device, d.k_type, d.v_type, &ki, &ctas, &fit);
   if (st != PA_OK) return st;
   const WsLayout lay = layout_of(ctas, b);
   if (ws_bytes < lay.total) return PA_ERR_INVALID;
@@ -536,7 +561,7 @@ extern "C" pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_
   static thread_local MergeParams m;  // kept off the stack
   // Launches in order on the stream, sharing the workspace: each one's kernel waits for the
   // one before to complete.
-  if (const int cluster = ki.step.fn ? step_cluster(b, ctas) : 0) {
+  if (const int cluster = ki.step.fn ? step_cluster(b, ctas, &fit) : 0) {
     static thread_local StepParams p;
     fill(p, b, d, q, q_stride, q_type, seq_lens_dev, scale, out, out_stride, out_type, lse, err);
     fill_pools(p, d, k_pool, v_pool, block_table, table_stride);
