@@ -558,11 +558,19 @@ size_t pa_decode_prefix_workspace_size(const pa_pool* pool, uint32_t n_seq, uint
  * workspace: ws_bytes >= pa_attend_window_workspace_size(), 256-byte aligned; contents as
  *           pa_decode's.
  *
- * Precision and range: as pa_decode_prefix, whose arithmetic it is (single tokens of large
- * batches with Q8_0 keys lose less: K and P are not rounded there).  An infinite or NaN
- * value of V (a stored one past 65504 is infinite) in a row that one of the tokens
- * sees can also reach others of the same sequence that do not see it (those up to 64
- * tokens away); in a row that none of them sees it has no effect, and K's never have.
+ * Precision and range: as pa_decode_prefix, whose arithmetic it is: Q of fp32 and bfloat16,
+ * quantised K, V and the softmax weights are each rounded to binary16 once, whatever out_type is;
+ * sums are fp32.  Single tokens of batches that fill the device, with Q8_0 keys and quantised values, lose
+ * less (K is exact there, the weights are in two parts).  So a token's last bits depend on how many
+ * sequences and new tokens stand beside it.  No form of this call keeps all keys exact: for logits of
+ * hundreds pa_decode is the call to make, which has no window.  It is also the faster one for single
+ * tokens over long contexts that are seen whole (8 x 8192 keys: Q4_0 23.6 us against 30.1, Q8_0
+ * 30.6 against 32.7, F16 45.4 against 48.5; 8 x 32768 of Q4_0 57 against 90).
+ *
+ * An infinite or NaN value of V (a stored one past 65504 is infinite) in a row that one of the
+ * tokens sees can also reach others of the same sequence that do not see it: those whose window
+ * or own position lies up to 64 tokens from it.  In a row that no token sees it has no effect, and K's
+ * reach nobody who does not see them.
  *
  * Launches: one for the sequences of fewer than 64 new tokens (448 times 64 query rows, or 256
  * single tokens, at a time), and a merge when a (64 query rows, KV head) is shared by

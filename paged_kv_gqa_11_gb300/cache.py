@@ -174,7 +174,10 @@ class PagedKVCache:
         32-bit whole numbers (numpy).  Pages that no new token sees are not read;
         they may have been released.  Rows of q after the last sequence's are left
         alone: those of a given out and lse stay, those of new ones are zeros.
-        Precision, workspace and streams: as decode_prefix.  Returns (out, lse)."""
+        Precision, workspace and streams: as decode_prefix (keys, values and
+        weights rounded to binary16 whatever out's type is; how, also depends on
+        the batch).  For single tokens that see long contexts whole, decode is
+        exacter and faster.  Returns (out, lse)."""
         return load_calls().attend_window(self.pool.address, q, self.k_pool, self.v_pool, block_table, seq_lens_dev,
                                           seq_lens_host, n_new, window, sinks, scale, out, lse, want_lse, workspace, self.err,
                                           stream)

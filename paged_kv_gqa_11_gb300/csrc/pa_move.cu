@@ -17,8 +17,9 @@
 // a head (dequantised, turned, its maximum found, quantised), which a warp hides by having the
 // next four heads' loads on their way.  K's rows and V's are in CTAs of their own, so that rows
 // turned in place do not leave every second warp idle.  Measured, one GB300: 24 rows 3.4 us (one launch),
-// 12000 rows of Q8_0 down by 777, 64 values turned (two launches) 28.5, 65536 rows of Q8_0 keys turned in place
-// (all 256 values, 2.0 TB/s read and written: the arithmetic) 70.6; with rows of both pools in one
+// 12000 rows of Q8_0 down by 777, 64 values turned (two launches) 31.1 (28.6 while the L2 holds them), the same rows
+// to other pages (disjoint, one launch) 22.3, without a turn 15.0 (7.7 are their bytes), 65536 rows of Q8_0 keys turned in place
+// (all 256 values, 2.0 TB/s read and written: the arithmetic) 71.3; with rows of both pools in one
 // warp and no loads ahead 138.  Partly turned heads packed so that a warp turns only their blocks
 // were slower (more registers, 154, and more shuffles than the arithmetic that they saved).
 #include <cuda_runtime.h>

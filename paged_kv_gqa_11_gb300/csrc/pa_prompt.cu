@@ -18,7 +18,8 @@
 // The workspace's layout, per (sequence, head); a core matrix is 8 rows x 16 bytes:
 //   K   two planes of 128 dims, each [8 keys][16 slots of 8 dims] core matrices (rows = keys);
 //   V   two planes of 128 dims, each [8 keys][16 slots of 8 dims] core matrices, transposed (rows = dims);
-// a run of row groups of a plane is one contiguous piece, and an MMA's B operand.
+// a run of row groups of a plane is one contiguous piece, and an MMA's B operand.  The row group in which the
+// first keys end may be there twice (SeqSpan), so that a value that only early tokens see meets no later ones.
 //
 // Tensor memory: O in columns 0-255, two buffers of S in 256-383 and 384-511; P as pairs
 // of binary16 in the first 64 columns of its S.
@@ -39,9 +40,9 @@
 // segments, the largest dealt first, each to the pair with least (4096 tokens, no window: 147 us
 // against 167; 2048 tokens, window 1024: 59 against 67; both before K and V had a warp each).
 //
-// Measured: 4096 tokens without a window in F16 140 us (1472 TFLOP/s of the 206 GFLOP that are not
-// masked, 0.75 of cuBLAS's burst rate); 2048 tokens, window 1024, Q8_0 / Q4_0 58 us, of which 6 for
-// the keys' launch.  What bounds it: the copy engine's 32 bytes a cycle, 2040 cycles for a
+// Measured: 4096 tokens without a window in F16 139 to 143 us replayed from a graph, 148 call by call (1393
+// TFLOP/s of the 206 GFLOP that are not masked, 0.71 of cuBLAS's burst rate); 2048 tokens, window 1024, Q8_0 / Q4_0
+// 61 us (58 while the L2 holds the rows), of which 6 for the keys' launch.  What bounds it: the copy engine's 32 bytes a cycle, 2040 cycles for a
 // tile's 64 KB beside 2048 of MMA (each alone runs at its rate, with all other traffic around it); the
 // engine and the MMAs wait for one another through a ring of five stages, 2300 cycles a tile.  A piece's end
 // costs 2 us: its O is read before the next piece's first PV.  V by cp.async (65 bytes a cycle and SM by

@@ -25,10 +25,14 @@ namespace {
 constexpr int64_t kMaxLen = 0x7fffffff - 2 * kKeys;  // a tile past the last key is still a 32-bit number
 constexpr uint32_t kMaxNew = 1u << 24;               // new tokens of a sequence
 constexpr int64_t kMaxPlaces = 1ll << 30;
-// Sequences of so many new tokens or more are the prompts' kernel's (Q8_0, 4 sequences of 4096 keys, 32 tokens
-// 45.8 us by the kernel of few, 64 tokens 75.7 by the prompts', 77.4 by the dense shared-prefix kernel with
-// nothing shared, whose arithmetic the kernel of few has; 2048 tokens, window 1024: 161 and 59).  The
-// prompts' kernel turns the keys into binary16 first, which fewer tokens do not pay for.
+// Sequences of so many new tokens or more are the prompts' kernel's, which turns the keys into binary16 first.
+// 63 tokens by the kernel of few and 64 by the prompts', us, without a window, sequences x keys:
+//          1 x 512      1 x 4096     1 x 32768  1 x 131072  4 x 4096     4 x 32768  16 x 2048
+//   Q4_0   13.6, 17.6   24.5, 33.2   83, 107    280, 354    58.6, 65.7   286, 388   112, 108
+//   Q8_0   14.2, 18.3   31.1, 33.8   133, 118   400, 385    83.9, 74.8   409, 401   159, 121
+//   F16    13.1, 17.5   23.8, 32.5   105, 96    462, 325    54.1, 61.2   468, 371   122, 99
+// The two pass each other near here for Q8_0 and F16 keys; with Q4_0 keys, and over short contexts, the kernel of few is
+// still up to a quarter faster at 63 tokens.  2048 tokens, window 1024: 161 us and 59.
 constexpr int32_t kPromptTokens = 64;
 
 // ------------------------------------------------------------------ merge

@@ -29,7 +29,10 @@
 //
 // What bounds it: latency.  Bulk copies of a row group's 2 to 8 KB take the copy engine 55
 // cycles each and 36 bytes a cycle, a tile of 128 keys 1 to 2.3 us, and 7 to 8 us pass from
-// launch to the merge's last row (8 tokens, window 4096, Q4_0: 19.4 us; 8 x 4, window 2048, F16: 16.4).
+// launch to the merge's last row (8 tokens, window 4096, Q4_0: 20.3 us, 0.28 of what their bytes
+// take; 8 x 4, window 2048, F16: 22.0 from HBM, 0.46, and 16.5 while the L2 holds the rows).  It was made for up to
+// 64 query rows; a single token has six, so pa_decode, made for one, is faster over long contexts (8 x 8192 keys, Q4_0:
+// 23.6 us, this kernel 30.1), and so is pa_prefix_kernel, whose walk has less to decide for a tile (28.1).
 // Many tokens have pa_prompt.cu, large batches of single ones pa_step_impl.cuh.
 #pragma once
 
