@@ -588,7 +588,7 @@ pa_status pa_attend_window(const pa_pool* pool, const void* q, int64_t q_stride,
  * tokens, longer sequences and windows, more first keys, or more sequences need no less, so that a
  * caller may size it once for the largest.  Sequences of 64 new tokens and more take 16 KB for
  * each KV head and 16 keys that they see, and up to three times 16 KB more for each head (131072 keys
- * of 4 heads without a window: 512 MB).  0 for an unsupported pool or lengths that the call refuses. */
+ * of 4 heads without a window: 537 MB).  0 for an unsupported pool or lengths that the call refuses. */
 size_t pa_attend_window_workspace_size(const pa_pool* pool, const int32_t* seq_lens_host, const int32_t* n_new,
                                        uint32_t n_seq, uint32_t window, uint32_t sinks, int device);
 
