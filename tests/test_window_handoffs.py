@@ -166,8 +166,7 @@ def test_the_model_sees_what_each_rule_is_for(without):
     assert faults > 5
 
 
-def test_the_second_meeting_alone_guards_the_shared_sums_of_the_warps():
-    """The sums' array itself is safe behind the first meeting: a warp writes a piece's results before it comes to the next
-    one's end."""
+def test_the_sums_are_safe_behind_the_first_meeting():
+    """A warp writes a piece's results before it comes to the next one's end; the second meeting is for what the sums are made of."""
     for seed in range(150):
         simulate(seed, second=False)
